@@ -362,3 +362,9 @@ class Plan:
 
     def __exit__(self, *exc):
         self.close()
+
+
+# The layer operators (include/tsx_layers.h).  They use the names above.
+from .layers import (ACTS, FORMS, Checkpoint, GatedAct, GroupNorm, Packer, tsx_gated_act,  # noqa: E402
+                     tsx_gated_act_backward, tsx_group_norm, tsx_group_norm_backward, tsx_group_norm_workspace,
+                     tsx_norm_desc, tsx_pack, tsx_unpack)

@@ -1,0 +1,112 @@
+// Internal declarations of the layer operators (include/tsx_layers.h): how
+// their rows are laid over threads, and their kernels' arguments.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tsx_internal.h"
+#include "tsx_layers.h"
+
+namespace tsx {
+
+// How [rows, cols] is laid over CTAs and threads.  A row is cut into `chunks`
+// runs of chunk_cols channels (grid.y); a CTA holds P rows of one run at a
+// time, V threads to a row, each with eight channels (csrc/tsx_oct.cuh).
+struct RowLayout {
+    int64_t rows;
+    int cols;
+    int chunk_cols;   // channels of a run: a multiple of 8, of the block where there are checkpoints
+    int chunks;
+    int V;            // threads to a row: ceil(chunk_cols / 8) rounded up to whole teams
+    int P;            // rows side by side
+    int team;         // neighbouring threads that share a checkpoint block (1, 2, ..., 16)
+    int threads;      // P * V rounded up to whole warps
+    bool vec;         // 16-byte vectors (else element by element)
+};
+
+constexpr int kOct = 8;                // channels to a thread
+constexpr int kLayerThreads = 512;     // most threads of a layer kernel's CTA
+
+// The layout of rows cut for CTAs of about `want` threads; block: channels
+// to a scale, 0 without checkpoints.
+RowLayout row_layout(int64_t rows, int64_t cols, int block, bool vec, int want);
+
+// A tensor as the kernels take it: `q` and `scale` in place of `x` for a
+// checkpoint ([rows, cols] bytes and [rows, ceil(cols / block)] floats).
+struct Saved {
+    const void* x;
+    const void* q;
+    const float* scale;
+};
+struct HeldOut {
+    void* q;
+    float* scale;
+};
+
+struct PackArgs {
+    RowLayout lay;
+    int64_t pitch;
+    int form, block;
+    int64_t blocks;   // scales to a row
+};
+cudaError_t launch_pack(int dtype, const PackArgs& a, const void* x, HeldOut held, cudaStream_t st);
+cudaError_t launch_unpack(int dtype, const PackArgs& a, const void* q, const float* scale, void* x, cudaStream_t st);
+
+struct GatedArgs {
+    RowLayout lay;
+    int64_t in_pitch, out_pitch;
+    int act, form, block;
+    int64_t blocks;
+};
+cudaError_t launch_gated(int dtype, const GatedArgs& a, const void* gate, const void* up, void* h, HeldOut held_gate,
+                         HeldOut held_up, cudaStream_t st);
+cudaError_t launch_gated_backward(int dtype, const GatedArgs& a, const void* dh, Saved gate, Saved up, void* dgate,
+                                  void* dup, void* h, cudaStream_t st);
+
+// Group norm.  The channels are cut into runs that hold whole groups (or, for
+// groups wider than a CTA's row, into `pieces` runs a group), the l rows of a
+// sample into `splits` ranges; a CTA takes one range of one run.
+struct NormLayout {
+    bool vec;
+    bool oct_in_group;   // vec, and eight consecutive channels never straddle two groups
+    int team;            // as in RowLayout
+    int run_groups;      // groups to a run
+    int run_cols;        // channels of a run
+    int runs;
+    int pieces;          // runs to a group (1 unless a group is wider than a CTA's row)
+    int V, P, threads;
+    int64_t splits;      // row ranges of a sample
+    int64_t range;       // rows to a range
+};
+
+struct NormArgs {
+    NormLayout lay;
+    int64_t n, l;
+    int c, groups, per_group;
+    int64_t x_pitch, y_pitch;
+    float eps;
+    int act, form, block;
+    int64_t blocks;      // scales to a row of a checkpoint
+    int wide_params;     // weight and bias are fp32 (else of the element type)
+};
+
+// Scratch of one call (see tsx_group_norm_workspace):
+//   part   [n][splits * pieces][groups] pairs: (mean, sum of squared deviations) forward, the two
+//          sums of the gradient backward
+//   chan   [slices][2][c] backward: sums for dweight and dbias, slices = n * splits
+struct NormScratch {
+    float2* part;
+    float* chan;
+};
+
+cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,
+                        float* mean, float* rstd, HeldOut held, NormScratch scratch, cudaStream_t st);
+cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,
+                                 const void* bias, const float* mean, const float* rstd, void* dx, float* dweight,
+                                 float* dbias, NormScratch scratch, cudaStream_t st);
+// Results of samples without rows: mean 0, rstd 1 / sqrt(eps).
+cudaError_t launch_norm_empty(float* mean, float* rstd, int64_t count, float eps, cudaStream_t st);
+
+}  // namespace tsx

@@ -1,0 +1,505 @@
+// The C ABI of the layer operators (include/tsx_layers.h): argument checks,
+// how rows are laid over threads, launches.
+
+#include "layers.h"
+
+#include <cmath>
+#include <cstdio>
+#include <numeric>
+
+#include "plan.h"
+
+namespace tsx {
+
+RowLayout row_layout(int64_t rows, int64_t cols, int block, bool vec, int want)
+{
+    RowLayout lay{};
+    lay.rows = rows;
+    lay.cols = int(cols);
+    lay.vec = vec;
+    const int64_t octs = (cols + kOct - 1) / kOct;
+    int team = block ? block / kOct : vec ? 1 : 16;
+    while (team > 1 && team / 2 >= octs)
+        team /= 2;
+    lay.team = team;
+    const int64_t chunks = (octs + want - 1) / want;
+    int64_t v = (octs + chunks - 1) / chunks;
+    v = (v + team - 1) / team * team;
+    lay.V = int(v);
+    lay.chunk_cols = lay.V * kOct;
+    lay.chunks = int((cols + lay.chunk_cols - 1) / lay.chunk_cols);
+    int64_t p = want / v;
+    p = p < 1 ? 1 : p > rows ? rows : p;
+    lay.P = int(p);
+    lay.threads = (lay.P * lay.V + 31) / 32 * 32;
+    return lay;
+}
+
+namespace {
+
+// Threads of the elementwise layer kernels' CTAs.
+constexpr int kElementwiseThreads = 256;
+constexpr int64_t kMaxExtent = 0x7fffffff;
+constexpr int kMaxChunks = 65535;   // grid.y
+
+int fail(int rc, const char* call, const char* msg)
+{
+    char buf[256];
+    std::snprintf(buf, sizeof buf, "%s: %s", call, msg);
+    set_last_error(buf);
+    return rc;
+}
+
+int launched(cudaError_t e, const char* call)
+{
+    if (e != cudaSuccess)
+        return fail(TSX_ERR_CUDA, call, cudaGetErrorString(e));
+    set_last_error("");
+    return TSX_OK;
+}
+
+bool known_dtype(int dtype) { return dtype == TSX_F16 || dtype == TSX_BF16 || dtype == TSX_F32; }
+bool known_act(int act) { return act == TSX_ACT_NONE || act == TSX_ACT_SILU || act == TSX_ACT_GELU; }
+
+bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// Shape, form and block of a call; TSX_OK also for an empty tensor.
+int check_shape(const char* call, int dtype, int64_t rows, int64_t cols, int form, int block)
+{
+    if (!known_dtype(dtype))
+        return fail(TSX_ERR_INVALID, call, "unknown dtype");
+    if (rows < 0 || cols < 0 || rows >= kMaxExtent || cols >= kMaxExtent)
+        return fail(TSX_ERR_INVALID, call, "rows and cols must be 0 .. 2^31 - 2");
+    if (form != TSX_INT8 && form != TSX_E4M3)
+        return fail(TSX_ERR_INVALID, call, "unknown 8-bit form");
+    if (block != 32 && block != 64 && block != 128)
+        return fail(TSX_ERR_INVALID, call, "block must be 32, 64 or 128");
+    return TSX_OK;
+}
+
+// Whether rows of `cols` elements at this pitch from `p` move as vectors.
+bool vectors(const void* p, int64_t cols, int64_t pitch, int es)
+{
+    return !p || (cols % kOct == 0 && pitch * es % 16 == 0 && aligned(p, 16));
+}
+// The same of the dense bytes of a checkpoint.
+bool held_vectors(const void* q, int64_t cols) { return !q || (cols % kOct == 0 && aligned(q, 8)); }
+
+int check_layout(const char* call, const RowLayout& lay)
+{
+    if (lay.chunks > kMaxChunks)
+        return fail(TSX_ERR_UNSUPPORTED, call, "rows are too long");
+    return TSX_OK;
+}
+
+int pack_args(const char* call, int dtype, int64_t rows, int64_t cols, int64_t pitch, int form, int block,
+              const void* x, const void* q, const float* scale, PackArgs* a)
+{
+    if (!x || !q || !scale)
+        return fail(TSX_ERR_INVALID, call, "x, q and scale are required");
+    const int es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(scale, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    a->lay = row_layout(rows, cols, block, vectors(x, cols, pitch, es) && held_vectors(q, cols), kElementwiseThreads);
+    a->pitch = pitch;
+    a->form = form;
+    a->block = block;
+    a->blocks = (cols + block - 1) / block;
+    return check_layout(call, a->lay);
+}
+
+}  // namespace
+}  // namespace tsx
+
+using namespace tsx;
+
+extern "C" int tsx_pack(tsx_dtype dtype, int64_t rows, int64_t cols, int64_t pitch, tsx_form form, int block,
+                        const void* x, void* q, float* scale, tsx_stream_t stream)
+{
+    const char* call = "tsx_pack";
+    int rc = check_shape(call, dtype, rows, cols, form, block);
+    if (rc != TSX_OK)
+        return rc;
+    if (pitch < cols)
+        return fail(TSX_ERR_INVALID, call, "the pitch is shorter than a row");
+    if (rows == 0 || cols == 0)
+        return launched(cudaSuccess, call);
+    PackArgs a{};
+    rc = pack_args(call, dtype, rows, cols, pitch, form, block, x, q, scale, &a);
+    if (rc != TSX_OK)
+        return rc;
+    return launched(launch_pack(dtype, a, x, HeldOut{q, scale}, reinterpret_cast<cudaStream_t>(stream)), call);
+}
+
+extern "C" int tsx_unpack(tsx_dtype dtype, int64_t rows, int64_t cols, int64_t pitch, tsx_form form, int block,
+                          const void* q, const float* scale, void* x, tsx_stream_t stream)
+{
+    const char* call = "tsx_unpack";
+    int rc = check_shape(call, dtype, rows, cols, form, block);
+    if (rc != TSX_OK)
+        return rc;
+    if (pitch < cols)
+        return fail(TSX_ERR_INVALID, call, "the pitch is shorter than a row");
+    if (rows == 0 || cols == 0)
+        return launched(cudaSuccess, call);
+    PackArgs a{};
+    rc = pack_args(call, dtype, rows, cols, pitch, form, block, x, q, scale, &a);
+    if (rc != TSX_OK)
+        return rc;
+    return launched(launch_unpack(dtype, a, q, scale, x, reinterpret_cast<cudaStream_t>(stream)), call);
+}
+
+namespace {
+
+// What forward and backward check alike.  held: the call reads or writes
+// checkpoints (all four pointers), which alone decide about `block`.
+int gated_args(const char* call, int dtype, int64_t rows, int64_t cols, int64_t in_pitch, int64_t out_pitch, int act,
+               int form, int block, GatedArgs* a)
+{
+    const int rc = check_shape(call, dtype, rows, cols, form, block);
+    if (rc != TSX_OK)
+        return rc;
+    if (!known_act(act))
+        return fail(TSX_ERR_INVALID, call, "unknown activation");
+    if (in_pitch < cols || out_pitch < cols)
+        return fail(TSX_ERR_INVALID, call, "a pitch is shorter than a row");
+    a->in_pitch = in_pitch;
+    a->out_pitch = out_pitch;
+    a->act = act;
+    a->form = form;
+    a->block = block;
+    a->blocks = (cols + block - 1) / block;
+    return TSX_OK;
+}
+
+}  // namespace
+
+extern "C" int tsx_gated_act(tsx_dtype dtype, int64_t rows, int64_t cols, int64_t in_pitch, int64_t out_pitch,
+                             tsx_act act, tsx_form form, int block, const void* gate, const void* up, void* h,
+                             void* q_gate, float* scale_gate, void* q_up, float* scale_up, tsx_stream_t stream)
+{
+    const char* call = "tsx_gated_act";
+    GatedArgs a{};
+    int rc = gated_args(call, dtype, rows, cols, in_pitch, out_pitch, act, form, block, &a);
+    if (rc != TSX_OK)
+        return rc;
+    const int held = !!q_gate + !!scale_gate + !!q_up + !!scale_up;
+    if (held != 0 && held != 4)
+        return fail(TSX_ERR_INVALID, call, "both checkpoints, or neither");
+    if (rows == 0 || cols == 0)
+        return launched(cudaSuccess, call);
+    if (!gate || !up || !h)
+        return fail(TSX_ERR_INVALID, call, "gate, up and h are required");
+    const int es = elem_size(dtype);
+    if (!aligned(gate, es) || !aligned(up, es) || !aligned(h, es) || !aligned(scale_gate, 4) || !aligned(scale_up, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    const bool vec = vectors(gate, cols, in_pitch, es) && vectors(up, cols, in_pitch, es) &&
+                     vectors(h, cols, out_pitch, es) && held_vectors(q_gate, cols) && held_vectors(q_up, cols);
+    a.lay = row_layout(rows, cols, held ? block : 0, vec, kElementwiseThreads);
+    rc = check_layout(call, a.lay);
+    if (rc != TSX_OK)
+        return rc;
+    return launched(launch_gated(dtype, a, gate, up, h, HeldOut{q_gate, scale_gate}, HeldOut{q_up, scale_up},
+                                 reinterpret_cast<cudaStream_t>(stream)),
+                    call);
+}
+
+extern "C" int tsx_gated_act_backward(tsx_dtype dtype, int64_t rows, int64_t cols, int64_t in_pitch,
+                                      int64_t out_pitch, tsx_act act, tsx_form form, int block, const void* dh,
+                                      const void* gate, const void* up, const void* q_gate, const float* scale_gate,
+                                      const void* q_up, const float* scale_up, void* dgate, void* dup, void* h,
+                                      tsx_stream_t stream)
+{
+    const char* call = "tsx_gated_act_backward";
+    GatedArgs a{};
+    int rc = gated_args(call, dtype, rows, cols, in_pitch, out_pitch, act, form, block, &a);
+    if (rc != TSX_OK)
+        return rc;
+    if (rows == 0 || cols == 0)
+        return launched(cudaSuccess, call);
+    const int held = !!q_gate + !!scale_gate + !!q_up + !!scale_up, full = !!gate + !!up;
+    if (!((held == 4 && full == 0) || (held == 0 && full == 2)))
+        return fail(TSX_ERR_INVALID, call, "gate and up are either two tensors or two checkpoints");
+    if (!dh || !dgate || !dup)
+        return fail(TSX_ERR_INVALID, call, "dh, dgate and dup are required");
+    const int es = elem_size(dtype);
+    if (!aligned(dh, es) || !aligned(gate, es) || !aligned(up, es) || !aligned(dgate, es) || !aligned(dup, es) ||
+        !aligned(h, es) || !aligned(scale_gate, 4) || !aligned(scale_up, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    const bool vec = vectors(dh, cols, out_pitch, es) && vectors(h, cols, out_pitch, es) &&
+                     vectors(gate, cols, in_pitch, es) && vectors(up, cols, in_pitch, es) &&
+                     vectors(dgate, cols, in_pitch, es) && vectors(dup, cols, in_pitch, es) &&
+                     held_vectors(q_gate, cols) && held_vectors(q_up, cols);
+    a.lay = row_layout(rows, cols, held ? block : 0, vec, kElementwiseThreads);
+    rc = check_layout(call, a.lay);
+    if (rc != TSX_OK)
+        return rc;
+    return launched(launch_gated_backward(dtype, a, dh, Saved{gate, q_gate, scale_gate}, Saved{up, q_up, scale_up},
+                                          dgate, dup, h, reinterpret_cast<cudaStream_t>(stream)),
+                    call);
+}
+
+// ---------------------------------------------------------- group norm
+
+namespace {
+
+// Channels of a CTA's run at most (its shared memory holds a pair of floats
+// for each channel and row lane, and for each group), and its threads.
+constexpr int kNormRun = 2048;
+constexpr int kNormThreads = 512;
+// Ranges are cut until about this many CTAs share the work: four to each of
+// the 152 SMs.  A constant of the chip, not read from it, so that results
+// depend on the shape alone.
+constexpr int64_t kNormCtas = 4 * 152;
+constexpr int kNormRowsAtOnce = 4;
+
+// The layout for rows of c channels; block: channels to a scale where the
+// call writes checkpoints, else 0.  False if this alignment (vec, block)
+// cannot be had with these groups.
+bool norm_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
+{
+    const int64_t per = d.c / d.groups;
+    NormLayout lay{};
+    lay.vec = vec;
+    lay.oct_in_group = vec && per % kOct == 0;
+    // runs start on whole octs / blocks
+    const int64_t align = block ? block : vec ? kOct : 1;
+    if (per > kNormRun) {
+        if (per % align != 0)
+            return false;
+        lay.run_groups = 1;
+        const int64_t pieces = (per + kNormRun - 1) / kNormRun;
+        const int64_t to = 128;   // whole teams of any size
+        lay.run_cols = int(((per + pieces - 1) / pieces + to - 1) / to * to);
+        lay.pieces = int((per + lay.run_cols - 1) / lay.run_cols);
+        lay.runs = int(d.groups) * lay.pieces;
+    } else {
+        int64_t groups = d.groups;
+        if (d.c > kNormRun) {
+            const int64_t unit = align / std::gcd(per, align);
+            groups = kNormRun / per / unit * unit;
+            if (groups == 0)
+                return false;
+        }
+        lay.run_groups = int(groups);
+        lay.run_cols = int(groups * per);
+        lay.pieces = 1;
+        lay.runs = int((d.groups + groups - 1) / groups);
+    }
+    const int octs = (lay.run_cols + kOct - 1) / kOct;
+    int team = block ? block / kOct : vec ? 1 : 16;
+    while (team > 1 && team / 2 >= octs)
+        team /= 2;
+    lay.team = team;
+    lay.V = (octs + team - 1) / team * team;
+    int64_t p = kNormThreads / lay.V;
+    p = p < 1 ? 1 : p > d.l ? d.l : p;
+    lay.P = int(p);
+    lay.threads = (lay.P * lay.V + 31) / 32 * 32;
+    const int64_t want = (kNormCtas + d.n * lay.runs - 1) / (d.n * lay.runs);
+    const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
+    const int64_t splits = want < most ? want : most;
+    lay.range = ((d.l + splits - 1) / splits + p - 1) / p * p;
+    lay.splits = (d.l + lay.range - 1) / lay.range;
+    *out = lay;
+    return true;
+}
+
+size_t part_bytes(const tsx_norm_desc& d, const NormLayout& lay)
+{
+    const size_t b = size_t(d.n) * size_t(lay.splits) * size_t(lay.pieces) * size_t(d.groups) * sizeof(float2);
+    return (b + 15) / 16 * 16;
+}
+size_t chan_bytes(const tsx_norm_desc& d, const NormLayout& lay)
+{
+    return size_t(d.n) * size_t(lay.splits) * 2 * size_t(d.c) * sizeof(float);
+}
+
+int check_norm(const char* call, const tsx_norm_desc* d)
+{
+    if (!d)
+        return fail(TSX_ERR_INVALID, call, "no descriptor");
+    if (d->n < 0 || d->l < 0 || (d->n > 0 && d->l > (kMaxExtent - 1) / d->n))
+        return fail(TSX_ERR_INVALID, call, "n and l must be >= 0 and n * l under 2^31 - 1");
+    const int rc = check_shape(call, d->dtype, d->n * d->l, d->c, d->form, d->block);
+    if (rc != TSX_OK)
+        return rc;
+    if (d->param_dtype != TSX_F32 && d->param_dtype != d->dtype)
+        return fail(TSX_ERR_INVALID, call, "weight and bias are fp32 or of the element type");
+    if (!known_act(d->act))
+        return fail(TSX_ERR_INVALID, call, "unknown activation");
+    if (d->groups < 1 || d->c % d->groups != 0)
+        return fail(TSX_ERR_INVALID, call, "c must be a multiple of groups >= 1");
+    if (d->x_pitch < d->c || d->y_pitch < d->c)
+        return fail(TSX_ERR_INVALID, call, "a pitch is shorter than a row");
+    if (!(d->eps >= 0.f) || std::isinf(d->eps))
+        return fail(TSX_ERR_INVALID, call, "eps must be finite and >= 0");
+    return TSX_OK;
+}
+
+// Scratch that covers every layout the call may take, whatever its pointers'
+// alignment.
+size_t norm_workspace(const tsx_norm_desc& d, bool backward)
+{
+    size_t most = 0;
+    if (d.n == 0 || d.l == 0 || d.c == 0)
+        return 0;
+    for (int kind = 0; kind < 3; ++kind) {
+        NormLayout lay;
+        if (!norm_layout(d, kind > 0, kind == 2 ? d.block : 0, &lay))
+            continue;
+        const size_t b = part_bytes(d, lay) + (backward ? chan_bytes(d, lay) : 0);
+        most = b > most ? b : most;
+        if (kind == 0 && norm_layout(d, false, d.block, &lay)) {
+            const size_t h = part_bytes(d, lay);
+            most = h > most ? h : most;
+        }
+    }
+    return most;
+}
+
+int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, NormArgs* a)
+{
+    if (!norm_layout(d, vec, block, &a->lay) && !norm_layout(d, false, block, &a->lay))
+        return fail(TSX_ERR_UNSUPPORTED, call, "no layout");
+    if (a->lay.runs > kMaxChunks)
+        return fail(TSX_ERR_UNSUPPORTED, call, "rows are too long");
+    a->n = d.n;
+    a->l = d.l;
+    a->c = int(d.c);
+    a->groups = d.groups;
+    a->per_group = int(d.c / d.groups);
+    a->x_pitch = d.x_pitch;
+    a->y_pitch = d.y_pitch;
+    a->eps = d.eps;
+    a->act = d.act;
+    a->form = d.form;
+    a->block = d.block;
+    a->blocks = (d.c + d.block - 1) / d.block;
+    a->wide_params = d.param_dtype == TSX_F32;
+    return TSX_OK;
+}
+
+int check_scratch(const char* call, const tsx_norm_desc& d, bool backward, const void* workspace, size_t bytes)
+{
+    if (bytes < norm_workspace(d, backward) || !workspace)
+        return fail(TSX_ERR_INVALID, call, "the workspace is smaller than tsx_group_norm_workspace says");
+    if (!aligned(workspace, 16))
+        return fail(TSX_ERR_ALIGN, call, "the workspace must be 16-byte aligned");
+    return TSX_OK;
+}
+
+}  // namespace
+
+extern "C" int tsx_group_norm_workspace(const tsx_norm_desc* desc, int backward, size_t* bytes)
+{
+    const char* call = "tsx_group_norm_workspace";
+    const int rc = check_norm(call, desc);
+    if (rc != TSX_OK)
+        return rc;
+    if (!bytes)
+        return fail(TSX_ERR_INVALID, call, "bytes is required");
+    *bytes = norm_workspace(*desc, backward != 0);
+    set_last_error("");
+    return TSX_OK;
+}
+
+extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const void* weight, const void* bias, void* y,
+                              float* mean, float* rstd, void* q, float* scale, void* workspace,
+                              size_t workspace_bytes, tsx_stream_t stream)
+{
+    const char* call = "tsx_group_norm";
+    int rc = check_norm(call, desc);
+    if (rc != TSX_OK)
+        return rc;
+    const tsx_norm_desc& d = *desc;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!q != !scale)
+        return fail(TSX_ERR_INVALID, call, "q and scale come together");
+    if (d.n == 0 || d.c == 0)
+        return launched(cudaSuccess, call);
+    if (!mean || !rstd)
+        return fail(TSX_ERR_INVALID, call, "mean and rstd are required");
+    if (!aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    if (d.l == 0)
+        return launched(launch_norm_empty(mean, rstd, d.n * d.groups, d.eps, st), call);
+    if (!x || !weight || !bias || !y)
+        return fail(TSX_ERR_INVALID, call, "x, weight, bias and y are required");
+    const int es = elem_size(d.dtype), ps = elem_size(d.param_dtype);
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, ps) || !aligned(bias, ps) || !aligned(scale, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    rc = check_scratch(call, d, false, workspace, workspace_bytes);
+    if (rc != TSX_OK)
+        return rc;
+    const bool vec = vectors(x, d.c, d.x_pitch, es) && vectors(y, d.c, d.y_pitch, es) && held_vectors(q, d.c);
+    // the checkpoint rides along where runs can start on its blocks
+    NormLayout lay;
+    const bool ride = q && (norm_layout(d, vec, d.block, &lay) || norm_layout(d, false, d.block, &lay));
+    NormArgs a{};
+    rc = norm_args(call, d, vec, ride ? d.block : 0, &a);
+    if (rc != TSX_OK)
+        return rc;
+    if (q && !ride) {
+        // before y is written: y may be x
+        PackArgs p{};
+        rc = pack_args(call, d.dtype, d.n * d.l, d.c, d.x_pitch, d.form, d.block, x, q, scale, &p);
+        if (rc != TSX_OK)
+            return rc;
+        const cudaError_t e = launch_pack(d.dtype, p, x, HeldOut{q, scale}, st);
+        if (e != cudaSuccess)
+            return launched(e, call);
+    }
+    const NormScratch scratch{static_cast<float2*>(workspace), nullptr};
+    return launched(launch_norm(d.dtype, a, x, weight, bias, y, mean, rstd,
+                                ride ? HeldOut{q, scale} : HeldOut{nullptr, nullptr}, scratch, st),
+                    call);
+}
+
+extern "C" int tsx_group_norm_backward(const tsx_norm_desc* desc, const void* dy, const void* x, const void* q,
+                                       const float* scale, const void* weight, const void* bias, const float* mean,
+                                       const float* rstd, void* dx, float* dweight, float* dbias, void* workspace,
+                                       size_t workspace_bytes, tsx_stream_t stream)
+{
+    const char* call = "tsx_group_norm_backward";
+    int rc = check_norm(call, desc);
+    if (rc != TSX_OK)
+        return rc;
+    const tsx_norm_desc& d = *desc;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (d.c == 0)
+        return launched(cudaSuccess, call);
+    if (!dweight || !dbias)
+        return fail(TSX_ERR_INVALID, call, "dweight and dbias are required");
+    if (!aligned(dweight, 4) || !aligned(dbias, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    if (d.n == 0 || d.l == 0) {
+        cudaError_t e = cudaMemsetAsync(dweight, 0, size_t(d.c) * sizeof(float), st);
+        if (e == cudaSuccess)
+            e = cudaMemsetAsync(dbias, 0, size_t(d.c) * sizeof(float), st);
+        return launched(e, call);
+    }
+    if (!q != !scale || !x == !q)
+        return fail(TSX_ERR_INVALID, call, "either x, or its checkpoint q and scale");
+    if (!dy || !weight || !bias || !mean || !rstd || !dx)
+        return fail(TSX_ERR_INVALID, call, "dy, weight, bias, mean, rstd and dx are required");
+    const int es = elem_size(d.dtype), ps = elem_size(d.param_dtype);
+    if (!aligned(dy, es) || !aligned(x, es) || !aligned(dx, es) || !aligned(weight, ps) || !aligned(bias, ps) ||
+        !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(scale, 4))
+        return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
+    rc = check_scratch(call, d, true, workspace, workspace_bytes);
+    if (rc != TSX_OK)
+        return rc;
+    const bool vec = vectors(dy, d.c, d.y_pitch, es) && vectors(x, d.c, d.x_pitch, es) &&
+                     vectors(dx, d.c, d.x_pitch, es) && held_vectors(q, d.c);
+    NormArgs a{};
+    rc = norm_args(call, d, vec, 0, &a);
+    if (rc != TSX_OK)
+        return rc;
+    NormScratch scratch;
+    scratch.part = static_cast<float2*>(workspace);
+    scratch.chan = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(d, a.lay));
+    return launched(launch_norm_backward(d.dtype, a, dy, Saved{x, q, scale}, weight, bias, mean, rstd, dx, dweight,
+                                         dbias, scratch, st),
+                    call);
+}

@@ -1,0 +1,387 @@
+// Pieces shared by the layer kernels (group norm, gated activation, 8-bit
+// checkpoints): eight channels of a row at a time, the activations and the
+// 8-bit forms.
+//
+// A thread always works on eight channels of a row, an "oct".  Where every
+// row and operand allows it (VEC), they are consecutive and move as 16-byte
+// vectors (two for fp32, one 8-byte vector for 8-bit numbers).  Otherwise
+// they lie `step` channels apart, so that the `step` neighbouring threads of
+// a team read neighbouring elements, and each moves by itself with its
+// channel checked against the row's end.  Either way a team covers the same
+// 8 * step consecutive channels, so whatever is computed over a team (a
+// checkpoint block's largest magnitude) does not depend on the path.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+#include "layers.h"
+
+namespace tsx {
+namespace dev {
+
+// Where a thread's oct sits in a row: channels ch, ch + step, ..., those
+// under `cols` exist.  VEC: step 1, and all eight exist or none.
+struct OctAt {
+    int ch;
+    int step;
+    int cols;
+};
+
+template <bool VEC>
+__device__ __forceinline__ OctAt oct_at(int v, int team, int cols)
+{
+    OctAt o;
+    o.cols = cols;
+    if constexpr (VEC) {
+        o.ch = v * 8;
+        o.step = 1;
+    } else {
+        o.ch = v / team * 8 * team + v % team;
+        o.step = team;
+    }
+    return o;
+}
+
+// Eight elements as they lie in memory.
+template <int DT>
+struct Oct {
+    uint32_t w[DT == TSX_F32 ? 8 : 4];
+};
+
+template <int DT>
+__device__ __forceinline__ void oct_zero(Oct<DT>& o)
+{
+#pragma unroll
+    for (int i = 0; i < int(sizeof(o.w) / 4); ++i)
+        o.w[i] = 0;
+}
+
+// The vector loads go past L1.  They are no read-only-cache loads, since an
+// output may be one of the inputs; every thread loads what it overwrites
+// before it stores.
+template <int DT, bool VEC>
+__device__ __forceinline__ Oct<DT> oct_load(const void* base, int64_t row_elems, const OctAt& at)
+{
+    Oct<DT> o;
+    if constexpr (VEC) {
+        const char* p = static_cast<const char*>(base) + (row_elems + at.ch) * elem_size(DT);
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+            : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
+            : "l"(p));
+        if constexpr (DT == TSX_F32)
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                : "=r"(o.w[4]), "=r"(o.w[5]), "=r"(o.w[6]), "=r"(o.w[7])
+                : "l"(p + 16));
+    } else if constexpr (DT == TSX_F32) {
+        const float* p = static_cast<const float*>(base) + row_elems + at.ch;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o.w[j] = at.ch + j * at.step < at.cols ? __float_as_uint(p[j * at.step]) : 0u;
+    } else {
+        const unsigned short* p = static_cast<const unsigned short*>(base) + row_elems + at.ch;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = at.ch + 2 * j * at.step < at.cols ? p[2 * j * at.step] : 0;
+            const uint32_t hi = at.ch + (2 * j + 1) * at.step < at.cols ? p[(2 * j + 1) * at.step] : 0;
+            o.w[j] = lo | hi << 16;
+        }
+    }
+    return o;
+}
+
+template <int DT>
+__device__ __forceinline__ void oct_floats(const Oct<DT>& o, float (&f)[8])
+{
+    if constexpr (DT == TSX_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = __uint_as_float(o.w[j]);
+    } else if constexpr (DT == TSX_BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(o.w[j] << 16);
+            f[2 * j + 1] = __uint_as_float(o.w[j] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o.w[j]));
+            f[2 * j] = v.x;
+            f[2 * j + 1] = v.y;
+        }
+    }
+}
+
+// Rounded once, to nearest even, into the element type.
+template <int DT>
+__device__ __forceinline__ Oct<DT> oct_round(const float (&f)[8])
+{
+    Oct<DT> o;
+    if constexpr (DT == TSX_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o.w[j] = __float_as_uint(f[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == TSX_BF16) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                o.w[j] = *reinterpret_cast<const uint32_t*>(&v);
+            } else {
+                const __half2 v = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
+                o.w[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        }
+    }
+    return o;
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void oct_store(void* base, int64_t row_elems, const OctAt& at, const Oct<DT>& o)
+{
+    if constexpr (VEC) {
+        char* p = static_cast<char*>(base) + (row_elems + at.ch) * elem_size(DT);
+        *reinterpret_cast<uint4*>(p) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+        if constexpr (DT == TSX_F32)
+            *reinterpret_cast<uint4*>(p + 16) = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
+    } else if constexpr (DT == TSX_F32) {
+        uint32_t* p = static_cast<uint32_t*>(base) + row_elems + at.ch;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at.ch + j * at.step < at.cols)
+                p[j * at.step] = o.w[j];
+    } else {
+        unsigned short* p = static_cast<unsigned short*>(base) + row_elems + at.ch;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at.ch + j * at.step < at.cols)
+                p[j * at.step] = static_cast<unsigned short>(o.w[j / 2] >> (j % 2 * 16));
+    }
+}
+
+// Eight fp32 (or, for parameters given in the element type, narrower) values
+// of a per-channel vector.
+template <int DT, bool VEC>
+__device__ __forceinline__ void param_floats(const void* base, bool wide, int ch0, const OctAt& at, float (&f)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f[j] = 0.f;
+        if (at.ch + j * at.step < at.cols) {
+            const int ch = ch0 + at.ch + j * at.step;
+            if (wide || DT == TSX_F32)
+                f[j] = __ldg(static_cast<const float*>(base) + ch);
+            else if constexpr (DT == TSX_BF16)
+                f[j] = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[ch]);
+            else if constexpr (DT == TSX_F16)
+                f[j] = __half2float(static_cast<const __half*>(base)[ch]);
+        }
+    }
+}
+
+// ----------------------------------------------------------- activations
+
+// sigmoid(z) = 1 / (1 + exp(-z)).  fp32 data take expf and an IEEE division.
+// 16-bit data take the hardware base-2 exponential and reciprocal
+// (ex2.approx, rcp.approx: a few fp32 ulps each; the rounded product
+// z log2(e) adds 2^-24 |z| relative): under 2^-18 wherever the result is not
+// below 2^-40, against the 2^-11 (fp16) and 2^-8 (bf16) of the result's own
+// rounding.
+template <int DT>
+__device__ __forceinline__ float sigmoid(float z)
+{
+    if constexpr (DT == TSX_F32) {
+        return __fdiv_rn(1.f, 1.f + expf(-z));
+    } else {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504088896341f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return r;
+    }
+}
+
+// The tanh form of gelu through the sigmoid: tanh(u) = 2 sigmoid(2 u) - 1, so
+// gelu(z) = z sigmoid(2 k (z + 0.044715 z^3)), k = sqrt(2 / pi).  The argument
+// is taken at |z| <= 24, where the sigmoid has long reached 0 or 1 in fp32:
+// the cube of a large z stays finite, and 0 * infinity is never formed.
+constexpr float kGelu2K = 1.5957691216057308f;
+constexpr float kGeluCube = 0.044715f;
+
+template <int DT>
+__device__ __forceinline__ float act_value(float z, int act)
+{
+    if (act == TSX_ACT_SILU)
+        return z * sigmoid<DT>(z);
+    if (act == TSX_ACT_GELU) {
+        const float t = fminf(fmaxf(z, -24.f), 24.f);
+        return z * sigmoid<DT>(kGelu2K * t * (1.f + kGeluCube * t * t));
+    }
+    return z;
+}
+
+// act(z) and its derivative.
+template <int DT>
+__device__ __forceinline__ void act_both(float z, int act, float& value, float& slope)
+{
+    if (act == TSX_ACT_SILU) {
+        const float p = sigmoid<DT>(z);
+        value = z * p;
+        slope = p + value * (1.f - p);
+    } else if (act == TSX_ACT_GELU) {
+        const float t = fminf(fmaxf(z, -24.f), 24.f);
+        const float t2 = t * t;
+        const float p = sigmoid<DT>(kGelu2K * t * (1.f + kGeluCube * t2));
+        value = z * p;
+        slope = p + value * (1.f - p) * (kGelu2K * (1.f + 3.f * kGeluCube * t2));
+    } else {
+        value = z;
+        slope = 1.f;
+    }
+}
+
+// ------------------------------------------------------------ 8-bit forms
+
+// One scale of a block from the bits of its largest magnitude: amax / 127
+// (int8) or amax / 448 (e4m3, its largest number), as a product with the
+// rounded reciprocal; inv is the factor that takes values to the 8-bit
+// numbers.  Under 2^-119 the block is held as zeros with scale 0 (the
+// reciprocal of a smaller scale would overflow).  A block with an infinity or
+// a NaN in it gets the scale NaN and so reads back as NaN throughout: a
+// gradient check downstream sees it.
+struct HeldScale {
+    float scale, inv;
+};
+__device__ __forceinline__ HeldScale held_scale(uint32_t amax_bits, int form)
+{
+    HeldScale s;
+    s.scale = __fmul_rn(__uint_as_float(amax_bits), form == TSX_INT8 ? 1.f / 127.f : 1.f / 448.f);
+    s.inv = __frcp_rn(s.scale);
+    if (amax_bits < 0x04000000u)   // 2^-119
+        s.scale = s.inv = 0.f;
+    if (amax_bits >= 0x7f800000u) {
+        s.scale = __uint_as_float(0x7fc00000u);
+        s.inv = 0.f;
+    }
+    return s;
+}
+
+// The largest magnitude of an oct, as bits: unsigned integers order
+// magnitudes as floats do, with infinity above every number and NaN above
+// infinity, which a float maximum would drop.
+__device__ __forceinline__ uint32_t oct_amax_bits(const float (&f)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+    return m;
+}
+
+// The maximum over the `team` (a power of two) neighbouring lanes.
+__device__ __forceinline__ uint32_t team_max(uint32_t m, int team)
+{
+    for (int d = 1; d < team; d <<= 1)
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
+// Eight 8-bit numbers as they lie in memory (channel j in byte j).
+struct Held {
+    uint32_t w[2];
+};
+
+// x * inv rounded to nearest even into the 8-bit form.  int8: adding 1.5 *
+// 2^23 leaves the whole number in the sum's low byte (|x inv| <= 127 plus
+// rounding, well inside); the product is rounded by itself first.
+__device__ __forceinline__ Held held_round(const float (&f)[8], const HeldScale& s, int form)
+{
+    Held h;
+    if (form == TSX_INT8) {
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            b[j] = __float_as_uint(__fadd_rn(__fmul_rn(f[j], s.inv), 12582912.f));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            h.w[k] = __byte_perm(__byte_perm(b[4 * k], b[4 * k + 1], 0x0040),
+                                 __byte_perm(b[4 * k + 2], b[4 * k + 3], 0x0040), 0x5410);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                make_float2(__fmul_rn(f[4 * k], s.inv), __fmul_rn(f[4 * k + 1], s.inv)), __NV_SATFINITE, __NV_E4M3);
+            uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(__fmul_rn(f[4 * k + 2], s.inv), __fmul_rn(f[4 * k + 3], s.inv)), __NV_SATFINITE,
+                __NV_E4M3);
+            h.w[k] = lo | hi << 16;
+        }
+    }
+    if (s.inv == 0.f)   // zeros; also where 0 * infinity or NaN stood
+        h.w[0] = h.w[1] = 0;
+    return h;
+}
+
+// The fp32 values q * scale.  int8: the byte, offset by 128, becomes the low
+// byte of 2^23 + b; subtracting 2^23 + 128 leaves the number exactly, without
+// an integer conversion.
+__device__ __forceinline__ void held_floats(const Held& h, float scale, int form, float (&f)[8])
+{
+    if (form == TSX_INT8) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t u = h.w[k] ^ 0x80808080u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[4 * k + j] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 | j)) - 8388736.f) * scale;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const __half2_raw r =
+                    __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h.w[k] >> (16 * j)), __NV_E4M3);
+                const float2 v = __half22float2(__half2(r));
+                f[4 * k + 2 * j] = v.x * scale;
+                f[4 * k + 2 * j + 1] = v.y * scale;
+            }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ Held held_load(const void* q, int64_t row_elems, const OctAt& at)
+{
+    Held h;
+    const uint8_t* p = static_cast<const uint8_t*>(q) + row_elems + at.ch;
+    if constexpr (VEC) {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(h.w[0]), "=r"(h.w[1]) : "l"(p));
+    } else {
+        h.w[0] = h.w[1] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at.ch + j * at.step < at.cols)
+                h.w[j / 4] |= static_cast<uint32_t>(p[j * at.step]) << (j % 4 * 8);
+    }
+    return h;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void held_store(void* q, int64_t row_elems, const OctAt& at, const Held& h)
+{
+    uint8_t* p = static_cast<uint8_t*>(q) + row_elems + at.ch;
+    if constexpr (VEC) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(h.w[0], h.w[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at.ch + j * at.step < at.cols)
+                p[j * at.step] = static_cast<uint8_t>(h.w[j / 4] >> (j % 4 * 8));
+    }
+}
+
+}  // namespace dev
+}  // namespace tsx
