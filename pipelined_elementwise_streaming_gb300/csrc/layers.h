@@ -77,9 +77,19 @@ struct NormLayout {
     int runs;
     int pieces;          // runs to a group (1 unless a group is wider than a CTA's row)
     int V, P, threads;
-    int64_t splits;      // row ranges of a sample
-    int64_t range;       // rows to a range
+    int64_t splits;      // row ranges of a sample; token kernels: CTAs that share the rows of a run
+    int64_t range;       // rows to a range, or to a rank
+    // kernels that hold samples on chip: CTAs of a cluster that share a
+    // sample, samples side by side in a CTA, row lanes of each (P = samples * lanes)
+    int ranks, samples, lanes;
+    int kind;            // NormKind
 };
+// How a call runs: streaming kernels that read their operands twice (any
+// layout), samples held on chip, tokens whose groups lie within a warp.
+enum NormKind { kNormStream = 0, kNormHeld = 1, kNormToken = 2 };
+// Rows of its oct that a thread holds: forward, and backward (x and dz in fp32).
+constexpr int kNormHeldRows = 8;
+constexpr int kNormHeldGradRows = 4;
 
 struct NormArgs {
     NormLayout lay;
@@ -93,9 +103,9 @@ struct NormArgs {
 };
 
 // Scratch of one call (see tsx_group_norm_workspace):
-//   part   [n][splits * pieces][groups] pairs: (mean, sum of squared deviations) forward, the two
-//          sums of the gradient backward
-//   chan   [slices][2][c] backward: sums for dweight and dbias, slices = n * splits
+//   part   streaming: [n][splits * pieces][groups] pairs: (mean, sum of squared deviations)
+//          forward, the two sums of the gradient backward
+//   chan   [slices][2][c] backward: sums for dweight and dbias, one slice to each of a run's CTAs
 struct NormScratch {
     float2* part;
     float* chan;
@@ -106,6 +116,19 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
 cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,
                                  const void* bias, const float* mean, const float* rstd, void* dx, float* dweight,
                                  float* dbias, NormScratch scratch, cudaStream_t st);
+cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,
+                             float* mean, float* rstd, HeldOut held, cudaStream_t st);
+cudaError_t launch_norm_held_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,
+                                      const void* bias, const float* mean, const float* rstd, void* dx,
+                                      float* dweight, float* dbias, NormScratch scratch, cudaStream_t st);
+cudaError_t launch_norm_token(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias,
+                              void* y, float* mean, float* rstd, HeldOut held, cudaStream_t st);
+cudaError_t launch_norm_token_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,
+                                       const void* bias, const float* mean, const float* rstd, void* dx,
+                                       float* dweight, float* dbias, NormScratch scratch, cudaStream_t st);
+// dweight and dbias from [slices][2][c] partial sums.
+cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* chan, float* dweight, float* dbias,
+                               cudaStream_t st);
 // Results of samples without rows: mean 0, rstd 1 / sqrt(eps).
 cudaError_t launch_norm_empty(float* mean, float* rstd, int64_t count, float eps, cudaStream_t st);
 

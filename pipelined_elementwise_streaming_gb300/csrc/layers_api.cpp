@@ -11,6 +11,23 @@
 
 namespace tsx {
 
+namespace {
+
+int round_up(int64_t v, int to) { return int((v + to - 1) / to * to); }
+
+// Neighbouring threads that share a checkpoint block, or (vec false) read
+// neighbouring elements; no more than the octs need.
+int team_of(int64_t cols, int block, bool vec)
+{
+    const int64_t octs = (cols + kOct - 1) / kOct;
+    int team = block ? block / kOct : vec ? 1 : 16;
+    while (team > 1 && team / 2 >= octs)
+        team /= 2;
+    return team;
+}
+
+}  // namespace
+
 RowLayout row_layout(int64_t rows, int64_t cols, int block, bool vec, int want)
 {
     RowLayout lay{};
@@ -18,13 +35,9 @@ RowLayout row_layout(int64_t rows, int64_t cols, int block, bool vec, int want)
     lay.cols = int(cols);
     lay.vec = vec;
     const int64_t octs = (cols + kOct - 1) / kOct;
-    int team = block ? block / kOct : vec ? 1 : 16;
-    while (team > 1 && team / 2 >= octs)
-        team /= 2;
-    lay.team = team;
+    lay.team = team_of(cols, block, vec);
     const int64_t chunks = (octs + want - 1) / want;
-    int64_t v = (octs + chunks - 1) / chunks;
-    v = (v + team - 1) / team * team;
+    const int64_t v = round_up((octs + chunks - 1) / chunks, lay.team);
     lay.V = int(v);
     lay.chunk_cols = lay.V * kOct;
     lay.chunks = int((cols + lay.chunk_cols - 1) / lay.chunk_cols);
@@ -247,19 +260,26 @@ namespace {
 // for each channel and row lane, and for each group), and its threads.
 constexpr int kNormRun = 2048;
 constexpr int kNormThreads = 512;
+constexpr int kTokenRun = 2048;
+constexpr int kTokenThreads = 256;
+constexpr int64_t kTokenCtas = 8 * 152, kTokenGradCtas = 2 * 152;
+constexpr int64_t kNormRanks = 16;     // CTAs of a cluster at most
+constexpr int64_t kNormSamples = 64;   // samples side by side at most
+constexpr int64_t kNormHeldCtas = 2 * 152;
 // Ranges are cut until about this many CTAs share the work: four to each of
 // the 152 SMs.  A constant of the chip, not read from it, so that results
 // depend on the shape alone.
 constexpr int64_t kNormCtas = 4 * 152;
 constexpr int kNormRowsAtOnce = 4;
 
-// The layout for rows of c channels; block: channels to a scale where the
-// call writes checkpoints, else 0.  False if this alignment (vec, block)
-// cannot be had with these groups.
-bool norm_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
+// The streaming layout for rows of c channels; block: channels to a scale
+// where the call writes checkpoints, else 0.  False if this alignment (vec,
+// block) cannot be had with these groups.
+bool stream_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
 {
     const int64_t per = d.c / d.groups;
     NormLayout lay{};
+    lay.kind = kNormStream;
     lay.vec = vec;
     lay.oct_in_group = vec && per % kOct == 0;
     // runs start on whole octs / blocks
@@ -286,33 +306,144 @@ bool norm_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
         lay.pieces = 1;
         lay.runs = int((d.groups + groups - 1) / groups);
     }
-    const int octs = (lay.run_cols + kOct - 1) / kOct;
-    int team = block ? block / kOct : vec ? 1 : 16;
-    while (team > 1 && team / 2 >= octs)
-        team /= 2;
-    lay.team = team;
-    lay.V = (octs + team - 1) / team * team;
+    lay.team = team_of(lay.run_cols, block, vec);
+    lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
     int64_t p = kNormThreads / lay.V;
     p = p < 1 ? 1 : p > d.l ? d.l : p;
     lay.P = int(p);
-    lay.threads = (lay.P * lay.V + 31) / 32 * 32;
+    lay.threads = round_up(lay.P * lay.V, 32);
     const int64_t want = (kNormCtas + d.n * lay.runs - 1) / (d.n * lay.runs);
     const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
     const int64_t splits = want < most ? want : most;
     lay.range = ((d.l + splits - 1) / splits + p - 1) / p * p;
     lay.splits = (d.l + lay.range - 1) / lay.range;
+    lay.ranks = lay.samples = 1;
+    lay.lanes = lay.P;
     *out = lay;
     return true;
 }
 
+// Tokens: groups of a power of two of octs, at most a warp's.
+bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
+{
+    const int64_t per = d.c / d.groups;
+    if (d.l != 1 || !vec || per % kOct != 0 || per > 32 * kOct || (per & (per - 1)) != 0)
+        return false;
+    NormLayout lay{};
+    lay.kind = kNormToken;
+    lay.vec = lay.oct_in_group = true;
+    const int64_t align = block > per ? block : per;   // powers of two
+    const int64_t cols = d.c < kTokenRun ? d.c : kTokenRun / align * align;
+    lay.run_cols = int(cols);
+    lay.run_groups = int(cols / per);
+    lay.pieces = 1;
+    lay.runs = int((d.c + cols - 1) / cols);
+    lay.team = team_of(lay.run_cols, block, true);
+    const int own = int(per / kOct);
+    lay.V = round_up(lay.run_cols / kOct, own > lay.team ? own : lay.team);
+    int64_t p = kTokenThreads / lay.V;
+    p = p < 1 ? 1 : p > d.n ? d.n : p;
+    lay.P = int(p);
+    lay.threads = round_up(lay.P * lay.V, 32);
+    lay.range = 1;
+    lay.ranks = lay.samples = lay.lanes = 1;
+    const int64_t at_once = p * (backward ? 2 : 4);
+    const int64_t most = (d.n + at_once - 1) / at_once;
+    const int64_t want = ((backward ? kTokenGradCtas : kTokenCtas) + lay.runs - 1) / lay.runs;
+    lay.splits = most < want ? most : want;
+    *out = lay;
+    return true;
+}
+
+// Samples on chip.  Among runs of channels from the widest down to 128 bytes
+// a row, the widest that spreads the work over two CTAs to an SM, or else the
+// one that spreads it furthest; a sample too long for one CTA is shared by a
+// cluster, which also spreads small batches.
+bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
+{
+    const int64_t per = d.c / d.groups;
+    if (!vec || per > kNormRun)
+        return false;
+    const int rows = backward ? kNormHeldGradRows : kNormHeldRows;
+    const int64_t align = block ? block : kOct;
+    const int64_t unit = align / std::gcd(per, align);
+    int64_t best_ctas = 0;
+    int64_t groups = d.groups;
+    if (d.c > kNormRun)
+        groups = kNormRun / per / unit * unit;
+    for (; groups > 0;) {
+        NormLayout lay{};
+        lay.kind = kNormHeld;
+        lay.vec = true;
+        lay.oct_in_group = per % kOct == 0;
+        lay.run_groups = int(groups);
+        lay.run_cols = int(groups * per);
+        lay.pieces = 1;
+        lay.runs = int((d.groups + groups - 1) / groups);
+        lay.team = team_of(lay.run_cols, block, true);
+        lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
+        const int64_t lanes = kNormThreads / lay.V;   // >= 2
+        int64_t ranks = 1;
+        while (ranks < kNormRanks && ranks * lanes * rows < d.l)
+            ranks *= 2;
+        if (ranks * lanes * rows >= d.l) {
+            // spread further while a CTA keeps a few rows to a lane
+            while (ranks < 8 && d.n * lay.runs * ranks < kNormHeldCtas && d.l / (2 * ranks) >= 2 * lanes)
+                ranks *= 2;
+            lay.ranks = int(ranks);
+            lay.range = (d.l + ranks - 1) / ranks;   // the last ranks may have no rows
+            // row lanes: as many as there are rows, or fewer with several
+            // samples to a CTA where there are samples enough
+            int64_t own = lay.range < lanes ? lay.range : lanes;
+            int64_t samples = 1;
+            if (lay.ranks == 1 && own < lanes) {
+                const int64_t few = (d.l + rows - 1) / rows;
+                const int64_t most = d.n * lay.runs / kNormHeldCtas;   // keep this many CTAs
+                samples = lanes / few < most ? lanes / few : most;
+                samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
+                own = lanes / samples < own ? lanes / samples : own;
+            }
+            lay.samples = int(samples);
+            lay.lanes = int(own);
+            lay.P = int(samples * own);
+            lay.threads = round_up(lay.P * lay.V, 32);
+            lay.splits = 1;
+            const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * lay.ranks;
+            if (ctas > best_ctas) {
+                best_ctas = ctas;
+                *out = lay;
+            }
+            if (ctas >= kNormHeldCtas)
+                return true;
+        }
+        const int64_t next = (groups / 2 + unit - 1) / unit * unit;
+        if (next >= groups || next * per * elem_size(d.dtype) < 128)
+            break;
+        groups = next;
+    }
+    return best_ctas > 0;
+}
+
+// How a call runs.
+bool norm_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
+{
+    return token_layout(d, vec, block, backward, out) || held_layout(d, vec, block, backward, out) ||
+           stream_layout(d, vec, block, out);
+}
+
 size_t part_bytes(const tsx_norm_desc& d, const NormLayout& lay)
 {
+    if (lay.kind != kNormStream)
+        return 0;
     const size_t b = size_t(d.n) * size_t(lay.splits) * size_t(lay.pieces) * size_t(d.groups) * sizeof(float2);
     return (b + 15) / 16 * 16;
 }
 size_t chan_bytes(const tsx_norm_desc& d, const NormLayout& lay)
 {
-    return size_t(d.n) * size_t(lay.splits) * 2 * size_t(d.c) * sizeof(float);
+    const size_t slices = lay.kind == kNormToken  ? size_t(lay.splits)
+                          : lay.kind == kNormHeld ? size_t((d.n + lay.samples - 1) / lay.samples) * lay.ranks
+                                                  : size_t(d.n) * size_t(lay.splits);
+    return slices * 2 * size_t(d.c) * sizeof(float);
 }
 
 int check_norm(const char* call, const tsx_norm_desc* d)
@@ -344,23 +475,20 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward)
     size_t most = 0;
     if (d.n == 0 || d.l == 0 || d.c == 0)
         return 0;
-    for (int kind = 0; kind < 3; ++kind) {
-        NormLayout lay;
-        if (!norm_layout(d, kind > 0, kind == 2 ? d.block : 0, &lay))
-            continue;
-        const size_t b = part_bytes(d, lay) + (backward ? chan_bytes(d, lay) : 0);
-        most = b > most ? b : most;
-        if (kind == 0 && norm_layout(d, false, d.block, &lay)) {
-            const size_t h = part_bytes(d, lay);
-            most = h > most ? h : most;
+    for (int vec = 0; vec < 2; ++vec)
+        for (int block : {0, d.block}) {
+            NormLayout lay;
+            if ((backward && block) || !norm_layout(d, vec != 0, block, backward, &lay))
+                continue;
+            const size_t b = part_bytes(d, lay) + (backward ? chan_bytes(d, lay) : 0);
+            most = b > most ? b : most;
         }
-    }
-    return most;
+    return most > 16 ? most : 16;
 }
 
-int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, NormArgs* a)
+int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, NormArgs* a)
 {
-    if (!norm_layout(d, vec, block, &a->lay) && !norm_layout(d, false, block, &a->lay))
+    if (!norm_layout(d, vec, block, backward, &a->lay) && !norm_layout(d, false, block, backward, &a->lay))
         return fail(TSX_ERR_UNSUPPORTED, call, "no layout");
     if (a->lay.runs > kMaxChunks)
         return fail(TSX_ERR_UNSUPPORTED, call, "rows are too long");
@@ -435,9 +563,9 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
     const bool vec = vectors(x, d.c, d.x_pitch, es) && vectors(y, d.c, d.y_pitch, es) && held_vectors(q, d.c);
     // the checkpoint rides along where runs can start on its blocks
     NormLayout lay;
-    const bool ride = q && (norm_layout(d, vec, d.block, &lay) || norm_layout(d, false, d.block, &lay));
+    const bool ride = q && (norm_layout(d, vec, d.block, false, &lay) || norm_layout(d, false, d.block, false, &lay));
     NormArgs a{};
-    rc = norm_args(call, d, vec, ride ? d.block : 0, &a);
+    rc = norm_args(call, d, vec, ride ? d.block : 0, false, &a);
     if (rc != TSX_OK)
         return rc;
     if (q && !ride) {
@@ -451,9 +579,15 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
             return launched(e, call);
     }
     const NormScratch scratch{static_cast<float2*>(workspace), nullptr};
-    return launched(launch_norm(d.dtype, a, x, weight, bias, y, mean, rstd,
-                                ride ? HeldOut{q, scale} : HeldOut{nullptr, nullptr}, scratch, st),
-                    call);
+    const HeldOut held = ride ? HeldOut{q, scale} : HeldOut{nullptr, nullptr};
+    cudaError_t e;
+    if (a.lay.kind == kNormToken)
+        e = launch_norm_token(d.dtype, a, x, weight, bias, y, mean, rstd, held, st);
+    else if (a.lay.kind == kNormHeld)
+        e = launch_norm_held(d.dtype, a, x, weight, bias, y, mean, rstd, held, st);
+    else
+        e = launch_norm(d.dtype, a, x, weight, bias, y, mean, rstd, held, scratch, st);
+    return launched(e, call);
 }
 
 extern "C" int tsx_group_norm_backward(const tsx_norm_desc* desc, const void* dy, const void* x, const void* q,
@@ -493,13 +627,15 @@ extern "C" int tsx_group_norm_backward(const tsx_norm_desc* desc, const void* dy
     const bool vec = vectors(dy, d.c, d.y_pitch, es) && vectors(x, d.c, d.x_pitch, es) &&
                      vectors(dx, d.c, d.x_pitch, es) && held_vectors(q, d.c);
     NormArgs a{};
-    rc = norm_args(call, d, vec, 0, &a);
+    rc = norm_args(call, d, vec, 0, true, &a);
     if (rc != TSX_OK)
         return rc;
     NormScratch scratch;
     scratch.part = static_cast<float2*>(workspace);
     scratch.chan = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(d, a.lay));
-    return launched(launch_norm_backward(d.dtype, a, dy, Saved{x, q, scale}, weight, bias, mean, rstd, dx, dweight,
-                                         dbias, scratch, st),
-                    call);
+    const Saved saved{x, q, scale};
+    const auto run = a.lay.kind == kNormToken  ? launch_norm_token_backward
+                     : a.lay.kind == kNormHeld ? launch_norm_held_backward
+                                               : launch_norm_backward;
+    return launched(run(d.dtype, a, dy, saved, weight, bias, mean, rstd, dx, dweight, dbias, scratch, st), call);
 }

@@ -59,7 +59,8 @@ tsx_group_norm_backward = lib.tsx_group_norm_backward
 
 class Checkpoint(NamedTuple):
     """A tensor held in 8 bits: q (int8 or float8_e4m3fn) stands for
-    q * scale, one fp32 scale to a block of a row's channels."""
+    q * scale, one fp32 scale to a block of a row's channels.  The calls take
+    any (q, scale) tuple."""
     q: object
     scale: object
 
@@ -234,9 +235,9 @@ class GatedAct(_Layer):
         or both Checkpoints."""
         with self._on(dh, stream) as w:
             pd = self._rows(dh, self.out_pitch, "dh", w.device)
-            if isinstance(gate, Checkpoint) != isinstance(up, Checkpoint):
+            if isinstance(gate, tuple) != isinstance(up, tuple):
                 _invalid("gate and up are either two tensors or two Checkpoints")
-            if isinstance(gate, Checkpoint):
+            if isinstance(gate, tuple):
                 saved = (None, None, *self._saved(gate, "gate", w.device), *self._saved(up, "up", w.device))
             else:
                 saved = (self._rows(gate, self.in_pitch, "gate", w.device),
@@ -303,7 +304,7 @@ class GroupNorm(_Layer):
         t = self._torch
         with self._on(dy, stream) as w:
             pdy = self._rows(dy, self.y_pitch, "dy", w.device, self._shape)
-            if isinstance(saved, Checkpoint):
+            if isinstance(saved, tuple):
                 src = (None, *self._saved(saved, "saved", w.device))
             else:
                 src = (self._rows(saved, self.x_pitch, "saved", w.device, self._shape), None, None)

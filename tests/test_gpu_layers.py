@@ -116,6 +116,19 @@ def test_norm_and_its_gradient(tsx, shape, dtype):
         check_norm(tsx, n, l, c, groups, dtype, act, seed=1000 * k + n + l + c)
 
 
+# what decides how a call runs: tokens whose groups lie within a warp (and not); small samples side by side in a CTA;
+# samples shared by clusters of 2, 8 and 16 CTAs, with ranks left without rows; samples only just too long for that
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [
+    (3000, 1, 512, 8), (40, 1, 1280, 5), (3, 1, 4096, 2), (9, 1, 24, 3), (700, 3, 64, 8), (900, 7, 320, 32),
+    (2000, 2, 16, 16), (1, 1000, 2048, 1), (1, 100, 2048, 1), (2, 4000, 64, 4), (1, 8192, 64, 2), (1, 8200, 64, 64),
+    (1, 17, 2048, 2048), (16, 300, 96, 4), (3, 512, 640, 32),
+], ids=lambda s: "x".join(map(str, s)))
+def test_norm_however_it_runs(tsx, shape, dtype):
+    n, l, c, groups = shape
+    check_norm(tsx, n, l, c, groups, dtype, "silu", seed=n + l + c)
+
+
 def check_norm(tsx, n, l, c, groups, dtype, act, seed, offset=0.3, x_pitch=None, y_pitch=None, param="f32", eps=1e-5,
                form="int8", block=128):
     x, x64 = values((n, l, c), dtype, seed, 1.5, offset)
