@@ -43,7 +43,7 @@ __device__ __forceinline__ Place place(const RowLayout& lay, int rows_at_once)
 // An oct to 8 bits with its team's scale, both stored.  Called by whole
 // warps; `live` threads hold channels.
 template <bool VEC>
-__device__ __forceinline__ void hold(const float (&f)[8], bool live, const Place& s, int64_t row, int team, int cols,
+__device__ __forceinline__ void hold(const float2 (&f)[4], bool live, const Place& s, int64_t row, int team, int cols,
                                      int block, int64_t blocks, int form, const HeldOut& out)
 {
     const uint32_t m = team_max(live ? oct_amax_bits(f) : 0u, team);
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kLayerThreads) pack_kernel(PackArgs a, const v
 #pragma unroll
     for (int i = 0; i < kRowsAtOnce; ++i) {
         const int64_t r = s.row0 + i * a.lay.P;
-        float f[8];
+        float2 f[4];
         oct_floats(o[i], f);
         hold<VEC>(f, s.live && r < a.lay.rows, s, r, a.lay.team, a.lay.cols, a.block, a.blocks, a.form, held);
     }
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kLayerThreads) unpack_kernel(PackArgs a, const
     for (int i = 0; i < kRowsAtOnce; ++i) {
         const int64_t r = s.row0 + i * a.lay.P;
         if (s.live && r < a.lay.rows) {
-            float f[8];
+            float2 f[4];
             held_floats(h[i], sc[i], a.form, f);
             oct_store<DT, VEC>(x, r * a.pitch + s.chunk0, s.at, oct_round<DT>(f));
         }
@@ -131,12 +131,13 @@ __global__ void __launch_bounds__(kLayerThreads)
     for (int i = 0; i < kGatedRows; ++i) {
         const int64_t r = s.row0 + i * a.lay.P;
         const bool live = s.live && r < a.lay.rows;
-        float fg[8], fu[8], fh[8];
+        float2 fg[4], fu[4], fh[4];
         oct_floats(g[i], fg);
         oct_floats(u[i], fu);
+        act_value(a.act, fg, fh);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            fh[j] = act_value<DT>(fg[j], a.act) * fu[j];
+        for (int j = 0; j < 4; ++j)
+            fh[j] = __fmul2_rn(fh[j], fu[j]);
         if (live)
             oct_store<DT, VEC>(h, r * a.out_pitch + s.chunk0, s.at, oct_round<DT>(fh));
         if constexpr (HOLD) {
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kLayerThreads)
         const int64_t r = s.row0 + i * a.lay.P;
         if (!(s.live && r < a.lay.rows))
             continue;
-        float fd[8], fg[8], fu[8];
+        float2 fd[4], fg[4], fu[4];
         oct_floats(d[i], fd);
         if constexpr (HELD) {
             held_floats(qg[i], sg[i], a.form, fg);
@@ -184,14 +185,13 @@ __global__ void __launch_bounds__(kLayerThreads)
             oct_floats(g[i], fg);
             oct_floats(u[i], fu);
         }
-        float og[8], ou[8], oh[8];
+        float2 og[4], ou[4], oh[4], value[4], slope[4];
+        act_both(a.act, fg, value, slope);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float value, slope;
-            act_both<DT>(fg[j], a.act, value, slope);
-            og[j] = fd[j] * fu[j] * slope;
-            ou[j] = fd[j] * value;
-            oh[j] = value * fu[j];
+        for (int j = 0; j < 4; ++j) {
+            og[j] = __fmul2_rn(__fmul2_rn(fd[j], fu[j]), slope[j]);
+            ou[j] = __fmul2_rn(fd[j], value[j]);
+            oh[j] = __fmul2_rn(value[j], fu[j]);
         }
         oct_store<DT, VEC>(dgate, r * a.in_pitch + s.chunk0, s.at, oct_round<DT>(og));
         oct_store<DT, VEC>(dup, r * a.in_pitch + s.chunk0, s.at, oct_round<DT>(ou));

@@ -11,13 +11,16 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRowsAtOnce = 4;   // rows whose loads a thread issues before it uses the first
+constexpr int kRowsAtOnce = 4;   // rows whose loads a thread issues together, one batch ahead of their use
+constexpr int kGradRows = 2;     // two operands: half as many
 
-// A CTA's range of rows: blockIdx.x counts ranges sample by sample.
+// A CTA's range of rows: blockIdx.x counts ranges sample by sample.  The
+// `ranks` CTAs of a cluster take neighbouring ranges and join their sums.
 struct Range {
     int64_t sample, split;
     int64_t row0;   // first row, counted through all samples
     int rows;       // rows of the range
+    int rank;
 };
 
 __device__ __forceinline__ Range range_of(const NormArgs& a)
@@ -26,60 +29,87 @@ __device__ __forceinline__ Range range_of(const NormArgs& a)
     const unsigned splits = static_cast<unsigned>(a.lay.splits);
     r.sample = blockIdx.x / splits;
     r.split = blockIdx.x % splits;
+    r.rank = static_cast<int>(static_cast<unsigned>(r.split) % static_cast<unsigned>(a.lay.ranks));
     r.row0 = r.sample * a.l + r.split * a.lay.range;
-    r.rows = static_cast<int>(min(a.lay.range, a.l - r.split * a.lay.range));
+    r.rows = range_rows(a, a.lay.range, r.split);
     return r;
 }
 
-// A range's place among the parts of its sample.
+// The parts of a sample: one to each cluster and piece.
+__device__ __forceinline__ int parts_of(const NormArgs& a) { return static_cast<int>(a.lay.splits) / a.lay.ranks * a.lay.pieces; }
+
 __device__ __forceinline__ float2* part_of(const NormArgs& a, const NormPlace& s, const Range& r, float2* part)
 {
-    return part + ((r.sample * a.lay.splits + r.split) * a.lay.pieces + s.piece) * a.groups + s.group0;
+    return part + (r.sample * parts_of(a) + r.split / a.lay.ranks * a.lay.pieces + s.piece) * a.groups + s.group0;
 }
 
 // ------------------------------------------------------------- forward
 
-// First kernel: (mean, M2) of every range, run and group.
-template <int DT, bool VEC, bool BY_OCT>
-__global__ void __launch_bounds__(kLayerThreads) norm_stats_kernel(NormArgs a, const void* x, float2* part)
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_rows(const NormArgs& a, const NormPlace& s, const Range& r, const void* x,
+                                          int r0, Oct<DT> (&o)[kRowsAtOnce])
 {
-    extern __shared__ float2 slots[];   // [P][width], then P counts
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i)
+        if (s.live && r0 + i * a.lay.P < r.rows)
+            o[i] = oct_load<DT, VEC>(x, (r.row0 + r0 + i * a.lay.P) * a.x_pitch + s.ch0, s.at);
+        else
+            oct_zero(o[i]);
+}
+
+// First kernel: (mean, M2) of every cluster's range, run and group.
+template <int DT, bool VEC, bool BY_OCT>
+__global__ void __launch_bounds__(kNormThreads, DT == TSX_F32 ? 2 : 3) norm_stats_kernel(NormArgs a, const void* x, float2* part)
+{
+    extern __shared__ float4 shared4[];
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a);
-    const int P = a.lay.P;
-    Triples<BY_OCT ? 1 : 8> t;
+    const int P = a.lay.P, width = run_width<BY_OCT>(s), stride = slot_stride(width);
+    float4* spare = shared4;                                                    // [warps]
+    float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);        // [run_groups]
+    float2* slots = sums + a.lay.run_groups;                                    // [P][stride]
+    Triples<BY_OCT> t;
     t.clear();
+    Oct<DT> o[kRowsAtOnce];
+    load_rows<DT, VEC>(a, s, r, x, s.p, o);
     for (int r0 = s.p; s.live && r0 < r.rows; r0 += kRowsAtOnce * P) {
-        Oct<DT> o[kRowsAtOnce];
-        int have = 0;
-#pragma unroll
-        for (int i = 0; i < kRowsAtOnce; ++i)
-            if (r0 + i * P < r.rows) {
-                o[i] = oct_load<DT, VEC>(x, (r.row0 + r0 + i * P) * a.x_pitch + s.ch0, s.at);
-                have = i + 1;
-            }
-        float f[kRowsAtOnce][8];
+        Oct<DT> next[kRowsAtOnce];
+        load_rows<DT, VEC>(a, s, r, x, r0 + kRowsAtOnce * P, next);
+        float2 f[kRowsAtOnce][4];
 #pragma unroll
         for (int i = 0; i < kRowsAtOnce; ++i)
             oct_floats(o[i], f[i]);
-        t.add_rows(f, have);
-    }
-    const int width = run_width<BY_OCT>(s);
-    float* counts = reinterpret_cast<float*>(slots + P * width);
-    join_lanes(s, s.p, P, slots, counts, width, t);
-    if (s.live && s.p == 0) {
-        if constexpr (BY_OCT) {
-            slots[s.at.ch / 8] = make_float2(t.mean[0], t.m2[0]);
-        } else {
+        if (r0 + (kRowsAtOnce - 1) * P < r.rows)
+            t.template add_rows<kRowsAtOnce, true>(f, kRowsAtOnce);
+        else
+            t.template add_rows<kRowsAtOnce, false>(f, (r.rows - r0 + P - 1) / P);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (s.at.ch + j * s.at.step < s.at.cols)
-                    slots[s.at.ch + j * s.at.step] = make_float2(t.mean[j], t.m2[j]);
-        }
+        for (int i = 0; i < kRowsAtOnce; ++i)
+            o[i] = next[i];
     }
+    if (s.live)
+        t.leave(s.at, slots + s.p * stride);
     __syncthreads();
-    join_columns(slots, s.groups, group_cols(a, s) / (BY_OCT ? 8 : 1), r.rows * (BY_OCT ? 8.f : 1.f),
-                 part_of(a, s, r, part));
+    float2* out = part_of(a, s, r, part);
+    join_groups(slots, stride, 1, s.groups, P, group_cols(a, s) / (BY_OCT ? 8 : 1), r.rows, BY_OCT ? 8.f : 1.f,
+                a.lay.ranks > 1 ? sums : out, spare);
+    if (a.lay.ranks > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (r.rank == 0)
+            for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
+                Triples<true> j;
+                j.clear();
+                for (int k = 0; k < a.lay.ranks; ++k) {
+                    const float2 u = cluster_pair(sums + g, k);
+                    const float mu[1] = {u.x}, dev[1] = {u.y};
+                    j.join(static_cast<float>(range_rows(a, a.lay.range, r.split + k)) * group_cols(a, s), mu, dev);
+                }
+                out[g] = make_float2(j.mean[0], j.m2[0]);
+            }
+        cluster_arrive();   // the others may leave once rank 0 has read them
+        cluster_wait();
+    }
 }
 
 // The statistics of the run's groups from their parts, into `stats` [groups]
@@ -88,7 +118,7 @@ __global__ void __launch_bounds__(kLayerThreads) norm_stats_kernel(NormArgs a, c
 __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s, int64_t sample, const float2* part,
                                            float2* stats, float4* work)
 {
-    const int count = static_cast<int>(a.lay.splits) * a.lay.pieces;
+    const int count = parts_of(a);
     const float2* first = part + sample * count * a.groups + s.group0;
     const float m = static_cast<float>(a.l) * static_cast<float>(a.per_group);
     const int threads = static_cast<int>(blockDim.x);
@@ -96,21 +126,17 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
     const int lanes = s.groups < threads ? threads / s.groups : 1;
     for (int i = threadIdx.x; i < lanes * s.groups; i += threads) {
         const int lane = i / s.groups, g = i - lane * s.groups;
-        Triples<1> t;
+        Triples<true> t;
         t.clear();
-        int split = lane / a.lay.pieces, piece = lane - split * a.lay.pieces;
 #pragma unroll 4
         for (int k = lane; k < count; k += lanes) {
             const float2 v = first[static_cast<int64_t>(k) * a.groups + g];
-            if (a.lay.pieces == 1) {
-                split = k;
-            } else {
-                split = k / a.lay.pieces;
-                piece = k - split * a.lay.pieces;
+            int range = k, cols = a.per_group;
+            if (a.lay.pieces > 1) {
+                range = k / a.lay.pieces;
+                cols = min(a.lay.run_cols, a.per_group - (k - range * a.lay.pieces) * a.lay.run_cols);
             }
-            const float rows = static_cast<float>(min(a.lay.range, a.l - split * a.lay.range));
-            const int cols =
-                a.lay.pieces == 1 ? a.per_group : min(a.lay.run_cols, a.per_group - piece * a.lay.run_cols);
+            const float rows = static_cast<float>(range_rows(a, a.lay.range * a.lay.ranks, range));
             const float mu[1] = {v.x}, dev[1] = {v.y};
             t.join(rows * static_cast<float>(cols), mu, dev);
         }
@@ -118,7 +144,7 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
     }
     __syncthreads();
     for (int g = threadIdx.x; g < s.groups; g += threads) {
-        Triples<1> t;
+        Triples<true> t;
         t.clear();
         for (int k = 0; k < lanes; ++k) {
             const float4 v = work[k * s.groups + g];
@@ -132,13 +158,16 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
 
 // Second kernel: y, and with HOLD the checkpoint of x.
 template <int DT, bool VEC, bool BY_OCT, bool HOLD>
-__global__ void __launch_bounds__(kLayerThreads)
+__global__ void __launch_bounds__(kNormThreads, DT == TSX_F32 ? 2 : 3)
     norm_apply_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                       float* rstd, HeldOut held, const float2* part)
 {
     extern __shared__ float4 work[];   // [threads or groups], then [run_groups] statistics
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a);
+    const int P = a.lay.P;
+    Oct<DT> o[kRowsAtOnce];
+    load_rows<DT, VEC>(a, s, r, x, s.p, o);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
@@ -149,33 +178,38 @@ __global__ void __launch_bounds__(kLayerThreads)
             mean[r.sample * a.groups + s.group0 + g] = stats[g].x;
             rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
         }
-    const int P = a.lay.P;
     // whole warps walk together: the teams' shuffles need every lane
     for (int base = 0; base < r.rows; base += kRowsAtOnce * P) {
         const int r0 = base + s.p;
-        Oct<DT> o[kRowsAtOnce];
-#pragma unroll
-        for (int i = 0; i < kRowsAtOnce; ++i)
-            if (s.live && r0 + i * P < r.rows)
-                o[i] = oct_load<DT, VEC>(x, (r.row0 + r0 + i * P) * a.x_pitch + s.ch0, s.at);
-            else
-                oct_zero(o[i]);
+        Oct<DT> next[kRowsAtOnce];
+        load_rows<DT, VEC>(a, s, r, x, r0 + kRowsAtOnce * P, next);
 #pragma unroll
         for (int i = 0; i < kRowsAtOnce; ++i) {
             const int64_t row = r.row0 + r0 + i * P;
             const bool live = s.live && r0 + i * P < r.rows;
-            float f[8], out[8];
+            float2 f[4], out[4];
             oct_floats(o[i], f);
-            k.template apply<DT>(a, f, out);
+            k.apply(a, f, out);
             if (live)
                 oct_store<DT, VEC>(y, row * a.y_pitch + s.ch0, s.at, oct_round<DT>(out));
             if constexpr (HOLD)
                 hold<VEC>(a, s, f, live, row, held);
+            o[i] = next[i];
         }
     }
 }
 
 // ------------------------------------------------------------ backward
+
+template <int DT, bool VEC, bool HELD>
+__device__ __forceinline__ void load_grad_rows(const NormArgs& a, const NormPlace& s, const Range& r, const void* dy,
+                                               const Saved& x, int r0, GradRow<DT, VEC, HELD> (&g)[kGradRows])
+{
+#pragma unroll
+    for (int i = 0; i < kGradRows; ++i)
+        if (s.live && r0 + i * a.lay.P < r.rows)
+            g[i].load(a, s, dy, x, r.row0 + r0 + i * a.lay.P);
+}
 
 __device__ __forceinline__ void load_stats(const NormArgs& a, const NormPlace& s, int64_t sample, const float* mean,
                                            const float* rstd, float2* stats)
@@ -187,132 +221,132 @@ __device__ __forceinline__ void load_stats(const NormArgs& a, const NormPlace& s
     __syncthreads();
 }
 
-constexpr int kGradRows = 2;   // two operands: half as many rows at once
-
-// First kernel: S1 and S2 of every range, run and group, and the range's sums
-// for dweight and dbias.
+// First kernel: S1 and S2 of every cluster's range, run and group, and the
+// range's sums for dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
-__global__ void __launch_bounds__(kLayerThreads)
+__global__ void __launch_bounds__(kNormThreads, 2)
     norm_sums_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, float2* part, float* chan)
 {
     extern __shared__ float2 shared[];
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a);
-    float2* stats = shared;                       // [run_groups]
-    float2* slots = shared + a.lay.run_groups;    // [P][run_cols]
+    const int P = a.lay.P, width = s.at.cols, stride = slot_stride(width);
+    float2* stats = shared;                         // [run_groups]: (mean, rstd), then (S1, S2)
+    float2* work = stats + a.lay.run_groups;        // [threads]
+    float2* columns = work + kNormThreads;          // [run_cols]
+    float2* slots = columns + a.lay.run_cols;       // [P][stride]
+    GradRow<DT, VEC, HELD> g[kGradRows];
+    load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, s.p, g);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     load_stats(a, s, r.sample, mean, rstd, stats);
     k.statistics(a, s, stats);
-    float sz[8], szx[8];   // sums of dz and dz xhat, channel by channel
+    float2 sz[4], szx[4];   // sums of dz and dz xhat, channel by channel
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        sz[j] = szx[j] = 0.f;
-    const int P = a.lay.P;
+    for (int j = 0; j < 4; ++j)
+        sz[j] = szx[j] = make_float2(0.f, 0.f);
     for (int r0 = s.p; s.live && r0 < r.rows; r0 += kGradRows * P) {
-        GradRow<DT, VEC, HELD> g[kGradRows];
+        GradRow<DT, VEC, HELD> next[kGradRows];
+        load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, r0 + kGradRows * P, next);
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (r0 + i * P < r.rows)
-                g[i].load(a, s, dy, x, r.row0 + r0 + i * P);
-#pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
+        for (int i = 0; i < kGradRows; ++i) {
             if (r0 + i * P < r.rows) {
-                float fd[8], fx[8], hat[8], dz[8];
-                g[i].floats(a, fd, fx);
-                k.template slopes<DT>(a, fd, fx, hat, dz);
+                float2 fd[4], fx[4], hat[4], dz[4];
+                oct_floats(g[i].dy, fd);
+                g[i].saved_floats(a, fx);
+                k.slopes(a, fd, fx, hat, dz);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sz[j] += dz[j];
-                    szx[j] += dz[j] * hat[j];
+                for (int j = 0; j < 4; ++j) {
+                    sz[j] = __fadd2_rn(sz[j], dz[j]);
+                    szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
                 }
             }
-    }
-    add_lanes(s, s.p, P, slots, s.at.cols, sz, szx);
-    if (s.live && s.p == 0) {
-        float* out = chan + (r.sample * a.lay.splits + r.split) * 2 * a.c + s.ch0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int ch = s.at.ch + j * s.at.step;
-            if (ch < s.at.cols) {
-                slots[ch] = make_float2(sz[j], szx[j]);
-                out[ch] = szx[j];
-                out[a.c + ch] = sz[j];
-            }
+            g[i] = next[i];
         }
     }
+    if (s.live)
+        leave_sums(s.at, sz, szx, slots + s.p * stride);
     __syncthreads();
-    weigh_columns<DT>(a, s, weight, slots, part_of(a, s, r, part));
+    sum_lanes(slots, stride, 1, P, width, columns, work);
+    float* out = chan + (r.sample * a.lay.splits + r.split) * 2 * a.c + s.ch0;
+    for (int ch = threadIdx.x; ch < width; ch += blockDim.x) {
+        out[ch] = columns[ch].y;
+        out[a.c + ch] = columns[ch].x;
+    }
+    float2* sums = part_of(a, s, r, part);
+    weigh_columns<DT>(a, s, 1, width, weight, columns, a.lay.ranks > 1 ? stats : sums);
+    if (a.lay.ranks > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (r.rank == 0)
+            for (int i = threadIdx.x; i < s.groups; i += blockDim.x) {
+                float2 t = make_float2(0.f, 0.f);
+                for (int n = 0; n < a.lay.ranks; ++n)
+                    t = __fadd2_rn(t, cluster_pair(stats + i, n));
+                sums[i] = t;
+            }
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Second kernel: dx.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
-__global__ void __launch_bounds__(kLayerThreads)
+__global__ void __launch_bounds__(kNormThreads, 2)
     norm_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, void* dx, const float2* part)
 {
     extern __shared__ float2 shared[];
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a);
+    const int P = a.lay.P;
     float2* stats = shared;                      // [run_groups]
-    float2* sums = stats + a.lay.run_groups;     // [run_groups]: S1 / M, S2 / M
+    float2* sums = stats + a.lay.run_groups;     // [run_groups]: -S1 / M, -S2 / M
     float2* work = sums + a.lay.run_groups;      // [threads or groups]
+    GradRow<DT, VEC, HELD> g[kGradRows];
+    load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, s.p, g);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
-    const int count = static_cast<int>(a.lay.splits) * a.lay.pieces;
+    const int count = parts_of(a);
     const float2* first = part + r.sample * count * a.groups + s.group0;
-    const float m = static_cast<float>(a.l) * static_cast<float>(a.per_group);
+    const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
     const int threads = static_cast<int>(blockDim.x);
     const int lanes = s.groups < threads ? threads / s.groups : 1;
     for (int i = threadIdx.x; i < lanes * s.groups; i += threads) {
-        const int lane = i / s.groups, g = i - lane * s.groups;
+        const int lane = i / s.groups, group = i - lane * s.groups;
         float2 t = make_float2(0.f, 0.f);
 #pragma unroll 4
-        for (int n = lane; n < count; n += lanes) {
-            const float2 v = first[static_cast<int64_t>(n) * a.groups + g];
-            t.x += v.x;
-            t.y += v.y;
-        }
+        for (int n = lane; n < count; n += lanes)
+            t = __fadd2_rn(t, first[static_cast<int64_t>(n) * a.groups + group]);
         work[i] = t;
     }
     __syncthreads();
-    for (int g = threadIdx.x; g < s.groups; g += threads) {
-        float2 t = work[g];
-        for (int n = 1; n < lanes; ++n) {
-            t.x += work[n * s.groups + g].x;
-            t.y += work[n * s.groups + g].y;
-        }
-        sums[g] = make_float2(t.x / m, t.y / m);
+    for (int i = threadIdx.x; i < s.groups; i += threads) {
+        float2 t = work[i];
+        for (int n = 1; n < lanes; ++n)
+            t = __fadd2_rn(t, work[n * s.groups + i]);
+        sums[i] = make_float2(t.x / m, t.y / m);
     }
     load_stats(a, s, r.sample, mean, rstd, stats);   // synchronises
     k.statistics(a, s, stats);
-    float s1[BY_OCT ? 1 : 8], s2[BY_OCT ? 1 : 8];
-#pragma unroll
-    for (int j = 0; j < (BY_OCT ? 1 : 8); ++j) {
-        const int ch = s.at.ch + j * s.at.step;
-        const float2 t = sums[ch < s.at.cols ? local_group(a, ch) : 0];
-        s1[j] = t.x;
-        s2[j] = t.y;
-    }
-    const int P = a.lay.P;
+    Grouped<BY_OCT> s1, s2;
+    grouped<BY_OCT>(a, s, sums, s1, s2);
     for (int r0 = s.p; s.live && r0 < r.rows; r0 += kGradRows * P) {
-        GradRow<DT, VEC, HELD> g[kGradRows];
+        GradRow<DT, VEC, HELD> next[kGradRows];
+        load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, r0 + kGradRows * P, next);
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (r0 + i * P < r.rows)
-                g[i].load(a, s, dy, x, r.row0 + r0 + i * P);
-#pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
+        for (int i = 0; i < kGradRows; ++i) {
             if (r0 + i * P < r.rows) {
-                float fd[8], fx[8], hat[8], dz[8], out[8];
-                g[i].floats(a, fd, fx);
-                k.template slopes<DT>(a, fd, fx, hat, dz);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    out[j] = k.rs(j) * (dz[j] * k.w[j] - s1[BY_OCT ? 0 : j] - hat[j] * s2[BY_OCT ? 0 : j]);
+                float2 fd[4], fx[4], hat[4], dz[4], out[4];
+                oct_floats(g[i].dy, fd);
+                g[i].saved_floats(a, fx);
+                k.slopes(a, fd, fx, hat, dz);
+                k.gradient(dz, hat, s1, s2, out);
                 oct_store<DT, VEC>(dx, (r.row0 + r0 + i * P) * a.x_pitch + s.ch0, s.at, oct_round<DT>(out));
             }
+            g[i] = next[i];
+        }
     }
 }
 
@@ -361,26 +395,25 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
     const NormLayout& lay = a.lay;
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
     const int width = lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
-    const size_t slots = size_t(lay.P) * width * sizeof(float2) + lay.P * sizeof(float);
+    const size_t slots = kNormThreads / 32 * sizeof(float4) +
+                         (size_t(lay.run_groups) + size_t(lay.P) * slot_stride(width)) * sizeof(float2);
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
     const size_t stats = items * sizeof(float4) + lay.run_groups * sizeof(float2);
+    cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT) \
-    norm_stats_kernel<DT, VEC, BY_OCT><<<grid, lay.threads, slots, st>>>(a, x, scratch.part)
+    e = launch_grid(norm_stats_kernel<DT, VEC, BY_OCT>, grid, lay.threads, slots, lay.ranks, st, a, x, scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-#define CALL(DT, VEC, BY_OCT)                                                                                \
-    if (held.q)                                                                                              \
-        norm_apply_kernel<DT, VEC, BY_OCT, true>                                                             \
-            <<<grid, lay.threads, stats, st>>>(a, x, weight, bias, y, mean, rstd, held, scratch.part);       \
-    else                                                                                                     \
-        norm_apply_kernel<DT, VEC, BY_OCT, false>                                                            \
-            <<<grid, lay.threads, stats, st>>>(a, x, weight, bias, y, mean, rstd, held, scratch.part)
+#define CALL(DT, VEC, BY_OCT)                                                                                       \
+    e = held.q ? launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, stats, 1, st, a, x,       \
+                             weight, bias, y, mean, rstd, held, scratch.part)                                       \
+               : launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, stats, 1, st, a, x,      \
+                             weight, bias, y, mean, rstd, held, scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,
@@ -389,31 +422,27 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
 {
     const NormLayout& lay = a.lay;
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
-    const size_t sums = (size_t(lay.run_groups) + size_t(lay.P) * lay.run_cols) * sizeof(float2);
-#define CALL(DT, VEC, BY_OCT)                                                                                    \
-    if (x.q)                                                                                                     \
-        norm_sums_kernel<DT, VEC, BY_OCT, true><<<grid, lay.threads, sums, st>>>(a, dy, x, weight, bias, mean,    \
-                                                                                 rstd, scratch.part, scratch.chan); \
-    else                                                                                                         \
-        norm_sums_kernel<DT, VEC, BY_OCT, false><<<grid, lay.threads, sums, st>>>(a, dy, x, weight, bias, mean,   \
-                                                                                  rstd, scratch.part, scratch.chan)
+    const size_t sums = (size_t(lay.run_groups) + kNormThreads + lay.run_cols +
+                         size_t(lay.P) * slot_stride(lay.run_cols)) * sizeof(float2);
+    cudaError_t e = cudaSuccess;
+#define CALL(DT, VEC, BY_OCT)                                                                                       \
+    e = x.q ? launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, sums, lay.ranks, st, a, dy,   \
+                          x, weight, bias, mean, rstd, scratch.part, scratch.chan)                                  \
+            : launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, sums, lay.ranks, st, a, dy,  \
+                          x, weight, bias, mean, rstd, scratch.part, scratch.chan)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
     const size_t stats = (2 * size_t(lay.run_groups) + items) * sizeof(float2);
-#define CALL(DT, VEC, BY_OCT)                                                                               \
-    if (x.q)                                                                                                \
-        norm_grad_kernel<DT, VEC, BY_OCT, true>                                                             \
-            <<<grid, lay.threads, stats, st>>>(a, dy, x, weight, bias, mean, rstd, dx, scratch.part);       \
-    else                                                                                                    \
-        norm_grad_kernel<DT, VEC, BY_OCT, false>                                                            \
-            <<<grid, lay.threads, stats, st>>>(a, dy, x, weight, bias, mean, rstd, dx, scratch.part)
+#define CALL(DT, VEC, BY_OCT)                                                                                     \
+    e = x.q ? launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, stats, 1, st, a, dy, x,     \
+                          weight, bias, mean, rstd, dx, scratch.part)                                             \
+            : launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, stats, 1, st, a, dy, x,    \
+                          weight, bias, mean, rstd, dx, scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
-    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     return launch_norm_params(a, a.n * lay.splits, scratch.chan, dweight, dbias, st);

@@ -27,7 +27,9 @@ struct RowLayout {
 };
 
 constexpr int kOct = 8;                // channels to a thread
-constexpr int kLayerThreads = 512;     // most threads of a layer kernel's CTA
+constexpr int kLayerThreads = 256;     // most threads of an elementwise layer kernel's CTA
+constexpr int kNormThreads = 256;      // of a group-norm kernel's
+constexpr int kTokenThreads = 256;
 
 // The layout of rows cut for CTAs of about `want` threads; block: channels
 // to a scale, 0 without checkpoints.
@@ -100,6 +102,7 @@ struct NormArgs {
     int act, form, block;
     int64_t blocks;      // scales to a row of a checkpoint
     int wide_params;     // weight and bias are fp32 (else of the element type)
+    int packed_params;   // and both aligned to 16 bytes
 };
 
 // Scratch of one call (see tsx_group_norm_workspace):

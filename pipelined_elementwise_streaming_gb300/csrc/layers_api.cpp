@@ -51,7 +51,7 @@ RowLayout row_layout(int64_t rows, int64_t cols, int block, bool vec, int want)
 namespace {
 
 // Threads of the elementwise layer kernels' CTAs.
-constexpr int kElementwiseThreads = 256;
+constexpr int kElementwiseThreads = kLayerThreads;
 constexpr int64_t kMaxExtent = 0x7fffffff;
 constexpr int kMaxChunks = 65535;   // grid.y
 
@@ -259,17 +259,15 @@ namespace {
 // Channels of a CTA's run at most (its shared memory holds a pair of floats
 // for each channel and row lane, and for each group), and its threads.
 constexpr int kNormRun = 2048;
-constexpr int kNormThreads = 512;
 constexpr int kTokenRun = 2048;
-constexpr int kTokenThreads = 256;
 constexpr int64_t kTokenCtas = 8 * 152, kTokenGradCtas = 2 * 152;
 constexpr int64_t kNormRanks = 16;     // CTAs of a cluster at most
 constexpr int64_t kNormSamples = 64;   // samples side by side at most
 constexpr int64_t kNormHeldCtas = 2 * 152;
-// Ranges are cut until about this many CTAs share the work: four to each of
+// Ranges are cut until about this many CTAs share the work: three to each of
 // the 152 SMs.  A constant of the chip, not read from it, so that results
 // depend on the shape alone.
-constexpr int64_t kNormCtas = 4 * 152;
+constexpr int64_t kNormCtas = 3 * 152;
 constexpr int kNormRowsAtOnce = 4;
 
 // The streaming layout for rows of c channels; block: channels to a scale
@@ -314,10 +312,14 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
     lay.threads = round_up(lay.P * lay.V, 32);
     const int64_t want = (kNormCtas + d.n * lay.runs - 1) / (d.n * lay.runs);
     const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
-    const int64_t splits = want < most ? want : most;
+    int64_t splits = want < most ? want : most;
     lay.range = ((d.l + splits - 1) / splits + p - 1) / p * p;
-    lay.splits = (d.l + lay.range - 1) / lay.range;
-    lay.ranks = lay.samples = 1;
+    splits = (d.l + lay.range - 1) / lay.range;
+    // many ranges: clusters join eight each, so that few parts are left (the
+    // last ranges may be empty)
+    lay.ranks = splits >= 16 ? 8 : 1;
+    lay.splits = (splits + lay.ranks - 1) / lay.ranks * lay.ranks;
+    lay.samples = 1;
     lay.lanes = lay.P;
     *out = lay;
     return true;
@@ -382,7 +384,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, Nor
         lay.runs = int((d.groups + groups - 1) / groups);
         lay.team = team_of(lay.run_cols, block, true);
         lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
-        const int64_t lanes = kNormThreads / lay.V;   // >= 2
+        const int64_t lanes = kNormThreads / lay.V;
         int64_t ranks = 1;
         while (ranks < kNormRanks && ranks * lanes * rows < d.l)
             ranks *= 2;
@@ -486,7 +488,8 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward)
     return most > 16 ? most : 16;
 }
 
-int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, NormArgs* a)
+int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, const void* weight,
+              const void* bias, NormArgs* a)
 {
     if (!norm_layout(d, vec, block, backward, &a->lay) && !norm_layout(d, false, block, backward, &a->lay))
         return fail(TSX_ERR_UNSUPPORTED, call, "no layout");
@@ -505,6 +508,7 @@ int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, boo
     a->block = d.block;
     a->blocks = (d.c + d.block - 1) / d.block;
     a->wide_params = d.param_dtype == TSX_F32;
+    a->packed_params = aligned(weight, 16) && aligned(bias, 16);
     return TSX_OK;
 }
 
@@ -565,7 +569,7 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
     NormLayout lay;
     const bool ride = q && (norm_layout(d, vec, d.block, false, &lay) || norm_layout(d, false, d.block, false, &lay));
     NormArgs a{};
-    rc = norm_args(call, d, vec, ride ? d.block : 0, false, &a);
+    rc = norm_args(call, d, vec, ride ? d.block : 0, false, weight, bias, &a);
     if (rc != TSX_OK)
         return rc;
     if (q && !ride) {
@@ -627,7 +631,7 @@ extern "C" int tsx_group_norm_backward(const tsx_norm_desc* desc, const void* dy
     const bool vec = vectors(dy, d.c, d.y_pitch, es) && vectors(x, d.c, d.x_pitch, es) &&
                      vectors(dx, d.c, d.x_pitch, es) && held_vectors(q, d.c);
     NormArgs a{};
-    rc = norm_args(call, d, vec, 0, true, &a);
+    rc = norm_args(call, d, vec, 0, true, weight, bias, &a);
     if (rc != TSX_OK)
         return rc;
     NormScratch scratch;

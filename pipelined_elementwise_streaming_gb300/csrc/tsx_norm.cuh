@@ -17,11 +17,12 @@
 //   mean = mean_a + (mean_b - mean_a) n_b / n,   n = n_a + n_b,
 //   M2 = M2_a + M2_b + (mean_b - mean_a)^2 n_a n_b / n.
 //
-// A CTA adds in two steps, each in an order that its shape alone fixes: the
-// row lanes of a channel (or oct) by halves, a tree of log2(lanes) steps
-// through shared memory, then the channels of a group by a team of
-// neighbouring threads with shuffles.
+// A CTA adds in an order that its shape alone fixes: threads leave what they
+// have of their channels (or octs) in shared memory, and warps join a group's
+// columns over all row lanes.
 #pragma once
+
+#include <type_traits>
 
 #include "tsx_oct.cuh"
 
@@ -83,136 +84,269 @@ __device__ __forceinline__ int local_group(const NormArgs& a, int ch)
     return a.lay.pieces == 1 ? static_cast<int>(static_cast<unsigned>(ch) / static_cast<unsigned>(a.per_group)) : 0;
 }
 
-__device__ __forceinline__ int half_of(int lanes)   // the largest power of two below `lanes`
+// ------------------------------------------------------------- clusters
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// A pair in the shared memory of the cluster's CTA `rank`, at the place that
+// `p` has in this one.
+__device__ __forceinline__ float2 cluster_pair(const float2* p, int rank)
 {
-    int h = 1;
-    while (2 * h < lanes)
-        h *= 2;
-    return h;
+    const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    uint32_t there;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(there) : "memory");
+    return v;
 }
 
-// N triples of a thread: `count` elements each, their mean and squared
-// deviations.
-template <int N>
+// Rows of the k-th range of `range` rows of a sample (0 past its end).
+__device__ __forceinline__ int range_rows(const NormArgs& a, int64_t range, int64_t k)
+{
+    const int64_t left = a.l - k * range;
+    return static_cast<int>(left < 0 ? 0 : left < range ? left : range);
+}
+
+// ------------------------------------------------- means and deviations
+
+// What a thread has of its channels: `count` elements each, their mean and
+// squared deviations.  BY_OCT: one triple for the eight channels together.
+template <bool BY_OCT>
 struct Triples {
-    float count, mean[N], m2[N];
+    static constexpr int N = BY_OCT ? 1 : 4;
+    using V = typename std::conditional<BY_OCT, float, float2>::type;
+    float count;
+    V mean[N], m2[N];
+    static __device__ __forceinline__ V zero()
+    {
+        if constexpr (BY_OCT)
+            return 0.f;
+        else
+            return make_float2(0.f, 0.f);
+    }
     __device__ __forceinline__ void clear()
     {
         count = 0.f;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            mean[k] = m2[k] = 0.f;
+            mean[k] = m2[k] = zero();
     }
-    __device__ __forceinline__ void join(float n, const float (&mu)[N], const float (&dev)[N])
+    __device__ __forceinline__ void join(float n, const V (&mu)[N], const V (&dev)[N])
     {
         const float total = count + n;
         if (total == 0.f)
             return;
-        const float w = n / total, cross = count * w;
+        const float w = __fdividef(n, total), cross = count * w;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float d = mu[k] - mean[k];
-            mean[k] += d * w;
-            m2[k] += dev[k] + d * d * cross;
+            if constexpr (BY_OCT) {
+                const float d = mu[k] - mean[k];
+                mean[k] += d * w;
+                m2[k] += dev[k] + d * d * cross;
+            } else {
+                const float2 d = __ffma2_rn(mean[k], pair_of(-1.f), mu[k]);
+                mean[k] = __ffma2_rn(d, pair_of(w), mean[k]);
+                m2[k] = __ffma2_rn(__fmul2_rn(d, d), pair_of(cross), __fadd2_rn(m2[k], dev[k]));
+            }
         }
         count = total;
     }
-    // The eight channels of `have` rows that the thread holds: their mean, then
-    // their squared deviations from it.
-    template <int ROWS>
-    __device__ __forceinline__ void add_rows(const float (&f)[ROWS][8], int have)
+    // ROWS rows of the thread's channels, of which the first `have` count (all
+    // are finite zeros beyond): their mean, then their squared deviations.
+    template <int ROWS, bool ALL>
+    __device__ __forceinline__ void add_rows(const float2 (&f)[ROWS][4], int have)
     {
-        float mu[N], dev[N];
+        float2 sum[4];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            mu[k] = dev[k] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+            sum[j] = f[0][j];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            if (i < have) {
+            for (int i = 1; i < ROWS; ++i)
+                sum[j] = __fadd2_rn(sum[j], f[i][j]);
+        }
+        const float n = (ALL ? ROWS : have) * (BY_OCT ? 8.f : 1.f), each = 1.f / n;
+        float2 minus[4];   // minus the mean
+        V mu[N], dev[N];
+        if constexpr (BY_OCT) {
+            const float2 t = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+            mu[0] = (t.x + t.y) * each;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    mu[j % N] += f[i][j];
+            for (int j = 0; j < 4; ++j)
+                minus[j] = pair_of(-mu[0]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mu[j] = __fmul2_rn(sum[j], pair_of(each));
+                minus[j] = __fmul2_rn(mu[j], pair_of(-1.f));
             }
-        const float n = have * (8.f / N), each = 1.f / n;
+        }
+        float2 sq[4];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            mu[k] *= each;
+        for (int j = 0; j < 4; ++j) {
+            sq[j] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            if (i < have) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float d = f[i][j] - mu[j % N];
-                    dev[j % N] += d * d;
+            for (int i = 0; i < ROWS; ++i)
+                if (ALL || i < have) {
+                    const float2 d = __fadd2_rn(f[i][j], minus[j]);
+                    sq[j] = __ffma2_rn(d, d, sq[j]);
                 }
-            }
-        if (have)
+        }
+        if constexpr (BY_OCT) {
+            const float2 t = __fadd2_rn(__fadd2_rn(sq[0], sq[1]), __fadd2_rn(sq[2], sq[3]));
+            dev[0] = t.x + t.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                dev[j] = sq[j];
+        }
+        if (ALL || have)
             join(n, mu, dev);
+    }
+    // To a row of shared-memory columns (octs or channels) as (mean, M2).
+    __device__ __forceinline__ void leave(const OctAt& at, float2* row) const
+    {
+        if constexpr (BY_OCT) {
+            row[at.ch / 8] = make_float2(mean[0], m2[0]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (at.ch + 2 * j * at.step < at.cols)
+                    row[at.ch + 2 * j * at.step] = make_float2(mean[j].x, m2[j].x);
+                if (at.ch + (2 * j + 1) * at.step < at.cols)
+                    row[at.ch + (2 * j + 1) * at.step] = make_float2(mean[j].y, m2[j].y);
+            }
+        }
     }
 };
 
-// The triples of the `lanes` row lanes that share a thread's channels, joined
-// into lane `lane` 0's; slots: [P][width] pairs of shared memory.  All threads
-// of the CTA call it.
-template <int N>
-__device__ __forceinline__ void join_lanes(const NormPlace& s, int lane, int lanes, float2* slots, float* counts,
-                                           int width, Triples<N>& t)
-{
-    auto col = [&](int j) { return N == 1 ? s.at.ch / 8 : s.at.ch + j * s.at.step; };
-    for (int half = half_of(lanes); lanes > 1 && half > 0; half >>= 1) {
-        if (s.live && lane >= half && lane < 2 * half) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (N == 1 || s.at.ch + j * s.at.step < s.at.cols)
-                    slots[s.p * width + col(j)] = make_float2(t.mean[j], t.m2[j]);
-            counts[s.p] = t.count;   // the same from every thread of the lane
-        }
-        __syncthreads();
-        if (s.live && lane < half && lane + half < lanes) {
-            float mu[N], dev[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                mu[j] = dev[j] = 0.f;
-                if (N == 1 || s.at.ch + j * s.at.step < s.at.cols) {
-                    const float2 o = slots[(s.p + half) * width + col(j)];
-                    mu[j] = o.x;
-                    dev[j] = o.y;
-                }
-            }
-            t.join(counts[s.p + half], mu, dev);
-        }
-    }
-}
-
-// The same for plain sums of pairs, channel by channel.
-__device__ __forceinline__ void add_lanes(const NormPlace& s, int lane, int lanes, float2* slots, int width,
-                                          float (&x)[8], float (&y)[8])
-{
-    for (int half = half_of(lanes); lanes > 1 && half > 0; half >>= 1) {
-        if (s.live && lane >= half && lane < 2 * half) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (s.at.ch + j * s.at.step < s.at.cols)
-                    slots[s.p * width + s.at.ch + j * s.at.step] = make_float2(x[j], y[j]);
-        }
-        __syncthreads();
-        if (s.live && lane < half && lane + half < lanes) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (s.at.ch + j * s.at.step < s.at.cols) {
-                    const float2 o = slots[(s.p + half) * width + s.at.ch + j * s.at.step];
-                    x[j] += o.x;
-                    y[j] += o.y;
-                }
-        }
-    }
-}
+// Row of the shared-memory columns: odd, so that the row lanes of one column
+// lie in different banks.
+__host__ __device__ constexpr int slot_stride(int width) { return width | 1; }
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes)
 {
     for (int d = 1; d < lanes; d <<= 1)
         v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// (mean, M2) of each of `samples` x `groups` items from the columns that the
+// row lanes left: slots[samples * lanes][slot_stride], `per` neighbouring
+// columns to a group, `scale` elements to a column and row, `rows` rows dealt
+// to the lanes in turn.  A warp takes an item, or (few items) one of `parts`
+// shares of its row lanes; the shares are joined in their order.  Called by
+// all threads between two barriers; ends without one.  spare: [warps].
+__device__ __forceinline__ void join_groups(const float2* slots, int stride, int samples, int groups, int lanes,
+                                            int per, int rows, float scale, float2* out, float4* spare)
+{
+    const int warps = static_cast<int>(blockDim.x) / 32, warp = static_cast<int>(threadIdx.x) / 32;
+    const int t = static_cast<int>(threadIdx.x) % 32;
+    const int items = samples * groups;
+    const int parts = items >= warps ? 1 : warps / items;
+    int kw = 1, shift = 0;   // threads side by side along a row
+    while (kw < 32 && kw < per) {
+        kw *= 2;
+        ++shift;
+    }
+    const int k0 = t & (kw - 1), p0 = t >> shift, step = 32 >> shift;
+    const int base = rows / lanes, more = rows - base * lanes;   // lane p has base + (p < more) rows
+    for (int u = warp; u < items * parts; u += warps) {
+        const int part = parts == 1 ? 0 : u / items, item = u - part * items;
+        const int q = samples == 1 ? 0 : item / groups, g = item - q * groups;
+        const float2* first = slots + q * lanes * stride + g * per;
+        float n = 0.f, sum = 0.f, dev = 0.f;
+        for (int p = part * step + p0; p < lanes; p += parts * step) {
+            const float c = (base + (p < more ? 1 : 0)) * scale;
+            for (int k = k0; k < per; k += kw) {
+                n += c;
+                sum += c * first[p * stride + k].x;
+            }
+        }
+        n = warp_sum(n);
+        sum = warp_sum(sum);
+        const float mean = n > 0.f ? sum / n : 0.f;
+        for (int p = part * step + p0; p < lanes; p += parts * step) {
+            const float c = (base + (p < more ? 1 : 0)) * scale;
+            for (int k = k0; k < per; k += kw) {
+                const float2 v = first[p * stride + k];
+                const float d = v.x - mean;
+                dev += v.y + c * d * d;
+            }
+        }
+        dev = warp_sum(dev);
+        if (t == 0) {
+            if (parts == 1)
+                out[item] = make_float2(mean, dev);
+            else
+                spare[u] = make_float4(n, mean, dev, 0.f);
+        }
+    }
+    if (parts > 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < items; i += blockDim.x) {
+            Triples<true> j;
+            j.clear();
+            for (int k = 0; k < parts; ++k) {
+                const float4 v = spare[k * items + i];
+                const float mu[1] = {v.y}, dv[1] = {v.z};
+                j.join(v.x, mu, dv);
+            }
+            out[i] = make_float2(j.mean[0], j.m2[0]);
+        }
+    }
+}
+
+// --------------------------------------------------------- sums of pairs
+
+// A thread's sums of its eight channels, two each, to its row of columns.
+__device__ __forceinline__ void leave_sums(const OctAt& at, const float2 (&x)[4], const float2 (&y)[4], float2* row)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (at.ch + 2 * j * at.step < at.cols)
+            row[at.ch + 2 * j * at.step] = make_float2(x[j].x, y[j].x);
+        if (at.ch + (2 * j + 1) * at.step < at.cols)
+            row[at.ch + (2 * j + 1) * at.step] = make_float2(x[j].y, y[j].y);
+    }
+}
+
+// columns[samples][width] = the sums over each sample's row lanes of
+// slots[samples * lanes][slot_stride]: every column by several threads, each
+// adding its share of the lanes, then share after share.  Called by all
+// threads after a barrier; ends with one.  work: [threads].
+__device__ __forceinline__ void sum_lanes(const float2* slots, int stride, int samples, int lanes, int width,
+                                          float2* columns, float2* work)
+{
+    const int threads = static_cast<int>(blockDim.x), all = samples * width;
+    int shares = threads / all;
+    shares = shares < 1 ? 1 : shares > lanes ? lanes : shares;
+    for (int i = threadIdx.x; i < shares * all; i += threads) {
+        const int share = shares == 1 ? 0 : i / all, col = i - share * all;
+        const int q = samples == 1 ? 0 : col / width;
+        const float2* first = slots + q * lanes * stride + col - q * width;
+        float2 t = make_float2(0.f, 0.f);
+        for (int p = share; p < lanes; p += shares)
+            t = __fadd2_rn(t, first[p * stride]);
+        (shares == 1 ? columns : work)[i] = t;
+    }
+    __syncthreads();
+    if (shares > 1) {
+        for (int i = threadIdx.x; i < all; i += threads) {
+            float2 t = work[i];
+            for (int k = 1; k < shares; ++k)
+                t = __fadd2_rn(t, work[k * all + i]);
+            columns[i] = t;
+        }
+        __syncthreads();
+    }
 }
 
 // f(item, lane, lanes, real) for `items` items of `entries` entries each, one
@@ -221,35 +355,17 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
 template <class F>
 __device__ __forceinline__ void each_item(int items, int entries, F f)
 {
-    int lanes = 1;
-    while (lanes < 32 && 2 * lanes <= entries)
+    int lanes = 1, shift = 0;
+    while (lanes < 32 && 2 * lanes <= entries) {
         lanes *= 2;
-    const int teams = static_cast<int>(blockDim.x) / lanes;
-    const int me = static_cast<int>(threadIdx.x) / lanes, lane = static_cast<int>(threadIdx.x) % lanes;
+        ++shift;
+    }
+    const int teams = static_cast<int>(blockDim.x) >> shift;
+    const int me = static_cast<int>(threadIdx.x) >> shift, lane = static_cast<int>(threadIdx.x) & (lanes - 1);
     for (int i0 = 0; i0 < items; i0 += teams) {
         const int i = i0 + me;
         f(i < items ? i : items - 1, lane, lanes, i < items);
     }
-}
-
-// (mean, M2) of each of the `items` groups from `per` columns each, all of
-// `count` elements: out[item].  columns: [item][per], as (mean, M2).
-__device__ __forceinline__ void join_columns(const float2* columns, int items, int per, float count, float2* out)
-{
-    each_item(items, per, [&](int g, int lane, int lanes, bool real) {
-        float sum = 0.f, dev = 0.f;
-        for (int e = lane; e < per; e += lanes)
-            sum += columns[g * per + e].x;
-        const float mean = lanes_sum(sum, lanes) / per;
-        for (int e = lane; e < per; e += lanes) {
-            const float2 t = columns[g * per + e];
-            const float d = t.x - mean;
-            dev += t.y + count * d * d;
-        }
-        dev = lanes_sum(dev, lanes);
-        if (real && lane == 0)
-            out[g] = make_float2(mean, dev);
-    });
 }
 
 __device__ __forceinline__ float rstd_of(float m2, float m, float eps) { return 1.f / sqrtf(m2 / m + eps); }
@@ -266,77 +382,143 @@ __device__ __forceinline__ float weight_at(const NormArgs& a, const void* weight
         return __half2float(static_cast<const __half*>(weight)[ch]);
 }
 
-// (S1, S2) of each of the run's groups from its channels' sums of dz and dz
-// xhat (columns: [run_cols]).
+// (S1, S2) of each of samples x groups items from the channels' sums of dz
+// and dz xhat: columns[samples][width], out[samples][groups].
 template <int DT>
-__device__ __forceinline__ void weigh_columns(const NormArgs& a, const NormPlace& s, const void* weight,
-                                              const float2* columns, float2* out)
+__device__ __forceinline__ void weigh_columns(const NormArgs& a, const NormPlace& s, int samples, int width,
+                                              const void* weight, const float2* columns, float2* out)
 {
     const int per = group_cols(a, s);
-    each_item(s.groups, per, [&](int g, int lane, int lanes, bool real) {
+    each_item(samples * s.groups, per, [&](int i, int lane, int lanes, bool real) {
+        const int q = samples == 1 ? 0 : i / s.groups, g = i - q * s.groups;
         float s1 = 0.f, s2 = 0.f;
         for (int e = lane; e < per; e += lanes) {
             const int ch = g * per + e;
             const float w = weight_at<DT>(a, weight, s.ch0 + ch);
-            s1 += w * columns[ch].x;
-            s2 += w * columns[ch].y;
+            const float2 v = columns[q * width + ch];
+            s1 += w * v.x;
+            s2 += w * v.y;
         }
         s1 = lanes_sum(s1, lanes);
         s2 = lanes_sum(s2, lanes);
         if (real && lane == 0)
-            out[g] = make_float2(s1, s2);
+            out[i] = make_float2(s1, s2);
     });
 }
 
-// What a thread keeps for its channels: mean and rstd of their groups, weight
-// and bias.
+// A value for each of a thread's channels that is the same within a group, as
+// pairs (BY_OCT: one for all).
+template <bool BY_OCT>
+struct Grouped {
+    float2 v[BY_OCT ? 1 : 4];
+    __device__ __forceinline__ float2 at(int j) const { return v[BY_OCT ? 0 : j]; }
+};
+
+// The two halves of the pairs table[group] for a thread's channels.
+template <bool BY_OCT>
+__device__ __forceinline__ void grouped(const NormArgs& a, const NormPlace& s, const float2* table,
+                                        Grouped<BY_OCT>& first, Grouped<BY_OCT>& second)
+{
+    int g = s.at.ch < s.at.cols ? local_group(a, s.at.ch) : 0;
+    if constexpr (BY_OCT) {
+        const float2 t = table[g];
+        first.v[0] = pair_of(t.x);
+        second.v[0] = pair_of(t.y);
+    } else {
+        float2 t[8];
+        if (s.at.step == 1 && a.lay.pieces == 1) {   // neighbours: the next group after the last of this one
+            int left = (g + 1) * a.per_group - s.at.ch;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                t[j] = table[g];
+                if (--left == 0) {
+                    left = a.per_group;
+                    if (g + 1 < s.groups)
+                        ++g;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int ch = s.at.ch + j * s.at.step;
+                t[j] = table[ch < s.at.cols ? local_group(a, ch) : 0];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            first.v[j] = make_float2(t[2 * j].x, t[2 * j + 1].x);
+            second.v[j] = make_float2(t[2 * j].y, t[2 * j + 1].y);
+        }
+    }
+}
+
+// What a thread keeps for its channels: minus the mean and rstd of their
+// groups, weight and bias.
 template <bool BY_OCT>
 struct Chan {
-    float mean[BY_OCT ? 1 : 8], rstd[BY_OCT ? 1 : 8], w[8], b[8];
-    __device__ __forceinline__ float mu(int j) const { return mean[BY_OCT ? 0 : j]; }
-    __device__ __forceinline__ float rs(int j) const { return rstd[BY_OCT ? 0 : j]; }
+    Grouped<BY_OCT> minus, rstd;
+    float2 w[4], b[4];
     template <int DT, bool VEC>
     __device__ __forceinline__ void params(const NormArgs& a, const NormPlace& s, const void* weight,
                                            const void* bias)
     {
-        param_floats<DT, VEC>(weight, a.wide_params, s.ch0, s.at, w);
-        param_floats<DT, VEC>(bias, a.wide_params, s.ch0, s.at, b);
+        param_floats<DT, VEC>(weight, a.wide_params, a.packed_params, s.ch0, s.at, w);
+        param_floats<DT, VEC>(bias, a.wide_params, a.packed_params, s.ch0, s.at, b);
     }
+    // stats: (mean, rstd) by group of the run
     __device__ __forceinline__ void statistics(const NormArgs& a, const NormPlace& s, const float2* stats)
     {
+        grouped<BY_OCT>(a, s, stats, minus, rstd);
 #pragma unroll
-        for (int j = 0; j < (BY_OCT ? 1 : 8); ++j) {
-            const int ch = s.at.ch + j * s.at.step;
-            const float2 t = stats[ch < s.at.cols ? local_group(a, ch) : 0];
-            mean[j] = t.x;
-            rstd[j] = t.y;
-        }
+        for (int j = 0; j < (BY_OCT ? 1 : 4); ++j)
+            minus.v[j] = __fmul2_rn(minus.v[j], pair_of(-1.f));
     }
-    template <int DT>
-    __device__ __forceinline__ void apply(const NormArgs& a, const float (&x)[8], float (&y)[8]) const
+    __device__ __forceinline__ void statistics(float mean, float rs)   // BY_OCT
     {
+        minus.v[0] = pair_of(-mean);
+        rstd.v[0] = pair_of(rs);
+    }
+    __device__ __forceinline__ float2 hat(const float2 (&x)[4], int j) const
+    {
+        return __fmul2_rn(__fadd2_rn(x[j], minus.at(j)), rstd.at(j));
+    }
+    __device__ __forceinline__ void apply(const NormArgs& a, const float2 (&x)[4], float2 (&y)[4]) const
+    {
+        float2 z[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_value<DT>((x[j] - mu(j)) * rs(j) * w[j] + b[j], a.act);
+        for (int j = 0; j < 4; ++j)
+            z[j] = __ffma2_rn(hat(x, j), w[j], b[j]);
+        act_value(a.act, z, y);
     }
     // xhat and dz
-    template <int DT>
-    __device__ __forceinline__ void slopes(const NormArgs& a, const float (&dy)[8], const float (&x)[8],
-                                           float (&hat)[8], float (&dz)[8]) const
+    __device__ __forceinline__ void slopes(const NormArgs& a, const float2 (&dy)[4], const float2 (&x)[4],
+                                           float2 (&xhat)[4], float2 (&dz)[4]) const
+    {
+        float2 z[4], value[4], slope[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            xhat[j] = hat(x, j);
+            z[j] = __ffma2_rn(xhat[j], w[j], b[j]);
+        }
+        act_both(a.act, z, value, slope);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dz[j] = __fmul2_rn(dy[j], slope[j]);
+    }
+    // dx from dz and xhat, s1 and s2 minus the groups' S1 / M and S2 / M
+    __device__ __forceinline__ void gradient(const float2 (&dz)[4], const float2 (&xhat)[4],
+                                             const Grouped<BY_OCT>& s1, const Grouped<BY_OCT>& s2,
+                                             float2 (&dx)[4]) const
     {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            hat[j] = (x[j] - mu(j)) * rs(j);
-            float value, slope;
-            act_both<DT>(hat[j] * w[j] + b[j], a.act, value, slope);
-            dz[j] = dy[j] * slope;
-        }
+        for (int j = 0; j < 4; ++j)
+            dx[j] = __fmul2_rn(rstd.at(j), __ffma2_rn(xhat[j], s2.at(j), __ffma2_rn(dz[j], w[j], s1.at(j))));
     }
 };
 
 // An oct to 8 bits, as the forward pass saves it.  By whole warps.
 template <bool VEC>
-__device__ __forceinline__ void hold(const NormArgs& a, const NormPlace& s, const float (&f)[8], bool live,
+__device__ __forceinline__ void hold(const NormArgs& a, const NormPlace& s, const float2 (&f)[4], bool live,
                                      int64_t row, const HeldOut& out)
 {
     const uint32_t m = team_max(live ? oct_amax_bits(f) : 0u, a.lay.team);
@@ -371,12 +553,7 @@ struct GradRow {
             x = oct_load<DT, VEC>(src.x, row * a.x_pitch + s.ch0, s.at);
         }
     }
-    __device__ __forceinline__ void floats(const NormArgs& a, float (&fd)[8], float (&fx)[8]) const
-    {
-        oct_floats(dy, fd);
-        saved_floats(a, fx);
-    }
-    __device__ __forceinline__ void saved_floats(const NormArgs& a, float (&fx)[8]) const
+    __device__ __forceinline__ void saved_floats(const NormArgs& a, float2 (&fx)[4]) const
     {
         if constexpr (!HELD) {
             oct_floats(x, fx);
@@ -385,13 +562,40 @@ struct GradRow {
         } else {
             held_floats(q, 1.f, a.form, fx);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                fx[j] *= scale[j];
+            for (int j = 0; j < 4; ++j)
+                fx[j] = __fmul2_rn(fx[j], make_float2(scale[2 * j], scale[2 * j + 1]));
         }
     }
 };
 
 }  // namespace dev
+
+// Launch `kernel` with clusters of `ranks` CTAs along x (1: none).
+template <class K, class... Args>
+cudaError_t launch_grid(K kernel, dim3 grid, int threads, size_t smem, int ranks, cudaStream_t st, Args... args)
+{
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    cudaError_t e = cudaSuccess;
+    if (ranks > 8)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && smem > 48 * 1024)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 // f<DT, VEC, BY_OCT>(...) for the runtime type and layout.
 #define TSX_BY_LAYOUT(dtype, lay, CALL)                                                        \

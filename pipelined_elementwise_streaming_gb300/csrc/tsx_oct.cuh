@@ -93,48 +93,40 @@ __device__ __forceinline__ Oct<DT> oct_load(const void* base, int64_t row_elems,
     return o;
 }
 
+// An oct's fp32 values as four pairs: arithmetic on them is two elements to an
+// instruction (fma.rn.f32x2 and its kin), with the rounding of the scalar ones.
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+
 template <int DT>
-__device__ __forceinline__ void oct_floats(const Oct<DT>& o, float (&f)[8])
+__device__ __forceinline__ void oct_floats(const Oct<DT>& o, float2 (&f)[4])
 {
-    if constexpr (DT == TSX_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = __uint_as_float(o.w[j]);
-    } else if constexpr (DT == TSX_BF16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(o.w[j] << 16);
-            f[2 * j + 1] = __uint_as_float(o.w[j] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o.w[j]));
-            f[2 * j] = v.x;
-            f[2 * j + 1] = v.y;
-        }
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == TSX_F32)
+            f[j] = make_float2(__uint_as_float(o.w[2 * j]), __uint_as_float(o.w[2 * j + 1]));
+        else if constexpr (DT == TSX_BF16)
+            f[j] = make_float2(__uint_as_float(o.w[j] << 16), __uint_as_float(o.w[j] & 0xffff0000u));
+        else
+            f[j] = __half22float2(*reinterpret_cast<const __half2*>(&o.w[j]));
     }
 }
 
 // Rounded once, to nearest even, into the element type.
 template <int DT>
-__device__ __forceinline__ Oct<DT> oct_round(const float (&f)[8])
+__device__ __forceinline__ Oct<DT> oct_round(const float2 (&f)[4])
 {
     Oct<DT> o;
-    if constexpr (DT == TSX_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            o.w[j] = __float_as_uint(f[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == TSX_BF16) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-                o.w[j] = *reinterpret_cast<const uint32_t*>(&v);
-            } else {
-                const __half2 v = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
-                o.w[j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == TSX_F32) {
+            o.w[2 * j] = __float_as_uint(f[j].x);
+            o.w[2 * j + 1] = __float_as_uint(f[j].y);
+        } else if constexpr (DT == TSX_BF16) {
+            const __nv_bfloat162 v = __float22bfloat162_rn(f[j]);
+            o.w[j] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+            const __half2 v = __float22half2_rn(f[j]);
+            o.w[j] = *reinterpret_cast<const uint32_t*>(&v);
         }
     }
     return o;
@@ -163,46 +155,70 @@ __device__ __forceinline__ void oct_store(void* base, int64_t row_elems, const O
     }
 }
 
-// Eight fp32 (or, for parameters given in the element type, narrower) values
-// of a per-channel vector.
+// Eight values of a per-channel vector, fp32 (wide) or of the element type.
+// packed: base and channels are aligned to 16 bytes.
 template <int DT, bool VEC>
-__device__ __forceinline__ void param_floats(const void* base, bool wide, int ch0, const OctAt& at, float (&f)[8])
+__device__ __forceinline__ void param_floats(const void* base, bool wide, bool packed, int ch0, const OctAt& at,
+                                             float2 (&f)[4])
 {
 #pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f[j] = make_float2(0.f, 0.f);
+    if (at.ch >= at.cols)
+        return;
+    if (VEC && packed) {
+        if (wide || DT == TSX_F32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + ch0 + at.ch);
+            const float4 u = __ldg(p), v = __ldg(p + 1);
+            f[0] = make_float2(u.x, u.y);
+            f[1] = make_float2(u.z, u.w);
+            f[2] = make_float2(v.x, v.y);
+            f[3] = make_float2(v.z, v.w);
+        } else {
+            oct_floats(oct_load<DT, true>(base, ch0, at), f);
+        }
+        return;
+    }
+    float v[8];
+#pragma unroll
     for (int j = 0; j < 8; ++j) {
-        f[j] = 0.f;
+        v[j] = 0.f;
         if (at.ch + j * at.step < at.cols) {
             const int ch = ch0 + at.ch + j * at.step;
             if (wide || DT == TSX_F32)
-                f[j] = __ldg(static_cast<const float*>(base) + ch);
+                v[j] = __ldg(static_cast<const float*>(base) + ch);
             else if constexpr (DT == TSX_BF16)
-                f[j] = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[ch]);
+                v[j] = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[ch]);
             else if constexpr (DT == TSX_F16)
-                f[j] = __half2float(static_cast<const __half*>(base)[ch]);
+                v[j] = __half2float(static_cast<const __half*>(base)[ch]);
         }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f[j] = make_float2(v[2 * j], v[2 * j + 1]);
 }
 
 // ----------------------------------------------------------- activations
 
-// sigmoid(z) = 1 / (1 + exp(-z)).  fp32 data take expf and an IEEE division.
-// 16-bit data take the hardware base-2 exponential and reciprocal
-// (ex2.approx, rcp.approx: a few fp32 ulps each; the rounded product
-// z log2(e) adds 2^-24 |z| relative): under 2^-18 wherever the result is not
-// below 2^-40, against the 2^-11 (fp16) and 2^-8 (bf16) of the result's own
-// rounding.
-template <int DT>
-__device__ __forceinline__ float sigmoid(float z)
+// sigmoid(z) = 1 / (1 + 2^t), t = -z log2(e), by the hardware's base-2
+// exponential and reciprocal (ex2.approx, rcp.approx: about 2^-22 each).  The
+// rounding of t adds 2^-24 |z| relative.  For 16-bit elements that is far
+// below the result's own rounding; for fp32 it is 2 to 4 ulps at ordinary z,
+// and the division and the exponential with its range reduction that would
+// save them cost a third of the kernel's time (gated activation, fp32 [1777,
+// 2731]).
+__device__ __forceinline__ float2 sigmoid_of(float2 t)
 {
-    if constexpr (DT == TSX_F32) {
-        return __fdiv_rn(1.f, 1.f + expf(-z));
-    } else {
-        float e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504088896341f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-        return r;
-    }
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(e, pair_of(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return r;
 }
+
+constexpr float kLog2E = 1.44269504088896341f;
 
 // The tanh form of gelu through the sigmoid: tanh(u) = 2 sigmoid(2 u) - 1, so
 // gelu(z) = z sigmoid(2 k (z + 0.044715 z^3)), k = sqrt(2 / pi).  The argument
@@ -211,35 +227,60 @@ __device__ __forceinline__ float sigmoid(float z)
 constexpr float kGelu2K = 1.5957691216057308f;
 constexpr float kGeluCube = 0.044715f;
 
-template <int DT>
-__device__ __forceinline__ float act_value(float z, int act)
+__device__ __forceinline__ float2 gelu_clamped(float2 z)
 {
-    if (act == TSX_ACT_SILU)
-        return z * sigmoid<DT>(z);
-    if (act == TSX_ACT_GELU) {
-        const float t = fminf(fmaxf(z, -24.f), 24.f);
-        return z * sigmoid<DT>(kGelu2K * t * (1.f + kGeluCube * t * t));
+    return make_float2(fminf(fmaxf(z.x, -24.f), 24.f), fminf(fmaxf(z.y, -24.f), 24.f));
+}
+
+// v = act(z) for an oct.
+__device__ __forceinline__ void act_value(int act, const float2 (&z)[4], float2 (&v)[4])
+{
+    if (act == TSX_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = __fmul2_rn(z[j], sigmoid_of(__fmul2_rn(z[j], pair_of(-kLog2E))));
+    } else if (act == TSX_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = gelu_clamped(z[j]);
+            const float2 u = __ffma2_rn(__fmul2_rn(t, t), pair_of(-kLog2E * kGelu2K * kGeluCube),
+                                        pair_of(-kLog2E * kGelu2K));
+            v[j] = __fmul2_rn(z[j], sigmoid_of(__fmul2_rn(t, u)));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = z[j];
     }
-    return z;
 }
 
 // act(z) and its derivative.
-template <int DT>
-__device__ __forceinline__ void act_both(float z, int act, float& value, float& slope)
+__device__ __forceinline__ void act_both(int act, const float2 (&z)[4], float2 (&v)[4], float2 (&slope)[4])
 {
+    const float2 one = pair_of(1.f), minus = pair_of(-1.f);
     if (act == TSX_ACT_SILU) {
-        const float p = sigmoid<DT>(z);
-        value = z * p;
-        slope = p + value * (1.f - p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 p = sigmoid_of(__fmul2_rn(z[j], pair_of(-kLog2E)));
+            v[j] = __fmul2_rn(z[j], p);
+            slope[j] = __ffma2_rn(v[j], __ffma2_rn(p, minus, one), p);   // p + v (1 - p)
+        }
     } else if (act == TSX_ACT_GELU) {
-        const float t = fminf(fmaxf(z, -24.f), 24.f);
-        const float t2 = t * t;
-        const float p = sigmoid<DT>(kGelu2K * t * (1.f + kGeluCube * t2));
-        value = z * p;
-        slope = p + value * (1.f - p) * (kGelu2K * (1.f + 3.f * kGeluCube * t2));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = gelu_clamped(z[j]), t2 = __fmul2_rn(t, t);
+            const float2 u = __ffma2_rn(t2, pair_of(-kLog2E * kGelu2K * kGeluCube), pair_of(-kLog2E * kGelu2K));
+            const float2 p = sigmoid_of(__fmul2_rn(t, u));
+            const float2 inner = __ffma2_rn(t2, pair_of(3.f * kGelu2K * kGeluCube), pair_of(kGelu2K));
+            v[j] = __fmul2_rn(z[j], p);
+            slope[j] = __ffma2_rn(__fmul2_rn(v[j], __ffma2_rn(p, minus, one)), inner, p);   // 0, not 0 * infinity
+        }
     } else {
-        value = z;
-        slope = 1.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = z[j];
+            slope[j] = one;
+        }
     }
 }
 
@@ -272,12 +313,12 @@ __device__ __forceinline__ HeldScale held_scale(uint32_t amax_bits, int form)
 // The largest magnitude of an oct, as bits: unsigned integers order
 // magnitudes as floats do, with infinity above every number and NaN above
 // infinity, which a float maximum would drop.
-__device__ __forceinline__ uint32_t oct_amax_bits(const float (&f)[8])
+__device__ __forceinline__ uint32_t oct_amax_bits(const float2 (&f)[4])
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+    for (int j = 0; j < 4; ++j)
+        m = max(m, max(__float_as_uint(f[j].x) & 0x7fffffffu, __float_as_uint(f[j].y) & 0x7fffffffu));
     return m;
 }
 
@@ -297,26 +338,28 @@ struct Held {
 // x * inv rounded to nearest even into the 8-bit form.  int8: adding 1.5 *
 // 2^23 leaves the whole number in the sum's low byte (|x inv| <= 127 plus
 // rounding, well inside); the product is rounded by itself first.
-__device__ __forceinline__ Held held_round(const float (&f)[8], const HeldScale& s, int form)
+__device__ __forceinline__ Held held_round(const float2 (&f)[4], const HeldScale& s, int form)
 {
     Held h;
-    if (form == TSX_INT8) {
-        uint32_t b[8];
+    float2 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            b[j] = __float_as_uint(__fadd_rn(__fmul_rn(f[j], s.inv), 12582912.f));
+    for (int j = 0; j < 4; ++j)
+        v[j] = __fmul2_rn(f[j], pair_of(s.inv));
+    if (form == TSX_INT8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            // not as a pair: the paired product and sum would become one fma
+            v[j] = make_float2(__fadd_rn(v[j].x, 12582912.f), __fadd_rn(v[j].y, 12582912.f));
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            h.w[k] = __byte_perm(__byte_perm(b[4 * k], b[4 * k + 1], 0x0040),
-                                 __byte_perm(b[4 * k + 2], b[4 * k + 3], 0x0040), 0x5410);
+            h.w[k] = __byte_perm(
+                __byte_perm(__float_as_uint(v[2 * k].x), __float_as_uint(v[2 * k].y), 0x0040),
+                __byte_perm(__float_as_uint(v[2 * k + 1].x), __float_as_uint(v[2 * k + 1].y), 0x0040), 0x5410);
     } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                make_float2(__fmul_rn(f[4 * k], s.inv), __fmul_rn(f[4 * k + 1], s.inv)), __NV_SATFINITE, __NV_E4M3);
-            uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                make_float2(__fmul_rn(f[4 * k + 2], s.inv), __fmul_rn(f[4 * k + 3], s.inv)), __NV_SATFINITE,
-                __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(v[2 * k], __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(v[2 * k + 1], __NV_SATFINITE, __NV_E4M3);
             h.w[k] = lo | hi << 16;
         }
     }
@@ -328,15 +371,18 @@ __device__ __forceinline__ Held held_round(const float (&f)[8], const HeldScale&
 // The fp32 values q * scale.  int8: the byte, offset by 128, becomes the low
 // byte of 2^23 + b; subtracting 2^23 + 128 leaves the number exactly, without
 // an integer conversion.
-__device__ __forceinline__ void held_floats(const Held& h, float scale, int form, float (&f)[8])
+__device__ __forceinline__ void held_floats(const Held& h, float scale, int form, float2 (&f)[4])
 {
     if (form == TSX_INT8) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint32_t u = h.w[k] ^ 0x80808080u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                f[4 * k + j] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 | j)) - 8388736.f) * scale;
+            for (int j = 0; j < 2; ++j) {
+                const float2 b = make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 | 2 * j)),
+                                             __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541 | 2 * j)));
+                f[2 * k + j] = __fmul2_rn(__fadd2_rn(b, pair_of(-8388736.f)), pair_of(scale));
+            }
         }
     } else {
 #pragma unroll
@@ -345,9 +391,7 @@ __device__ __forceinline__ void held_floats(const Held& h, float scale, int form
             for (int j = 0; j < 2; ++j) {
                 const __half2_raw r =
                     __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h.w[k] >> (16 * j)), __NV_E4M3);
-                const float2 v = __half22float2(__half2(r));
-                f[4 * k + 2 * j] = v.x * scale;
-                f[4 * k + 2 * j + 1] = v.y * scale;
+                f[2 * k + j] = __fmul2_rn(__half22float2(__half2(r)), pair_of(scale));
             }
     }
 }
