@@ -17,13 +17,16 @@ namespace {
 
 using namespace dev;
 
-// Rows whose loads a thread issues before it uses the first.
+// Rows whose loads a thread issues before it uses the first: of one operand,
+// and of two or three.
 constexpr int kRowsAtOnce = 4;
+constexpr int kGatedRows = 2;
 
 struct Place {
     OctAt at;
-    int64_t row0;   // the thread's first row
-    int chunk0;     // the run's first channel
+    int64_t row0;   // the thread's first row; the others are P apart
+    int ch;         // its first channel, counted from the row's start
+    int rows;       // how many of its rows exist (0 for spare threads of the last warp)
     bool live;      // the thread has channels
 };
 
@@ -32,34 +35,45 @@ __device__ __forceinline__ Place place(const RowLayout& lay, int rows_at_once)
 {
     Place s;
     const int p = static_cast<int>(threadIdx.x) / lay.V, v = static_cast<int>(threadIdx.x) - p * lay.V;
-    s.chunk0 = static_cast<int>(blockIdx.y) * lay.chunk_cols;
-    const int cols = min(lay.chunk_cols, lay.cols - s.chunk0);
+    const int chunk0 = static_cast<int>(blockIdx.y) * lay.chunk_cols;
+    const int cols = min(lay.chunk_cols, lay.cols - chunk0);
     s.at = oct_at<VEC>(v, lay.team, cols);
+    s.ch = chunk0 + s.at.ch;
     s.live = p < lay.P && s.at.ch < cols;
     s.row0 = static_cast<int64_t>(blockIdx.x) * (lay.P * rows_at_once) + p;
+    const int64_t left = lay.rows - s.row0;
+    s.rows = p >= lay.P || left <= 0 ? 0 : static_cast<int>(min((left + lay.P - 1) / lay.P, int64_t(rows_at_once)));
     return s;
 }
 
-// An oct to 8 bits with its team's scale, both stored.  Called by whole
-// warps; `live` threads hold channels.
-template <bool VEC>
-__device__ __forceinline__ void hold(const float2 (&f)[4], bool live, const Place& s, int64_t row, int team, int cols,
-                                     int block, int64_t blocks, int form, const HeldOut& out)
+// N rows of an operand; those that do not exist are zeros.
+template <int DT, bool VEC, int N>
+__device__ __forceinline__ void load_rows(const Place& s, const void* base, int64_t pitch, int P, Oct<DT> (&o)[N])
 {
-    const uint32_t m = team_max(live ? oct_amax_bits(f) : 0u, team);
-    const HeldScale hs = held_scale(m, form);
-    if (!live)
-        return;
-    held_store<VEC>(out.q, row * cols + s.chunk0, s.at, held_round(f, hs, form));
-    const int ch = s.chunk0 + s.at.ch;
-    if (ch % block == 0)   // the block's first thread
-        out.scale[row * blocks + ch / block] = hs.scale;
+    const char* p = oct_ptr<DT>(base, s.row0, pitch, s.ch);
+    const int64_t step = P * pitch * elem_size(DT);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (s.live && i < s.rows)
+            o[i] = oct_load<DT, VEC>(p + i * step, s.at);
+        else
+            oct_zero(o[i]);
 }
 
-template <bool VEC>
-__device__ __forceinline__ float scale_of(const float* scale, int64_t row, int64_t blocks, const Place& s, int block)
+// The same of a checkpoint's numbers and scales.
+template <bool VEC, int N>
+__device__ __forceinline__ void load_held(const Place& s, const void* q, const float* scale, const RowLayout& lay,
+                                          int64_t blocks, int block, Held (&h)[N], float (&sc)[N])
 {
-    return __ldg(scale + row * blocks + (s.chunk0 + s.at.ch) / block);
+    const uint8_t* p = static_cast<const uint8_t*>(q) + s.row0 * lay.cols + s.ch;
+    const float* ps = scale + s.row0 * blocks + s.ch / block;
+    const int64_t step = static_cast<int64_t>(lay.P) * lay.cols, step_s = lay.P * blocks;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (s.live && i < s.rows) {
+            h[i] = held_load<VEC>(p + i * step, s.at);
+            sc[i] = __ldg(ps + i * step_s);
+        }
 }
 
 template <int DT, bool VEC>
@@ -67,20 +81,9 @@ __global__ void __launch_bounds__(kLayerThreads) pack_kernel(PackArgs a, const v
 {
     const Place s = place<VEC>(a.lay, kRowsAtOnce);
     Oct<DT> o[kRowsAtOnce];
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        oct_zero(o[i]);
-        if (s.live && r < a.lay.rows)
-            o[i] = oct_load<DT, VEC>(x, r * a.pitch + s.chunk0, s.at);
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        float2 f[4];
-        oct_floats(o[i], f);
-        hold<VEC>(f, s.live && r < a.lay.rows, s, r, a.lay.team, a.lay.cols, a.block, a.blocks, a.form, held);
-    }
+    load_rows<DT, VEC>(s, x, a.pitch, a.lay.P, o);
+    hold_rows<DT, VEC>(o, s.rows, s.live, s.at, a.lay.team, a.form,
+                       HeldPtr(held, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), 0);
 }
 
 template <int DT, bool VEC>
@@ -89,27 +92,17 @@ __global__ void __launch_bounds__(kLayerThreads) unpack_kernel(PackArgs a, const
     const Place s = place<VEC>(a.lay, kRowsAtOnce);
     Held h[kRowsAtOnce];
     float sc[kRowsAtOnce];
+    load_held<VEC>(s, q, scale, a.lay, a.blocks, a.block, h, sc);
+    char* p = oct_ptr<DT>(x, s.row0, a.pitch, s.ch);
+    const int64_t step = a.lay.P * a.pitch * elem_size(DT);
 #pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        if (s.live && r < a.lay.rows) {
-            h[i] = held_load<VEC>(q, r * a.lay.cols + s.chunk0, s.at);
-            sc[i] = scale_of<VEC>(scale, r, a.blocks, s, a.block);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        if (s.live && r < a.lay.rows) {
+    for (int i = 0; i < kRowsAtOnce; ++i)
+        if (s.live && i < s.rows) {
             float2 f[4];
             held_floats(h[i], sc[i], a.form, f);
-            oct_store<DT, VEC>(x, r * a.pitch + s.chunk0, s.at, oct_round<DT>(f));
+            oct_store<DT, VEC>(p + i * step, s.at, oct_round<DT>(f));
         }
-    }
 }
-
-// Two inputs: half as many rows at once.
-constexpr int kGatedRows = 2;
 
 template <int DT, bool VEC, bool HOLD>
 __global__ void __launch_bounds__(kLayerThreads)
@@ -117,20 +110,14 @@ __global__ void __launch_bounds__(kLayerThreads)
 {
     const Place s = place<VEC>(a.lay, kGatedRows);
     Oct<DT> g[kGatedRows], u[kGatedRows];
+    load_rows<DT, VEC>(s, gate, a.in_pitch, a.lay.P, g);
+    load_rows<DT, VEC>(s, up, a.in_pitch, a.lay.P, u);
+    char* ph = oct_ptr<DT>(h, s.row0, a.out_pitch, s.ch);
+    const int64_t step = a.lay.P * a.out_pitch * elem_size(DT);
 #pragma unroll
     for (int i = 0; i < kGatedRows; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        oct_zero(g[i]);
-        oct_zero(u[i]);
-        if (s.live && r < a.lay.rows) {
-            g[i] = oct_load<DT, VEC>(gate, r * a.in_pitch + s.chunk0, s.at);
-            u[i] = oct_load<DT, VEC>(up, r * a.in_pitch + s.chunk0, s.at);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kGatedRows; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        const bool live = s.live && r < a.lay.rows;
+        if (!(s.live && i < s.rows))
+            continue;
         float2 fg[4], fu[4], fh[4];
         oct_floats(g[i], fg);
         oct_floats(u[i], fu);
@@ -138,12 +125,13 @@ __global__ void __launch_bounds__(kLayerThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             fh[j] = __fmul2_rn(fh[j], fu[j]);
-        if (live)
-            oct_store<DT, VEC>(h, r * a.out_pitch + s.chunk0, s.at, oct_round<DT>(fh));
-        if constexpr (HOLD) {
-            hold<VEC>(fg, live, s, r, a.lay.team, a.lay.cols, a.block, a.blocks, a.form, held_gate);
-            hold<VEC>(fu, live, s, r, a.lay.team, a.lay.cols, a.block, a.blocks, a.form, held_up);
-        }
+        oct_store<DT, VEC>(ph + i * step, s.at, oct_round<DT>(fh));
+    }
+    if constexpr (HOLD) {
+        hold_rows<DT, VEC>(g, s.rows, s.live, s.at, a.lay.team, a.form,
+                           HeldPtr(held_gate, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), 0);
+        hold_rows<DT, VEC>(u, s.rows, s.live, s.at, a.lay.team, a.form,
+                           HeldPtr(held_up, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), 0);
     }
 }
 
@@ -155,26 +143,21 @@ __global__ void __launch_bounds__(kLayerThreads)
     Oct<DT> d[kGatedRows], g[kGatedRows], u[kGatedRows];
     Held qg[kGatedRows], qu[kGatedRows];
     float sg[kGatedRows], su[kGatedRows];
-#pragma unroll
-    for (int i = 0; i < kGatedRows; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        if (s.live && r < a.lay.rows) {
-            d[i] = oct_load<DT, VEC>(dh, r * a.out_pitch + s.chunk0, s.at);
-            if constexpr (HELD) {
-                qg[i] = held_load<VEC>(gate.q, r * a.lay.cols + s.chunk0, s.at);
-                qu[i] = held_load<VEC>(up.q, r * a.lay.cols + s.chunk0, s.at);
-                sg[i] = scale_of<VEC>(gate.scale, r, a.blocks, s, a.block);
-                su[i] = scale_of<VEC>(up.scale, r, a.blocks, s, a.block);
-            } else {
-                g[i] = oct_load<DT, VEC>(gate.x, r * a.in_pitch + s.chunk0, s.at);
-                u[i] = oct_load<DT, VEC>(up.x, r * a.in_pitch + s.chunk0, s.at);
-            }
-        }
+    load_rows<DT, VEC>(s, dh, a.out_pitch, a.lay.P, d);
+    if constexpr (HELD) {
+        load_held<VEC>(s, gate.q, gate.scale, a.lay, a.blocks, a.block, qg, sg);
+        load_held<VEC>(s, up.q, up.scale, a.lay, a.blocks, a.block, qu, su);
+    } else {
+        load_rows<DT, VEC>(s, gate.x, a.in_pitch, a.lay.P, g);
+        load_rows<DT, VEC>(s, up.x, a.in_pitch, a.lay.P, u);
     }
+    char* pg = oct_ptr<DT>(dgate, s.row0, a.in_pitch, s.ch);
+    char* pu = oct_ptr<DT>(dup, s.row0, a.in_pitch, s.ch);
+    char* ph = oct_ptr<DT>(h, s.row0, a.out_pitch, s.ch);
+    const int64_t in_step = a.lay.P * a.in_pitch * elem_size(DT), out_step = a.lay.P * a.out_pitch * elem_size(DT);
 #pragma unroll
     for (int i = 0; i < kGatedRows; ++i) {
-        const int64_t r = s.row0 + i * a.lay.P;
-        if (!(s.live && r < a.lay.rows))
+        if (!(s.live && i < s.rows))
             continue;
         float2 fd[4], fg[4], fu[4];
         oct_floats(d[i], fd);
@@ -193,10 +176,10 @@ __global__ void __launch_bounds__(kLayerThreads)
             ou[j] = __fmul2_rn(fd[j], value[j]);
             oh[j] = __fmul2_rn(value[j], fu[j]);
         }
-        oct_store<DT, VEC>(dgate, r * a.in_pitch + s.chunk0, s.at, oct_round<DT>(og));
-        oct_store<DT, VEC>(dup, r * a.in_pitch + s.chunk0, s.at, oct_round<DT>(ou));
+        oct_store<DT, VEC>(pg + i * in_step, s.at, oct_round<DT>(og));
+        oct_store<DT, VEC>(pu + i * in_step, s.at, oct_round<DT>(ou));
         if (h)
-            oct_store<DT, VEC>(h, r * a.out_pitch + s.chunk0, s.at, oct_round<DT>(oh));
+            oct_store<DT, VEC>(ph + i * out_step, s.at, oct_round<DT>(oh));
     }
 }
 

@@ -11,8 +11,15 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRowsAtOnce = 4;   // rows whose loads a thread issues together, one batch ahead of their use
-constexpr int kGradRows = 2;     // two operands: half as many
+// Rows whose loads a thread issues before it uses the first.
+constexpr int kApplyRows = 4;
+constexpr int kGradRows = 4;
+template <int DT>
+TSX_HD constexpr int stats_rows() { return DT == TSX_F32 ? 4 : 8; }
+
+// CTAs to an SM that the registers are cut for.
+template <int DT, bool VEC>
+TSX_HD constexpr int forward_ctas() { return DT == TSX_F32 || !VEC ? 3 : 4; }
 
 // A CTA's range of rows: blockIdx.x counts ranges sample by sample.  The
 // `ranks` CTAs of a cluster take neighbouring ranges and join their sums.
@@ -21,9 +28,10 @@ struct Range {
     int64_t row0;   // first row, counted through all samples
     int rows;       // rows of the range
     int rank;
+    int mine;       // rows of the thread's lane: p, p + P, ...
 };
 
-__device__ __forceinline__ Range range_of(const NormArgs& a)
+__device__ __forceinline__ Range range_of(const NormArgs& a, const NormPlace& s)
 {
     Range r;
     const unsigned splits = static_cast<unsigned>(a.lay.splits);
@@ -32,6 +40,7 @@ __device__ __forceinline__ Range range_of(const NormArgs& a)
     r.rank = static_cast<int>(static_cast<unsigned>(r.split) % static_cast<unsigned>(a.lay.ranks));
     r.row0 = r.sample * a.l + r.split * a.lay.range;
     r.rows = range_rows(a, a.lay.range, r.split);
+    r.mine = s.p < a.lay.P && s.p < r.rows ? (r.rows - s.p + a.lay.P - 1) / a.lay.P : 0;
     return r;
 }
 
@@ -45,47 +54,25 @@ __device__ __forceinline__ float2* part_of(const NormArgs& a, const NormPlace& s
 
 // ------------------------------------------------------------- forward
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_rows(const NormArgs& a, const NormPlace& s, const Range& r, const void* x,
-                                          int r0, Oct<DT> (&o)[kRowsAtOnce])
-{
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i)
-        if (s.live && r0 + i * a.lay.P < r.rows)
-            o[i] = oct_load<DT, VEC>(x, (r.row0 + r0 + i * a.lay.P) * a.x_pitch + s.ch0, s.at);
-        else
-            oct_zero(o[i]);
-}
-
 // First kernel: (mean, M2) of every cluster's range, run and group.
 template <int DT, bool VEC, bool BY_OCT>
-__global__ void __launch_bounds__(kNormThreads, DT == TSX_F32 ? 2 : 3) norm_stats_kernel(NormArgs a, const void* x, float2* part)
+__global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>()) norm_stats_kernel(NormArgs a, const void* x, float2* part)
 {
     extern __shared__ float4 shared4[];
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a);
+    const Range r = range_of(a, s);
     const int P = a.lay.P, width = run_width<BY_OCT>(s), stride = slot_stride(width);
     float4* spare = shared4;                                                    // [warps]
     float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);        // [run_groups]
     float2* slots = sums + a.lay.run_groups;                                    // [P][stride]
     Triples<BY_OCT> t;
     t.clear();
-    Oct<DT> o[kRowsAtOnce];
-    load_rows<DT, VEC>(a, s, r, x, s.p, o);
-    for (int r0 = s.p; s.live && r0 < r.rows; r0 += kRowsAtOnce * P) {
-        Oct<DT> next[kRowsAtOnce];
-        load_rows<DT, VEC>(a, s, r, x, r0 + kRowsAtOnce * P, next);
-        float2 f[kRowsAtOnce][4];
-#pragma unroll
-        for (int i = 0; i < kRowsAtOnce; ++i)
-            oct_floats(o[i], f[i]);
-        if (r0 + (kRowsAtOnce - 1) * P < r.rows)
-            t.template add_rows<kRowsAtOnce, true>(f, kRowsAtOnce);
-        else
-            t.template add_rows<kRowsAtOnce, false>(f, (r.rows - r0 + P - 1) / P);
-#pragma unroll
-        for (int i = 0; i < kRowsAtOnce; ++i)
-            o[i] = next[i];
+    constexpr int N = stats_rows<DT>();
+    const Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
+    for (int i0 = 0; s.live && i0 < r.mine; i0 += N) {
+        Oct<DT> o[N];
+        load_rows<DT, VEC>(w, s.at, i0, r.mine - i0, o);
+        t.add_octs(o, r.mine - i0);
     }
     if (s.live)
         t.leave(s.at, slots + s.p * stride);
@@ -158,16 +145,14 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
 
 // Second kernel: y, and with HOLD the checkpoint of x.
 template <int DT, bool VEC, bool BY_OCT, bool HOLD>
-__global__ void __launch_bounds__(kNormThreads, DT == TSX_F32 ? 2 : 3)
+__global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
     norm_apply_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                       float* rstd, HeldOut held, const float2* part)
 {
     extern __shared__ float4 work[];   // [threads or groups], then [run_groups] statistics
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a);
+    const Range r = range_of(a, s);
     const int P = a.lay.P;
-    Oct<DT> o[kRowsAtOnce];
-    load_rows<DT, VEC>(a, s, r, x, s.p, o);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
@@ -178,38 +163,30 @@ __global__ void __launch_bounds__(kNormThreads, DT == TSX_F32 ? 2 : 3)
             mean[r.sample * a.groups + s.group0 + g] = stats[g].x;
             rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
         }
-    // whole warps walk together: the teams' shuffles need every lane
-    for (int base = 0; base < r.rows; base += kRowsAtOnce * P) {
-        const int r0 = base + s.p;
-        Oct<DT> next[kRowsAtOnce];
-        load_rows<DT, VEC>(a, s, r, x, r0 + kRowsAtOnce * P, next);
+    k.scale_weight();
+    const Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
+    const WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
+    HeldPtr to;
+    if constexpr (HOLD)
+        to = HeldPtr(held, r.row0 + s.p, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
+    // a team's threads share their rows, so they come to its shuffles together
+    for (int i0 = 0; i0 < r.mine; i0 += kApplyRows) {
+        Oct<DT> o[kApplyRows];
+        load_rows<DT, VEC>(w, s.at, i0, s.live ? r.mine - i0 : 0, o);
 #pragma unroll
-        for (int i = 0; i < kRowsAtOnce; ++i) {
-            const int64_t row = r.row0 + r0 + i * P;
-            const bool live = s.live && r0 + i * P < r.rows;
-            float2 f[4], out[4];
-            oct_floats(o[i], f);
-            k.apply(a, f, out);
-            if (live)
-                oct_store<DT, VEC>(y, row * a.y_pitch + s.ch0, s.at, oct_round<DT>(out));
-            if constexpr (HOLD)
-                hold<VEC>(a, s, f, live, row, held);
-            o[i] = next[i];
-        }
+        for (int i = 0; i < kApplyRows; ++i)
+            if (s.live && i0 + i < r.mine) {
+                float2 f[4], v[4];
+                oct_floats(o[i], f);
+                k.apply(a.act, f, v);
+                oct_store<DT, VEC>(out.p + (i0 + i) * out.step, s.at, oct_round<DT>(v));
+            }
+        if constexpr (HOLD)
+            hold_rows<DT, VEC>(o, r.mine - i0, s.live, s.at, a.lay.team, a.form, to, i0);
     }
 }
 
 // ------------------------------------------------------------ backward
-
-template <int DT, bool VEC, bool HELD>
-__device__ __forceinline__ void load_grad_rows(const NormArgs& a, const NormPlace& s, const Range& r, const void* dy,
-                                               const Saved& x, int r0, GradRow<DT, VEC, HELD> (&g)[kGradRows])
-{
-#pragma unroll
-    for (int i = 0; i < kGradRows; ++i)
-        if (s.live && r0 + i * a.lay.P < r.rows)
-            g[i].load(a, s, dy, x, r.row0 + r0 + i * a.lay.P);
-}
 
 __device__ __forceinline__ void load_stats(const NormArgs& a, const NormPlace& s, int64_t sample, const float* mean,
                                            const float* rstd, float2* stats)
@@ -230,14 +207,12 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 {
     extern __shared__ float2 shared[];
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a);
+    const Range r = range_of(a, s);
     const int P = a.lay.P, width = s.at.cols, stride = slot_stride(width);
     float2* stats = shared;                         // [run_groups]: (mean, rstd), then (S1, S2)
     float2* work = stats + a.lay.run_groups;        // [threads]
     float2* columns = work + kNormThreads;          // [run_cols]
     float2* slots = columns + a.lay.run_cols;       // [P][stride]
-    GradRow<DT, VEC, HELD> g[kGradRows];
-    load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, s.p, g);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     load_stats(a, s, r.sample, mean, rstd, stats);
@@ -246,12 +221,16 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-    for (int r0 = s.p; s.live && r0 < r.rows; r0 += kGradRows * P) {
-        GradRow<DT, VEC, HELD> next[kGradRows];
-        load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, r0 + kGradRows * P, next);
+    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    for (int i0 = 0; s.live && i0 < r.mine; i0 += kGradRows) {
+        GradRow<DT, VEC, HELD> g[kGradRows];
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i) {
-            if (r0 + i * P < r.rows) {
+        for (int i = 0; i < kGradRows; ++i)
+            if (i0 + i < r.mine)
+                g[i].load(a, s, w, i0 + i);
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i)
+            if (i0 + i < r.mine) {
                 float2 fd[4], fx[4], hat[4], dz[4];
                 oct_floats(g[i].dy, fd);
                 g[i].saved_floats(a, fx);
@@ -262,8 +241,6 @@ __global__ void __launch_bounds__(kNormThreads, 2)
                     szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
                 }
             }
-            g[i] = next[i];
-        }
     }
     if (s.live)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
@@ -299,13 +276,11 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 {
     extern __shared__ float2 shared[];
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a);
+    const Range r = range_of(a, s);
     const int P = a.lay.P;
     float2* stats = shared;                      // [run_groups]
     float2* sums = stats + a.lay.run_groups;     // [run_groups]: -S1 / M, -S2 / M
     float2* work = sums + a.lay.run_groups;      // [threads or groups]
-    GradRow<DT, VEC, HELD> g[kGradRows];
-    load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, s.p, g);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     const int count = parts_of(a);
@@ -332,21 +307,24 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     k.statistics(a, s, stats);
     Grouped<BY_OCT> s1, s2;
     grouped<BY_OCT>(a, s, sums, s1, s2);
-    for (int r0 = s.p; s.live && r0 < r.rows; r0 += kGradRows * P) {
-        GradRow<DT, VEC, HELD> next[kGradRows];
-        load_grad_rows<DT, VEC, HELD>(a, s, r, dy, x, r0 + kGradRows * P, next);
+    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    const WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
+    for (int i0 = 0; s.live && i0 < r.mine; i0 += kGradRows) {
+        GradRow<DT, VEC, HELD> g[kGradRows];
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i) {
-            if (r0 + i * P < r.rows) {
-                float2 fd[4], fx[4], hat[4], dz[4], out[4];
+        for (int i = 0; i < kGradRows; ++i)
+            if (i0 + i < r.mine)
+                g[i].load(a, s, w, i0 + i);
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i)
+            if (i0 + i < r.mine) {
+                float2 fd[4], fx[4], hat[4], dz[4], v[4];
                 oct_floats(g[i].dy, fd);
                 g[i].saved_floats(a, fx);
                 k.slopes(a, fd, fx, hat, dz);
-                k.gradient(dz, hat, s1, s2, out);
-                oct_store<DT, VEC>(dx, (r.row0 + r0 + i * P) * a.x_pitch + s.ch0, s.at, oct_round<DT>(out));
+                k.gradient(dz, hat, s1, s2, v);
+                oct_store<DT, VEC>(out.p + (i0 + i) * out.step, s.at, oct_round<DT>(v));
             }
-            g[i] = next[i];
-        }
     }
 }
 

@@ -26,6 +26,7 @@ struct HeldPlace {
     int64_t sample;
     int64_t row0;     // the part's first row, counted through all samples
     int rows;         // rows of the part
+    int mine;         // rows of the thread's lane
 };
 
 __device__ __forceinline__ HeldPlace held_place(const NormArgs& a, NormPlace& s)
@@ -40,11 +41,12 @@ __device__ __forceinline__ HeldPlace held_place(const NormArgs& a, NormPlace& s)
     s.live = s.live && h.sample < a.n;
     h.row0 = h.sample * a.l + h.rank * lay.range;
     h.rows = range_rows(a, lay.range, h.rank);
+    h.mine = s.p < lay.P && h.sample < a.n && h.lane < h.rows ? (h.rows - h.lane + lay.lanes - 1) / lay.lanes : 0;
     return h;
 }
 
 template <int DT, bool BY_OCT, bool HOLD, int ROWS>
-__global__ void __launch_bounds__(kNormThreads, ROWS * (DT == TSX_F32 ? 2 : 1) > 8 ? 2 : 3)
+__global__ void __launch_bounds__(kNormThreads, 2)
     norm_held_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                      float* rstd, HeldOut held)
 {
@@ -53,16 +55,8 @@ __global__ void __launch_bounds__(kNormThreads, ROWS * (DT == TSX_F32 ? 2 : 1) >
     NormPlace s = norm_place<true>(a);
     const HeldPlace h = held_place(a, s);
     Oct<DT> o[ROWS];
-    int have = 0;   // rows that the thread holds
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int r = h.lane + i * lay.lanes;
-        oct_zero(o[i]);
-        if (s.live && r < h.rows) {
-            o[i] = oct_load<DT, true>(x, (h.row0 + r) * a.x_pitch + s.ch0, s.at);
-            have = i + 1;
-        }
-    }
+    const int have = h.mine;
+    load_rows<DT, true>(walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s), s.at, 0, s.live ? have : 0, o);
     Chan<BY_OCT> k;
     k.template params<DT, true>(a, s, weight, bias);
 
@@ -73,17 +67,8 @@ __global__ void __launch_bounds__(kNormThreads, ROWS * (DT == TSX_F32 ? 2 : 1) >
     float2* slots = stats + items;                                          // [P][stride]
     Triples<BY_OCT> t;
     t.clear();
-#pragma unroll
-    for (int i0 = 0; i0 < ROWS; i0 += 4) {
-        float2 f[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            oct_floats(o[i0 + i], f[i]);
-        if (have >= i0 + 4)
-            t.template add_rows<4, true>(f, 4);
-        else if (have > i0)
-            t.template add_rows<4, false>(f, have - i0);
-    }
+    if (s.live)
+        t.add_octs(o, have);
     if (s.p < lay.P && s.at.ch < s.at.cols)   // absent samples leave zeros
         t.leave(s.at, slots + s.p * stride);
     __syncthreads();
@@ -121,17 +106,24 @@ __global__ void __launch_bounds__(kNormThreads, ROWS * (DT == TSX_F32 ? 2 : 1) >
         cluster_arrive();   // this CTA has read the others; they may leave once all have
     __syncthreads();
     k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
+    k.scale_weight();
+    const WalkOut out = walk_out<DT>(y, h.row0 + h.lane, lay.lanes, a.y_pitch, s);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int64_t row = h.row0 + h.lane + i * lay.lanes;
-        float2 f[4], out[4];
-        oct_floats(o[i], f);
-        if (i < have) {
-            k.apply(a, f, out);
-            oct_store<DT, true>(y, row * a.y_pitch + s.ch0, s.at, oct_round<DT>(out));
+    for (int i = 0; i < ROWS; ++i)
+        if (s.live && i < have) {
+            float2 f[4], v[4];
+            oct_floats(o[i], f);
+            k.apply(a.act, f, v);
+            oct_store<DT, true>(out.p + i * out.step, s.at, oct_round<DT>(v));
         }
-        if constexpr (HOLD)
-            hold<true>(a, s, f, i < have, row, held);
+    if constexpr (HOLD) {
+        const HeldPtr to(held, h.row0 + h.lane, lay.lanes, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
+#pragma unroll
+        for (int i0 = 0; i0 < ROWS; i0 += 4) {
+            const Oct<DT> four[4] = {o[i0], o[i0 + 1], o[i0 + 2], o[i0 + 3]};
+            if (i0 < have)
+                hold_rows<DT, true>(four, have - i0, s.live, s.at, lay.team, a.form, to, i0);
+        }
     }
     if (lay.ranks > 1)
         cluster_wait();
@@ -149,15 +141,12 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     NormPlace s = norm_place<true>(a);
     const HeldPlace h = held_place(a, s);
     GradRow<DT, true, HELD> g[kHeldGradRows];
-    int have = 0;
+    const int have = s.live ? h.mine : 0;
+    const GradWalk<DT, true, HELD> w(a, s, dy, x, h.row0 + h.lane, lay.lanes);
 #pragma unroll
-    for (int i = 0; i < kHeldGradRows; ++i) {
-        const int r = h.lane + i * lay.lanes;
-        if (s.live && r < h.rows) {
-            g[i].load(a, s, dy, x, h.row0 + r);
-            have = i + 1;
-        }
-    }
+    for (int i = 0; i < kHeldGradRows; ++i)
+        if (i < have)
+            g[i].load(a, s, w, i);
     Chan<BY_OCT> k;
     k.template params<DT, true>(a, s, weight, bias);
     const int width = s.at.cols, stride = slot_stride(width), items = lay.samples * s.groups;
@@ -225,6 +214,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     __syncthreads();
     Grouped<BY_OCT> s1, s2;
     grouped<BY_OCT>(a, s, stats + (s.live ? h.q : 0) * s.groups, s1, s2);
+    const WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
 #pragma unroll
     for (int i = 0; i < kHeldGradRows; ++i)
         if (i < have) {
@@ -234,7 +224,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             for (int j = 0; j < 4; ++j)
                 hat[j] = k.hat(fx, j);
             k.gradient(dz[i], hat, s1, s2, res);
-            oct_store<DT, true>(dx, (h.row0 + h.lane + i * lay.lanes) * a.x_pitch + s.ch0, s.at, oct_round<DT>(res));
+            oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(res));
         }
     if (lay.ranks > 1)
         cluster_wait();

@@ -32,7 +32,7 @@ __device__ __forceinline__ float oct_sum(const float2 (&f)[4])
 }
 
 template <int DT, bool HOLD>
-__global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 ? 2 : 3)
+__global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
     norm_token_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                       float* rstd, HeldOut held)
 {
@@ -45,22 +45,14 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 ? 2 : 3)
     const bool first = s.at.ch % a.per_group == 0;
     const int P = a.lay.P;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (P * kTokenRows);
-    Oct<DT> o[kTokenRows];
-    int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenRows);
-    auto load = [&](int64_t from, Oct<DT> (&to)[kTokenRows]) {
-#pragma unroll
-        for (int i = 0; i < kTokenRows; ++i) {
-            const int64_t row = from + i * P + s.p;
-            if (s.live && row < a.n)
-                to[i] = oct_load<DT, true>(x, row * a.x_pitch + s.ch0, s.at);
-            else
-                oct_zero(to[i]);
-        }
-    };
-    load(base, o);
-    for (; base < a.n; base += stride) {
-        Oct<DT> next[kTokenRows];
-        load(base + stride, next);
+    // rows of the thread: first + i * P for i < 4, then a stride further on
+    const Walk w = walk<DT>(x, 0, P, a.x_pitch, s);
+    const WalkOut to = walk_out<DT>(y, 0, P, a.y_pitch, s);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenRows); base < a.n; base += stride) {
+        const int64_t row0 = base + s.p;
+        const int n = s.p < P && row0 < a.n ? static_cast<int>(min((a.n - row0 + P - 1) / P, int64_t(kTokenRows))) : 0;
+        Oct<DT> o[kTokenRows];
+        load_rows<DT, true>(Walk{w.p + row0 * a.x_pitch * elem_size(DT), w.step}, s.at, 0, s.live ? n : 0, o);
         float mu[kTokenRows], dev[kTokenRows];
 #pragma unroll
         for (int i = 0; i < kTokenRows; ++i) {
@@ -82,26 +74,25 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 ? 2 : 3)
             dev[i] = sq.x + sq.y;
         }
         team_sums(dev, lanes);
+        char* out = to.p + row0 * a.y_pitch * elem_size(DT);
 #pragma unroll
         for (int i = 0; i < kTokenRows; ++i) {
-            const int64_t row = base + i * P + s.p;
-            const bool live = s.live && row < a.n;
             const float rs = rstd_of(dev[i], m, a.eps);
-            float2 f[4], out[4];
-            oct_floats(o[i], f);
-            k.statistics(mu[i], rs);
-            k.apply(a, f, out);
-            if (live) {
-                oct_store<DT, true>(y, row * a.y_pitch + s.ch0, s.at, oct_round<DT>(out));
+            if (s.live && i < n) {
+                float2 f[4], v[4];
+                oct_floats(o[i], f);
+                k.statistics(mu[i], rs);
+                k.apply_scaled(a.act, f, v);
+                oct_store<DT, true>(out + i * to.step, s.at, oct_round<DT>(v));
                 if (first) {
-                    mean[row * a.groups + group] = mu[i];
-                    rstd[row * a.groups + group] = rs;
+                    mean[(row0 + i * P) * a.groups + group] = mu[i];
+                    rstd[(row0 + i * P) * a.groups + group] = rs;
                 }
             }
-            if constexpr (HOLD)
-                hold<true>(a, s, f, live, row, held);
-            o[i] = next[i];
         }
+        if constexpr (HOLD)
+            hold_rows<DT, true>(o, n, s.live, s.at, a.lay.team, a.form,
+                                HeldPtr(held, row0, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block), 0);
     }
 }
 
@@ -119,41 +110,33 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
     const int group = s.group0 + local_group(a, s.at.ch);
     const int P = a.lay.P;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (P * kTokenGradRows);
-    struct Row {
-        GradRow<DT, true, HELD> g;
-        float mu, rs;
-    };
-    Row cur[kTokenGradRows];
-    auto load = [&](int64_t from, Row (&to)[kTokenGradRows]) {
-#pragma unroll
-        for (int i = 0; i < kTokenGradRows; ++i) {
-            const int64_t row = from + i * P + s.p;
-            if (s.live && row < a.n) {
-                to[i].g.load(a, s, dy, x, row);
-                to[i].mu = __ldg(mean + row * a.groups + group);
-                to[i].rs = __ldg(rstd + row * a.groups + group);
-            }
-        }
-    };
     float2 sz[4], szx[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-    int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenGradRows);
-    load(base, cur);
-    for (; base < a.n; base += stride) {
-        Row next[kTokenGradRows];
-        load(base + stride, next);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenGradRows); base < a.n; base += stride) {
+        const int64_t row0 = base + s.p;
+        const int n = s.live && row0 < a.n ? static_cast<int>(min((a.n - row0 + P - 1) / P, int64_t(kTokenGradRows))) : 0;
+        const GradWalk<DT, true, HELD> w(a, s, dy, x, row0, P);
+        GradRow<DT, true, HELD> g[kTokenGradRows];
+        float mu[kTokenGradRows], rs[kTokenGradRows];
+#pragma unroll
+        for (int i = 0; i < kTokenGradRows; ++i)
+            if (i < n) {
+                g[i].load(a, s, w, i);
+                mu[i] = __ldg(mean + (row0 + i * P) * a.groups + group);
+                rs[i] = __ldg(rstd + (row0 + i * P) * a.groups + group);
+            }
         float2 hat[kTokenGradRows][4], dz[kTokenGradRows][4];
         float s1[kTokenGradRows], s2[kTokenGradRows];
 #pragma unroll
         for (int i = 0; i < kTokenGradRows; ++i) {
             s1[i] = s2[i] = 0.f;
-            if (s.live && base + i * P + s.p < a.n) {
+            if (i < n) {
                 float2 fd[4], fx[4], t1 = make_float2(0.f, 0.f), t2 = t1;
-                oct_floats(cur[i].g.dy, fd);
-                cur[i].g.saved_floats(a, fx);
-                k.statistics(cur[i].mu, cur[i].rs);
+                oct_floats(g[i].dy, fd);
+                g[i].saved_floats(a, fx);
+                k.statistics(mu[i], rs[i]);
                 k.slopes(a, fd, fx, hat[i], dz[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -169,20 +152,18 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
         }
         team_sums(s1, lanes);
         team_sums(s2, lanes);
+        const WalkOut to = walk_out<DT>(dx, row0, P, a.x_pitch, s);
 #pragma unroll
-        for (int i = 0; i < kTokenGradRows; ++i) {
-            const int64_t row = base + i * P + s.p;
-            if (s.live && row < a.n) {
+        for (int i = 0; i < kTokenGradRows; ++i)
+            if (i < n) {
                 Grouped<true> g1, g2;
                 g1.v[0] = pair_of(s1[i] * minus_m);
                 g2.v[0] = pair_of(s2[i] * minus_m);
                 float2 out[4];
-                k.statistics(cur[i].mu, cur[i].rs);
+                k.statistics(mu[i], rs[i]);
                 k.gradient(dz[i], hat[i], g1, g2, out);
-                oct_store<DT, true>(dx, row * a.x_pitch + s.ch0, s.at, oct_round<DT>(out));
+                oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(out));
             }
-            cur[i] = next[i];
-        }
     }
     const int width = s.at.cols, slot = slot_stride(width);
     float2* work = shared;                      // [threads]

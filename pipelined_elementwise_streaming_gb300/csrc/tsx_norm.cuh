@@ -203,6 +203,22 @@ struct Triples {
         if (ALL || have)
             join(n, mu, dev);
     }
+    // The first `have` of N rows' octs, four at a time.
+    template <int DT, int ROWS>
+    __device__ __forceinline__ void add_octs(const Oct<DT> (&o)[ROWS], int have)
+    {
+#pragma unroll
+        for (int i0 = 0; i0 < ROWS; i0 += 4) {
+            float2 f[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                oct_floats(o[i0 + i], f[i]);
+            if (have >= i0 + 4)
+                add_rows<4, true>(f, 4);
+            else if (have > i0)
+                add_rows<4, false>(f, have - i0);
+        }
+    }
     // To a row of shared-memory columns (octs or channels) as (mean, M2).
     __device__ __forceinline__ void leave(const OctAt& at, float2* row) const
     {
@@ -482,13 +498,29 @@ struct Chan {
     {
         return __fmul2_rn(__fadd2_rn(x[j], minus.at(j)), rstd.at(j));
     }
-    __device__ __forceinline__ void apply(const NormArgs& a, const float2 (&x)[4], float2 (&y)[4]) const
+    // y of the forward pass, for which w has become rstd weight
+    __device__ __forceinline__ void scale_weight()
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = __fmul2_rn(rstd.at(j), w[j]);
+    }
+    __device__ __forceinline__ void apply(int act, const float2 (&x)[4], float2 (&y)[4]) const
+    {
+        float2 z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            z[j] = __ffma2_rn(__fadd2_rn(x[j], minus.at(j)), w[j], b[j]);
+        act_value(act, z, y);
+    }
+    // the same with the weight as it is
+    __device__ __forceinline__ void apply_scaled(int act, const float2 (&x)[4], float2 (&y)[4]) const
     {
         float2 z[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             z[j] = __ffma2_rn(hat(x, j), w[j], b[j]);
-        act_value(a.act, z, y);
+        act_value(act, z, y);
     }
     // xhat and dz
     __device__ __forceinline__ void slopes(const NormArgs& a, const float2 (&dy)[4], const float2 (&x)[4],
@@ -516,41 +548,94 @@ struct Chan {
     }
 };
 
-// An oct to 8 bits, as the forward pass saves it.  By whole warps.
-template <bool VEC>
-__device__ __forceinline__ void hold(const NormArgs& a, const NormPlace& s, const float2 (&f)[4], bool live,
-                                     int64_t row, const HeldOut& out)
+// Where a thread reads or writes an operand: its first row, and the step from
+// one of its rows to the next.
+struct Walk {
+    const char* p;
+    int64_t step;
+};
+template <int DT>
+__device__ __forceinline__ Walk walk(const void* base, int64_t row, int rows_apart, int64_t pitch, const NormPlace& s)
 {
-    const uint32_t m = team_max(live ? oct_amax_bits(f) : 0u, a.lay.team);
-    const HeldScale hs = held_scale(m, a.form);
-    if (!live)
-        return;
-    held_store<VEC>(out.q, row * a.c + s.ch0, s.at, held_round(f, hs, a.form));
-    const int ch = s.ch0 + s.at.ch;
-    if (ch % a.block == 0)
-        out.scale[row * a.blocks + ch / a.block] = hs.scale;
+    return Walk{oct_ptr<DT>(base, row, pitch, s.ch0 + s.at.ch), rows_apart * pitch * elem_size(DT)};
+}
+struct WalkOut {
+    char* p;
+    int64_t step;
+};
+template <int DT>
+__device__ __forceinline__ WalkOut walk_out(void* base, int64_t row, int rows_apart, int64_t pitch,
+                                            const NormPlace& s)
+{
+    return WalkOut{oct_ptr<DT>(base, row, pitch, s.ch0 + s.at.ch), rows_apart * pitch * elem_size(DT)};
 }
 
-// What the backward pass loads of one row's oct.
+// N rows from row `first` of a walk on, of which the thread has `n` (>= N: no
+// row is looked at twice).
+template <int DT, bool VEC, int N>
+__device__ __forceinline__ void load_rows(const Walk& w, const OctAt& at, int first, int n, Oct<DT> (&o)[N])
+{
+    const char* p = w.p + first * w.step;
+    if (n >= N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            o[i] = oct_load<DT, VEC>(p + i * w.step, at);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n)
+                o[i] = oct_load<DT, VEC>(p + i * w.step, at);
+            else
+                oct_zero(o[i]);
+    }
+}
+
+// What the backward pass reads: dy, and x or its checkpoint.
+template <int DT, bool VEC, bool HELD>
+struct GradWalk {
+    Walk dy, x;
+    const uint8_t* q;
+    const float* scale;
+    int64_t q_step, scale_step;
+    __device__ __forceinline__ GradWalk(const NormArgs& a, const NormPlace& s, const void* pdy, const Saved& src,
+                                        int64_t row, int rows_apart)
+    {
+        dy = walk<DT>(pdy, row, rows_apart, a.y_pitch, s);
+        if constexpr (HELD) {
+            q = static_cast<const uint8_t*>(src.q) + row * a.c + s.ch0 + s.at.ch;
+            q_step = static_cast<int64_t>(rows_apart) * a.c;
+            scale = src.scale + row * a.blocks + (VEC ? (s.ch0 + s.at.ch) / a.block : 0);
+            scale_step = rows_apart * a.blocks;
+        } else {
+            x = walk<DT>(src.x, row, rows_apart, a.x_pitch, s);
+        }
+    }
+};
+
+// One row of them.
 template <int DT, bool VEC, bool HELD>
 struct GradRow {
     Oct<DT> dy;
     Oct<DT> x;      // HELD: unused
     Held q;
     float scale[VEC ? 1 : 8];   // consecutive channels of an aligned oct share a block; others need not
-    __device__ __forceinline__ void load(const NormArgs& a, const NormPlace& s, const void* pdy, const Saved& src,
-                                         int64_t row)
+    __device__ __forceinline__ void load(const NormArgs& a, const NormPlace& s, const GradWalk<DT, VEC, HELD>& w,
+                                         int i)
     {
-        dy = oct_load<DT, VEC>(pdy, row * a.y_pitch + s.ch0, s.at);
+        dy = oct_load<DT, VEC>(w.dy.p + i * w.dy.step, s.at);
         if constexpr (HELD) {
-            q = held_load<VEC>(src.q, row * a.c + s.ch0, s.at);
+            q = held_load<VEC>(w.q + i * w.q_step, s.at);
+            if constexpr (VEC) {
+                scale[0] = __ldg(w.scale + i * w.scale_step);
+            } else {
 #pragma unroll
-            for (int j = 0; j < (VEC ? 1 : 8); ++j) {
-                const int ch = s.at.ch + j * s.at.step;
-                scale[j] = ch < s.at.cols ? __ldg(src.scale + row * a.blocks + (s.ch0 + ch) / a.block) : 0.f;
+                for (int j = 0; j < 8; ++j) {
+                    const int ch = s.at.ch + j * s.at.step;
+                    scale[j] = ch < s.at.cols ? __ldg(w.scale + i * w.scale_step + (s.ch0 + ch) / a.block) : 0.f;
+                }
             }
         } else {
-            x = oct_load<DT, VEC>(src.x, row * a.x_pitch + s.ch0, s.at);
+            x = oct_load<DT, VEC>(w.x.p + i * w.x.step, s.at);
         }
     }
     __device__ __forceinline__ void saved_floats(const NormArgs& a, float2 (&fx)[4]) const

@@ -60,15 +60,26 @@ __device__ __forceinline__ void oct_zero(Oct<DT>& o)
         o.w[i] = 0;
 }
 
+// Address of an oct's first element; rows are `pitch` elements apart.
+template <int DT>
+__device__ __forceinline__ const char* oct_ptr(const void* base, int64_t row, int64_t pitch, int ch)
+{
+    return static_cast<const char*>(base) + (row * pitch + ch) * elem_size(DT);
+}
+template <int DT>
+__device__ __forceinline__ char* oct_ptr(void* base, int64_t row, int64_t pitch, int ch)
+{
+    return static_cast<char*>(base) + (row * pitch + ch) * elem_size(DT);
+}
+
 // The vector loads go past L1.  They are no read-only-cache loads, since an
 // output may be one of the inputs; every thread loads what it overwrites
 // before it stores.
 template <int DT, bool VEC>
-__device__ __forceinline__ Oct<DT> oct_load(const void* base, int64_t row_elems, const OctAt& at)
+__device__ __forceinline__ Oct<DT> oct_load(const char* p, const OctAt& at)
 {
     Oct<DT> o;
     if constexpr (VEC) {
-        const char* p = static_cast<const char*>(base) + (row_elems + at.ch) * elem_size(DT);
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
             : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
             : "l"(p));
@@ -77,16 +88,16 @@ __device__ __forceinline__ Oct<DT> oct_load(const void* base, int64_t row_elems,
                 : "=r"(o.w[4]), "=r"(o.w[5]), "=r"(o.w[6]), "=r"(o.w[7])
                 : "l"(p + 16));
     } else if constexpr (DT == TSX_F32) {
-        const float* p = static_cast<const float*>(base) + row_elems + at.ch;
+        const float* e = reinterpret_cast<const float*>(p);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            o.w[j] = at.ch + j * at.step < at.cols ? __float_as_uint(p[j * at.step]) : 0u;
+            o.w[j] = at.ch + j * at.step < at.cols ? __float_as_uint(e[j * at.step]) : 0u;
     } else {
-        const unsigned short* p = static_cast<const unsigned short*>(base) + row_elems + at.ch;
+        const unsigned short* e = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = at.ch + 2 * j * at.step < at.cols ? p[2 * j * at.step] : 0;
-            const uint32_t hi = at.ch + (2 * j + 1) * at.step < at.cols ? p[(2 * j + 1) * at.step] : 0;
+            const uint32_t lo = at.ch + 2 * j * at.step < at.cols ? e[2 * j * at.step] : 0;
+            const uint32_t hi = at.ch + (2 * j + 1) * at.step < at.cols ? e[(2 * j + 1) * at.step] : 0;
             o.w[j] = lo | hi << 16;
         }
     }
@@ -133,25 +144,24 @@ __device__ __forceinline__ Oct<DT> oct_round(const float2 (&f)[4])
 }
 
 template <int DT, bool VEC>
-__device__ __forceinline__ void oct_store(void* base, int64_t row_elems, const OctAt& at, const Oct<DT>& o)
+__device__ __forceinline__ void oct_store(char* p, const OctAt& at, const Oct<DT>& o)
 {
     if constexpr (VEC) {
-        char* p = static_cast<char*>(base) + (row_elems + at.ch) * elem_size(DT);
         *reinterpret_cast<uint4*>(p) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
         if constexpr (DT == TSX_F32)
             *reinterpret_cast<uint4*>(p + 16) = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
     } else if constexpr (DT == TSX_F32) {
-        uint32_t* p = static_cast<uint32_t*>(base) + row_elems + at.ch;
+        uint32_t* e = reinterpret_cast<uint32_t*>(p);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (at.ch + j * at.step < at.cols)
-                p[j * at.step] = o.w[j];
+                e[j * at.step] = o.w[j];
     } else {
-        unsigned short* p = static_cast<unsigned short*>(base) + row_elems + at.ch;
+        unsigned short* e = reinterpret_cast<unsigned short*>(p);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (at.ch + j * at.step < at.cols)
-                p[j * at.step] = static_cast<unsigned short>(o.w[j / 2] >> (j % 2 * 16));
+                e[j * at.step] = static_cast<unsigned short>(o.w[j / 2] >> (j % 2 * 16));
     }
 }
 
@@ -175,7 +185,7 @@ __device__ __forceinline__ void param_floats(const void* base, bool wide, bool p
             f[2] = make_float2(v.x, v.y);
             f[3] = make_float2(v.z, v.w);
         } else {
-            oct_floats(oct_load<DT, true>(base, ch0, at), f);
+            oct_floats(oct_load<DT, true>(oct_ptr<DT>(base, 0, 0, ch0 + at.ch), at), f);
         }
         return;
     }
@@ -310,24 +320,35 @@ __device__ __forceinline__ HeldScale held_scale(uint32_t amax_bits, int form)
     return s;
 }
 
-// The largest magnitude of an oct, as bits: unsigned integers order
-// magnitudes as floats do, with infinity above every number and NaN above
-// infinity, which a float maximum would drop.
-__device__ __forceinline__ uint32_t oct_amax_bits(const float2 (&f)[4])
+// The largest magnitude of an oct, as the element type's bits: unsigned
+// integers order magnitudes as floats do, with infinity above every number and
+// NaN above infinity, which a float maximum would drop.  16-bit elements are
+// compared two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t oct_amax_bits(const Oct<DT>& o)
 {
-    uint32_t m = 0;
+    if constexpr (DT == TSX_F32) {
+        uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        m = max(m, max(__float_as_uint(f[j].x) & 0x7fffffffu, __float_as_uint(f[j].y) & 0x7fffffffu));
-    return m;
+        for (int j = 0; j < 8; ++j)
+            m = max(m, o.w[j] & 0x7fffffffu);
+        return m;
+    } else {
+        const uint32_t m = __vmaxu2(__vmaxu2(o.w[0] & 0x7fff7fffu, o.w[1] & 0x7fff7fffu),
+                                    __vmaxu2(o.w[2] & 0x7fff7fffu, o.w[3] & 0x7fff7fffu));
+        return max(m & 0xffffu, m >> 16);
+    }
 }
-
-// The maximum over the `team` (a power of two) neighbouring lanes.
-__device__ __forceinline__ uint32_t team_max(uint32_t m, int team)
+// Those bits as an fp32 magnitude.
+template <int DT>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t m)
 {
-    for (int d = 1; d < team; d <<= 1)
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    return m;
+    if constexpr (DT == TSX_F32)
+        return m;
+    else if constexpr (DT == TSX_BF16)
+        return m << 16;
+    else
+        return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
 }
 
 // Eight 8-bit numbers as they lie in memory (channel j in byte j).
@@ -338,13 +359,13 @@ struct Held {
 // x * inv rounded to nearest even into the 8-bit form.  int8: adding 1.5 *
 // 2^23 leaves the whole number in the sum's low byte (|x inv| <= 127 plus
 // rounding, well inside); the product is rounded by itself first.
-__device__ __forceinline__ Held held_round(const float2 (&f)[4], const HeldScale& s, int form)
+__device__ __forceinline__ Held held_round(const float2 (&f)[4], float inv, int form)
 {
     Held h;
     float2 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        v[j] = __fmul2_rn(f[j], pair_of(s.inv));
+        v[j] = __fmul2_rn(f[j], pair_of(inv));
     if (form == TSX_INT8) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -363,7 +384,7 @@ __device__ __forceinline__ Held held_round(const float2 (&f)[4], const HeldScale
             h.w[k] = lo | hi << 16;
         }
     }
-    if (s.inv == 0.f)   // zeros; also where 0 * infinity or NaN stood
+    if (inv == 0.f)   // zeros; also where 0 * infinity or NaN stood
         h.w[0] = h.w[1] = 0;
     return h;
 }
@@ -397,10 +418,9 @@ __device__ __forceinline__ void held_floats(const Held& h, float scale, int form
 }
 
 template <bool VEC>
-__device__ __forceinline__ Held held_load(const void* q, int64_t row_elems, const OctAt& at)
+__device__ __forceinline__ Held held_load(const uint8_t* p, const OctAt& at)
 {
     Held h;
-    const uint8_t* p = static_cast<const uint8_t*>(q) + row_elems + at.ch;
     if constexpr (VEC) {
         asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(h.w[0]), "=r"(h.w[1]) : "l"(p));
     } else {
@@ -414,9 +434,8 @@ __device__ __forceinline__ Held held_load(const void* q, int64_t row_elems, cons
 }
 
 template <bool VEC>
-__device__ __forceinline__ void held_store(void* q, int64_t row_elems, const OctAt& at, const Held& h)
+__device__ __forceinline__ void held_store(uint8_t* p, const OctAt& at, const Held& h)
 {
-    uint8_t* p = static_cast<uint8_t*>(q) + row_elems + at.ch;
     if constexpr (VEC) {
         *reinterpret_cast<uint2*>(p) = make_uint2(h.w[0], h.w[1]);
     } else {
@@ -425,6 +444,92 @@ __device__ __forceinline__ void held_store(void* q, int64_t row_elems, const Oct
             if (at.ch + j * at.step < at.cols)
                 p[j * at.step] = static_cast<uint8_t>(h.w[j / 4] >> (j % 4 * 8));
     }
+}
+
+// Where a thread's checkpoint bytes and its team's scale go: first row, and
+// from row to row of its walk.
+struct HeldPtr {
+    uint8_t* q;
+    float* scale;
+    int64_t q_step, scale_step;
+    __device__ __forceinline__ HeldPtr() {}
+    __device__ __forceinline__ HeldPtr(const HeldOut& out, int64_t row, int64_t rows_apart, int cols, int64_t blocks,
+                                       int ch, int block)
+        : q(static_cast<uint8_t*>(out.q) + row * cols + ch),
+          scale(out.scale + row * blocks + ch / block),
+          q_step(rows_apart * cols),
+          scale_step(rows_apart * blocks)
+    {
+    }
+};
+
+// N rows of a thread's oct to 8 bits, each with its team's scale, from row
+// `first` of its walk on; the first `n` rows exist (0: the thread only lends
+// its lane).  All lanes of a team come together, with the same n; `live`
+// threads hold channels.  The maxima of two rows of 16-bit elements share a
+// shuffle, and where a team has as many lanes as there are rows, each lane
+// works out one row's scale for all.
+template <int DT, bool VEC, int N>
+__device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool live, const OctAt& at, int team,
+                                          int form, const HeldPtr& out, int first)
+{
+    static_assert(N == 2 || N == 4, "rows");
+    const int lane = static_cast<int>(threadIdx.x) & 31, base = lane & ~(team - 1);
+    const uint32_t mask = (team == 32 ? 0xffffffffu : (1u << team) - 1u) << base;
+    const bool block = at.ch - (lane - base) * (VEC ? kOct : 1) < at.cols;   // the team has a block at all
+    uint32_t m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        m[i] = live ? oct_amax_bits<DT>(o[i]) : 0u;
+    if constexpr (DT == TSX_F32) {
+        for (int d = 1; d < team; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                m[i] = max(m[i], __shfl_xor_sync(mask, m[i], d));
+    } else {
+        uint32_t two[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            two[i] = m[2 * i] | m[2 * i + 1] << 16;
+        for (int d = 1; d < team; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                two[i] = __vmaxu2(two[i], __shfl_xor_sync(mask, two[i], d));
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            m[2 * i] = two[i] & 0xffffu;
+            m[2 * i + 1] = two[i] >> 16;
+        }
+    }
+    float inv[N];
+    if (team >= N) {
+        const int mine = lane - base;   // the first N lanes of the team have a row each
+        uint32_t own = m[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i)
+            own = mine == i ? m[i] : own;
+        const HeldScale s = held_scale(magnitude_bits<DT>(own), form);
+        if (block && mine < N && mine < n)
+            out.scale[(first + mine) * out.scale_step] = s.scale;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            inv[i] = __shfl_sync(mask, s.inv, base + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const HeldScale s = held_scale(magnitude_bits<DT>(m[i]), form);
+            inv[i] = s.inv;
+            if (block && lane == base && i < n)
+                out.scale[(first + i) * out.scale_step] = s.scale;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (live && i < n) {
+            float2 f[4];
+            oct_floats(o[i], f);
+            held_store<VEC>(out.q + (first + i) * out.q_step, at, held_round(f, inv[i], form));
+        }
 }
 
 }  // namespace dev
