@@ -99,9 +99,11 @@ typedef struct tsx_norm_desc {
 
 /* Bytes of scratch that tsx_group_norm (backward 0) or
  * tsx_group_norm_backward (backward 1) needs for this shape: device memory,
- * 16-byte aligned, that the call overwrites and no later call needs.  Host
- * only. */
-int tsx_group_norm_workspace(const tsx_norm_desc *desc, int backward, size_t *bytes);
+ * 16-byte aligned, that the call overwrites and no later call needs.  aligned
+ * 0: enough whatever the alignment of the tensors; 1: enough if the base
+ * pointers of x, y (dy, dx) and the checkpoint's q are multiples of 16 bytes.
+ * 0 bytes: the workspace may be NULL.  Host only. */
+int tsx_group_norm_workspace(const tsx_norm_desc *desc, int backward, int aligned, size_t *bytes);
 
 /* y = act((x - mean) rstd weight + bias), with mean and rstd = 1 / sqrt(var +
  * eps) of every sample's groups also written to mean and rstd [n, groups]

@@ -19,7 +19,7 @@ TSX_HD constexpr int stats_rows() { return DT == TSX_F32 ? 4 : 8; }
 
 // CTAs to an SM that the registers are cut for.
 template <int DT, bool VEC>
-TSX_HD constexpr int forward_ctas() { return DT == TSX_F32 || !VEC ? 3 : 4; }
+TSX_HD constexpr int forward_ctas() { return 3; }
 
 // A CTA's range of rows: blockIdx.x counts ranges sample by sample.  The
 // `ranks` CTAs of a cluster take neighbouring ranges and join their sums.
@@ -64,7 +64,11 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>()) norm_st
     const int P = a.lay.P, width = run_width<BY_OCT>(s), stride = slot_stride(width);
     float4* spare = shared4;                                                    // [warps]
     float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);        // [run_groups]
-    float2* slots = sums + a.lay.run_groups;                                    // [P][stride]
+    float2* ranks = sums + a.lay.run_groups;                                    // clusters: [ranks][run_groups]
+    float2* slots = ranks + (a.lay.ranks > 1 ? a.lay.ranks * a.lay.run_groups : 0);   // [P][stride]
+    let_next_start();
+    if (a.lay.ranks > 1)
+        cluster_arrive();   // waited for before anything is put into another CTA
     Triples<BY_OCT> t;
     t.clear();
     constexpr int N = stats_rows<DT>();
@@ -81,21 +85,23 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>()) norm_st
     join_groups(slots, stride, 1, s.groups, P, group_cols(a, s) / (BY_OCT ? 8 : 1), r.rows, BY_OCT ? 8.f : 1.f,
                 a.lay.ranks > 1 ? sums : out, spare);
     if (a.lay.ranks > 1) {
+        __syncthreads();
+        cluster_wait();
+        for (int g = threadIdx.x; g < s.groups; g += blockDim.x)
+            cluster_put(ranks + r.rank * s.groups + g, 0, sums[g]);
         cluster_arrive();
         cluster_wait();
         if (r.rank == 0)
             for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
                 Triples<true> j;
                 j.clear();
-                for (int k = 0; k < a.lay.ranks; ++k) {
-                    const float2 u = cluster_pair(sums + g, k);
+                for (int i = 0; i < a.lay.ranks; ++i) {
+                    const float2 u = ranks[i * s.groups + g];
                     const float mu[1] = {u.x}, dev[1] = {u.y};
-                    j.join(static_cast<float>(range_rows(a, a.lay.range, r.split + k)) * group_cols(a, s), mu, dev);
+                    j.join(static_cast<float>(range_rows(a, a.lay.range, r.split + i)) * group_cols(a, s), mu, dev);
                 }
                 out[g] = make_float2(j.mean[0], j.m2[0]);
             }
-        cluster_arrive();   // the others may leave once rank 0 has read them
-        cluster_wait();
     }
 }
 
@@ -138,7 +144,7 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
             const float mu[1] = {v.y}, dev[1] = {v.z};
             t.join(v.x, mu, dev);
         }
-        stats[g] = make_float2(t.mean[0], rstd_of(t.m2[0], m, a.eps));
+        stats[g] = make_float2(t.mean[0], rstd_of(t.m2[0], 1.f / m, a.eps));
     }
     __syncthreads();
 }
@@ -156,6 +162,10 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
+    const Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
+    Oct<DT> o[kApplyRows];
+    load_rows<DT, VEC>(w, s.at, 0, s.live ? r.mine : 0, o);   // the first rows, before the sums are there
+    wait_for_last();
     join_parts(a, s, r.sample, part, stats, work);
     k.statistics(a, s, stats);
     if (r.split == 0 && s.piece == 0)
@@ -164,15 +174,14 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
             rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
         }
     k.scale_weight();
-    const Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
     const WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
     HeldPtr to;
     if constexpr (HOLD)
         to = HeldPtr(held, r.row0 + s.p, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
     // a team's threads share their rows, so they come to its shuffles together
     for (int i0 = 0; i0 < r.mine; i0 += kApplyRows) {
-        Oct<DT> o[kApplyRows];
-        load_rows<DT, VEC>(w, s.at, i0, s.live ? r.mine - i0 : 0, o);
+        if (i0 > 0)
+            load_rows<DT, VEC>(w, s.at, i0, s.live ? r.mine - i0 : 0, o);
 #pragma unroll
         for (int i = 0; i < kApplyRows; ++i)
             if (s.live && i0 + i < r.mine) {
@@ -210,9 +219,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     const Range r = range_of(a, s);
     const int P = a.lay.P, width = s.at.cols, stride = slot_stride(width);
     float2* stats = shared;                         // [run_groups]: (mean, rstd), then (S1, S2)
-    float2* work = stats + a.lay.run_groups;        // [threads]
+    float2* ranks = stats + a.lay.run_groups;       // clusters: [ranks][run_groups]
+    float2* work = ranks + (a.lay.ranks > 1 ? a.lay.ranks * a.lay.run_groups : 0);   // [threads]
     float2* columns = work + kNormThreads;          // [run_cols]
     float2* slots = columns + a.lay.run_cols;       // [P][stride]
+    let_next_start();
+    if (a.lay.ranks > 1)
+        cluster_arrive();
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     load_stats(a, s, r.sample, mean, rstd, stats);
@@ -254,27 +267,64 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* sums = part_of(a, s, r, part);
     weigh_columns<DT>(a, s, 1, width, weight, columns, a.lay.ranks > 1 ? stats : sums);
     if (a.lay.ranks > 1) {
+        __syncthreads();
+        cluster_wait();
+        for (int i = threadIdx.x; i < s.groups; i += blockDim.x)
+            cluster_put(ranks + r.rank * s.groups + i, 0, stats[i]);
         cluster_arrive();
         cluster_wait();
         if (r.rank == 0)
             for (int i = threadIdx.x; i < s.groups; i += blockDim.x) {
-                float2 t = make_float2(0.f, 0.f);
-                for (int n = 0; n < a.lay.ranks; ++n)
-                    t = __fadd2_rn(t, cluster_pair(stats + i, n));
+                float2 t = ranks[i];
+                for (int n = 1; n < a.lay.ranks; ++n)
+                    t = __fadd2_rn(t, ranks[n * s.groups + i]);
                 sums[i] = t;
             }
-        cluster_arrive();
-        cluster_wait();
     }
 }
 
-// Second kernel: dx.
+// dweight and dbias: the sums of the [slices][2][c] partial sums.  A CTA takes
+// 32 of the 2 c columns: every warp adds every warps-th slice, then the warps
+// are added in their order.
+constexpr int kParamCols = 32;
+__device__ __forceinline__ void add_params(const float* chan, int64_t slices, int c, int64_t block, float* dweight,
+                                           float* dbias, float* work)
+{
+    const int lane = static_cast<int>(threadIdx.x) % kParamCols, warp = static_cast<int>(threadIdx.x) / kParamCols;
+    const int warps = static_cast<int>(blockDim.x) / kParamCols;
+    const int64_t col = block * kParamCols + lane;   // of 2 c
+    float t = 0.f;
+    if (col < 2 * static_cast<int64_t>(c)) {
+#pragma unroll 8
+        for (int64_t i = warp; i < slices; i += warps)
+            t += chan[i * 2 * c + col];
+    }
+    work[warp * kParamCols + lane] = t;
+    __syncthreads();
+    if (warp == 0 && col < 2 * static_cast<int64_t>(c)) {
+        for (int i = 1; i < warps; ++i)
+            t += work[i * kParamCols + lane];
+        if (col < c)
+            dweight[col] = t;
+        else
+            dbias[col - c] = t;
+    }
+}
+
+// Second kernel: dx; the CTAs past the ranges' add up dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
 __global__ void __launch_bounds__(kNormThreads, 2)
     norm_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
-                     const float* rstd, void* dx, const float2* part)
+                     const float* rstd, void* dx, float* dweight, float* dbias, const float2* part, const float* chan)
 {
     extern __shared__ float2 shared[];
+    const int64_t ranges = a.n * a.lay.splits;
+    if (blockIdx.x >= ranges) {
+        wait_for_last();
+        add_params(chan, ranges, a.c, (blockIdx.x - ranges) * gridDim.y + blockIdx.y, dweight, dbias,
+                   reinterpret_cast<float*>(shared));
+        return;
+    }
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a, s);
     const int P = a.lay.P;
@@ -283,6 +333,15 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* work = sums + a.lay.run_groups;      // [threads or groups]
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
+    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    GradRow<DT, VEC, HELD> g[kGradRows];
+    if (s.live) {   // the first rows, before the sums are there
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i)
+            if (i < r.mine)
+                g[i].load(a, s, w, i);
+    }
+    wait_for_last();
     const int count = parts_of(a);
     const float2* first = part + r.sample * count * a.groups + s.group0;
     const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
@@ -307,14 +366,14 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     k.statistics(a, s, stats);
     Grouped<BY_OCT> s1, s2;
     grouped<BY_OCT>(a, s, sums, s1, s2);
-    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
     const WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
     for (int i0 = 0; s.live && i0 < r.mine; i0 += kGradRows) {
-        GradRow<DT, VEC, HELD> g[kGradRows];
+        if (i0 > 0) {
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (i0 + i < r.mine)
-                g[i].load(a, s, w, i0 + i);
+            for (int i = 0; i < kGradRows; ++i)
+                if (i0 + i < r.mine)
+                    g[i].load(a, s, w, i0 + i);
+        }
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i)
             if (i0 + i < r.mine) {
@@ -328,32 +387,12 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     }
 }
 
-// dweight and dbias: the sums of the [slices][2][c] partial sums, slice after
-// slice within each of 32 lanes, then the lanes by halves.
-constexpr int kParamCols = 32, kParamLanes = 32;
-__global__ void __launch_bounds__(kParamCols* kParamLanes)
+__global__ void __launch_bounds__(1024)
     norm_params_kernel(const float* chan, int64_t slices, int c, float* dweight, float* dbias)
 {
-    __shared__ float part[kParamLanes][kParamCols];
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * kParamCols + threadIdx.x;   // of 2 c
-    float t = 0.f;
-    if (col < 2 * static_cast<int64_t>(c)) {
-#pragma unroll 8
-        for (int64_t i = threadIdx.y; i < slices; i += kParamLanes)
-            t += chan[i * 2 * c + col];
-    }
-    part[threadIdx.y][threadIdx.x] = t;
-    for (int half = kParamLanes / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        if (static_cast<int>(threadIdx.y) < half)
-            part[threadIdx.y][threadIdx.x] += part[threadIdx.y + half][threadIdx.x];
-    }
-    if (threadIdx.y == 0 && col < 2 * static_cast<int64_t>(c)) {
-        if (col < c)
-            dweight[col] = part[0][threadIdx.x];
-        else
-            dbias[col - c] = part[0][threadIdx.x];
-    }
+    __shared__ float work[1024];
+    wait_for_last();
+    add_params(chan, slices, c, blockIdx.x, dweight, dbias, work);
 }
 
 __global__ void norm_empty_kernel(float* mean, float* rstd, int64_t count, float eps)
@@ -367,6 +406,14 @@ __global__ void norm_empty_kernel(float* mean, float* rstd, int64_t count, float
 
 }  // namespace
 
+namespace {
+
+// Pairs that the first kernels keep for their groups, and in clusters for
+// every rank's.
+size_t rank_sums(const NormLayout& lay) { return size_t(lay.run_groups) * (lay.ranks > 1 ? lay.ranks + 1 : 1); }
+
+}  // namespace
+
 cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,
                         float* mean, float* rstd, HeldOut held, NormScratch scratch, cudaStream_t st)
 {
@@ -374,20 +421,21 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
     const int width = lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
     const size_t slots = kNormThreads / 32 * sizeof(float4) +
-                         (size_t(lay.run_groups) + size_t(lay.P) * slot_stride(width)) * sizeof(float2);
+                         (rank_sums(lay) + size_t(lay.P) * slot_stride(width)) * sizeof(float2);
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
     const size_t stats = items * sizeof(float4) + lay.run_groups * sizeof(float2);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT) \
-    e = launch_grid(norm_stats_kernel<DT, VEC, BY_OCT>, grid, lay.threads, slots, lay.ranks, st, a, x, scratch.part)
+    e = launch_grid(norm_stats_kernel<DT, VEC, BY_OCT>, grid, lay.threads, slots, lay.ranks, false, st, a, x, \
+                    scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
     if (e != cudaSuccess)
         return e;
 #define CALL(DT, VEC, BY_OCT)                                                                                       \
-    e = held.q ? launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, stats, 1, st, a, x,       \
+    e = held.q ? launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, stats, 1, true, st, a, x, \
                              weight, bias, y, mean, rstd, held, scratch.part)                                       \
-               : launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, stats, 1, st, a, x,      \
+               : launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, stats, 1, true, st, a, x, \
                              weight, bias, y, mean, rstd, held, scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
@@ -400,13 +448,13 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
 {
     const NormLayout& lay = a.lay;
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
-    const size_t sums = (size_t(lay.run_groups) + kNormThreads + lay.run_cols +
+    const size_t sums = (rank_sums(lay) + kNormThreads + lay.run_cols +
                          size_t(lay.P) * slot_stride(lay.run_cols)) * sizeof(float2);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT)                                                                                       \
-    e = x.q ? launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, sums, lay.ranks, st, a, dy,   \
+    e = x.q ? launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, scratch.part, scratch.chan)                                  \
-            : launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, sums, lay.ranks, st, a, dy,  \
+            : launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, scratch.part, scratch.chan)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
@@ -414,25 +462,24 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
         return e;
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
     const size_t stats = (2 * size_t(lay.run_groups) + items) * sizeof(float2);
+    const int64_t param_ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
+    const dim3 all(unsigned(grid.x + (param_ctas + lay.runs - 1) / lay.runs), grid.y);
 #define CALL(DT, VEC, BY_OCT)                                                                                     \
-    e = x.q ? launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, stats, 1, st, a, dy, x,     \
-                          weight, bias, mean, rstd, dx, scratch.part)                                             \
-            : launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, stats, 1, st, a, dy, x,    \
-                          weight, bias, mean, rstd, dx, scratch.part)
+    e = x.q ? launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, true>, all, lay.threads, stats, 1, true, st, a, dy, x,  \
+                          weight, bias, mean, rstd, dx, dweight, dbias, scratch.part, scratch.chan)               \
+            : launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, false>, all, lay.threads, stats, 1, true, st, a, dy, x, \
+                          weight, bias, mean, rstd, dx, dweight, dbias, scratch.part, scratch.chan)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
-    if (e != cudaSuccess)
-        return e;
-    return launch_norm_params(a, a.n * lay.splits, scratch.chan, dweight, dbias, st);
+    return e;
 }
 
 cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* chan, float* dweight, float* dbias,
                                cudaStream_t st)
 {
-    const int64_t cols = 2 * int64_t(a.c);
-    norm_params_kernel<<<unsigned((cols + kParamCols - 1) / kParamCols), dim3(kParamCols, kParamLanes), 0, st>>>(
-        chan, slices, a.c, dweight, dbias);
-    return cudaGetLastError();
+    const int64_t ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
+    return launch_grid(norm_params_kernel, dim3(unsigned(ctas)), 1024, 0, 1, true, st, chan, slices, a.c, dweight,
+                       dbias);
 }
 
 cudaError_t launch_norm_empty(float* mean, float* rstd, int64_t count, float eps, cudaStream_t st)

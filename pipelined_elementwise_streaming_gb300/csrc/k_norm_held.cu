@@ -45,6 +45,18 @@ __device__ __forceinline__ HeldPlace held_place(const NormArgs& a, NormPlace& s)
     return h;
 }
 
+// all[ranks][items] = every rank's sums; then says that this CTA has read the
+// others (they may leave once all have).  After a cluster barrier.
+__device__ __forceinline__ void gather_ranks(const float2* sums, int items, int ranks, float2* all)
+{
+    for (int i = threadIdx.x; i < ranks * items; i += blockDim.x) {
+        const int r = i / items;
+        all[i] = cluster_pair(sums + i - r * items, r);
+    }
+    cluster_arrive();
+    __syncthreads();
+}
+
 template <int DT, bool BY_OCT, bool HOLD, int ROWS>
 __global__ void __launch_bounds__(kNormThreads, 2)
     norm_held_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
@@ -64,7 +76,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float4* spare = shared4;                                                // [warps]
     float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);    // [samples][groups]: (mean, M2) of the part
     float2* stats = sums + items;                                           // [samples][groups]: (mean, rstd)
-    float2* slots = stats + items;                                          // [P][stride]
+    float2* slots = stats + items;                                          // [P][stride]; then [ranks][items]
     Triples<BY_OCT> t;
     t.clear();
     if (s.live)
@@ -80,6 +92,8 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     } else {
         __syncthreads();
     }
+    if (lay.ranks > 1)
+        gather_ranks(sums, items, lay.ranks, slots);
     const float m = static_cast<float>(a.l) * static_cast<float>(a.per_group);
     for (int i = threadIdx.x; i < items; i += blockDim.x) {
         float2 v = sums[i];
@@ -87,13 +101,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             Triples<true> j;
             j.clear();
             for (int r = 0; r < lay.ranks; ++r) {
-                const float2 u = cluster_pair(&sums[i], r);
+                const float2 u = slots[r * items + i];
                 const float mu[1] = {u.x}, dev[1] = {u.y};
                 j.join(static_cast<float>(range_rows(a, lay.range, r)) * a.per_group, mu, dev);
             }
             v = make_float2(j.mean[0], j.m2[0]);
         }
-        v.y = rstd_of(v.y, m, a.eps);
+        v.y = rstd_of(v.y, 1.f / m, a.eps);
         stats[i] = v;
         const int q = lay.samples == 1 ? 0 : i / s.groups;
         const int64_t sample = h.tile * lay.samples + q;
@@ -102,8 +116,6 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             rstd[sample * a.groups + s.group0 + i - q * s.groups] = v.y;
         }
     }
-    if (lay.ranks > 1)
-        cluster_arrive();   // this CTA has read the others; they may leave once all have
     __syncthreads();
     k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
     k.scale_weight();
@@ -154,7 +166,8 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* stats = sums + items;                    // [samples][groups]: (mean, rstd), then -S1 / M, -S2 / M
     float2* work = stats + items;                    // [threads]
     float2* columns = work + kNormThreads;           // [samples][width]
-    float2* slots = columns + lay.samples * width;   // [P][stride]
+    float2* slots = columns + lay.samples * width;   // [P][stride]; then [ranks][items]
+    let_next_start();
     for (int i = threadIdx.x; i < items; i += blockDim.x) {
         const int q = lay.samples == 1 ? 0 : i / s.groups;
         const int64_t sample = h.tile * lay.samples + q;
@@ -199,18 +212,18 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     } else {
         __syncthreads();
     }
+    if (lay.ranks > 1)
+        gather_ranks(sums, items, lay.ranks, slots);
     const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
     for (int i = threadIdx.x; i < items; i += blockDim.x) {
         float2 v = sums[i];
         if (lay.ranks > 1) {
-            v = make_float2(0.f, 0.f);
-            for (int r = 0; r < lay.ranks; ++r)
-                v = __fadd2_rn(v, cluster_pair(&sums[i], r));
+            v = slots[i];
+            for (int r = 1; r < lay.ranks; ++r)
+                v = __fadd2_rn(v, slots[r * items + i]);
         }
         stats[i] = make_float2(v.x / m, v.y / m);
     }
-    if (lay.ranks > 1)
-        cluster_arrive();
     __syncthreads();
     Grouped<BY_OCT> s1, s2;
     grouped<BY_OCT>(a, s, stats + (s.live ? h.q : 0) * s.groups, s1, s2);
@@ -246,6 +259,18 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }                                                           \
     } while (0)
 
+namespace {
+
+// Pairs of shared memory for the columns, which the ranks' sums reuse.
+size_t slot_pairs(const NormLayout& lay, int width)
+{
+    const size_t slots = size_t(lay.P) * slot_stride(width);
+    const size_t all = lay.ranks > 1 ? size_t(lay.ranks) * lay.samples * lay.run_groups : 0;
+    return slots > all ? slots : all;
+}
+
+}  // namespace
+
 cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,
                              float* mean, float* rstd, HeldOut held, cudaStream_t st)
 {
@@ -253,12 +278,12 @@ cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const 
     const dim3 grid(unsigned((a.n + lay.samples - 1) / lay.samples * lay.ranks), unsigned(lay.runs));
     const int width = lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
     const size_t smem = kNormThreads / 32 * sizeof(float4) +
-                        (2 * size_t(lay.samples) * lay.run_groups + size_t(lay.P) * slot_stride(width)) * sizeof(float2);
+                        (2 * size_t(lay.samples) * lay.run_groups + slot_pairs(lay, width)) * sizeof(float2);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, BY_OCT)                                                                                            \
-    e = held.q ? launch_grid(norm_held_kernel<DT, BY_OCT, true, kHeldRows>, grid, lay.threads, smem, lay.ranks, st, \
+    e = held.q ? launch_grid(norm_held_kernel<DT, BY_OCT, true, kHeldRows>, grid, lay.threads, smem, lay.ranks, false, st, \
                              a, x, weight, bias, y, mean, rstd, held)                                               \
-               : launch_grid(norm_held_kernel<DT, BY_OCT, false, kHeldRows>, grid, lay.threads, smem, lay.ranks,    \
+               : launch_grid(norm_held_kernel<DT, BY_OCT, false, kHeldRows>, grid, lay.threads, smem, lay.ranks, false, \
                              st, a, x, weight, bias, y, mean, rstd, held)
     TSX_BY_HELD(dtype, lay.oct_in_group, CALL);
 #undef CALL
@@ -273,13 +298,13 @@ cudaError_t launch_norm_held_backward(int dtype, const NormArgs& a, const void* 
     const int64_t slices = (a.n + lay.samples - 1) / lay.samples * lay.ranks;
     const dim3 grid(unsigned(slices), unsigned(lay.runs));
     const size_t smem = (2 * size_t(lay.samples) * lay.run_groups + kNormThreads +
-                         size_t(lay.samples) * lay.run_cols + size_t(lay.P) * slot_stride(lay.run_cols)) *
+                         size_t(lay.samples) * lay.run_cols + slot_pairs(lay, lay.run_cols)) *
                         sizeof(float2);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, BY_OCT)                                                                                           \
-    e = x.q ? launch_grid(norm_held_grad_kernel<DT, BY_OCT, true>, grid, lay.threads, smem, lay.ranks, st, a, dy,  \
+    e = x.q ? launch_grid(norm_held_grad_kernel<DT, BY_OCT, true>, grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, dx, scratch.chan)                                           \
-            : launch_grid(norm_held_grad_kernel<DT, BY_OCT, false>, grid, lay.threads, smem, lay.ranks, st, a, dy, \
+            : launch_grid(norm_held_grad_kernel<DT, BY_OCT, false>, grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, dx, scratch.chan)
     TSX_BY_HELD(dtype, lay.oct_in_group, CALL);
 #undef CALL

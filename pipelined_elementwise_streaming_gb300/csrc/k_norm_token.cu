@@ -38,13 +38,14 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
 {
     const NormPlace s = norm_place<true>(a);
     const int lanes = a.per_group / 8;   // threads to a group
-    const float m = static_cast<float>(a.per_group), inv_m = 1.f / m;   // a power of two
+    const float inv_m = 1.f / static_cast<float>(a.per_group);   // a power of two
     Chan<true> k;
     k.params<DT, true>(a, s, weight, bias);
     const int group = s.group0 + local_group(a, s.at.ch);
     const bool first = s.at.ch % a.per_group == 0;
     const int P = a.lay.P;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (P * kTokenRows);
+    const int step_s = P * a.groups;
     // rows of the thread: first + i * P for i < 4, then a stride further on
     const Walk w = walk<DT>(x, 0, P, a.x_pitch, s);
     const WalkOut to = walk_out<DT>(y, 0, P, a.y_pitch, s);
@@ -75,9 +76,11 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
         }
         team_sums(dev, lanes);
         char* out = to.p + row0 * a.y_pitch * elem_size(DT);
+        float* pm = mean + row0 * a.groups + group;
+        float* pr = rstd + row0 * a.groups + group;
 #pragma unroll
         for (int i = 0; i < kTokenRows; ++i) {
-            const float rs = rstd_of(dev[i], m, a.eps);
+            const float rs = rstd_of(dev[i], inv_m, a.eps);
             if (s.live && i < n) {
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
@@ -85,8 +88,8 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
                 k.apply_scaled(a.act, f, v);
                 oct_store<DT, true>(out + i * to.step, s.at, oct_round<DT>(v));
                 if (first) {
-                    mean[(row0 + i * P) * a.groups + group] = mu[i];
-                    rstd[(row0 + i * P) * a.groups + group] = rs;
+                    pm[i * step_s] = mu[i];
+                    pr[i * step_s] = rs;
                 }
             }
         }
@@ -110,6 +113,8 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
     const int group = s.group0 + local_group(a, s.at.ch);
     const int P = a.lay.P;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (P * kTokenGradRows);
+    let_next_start();
+    const int step_s = P * a.groups;
     float2 sz[4], szx[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -119,13 +124,15 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
         const int n = s.live && row0 < a.n ? static_cast<int>(min((a.n - row0 + P - 1) / P, int64_t(kTokenGradRows))) : 0;
         const GradWalk<DT, true, HELD> w(a, s, dy, x, row0, P);
         GradRow<DT, true, HELD> g[kTokenGradRows];
+        const float* pm = mean + row0 * a.groups + group;
+        const float* pr = rstd + row0 * a.groups + group;
         float mu[kTokenGradRows], rs[kTokenGradRows];
 #pragma unroll
         for (int i = 0; i < kTokenGradRows; ++i)
             if (i < n) {
                 g[i].load(a, s, w, i);
-                mu[i] = __ldg(mean + (row0 + i * P) * a.groups + group);
-                rs[i] = __ldg(rstd + (row0 + i * P) * a.groups + group);
+                mu[i] = __ldg(pm + i * step_s);
+                rs[i] = __ldg(pr + i * step_s);
             }
         float2 hat[kTokenGradRows][4], dz[kTokenGradRows][4];
         float s1[kTokenGradRows], s2[kTokenGradRows];

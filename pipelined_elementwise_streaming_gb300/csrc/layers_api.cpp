@@ -261,19 +261,20 @@ namespace {
 constexpr int kNormRun = 2048;
 constexpr int kTokenRun = 2048;
 constexpr int64_t kTokenCtas = 8 * 152, kTokenGradCtas = 2 * 152;
-constexpr int64_t kNormRanks = 16;     // CTAs of a cluster at most
+constexpr int64_t kNormRanks = 8;      // CTAs of a cluster at most
 constexpr int64_t kNormSamples = 64;   // samples side by side at most
 constexpr int64_t kNormHeldCtas = 2 * 152;
-// Ranges are cut until about this many CTAs share the work: three to each of
-// the 152 SMs.  A constant of the chip, not read from it, so that results
-// depend on the shape alone.
-constexpr int64_t kNormCtas = 3 * 152;
+// Ranges are cut so that at most this many CTAs share the work: as many as the
+// 152 SMs hold at once, three each forward and two backward.  A constant of the
+// chip, not read from it, so that results depend on the shape alone.
+constexpr int64_t kNormCtas = 3 * 152, kNormGradCtas = 2 * 152;
+constexpr int64_t kNormParts = 128;   // parts of a sample that the second kernel's CTAs join by themselves
 constexpr int kNormRowsAtOnce = 4;
 
 // The streaming layout for rows of c channels; block: channels to a scale
 // where the call writes checkpoints, else 0.  False if this alignment (vec,
 // block) cannot be had with these groups.
-bool stream_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
+bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
 {
     const int64_t per = d.c / d.groups;
     NormLayout lay{};
@@ -310,15 +311,14 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, NormLayout* out)
     p = p < 1 ? 1 : p > d.l ? d.l : p;
     lay.P = int(p);
     lay.threads = round_up(lay.P * lay.V, 32);
-    const int64_t want = (kNormCtas + d.n * lay.runs - 1) / (d.n * lay.runs);
+    const int64_t ctas = (backward ? kNormGradCtas : kNormCtas) / (d.n * lay.runs);
     const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
-    int64_t splits = want < most ? want : most;
-    lay.range = ((d.l + splits - 1) / splits + p - 1) / p * p;
-    splits = (d.l + lay.range - 1) / lay.range;
-    // many ranges: clusters join eight each, so that few parts are left (the
-    // last ranges may be empty)
-    lay.ranks = splits >= 16 ? 8 : 1;
-    lay.splits = (splits + lay.ranks - 1) / lay.ranks * lay.ranks;
+    int64_t splits = ctas < 1 ? 1 : ctas < most ? ctas : most;
+    // many ranges: clusters join eight each, so that few parts are left
+    lay.ranks = splits > kNormParts ? 8 : 1;
+    splits = splits / lay.ranks * lay.ranks;
+    lay.range = (d.l + splits - 1) / splits;   // the last ranges may be short, or empty
+    lay.splits = splits;
     lay.samples = 1;
     lay.lanes = lay.P;
     *out = lay;
@@ -430,7 +430,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, Nor
 bool norm_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
 {
     return token_layout(d, vec, block, backward, out) || held_layout(d, vec, block, backward, out) ||
-           stream_layout(d, vec, block, out);
+           stream_layout(d, vec, block, backward, out);
 }
 
 size_t part_bytes(const tsx_norm_desc& d, const NormLayout& lay)
@@ -472,12 +472,15 @@ int check_norm(const char* call, const tsx_norm_desc* d)
 
 // Scratch that covers every layout the call may take, whatever its pointers'
 // alignment.
-size_t norm_workspace(const tsx_norm_desc& d, bool backward)
+size_t norm_workspace(const tsx_norm_desc& d, bool backward, bool aligned)
 {
     size_t most = 0;
     if (d.n == 0 || d.l == 0 || d.c == 0)
         return 0;
-    for (int vec = 0; vec < 2; ++vec)
+    // rows of whole vectors: then an aligned call takes no other layout
+    const int64_t es = elem_size(d.dtype);
+    const bool whole = d.c % kOct == 0 && d.x_pitch * es % 16 == 0 && d.y_pitch * es % 16 == 0;
+    for (int vec = aligned && whole ? 1 : 0; vec < (whole ? 2 : 1); ++vec)
         for (int block : {0, d.block}) {
             NormLayout lay;
             if ((backward && block) || !norm_layout(d, vec != 0, block, backward, &lay))
@@ -485,7 +488,7 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward)
             const size_t b = part_bytes(d, lay) + (backward ? chan_bytes(d, lay) : 0);
             most = b > most ? b : most;
         }
-    return most > 16 ? most : 16;
+    return most;
 }
 
 int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, const void* weight,
@@ -512,9 +515,11 @@ int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, boo
     return TSX_OK;
 }
 
-int check_scratch(const char* call, const tsx_norm_desc& d, bool backward, const void* workspace, size_t bytes)
+int check_scratch(const char* call, size_t need, const void* workspace, size_t bytes)
 {
-    if (bytes < norm_workspace(d, backward) || !workspace)
+    if (need == 0)
+        return TSX_OK;
+    if (bytes < need || !workspace)
         return fail(TSX_ERR_INVALID, call, "the workspace is smaller than tsx_group_norm_workspace says");
     if (!aligned(workspace, 16))
         return fail(TSX_ERR_ALIGN, call, "the workspace must be 16-byte aligned");
@@ -523,7 +528,7 @@ int check_scratch(const char* call, const tsx_norm_desc& d, bool backward, const
 
 }  // namespace
 
-extern "C" int tsx_group_norm_workspace(const tsx_norm_desc* desc, int backward, size_t* bytes)
+extern "C" int tsx_group_norm_workspace(const tsx_norm_desc* desc, int backward, int aligned, size_t* bytes)
 {
     const char* call = "tsx_group_norm_workspace";
     const int rc = check_norm(call, desc);
@@ -531,7 +536,7 @@ extern "C" int tsx_group_norm_workspace(const tsx_norm_desc* desc, int backward,
         return rc;
     if (!bytes)
         return fail(TSX_ERR_INVALID, call, "bytes is required");
-    *bytes = norm_workspace(*desc, backward != 0);
+    *bytes = norm_workspace(*desc, backward != 0, aligned != 0);
     set_last_error("");
     return TSX_OK;
 }
@@ -561,15 +566,14 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
     const int es = elem_size(d.dtype), ps = elem_size(d.param_dtype);
     if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, ps) || !aligned(bias, ps) || !aligned(scale, 4))
         return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
-    rc = check_scratch(call, d, false, workspace, workspace_bytes);
-    if (rc != TSX_OK)
-        return rc;
     const bool vec = vectors(x, d.c, d.x_pitch, es) && vectors(y, d.c, d.y_pitch, es) && held_vectors(q, d.c);
     // the checkpoint rides along where runs can start on its blocks
     NormLayout lay;
     const bool ride = q && (norm_layout(d, vec, d.block, false, &lay) || norm_layout(d, false, d.block, false, &lay));
     NormArgs a{};
     rc = norm_args(call, d, vec, ride ? d.block : 0, false, weight, bias, &a);
+    if (rc == TSX_OK)
+        rc = check_scratch(call, part_bytes(d, a.lay), workspace, workspace_bytes);
     if (rc != TSX_OK)
         return rc;
     if (q && !ride) {
@@ -625,13 +629,12 @@ extern "C" int tsx_group_norm_backward(const tsx_norm_desc* desc, const void* dy
     if (!aligned(dy, es) || !aligned(x, es) || !aligned(dx, es) || !aligned(weight, ps) || !aligned(bias, ps) ||
         !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(scale, 4))
         return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
-    rc = check_scratch(call, d, true, workspace, workspace_bytes);
-    if (rc != TSX_OK)
-        return rc;
     const bool vec = vectors(dy, d.c, d.y_pitch, es) && vectors(x, d.c, d.x_pitch, es) &&
                      vectors(dx, d.c, d.x_pitch, es) && held_vectors(q, d.c);
     NormArgs a{};
     rc = norm_args(call, d, vec, 0, true, weight, bias, &a);
+    if (rc == TSX_OK)
+        rc = check_scratch(call, part_bytes(d, a.lay) + chan_bytes(d, a.lay), workspace, workspace_bytes);
     if (rc != TSX_OK)
         return rc;
     NormScratch scratch;

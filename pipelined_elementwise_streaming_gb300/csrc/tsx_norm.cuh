@@ -101,6 +101,21 @@ __device__ __forceinline__ float2 cluster_pair(const float2* p, int rank)
     return v;
 }
 
+// The place that `p` has in this CTA, in the cluster's CTA `rank`.
+__device__ __forceinline__ void cluster_put(const float2* p, int rank, float2 v)
+{
+    const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(there), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// Programmatic launches: a kernel lets the next one of the stream start once
+// all its CTAs have said so (or ended), and that one waits for it to end, its
+// memory visible, before it uses what it wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Rows of the k-th range of `range` rows of a sample (0 past its end).
 __device__ __forceinline__ int range_rows(const NormArgs& a, int64_t range, int64_t k)
 {
@@ -246,59 +261,57 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
         v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-
 // (mean, M2) of each of `samples` x `groups` items from the columns that the
 // row lanes left: slots[samples * lanes][slot_stride], `per` neighbouring
 // columns to a group, `scale` elements to a column and row, `rows` rows dealt
-// to the lanes in turn.  A warp takes an item, or (few items) one of `parts`
-// shares of its row lanes; the shares are joined in their order.  Called by
-// all threads between two barriers; ends without one.  spare: [warps].
+// to the lanes in turn.  Every item has a team of neighbouring threads, up to
+// a warp; where there are fewer items than warps, each warp takes one of an
+// item's `parts` shares of the row lanes, and the shares are joined in their
+// order.  Called by all threads after a barrier; ends without one.
+// spare: [warps].
 __device__ __forceinline__ void join_groups(const float2* slots, int stride, int samples, int groups, int lanes,
                                             int per, int rows, float scale, float2* out, float4* spare)
 {
-    const int warps = static_cast<int>(blockDim.x) / 32, warp = static_cast<int>(threadIdx.x) / 32;
-    const int t = static_cast<int>(threadIdx.x) % 32;
-    const int items = samples * groups;
+    const int warps = static_cast<int>(blockDim.x) / 32, items = samples * groups;
     const int parts = items >= warps ? 1 : warps / items;
-    int kw = 1, shift = 0;   // threads side by side along a row
-    while (kw < 32 && kw < per) {
-        kw *= 2;
-        ++shift;
-    }
-    const int k0 = t & (kw - 1), p0 = t >> shift, step = 32 >> shift;
+    int shift = 5;   // log2 of the team
+    while (shift > 0 && (warps << (5 - shift)) < items)
+        --shift;
+    const int team = 1 << shift, teams = static_cast<int>(blockDim.x) >> shift;
+    const int me = static_cast<int>(threadIdx.x) >> shift, t = static_cast<int>(threadIdx.x) & (team - 1);
+    int wide = 0;   // log2 of the team's threads side by side along a row
+    while (wide < shift && (1 << wide) < per)
+        ++wide;
+    const int k0 = t & ((1 << wide) - 1), p0 = t >> wide, step = team >> wide;
     const int base = rows / lanes, more = rows - base * lanes;   // lane p has base + (p < more) rows
-    for (int u = warp; u < items * parts; u += warps) {
+    for (int u0 = 0; u0 < items * parts; u0 += teams) {
+        const int u = min(u0 + me, items * parts - 1);   // spare teams repeat the last
         const int part = parts == 1 ? 0 : u / items, item = u - part * items;
         const int q = samples == 1 ? 0 : item / groups, g = item - q * groups;
         const float2* first = slots + q * lanes * stride + g * per;
         float n = 0.f, sum = 0.f, dev = 0.f;
         for (int p = part * step + p0; p < lanes; p += parts * step) {
             const float c = (base + (p < more ? 1 : 0)) * scale;
-            for (int k = k0; k < per; k += kw) {
+            for (int k = k0; k < per; k += 1 << wide) {
                 n += c;
                 sum += c * first[p * stride + k].x;
             }
         }
-        n = warp_sum(n);
-        sum = warp_sum(sum);
-        const float mean = n > 0.f ? sum / n : 0.f;
+        for (int d = 1; d < team; d <<= 1) {
+            n += __shfl_xor_sync(0xffffffffu, n, d);
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
+        const float mean = n > 0.f ? __fdividef(sum, n) : 0.f;
         for (int p = part * step + p0; p < lanes; p += parts * step) {
             const float c = (base + (p < more ? 1 : 0)) * scale;
-            for (int k = k0; k < per; k += kw) {
+            for (int k = k0; k < per; k += 1 << wide) {
                 const float2 v = first[p * stride + k];
                 const float d = v.x - mean;
                 dev += v.y + c * d * d;
             }
         }
-        dev = warp_sum(dev);
-        if (t == 0) {
+        dev = lanes_sum(dev, team);
+        if (t == 0 && u0 + me < items * parts) {
             if (parts == 1)
                 out[item] = make_float2(mean, dev);
             else
@@ -384,7 +397,9 @@ __device__ __forceinline__ void each_item(int items, int entries, F f)
     }
 }
 
-__device__ __forceinline__ float rstd_of(float m2, float m, float eps) { return 1.f / sqrtf(m2 / m + eps); }
+// rsqrtf is within two ulps and one instruction where 1 / sqrtf takes dozens;
+// every thread of a token's group forms it.
+__device__ __forceinline__ float rstd_of(float m2, float inv_m, float eps) { return rsqrtf(m2 * inv_m + eps); }
 
 // One weight, as fp32.
 template <int DT>
@@ -655,30 +670,37 @@ struct GradRow {
 
 }  // namespace dev
 
-// Launch `kernel` with clusters of `ranks` CTAs along x (1: none).
+// Launch `kernel` with clusters of `ranks` CTAs along x (1: none); `early`: it
+// may start while the stream's last kernel still runs (it waits by itself).
 template <class K, class... Args>
-cudaError_t launch_grid(K kernel, dim3 grid, int threads, size_t smem, int ranks, cudaStream_t st, Args... args)
+cudaError_t launch_grid(K kernel, dim3 grid, int threads, size_t smem, int ranks, bool early, cudaStream_t st,
+                        Args... args)
 {
-    const void* fn = reinterpret_cast<const void*>(kernel);
-    cudaError_t e = cudaSuccess;
-    if (ranks > 8)
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && smem > 48 * 1024)
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess)
-        return e;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = unsigned(ranks);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    cudaLaunchAttribute attr[2]{};
+    if (ranks > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = unsigned(ranks);
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (early) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = attr;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -586,7 +586,7 @@ def test_refusals(tsx):
     ref_d = ctypes.byref(d)
     stats = torch.zeros(32, device="cuda")
     m = stats.data_ptr()
-    small = tsx.tsx_group_norm(ref_d, p, w.data_ptr(), w.data_ptr(), p, m, m, None, None, m, 8, s)
+    small = tsx.tsx_group_norm_backward(ref_d, p, p, None, None, w.data_ptr(), w.data_ptr(), m, m, p, m, m, m, 8, s)
     assert small == tsx.TSX_ERR_INVALID and "workspace" in tsx.tsx_last_error()
     both = tsx.tsx_group_norm_backward(ref_d, p, p, p, m, w.data_ptr(), w.data_ptr(), m, m, p, m, m, m, 1 << 20, s)
     assert both == tsx.TSX_ERR_INVALID

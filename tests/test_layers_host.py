@@ -28,7 +28,11 @@ def desc(tsx, **kw):
 
 def workspace(tsx, backward=0, **kw):
     size = ctypes.c_size_t(99)
-    rc = tsx.tsx_group_norm_workspace(ctypes.byref(desc(tsx, **kw)), backward, ctypes.byref(size))
+    rc = tsx.tsx_group_norm_workspace(ctypes.byref(desc(tsx, **kw)), backward, 0, ctypes.byref(size))
+    if rc == tsx.TSX_OK:   # never more for aligned tensors
+        least = ctypes.c_size_t(99)
+        assert tsx.tsx_group_norm_workspace(ctypes.byref(desc(tsx, **kw)), backward, 1, ctypes.byref(least)) == rc
+        assert least.value <= size.value
     return rc, size.value
 
 
@@ -39,7 +43,7 @@ def test_shapes_that_are_refused(tsx):
         rc, _ = workspace(tsx, **bad)
         assert rc == tsx.TSX_ERR_INVALID, bad
         assert tsx.tsx_last_error()
-    assert tsx.tsx_group_norm_workspace(None, 0, None) == tsx.TSX_ERR_INVALID
+    assert tsx.tsx_group_norm_workspace(None, 0, 0, None) == tsx.TSX_ERR_INVALID
     head = (1, 4, 64, 64, 0, 128)
     for k, v in ((0, 9), (1, -1), (2, 1 << 31), (3, 63), (4, 5), (5, 100)):
         args = list(head)
