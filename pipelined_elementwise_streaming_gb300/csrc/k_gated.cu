@@ -30,8 +30,8 @@ struct Place {
     bool live;      // the thread has channels
 };
 
-template <bool VEC>
-__device__ __forceinline__ Place place(const RowLayout& lay, int rows_at_once)
+template <bool VEC, int ROWS>
+__device__ __forceinline__ Place place(const RowLayout& lay)
 {
     Place s;
     const int p = static_cast<int>(threadIdx.x) / lay.V, v = static_cast<int>(threadIdx.x) - p * lay.V;
@@ -40,9 +40,12 @@ __device__ __forceinline__ Place place(const RowLayout& lay, int rows_at_once)
     s.at = oct_at<VEC>(v, lay.team, cols);
     s.ch = chunk0 + s.at.ch;
     s.live = p < lay.P && s.at.ch < cols;
-    s.row0 = static_cast<int64_t>(blockIdx.x) * (lay.P * rows_at_once) + p;
+    s.row0 = static_cast<int64_t>(blockIdx.x) * (lay.P * ROWS) + p;
     const int64_t left = lay.rows - s.row0;
-    s.rows = p >= lay.P || left <= 0 ? 0 : static_cast<int>(min((left + lay.P - 1) / lay.P, int64_t(rows_at_once)));
+    s.rows = 0;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        s.rows += p < lay.P && left > i * lay.P ? 1 : 0;
     return s;
 }
 
@@ -79,17 +82,17 @@ __device__ __forceinline__ void load_held(const Place& s, const void* q, const f
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kLayerThreads) pack_kernel(PackArgs a, const void* x, HeldOut held)
 {
-    const Place s = place<VEC>(a.lay, kRowsAtOnce);
+    const Place s = place<VEC, kRowsAtOnce>(a.lay);
     Oct<DT> o[kRowsAtOnce];
     load_rows<DT, VEC>(s, x, a.pitch, a.lay.P, o);
     hold_rows<DT, VEC>(o, s.rows, s.live, s.at, a.lay.team, a.form,
-                       HeldPtr(held, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), 0);
+                       HeldPtr(held, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block));
 }
 
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kLayerThreads) unpack_kernel(PackArgs a, const void* q, const float* scale, void* x)
 {
-    const Place s = place<VEC>(a.lay, kRowsAtOnce);
+    const Place s = place<VEC, kRowsAtOnce>(a.lay);
     Held h[kRowsAtOnce];
     float sc[kRowsAtOnce];
     load_held<VEC>(s, q, scale, a.lay, a.blocks, a.block, h, sc);
@@ -108,7 +111,7 @@ template <int DT, bool VEC, bool HOLD>
 __global__ void __launch_bounds__(kLayerThreads)
     gated_kernel(GatedArgs a, const void* gate, const void* up, void* h, HeldOut held_gate, HeldOut held_up)
 {
-    const Place s = place<VEC>(a.lay, kGatedRows);
+    const Place s = place<VEC, kGatedRows>(a.lay);
     Oct<DT> g[kGatedRows], u[kGatedRows];
     load_rows<DT, VEC>(s, gate, a.in_pitch, a.lay.P, g);
     load_rows<DT, VEC>(s, up, a.in_pitch, a.lay.P, u);
@@ -129,9 +132,9 @@ __global__ void __launch_bounds__(kLayerThreads)
     }
     if constexpr (HOLD) {
         hold_rows<DT, VEC>(g, s.rows, s.live, s.at, a.lay.team, a.form,
-                           HeldPtr(held_gate, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), 0);
+                           HeldPtr(held_gate, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block));
         hold_rows<DT, VEC>(u, s.rows, s.live, s.at, a.lay.team, a.form,
-                           HeldPtr(held_up, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), 0);
+                           HeldPtr(held_up, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block));
     }
 }
 
@@ -139,7 +142,7 @@ template <int DT, bool VEC, bool HELD>
 __global__ void __launch_bounds__(kLayerThreads)
     gated_backward_kernel(GatedArgs a, const void* dh, Saved gate, Saved up, void* dgate, void* dup, void* h)
 {
-    const Place s = place<VEC>(a.lay, kGatedRows);
+    const Place s = place<VEC, kGatedRows>(a.lay);
     Oct<DT> d[kGatedRows], g[kGatedRows], u[kGatedRows];
     Held qg[kGatedRows], qu[kGatedRows];
     float sg[kGatedRows], su[kGatedRows];

@@ -72,11 +72,12 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>()) norm_st
     Triples<BY_OCT> t;
     t.clear();
     constexpr int N = stats_rows<DT>();
-    const Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
-    for (int i0 = 0; s.live && i0 < r.mine; i0 += N) {
+    Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
+    for (int left = s.live ? r.mine : 0; left > 0; left -= N) {
         Oct<DT> o[N];
-        load_rows<DT, VEC>(w, s.at, i0, r.mine - i0, o);
-        t.add_octs(o, r.mine - i0);
+        load_rows<DT, VEC>(w, s.at, left, o);
+        t.add_octs(o, left);
+        w.p += N * w.step;
     }
     if (s.live)
         t.leave(s.at, slots + s.p * stride);
@@ -117,6 +118,9 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
     const int threads = static_cast<int>(blockDim.x);
     // `lanes` threads to a group, each joins every lanes-th part
     const int lanes = s.groups < threads ? threads / s.groups : 1;
+    const int64_t range = a.lay.range * a.lay.ranks;
+    const int full = static_cast<int>(a.l / range);   // ranges before the one that may be short
+    const float rows = static_cast<float>(range), rest = static_cast<float>(a.l - full * range);
     for (int i = threadIdx.x; i < lanes * s.groups; i += threads) {
         const int lane = i / s.groups, g = i - lane * s.groups;
         Triples<true> t;
@@ -124,14 +128,13 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
 #pragma unroll 4
         for (int k = lane; k < count; k += lanes) {
             const float2 v = first[static_cast<int64_t>(k) * a.groups + g];
-            int range = k, cols = a.per_group;
+            int split = k, cols = a.per_group;
             if (a.lay.pieces > 1) {
-                range = k / a.lay.pieces;
-                cols = min(a.lay.run_cols, a.per_group - (k - range * a.lay.pieces) * a.lay.run_cols);
+                split = k / a.lay.pieces;
+                cols = min(a.lay.run_cols, a.per_group - (k - split * a.lay.pieces) * a.lay.run_cols);
             }
-            const float rows = static_cast<float>(range_rows(a, a.lay.range * a.lay.ranks, range));
             const float mu[1] = {v.x}, dev[1] = {v.y};
-            t.join(rows * static_cast<float>(cols), mu, dev);
+            t.join((split < full ? rows : split == full ? rest : 0.f) * static_cast<float>(cols), mu, dev);
         }
         work[i] = make_float4(t.count, t.mean[0], t.m2[0], 0.f);
     }
@@ -162,9 +165,9 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
-    const Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
+    Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
     Oct<DT> o[kApplyRows];
-    load_rows<DT, VEC>(w, s.at, 0, s.live ? r.mine : 0, o);   // the first rows, before the sums are there
+    load_rows<DT, VEC>(w, s.at, s.live ? r.mine : 0, o);   // the first rows, before the sums are there
     wait_for_last();
     join_parts(a, s, r.sample, part, stats, work);
     k.statistics(a, s, stats);
@@ -174,24 +177,27 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
             rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
         }
     k.scale_weight();
-    const WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
+    WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
     HeldPtr to;
     if constexpr (HOLD)
         to = HeldPtr(held, r.row0 + s.p, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
     // a team's threads share their rows, so they come to its shuffles together
-    for (int i0 = 0; i0 < r.mine; i0 += kApplyRows) {
-        if (i0 > 0)
-            load_rows<DT, VEC>(w, s.at, i0, s.live ? r.mine - i0 : 0, o);
+    for (int left = r.mine; left > 0; left -= kApplyRows) {
 #pragma unroll
         for (int i = 0; i < kApplyRows; ++i)
-            if (s.live && i0 + i < r.mine) {
+            if (s.live && i < left) {
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
                 k.apply(a.act, f, v);
-                oct_store<DT, VEC>(out.p + (i0 + i) * out.step, s.at, oct_round<DT>(v));
+                oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
             }
-        if constexpr (HOLD)
-            hold_rows<DT, VEC>(o, r.mine - i0, s.live, s.at, a.lay.team, a.form, to, i0);
+        out.p += kApplyRows * out.step;
+        if constexpr (HOLD) {
+            hold_rows<DT, VEC>(o, left, s.live, s.at, a.lay.team, a.form, to);
+            to.advance(kApplyRows);
+        }
+        w.p += kApplyRows * w.step;
+        load_rows<DT, VEC>(w, s.at, s.live ? left - kApplyRows : 0, o);
     }
 }
 
@@ -234,16 +240,17 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    for (int i0 = 0; s.live && i0 < r.mine; i0 += kGradRows) {
+    GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    for (int left = s.live ? r.mine : 0; left > 0; left -= kGradRows) {
         GradRow<DT, VEC, HELD> g[kGradRows];
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i)
-            if (i0 + i < r.mine)
-                g[i].load(a, s, w, i0 + i);
+            if (i < left)
+                g[i].load(a, s, w, i);
+        w.advance(kGradRows);
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i)
-            if (i0 + i < r.mine) {
+            if (i < left) {
                 float2 fd[4], fx[4], hat[4], dz[4];
                 oct_floats(g[i].dy, fd);
                 g[i].saved_floats(a, fx);
@@ -333,14 +340,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* work = sums + a.lay.run_groups;      // [threads or groups]
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
-    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
     GradRow<DT, VEC, HELD> g[kGradRows];
-    if (s.live) {   // the first rows, before the sums are there
+    int left = s.live ? r.mine : 0;
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (i < r.mine)
-                g[i].load(a, s, w, i);
-    }
+    for (int i = 0; i < kGradRows; ++i)   // the first rows, before the sums are there
+        if (i < left)
+            g[i].load(a, s, w, i);
     wait_for_last();
     const int count = parts_of(a);
     const float2* first = part + r.sample * count * a.groups + s.group0;
@@ -366,24 +372,24 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     k.statistics(a, s, stats);
     Grouped<BY_OCT> s1, s2;
     grouped<BY_OCT>(a, s, sums, s1, s2);
-    const WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
-    for (int i0 = 0; s.live && i0 < r.mine; i0 += kGradRows) {
-        if (i0 > 0) {
-#pragma unroll
-            for (int i = 0; i < kGradRows; ++i)
-                if (i0 + i < r.mine)
-                    g[i].load(a, s, w, i0 + i);
-        }
+    WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
+    for (; left > 0; left -= kGradRows) {
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i)
-            if (i0 + i < r.mine) {
+            if (i < left) {
                 float2 fd[4], fx[4], hat[4], dz[4], v[4];
                 oct_floats(g[i].dy, fd);
                 g[i].saved_floats(a, fx);
                 k.slopes(a, fd, fx, hat, dz);
                 k.gradient(dz, hat, s1, s2, v);
-                oct_store<DT, VEC>(out.p + (i0 + i) * out.step, s.at, oct_round<DT>(v));
+                oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
             }
+        out.p += kGradRows * out.step;
+        w.advance(kGradRows);
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i)
+            if (i < left - kGradRows)
+                g[i].load(a, s, w, i);
     }
 }
 

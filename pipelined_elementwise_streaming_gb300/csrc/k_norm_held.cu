@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     const HeldPlace h = held_place(a, s);
     Oct<DT> o[ROWS];
     const int have = h.mine;
-    load_rows<DT, true>(walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s), s.at, 0, s.live ? have : 0, o);
+    load_rows<DT, true>(walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s), s.at, s.live ? have : 0, o);
     Chan<BY_OCT> k;
     k.template params<DT, true>(a, s, weight, bias);
 
@@ -129,12 +129,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             oct_store<DT, true>(out.p + i * out.step, s.at, oct_round<DT>(v));
         }
     if constexpr (HOLD) {
-        const HeldPtr to(held, h.row0 + h.lane, lay.lanes, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
+        HeldPtr to(held, h.row0 + h.lane, lay.lanes, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
 #pragma unroll
         for (int i0 = 0; i0 < ROWS; i0 += 4) {
             const Oct<DT> four[4] = {o[i0], o[i0 + 1], o[i0 + 2], o[i0 + 3]};
             if (i0 < have)
-                hold_rows<DT, true>(four, have - i0, s.live, s.at, lay.team, a.form, to, i0);
+                hold_rows<DT, true>(four, have - i0, s.live, s.at, lay.team, a.form, to);
+            to.advance(4);
         }
     }
     if (lay.ranks > 1)

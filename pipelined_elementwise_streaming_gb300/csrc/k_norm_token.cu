@@ -14,6 +14,17 @@ using namespace dev;
 constexpr int kTokenRows = 4;       // rows whose loads a thread issues before it uses the first
 constexpr int kTokenGradRows = 2;   // two operands a row
 
+// How many of a thread's next N rows, P apart, exist with `left` rows to go.
+template <int N>
+__device__ __forceinline__ int rows_at(int64_t left, int P)
+{
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        n += left > i * P ? 1 : 0;
+    return n;
+}
+
 // Sums over each group's lanes, all rows at once: the shuffles of one row hide
 // the latency of another's.
 template <int N>
@@ -51,9 +62,9 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
     const WalkOut to = walk_out<DT>(y, 0, P, a.y_pitch, s);
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenRows); base < a.n; base += stride) {
         const int64_t row0 = base + s.p;
-        const int n = s.p < P && row0 < a.n ? static_cast<int>(min((a.n - row0 + P - 1) / P, int64_t(kTokenRows))) : 0;
+        const int n = s.p < P ? rows_at<kTokenRows>(a.n - row0, P) : 0;
         Oct<DT> o[kTokenRows];
-        load_rows<DT, true>(Walk{w.p + row0 * a.x_pitch * elem_size(DT), w.step}, s.at, 0, s.live ? n : 0, o);
+        load_rows<DT, true>(Walk{w.p + row0 * a.x_pitch * elem_size(DT), w.step}, s.at, s.live ? n : 0, o);
         float mu[kTokenRows], dev[kTokenRows];
 #pragma unroll
         for (int i = 0; i < kTokenRows; ++i) {
@@ -95,7 +106,7 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
         }
         if constexpr (HOLD)
             hold_rows<DT, true>(o, n, s.live, s.at, a.lay.team, a.form,
-                                HeldPtr(held, row0, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block), 0);
+                                HeldPtr(held, row0, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block));
     }
 }
 
@@ -121,7 +132,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenGradRows); base < a.n; base += stride) {
         const int64_t row0 = base + s.p;
-        const int n = s.live && row0 < a.n ? static_cast<int>(min((a.n - row0 + P - 1) / P, int64_t(kTokenGradRows))) : 0;
+        const int n = s.live ? rows_at<kTokenGradRows>(a.n - row0, P) : 0;
         const GradWalk<DT, true, HELD> w(a, s, dy, x, row0, P);
         GradRow<DT, true, HELD> g[kTokenGradRows];
         const float* pm = mean + row0 * a.groups + group;

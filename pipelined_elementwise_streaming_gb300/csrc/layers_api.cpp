@@ -260,7 +260,7 @@ namespace {
 // for each channel and row lane, and for each group), and its threads.
 constexpr int kNormRun = 2048;
 constexpr int kTokenRun = 2048;
-constexpr int64_t kTokenCtas = 8 * 152, kTokenGradCtas = 2 * 152;
+constexpr int64_t kTokenCtas = 3 * 152, kTokenGradCtas = 2 * 152;
 constexpr int64_t kNormRanks = 8;      // CTAs of a cluster at most
 constexpr int64_t kNormSamples = 64;   // samples side by side at most
 constexpr int64_t kNormHeldCtas = 2 * 152;
@@ -268,7 +268,7 @@ constexpr int64_t kNormHeldCtas = 2 * 152;
 // 152 SMs hold at once, three each forward and two backward.  A constant of the
 // chip, not read from it, so that results depend on the shape alone.
 constexpr int64_t kNormCtas = 3 * 152, kNormGradCtas = 2 * 152;
-constexpr int64_t kNormParts = 128;   // parts of a sample that the second kernel's CTAs join by themselves
+constexpr int64_t kNormParts = 32;   // parts of a sample that the second kernel's CTAs join by themselves
 constexpr int kNormRowsAtOnce = 4;
 
 // The streaming layout for rows of c channels; block: channels to a scale
@@ -314,8 +314,14 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
     const int64_t ctas = (backward ? kNormGradCtas : kNormCtas) / (d.n * lay.runs);
     const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
     int64_t splits = ctas < 1 ? 1 : ctas < most ? ctas : most;
-    // many ranges: clusters join eight each, so that few parts are left
-    lay.ranks = splits > kNormParts ? 8 : 1;
+    // many ranges: clusters join four or eight each, so that few parts are
+    // left.  The SMs hold fewer CTAs in clusters of eight (408 of 456, 288 of
+    // 304), and a second wave for the last costs more than the room
+    lay.ranks = splits > 4 * kNormParts ? 8 : splits > kNormParts ? 4 : 1;
+    if (lay.ranks == 8 && splits > ctas * 5 / 6)
+        splits = ctas * 5 / 6;
+    if (lay.ranks == 4 && splits > ctas * 15 / 16)
+        splits = ctas * 15 / 16;
     splits = splits / lay.ranks * lay.ranks;
     lay.range = (d.l + splits - 1) / splits;   // the last ranges may be short, or empty
     lay.splits = splits;
@@ -351,8 +357,8 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     lay.ranks = lay.samples = lay.lanes = 1;
     const int64_t at_once = p * (backward ? 2 : 4);
     const int64_t most = (d.n + at_once - 1) / at_once;
-    const int64_t want = ((backward ? kTokenGradCtas : kTokenCtas) + lay.runs - 1) / lay.runs;
-    lay.splits = most < want ? most : want;
+    const int64_t want = (backward ? kTokenGradCtas : kTokenCtas) / lay.runs;
+    lay.splits = most < want ? most : want < 1 ? 1 : want;
     *out = lay;
     return true;
 }

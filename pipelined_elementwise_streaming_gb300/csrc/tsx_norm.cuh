@@ -585,21 +585,20 @@ __device__ __forceinline__ WalkOut walk_out(void* base, int64_t row, int rows_ap
     return WalkOut{oct_ptr<DT>(base, row, pitch, s.ch0 + s.at.ch), rows_apart * pitch * elem_size(DT)};
 }
 
-// N rows from row `first` of a walk on, of which the thread has `n` (>= N: no
-// row is looked at twice).
+// The next N rows of a walk, of which the thread has `n` (>= N: no row is
+// looked at twice).
 template <int DT, bool VEC, int N>
-__device__ __forceinline__ void load_rows(const Walk& w, const OctAt& at, int first, int n, Oct<DT> (&o)[N])
+__device__ __forceinline__ void load_rows(const Walk& w, const OctAt& at, int n, Oct<DT> (&o)[N])
 {
-    const char* p = w.p + first * w.step;
     if (n >= N) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            o[i] = oct_load<DT, VEC>(p + i * w.step, at);
+            o[i] = oct_load<DT, VEC>(w.p + i * w.step, at);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (i < n)
-                o[i] = oct_load<DT, VEC>(p + i * w.step, at);
+                o[i] = oct_load<DT, VEC>(w.p + i * w.step, at);
             else
                 oct_zero(o[i]);
     }
@@ -625,9 +624,19 @@ struct GradWalk {
             x = walk<DT>(src.x, row, rows_apart, a.x_pitch, s);
         }
     }
+    __device__ __forceinline__ void advance(int rows)
+    {
+        dy.p += rows * dy.step;
+        if constexpr (HELD) {
+            q += rows * q_step;
+            scale += rows * scale_step;
+        } else {
+            x.p += rows * x.step;
+        }
+    }
 };
 
-// One row of them.
+// One row of them: the i-th of the walk's next ones.
 template <int DT, bool VEC, bool HELD>
 struct GradRow {
     Oct<DT> dy;

@@ -461,17 +461,22 @@ struct HeldPtr {
           scale_step(rows_apart * blocks)
     {
     }
+    __device__ __forceinline__ void advance(int rows)
+    {
+        q += rows * q_step;
+        scale += rows * scale_step;
+    }
 };
 
-// N rows of a thread's oct to 8 bits, each with its team's scale, from row
-// `first` of its walk on; the first `n` rows exist (0: the thread only lends
+// N rows of a thread's oct to 8 bits, each with its team's scale, to where
+// `out` points; the first `n` rows exist (0: the thread only lends
 // its lane).  All lanes of a team come together, with the same n; `live`
 // threads hold channels.  The maxima of two rows of 16-bit elements share a
 // shuffle, and where a team has as many lanes as there are rows, each lane
 // works out one row's scale for all.
 template <int DT, bool VEC, int N>
 __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool live, const OctAt& at, int team,
-                                          int form, const HeldPtr& out, int first)
+                                          int form, const HeldPtr& out)
 {
     static_assert(N == 2 || N == 4, "rows");
     const int lane = static_cast<int>(threadIdx.x) & 31, base = lane & ~(team - 1);
@@ -510,7 +515,7 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
             own = mine == i ? m[i] : own;
         const HeldScale s = held_scale(magnitude_bits<DT>(own), form);
         if (block && mine < N && mine < n)
-            out.scale[(first + mine) * out.scale_step] = s.scale;
+            out.scale[mine * out.scale_step] = s.scale;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             inv[i] = __shfl_sync(mask, s.inv, base + i);
@@ -520,7 +525,7 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
             const HeldScale s = held_scale(magnitude_bits<DT>(m[i]), form);
             inv[i] = s.inv;
             if (block && lane == base && i < n)
-                out.scale[(first + i) * out.scale_step] = s.scale;
+                out.scale[i * out.scale_step] = s.scale;
         }
     }
 #pragma unroll
@@ -528,7 +533,7 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
         if (live && i < n) {
             float2 f[4];
             oct_floats(o[i], f);
-            held_store<VEC>(out.q + (first + i) * out.q_step, at, held_round(f, inv[i], form));
+            held_store<VEC>(out.q + i * out.q_step, at, held_round(f, inv[i], form));
         }
 }
 
