@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a, s);
     const int P = a.lay.P;
-    Chan<BY_OCT> k;
+    Affine k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
     Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
@@ -170,13 +170,12 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
     load_rows<DT, VEC>(w, s.at, s.live ? r.mine : 0, o);   // the first rows, before the sums are there
     wait_for_last();
     join_parts(a, s, r.sample, part, stats, work);
-    k.statistics(a, s, stats);
+    k.template statistics<BY_OCT>(a, s, stats);
     if (r.split == 0 && s.piece == 0)
         for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
             mean[r.sample * a.groups + s.group0 + g] = stats[g].x;
             rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
         }
-    k.scale_weight();
     WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
     HeldPtr to;
     if constexpr (HOLD)
@@ -251,10 +250,10 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i)
             if (i < left) {
-                float2 fd[4], fx[4], hat[4], dz[4];
+                float2 fd[4], hat[4], dz[4];
                 oct_floats(g[i].dy, fd);
-                g[i].saved_floats(a, fx);
-                k.slopes(a, fd, fx, hat, dz);
+                g[i].hats(a, k, hat);
+                k.slopes(a, fd, hat, dz);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     sz[j] = __fadd2_rn(sz[j], dz[j]);
@@ -370,18 +369,18 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     }
     load_stats(a, s, r.sample, mean, rstd, stats);   // synchronises
     k.statistics(a, s, stats);
-    Grouped<BY_OCT> s1, s2;
-    grouped<BY_OCT>(a, s, sums, s1, s2);
+    Gradient<BY_OCT> to;
+    to.set(a, s, k, sums);
     WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
     for (; left > 0; left -= kGradRows) {
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i)
             if (i < left) {
-                float2 fd[4], fx[4], hat[4], dz[4], v[4];
+                float2 fd[4], hat[4], dz[4], v[4];
                 oct_floats(g[i].dy, fd);
-                g[i].saved_floats(a, fx);
-                k.slopes(a, fd, fx, hat, dz);
-                k.gradient(dz, hat, s1, s2, v);
+                g[i].hats(a, k, hat);
+                k.slopes(a, fd, hat, dz);
+                to.of(dz, hat, v);
                 oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
             }
         out.p += kGradRows * out.step;

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     Oct<DT> o[ROWS];
     const int have = h.mine;
     load_rows<DT, true>(walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s), s.at, s.live ? have : 0, o);
-    Chan<BY_OCT> k;
+    Affine k;
     k.template params<DT, true>(a, s, weight, bias);
 
     const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
@@ -117,8 +117,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }
     }
     __syncthreads();
-    k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
-    k.scale_weight();
+    k.template statistics<BY_OCT>(a, s, stats + (s.live ? h.q : 0) * s.groups);
     const WalkOut out = walk_out<DT>(y, h.row0 + h.lane, lay.lanes, a.y_pitch, s);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
@@ -184,10 +183,10 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll
     for (int i = 0; i < kHeldGradRows; ++i)
         if (i < have) {
-            float2 fd[4], fx[4], hat[4];
+            float2 fd[4], hat[4];
             oct_floats(g[i].dy, fd);
-            g[i].saved_floats(a, fx);
-            k.slopes(a, fd, fx, hat, dz[i]);
+            g[i].hats(a, k, hat);
+            k.slopes(a, fd, hat, dz[i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sz[j] = __fadd2_rn(sz[j], dz[i][j]);
@@ -226,18 +225,15 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         stats[i] = make_float2(v.x / m, v.y / m);
     }
     __syncthreads();
-    Grouped<BY_OCT> s1, s2;
-    grouped<BY_OCT>(a, s, stats + (s.live ? h.q : 0) * s.groups, s1, s2);
+    Gradient<BY_OCT> grad;
+    grad.set(a, s, k, stats + (s.live ? h.q : 0) * s.groups);
     const WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
 #pragma unroll
     for (int i = 0; i < kHeldGradRows; ++i)
         if (i < have) {
-            float2 fx[4], hat[4], res[4];
-            g[i].saved_floats(a, fx);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                hat[j] = k.hat(fx, j);
-            k.gradient(dz[i], hat, s1, s2, res);
+            float2 hat[4], res[4];
+            g[i].hats(a, k, hat);
+            grad.of(dz[i], hat, res);
             oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(res));
         }
     if (lay.ranks > 1)

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
     const NormPlace s = norm_place<true>(a);
     const int lanes = a.per_group / 8;   // threads to a group
     const float inv_m = 1.f / static_cast<float>(a.per_group);   // a power of two
-    Chan<true> k;
+    Affine k;
     k.params<DT, true>(a, s, weight, bias);
     const int group = s.group0 + local_group(a, s.at.ch);
     const bool first = s.at.ch % a.per_group == 0;
@@ -95,8 +95,10 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
             if (s.live && i < n) {
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
-                k.statistics(mu[i], rs);
-                k.apply_scaled(a.act, f, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    f[j] = __ffma2_rn(f[j], pair_of(rs), pair_of(-mu[i] * rs));
+                k.apply(a.act, f, v);   // scale and shift are weight and bias as they came
                 oct_store<DT, true>(out + i * to.step, s.at, oct_round<DT>(v));
                 if (first) {
                     pm[i * step_s] = mu[i];
@@ -118,7 +120,8 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
     extern __shared__ float2 shared[];
     const NormPlace s = norm_place<true>(a);
     const int lanes = a.per_group / 8;
-    const float minus_m = -1.f / static_cast<float>(a.per_group);
+    // w carries act_scale
+    const float minus_m = -1.f / (static_cast<float>(a.per_group) * act_scale(a.act));
     Chan<true> k;
     k.params<DT, true>(a, s, weight, bias);
     const int group = s.group0 + local_group(a, s.at.ch);
@@ -151,11 +154,11 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
         for (int i = 0; i < kTokenGradRows; ++i) {
             s1[i] = s2[i] = 0.f;
             if (i < n) {
-                float2 fd[4], fx[4], t1 = make_float2(0.f, 0.f), t2 = t1;
+                float2 fd[4], t1 = make_float2(0.f, 0.f), t2 = t1;
                 oct_floats(g[i].dy, fd);
-                g[i].saved_floats(a, fx);
                 k.statistics(mu[i], rs[i]);
-                k.slopes(a, fd, fx, hat[i], dz[i]);
+                g[i].hats(a, k, hat[i]);
+                k.slopes(a, fd, hat[i], dz[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 dzx = __fmul2_rn(dz[i][j], hat[i][j]);
@@ -174,12 +177,11 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
 #pragma unroll
         for (int i = 0; i < kTokenGradRows; ++i)
             if (i < n) {
-                Grouped<true> g1, g2;
-                g1.v[0] = pair_of(s1[i] * minus_m);
-                g2.v[0] = pair_of(s2[i] * minus_m);
+                Gradient<true> grad;
                 float2 out[4];
                 k.statistics(mu[i], rs[i]);
-                k.gradient(dz[i], hat[i], g1, g2, out);
+                grad.set(a, k, s1[i] * minus_m, s2[i] * minus_m);
+                grad.of(dz[i], hat[i], out);
                 oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(out));
             }
     }

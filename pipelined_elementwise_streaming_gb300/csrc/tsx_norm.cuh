@@ -483,11 +483,47 @@ __device__ __forceinline__ void grouped(const NormArgs& a, const NormPlace& s, c
     }
 }
 
-// What a thread keeps for its channels: minus the mean and rstd of their
-// groups, weight and bias.
+// What a thread keeps for its channels forward: y = act(x scale + shift), scale
+// = rstd weight, shift = bias - mean scale.  Against (x - mean) scale + bias
+// this rounds mean scale once more, an error of the size that the rounded mean
+// has already, and takes one operation less.
+struct Affine {
+    float2 scale[4], shift[4];
+    // before the statistics are there: weight and bias
+    template <int DT, bool VEC>
+    __device__ __forceinline__ void params(const NormArgs& a, const NormPlace& s, const void* weight,
+                                           const void* bias)
+    {
+        param_floats<DT, VEC>(weight, a.wide_params, a.packed_params, s.ch0, s.at, scale);
+        param_floats<DT, VEC>(bias, a.wide_params, a.packed_params, s.ch0, s.at, shift);
+    }
+    // stats: (mean, rstd) by group of the run
+    template <bool BY_OCT>
+    __device__ __forceinline__ void statistics(const NormArgs& a, const NormPlace& s, const float2* stats)
+    {
+        Grouped<BY_OCT> mean, rstd;
+        grouped<BY_OCT>(a, s, stats, mean, rstd);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            scale[j] = __fmul2_rn(scale[j], rstd.at(j));
+            shift[j] = __ffma2_rn(__fmul2_rn(mean.at(j), pair_of(-1.f)), scale[j], shift[j]);
+        }
+    }
+    __device__ __forceinline__ void apply(int act, const float2 (&x)[4], float2 (&y)[4]) const
+    {
+        float2 z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            z[j] = __ffma2_rn(x[j], scale[j], shift[j]);
+        act_value(act, z, y);
+    }
+};
+
+// And backward: xhat = x rstd + off, off = -mean rstd (see above); weight and
+// bias times act_scale, so that act' comes from t = xhat w + b.
 template <bool BY_OCT>
 struct Chan {
-    Grouped<BY_OCT> minus, rstd;
+    Grouped<BY_OCT> off, rstd;
     float2 w[4], b[4];
     template <int DT, bool VEC>
     __device__ __forceinline__ void params(const NormArgs& a, const NormPlace& s, const void* weight,
@@ -495,71 +531,75 @@ struct Chan {
     {
         param_floats<DT, VEC>(weight, a.wide_params, a.packed_params, s.ch0, s.at, w);
         param_floats<DT, VEC>(bias, a.wide_params, a.packed_params, s.ch0, s.at, b);
+        const float2 f = pair_of(act_scale(a.act));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = __fmul2_rn(w[j], f);
+            b[j] = __fmul2_rn(b[j], f);
+        }
     }
-    // stats: (mean, rstd) by group of the run
     __device__ __forceinline__ void statistics(const NormArgs& a, const NormPlace& s, const float2* stats)
     {
-        grouped<BY_OCT>(a, s, stats, minus, rstd);
+        grouped<BY_OCT>(a, s, stats, off, rstd);
 #pragma unroll
         for (int j = 0; j < (BY_OCT ? 1 : 4); ++j)
-            minus.v[j] = __fmul2_rn(minus.v[j], pair_of(-1.f));
+            off.v[j] = __fmul2_rn(__fmul2_rn(off.v[j], pair_of(-1.f)), rstd.v[j]);
     }
     __device__ __forceinline__ void statistics(float mean, float rs)   // BY_OCT
     {
-        minus.v[0] = pair_of(-mean);
+        off.v[0] = pair_of(-mean * rs);
         rstd.v[0] = pair_of(rs);
     }
-    __device__ __forceinline__ float2 hat(const float2 (&x)[4], int j) const
+    // dz
+    __device__ __forceinline__ void slopes(const NormArgs& a, const float2 (&dy)[4], const float2 (&xhat)[4],
+                                           float2 (&dz)[4]) const
     {
-        return __fmul2_rn(__fadd2_rn(x[j], minus.at(j)), rstd.at(j));
-    }
-    // y of the forward pass, for which w has become rstd weight
-    __device__ __forceinline__ void scale_weight()
-    {
+        float2 t[4], slope[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            w[j] = __fmul2_rn(rstd.at(j), w[j]);
-    }
-    __device__ __forceinline__ void apply(int act, const float2 (&x)[4], float2 (&y)[4]) const
-    {
-        float2 z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            z[j] = __ffma2_rn(__fadd2_rn(x[j], minus.at(j)), w[j], b[j]);
-        act_value(act, z, y);
-    }
-    // the same with the weight as it is
-    __device__ __forceinline__ void apply_scaled(int act, const float2 (&x)[4], float2 (&y)[4]) const
-    {
-        float2 z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            z[j] = __ffma2_rn(hat(x, j), w[j], b[j]);
-        act_value(act, z, y);
-    }
-    // xhat and dz
-    __device__ __forceinline__ void slopes(const NormArgs& a, const float2 (&dy)[4], const float2 (&x)[4],
-                                           float2 (&xhat)[4], float2 (&dz)[4]) const
-    {
-        float2 z[4], value[4], slope[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            xhat[j] = hat(x, j);
-            z[j] = __ffma2_rn(xhat[j], w[j], b[j]);
-        }
-        act_both(a.act, z, value, slope);
+            t[j] = __ffma2_rn(xhat[j], w[j], b[j]);
+        act_slope(a.act, t, slope);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             dz[j] = __fmul2_rn(dy[j], slope[j]);
     }
-    // dx from dz and xhat, s1 and s2 minus the groups' S1 / M and S2 / M
-    __device__ __forceinline__ void gradient(const float2 (&dz)[4], const float2 (&xhat)[4],
-                                             const Grouped<BY_OCT>& s1, const Grouped<BY_OCT>& s2,
-                                             float2 (&dx)[4]) const
+};
+
+// dx = dz (rstd weight) - rstd S1 / M - xhat rstd S2 / M.
+template <bool BY_OCT>
+struct Gradient {
+    Grouped<BY_OCT> s1, s2;   // minus rstd S1 / M and rstd S2 / M
+    float2 w[4];              // rstd weight
+    // sums: (-S1 / M, -S2 / M) by group of the run
+    __device__ __forceinline__ void set(const NormArgs& a, const NormPlace& s, const Chan<BY_OCT>& k,
+                                        const float2* sums)
+    {
+        grouped<BY_OCT>(a, s, sums, s1, s2);
+        scale(a, k);
+    }
+    __device__ __forceinline__ void set(const NormArgs& a, const Chan<BY_OCT>& k, float sum1, float sum2)   // BY_OCT
+    {
+        s1.v[0] = pair_of(sum1);
+        s2.v[0] = pair_of(sum2);
+        scale(a, k);
+    }
+    __device__ __forceinline__ void scale(const NormArgs& a, const Chan<BY_OCT>& k)
+    {
+        const float2 f = pair_of(1.f / act_scale(a.act));
+#pragma unroll
+        for (int j = 0; j < (BY_OCT ? 1 : 4); ++j) {
+            s1.v[j] = __fmul2_rn(s1.v[j], k.rstd.v[j]);
+            s2.v[j] = __fmul2_rn(s2.v[j], k.rstd.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = __fmul2_rn(k.w[j], __fmul2_rn(f, k.rstd.at(j)));
+    }
+    __device__ __forceinline__ void of(const float2 (&dz)[4], const float2 (&xhat)[4], float2 (&dx)[4]) const
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            dx[j] = __fmul2_rn(rstd.at(j), __ffma2_rn(xhat[j], s2.at(j), __ffma2_rn(dz[j], w[j], s1.at(j))));
+            dx[j] = __ffma2_rn(xhat[j], s2.at(j), __ffma2_rn(dz[j], w[j], s1.at(j)));
     }
 };
 
@@ -662,17 +702,24 @@ struct GradRow {
             x = oct_load<DT, VEC>(w.x.p + i * w.x.step, s.at);
         }
     }
-    __device__ __forceinline__ void saved_floats(const NormArgs& a, float2 (&fx)[4]) const
+    // xhat = x rstd + off; of a checkpoint q (scale rstd) + off
+    template <bool BY_OCT>
+    __device__ __forceinline__ void hats(const NormArgs& a, const Chan<BY_OCT>& k, float2 (&hat)[4]) const
     {
-        if constexpr (!HELD) {
-            oct_floats(x, fx);
-        } else if constexpr (VEC) {
-            held_floats(q, scale[0], a.form, fx);
-        } else {
-            held_floats(q, 1.f, a.form, fx);
+        float2 f[4];
+        if constexpr (!HELD)
+            oct_floats(x, f);
+        else
+            held_numbers(q, a.form, f);
+        const float2 one = HELD && VEC && BY_OCT ? __fmul2_rn(k.rstd.at(0), pair_of(scale[0])) : k.rstd.at(0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                fx[j] = __fmul2_rn(fx[j], make_float2(scale[2 * j], scale[2 * j + 1]));
+        for (int j = 0; j < 4; ++j) {
+            float2 r = BY_OCT ? one : k.rstd.at(j);
+            if constexpr (HELD && VEC && !BY_OCT)
+                r = __fmul2_rn(r, pair_of(scale[0]));
+            else if constexpr (HELD && !VEC)
+                r = __fmul2_rn(r, make_float2(scale[2 * j], scale[2 * j + 1]));
+            hat[j] = __ffma2_rn(f[j], r, k.off.at(j));
         }
     }
 };

@@ -264,7 +264,38 @@ __device__ __forceinline__ void act_value(int act, const float2 (&z)[4], float2 
     }
 }
 
-// act(z) and its derivative.
+// act(z) and its derivative, from t = act_scale(act) * z.  For silu the factor
+// is the exponential's -log2(e), which a caller with a product to spare folds
+// into it: with p the sigmoid, act = -ln(2) t p and act' = p + act (1 - p).
+__device__ __forceinline__ float act_scale(int act) { return act == TSX_ACT_SILU ? -kLog2E : 1.f; }
+constexpr float kLn2 = 0.693147180559945309f;
+
+__device__ __forceinline__ void act_slope(int act, const float2 (&t)[4], float2 (&slope)[4])
+{
+    const float2 one = pair_of(1.f), minus = pair_of(-1.f);
+    if (act == TSX_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 p = sigmoid_of(t[j]);
+            slope[j] = __ffma2_rn(__fmul2_rn(t[j], p), __ffma2_rn(p, pair_of(kLn2), pair_of(-kLn2)), p);
+        }
+    } else if (act == TSX_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 c = gelu_clamped(t[j]), c2 = __fmul2_rn(c, c);
+            const float2 u = __ffma2_rn(c2, pair_of(-kLog2E * kGelu2K * kGeluCube), pair_of(-kLog2E * kGelu2K));
+            const float2 p = sigmoid_of(__fmul2_rn(c, u));
+            const float2 inner = __ffma2_rn(c2, pair_of(3.f * kGelu2K * kGeluCube), pair_of(kGelu2K));
+            const float2 rest = __fmul2_rn(__fmul2_rn(t[j], p), __ffma2_rn(p, minus, one));
+            slope[j] = __ffma2_rn(rest, inner, p);   // 0, not 0 * infinity
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            slope[j] = one;
+    }
+}
+
 __device__ __forceinline__ void act_both(int act, const float2 (&z)[4], float2 (&v)[4], float2 (&slope)[4])
 {
     const float2 one = pair_of(1.f), minus = pair_of(-1.f);
@@ -389,10 +420,10 @@ __device__ __forceinline__ Held held_round(const float2 (&f)[4], float inv, int 
     return h;
 }
 
-// The fp32 values q * scale.  int8: the byte, offset by 128, becomes the low
-// byte of 2^23 + b; subtracting 2^23 + 128 leaves the number exactly, without
-// an integer conversion.
-__device__ __forceinline__ void held_floats(const Held& h, float scale, int form, float2 (&f)[4])
+// The numbers q.  int8: the byte, offset by 128, becomes the low byte of 2^23 +
+// b; subtracting 2^23 + 128 leaves the number exactly, without an integer
+// conversion.
+__device__ __forceinline__ void held_numbers(const Held& h, int form, float2 (&f)[4])
 {
     if (form == TSX_INT8) {
 #pragma unroll
@@ -402,7 +433,7 @@ __device__ __forceinline__ void held_floats(const Held& h, float scale, int form
             for (int j = 0; j < 2; ++j) {
                 const float2 b = make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 | 2 * j)),
                                              __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541 | 2 * j)));
-                f[2 * k + j] = __fmul2_rn(__fadd2_rn(b, pair_of(-8388736.f)), pair_of(scale));
+                f[2 * k + j] = __fadd2_rn(b, pair_of(-8388736.f));
             }
         }
     } else {
@@ -412,9 +443,18 @@ __device__ __forceinline__ void held_floats(const Held& h, float scale, int form
             for (int j = 0; j < 2; ++j) {
                 const __half2_raw r =
                     __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h.w[k] >> (16 * j)), __NV_E4M3);
-                f[2 * k + j] = __fmul2_rn(__half22float2(__half2(r)), pair_of(scale));
+                f[2 * k + j] = __half22float2(__half2(r));
             }
     }
+}
+
+// The fp32 values q * scale.
+__device__ __forceinline__ void held_floats(const Held& h, float scale, int form, float2 (&f)[4])
+{
+    held_numbers(h, form, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f[j] = __fmul2_rn(f[j], pair_of(scale));
 }
 
 template <bool VEC>
