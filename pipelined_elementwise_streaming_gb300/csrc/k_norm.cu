@@ -13,7 +13,7 @@ using namespace dev;
 
 // Rows whose loads a thread issues before it uses the first.
 constexpr int kApplyRows = 4;
-constexpr int kGradRows = 4;
+constexpr int kGradRows = 2;   // element by element
 template <int DT>
 TSX_HD constexpr int stats_rows() { return DT == TSX_F32 ? 4 : 8; }
 
@@ -212,6 +212,49 @@ __device__ __forceinline__ void load_stats(const NormArgs& a, const NormPlace& s
     __syncthreads();
 }
 
+__device__ __forceinline__ char* next_16(float2* p)
+{
+    return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15));
+}
+
+// use(row, i) for a thread's `rows` rows, through the queue where they are
+// vectors; begin() runs once the first are on their way.
+template <int DT, bool VEC, bool HELD, class Begin, class Use>
+__device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, GradWalk<DT, VEC, HELD> w,
+                                         char* queue, int rows, Begin begin, Use use)
+{
+    if constexpr (VEC) {
+        GradQueue<DT, HELD> q(w, queue, rows);
+        begin();
+        for (int i0 = 0; i0 < rows; i0 += kQueueBatch) {
+            cp_async_wait(GradQueue<DT, HELD>::kBatches - 1);
+            GradRow<DT, true, HELD> g[kQueueBatch];
+#pragma unroll
+            for (int i = 0; i < kQueueBatch; ++i)
+                if (i0 + i < rows) {
+                    q.take(i, g[i]);
+                    use(g[i], i0 + i);
+                }
+            q.ask();
+        }
+        cp_async_wait(0);
+    } else {
+        begin();
+        for (int i0 = 0; i0 < rows; i0 += kGradRows) {
+            GradRow<DT, VEC, HELD> g[kGradRows];
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i)
+                if (i0 + i < rows)
+                    g[i].load(a, s, w, i);
+            w.advance(kGradRows);
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i)
+                if (i0 + i < rows)
+                    use(g[i], i0 + i);
+        }
+    }
+}
+
 // First kernel: S1 and S2 of every cluster's range, run and group, and the
 // range's sums for dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
@@ -219,7 +262,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     norm_sums_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, float2* part, float* chan)
 {
-    extern __shared__ float2 shared[];
+    extern __shared__ __align__(16) float2 shared[];
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a, s);
     const int P = a.lay.P, width = s.at.cols, stride = slot_stride(width);
@@ -228,6 +271,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* work = ranks + (a.lay.ranks > 1 ? a.lay.ranks * a.lay.run_groups : 0);   // [threads]
     float2* columns = work + kNormThreads;          // [run_cols]
     float2* slots = columns + a.lay.run_cols;       // [P][stride]
+    char* queue = next_16(slots + P * stride);
     let_next_start();
     if (a.lay.ranks > 1)
         cluster_arrive();
@@ -239,28 +283,18 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-    GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    for (int left = s.live ? r.mine : 0; left > 0; left -= kGradRows) {
-        GradRow<DT, VEC, HELD> g[kGradRows];
+    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, [] {}, [&](const GradRow<DT, VEC, HELD>& g, int) {
+        float2 fd[4], hat[4], dz[4];
+        oct_floats(g.dy, fd);
+        g.hats(a, k, hat);
+        k.slopes(a, fd, hat, dz);
 #pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (i < left)
-                g[i].load(a, s, w, i);
-        w.advance(kGradRows);
-#pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (i < left) {
-                float2 fd[4], hat[4], dz[4];
-                oct_floats(g[i].dy, fd);
-                g[i].hats(a, k, hat);
-                k.slopes(a, fd, hat, dz);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sz[j] = __fadd2_rn(sz[j], dz[j]);
-                    szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
-                }
-            }
-    }
+        for (int j = 0; j < 4; ++j) {
+            sz[j] = __fadd2_rn(sz[j], dz[j]);
+            szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+        }
+    });
     if (s.live)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
     __syncthreads();
@@ -323,7 +357,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     norm_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, void* dx, float* dweight, float* dbias, const float2* part, const float* chan)
 {
-    extern __shared__ float2 shared[];
+    extern __shared__ __align__(16) float2 shared[];
     const int64_t ranges = a.n * a.lay.splits;
     if (blockIdx.x >= ranges) {
         wait_for_last();
@@ -337,20 +371,18 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* stats = shared;                      // [run_groups]
     float2* sums = stats + a.lay.run_groups;     // [run_groups]: -S1 / M, -S2 / M
     float2* work = sums + a.lay.run_groups;      // [threads or groups]
+    const int threads = static_cast<int>(blockDim.x);
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
-    GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    GradRow<DT, VEC, HELD> g[kGradRows];
-    int left = s.live ? r.mine : 0;
-#pragma unroll
-    for (int i = 0; i < kGradRows; ++i)   // the first rows, before the sums are there
-        if (i < left)
-            g[i].load(a, s, w, i);
+    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+    char* queue = next_16(work + max(threads, a.lay.run_groups));
+    Gradient<BY_OCT> to;
+    WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
+    auto begin = [&] {
     wait_for_last();
     const int count = parts_of(a);
     const float2* first = part + r.sample * count * a.groups + s.group0;
     const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
-    const int threads = static_cast<int>(blockDim.x);
     const int lanes = s.groups < threads ? threads / s.groups : 1;
     for (int i = threadIdx.x; i < lanes * s.groups; i += threads) {
         const int lane = i / s.groups, group = i - lane * s.groups;
@@ -369,27 +401,17 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     }
     load_stats(a, s, r.sample, mean, rstd, stats);   // synchronises
     k.statistics(a, s, stats);
-    Gradient<BY_OCT> to;
     to.set(a, s, k, sums);
-    WalkOut out = walk_out<DT>(dx, r.row0 + s.p, P, a.x_pitch, s);
-    for (; left > 0; left -= kGradRows) {
-#pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (i < left) {
-                float2 fd[4], hat[4], dz[4], v[4];
-                oct_floats(g[i].dy, fd);
-                g[i].hats(a, k, hat);
-                k.slopes(a, fd, hat, dz);
-                to.of(dz, hat, v);
-                oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
-            }
-        out.p += kGradRows * out.step;
-        w.advance(kGradRows);
-#pragma unroll
-        for (int i = 0; i < kGradRows; ++i)
-            if (i < left - kGradRows)
-                g[i].load(a, s, w, i);
-    }
+    };
+    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin, [&](const GradRow<DT, VEC, HELD>& g, int) {
+        float2 fd[4], hat[4], dz[4], v[4];
+        oct_floats(g.dy, fd);
+        g.hats(a, k, hat);
+        k.slopes(a, fd, hat, dz);
+        to.of(dz, hat, v);
+        oct_store<DT, VEC>(out.p, s.at, oct_round<DT>(v));
+        out.p += out.step;
+    });
 }
 
 __global__ void __launch_bounds__(1024)
@@ -415,6 +437,16 @@ namespace {
 
 // Pairs that the first kernels keep for their groups, and in clusters for
 // every rank's.
+size_t queue_bytes(int dtype, const NormLayout& lay, bool held)
+{
+    if (!lay.vec)
+        return 0;
+    const int row = dtype == TSX_F32 ? (held ? queue_row_bytes<TSX_F32, true>() : queue_row_bytes<TSX_F32, false>())
+                                     : (held ? queue_row_bytes<TSX_BF16, true>() : queue_row_bytes<TSX_BF16, false>());
+    const int rows = dtype == TSX_F32 ? queue_rows<TSX_F32>() : queue_rows<TSX_BF16>();
+    return 16 + size_t(lay.threads) * rows * row;   // after the next multiple of 16
+}
+
 size_t rank_sums(const NormLayout& lay) { return size_t(lay.run_groups) * (lay.ranks > 1 ? lay.ranks + 1 : 1); }
 
 }  // namespace
@@ -454,7 +486,7 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
     const NormLayout& lay = a.lay;
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
     const size_t sums = (rank_sums(lay) + kNormThreads + lay.run_cols +
-                         size_t(lay.P) * slot_stride(lay.run_cols)) * sizeof(float2);
+                         size_t(lay.P) * slot_stride(lay.run_cols)) * sizeof(float2) + queue_bytes(dtype, lay, x.q);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT)                                                                                       \
     e = x.q ? launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
@@ -466,7 +498,7 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
     if (e != cudaSuccess)
         return e;
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
-    const size_t stats = (2 * size_t(lay.run_groups) + items) * sizeof(float2);
+    const size_t stats = (2 * size_t(lay.run_groups) + items) * sizeof(float2) + queue_bytes(dtype, lay, x.q);
     const int64_t param_ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
     const dim3 all(unsigned(grid.x + (param_ctas + lay.runs - 1) / lay.runs), grid.y);
 #define CALL(DT, VEC, BY_OCT)                                                                                     \

@@ -24,6 +24,7 @@
 
 #include <type_traits>
 
+#include "tsx_device.cuh"
 #include "tsx_oct.cuh"
 
 namespace tsx {
@@ -721,6 +722,95 @@ struct GradRow {
                 r = __fmul2_rn(r, make_float2(scale[2 * j], scale[2 * j + 1]));
             hat[j] = __ffma2_rn(f[j], r, k.off.at(j));
         }
+    }
+};
+
+// The backward pass's rows on their way: a queue in shared memory that each
+// thread fills by cp.async for itself alone, so that no barrier guards it and
+// the bytes in flight do not depend on registers.  The streaming kernels hold
+// dz's sums, weights and statistics in over 50 registers; with four rows in
+// registers beside them, 57 KB an SM were on their way in bursts (sums of
+// bf16 [4, 16384, 512] from int8: 34 us), with a queue of eight rows twice
+// that without a pause.
+constexpr int kQueueBatch = 2;   // rows to a cp.async group
+template <int DT>
+TSX_HD constexpr int queue_rows() { return DT == TSX_F32 ? 4 : 8; }
+template <int DT, bool HELD>
+TSX_HD constexpr int queue_row_bytes()   // of one thread
+{
+    return elem_size(DT) * 8 + (HELD ? 8 + 4 : elem_size(DT) * 8);
+}
+
+template <int DT, bool HELD>
+struct GradQueue {
+    static constexpr int kRows = queue_rows<DT>(), kBatches = kRows / kQueueBatch;
+    static constexpr uint32_t kOctBytes = elem_size(DT) * 8;
+    GradWalk<DT, true, HELD> w;
+    uint32_t dy, x, scale;   // this thread's place in the queue's arrays
+    uint32_t row16, row8, row4;   // bytes from row to row of them
+    int in, left;            // rows asked for so far; rows that are still to be asked for
+    __device__ __forceinline__ GradQueue(const GradWalk<DT, true, HELD>& walk, char* shared, int rows)
+        : w(walk), in(0), left(rows)
+    {
+        const uint32_t t = threadIdx.x, n = blockDim.x;
+        row16 = n * 16;
+        row8 = n * 8;
+        row4 = n * 4;
+        dy = smem_addr(shared) + t * 16;
+        const uint32_t after = smem_addr(shared) + kRows * n * kOctBytes;
+        x = after + t * (HELD ? 8 : 16);
+        scale = after + kRows * n * 8 + t * 4;
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b)
+            ask();
+    }
+    // The next batch, into the slots of the batch that was taken last.
+    __device__ __forceinline__ void ask()
+    {
+#pragma unroll
+        for (int i = 0; i < kQueueBatch; ++i)
+            if (i < left) {
+                const uint32_t slot = (in + i) % kRows;
+                const char* pd = w.dy.p + i * w.dy.step;
+#pragma unroll
+                for (uint32_t h = 0; h < kOctBytes / 16; ++h)
+                    cp_async(dy + (slot * (kOctBytes / 16) + h) * row16, pd + 16 * h, 16, 16);
+                if constexpr (HELD) {
+                    cp_async(x + slot * row8, w.q + i * w.q_step, 8, 8);
+                    cp_async(scale + slot * row4, w.scale + i * w.scale_step, 4, 4);
+                } else {
+                    const char* px = w.x.p + i * w.x.step;
+#pragma unroll
+                    for (uint32_t h = 0; h < kOctBytes / 16; ++h)
+                        cp_async(x + (slot * (kOctBytes / 16) + h) * row16, px + 16 * h, 16, 16);
+                }
+            }
+        cp_async_commit();
+        w.advance(kQueueBatch);
+        in += kQueueBatch;
+        left -= kQueueBatch;
+    }
+    // The i-th row of the oldest batch.
+    __device__ __forceinline__ void take(int i, GradRow<DT, true, HELD>& g) const
+    {
+        const uint32_t slot = (in + i) % kRows;
+#pragma unroll
+        for (uint32_t h = 0; h < kOctBytes / 16; ++h)
+            lds16(dy + (slot * (kOctBytes / 16) + h) * row16, g.dy.w + 4 * h);
+        if constexpr (HELD) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(g.q.w[0]), "=r"(g.q.w[1]) : "r"(x + slot * row8));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scale + slot * row4));
+        } else {
+#pragma unroll
+            for (uint32_t h = 0; h < kOctBytes / 16; ++h)
+                lds16(x + (slot * (kOctBytes / 16) + h) * row16, g.x.w + 4 * h);
+        }
+    }
+    static __device__ __forceinline__ void lds16(uint32_t at, uint32_t* w)
+    {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at));
     }
 };
 
