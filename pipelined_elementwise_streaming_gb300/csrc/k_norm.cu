@@ -18,8 +18,8 @@ template <int DT>
 TSX_HD constexpr int stats_rows() { return DT == TSX_F32 ? 4 : 8; }
 
 // CTAs to an SM that the registers are cut for.
-template <int DT, bool VEC>
-TSX_HD constexpr int forward_ctas() { return 3; }
+constexpr int kForwardCtas = 3;
+constexpr int kBackwardCtas = 2;
 
 // A CTA's range of rows: blockIdx.x counts ranges sample by sample.  The
 // `ranks` CTAs of a cluster take neighbouring ranges and join their sums.
@@ -56,7 +56,7 @@ __device__ __forceinline__ float2* part_of(const NormArgs& a, const NormPlace& s
 
 // First kernel: (mean, M2) of every cluster's range, run and group.
 template <int DT, bool VEC, bool BY_OCT>
-__global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>()) norm_stats_kernel(NormArgs a, const void* x, float2* part)
+__global__ void __launch_bounds__(kNormThreads, kForwardCtas) norm_stats_kernel(NormArgs a, const void* x, float2* part)
 {
     extern __shared__ float4 shared4[];
     const NormPlace s = norm_place<VEC>(a);
@@ -154,7 +154,7 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
 
 // Second kernel: y, and with HOLD the checkpoint of x.
 template <int DT, bool VEC, bool BY_OCT, bool HOLD>
-__global__ void __launch_bounds__(kNormThreads, forward_ctas<DT, VEC>())
+__global__ void __launch_bounds__(kNormThreads, kForwardCtas)
     norm_apply_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                       float* rstd, HeldOut held, const float2* part)
 {
@@ -217,7 +217,7 @@ __device__ __forceinline__ char* next_16(float2* p)
     return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15));
 }
 
-// use(row, i) for a thread's `rows` rows, through the queue where they are
+// use(row) for each of a thread's `rows` rows, through the queue where they are
 // vectors; begin() runs once the first are on their way.
 template <int DT, bool VEC, bool HELD, class Begin, class Use>
 __device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, GradWalk<DT, VEC, HELD> w,
@@ -226,17 +226,19 @@ __device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, 
     if constexpr (VEC) {
         GradQueue<DT, HELD> q(w, queue, rows);
         begin();
-        for (int i0 = 0; i0 < rows; i0 += kQueueBatch) {
-            cp_async_wait(GradQueue<DT, HELD>::kBatches - 1);
-            GradRow<DT, true, HELD> g[kQueueBatch];
+        for (int left = rows; left > 0; left -= q.kRows)
 #pragma unroll
-            for (int i = 0; i < kQueueBatch; ++i)
-                if (i0 + i < rows) {
-                    q.take(i, g[i]);
-                    use(g[i], i0 + i);
-                }
-            q.ask();
-        }
+            for (int b = 0; b < q.kBatches; ++b) {
+                cp_async_wait(q.kBatches - 1);
+                GradRow<DT, true, HELD> g[kQueueBatch];
+#pragma unroll
+                for (int i = 0; i < kQueueBatch; ++i)
+                    if (b * kQueueBatch + i < left) {
+                        q.take(b, i, g[i]);
+                        use(g[i]);
+                    }
+                q.ask(b);
+            }
         cp_async_wait(0);
     } else {
         begin();
@@ -250,7 +252,7 @@ __device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, 
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i)
                 if (i0 + i < rows)
-                    use(g[i], i0 + i);
+                    use(g[i]);
         }
     }
 }
@@ -258,7 +260,7 @@ __device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, 
 // First kernel: S1 and S2 of every cluster's range, run and group, and the
 // range's sums for dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
-__global__ void __launch_bounds__(kNormThreads, 2)
+__global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     norm_sums_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, float2* part, float* chan)
 {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
     const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, [] {}, [&](const GradRow<DT, VEC, HELD>& g, int) {
+    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, [] {}, [&](const GradRow<DT, VEC, HELD>& g) {
         float2 fd[4], hat[4], dz[4];
         oct_floats(g.dy, fd);
         g.hats(a, k, hat);
@@ -297,15 +299,33 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     });
     if (s.live)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
-    __syncthreads();
-    sum_lanes(slots, stride, 1, P, width, columns, work);
+    float2* sums = part_of(a, s, r, part);
+    float2* mine = a.lay.ranks > 1 ? stats : sums;
+    if constexpr (BY_OCT) {
+        // S1 and S2 from the threads' weighted sums, beside the channels' sums
+        float2 t1 = make_float2(0.f, 0.f), t2 = t1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            t1 = __ffma2_rn(sz[j], k.w[j], t1);
+            t2 = __ffma2_rn(szx[j], k.w[j], t2);
+        }
+        const float f = 1.f / act_scale(a.act);
+        if (s.live)
+            work[s.p * (width / 8) + s.at.ch / 8] = make_float2((t1.x + t1.y) * f, (t2.x + t2.y) * f);
+        __syncthreads();
+        add_octs(work, width / 8, P, s.groups, group_cols(a, s) / 8, mine);
+        __syncthreads();
+        sum_lanes(slots, stride, 1, P, width, columns, work);
+    } else {
+        __syncthreads();
+        sum_lanes(slots, stride, 1, P, width, columns, work);
+        weigh_columns<DT>(a, s, 1, width, weight, columns, mine);
+    }
     float* out = chan + (r.sample * a.lay.splits + r.split) * 2 * a.c + s.ch0;
     for (int ch = threadIdx.x; ch < width; ch += blockDim.x) {
         out[ch] = columns[ch].y;
         out[a.c + ch] = columns[ch].x;
     }
-    float2* sums = part_of(a, s, r, part);
-    weigh_columns<DT>(a, s, 1, width, weight, columns, a.lay.ranks > 1 ? stats : sums);
     if (a.lay.ranks > 1) {
         __syncthreads();
         cluster_wait();
@@ -353,7 +373,7 @@ __device__ __forceinline__ void add_params(const float* chan, int64_t slices, in
 
 // Second kernel: dx; the CTAs past the ranges' add up dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
-__global__ void __launch_bounds__(kNormThreads, 2)
+__global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     norm_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, void* dx, float* dweight, float* dbias, const float2* part, const float* chan)
 {
@@ -403,7 +423,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     k.statistics(a, s, stats);
     to.set(a, s, k, sums);
     };
-    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin, [&](const GradRow<DT, VEC, HELD>& g, int) {
+    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin, [&](const GradRow<DT, VEC, HELD>& g) {
         float2 fd[4], hat[4], dz[4], v[4];
         oct_floats(g.dy, fd);
         g.hats(a, k, hat);
@@ -444,7 +464,7 @@ size_t queue_bytes(int dtype, const NormLayout& lay, bool held)
     const int row = dtype == TSX_F32 ? (held ? queue_row_bytes<TSX_F32, true>() : queue_row_bytes<TSX_F32, false>())
                                      : (held ? queue_row_bytes<TSX_BF16, true>() : queue_row_bytes<TSX_BF16, false>());
     const int rows = dtype == TSX_F32 ? queue_rows<TSX_F32>() : queue_rows<TSX_BF16>();
-    return 16 + size_t(lay.threads) * rows * row;   // after the next multiple of 16
+    return 16 + size_t(kNormThreads) * rows * row;   // after the next multiple of 16
 }
 
 size_t rank_sums(const NormLayout& lay) { return size_t(lay.run_groups) * (lay.ranks > 1 ? lay.ranks + 1 : 1); }

@@ -268,8 +268,16 @@ constexpr int64_t kNormHeldCtas = 2 * 152;
 // 152 SMs hold at once, three each forward and two backward.  A constant of the
 // chip, not read from it, so that results depend on the shape alone.
 constexpr int64_t kNormCtas = 3 * 152, kNormGradCtas = 2 * 152;
-constexpr int64_t kNormParts = 32;   // parts of a sample that the second kernel's CTAs join by themselves
+constexpr int64_t kNormWide = 640;
+constexpr int64_t kNormParts = 160;   // parts of a sample that the second kernel's CTAs join by themselves
 constexpr int kNormRowsAtOnce = 4;
+
+// Threads of a CTA that a run of channels puts to work.
+int64_t filled(int64_t cols, int team)
+{
+    const int64_t v = round_up((cols + kOct - 1) / kOct, team);
+    return v > kNormThreads ? 0 : kNormThreads / v * ((cols + kOct - 1) / kOct);
+}
 
 // The streaming layout for rows of c channels; block: channels to a scale
 // where the call writes checkpoints, else 0.  False if this alignment (vec,
@@ -293,13 +301,25 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
         lay.pieces = int((per + lay.run_cols - 1) / lay.run_cols);
         lay.runs = int(d.groups) * lay.pieces;
     } else {
-        int64_t groups = d.groups;
-        if (d.c > kNormRun) {
-            const int64_t unit = align / std::gcd(per, align);
-            groups = kNormRun / per / unit * unit;
-            if (groups == 0)
-                return false;
-        }
+        // the widest run of at most kNormWide channels that fills a CTA with
+        // rows side by side, or the one that comes nearest
+        const int64_t unit = align / std::gcd(per, align);
+        int64_t groups = d.c <= kNormRun ? d.groups : 0, best = groups ? filled(d.c, team_of(d.c, block, vec)) : 0;
+        if (d.c > kNormWide)
+            for (int64_t g = kNormRun / per / unit * unit; g > 0; g -= unit) {
+                const int64_t cols = g * per;
+                if (g >= d.groups || (cols > kNormWide && g > unit && best > 0))
+                    continue;
+                if (cols * elem_size(d.dtype) < 128 && groups > 0)
+                    break;
+                const int64_t full = filled(cols, team_of(cols, block, vec));
+                if (full > best) {
+                    best = full;
+                    groups = g;
+                }
+            }
+        if (groups == 0)
+            return false;
         lay.run_groups = int(groups);
         lay.run_cols = int(groups * per);
         lay.pieces = 1;
@@ -314,14 +334,11 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
     const int64_t ctas = (backward ? kNormGradCtas : kNormCtas) / (d.n * lay.runs);
     const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
     int64_t splits = ctas < 1 ? 1 : ctas < most ? ctas : most;
-    // many ranges: clusters join four or eight each, so that few parts are
-    // left.  The SMs hold fewer CTAs in clusters of eight (408 of 456, 288 of
+    // many ranges: clusters join eight each, so that few parts are left.  The SMs hold fewer CTAs in clusters of eight (408 of 456, 288 of
     // 304), and a second wave for the last costs more than the room
-    lay.ranks = splits > 4 * kNormParts ? 8 : splits > kNormParts ? 4 : 1;
+    lay.ranks = splits > kNormParts ? 8 : 1;
     if (lay.ranks == 8 && splits > ctas * 5 / 6)
         splits = ctas * 5 / 6;
-    if (lay.ranks == 4 && splits > ctas * 15 / 16)
-        splits = ctas * 15 / 16;
     splits = splits / lay.ranks * lay.ranks;
     lay.range = (d.l + splits - 1) / splits;   // the last ranges may be short, or empty
     lay.splits = splits;

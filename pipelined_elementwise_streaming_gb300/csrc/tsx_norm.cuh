@@ -438,6 +438,23 @@ __device__ __forceinline__ void weigh_columns(const NormArgs& a, const NormPlace
     });
 }
 
+// out[group] = the sums of a group's pairs, one to an oct and row lane:
+// pairs[lanes][width], `per` neighbouring octs to a group.  By whole warps.
+__device__ __forceinline__ void add_octs(const float2* pairs, int width, int lanes, int groups, int per, float2* out)
+{
+    each_item(groups, lanes * per, [&](int g, int lane, int team, bool real) {
+        float2 t = make_float2(0.f, 0.f);
+        for (int e = lane; e < lanes * per; e += team) {
+            const int p = e / per;
+            t = __fadd2_rn(t, pairs[p * width + g * per + e - p * per]);
+        }
+        t.x = lanes_sum(t.x, team);
+        t.y = lanes_sum(t.y, team);
+        if (real && lane == 0)
+            out[g] = t;
+    });
+}
+
 // A value for each of a thread's channels that is the same within a group, as
 // pairs (BY_OCT: one for all).
 template <bool BY_OCT>
@@ -744,66 +761,61 @@ TSX_HD constexpr int queue_row_bytes()   // of one thread
 template <int DT, bool HELD>
 struct GradQueue {
     static constexpr int kRows = queue_rows<DT>(), kBatches = kRows / kQueueBatch;
-    static constexpr uint32_t kOctBytes = elem_size(DT) * 8;
+    static constexpr uint32_t kVecs = elem_size(DT) / 2;   // 16-byte vectors of an oct
+    static constexpr uint32_t k16 = kNormThreads * 16, k8 = kNormThreads * 8, k4 = kNormThreads * 4;
     GradWalk<DT, true, HELD> w;
     uint32_t dy, x, scale;   // this thread's place in the queue's arrays
-    uint32_t row16, row8, row4;   // bytes from row to row of them
-    int in, left;            // rows asked for so far; rows that are still to be asked for
+    int left;                // rows that are still to be asked for
     __device__ __forceinline__ GradQueue(const GradWalk<DT, true, HELD>& walk, char* shared, int rows)
-        : w(walk), in(0), left(rows)
+        : w(walk), left(rows)
     {
-        const uint32_t t = threadIdx.x, n = blockDim.x;
-        row16 = n * 16;
-        row8 = n * 8;
-        row4 = n * 4;
-        dy = smem_addr(shared) + t * 16;
-        const uint32_t after = smem_addr(shared) + kRows * n * kOctBytes;
-        x = after + t * (HELD ? 8 : 16);
-        scale = after + kRows * n * 8 + t * 4;
+        dy = smem_addr(shared) + threadIdx.x * 16;
+        const uint32_t after = smem_addr(shared) + kRows * kVecs * k16;
+        x = after + threadIdx.x * (HELD ? 8 : 16);
+        scale = after + kRows * k8 + threadIdx.x * 4;
 #pragma unroll
         for (int b = 0; b < kBatches; ++b)
-            ask();
+            ask(b);
     }
-    // The next batch, into the slots of the batch that was taken last.
-    __device__ __forceinline__ void ask()
+    // The walk's next rows, into the slots of batch b.
+    __device__ __forceinline__ void ask(int b)
     {
 #pragma unroll
         for (int i = 0; i < kQueueBatch; ++i)
             if (i < left) {
-                const uint32_t slot = (in + i) % kRows;
+                const uint32_t slot = b * kQueueBatch + i;
                 const char* pd = w.dy.p + i * w.dy.step;
 #pragma unroll
-                for (uint32_t h = 0; h < kOctBytes / 16; ++h)
-                    cp_async(dy + (slot * (kOctBytes / 16) + h) * row16, pd + 16 * h, 16, 16);
+                for (uint32_t h = 0; h < kVecs; ++h)
+                    cp_async(dy + (slot * kVecs + h) * k16, pd + 16 * h, 16, 16);
                 if constexpr (HELD) {
-                    cp_async(x + slot * row8, w.q + i * w.q_step, 8, 8);
-                    cp_async(scale + slot * row4, w.scale + i * w.scale_step, 4, 4);
+                    cp_async(x + slot * k8, w.q + i * w.q_step, 8, 8);
+                    cp_async(scale + slot * k4, w.scale + i * w.scale_step, 4, 4);
                 } else {
                     const char* px = w.x.p + i * w.x.step;
 #pragma unroll
-                    for (uint32_t h = 0; h < kOctBytes / 16; ++h)
-                        cp_async(x + (slot * (kOctBytes / 16) + h) * row16, px + 16 * h, 16, 16);
+                    for (uint32_t h = 0; h < kVecs; ++h)
+                        cp_async(x + (slot * kVecs + h) * k16, px + 16 * h, 16, 16);
                 }
             }
         cp_async_commit();
         w.advance(kQueueBatch);
-        in += kQueueBatch;
         left -= kQueueBatch;
     }
-    // The i-th row of the oldest batch.
-    __device__ __forceinline__ void take(int i, GradRow<DT, true, HELD>& g) const
+    // Row i of batch b.
+    __device__ __forceinline__ void take(int b, int i, GradRow<DT, true, HELD>& g) const
     {
-        const uint32_t slot = (in + i) % kRows;
+        const uint32_t slot = b * kQueueBatch + i;
 #pragma unroll
-        for (uint32_t h = 0; h < kOctBytes / 16; ++h)
-            lds16(dy + (slot * (kOctBytes / 16) + h) * row16, g.dy.w + 4 * h);
+        for (uint32_t h = 0; h < kVecs; ++h)
+            lds16(dy + (slot * kVecs + h) * k16, g.dy.w + 4 * h);
         if constexpr (HELD) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(g.q.w[0]), "=r"(g.q.w[1]) : "r"(x + slot * row8));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scale + slot * row4));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(g.q.w[0]), "=r"(g.q.w[1]) : "r"(x + slot * k8));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scale + slot * k4));
         } else {
 #pragma unroll
-            for (uint32_t h = 0; h < kOctBytes / 16; ++h)
-                lds16(x + (slot * (kOctBytes / 16) + h) * row16, g.x.w + 4 * h);
+            for (uint32_t h = 0; h < kVecs; ++h)
+                lds16(x + (slot * kVecs + h) * k16, g.x.w + 4 * h);
         }
     }
     static __device__ __forceinline__ void lds16(uint32_t at, uint32_t* w)
