@@ -483,16 +483,16 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
     const size_t stats = items * sizeof(float4) + lay.run_groups * sizeof(float2);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT) \
-    e = launch_grid(norm_stats_kernel<DT, VEC, BY_OCT>, grid, lay.threads, slots, lay.ranks, false, st, a, x, \
+    e = launch_grid<norm_stats_kernel<DT, VEC, BY_OCT>>(grid, lay.threads, slots, lay.ranks, false, st, a, x, \
                     scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
     if (e != cudaSuccess)
         return e;
 #define CALL(DT, VEC, BY_OCT)                                                                                       \
-    e = held.q ? launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, stats, 1, true, st, a, x, \
+    e = held.q ? launch_grid<norm_apply_kernel<DT, VEC, BY_OCT, true>>(grid, lay.threads, stats, 1, true, st, a, x, \
                              weight, bias, y, mean, rstd, held, scratch.part)                                       \
-               : launch_grid(norm_apply_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, stats, 1, true, st, a, x, \
+               : launch_grid<norm_apply_kernel<DT, VEC, BY_OCT, false>>(grid, lay.threads, stats, 1, true, st, a, x, \
                              weight, bias, y, mean, rstd, held, scratch.part)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
@@ -509,9 +509,9 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
                          size_t(lay.P) * slot_stride(lay.run_cols)) * sizeof(float2) + queue_bytes(dtype, lay, x.q);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT)                                                                                       \
-    e = x.q ? launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, true>, grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
+    e = x.q ? launch_grid<norm_sums_kernel<DT, VEC, BY_OCT, true>>(grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, scratch.part, scratch.chan)                                  \
-            : launch_grid(norm_sums_kernel<DT, VEC, BY_OCT, false>, grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
+            : launch_grid<norm_sums_kernel<DT, VEC, BY_OCT, false>>(grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, scratch.part, scratch.chan)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
@@ -522,9 +522,9 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
     const int64_t param_ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
     const dim3 all(unsigned(grid.x + (param_ctas + lay.runs - 1) / lay.runs), grid.y);
 #define CALL(DT, VEC, BY_OCT)                                                                                     \
-    e = x.q ? launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, true>, all, lay.threads, stats, 1, true, st, a, dy, x,  \
+    e = x.q ? launch_grid<norm_grad_kernel<DT, VEC, BY_OCT, true>>(all, lay.threads, stats, 1, true, st, a, dy, x,  \
                           weight, bias, mean, rstd, dx, dweight, dbias, scratch.part, scratch.chan)               \
-            : launch_grid(norm_grad_kernel<DT, VEC, BY_OCT, false>, all, lay.threads, stats, 1, true, st, a, dy, x, \
+            : launch_grid<norm_grad_kernel<DT, VEC, BY_OCT, false>>(all, lay.threads, stats, 1, true, st, a, dy, x, \
                           weight, bias, mean, rstd, dx, dweight, dbias, scratch.part, scratch.chan)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
@@ -535,7 +535,7 @@ cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* c
                                cudaStream_t st)
 {
     const int64_t ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
-    return launch_grid(norm_params_kernel, dim3(unsigned(ctas)), 1024, 0, 1, true, st, chan, slices, a.c, dweight,
+    return launch_grid<norm_params_kernel>(dim3(unsigned(ctas)), 1024, 0, 1, true, st, chan, slices, a.c, dweight,
                        dbias);
 }
 

@@ -1,12 +1,17 @@
 // Group norm of samples that fit on chip: a CTA, or a cluster of CTAs that
-// share a sample's rows, holds a run of channels of a sample in registers, so
-// that its operands are read once.  HBM bounds it, and for small tensors the
-// chain load - sum - barrier - store.
+// share a sample's rows, holds a run of channels of a sample in shared memory,
+// so that its operands are read once.  The first step is bound by HBM; where
+// all samples fit on the chip at once, which is where this kernel is taken for
+// samples of more than one CTA, so is the whole but for one chain load - sum -
+// cluster barrier - store.
 //
-// A thread holds up to kHeldRows rows of its oct.  The statistics go through
-// the CTA's shared memory (tsx_norm.cuh) and, in a cluster, through every
-// CTA's copy of the groups' sums: all ranks join the ranks' sums in the same
-// order, so they agree to the bit.  A CTA takes Q small samples side by side.
+// Every thread fills its own slots of shared memory by cp.async and reads them
+// back itself, all rows at once on their way in up to eight groups, so that no
+// barrier guards them and the sums start with the first group.  The
+// statistics go through the CTA's shared memory (tsx_norm.cuh) and, in a
+// cluster, through every CTA's copy of the groups' sums: all ranks join the
+// ranks' sums in the same order, so they agree to the bit.  A CTA takes Q small
+// samples side by side.
 
 #include "tsx_norm.cuh"
 
@@ -15,8 +20,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kHeldRows = kNormHeldRows;
-constexpr int kHeldGradRows = kNormHeldGradRows;
+constexpr int kAskGroups = 8;   // cp.async groups
 
 // Which rows a thread holds: lane, lane + lanes, ... of its sample's part.
 struct HeldPlace {
@@ -57,8 +61,52 @@ __device__ __forceinline__ void gather_ranks(const float2* sums, int items, int 
     __syncthreads();
 }
 
-template <int DT, bool BY_OCT, bool HOLD, int ROWS>
-__global__ void __launch_bounds__(kNormThreads, 2)
+// Rows to a cp.async group: all that a lane may have in at most kAskGroups
+// groups of whole fours.
+__device__ __forceinline__ int rows_to_group(const NormLayout& lay)
+{
+    return ((lay.lane_rows + kAskGroups - 1) / kAskGroups + 3) / 4 * 4;
+}
+
+// A thread's octs of one operand in shared memory.
+template <int DT>
+struct Slots {
+    static constexpr uint32_t kVecs = elem_size(DT) / 2;   // 16-byte vectors of an oct
+    uint32_t at, step;   // first oct; from vector to vector
+    __device__ __forceinline__ explicit Slots(const char* shared)
+        : at(smem_addr(shared) + threadIdx.x * 16), step(blockDim.x * 16)
+    {
+    }
+    __device__ __forceinline__ void ask(int i, const char* from) const
+    {
+#pragma unroll
+        for (uint32_t h = 0; h < kVecs; ++h)
+            cp_async(at + (i * kVecs + h) * step, from + 16 * h, 16, 16);
+    }
+    __device__ __forceinline__ Oct<DT> take(int i) const
+    {
+        Oct<DT> o;
+#pragma unroll
+        for (uint32_t h = 0; h < kVecs; ++h)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(o.w[4 * h]), "=r"(o.w[4 * h + 1]), "=r"(o.w[4 * h + 2]), "=r"(o.w[4 * h + 3])
+                         : "r"(at + (i * kVecs + h) * step));
+        return o;
+    }
+    // Four octs from i on; those past the thread's n rows are zeros.
+    __device__ __forceinline__ void take4(int i, int n, Oct<DT> (&o)[4]) const
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n)
+                o[k] = take(i + k);
+            else
+                oct_zero(o[k]);
+    }
+};
+
+template <int DT, bool BY_OCT, bool HOLD>
+__global__ void __launch_bounds__(kHeldThreads)
     norm_held_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                      float* rstd, HeldOut held)
 {
@@ -66,21 +114,37 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     const NormLayout& lay = a.lay;
     NormPlace s = norm_place<true>(a);
     const HeldPlace h = held_place(a, s);
-    Oct<DT> o[ROWS];
-    const int have = h.mine;
-    load_rows<DT, true>(walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s), s.at, s.live ? have : 0, o);
+    const int mine = s.live ? h.mine : 0;
+    const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
+    const Slots<DT> rows(reinterpret_cast<char*>(shared4));
+    float4* spare = shared4 + Slots<DT>::kVecs * lay.lane_rows * blockDim.x;   // [warps]
+    float2* sums = reinterpret_cast<float2*>(spare + kHeldThreads / 32);       // [samples][groups]: (mean, M2) of the part
+    float2* stats = sums + items;                                              // [samples][groups]: (mean, rstd)
+    float2* slots = stats + items;                                             // [P][stride]; then [ranks][items]
+    const int each = rows_to_group(lay);
+    {
+        Walk w = walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
+        for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
+            for (int i = i0; i < min(i0 + each, mine); ++i) {
+                rows.ask(i, w.p);
+                w.p += w.step;
+            }
+            cp_async_commit();
+        }
+    }
     Affine k;
     k.template params<DT, true>(a, s, weight, bias);
-
-    const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
-    float4* spare = shared4;                                                // [warps]
-    float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);    // [samples][groups]: (mean, M2) of the part
-    float2* stats = sums + items;                                           // [samples][groups]: (mean, rstd)
-    float2* slots = stats + items;                                          // [P][stride]; then [ranks][items]
     Triples<BY_OCT> t;
     t.clear();
-    if (s.live)
-        t.add_octs(o, have);
+    int pending = (lay.lane_rows + each - 1) / each;
+    for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
+        cp_async_wait(--pending);
+        for (int i = i0; i < min(i0 + each, mine); i += 4) {
+            Oct<DT> o[4];
+            rows.take4(i, mine, o);
+            t.add_octs(o, mine - i);
+        }
+    }
     if (s.p < lay.P && s.at.ch < s.at.cols)   // absent samples leave zeros
         t.leave(s.at, slots + s.p * stride);
     __syncthreads();
@@ -89,11 +153,10 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     if (lay.ranks > 1) {
         cluster_arrive();
         cluster_wait();
+        gather_ranks(sums, items, lay.ranks, slots);
     } else {
         __syncthreads();
     }
-    if (lay.ranks > 1)
-        gather_ranks(sums, items, lay.ranks, slots);
     const float m = static_cast<float>(a.l) * static_cast<float>(a.per_group);
     for (int i = threadIdx.x; i < items; i += blockDim.x) {
         float2 v = sums[i];
@@ -118,57 +181,87 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     }
     __syncthreads();
     k.template statistics<BY_OCT>(a, s, stats + (s.live ? h.q : 0) * s.groups);
-    const WalkOut out = walk_out<DT>(y, h.row0 + h.lane, lay.lanes, a.y_pitch, s);
+    WalkOut out = walk_out<DT>(y, h.row0 + h.lane, lay.lanes, a.y_pitch, s);
+    HeldPtr to;
+    if constexpr (HOLD)
+        to = HeldPtr(held, h.row0 + h.lane, lay.lanes, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
+    for (int i0 = 0; i0 < h.mine; i0 += 4) {   // the same for all threads of a team
+        Oct<DT> o[4];
+        rows.take4(i0, mine, o);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-        if (s.live && i < have) {
-            float2 f[4], v[4];
-            oct_floats(o[i], f);
-            k.apply(a.act, f, v);
-            oct_store<DT, true>(out.p + i * out.step, s.at, oct_round<DT>(v));
-        }
-    if constexpr (HOLD) {
-        HeldPtr to(held, h.row0 + h.lane, lay.lanes, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
-#pragma unroll
-        for (int i0 = 0; i0 < ROWS; i0 += 4) {
-            const Oct<DT> four[4] = {o[i0], o[i0 + 1], o[i0 + 2], o[i0 + 3]};
-            if (i0 < have)
-                hold_rows<DT, true>(four, have - i0, s.live, s.at, lay.team, a.form, to);
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i < mine) {
+                float2 f[4], v[4];
+                oct_floats(o[i], f);
+                k.apply(a.act, f, v);
+                oct_store<DT, true>(out.p + i * out.step, s.at, oct_round<DT>(v));
+            }
+        out.p += 4 * out.step;
+        if constexpr (HOLD) {
+            hold_rows<DT, true>(o, h.mine - i0, s.live, s.at, lay.team, a.form, to);
             to.advance(4);
         }
     }
     if (lay.ranks > 1)
-        cluster_wait();
+        cluster_wait();   // until every rank has read this one's sums
 }
 
-// The gradient: a thread keeps dz in fp32 (forming it again would cost the
-// activation's special functions twice) and x as it came.
+// The gradient.  dz is formed twice rather than held in fp32: the second time
+// costs a few instructions an element, the room would halve the rows that a
+// CTA holds.
 template <int DT, bool BY_OCT, bool HELD>
-__global__ void __launch_bounds__(kNormThreads, 2)
+__global__ void __launch_bounds__(kHeldThreads)
     norm_held_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias,
                           const float* mean, const float* rstd, void* dx, float* chan)
 {
-    extern __shared__ float2 shared[];
+    extern __shared__ float4 shared4[];
     const NormLayout& lay = a.lay;
     NormPlace s = norm_place<true>(a);
     const HeldPlace h = held_place(a, s);
-    GradRow<DT, true, HELD> g[kHeldGradRows];
-    const int have = s.live ? h.mine : 0;
-    const GradWalk<DT, true, HELD> w(a, s, dy, x, h.row0 + h.lane, lay.lanes);
-#pragma unroll
-    for (int i = 0; i < kHeldGradRows; ++i)
-        if (i < have)
-            g[i].load(a, s, w, i);
-    Chan<BY_OCT> k;
-    k.template params<DT, true>(a, s, weight, bias);
+    const int mine = s.live ? h.mine : 0, threads = static_cast<int>(blockDim.x);
     const int width = s.at.cols, stride = slot_stride(width), items = lay.samples * s.groups;
-    float2* sums = shared;                           // [samples][groups]: S1, S2 of the part
+    // dy's octs; x's, or the checkpoint's numbers and scales
+    const Slots<DT> rows(reinterpret_cast<char*>(shared4));
+    char* second = reinterpret_cast<char*>(shared4 + Slots<DT>::kVecs * lay.lane_rows * threads);
+    const Slots<DT> xs(second);
+    const uint32_t qs = smem_addr(second) + threadIdx.x * 8;
+    const uint32_t scales = smem_addr(second) + lay.lane_rows * threads * 8 + threadIdx.x * 4;
+    const size_t bytes = size_t(lay.lane_rows) * threads * (HELD ? 12 : 16 * Slots<DT>::kVecs);
+    float2* sums = reinterpret_cast<float2*>(second + bytes);   // [samples][groups]: S1, S2 of the part
     float2* stats = sums + items;                    // [samples][groups]: (mean, rstd), then -S1 / M, -S2 / M
     float2* work = stats + items;                    // [threads]
-    float2* columns = work + kNormThreads;           // [samples][width]
+    float2* columns = work + kHeldThreads;           // [samples][width]
     float2* slots = columns + lay.samples * width;   // [P][stride]; then [ranks][items]
     let_next_start();
-    for (int i = threadIdx.x; i < items; i += blockDim.x) {
+    const int each = rows_to_group(lay);
+    {
+        GradWalk<DT, true, HELD> w(a, s, dy, x, h.row0 + h.lane, lay.lanes);
+        for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
+            for (int i = i0; i < min(i0 + each, mine); ++i) {
+                rows.ask(i, w.dy.p);
+                if constexpr (HELD) {
+                    cp_async(qs + i * threads * 8, w.q, 8, 8);
+                    cp_async(scales + i * threads * 4, w.scale, 4, 4);
+                } else {
+                    xs.ask(i, w.x.p);
+                }
+                w.advance(1);
+            }
+            cp_async_commit();
+        }
+    }
+    auto take = [&](int i, GradRow<DT, true, HELD>& g) {
+        g.dy = rows.take(i);
+        if constexpr (HELD) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(g.q.w[0]), "=r"(g.q.w[1]) : "r"(qs + i * threads * 8));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scales + i * threads * 4));
+        } else {
+            g.x = xs.take(i);
+        }
+    };
+    Chan<BY_OCT> k;
+    k.template params<DT, true>(a, s, weight, bias);
+    for (int i = threadIdx.x; i < items; i += threads) {
         const int q = lay.samples == 1 ? 0 : i / s.groups;
         const int64_t sample = h.tile * lay.samples + q;
         const int64_t at = sample * a.groups + s.group0 + i - q * s.groups;
@@ -176,30 +269,35 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     }
     __syncthreads();
     k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
-    float2 dz[kHeldGradRows][4], sz[4], szx[4];
+    float2 sz[4], szx[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kHeldGradRows; ++i)
-        if (i < have) {
-            float2 fd[4], hat[4];
-            oct_floats(g[i].dy, fd);
-            g[i].hats(a, k, hat);
-            k.slopes(a, fd, hat, dz[i]);
+    int pending = (lay.lane_rows + each - 1) / each;
+    for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
+        cp_async_wait(--pending);
+#pragma unroll 2
+        for (int i = i0; i < min(i0 + each, mine); ++i) {
+            GradRow<DT, true, HELD> g;
+            float2 fd[4], hat[4], dz[4];
+            take(i, g);
+            oct_floats(g.dy, fd);
+            g.hats(a, k, hat);
+            k.slopes(a, fd, hat, dz);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                sz[j] = __fadd2_rn(sz[j], dz[i][j]);
-                szx[j] = __ffma2_rn(dz[i][j], hat[j], szx[j]);
+                sz[j] = __fadd2_rn(sz[j], dz[j]);
+                szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
             }
         }
+    }
     if (s.p < lay.P && s.at.ch < s.at.cols)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
     __syncthreads();
     sum_lanes(slots, stride, lay.samples, lay.lanes, width, columns, work);
     weigh_columns<DT>(a, s, lay.samples, width, weight, columns, sums);
     float* out = chan + static_cast<int64_t>(blockIdx.x) * 2 * a.c + s.ch0;
-    for (int ch = threadIdx.x; ch < width; ch += blockDim.x) {
+    for (int ch = threadIdx.x; ch < width; ch += threads) {
         float2 v = columns[ch];
         for (int q = 1; q < lay.samples; ++q)
             v = __fadd2_rn(v, columns[q * width + ch]);
@@ -209,13 +307,12 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     if (lay.ranks > 1) {
         cluster_arrive();
         cluster_wait();
+        gather_ranks(sums, items, lay.ranks, slots);
     } else {
         __syncthreads();
     }
-    if (lay.ranks > 1)
-        gather_ranks(sums, items, lay.ranks, slots);
     const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
-    for (int i = threadIdx.x; i < items; i += blockDim.x) {
+    for (int i = threadIdx.x; i < items; i += threads) {
         float2 v = sums[i];
         if (lay.ranks > 1) {
             v = slots[i];
@@ -227,15 +324,19 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     __syncthreads();
     Gradient<BY_OCT> grad;
     grad.set(a, s, k, stats + (s.live ? h.q : 0) * s.groups);
-    const WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
-#pragma unroll
-    for (int i = 0; i < kHeldGradRows; ++i)
-        if (i < have) {
-            float2 hat[4], res[4];
-            g[i].hats(a, k, hat);
-            grad.of(dz[i], hat, res);
-            oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(res));
-        }
+    WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
+#pragma unroll 2
+    for (int i = 0; i < mine; ++i) {
+        GradRow<DT, true, HELD> g;
+        float2 fd[4], hat[4], dz[4], res[4];
+        take(i, g);
+        oct_floats(g.dy, fd);
+        g.hats(a, k, hat);
+        k.slopes(a, fd, hat, dz);
+        grad.of(dz, hat, res);
+        oct_store<DT, true>(to.p, s.at, oct_round<DT>(res));
+        to.p += to.step;
+    }
     if (lay.ranks > 1)
         cluster_wait();
 }
@@ -256,31 +357,32 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }                                                           \
     } while (0)
 
-namespace {
-
-// Pairs of shared memory for the columns, which the ranks' sums reuse.
-size_t slot_pairs(const NormLayout& lay, int width)
+size_t held_bytes(const NormLayout& lay, int es, bool backward, bool held)
 {
-    const size_t slots = size_t(lay.P) * slot_stride(width);
-    const size_t all = lay.ranks > 1 ? size_t(lay.ranks) * lay.samples * lay.run_groups : 0;
-    return slots > all ? slots : all;
+    const size_t octs = size_t(lay.lane_rows) * lay.threads;
+    const size_t items = size_t(lay.samples) * lay.run_groups;
+    const int width = !backward && lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
+    size_t slots = size_t(lay.P) * slot_stride(width);
+    if (lay.ranks > 1 && slots < size_t(lay.ranks) * items)
+        slots = size_t(lay.ranks) * items;   // the ranks' sums reuse them
+    size_t pairs = 2 * items + slots;
+    if (backward)
+        pairs += kHeldThreads + size_t(lay.samples) * width;
+    return octs * es * 8 + (backward ? octs * (held ? 12 : es * 8) : kHeldThreads / 32 * sizeof(float4)) +
+           pairs * sizeof(float2);
 }
-
-}  // namespace
 
 cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,
                              float* mean, float* rstd, HeldOut held, cudaStream_t st)
 {
     const NormLayout& lay = a.lay;
     const dim3 grid(unsigned((a.n + lay.samples - 1) / lay.samples * lay.ranks), unsigned(lay.runs));
-    const int width = lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
-    const size_t smem = kNormThreads / 32 * sizeof(float4) +
-                        (2 * size_t(lay.samples) * lay.run_groups + slot_pairs(lay, width)) * sizeof(float2);
+    const size_t smem = held_bytes(lay, elem_size(dtype), false, false);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, BY_OCT)                                                                                            \
-    e = held.q ? launch_grid(norm_held_kernel<DT, BY_OCT, true, kHeldRows>, grid, lay.threads, smem, lay.ranks, false, st, \
+    e = held.q ? launch_grid<norm_held_kernel<DT, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, \
                              a, x, weight, bias, y, mean, rstd, held)                                               \
-               : launch_grid(norm_held_kernel<DT, BY_OCT, false, kHeldRows>, grid, lay.threads, smem, lay.ranks, false, \
+               : launch_grid<norm_held_kernel<DT, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, \
                              st, a, x, weight, bias, y, mean, rstd, held)
     TSX_BY_HELD(dtype, lay.oct_in_group, CALL);
 #undef CALL
@@ -294,14 +396,12 @@ cudaError_t launch_norm_held_backward(int dtype, const NormArgs& a, const void* 
     const NormLayout& lay = a.lay;
     const int64_t slices = (a.n + lay.samples - 1) / lay.samples * lay.ranks;
     const dim3 grid(unsigned(slices), unsigned(lay.runs));
-    const size_t smem = (2 * size_t(lay.samples) * lay.run_groups + kNormThreads +
-                         size_t(lay.samples) * lay.run_cols + slot_pairs(lay, lay.run_cols)) *
-                        sizeof(float2);
+    const size_t smem = held_bytes(lay, elem_size(dtype), true, x.q != nullptr);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, BY_OCT)                                                                                           \
-    e = x.q ? launch_grid(norm_held_grad_kernel<DT, BY_OCT, true>, grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
+    e = x.q ? launch_grid<norm_held_grad_kernel<DT, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, dx, scratch.chan)                                           \
-            : launch_grid(norm_held_grad_kernel<DT, BY_OCT, false>, grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
+            : launch_grid<norm_held_grad_kernel<DT, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, dx, scratch.chan)
     TSX_BY_HELD(dtype, lay.oct_in_group, CALL);
 #undef CALL

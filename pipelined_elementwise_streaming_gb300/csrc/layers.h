@@ -84,14 +84,13 @@ struct NormLayout {
     // kernels that hold samples on chip: CTAs of a cluster that share a
     // sample, samples side by side in a CTA, row lanes of each (P = samples * lanes)
     int ranks, samples, lanes;
+    int lane_rows;       // rows to a lane at most
     int kind;            // NormKind
 };
 // How a call runs: streaming kernels that read their operands twice (any
 // layout), samples held on chip, tokens whose groups lie within a warp.
 enum NormKind { kNormStream = 0, kNormHeld = 1, kNormToken = 2 };
-// Rows of its oct that a thread holds: forward, and backward (x and dz in fp32).
-constexpr int kNormHeldRows = 8;
-constexpr int kNormHeldGradRows = 4;
+constexpr int kHeldThreads = 512;   // most threads of the kernels that hold samples on chip
 
 struct NormArgs {
     NormLayout lay;
@@ -119,6 +118,8 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
 cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,
                                  const void* bias, const float* mean, const float* rstd, void* dx, float* dweight,
                                  float* dbias, NormScratch scratch, cudaStream_t st);
+// Shared memory of a CTA of the kernels that hold samples on chip.
+size_t held_bytes(const NormLayout& lay, int es, bool backward, bool held);
 cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,
                              float* mean, float* rstd, HeldOut held, cudaStream_t st);
 cudaError_t launch_norm_held_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,

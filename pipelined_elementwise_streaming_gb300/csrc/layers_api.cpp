@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <numeric>
 
 #include "plan.h"
@@ -263,7 +264,10 @@ constexpr int kTokenRun = 2048;
 constexpr int64_t kTokenCtas = 3 * 152, kTokenGradCtas = 2 * 152;
 constexpr int64_t kNormRanks = 8;      // CTAs of a cluster at most
 constexpr int64_t kNormSamples = 64;   // samples side by side at most
-constexpr int64_t kNormHeldCtas = 2 * 152;
+constexpr int64_t kHeldCtas = 2 * 152;    // CTAs to keep before samples are put side by side
+constexpr int64_t kHeldRows = 64;         // rows to a lane at most
+// CTAs of clusters of eight that the SMs hold with one CTA to an SM
+constexpr int64_t kHeldWave = 144;
 // Ranges are cut so that at most this many CTAs share the work: as many as the
 // 152 SMs hold at once, three each forward and two backward.  A constant of the
 // chip, not read from it, so that results depend on the shape alone.
@@ -380,80 +384,123 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     return true;
 }
 
-// Samples on chip.  Among runs of channels from the widest down to 128 bytes
-// a row, the widest that spreads the work over two CTAs to an SM, or else the
-// one that spreads it furthest; a sample too long for one CTA is shared by a
-// cluster, which also spreads small batches.
-bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
+// Samples on chip.  CTAs of 512 threads have an SM to themselves, CTAs of 256
+// share it in twos.  A sample of several CTAs (a cluster) is held only if all
+// samples fit on the chip at once: the chain from the loads over the cluster's
+// barrier to the stores is then gone through once, in less time than the
+// streaming kernels' two launches, and beyond that it is not (measured: see
+// k_norm_held.cu).  Samples of one CTA are held however many there are.
+bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
 {
     const int64_t per = d.c / d.groups;
     if (!vec || per > kNormRun)
         return false;
-    const int rows = backward ? kNormHeldGradRows : kNormHeldRows;
+    const int es = elem_size(d.dtype);
     const int64_t align = block ? block : kOct;
     const int64_t unit = align / std::gcd(per, align);
-    int64_t best_ctas = 0;
-    int64_t groups = d.groups;
-    if (d.c > kNormRun)
-        groups = kNormRun / per / unit * unit;
-    for (; groups > 0;) {
-        NormLayout lay{};
-        lay.kind = kNormHeld;
-        lay.vec = true;
-        lay.oct_in_group = per % kOct == 0;
-        lay.run_groups = int(groups);
-        lay.run_cols = int(groups * per);
-        lay.pieces = 1;
-        lay.runs = int((d.groups + groups - 1) / groups);
-        lay.team = team_of(lay.run_cols, block, true);
-        lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
-        const int64_t lanes = kNormThreads / lay.V;
-        int64_t ranks = 1;
-        while (ranks < kNormRanks && ranks * lanes * rows < d.l)
-            ranks *= 2;
-        if (ranks * lanes * rows >= d.l) {
-            // spread further while a CTA keeps a few rows to a lane
-            while (ranks < 8 && d.n * lay.runs * ranks < kNormHeldCtas && d.l / (2 * ranks) >= 2 * lanes)
-                ranks *= 2;
-            lay.ranks = int(ranks);
-            lay.range = (d.l + ranks - 1) / ranks;   // the last ranks may have no rows
-            // row lanes: as many as there are rows, or fewer with several
-            // samples to a CTA where there are samples enough
-            int64_t own = lay.range < lanes ? lay.range : lanes;
-            int64_t samples = 1;
-            if (lay.ranks == 1 && own < lanes) {
-                const int64_t few = (d.l + rows - 1) / rows;
-                const int64_t most = d.n * lay.runs / kNormHeldCtas;   // keep this many CTAs
-                samples = lanes / few < most ? lanes / few : most;
-                samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
-                own = lanes / samples < own ? lanes / samples : own;
+    int64_t best = 0;   // CTAs of the layout found
+    for (int64_t groups = d.c <= kNormRun ? d.groups : kNormRun / per / unit * unit; groups > 0;) {
+        for (int threads : {256, 512})
+            for (int ranks = 1; ranks <= kNormRanks; ranks *= 2) {
+                NormLayout lay{};
+                lay.kind = kNormHeld;
+                lay.vec = true;
+                lay.oct_in_group = per % kOct == 0;
+                lay.run_groups = int(groups);
+                lay.run_cols = int(groups * per);
+                lay.pieces = 1;
+                lay.runs = int((d.groups + groups - 1) / groups);
+                lay.team = team_of(lay.run_cols, block, true);
+                lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
+                const int64_t lanes = threads / lay.V;
+                lay.ranks = ranks;
+                lay.range = (d.l + ranks - 1) / ranks;   // the last ranks may have no rows
+                lay.splits = 1;
+                // row lanes: as many as there are rows; several samples side
+                // by side where there are CTAs enough
+                int64_t own = lay.range < lanes ? lay.range : lanes, samples = 1;
+                if (ranks == 1 && own < lanes) {
+                    const int64_t most = d.n * lay.runs / kHeldCtas;
+                    samples = lanes / own < most ? lanes / own : most;
+                    samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
+                }
+                lay.samples = int(samples);
+                lay.lanes = int(own);
+                lay.P = int(samples * own);
+                lay.threads = round_up(lay.P * lay.V, 32);
+                const int64_t lane_rows = (lay.range + own - 1) / own;
+                if (lane_rows > kHeldRows)
+                    continue;
+                lay.lane_rows = int(lane_rows);
+                const int64_t room = (threads == 512 ? kMaxDynSmem : (kSmemPerSm - 2 * kSmemPerCtaReserved) / 2);
+                if (int64_t(held_bytes(lay, es, backward, held)) > room)
+                    continue;
+                const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * ranks;
+                const int64_t wave = threads == 512 ? (ranks > 1 ? kHeldWave : 152) : (ranks > 1 ? 2 * kHeldWave : 304);
+                if ((ranks > 1 || threads == 512) && ctas > wave)
+                    continue;
+                // the most CTAs, and of those the widest runs and fewest ranks
+                if (ctas > best) {
+                    best = ctas;
+                    *out = lay;
+                }
+                if (ranks == 1 && ctas >= wave)
+                    return true;
             }
-            lay.samples = int(samples);
-            lay.lanes = int(own);
-            lay.P = int(samples * own);
-            lay.threads = round_up(lay.P * lay.V, 32);
-            lay.splits = 1;
-            const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * lay.ranks;
-            if (ctas > best_ctas) {
-                best_ctas = ctas;
-                *out = lay;
-            }
-            if (ctas >= kNormHeldCtas)
-                return true;
-        }
         const int64_t next = (groups / 2 + unit - 1) / unit * unit;
-        if (next >= groups || next * per * elem_size(d.dtype) < 128)
+        if (next >= groups || next * per * es < 128)
             break;
         groups = next;
     }
-    return best_ctas > 0;
+    return best > 0;
 }
 
-// How a call runs.
-bool norm_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, NormLayout* out)
+// How a call runs; held: backward from a checkpoint.  The search takes
+// microseconds, as long as a launch, so a thread remembers the layouts of its
+// last shapes.
+bool find_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
 {
-    return token_layout(d, vec, block, backward, out) || held_layout(d, vec, block, backward, out) ||
+    return token_layout(d, vec, block, backward, out) || held_layout(d, vec, block, backward, held, out) ||
            stream_layout(d, vec, block, backward, out);
+}
+
+struct LayoutKey {
+    int64_t n, l, c;
+    int32_t dtype, groups, block, flags;
+};
+
+bool norm_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
+{
+    struct Entry {
+        LayoutKey key;
+        bool used, found;
+        NormLayout lay;
+    };
+    constexpr int kEntries = 16;
+    thread_local Entry entries[kEntries];
+    thread_local int next;
+    LayoutKey key;
+    std::memset(&key, 0, sizeof key);
+    key.n = d.n;
+    key.l = d.l;
+    key.c = d.c;
+    key.dtype = d.dtype;
+    key.groups = d.groups;
+    key.block = block;
+    key.flags = vec | backward << 1 | held << 2;
+    for (const Entry& e : entries)
+        if (e.used && std::memcmp(&e.key, &key, sizeof key) == 0) {
+            *out = e.lay;
+            return e.found;
+        }
+    Entry& e = entries[next];
+    next = (next + 1) % kEntries;
+    e.key = key;
+    e.lay = NormLayout{};
+    e.found = find_layout(d, vec, block, backward, held, &e.lay);
+    e.used = true;
+    *out = e.lay;
+    return e.found;
 }
 
 size_t part_bytes(const tsx_norm_desc& d, const NormLayout& lay)
@@ -504,9 +551,9 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward, bool aligned)
     const int64_t es = elem_size(d.dtype);
     const bool whole = d.c % kOct == 0 && d.x_pitch * es % 16 == 0 && d.y_pitch * es % 16 == 0;
     for (int vec = aligned && whole ? 1 : 0; vec < (whole ? 2 : 1); ++vec)
-        for (int block : {0, d.block}) {
+        for (int held = 0; held < 2; ++held) {   // with a checkpoint, written or read
             NormLayout lay;
-            if ((backward && block) || !norm_layout(d, vec != 0, block, backward, &lay))
+            if (!norm_layout(d, vec != 0, held && !backward ? d.block : 0, backward, held != 0, &lay))
                 continue;
             const size_t b = part_bytes(d, lay) + (backward ? chan_bytes(d, lay) : 0);
             most = b > most ? b : most;
@@ -514,10 +561,10 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward, bool aligned)
     return most;
 }
 
-int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, const void* weight,
+int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, const void* weight,
               const void* bias, NormArgs* a)
 {
-    if (!norm_layout(d, vec, block, backward, &a->lay) && !norm_layout(d, false, block, backward, &a->lay))
+    if (!norm_layout(d, vec, block, backward, held, &a->lay) && !norm_layout(d, false, block, backward, held, &a->lay))
         return fail(TSX_ERR_UNSUPPORTED, call, "no layout");
     if (a->lay.runs > kMaxChunks)
         return fail(TSX_ERR_UNSUPPORTED, call, "rows are too long");
@@ -592,9 +639,9 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
     const bool vec = vectors(x, d.c, d.x_pitch, es) && vectors(y, d.c, d.y_pitch, es) && held_vectors(q, d.c);
     // the checkpoint rides along where runs can start on its blocks
     NormLayout lay;
-    const bool ride = q && (norm_layout(d, vec, d.block, false, &lay) || norm_layout(d, false, d.block, false, &lay));
+    const bool ride = q && (norm_layout(d, vec, d.block, false, true, &lay) || norm_layout(d, false, d.block, false, true, &lay));
     NormArgs a{};
-    rc = norm_args(call, d, vec, ride ? d.block : 0, false, weight, bias, &a);
+    rc = norm_args(call, d, vec, ride ? d.block : 0, false, ride, weight, bias, &a);
     if (rc == TSX_OK)
         rc = check_scratch(call, part_bytes(d, a.lay), workspace, workspace_bytes);
     if (rc != TSX_OK)
@@ -655,7 +702,7 @@ extern "C" int tsx_group_norm_backward(const tsx_norm_desc* desc, const void* dy
     const bool vec = vectors(dy, d.c, d.y_pitch, es) && vectors(x, d.c, d.x_pitch, es) &&
                      vectors(dx, d.c, d.x_pitch, es) && held_vectors(q, d.c);
     NormArgs a{};
-    rc = norm_args(call, d, vec, 0, true, weight, bias, &a);
+    rc = norm_args(call, d, vec, 0, true, q != nullptr, weight, bias, &a);
     if (rc == TSX_OK)
         rc = check_scratch(call, part_bytes(d, a.lay) + chan_bytes(d, a.lay), workspace, workspace_bytes);
     if (rc != TSX_OK)

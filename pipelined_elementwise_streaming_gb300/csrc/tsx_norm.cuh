@@ -22,6 +22,7 @@
 // columns over all row lanes.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "tsx_device.cuh"
@@ -828,15 +829,23 @@ struct GradQueue {
 
 }  // namespace dev
 
-// Launch `kernel` with clusters of `ranks` CTAs along x (1: none); `early`: it
+// Launch `Kernel` with clusters of `ranks` CTAs along x (1: none); `early`: it
 // may start while the stream's last kernel still runs (it waits by itself).
-template <class K, class... Args>
-cudaError_t launch_grid(K kernel, dim3 grid, int threads, size_t smem, int ranks, bool early, cudaStream_t st,
-                        Args... args)
+// More than 48 KB of shared memory is asked for once on each device.
+template <auto Kernel, class... Args>
+cudaError_t launch_grid(dim3 grid, int threads, size_t smem, int ranks, bool early, cudaStream_t st, Args... args)
 {
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        constexpr int kDevices = 64;
+        static std::atomic<bool> allowed[kDevices];
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e == cudaSuccess && (device >= kDevices || !allowed[device].load())) {
+            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
+            if (e == cudaSuccess && device < kDevices)
+                allowed[device].store(true);
+        }
         if (e != cudaSuccess)
             return e;
     }
@@ -858,7 +867,7 @@ cudaError_t launch_grid(K kernel, dim3 grid, int threads, size_t smem, int ranks
         ++cfg.numAttrs;
     }
     cfg.attrs = attr;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, Kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
