@@ -68,8 +68,9 @@ __device__ __forceinline__ int rows_to_group(const NormLayout& lay)
     return ((lay.lane_rows + kAskGroups - 1) / kAskGroups + 3) / 4 * 4;
 }
 
-// A thread's octs of one operand in shared memory.
-template <int DT>
+// A thread's octs of one operand in shared memory.  Octs that are no vectors
+// go through registers.
+template <int DT, bool VEC>
 struct Slots {
     static constexpr uint32_t kVecs = elem_size(DT) / 2;   // 16-byte vectors of an oct
     uint32_t at, step;   // first oct; from vector to vector
@@ -77,11 +78,20 @@ struct Slots {
         : at(smem_addr(shared) + threadIdx.x * 16), step(blockDim.x * 16)
     {
     }
-    __device__ __forceinline__ void ask(int i, const char* from) const
+    __device__ __forceinline__ void ask(int i, const char* from, const OctAt& oct) const
     {
+        if constexpr (VEC) {
 #pragma unroll
-        for (uint32_t h = 0; h < kVecs; ++h)
-            cp_async(at + (i * kVecs + h) * step, from + 16 * h, 16, 16);
+            for (uint32_t h = 0; h < kVecs; ++h)
+                cp_async(at + (i * kVecs + h) * step, from + 16 * h, 16, 16);
+        } else {
+            const Oct<DT> o = oct_load<DT, false>(from, oct);
+#pragma unroll
+            for (uint32_t h = 0; h < kVecs; ++h)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (i * kVecs + h) * step),
+                             "r"(o.w[4 * h]), "r"(o.w[4 * h + 1]), "r"(o.w[4 * h + 2]), "r"(o.w[4 * h + 3])
+                             : "memory");
+        }
     }
     __device__ __forceinline__ Oct<DT> take(int i) const
     {
@@ -105,19 +115,19 @@ struct Slots {
     }
 };
 
-template <int DT, bool BY_OCT, bool HOLD>
+template <int DT, bool VEC, bool BY_OCT, bool HOLD>
 __global__ void __launch_bounds__(kHeldThreads)
     norm_held_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                      float* rstd, HeldOut held)
 {
     extern __shared__ float4 shared4[];
     const NormLayout& lay = a.lay;
-    NormPlace s = norm_place<true>(a);
+    NormPlace s = norm_place<VEC>(a);
     const HeldPlace h = held_place(a, s);
     const int mine = s.live ? h.mine : 0;
     const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
-    const Slots<DT> rows(reinterpret_cast<char*>(shared4));
-    float4* spare = shared4 + Slots<DT>::kVecs * lay.lane_rows * blockDim.x;   // [warps]
+    const Slots<DT, VEC> rows(reinterpret_cast<char*>(shared4));
+    float4* spare = shared4 + Slots<DT, VEC>::kVecs * lay.lane_rows * blockDim.x;   // [warps]
     float2* sums = reinterpret_cast<float2*>(spare + kHeldThreads / 32);       // [samples][groups]: (mean, M2) of the part
     float2* stats = sums + items;                                              // [samples][groups]: (mean, rstd)
     float2* slots = stats + items;                                             // [P][stride]; then [ranks][items]
@@ -126,14 +136,14 @@ __global__ void __launch_bounds__(kHeldThreads)
         Walk w = walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
         for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
             for (int i = i0; i < min(i0 + each, mine); ++i) {
-                rows.ask(i, w.p);
+                rows.ask(i, w.p, s.at);
                 w.p += w.step;
             }
             cp_async_commit();
         }
     }
     Affine k;
-    k.template params<DT, true>(a, s, weight, bias);
+    k.template params<DT, VEC>(a, s, weight, bias);
     Triples<BY_OCT> t;
     t.clear();
     int pending = (lay.lane_rows + each - 1) / each;
@@ -194,11 +204,11 @@ __global__ void __launch_bounds__(kHeldThreads)
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
                 k.apply(a.act, f, v);
-                oct_store<DT, true>(out.p + i * out.step, s.at, oct_round<DT>(v));
+                oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
             }
         out.p += 4 * out.step;
         if constexpr (HOLD) {
-            hold_rows<DT, true>(o, h.mine - i0, s.live, s.at, lay.team, a.form, to);
+            hold_rows<DT, VEC>(o, h.mine - i0, s.live, s.at, lay.team, a.form, to);
             to.advance(4);
         }
     }
@@ -209,24 +219,24 @@ __global__ void __launch_bounds__(kHeldThreads)
 // The gradient.  dz is formed twice rather than held in fp32: the second time
 // costs a few instructions an element, the room would halve the rows that a
 // CTA holds.
-template <int DT, bool BY_OCT, bool HELD>
+template <int DT, bool VEC, bool BY_OCT, bool HELD>
 __global__ void __launch_bounds__(kHeldThreads)
     norm_held_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias,
                           const float* mean, const float* rstd, void* dx, float* chan)
 {
     extern __shared__ float4 shared4[];
     const NormLayout& lay = a.lay;
-    NormPlace s = norm_place<true>(a);
+    NormPlace s = norm_place<VEC>(a);
     const HeldPlace h = held_place(a, s);
     const int mine = s.live ? h.mine : 0, threads = static_cast<int>(blockDim.x);
     const int width = s.at.cols, stride = slot_stride(width), items = lay.samples * s.groups;
     // dy's octs; x's, or the checkpoint's numbers and scales
-    const Slots<DT> rows(reinterpret_cast<char*>(shared4));
-    char* second = reinterpret_cast<char*>(shared4 + Slots<DT>::kVecs * lay.lane_rows * threads);
-    const Slots<DT> xs(second);
+    const Slots<DT, VEC> rows(reinterpret_cast<char*>(shared4));
+    char* second = reinterpret_cast<char*>(shared4 + Slots<DT, VEC>::kVecs * lay.lane_rows * threads);
+    const Slots<DT, VEC> xs(second);
     const uint32_t qs = smem_addr(second) + threadIdx.x * 8;
     const uint32_t scales = smem_addr(second) + lay.lane_rows * threads * 8 + threadIdx.x * 4;
-    const size_t bytes = size_t(lay.lane_rows) * threads * (HELD ? 12 : 16 * Slots<DT>::kVecs);
+    const size_t bytes = size_t(lay.lane_rows) * threads * (HELD ? 12 : 16 * Slots<DT, VEC>::kVecs);
     float2* sums = reinterpret_cast<float2*>(second + bytes);   // [samples][groups]: S1, S2 of the part
     float2* stats = sums + items;                    // [samples][groups]: (mean, rstd), then -S1 / M, -S2 / M
     float2* work = stats + items;                    // [threads]
@@ -234,33 +244,41 @@ __global__ void __launch_bounds__(kHeldThreads)
     float2* slots = columns + lay.samples * width;   // [P][stride]; then [ranks][items]
     let_next_start();
     const int each = rows_to_group(lay);
+    const GradWalk<DT, VEC, HELD> walk_rows(a, s, dy, x, h.row0 + h.lane, lay.lanes);
     {
-        GradWalk<DT, true, HELD> w(a, s, dy, x, h.row0 + h.lane, lay.lanes);
+        GradWalk<DT, VEC, HELD> w = walk_rows;
         for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
             for (int i = i0; i < min(i0 + each, mine); ++i) {
-                rows.ask(i, w.dy.p);
-                if constexpr (HELD) {
+                rows.ask(i, w.dy.p, s.at);
+                if constexpr (HELD && VEC) {
                     cp_async(qs + i * threads * 8, w.q, 8, 8);
                     cp_async(scales + i * threads * 4, w.scale, 4, 4);
+                } else if constexpr (HELD) {
+                    const Held q = held_load<false>(w.q, s.at);
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qs + i * threads * 8), "r"(q.w[0]), "r"(q.w[1])
+                                 : "memory");
                 } else {
-                    xs.ask(i, w.x.p);
+                    xs.ask(i, w.x.p, s.at);
                 }
                 w.advance(1);
             }
             cp_async_commit();
         }
     }
-    auto take = [&](int i, GradRow<DT, true, HELD>& g) {
+    auto take = [&](int i, GradRow<DT, VEC, HELD>& g) {
         g.dy = rows.take(i);
         if constexpr (HELD) {
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(g.q.w[0]), "=r"(g.q.w[1]) : "r"(qs + i * threads * 8));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scales + i * threads * 4));
+            if constexpr (VEC)
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scales + i * threads * 4));
+            else
+                g.load_scales(a, s, walk_rows, i);   // one to a channel: again from L1 or L2
         } else {
             g.x = xs.take(i);
         }
     };
     Chan<BY_OCT> k;
-    k.template params<DT, true>(a, s, weight, bias);
+    k.template params<DT, VEC>(a, s, weight, bias);
     for (int i = threadIdx.x; i < items; i += threads) {
         const int q = lay.samples == 1 ? 0 : i / s.groups;
         const int64_t sample = h.tile * lay.samples + q;
@@ -278,7 +296,7 @@ __global__ void __launch_bounds__(kHeldThreads)
         cp_async_wait(--pending);
 #pragma unroll 2
         for (int i = i0; i < min(i0 + each, mine); ++i) {
-            GradRow<DT, true, HELD> g;
+            GradRow<DT, VEC, HELD> g;
             float2 fd[4], hat[4], dz[4];
             take(i, g);
             oct_floats(g.dy, fd);
@@ -327,14 +345,14 @@ __global__ void __launch_bounds__(kHeldThreads)
     WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
 #pragma unroll 2
     for (int i = 0; i < mine; ++i) {
-        GradRow<DT, true, HELD> g;
+        GradRow<DT, VEC, HELD> g;
         float2 fd[4], hat[4], dz[4], res[4];
         take(i, g);
         oct_floats(g.dy, fd);
         g.hats(a, k, hat);
         k.slopes(a, fd, hat, dz);
         grad.of(dz, hat, res);
-        oct_store<DT, true>(to.p, s.at, oct_round<DT>(res));
+        oct_store<DT, VEC>(to.p, s.at, oct_round<DT>(res));
         to.p += to.step;
     }
     if (lay.ranks > 1)
@@ -342,20 +360,6 @@ __global__ void __launch_bounds__(kHeldThreads)
 }
 
 }  // namespace
-
-#define TSX_BY_HELD(dtype, by_oct, CALL)                            \
-    do {                                                            \
-        if ((dtype) == TSX_F16) {                                   \
-            if (by_oct) { CALL(TSX_F16, true); }                    \
-            else { CALL(TSX_F16, false); }                          \
-        } else if ((dtype) == TSX_BF16) {                           \
-            if (by_oct) { CALL(TSX_BF16, true); }                   \
-            else { CALL(TSX_BF16, false); }                         \
-        } else {                                                    \
-            if (by_oct) { CALL(TSX_F32, true); }                    \
-            else { CALL(TSX_F32, false); }                          \
-        }                                                           \
-    } while (0)
 
 size_t held_bytes(const NormLayout& lay, int es, bool backward, bool held)
 {
@@ -379,12 +383,12 @@ cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const 
     const dim3 grid(unsigned((a.n + lay.samples - 1) / lay.samples * lay.ranks), unsigned(lay.runs));
     const size_t smem = held_bytes(lay, elem_size(dtype), false, false);
     cudaError_t e = cudaSuccess;
-#define CALL(DT, BY_OCT)                                                                                            \
-    e = held.q ? launch_grid<norm_held_kernel<DT, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, \
+#define CALL(DT, VEC, BY_OCT)                                                                                            \
+    e = held.q ? launch_grid<norm_held_kernel<DT, VEC, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, \
                              a, x, weight, bias, y, mean, rstd, held)                                               \
-               : launch_grid<norm_held_kernel<DT, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, \
+               : launch_grid<norm_held_kernel<DT, VEC, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, \
                              st, a, x, weight, bias, y, mean, rstd, held)
-    TSX_BY_HELD(dtype, lay.oct_in_group, CALL);
+    TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
     return e;
 }
@@ -398,12 +402,12 @@ cudaError_t launch_norm_held_backward(int dtype, const NormArgs& a, const void* 
     const dim3 grid(unsigned(slices), unsigned(lay.runs));
     const size_t smem = held_bytes(lay, elem_size(dtype), true, x.q != nullptr);
     cudaError_t e = cudaSuccess;
-#define CALL(DT, BY_OCT)                                                                                           \
-    e = x.q ? launch_grid<norm_held_grad_kernel<DT, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
+#define CALL(DT, VEC, BY_OCT)                                                                                           \
+    e = x.q ? launch_grid<norm_held_grad_kernel<DT, VEC, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, dx, scratch.chan)                                           \
-            : launch_grid<norm_held_grad_kernel<DT, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
+            : launch_grid<norm_held_grad_kernel<DT, VEC, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
                           x, weight, bias, mean, rstd, dx, scratch.chan)
-    TSX_BY_HELD(dtype, lay.oct_in_group, CALL);
+    TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
     if (e != cudaSuccess)
         return e;

@@ -393,10 +393,10 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
 bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
 {
     const int64_t per = d.c / d.groups;
-    if (!vec || per > kNormRun)
+    if (per > kNormRun)
         return false;
     const int es = elem_size(d.dtype);
-    const int64_t align = block ? block : kOct;
+    const int64_t align = block ? block : vec ? kOct : 1;
     const int64_t unit = align / std::gcd(per, align);
     int64_t best = 0;   // CTAs of the layout found
     for (int64_t groups = d.c <= kNormRun ? d.groups : kNormRun / per / unit * unit; groups > 0;) {
@@ -404,25 +404,29 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             for (int ranks = 1; ranks <= kNormRanks; ranks *= 2) {
                 NormLayout lay{};
                 lay.kind = kNormHeld;
-                lay.vec = true;
-                lay.oct_in_group = per % kOct == 0;
+                lay.vec = vec;
+                lay.oct_in_group = vec && per % kOct == 0;
                 lay.run_groups = int(groups);
                 lay.run_cols = int(groups * per);
                 lay.pieces = 1;
                 lay.runs = int((d.groups + groups - 1) / groups);
-                lay.team = team_of(lay.run_cols, block, true);
+                lay.team = team_of(lay.run_cols, block, vec);
                 lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
                 const int64_t lanes = threads / lay.V;
+                if (lanes == 0)
+                    continue;
                 lay.ranks = ranks;
                 lay.range = (d.l + ranks - 1) / ranks;   // the last ranks may have no rows
                 lay.splits = 1;
-                // row lanes: as many as there are rows; several samples side
-                // by side where there are CTAs enough
+                // row lanes: as many as there are rows, or fewer, of eight rows
+                // each, with several samples side by side while there are
+                // CTAs enough
                 int64_t own = lay.range < lanes ? lay.range : lanes, samples = 1;
-                if (ranks == 1 && own < lanes) {
-                    const int64_t most = d.n * lay.runs / kHeldCtas;
-                    samples = lanes / own < most ? lanes / own : most;
+                if (ranks == 1) {
+                    const int64_t few = (lay.range + 7) / 8, most = d.n * lay.runs / kHeldCtas;
+                    samples = lanes / few < most ? lanes / few : most;
                     samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
+                    own = lanes / samples < own ? lanes / samples : own;
                 }
                 lay.samples = int(samples);
                 lay.lanes = int(own);

@@ -708,17 +708,22 @@ struct GradRow {
         dy = oct_load<DT, VEC>(w.dy.p + i * w.dy.step, s.at);
         if constexpr (HELD) {
             q = held_load<VEC>(w.q + i * w.q_step, s.at);
-            if constexpr (VEC) {
-                scale[0] = __ldg(w.scale + i * w.scale_step);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int ch = s.at.ch + j * s.at.step;
-                    scale[j] = ch < s.at.cols ? __ldg(w.scale + i * w.scale_step + (s.ch0 + ch) / a.block) : 0.f;
-                }
-            }
+            load_scales(a, s, w, i);
         } else {
             x = oct_load<DT, VEC>(w.x.p + i * w.x.step, s.at);
+        }
+    }
+    __device__ __forceinline__ void load_scales(const NormArgs& a, const NormPlace& s,
+                                                const GradWalk<DT, VEC, HELD>& w, int i)
+    {
+        if constexpr (VEC) {
+            scale[0] = __ldg(w.scale + i * w.scale_step);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int ch = s.at.ch + j * s.at.step;
+                scale[j] = ch < s.at.cols ? __ldg(w.scale + i * w.scale_step + (s.ch0 + ch) / a.block) : 0.f;
+            }
         }
     }
     // xhat = x rstd + off; of a checkpoint q (scale rstd) + off
