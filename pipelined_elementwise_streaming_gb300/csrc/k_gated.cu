@@ -21,6 +21,8 @@ using namespace dev;
 // and of two or three.
 constexpr int kRowsAtOnce = 4;
 constexpr int kGatedRows = 2;
+template <int DT>
+TSX_HD constexpr int pack_rows() { return DT == TSX_F32 ? 4 : 8; }
 
 struct Place {
     OctAt at;
@@ -82,11 +84,18 @@ __device__ __forceinline__ void load_held(const Place& s, const void* q, const f
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kLayerThreads) pack_kernel(PackArgs a, const void* x, HeldOut held)
 {
-    const Place s = place<VEC, kRowsAtOnce>(a.lay);
-    Oct<DT> o[kRowsAtOnce];
+    constexpr int N = pack_rows<DT>();
+    const Place s = place<VEC, N>(a.lay);
+    Oct<DT> o[N];
     load_rows<DT, VEC>(s, x, a.pitch, a.lay.P, o);
-    hold_rows<DT, VEC>(o, s.rows, s.live, s.at, a.lay.team, a.form,
-                       HeldPtr(held, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block));
+    HeldPtr to(held, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block);
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const Oct<DT> four[4] = {o[i], o[i + 1], o[i + 2], o[i + 3]};
+        if (i < s.rows)
+            hold_rows<DT, VEC>(four, s.rows - i, s.live, s.at, a.lay.team, a.form, to);
+        to.advance(4);
+    }
 }
 
 template <int DT, bool VEC>
@@ -210,7 +219,7 @@ dim3 grid_of(const RowLayout& lay, int rows_at_once)
 
 cudaError_t launch_pack(int dtype, const PackArgs& a, const void* x, HeldOut held, cudaStream_t st)
 {
-    const dim3 grid = grid_of(a.lay, kRowsAtOnce);
+    const dim3 grid = grid_of(a.lay, dtype == TSX_F32 ? pack_rows<TSX_F32>() : pack_rows<TSX_BF16>());
 #define CALL(DT, VEC) pack_kernel<DT, VEC><<<grid, a.lay.threads, 0, st>>>(a, x, held)
     TSX_BY_TYPE(dtype, a.lay.vec, CALL);
 #undef CALL

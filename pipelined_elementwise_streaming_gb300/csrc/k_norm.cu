@@ -11,15 +11,17 @@ namespace {
 
 using namespace dev;
 
-// Rows whose loads a thread issues before it uses the first.
-constexpr int kApplyRows = 4;
-constexpr int kGradRows = 2;   // element by element
-template <int DT>
-TSX_HD constexpr int stats_rows() { return DT == TSX_F32 ? 4 : 8; }
+constexpr int kGradRows = 2;   // rows that a thread loads at once where they go element by element
 
 // CTAs to an SM that the registers are cut for.
-constexpr int kForwardCtas = 3;
+template <int DT>
+TSX_HD constexpr int forward_ctas() { return DT == TSX_F32 ? 2 : 3; }
 constexpr int kBackwardCtas = 2;
+
+__device__ __forceinline__ char* next_16(float2* p)
+{
+    return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15));
+}
 
 // A CTA's range of rows: blockIdx.x counts ranges sample by sample.  The
 // `ranks` CTAs of a cluster take neighbouring ranges and join their sums.
@@ -56,7 +58,7 @@ __device__ __forceinline__ float2* part_of(const NormArgs& a, const NormPlace& s
 
 // First kernel: (mean, M2) of every cluster's range, run and group.
 template <int DT, bool VEC, bool BY_OCT>
-__global__ void __launch_bounds__(kNormThreads, kForwardCtas) norm_stats_kernel(NormArgs a, const void* x, float2* part)
+__global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>()) norm_stats_kernel(NormArgs a, const void* x, float2* part)
 {
     extern __shared__ float4 shared4[];
     const NormPlace s = norm_place<VEC>(a);
@@ -71,14 +73,11 @@ __global__ void __launch_bounds__(kNormThreads, kForwardCtas) norm_stats_kernel(
         cluster_arrive();   // waited for before anything is put into another CTA
     Triples<BY_OCT> t;
     t.clear();
-    constexpr int N = stats_rows<DT>();
-    Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
-    for (int left = s.live ? r.mine : 0; left > 0; left -= N) {
-        Oct<DT> o[N];
-        load_rows<DT, VEC>(w, s.at, left, o);
-        t.add_octs(o, left);
-        w.p += N * w.step;
-    }
+    each_four<DT, VEC>(walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s), s.at, next_16(slots + P * stride), r.mine, r.mine, s.live,
+                       [] {}, [&](const Oct<DT>(&o)[4], int n) {
+                           if (s.live)
+                               t.add_octs(o, n);
+                       });
     if (s.live)
         t.leave(s.at, slots + s.p * stride);
     __syncthreads();
@@ -154,7 +153,7 @@ __device__ __forceinline__ void join_parts(const NormArgs& a, const NormPlace& s
 
 // Second kernel: y, and with HOLD the checkpoint of x.
 template <int DT, bool VEC, bool BY_OCT, bool HOLD>
-__global__ void __launch_bounds__(kNormThreads, kForwardCtas)
+__global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
     norm_apply_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                       float* rstd, HeldOut held, const float2* part)
 {
@@ -165,39 +164,36 @@ __global__ void __launch_bounds__(kNormThreads, kForwardCtas)
     Affine k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
-    Walk w = walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s);
-    Oct<DT> o[kApplyRows];
-    load_rows<DT, VEC>(w, s.at, s.live ? r.mine : 0, o);   // the first rows, before the sums are there
-    wait_for_last();
-    join_parts(a, s, r.sample, part, stats, work);
-    k.template statistics<BY_OCT>(a, s, stats);
-    if (r.split == 0 && s.piece == 0)
-        for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
-            mean[r.sample * a.groups + s.group0 + g] = stats[g].x;
-            rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
-        }
     WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
     HeldPtr to;
     if constexpr (HOLD)
         to = HeldPtr(held, r.row0 + s.p, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
-    // a team's threads share their rows, so they come to its shuffles together
-    for (int left = r.mine; left > 0; left -= kApplyRows) {
-#pragma unroll
-        for (int i = 0; i < kApplyRows; ++i)
-            if (s.live && i < left) {
-                float2 f[4], v[4];
-                oct_floats(o[i], f);
-                k.apply(a.act, f, v);
-                oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
+    auto begin = [&] {
+        wait_for_last();
+        join_parts(a, s, r.sample, part, stats, work);
+        k.template statistics<BY_OCT>(a, s, stats);
+        if (r.split == 0 && s.piece == 0)
+            for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
+                mean[r.sample * a.groups + s.group0 + g] = stats[g].x;
+                rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
             }
-        out.p += kApplyRows * out.step;
-        if constexpr (HOLD) {
-            hold_rows<DT, VEC>(o, left, s.live, s.at, a.lay.team, a.form, to);
-            to.advance(kApplyRows);
-        }
-        w.p += kApplyRows * w.step;
-        load_rows<DT, VEC>(w, s.at, s.live ? left - kApplyRows : 0, o);
-    }
+    };
+    each_four<DT, VEC>(walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s), s.at, next_16(stats + a.lay.run_groups), r.mine,
+                       r.mine, s.live, begin, [&](const Oct<DT>(&o)[4], int n) {
+#pragma unroll
+                           for (int i = 0; i < 4; ++i)
+                               if (s.live && i < n) {
+                                   float2 f[4], v[4];
+                                   oct_floats(o[i], f);
+                                   k.apply(a.act, f, v);
+                                   oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
+                               }
+                           out.p += 4 * out.step;
+                           if constexpr (HOLD) {
+                               hold_rows<DT, VEC>(o, n, s.live, s.at, a.lay.team, a.form, to);
+                               to.advance(4);
+                           }
+                       });
 }
 
 // ------------------------------------------------------------ backward
@@ -210,11 +206,6 @@ __device__ __forceinline__ void load_stats(const NormArgs& a, const NormPlace& s
         stats[g] = make_float2(mean[at], rstd[at]);
     }
     __syncthreads();
-}
-
-__device__ __forceinline__ char* next_16(float2* p)
-{
-    return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15));
 }
 
 // use(row) for each of a thread's `rows` rows, through the queue where they are
@@ -467,6 +458,13 @@ size_t queue_bytes(int dtype, const NormLayout& lay, bool held)
     return 16 + size_t(kNormThreads) * rows * row;   // after the next multiple of 16
 }
 
+size_t row_queue_bytes(int dtype, const NormLayout& lay)
+{
+    if (!lay.vec)
+        return 0;
+    return 16 + (dtype == TSX_F32 ? RowQueue<TSX_F32>::kBytes : RowQueue<TSX_BF16>::kBytes);
+}
+
 size_t rank_sums(const NormLayout& lay) { return size_t(lay.run_groups) * (lay.ranks > 1 ? lay.ranks + 1 : 1); }
 
 }  // namespace
@@ -478,9 +476,9 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
     const int width = lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
     const size_t slots = kNormThreads / 32 * sizeof(float4) +
-                         (rank_sums(lay) + size_t(lay.P) * slot_stride(width)) * sizeof(float2);
+                         (rank_sums(lay) + size_t(lay.P) * slot_stride(width)) * sizeof(float2) + row_queue_bytes(dtype, lay);
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
-    const size_t stats = items * sizeof(float4) + lay.run_groups * sizeof(float2);
+    const size_t stats = items * sizeof(float4) + lay.run_groups * sizeof(float2) + row_queue_bytes(dtype, lay);
     cudaError_t e = cudaSuccess;
 #define CALL(DT, VEC, BY_OCT) \
     e = launch_grid<norm_stats_kernel<DT, VEC, BY_OCT>>(grid, lay.threads, slots, lay.ranks, false, st, a, x, \

@@ -11,8 +11,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kTokenRows = 4;       // rows whose loads a thread issues before it uses the first
-constexpr int kTokenGradRows = 2;   // two operands a row
+constexpr int kTokenGradRows = 2;   // rows whose loads a thread issues before it uses the first
 
 // How many of a thread's next N rows, P apart, exist with `left` rows to go.
 template <int N>
@@ -55,26 +54,30 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
     const int group = s.group0 + local_group(a, s.at.ch);
     const bool first = s.at.ch % a.per_group == 0;
     const int P = a.lay.P;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (P * kTokenRows);
     const int step_s = P * a.groups;
-    // rows of the thread: first + i * P for i < 4, then a stride further on
-    const Walk w = walk<DT>(x, 0, P, a.x_pitch, s);
-    const WalkOut to = walk_out<DT>(y, 0, P, a.y_pitch, s);
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenRows); base < a.n; base += stride) {
-        const int64_t row0 = base + s.p;
-        const int n = s.p < P ? rows_at<kTokenRows>(a.n - row0, P) : 0;
-        Oct<DT> o[kTokenRows];
-        load_rows<DT, true>(Walk{w.p + row0 * a.x_pitch * elem_size(DT), w.step}, s.at, s.live ? n : 0, o);
-        float mu[kTokenRows], dev[kTokenRows];
+    // the CTA's rows: P side by side from a contiguous share of all rows
+    const int64_t share = a.lay.range, first_row = static_cast<int64_t>(blockIdx.x) * share;
+    const int rows = static_cast<int>(min(share, a.n - first_row));
+    const int mine = s.p < P && s.p < rows ? (rows - s.p + P - 1) / P : 0;
+    const int64_t row0 = first_row + s.p;
+    const WalkOut to = walk_out<DT>(y, row0, P, a.y_pitch, s);
+    char* out = to.p;
+    float* pm = mean + row0 * a.groups + group;
+    float* pr = rstd + row0 * a.groups + group;
+    HeldPtr hp;
+    if constexpr (HOLD)
+        hp = HeldPtr(held, row0, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
+    auto use = [&](const Oct<DT>(&o)[4], int n) {
+        float mu[4], dev[4];
 #pragma unroll
-        for (int i = 0; i < kTokenRows; ++i) {
+        for (int i = 0; i < 4; ++i) {
             float2 f[4];
             oct_floats(o[i], f);
             mu[i] = oct_sum(f);
         }
         team_sums(mu, lanes);
 #pragma unroll
-        for (int i = 0; i < kTokenRows; ++i) {
+        for (int i = 0; i < 4; ++i) {
             float2 f[4], sq = make_float2(0.f, 0.f);
             oct_floats(o[i], f);
             mu[i] *= inv_m;
@@ -86,11 +89,8 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
             dev[i] = sq.x + sq.y;
         }
         team_sums(dev, lanes);
-        char* out = to.p + row0 * a.y_pitch * elem_size(DT);
-        float* pm = mean + row0 * a.groups + group;
-        float* pr = rstd + row0 * a.groups + group;
 #pragma unroll
-        for (int i = 0; i < kTokenRows; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float rs = rstd_of(dev[i], inv_m, a.eps);
             if (s.live && i < n) {
                 float2 f[4], v[4];
@@ -106,10 +106,18 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
                 }
             }
         }
-        if constexpr (HOLD)
-            hold_rows<DT, true>(o, n, s.live, s.at, a.lay.team, a.form,
-                                HeldPtr(held, row0, P, a.c, a.blocks, s.ch0 + s.at.ch, a.block));
-    }
+        out += 4 * to.step;
+        pm += 4 * step_s;
+        pr += 4 * step_s;
+        if constexpr (HOLD) {
+            hold_rows<DT, true>(o, n, s.live, s.at, a.lay.team, a.form, hp);
+            hp.advance(4);
+        }
+    };
+    // every lane of a warp comes to the shuffles
+    extern __shared__ float4 queue[];
+    each_four<DT, true>(walk<DT>(x, row0, P, a.x_pitch, s), s.at, reinterpret_cast<char*>(queue), (rows + P - 1) / P,
+                        mine, s.live, [] {}, use);
 }
 
 template <int DT, bool HELD>
@@ -206,16 +214,17 @@ cudaError_t launch_norm_token(int dtype, const NormArgs& a, const void* x, const
                               void* y, float* mean, float* rstd, HeldOut held, cudaStream_t st)
 {
     const dim3 grid(unsigned(a.lay.splits), unsigned(a.lay.runs));
-#define CALL(DT)                                                                                                  \
-    if (held.q)                                                                                                   \
-        norm_token_kernel<DT, true><<<grid, a.lay.threads, 0, st>>>(a, x, weight, bias, y, mean, rstd, held);     \
-    else                                                                                                          \
-        norm_token_kernel<DT, false><<<grid, a.lay.threads, 0, st>>>(a, x, weight, bias, y, mean, rstd, held)
+    cudaError_t e = cudaSuccess;
+#define CALL(DT)                                                                                                     \
+    e = held.q ? launch_grid<norm_token_kernel<DT, true>>(grid, a.lay.threads, RowQueue<DT>::kBytes, 1, false, st,   \
+                                                          a, x, weight, bias, y, mean, rstd, held)                   \
+               : launch_grid<norm_token_kernel<DT, false>>(grid, a.lay.threads, RowQueue<DT>::kBytes, 1, false, st,  \
+                                                           a, x, weight, bias, y, mean, rstd, held)
     if (dtype == TSX_F16) { CALL(TSX_F16); }
     else if (dtype == TSX_BF16) { CALL(TSX_BF16); }
     else { CALL(TSX_F32); }
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_norm_token_backward(int dtype, const NormArgs& a, const void* dy, Saved x, const void* weight,

@@ -269,9 +269,9 @@ constexpr int64_t kHeldRows = 64;         // rows to a lane at most
 // CTAs of clusters of eight that the SMs hold with one CTA to an SM
 constexpr int64_t kHeldWave = 144;
 // Ranges are cut so that at most this many CTAs share the work: as many as the
-// 152 SMs hold at once, three each forward and two backward.  A constant of the
-// chip, not read from it, so that results depend on the shape alone.
-constexpr int64_t kNormCtas = 3 * 152, kNormGradCtas = 2 * 152;
+// 152 SMs hold at once, two each backward and for fp32, else three.  A constant
+// of the chip, not read from it, so that results depend on the shape alone.
+constexpr int64_t kNormThrees = 3 * 152, kNormPairs = 2 * 152;
 constexpr int64_t kNormWide = 640;
 constexpr int64_t kNormParts = 160;   // parts of a sample that the second kernel's CTAs join by themselves
 constexpr int kNormRowsAtOnce = 4;
@@ -335,7 +335,7 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
     p = p < 1 ? 1 : p > d.l ? d.l : p;
     lay.P = int(p);
     lay.threads = round_up(lay.P * lay.V, 32);
-    const int64_t ctas = (backward ? kNormGradCtas : kNormCtas) / (d.n * lay.runs);
+    const int64_t ctas = (backward || d.dtype == TSX_F32 ? kNormPairs : kNormThrees) / (d.n * lay.runs);
     const int64_t most = (d.l + p * kNormRowsAtOnce - 1) / (p * kNormRowsAtOnce);
     int64_t splits = ctas < 1 ? 1 : ctas < most ? ctas : most;
     // many ranges: clusters join eight each, so that few parts are left.  The SMs hold fewer CTAs in clusters of eight (408 of 456, 288 of
@@ -374,12 +374,14 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     p = p < 1 ? 1 : p > d.n ? d.n : p;
     lay.P = int(p);
     lay.threads = round_up(lay.P * lay.V, 32);
-    lay.range = 1;
     lay.ranks = lay.samples = lay.lanes = 1;
     const int64_t at_once = p * (backward ? 2 : 4);
     const int64_t most = (d.n + at_once - 1) / at_once;
     const int64_t want = (backward ? kTokenGradCtas : kTokenCtas) / lay.runs;
     lay.splits = most < want ? most : want < 1 ? 1 : want;
+    lay.range = (d.n + lay.splits - 1) / lay.splits;   // forward: rows to a CTA
+    if (!backward)
+        lay.splits = (d.n + lay.range - 1) / lay.range;
     *out = lay;
     return true;
 }

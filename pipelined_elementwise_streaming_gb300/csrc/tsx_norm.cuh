@@ -748,13 +748,103 @@ struct GradRow {
     }
 };
 
-// The backward pass's rows on their way: a queue in shared memory that each
-// thread fills by cp.async for itself alone, so that no barrier guards it and
-// the bytes in flight do not depend on registers.  The streaming kernels hold
-// dz's sums, weights and statistics in over 50 registers; with four rows in
-// registers beside them, 57 KB an SM were on their way in bursts (sums of
-// bf16 [4, 16384, 512] from int8: 34 us), with a queue of eight rows twice
-// that without a pause.
+// Rows of x on their way: a queue in shared memory that each thread fills by
+// cp.async for itself alone, so that no barrier guards it and the bytes in
+// flight do not depend on registers.  Four rows to a batch; kBatches batches
+// are on their way at any time.
+template <int DT>
+struct RowQueue {
+    static constexpr int kBatch = 4, kBatches = DT == TSX_F32 ? 2 : 3, kRows = kBatch * kBatches;
+    static constexpr uint32_t kVecs = elem_size(DT) / 2;   // 16-byte vectors of an oct
+    static constexpr uint32_t kStep = kNormThreads * 16;
+    static constexpr size_t kBytes = size_t(kRows) * kVecs * kStep;
+    Walk w;
+    uint32_t at;   // this thread's first slot
+    int left;      // rows that are still to be asked for
+    __device__ __forceinline__ RowQueue(const Walk& walk, char* shared, int rows)
+        : w(walk), at(smem_addr(shared) + threadIdx.x * 16), left(rows)
+    {
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b)
+            ask(b);
+    }
+    // The walk's next rows, into the slots of batch b.
+    __device__ __forceinline__ void ask(int b)
+    {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i < left) {
+#pragma unroll
+                for (uint32_t h = 0; h < kVecs; ++h)
+                    cp_async(at + ((b * kBatch + i) * kVecs + h) * kStep, w.p + i * w.step + 16 * h, 16, 16);
+            }
+        cp_async_commit();
+        w.p += kBatch * w.step;
+        left -= kBatch;
+    }
+    // The rows of batch b, the oldest, of which n exist; others are zeros.
+    __device__ __forceinline__ void take(int b, int n, Oct<DT> (&o)[kBatch]) const
+    {
+        cp_async_wait(kBatches - 1);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i < n) {
+#pragma unroll
+                for (uint32_t h = 0; h < kVecs; ++h)
+                    lds16(at + ((b * kBatch + i) * kVecs + h) * kStep, o[i].w + 4 * h);
+            } else {
+                oct_zero(o[i]);
+            }
+    }
+    static __device__ __forceinline__ void lds16(uint32_t at, uint32_t* w)
+    {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at));
+    }
+};
+
+// use(o, n) for a thread's rows, four octs o at a time, of which n exist,
+// through the queue where they are vectors.  `loop` rows are gone through, of
+// which the thread's row lane has `count` (n is below zero past them): lanes
+// that meet in shuffles come with the same `loop`.  `live` threads have
+// channels; the others' octs are zeros.  begin() runs once the first rows are
+// on their way.
+template <int DT, bool VEC, class Begin, class Use>
+__device__ __forceinline__ void each_four(Walk w, const OctAt& at, char* queue, int loop, int count, bool live,
+                                          Begin begin, Use use)
+{
+    if constexpr (VEC) {
+        RowQueue<DT> q(w, queue, live ? count : 0);
+        begin();
+        for (int done = 0; done < loop; done += q.kRows)
+#pragma unroll
+            for (int b = 0; b < q.kBatches; ++b) {
+                const int i = done + b * q.kBatch;
+                if (i < loop) {
+                    Oct<DT> o[4];
+                    q.take(b, live ? count - i : 0, o);
+                    use(o, count - i);
+                    q.ask(b);
+                }
+            }
+        cp_async_wait(0);
+    } else {
+        begin();
+        for (int i = 0; i < loop; i += 4) {
+            Oct<DT> o[4];
+            load_rows<DT, VEC>(w, at, live ? count - i : 0, o);
+            w.p += 4 * w.step;
+            use(o, count - i);
+        }
+    }
+}
+
+// The backward pass's rows on their way, dy and x or its checkpoint, the same
+// way.  The streaming kernels hold dz's sums, weights and statistics in over 50
+// registers; with four rows in registers beside them, 57 KB an SM were on their
+// way in bursts (sums of bf16 [4, 16384, 512] from int8: 34 us), with a queue
+// of eight rows twice that without a pause (31 us).
 constexpr int kQueueBatch = 2;   // rows to a cp.async group
 template <int DT>
 TSX_HD constexpr int queue_rows() { return DT == TSX_F32 ? 4 : 8; }

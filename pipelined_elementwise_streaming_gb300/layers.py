@@ -144,7 +144,7 @@ class _Layer:
         if pitch == self.cols:
             return self._new(self._shape, dtype=self._torch_dtype, device=device)
         wide = self._new((*self._shape[:-1], pitch), dtype=self._torch_dtype, device=device)
-        return wide[..., : self.cols]
+        return wide.as_strided(self._shape, wide.stride())
 
     def _new_checkpoint(self, device) -> Checkpoint:
         return Checkpoint(self._new(self._q_shape, dtype=self._q_dtype, device=device),
@@ -292,7 +292,6 @@ class GroupNorm(_Layer):
         self._shape = (self.n, self.l, self.cols)
         self._x, self._y = self._strides_of(self.x_pitch), self._strides_of(self.y_pitch)
         self._channels, self._stats = (self.cols,), (self.n, self.groups)
-        self._two_stats = (2, self.n, self.groups)
         self._desc = tsx_norm_desc(self._dtype_code, _named(DTYPES, param_dtype, "param_dtype"),
                                    _named(ACTS, act, "activation"), self.groups, self._form_code, self.block, self.n,
                                    self.l, self.cols, self.x_pitch, self.y_pitch, eps)
@@ -322,7 +321,7 @@ class GroupNorm(_Layer):
         else:
             py = self._ptr(out, self._y, "out", dev)
         new, device = self._new, x.device
-        mean, rstd = new(self._two_stats, dtype=f32, device=device).unbind()
+        mean, rstd = new(self._stats, dtype=f32, device=device), new(self._stats, dtype=f32, device=device)
         if checkpoint:
             saved = self._new_checkpoint(device)
             pq, ps = saved.q.data_ptr(), saved.scale.data_ptr()
@@ -357,7 +356,7 @@ class GroupNorm(_Layer):
         else:
             pdx = self._ptr(out, self._x, "out", dev)
         new, device = self._new, dy.device
-        dweight, dbias = new((2, self.cols), dtype=f32, device=device).unbind()
+        dweight, dbias = new(self._channels, dtype=f32, device=device), new(self._channels, dtype=f32, device=device)
         size = self._scratch[1][not (pdy | pdx | (src[0] or src[1] or 0)) & 15]
         scratch = new((size,), dtype=self._byte, device=device)
         rc = tsx_group_norm_backward(self._ref, pdy, *src, pw, pb, pm, pr, pdx, dweight.data_ptr(), dbias.data_ptr(),
