@@ -116,7 +116,7 @@ struct Slots {
 };
 
 template <int DT, bool VEC, bool BY_OCT, bool HOLD>
-__global__ void __launch_bounds__(kHeldThreads)
+__global__ void __launch_bounds__(kNormThreads, 2)
     norm_held_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                      float* rstd, HeldOut held)
 {
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kHeldThreads)
     const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
     const Slots<DT, VEC> rows(reinterpret_cast<char*>(shared4));
     float4* spare = shared4 + Slots<DT, VEC>::kVecs * lay.lane_rows * blockDim.x;   // [warps]
-    float2* sums = reinterpret_cast<float2*>(spare + kHeldThreads / 32);       // [samples][groups]: (mean, M2) of the part
+    float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);       // [samples][groups]: (mean, M2) of the part
     float2* stats = sums + items;                                              // [samples][groups]: (mean, rstd)
     float2* slots = stats + items;                                             // [P][stride]; then [ranks][items]
     const int each = rows_to_group(lay);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kHeldThreads)
 // costs a few instructions an element, the room would halve the rows that a
 // CTA holds.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
-__global__ void __launch_bounds__(kHeldThreads)
+__global__ void __launch_bounds__(kNormThreads, 2)
     norm_held_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias,
                           const float* mean, const float* rstd, void* dx, float* chan)
 {
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kHeldThreads)
     float2* sums = reinterpret_cast<float2*>(second + bytes);   // [samples][groups]: S1, S2 of the part
     float2* stats = sums + items;                    // [samples][groups]: (mean, rstd), then -S1 / M, -S2 / M
     float2* work = stats + items;                    // [threads]
-    float2* columns = work + kHeldThreads;           // [samples][width]
+    float2* columns = work + kNormThreads;           // [samples][width]
     float2* slots = columns + lay.samples * width;   // [P][stride]; then [ranks][items]
     let_next_start();
     const int each = rows_to_group(lay);
@@ -371,8 +371,8 @@ size_t held_bytes(const NormLayout& lay, int es, bool backward, bool held)
         slots = size_t(lay.ranks) * items;   // the ranks' sums reuse them
     size_t pairs = 2 * items + slots;
     if (backward)
-        pairs += kHeldThreads + size_t(lay.samples) * width;
-    return octs * es * 8 + (backward ? octs * (held ? 12 : es * 8) : kHeldThreads / 32 * sizeof(float4)) +
+        pairs += kNormThreads + size_t(lay.samples) * width;
+    return octs * es * 8 + (backward ? octs * (held ? 12 : es * 8) : kNormThreads / 32 * sizeof(float4)) +
            pairs * sizeof(float2);
 }
 

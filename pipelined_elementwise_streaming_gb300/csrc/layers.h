@@ -90,7 +90,6 @@ struct NormLayout {
 // How a call runs: streaming kernels that read their operands twice (any
 // layout), samples held on chip, tokens whose groups lie within a warp.
 enum NormKind { kNormStream = 0, kNormHeld = 1, kNormToken = 2 };
-constexpr int kHeldThreads = 512;   // most threads of the kernels that hold samples on chip
 
 struct NormArgs {
     NormLayout lay;

@@ -265,9 +265,9 @@ constexpr int64_t kTokenCtas = 3 * 152, kTokenGradCtas = 2 * 152;
 constexpr int64_t kNormRanks = 8;      // CTAs of a cluster at most
 constexpr int64_t kNormSamples = 64;   // samples side by side at most
 constexpr int64_t kHeldCtas = 2 * 152;    // CTAs to keep before samples are put side by side
+constexpr int64_t kHeldFew = 16384;       // elements to a CTA where there are fewer CTAs than half the SMs
 constexpr int64_t kHeldRows = 64;         // rows to a lane at most
-// CTAs of clusters of eight that the SMs hold with one CTA to an SM
-constexpr int64_t kHeldWave = 144;
+constexpr int64_t kHeldWave = 256;        // CTAs of clusters of eight that the SMs hold at once, two each
 // Ranges are cut so that at most this many CTAs share the work: as many as the
 // 152 SMs hold at once, two each backward and for fp32, else three.  A constant
 // of the chip, not read from it, so that results depend on the shape alone.
@@ -386,12 +386,12 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     return true;
 }
 
-// Samples on chip.  CTAs of 512 threads have an SM to themselves, CTAs of 256
-// share it in twos.  A sample of several CTAs (a cluster) is held only if all
-// samples fit on the chip at once: the chain from the loads over the cluster's
-// barrier to the stores is then gone through once, in less time than the
-// streaming kernels' two launches, and beyond that it is not (measured: see
-// k_norm_held.cu).  Samples of one CTA are held however many there are.
+// Samples on chip.  Two CTAs share an SM.  A sample of several CTAs (a cluster)
+// is held only if all samples fit on the chip at once: the chain from the loads
+// over the cluster's barrier to the stores is then gone through once, in less
+// time than the streaming kernels' two launches, and beyond that it is not
+// (measured: see k_norm_held.cu).  Samples of one CTA are held however many
+// there are.
 bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
 {
     const int64_t per = d.c / d.groups;
@@ -402,63 +402,67 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
     const int64_t unit = align / std::gcd(per, align);
     int64_t best = 0;   // CTAs of the layout found
     for (int64_t groups = d.c <= kNormRun ? d.groups : kNormRun / per / unit * unit; groups > 0;) {
-        for (int threads : {256, 512})
-            for (int ranks = 1; ranks <= kNormRanks; ranks *= 2) {
-                NormLayout lay{};
-                lay.kind = kNormHeld;
-                lay.vec = vec;
-                lay.oct_in_group = vec && per % kOct == 0;
-                lay.run_groups = int(groups);
-                lay.run_cols = int(groups * per);
-                lay.pieces = 1;
-                lay.runs = int((d.groups + groups - 1) / groups);
-                lay.team = team_of(lay.run_cols, block, vec);
-                lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
-                const int64_t lanes = threads / lay.V;
-                if (lanes == 0)
-                    continue;
-                lay.ranks = ranks;
-                lay.range = (d.l + ranks - 1) / ranks;   // the last ranks may have no rows
-                lay.splits = 1;
-                // row lanes: as many as there are rows, or fewer, of eight rows
-                // each, with several samples side by side while there are
-                // CTAs enough
-                int64_t own = lay.range < lanes ? lay.range : lanes, samples = 1;
-                if (ranks == 1) {
-                    const int64_t few = (lay.range + 7) / 8, most = d.n * lay.runs / kHeldCtas;
-                    samples = lanes / few < most ? lanes / few : most;
-                    samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
-                    own = lanes / samples < own ? lanes / samples : own;
-                }
-                lay.samples = int(samples);
-                lay.lanes = int(own);
-                lay.P = int(samples * own);
-                lay.threads = round_up(lay.P * lay.V, 32);
-                const int64_t lane_rows = (lay.range + own - 1) / own;
-                if (lane_rows > kHeldRows)
-                    continue;
-                lay.lane_rows = int(lane_rows);
-                const int64_t room = (threads == 512 ? kMaxDynSmem : (kSmemPerSm - 2 * kSmemPerCtaReserved) / 2);
-                if (int64_t(held_bytes(lay, es, backward, held)) > room)
-                    continue;
-                const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * ranks;
-                const int64_t wave = threads == 512 ? (ranks > 1 ? kHeldWave : 152) : (ranks > 1 ? 2 * kHeldWave : 304);
-                if ((ranks > 1 || threads == 512) && ctas > wave)
-                    continue;
-                // the most CTAs, and of those the widest runs and fewest ranks
-                if (ctas > best) {
-                    best = ctas;
-                    *out = lay;
-                }
-                if (ranks == 1 && ctas >= wave)
-                    return true;
+        for (int ranks = 1; ranks <= kNormRanks; ranks *= 2) {
+            NormLayout lay{};
+            lay.kind = kNormHeld;
+            lay.vec = vec;
+            lay.oct_in_group = vec && per % kOct == 0;
+            lay.run_groups = int(groups);
+            lay.run_cols = int(groups * per);
+            lay.pieces = 1;
+            lay.runs = int((d.groups + groups - 1) / groups);
+            lay.team = team_of(lay.run_cols, block, vec);
+            lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
+            const int64_t lanes = kNormThreads / lay.V;
+            if (lanes == 0)
+                continue;
+            lay.ranks = ranks;
+            lay.range = (d.l + ranks - 1) / ranks;   // the last ranks may have no rows
+            lay.splits = 1;
+            // row lanes: as many as there are rows, or fewer, of eight rows
+            // each, with several samples side by side while there are
+            // CTAs enough
+            int64_t own = lay.range < lanes ? lay.range : lanes, samples = 1;
+            if (ranks == 1) {
+                const int64_t few = (lay.range + 7) / 8, most = d.n * lay.runs / kHeldCtas;
+                samples = lanes / few < most ? lanes / few : most;
+                samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
+                own = lanes / samples < own ? lanes / samples : own;
             }
+            lay.samples = int(samples);
+            lay.lanes = int(own);
+            lay.P = int(samples * own);
+            lay.threads = round_up(lay.P * lay.V, 32);
+            const int64_t lane_rows = (lay.range + own - 1) / own;
+            if (lane_rows > kHeldRows)
+                continue;
+            lay.lane_rows = int(lane_rows);
+            if (int64_t(held_bytes(lay, es, backward, held)) > kSmemPerSm / 2 - kSmemPerCtaReserved)
+                continue;
+            const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * ranks;
+            if (ranks > 1 && ctas > kHeldWave)
+                continue;
+            // long samples in many CTAs: the backward pass would hold runs of
+            // 128 bytes only (bf16 [256, 256, 512]: 72 us against 58 streaming;
+            // [2000, 64, 256]: 81 against 113)
+            if (backward && d.l >= 128 && ctas > 2 * kHeldCtas)
+                continue;
+            // the most CTAs, and of those the widest runs and fewest ranks
+            if (ctas > best) {
+                best = ctas;
+                *out = lay;
+            }
+            if (ranks == 1 && ctas >= kHeldCtas)
+                return true;
+        }
         const int64_t next = (groups / 2 + unit - 1) / unit * unit;
         if (next >= groups || next * per * es < 128)
             break;
         groups = next;
     }
-    return best > 0;
+    // a few CTAs with much to do: the streaming kernels spread it further
+    const int64_t elements = d.n * d.l * d.c;
+    return best >= 76 || (best > 0 && elements <= best * kHeldFew);
 }
 
 // How a call runs; held: backward from a checkpoint.  The search takes
