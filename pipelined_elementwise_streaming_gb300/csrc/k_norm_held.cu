@@ -10,8 +10,18 @@
 // barrier guards them and the sums start with the first group.  The
 // statistics go through the CTA's shared memory (tsx_norm.cuh) and, in a
 // cluster, through every CTA's copy of the groups' sums: all ranks join the
-// ranks' sums in the same order, so they agree to the bit.  A CTA takes Q small
-// samples side by side.
+// ranks' sums in the same order, so they agree to the bit.  A CTA takes several
+// small samples side by side.
+//
+// Measured on GB300, GPU time of a call in a CUDA graph, against the streaming
+// kernels: f16 [8, 4096, 320] forward 17.3 us (18.5), bf16 [4, 1024, 1280] 9.9
+// (16.9) and its gradient 16.3 (19.3).  The tensors' own time at HBM's rate is
+// 6.2, 3.1 and 4.6 us; what is left is the chain, of which the arithmetic of
+// two CTAs of 256 threads to an SM is the longest part.  Clusters of 16, or one
+// CTA of 512 threads to an SM, were slower: the SMs hold 14 clusters of 16 at
+// two CTAs to an SM, 36 of eight, and a second wave doubles the time (bf16 [16,
+// 1024, 640] with its checkpoint 46 us in 16 clusters of large CTAs, 21
+// streaming).
 
 #include "tsx_norm.cuh"
 

@@ -272,7 +272,7 @@ constexpr int64_t kHeldWave = 256;        // CTAs of clusters of eight that the 
 // 152 SMs hold at once, two each backward and for fp32, else three.  A constant
 // of the chip, not read from it, so that results depend on the shape alone.
 constexpr int64_t kNormThrees = 3 * 152, kNormPairs = 2 * 152;
-constexpr int64_t kNormWide = 640;
+constexpr int64_t kNormWide = 640, kNormGroups = 128;
 constexpr int64_t kNormParts = 160;   // parts of a sample that the second kernel's CTAs join by themselves
 constexpr int kNormRowsAtOnce = 4;
 
@@ -305,14 +305,18 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
         lay.pieces = int((per + lay.run_cols - 1) / lay.run_cols);
         lay.runs = int(d.groups) * lay.pieces;
     } else {
-        // the widest run of at most kNormWide channels that fills a CTA with
-        // rows side by side, or the one that comes nearest
+        // the widest run of at most kNormWide channels and kNormGroups groups
+        // that fills a CTA with rows side by side, or the one that comes
+        // nearest; one of whole 128 bytes if any
         const int64_t unit = align / std::gcd(per, align);
-        int64_t groups = d.c <= kNormRun ? d.groups : 0, best = groups ? filled(d.c, team_of(d.c, block, vec)) : 0;
-        if (d.c > kNormWide)
+        int64_t groups = 0, best = 0;
+        if (d.c <= kNormWide && d.groups <= kNormGroups) {
+            groups = d.groups;
+        } else {
+            const int64_t all = d.c <= kNormRun ? d.groups : 0;   // where runs cannot start on whole octs or blocks
             for (int64_t g = kNormRun / per / unit * unit; g > 0; g -= unit) {
                 const int64_t cols = g * per;
-                if (g >= d.groups || (cols > kNormWide && g > unit && best > 0))
+                if (g >= d.groups || ((cols > kNormWide || g > kNormGroups) && g > unit))
                     continue;
                 if (cols * elem_size(d.dtype) < 128 && groups > 0)
                     break;
@@ -322,6 +326,9 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
                     groups = g;
                 }
             }
+            if (groups == 0)
+                groups = all;
+        }
         if (groups == 0)
             return false;
         lay.run_groups = int(groups);

@@ -263,6 +263,7 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
         v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
+
 // (mean, M2) of each of `samples` x `groups` items from the columns that the
 // row lanes left: slots[samples * lanes][slot_stride], `per` neighbouring
 // columns to a group, `scale` elements to a column and row, `rows` rows dealt

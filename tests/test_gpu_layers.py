@@ -123,6 +123,7 @@ def test_norm_and_its_gradient(tsx, shape, dtype):
     (3000, 1, 512, 8), (40, 1, 1280, 5), (3, 1, 4096, 2), (9, 1, 24, 3), (700, 3, 64, 8), (900, 7, 320, 32),
     (2000, 2, 16, 16), (1, 1000, 2048, 1), (1, 100, 2048, 1), (2, 4000, 64, 4), (1, 8192, 64, 2), (1, 8200, 64, 64),
     (1, 17, 2048, 2048), (16, 300, 96, 4), (3, 512, 640, 32),
+    (1, 5000, 2048, 2048), (1, 9000, 320, 320), (2, 3000, 1000, 1), (1, 20000, 24, 3), (600, 200, 64, 4),
 ], ids=lambda s: "x".join(map(str, s)))
 def test_norm_however_it_runs(tsx, shape, dtype):
     n, l, c, groups = shape
