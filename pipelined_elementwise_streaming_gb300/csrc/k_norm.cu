@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a, s);
     const int P = a.lay.P;
-    Affine k;
+    Affine<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     float2* stats = reinterpret_cast<float2*>(work + max(static_cast<int>(blockDim.x), a.lay.run_groups));
     WalkOut out = walk_out<DT>(y, r.row0 + s.p, P, a.y_pitch, s);
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
     auto begin = [&] {
         wait_for_last();
         join_parts(a, s, r.sample, part, stats, work);
-        k.template statistics<BY_OCT>(a, s, stats);
+        k.statistics(a, s, stats);
         if (r.split == 0 && s.piece == 0)
             for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
                 mean[r.sample * a.groups + s.group0 + g] = stats[g].x;
@@ -265,8 +265,8 @@ __device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, 
     }
 }
 
-// First kernel: S1 and S2 of every cluster's range, run and group, and the
-// range's sums for dweight and dbias.
+// First kernel: S1 and S2 (times act_scale) of every cluster's range, run and
+// group, and the range's sums for dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
 __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     norm_sums_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
@@ -317,9 +317,8 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
             t1 = __ffma2_rn(sz[j], k.w[j], t1);
             t2 = __ffma2_rn(szx[j], k.w[j], t2);
         }
-        const float f = 1.f / act_scale(a.act);
         if (s.live)
-            work[s.p * (width / 8) + s.at.ch / 8] = make_float2((t1.x + t1.y) * f, (t2.x + t2.y) * f);
+            work[s.p * (width / 8) + s.at.ch / 8] = make_float2(t1.x + t1.y, t2.x + t2.y);
         __syncthreads();
         add_octs(work, width / 8, P, s.groups, group_cols(a, s) / 8, mine);
         __syncthreads();
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
         oct_floats(g.dy, fd);
         g.hats(a, k, hat);
         k.slopes(a, fd, hat, dz);
-        to.of(dz, hat, v);
+        to.of(k, dz, hat, v);
         oct_store<DT, VEC>(out.p, s.at, oct_round<DT>(v));
         out.p += out.step;
     });

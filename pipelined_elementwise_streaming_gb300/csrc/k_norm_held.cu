@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             cp_async_commit();
         }
     }
-    Affine k;
+    Affine<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     Triples<BY_OCT> t;
     t.clear();
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }
     }
     __syncthreads();
-    k.template statistics<BY_OCT>(a, s, stats + (s.live ? h.q : 0) * s.groups);
+    k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
     WalkOut out = walk_out<DT>(y, h.row0 + h.lane, lay.lanes, a.y_pitch, s);
     HeldPtr to;
     if constexpr (HOLD)
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         oct_floats(g.dy, fd);
         g.hats(a, k, hat);
         k.slopes(a, fd, hat, dz);
-        grad.of(dz, hat, res);
+        grad.of(k, dz, hat, res);
         oct_store<DT, VEC>(to.p, s.at, oct_round<DT>(res));
         to.p += to.step;
     }

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
     const NormPlace s = norm_place<true>(a);
     const int lanes = a.per_group / 8;   // threads to a group
     const float inv_m = 1.f / static_cast<float>(a.per_group);   // a power of two
-    Affine k;
+    Affine<true> k;
     k.params<DT, true>(a, s, weight, bias);
     const int group = s.group0 + local_group(a, s.at.ch);
     const bool first = s.at.ch % a.per_group == 0;
@@ -96,9 +96,11 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    f[j] = __ffma2_rn(f[j], pair_of(rs), pair_of(-mu[i] * rs));
-                k.apply(a.act, f, v);   // scale and shift are weight and bias as they came
+                for (int j = 0; j < 4; ++j) {
+                    const float2 hat = __fmul2_rn(__fadd2_rn(f[j], pair_of(-mu[i])), pair_of(rs));
+                    f[j] = __ffma2_rn(hat, k.scale[j], k.bias[j]);   // weight and bias as they came
+                }
+                act_value(a.act, f, v);
                 oct_store<DT, true>(out + i * to.step, s.at, oct_round<DT>(v));
                 if (first) {
                     pm[i * step_s] = mu[i];
@@ -128,8 +130,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
     extern __shared__ float2 shared[];
     const NormPlace s = norm_place<true>(a);
     const int lanes = a.per_group / 8;
-    // w carries act_scale
-    const float minus_m = -1.f / (static_cast<float>(a.per_group) * act_scale(a.act));
+    const float minus_m = -1.f / static_cast<float>(a.per_group);
     Chan<true> k;
     k.params<DT, true>(a, s, weight, bias);
     const int group = s.group0 + local_group(a, s.at.ch);
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
                 float2 out[4];
                 k.statistics(mu[i], rs[i]);
                 grad.set(a, k, s1[i] * minus_m, s2[i] * minus_m);
-                grad.of(dz[i], hat[i], out);
+                grad.of(k, dz[i], hat[i], out);
                 oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(out));
             }
     }

@@ -557,8 +557,15 @@ int check_norm(const char* call, const tsx_norm_desc* d)
     return TSX_OK;
 }
 
-// Scratch that covers every layout the call may take, whatever its pointers'
-// alignment.
+// The layout that a call takes: with vectors where its rows allow them and its
+// groups' runs can start on them.
+bool call_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
+{
+    return norm_layout(d, vec, block, backward, held, out) ||
+           (vec && norm_layout(d, false, block, backward, held, out));
+}
+
+// Scratch that covers every layout the call may take.
 size_t norm_workspace(const tsx_norm_desc& d, bool backward, bool aligned)
 {
     size_t most = 0;
@@ -570,7 +577,7 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward, bool aligned)
     for (int vec = aligned && whole ? 1 : 0; vec < (whole ? 2 : 1); ++vec)
         for (int held = 0; held < 2; ++held) {   // with a checkpoint, written or read
             NormLayout lay;
-            if (!norm_layout(d, vec != 0, held && !backward ? d.block : 0, backward, held != 0, &lay))
+            if (!call_layout(d, vec != 0, held && !backward ? d.block : 0, backward, held != 0, &lay))
                 continue;
             const size_t b = part_bytes(d, lay) + (backward ? chan_bytes(d, lay) : 0);
             most = b > most ? b : most;
@@ -581,7 +588,7 @@ size_t norm_workspace(const tsx_norm_desc& d, bool backward, bool aligned)
 int norm_args(const char* call, const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, const void* weight,
               const void* bias, NormArgs* a)
 {
-    if (!norm_layout(d, vec, block, backward, held, &a->lay) && !norm_layout(d, false, block, backward, held, &a->lay))
+    if (!call_layout(d, vec, block, backward, held, &a->lay))
         return fail(TSX_ERR_UNSUPPORTED, call, "no layout");
     if (a->lay.runs > kMaxChunks)
         return fail(TSX_ERR_UNSUPPORTED, call, "rows are too long");
@@ -656,7 +663,7 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
     const bool vec = vectors(x, d.c, d.x_pitch, es) && vectors(y, d.c, d.y_pitch, es) && held_vectors(q, d.c);
     // the checkpoint rides along where runs can start on its blocks
     NormLayout lay;
-    const bool ride = q && (norm_layout(d, vec, d.block, false, true, &lay) || norm_layout(d, false, d.block, false, true, &lay));
+    const bool ride = q && call_layout(d, vec, d.block, false, true, &lay);
     NormArgs a{};
     rc = norm_args(call, d, vec, ride ? d.block : 0, false, ride, weight, bias, &a);
     if (rc == TSX_OK)

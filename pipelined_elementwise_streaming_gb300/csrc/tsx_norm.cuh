@@ -416,8 +416,9 @@ __device__ __forceinline__ float weight_at(const NormArgs& a, const void* weight
         return __half2float(static_cast<const __half*>(weight)[ch]);
 }
 
-// (S1, S2) of each of samples x groups items from the channels' sums of dz
-// and dz xhat: columns[samples][width], out[samples][groups].
+// (S1, S2), times act_scale, of each of samples x groups items from the
+// channels' sums of dz and dz xhat: columns[samples][width],
+// out[samples][groups].
 template <int DT>
 __device__ __forceinline__ void weigh_columns(const NormArgs& a, const NormPlace& s, int samples, int width,
                                               const void* weight, const float2* columns, float2* out)
@@ -428,7 +429,7 @@ __device__ __forceinline__ void weigh_columns(const NormArgs& a, const NormPlace
         float s1 = 0.f, s2 = 0.f;
         for (int e = lane; e < per; e += lanes) {
             const int ch = g * per + e;
-            const float w = weight_at<DT>(a, weight, s.ch0 + ch);
+            const float w = weight_at<DT>(a, weight, s.ch0 + ch) * act_scale(a.act);
             const float2 v = columns[q * width + ch];
             s1 += w * v.x;
             s2 += w * v.y;
@@ -503,47 +504,49 @@ __device__ __forceinline__ void grouped(const NormArgs& a, const NormPlace& s, c
     }
 }
 
-// What a thread keeps for its channels forward: y = act(x scale + shift), scale
-// = rstd weight, shift = bias - mean scale.  Against (x - mean) scale + bias
-// this rounds mean scale once more, an error of the size that the rounded mean
-// has already, and takes one operation less.
+// What a thread keeps for its channels forward: y = act((x - mean) scale +
+// bias), scale = rstd weight.  One operation less, x scale + (bias - mean
+// scale), would leave the rounding of mean scale, which is large where a group
+// is constant and rstd as large as 1 / sqrt(eps).
+template <bool BY_OCT>
 struct Affine {
-    float2 scale[4], shift[4];
+    Grouped<BY_OCT> minus;   // minus the mean
+    float2 scale[4], bias[4];
     // before the statistics are there: weight and bias
     template <int DT, bool VEC>
     __device__ __forceinline__ void params(const NormArgs& a, const NormPlace& s, const void* weight,
-                                           const void* bias)
+                                           const void* bias_)
     {
         param_floats<DT, VEC>(weight, a.wide_params, a.packed_params, s.ch0, s.at, scale);
-        param_floats<DT, VEC>(bias, a.wide_params, a.packed_params, s.ch0, s.at, shift);
+        param_floats<DT, VEC>(bias_, a.wide_params, a.packed_params, s.ch0, s.at, bias);
     }
     // stats: (mean, rstd) by group of the run
-    template <bool BY_OCT>
     __device__ __forceinline__ void statistics(const NormArgs& a, const NormPlace& s, const float2* stats)
     {
-        Grouped<BY_OCT> mean, rstd;
-        grouped<BY_OCT>(a, s, stats, mean, rstd);
+        Grouped<BY_OCT> rstd;
+        grouped<BY_OCT>(a, s, stats, minus, rstd);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < (BY_OCT ? 1 : 4); ++j)
+            minus.v[j] = __fmul2_rn(minus.v[j], pair_of(-1.f));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
             scale[j] = __fmul2_rn(scale[j], rstd.at(j));
-            shift[j] = __ffma2_rn(__fmul2_rn(mean.at(j), pair_of(-1.f)), scale[j], shift[j]);
-        }
     }
     __device__ __forceinline__ void apply(int act, const float2 (&x)[4], float2 (&y)[4]) const
     {
         float2 z[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            z[j] = __ffma2_rn(x[j], scale[j], shift[j]);
+            z[j] = __ffma2_rn(__fadd2_rn(x[j], minus.at(j)), scale[j], bias[j]);
         act_value(act, z, y);
     }
 };
 
-// And backward: xhat = x rstd + off, off = -mean rstd (see above); weight and
-// bias times act_scale, so that act' comes from t = xhat w + b.
+// And backward: xhat = (x - mean) rstd; weight and bias times act_scale, so
+// that act' comes from t = xhat w + b.
 template <bool BY_OCT>
 struct Chan {
-    Grouped<BY_OCT> off, rstd;
+    Grouped<BY_OCT> minus, rstd;
     float2 w[4], b[4];
     template <int DT, bool VEC>
     __device__ __forceinline__ void params(const NormArgs& a, const NormPlace& s, const void* weight,
@@ -560,14 +563,14 @@ struct Chan {
     }
     __device__ __forceinline__ void statistics(const NormArgs& a, const NormPlace& s, const float2* stats)
     {
-        grouped<BY_OCT>(a, s, stats, off, rstd);
+        grouped<BY_OCT>(a, s, stats, minus, rstd);
 #pragma unroll
         for (int j = 0; j < (BY_OCT ? 1 : 4); ++j)
-            off.v[j] = __fmul2_rn(__fmul2_rn(off.v[j], pair_of(-1.f)), rstd.v[j]);
+            minus.v[j] = __fmul2_rn(minus.v[j], pair_of(-1.f));
     }
     __device__ __forceinline__ void statistics(float mean, float rs)   // BY_OCT
     {
-        off.v[0] = pair_of(-mean * rs);
+        minus.v[0] = pair_of(-mean);
         rstd.v[0] = pair_of(rs);
     }
     // dz
@@ -585,11 +588,13 @@ struct Chan {
     }
 };
 
-// dx = dz (rstd weight) - rstd S1 / M - xhat rstd S2 / M.
+// dx = rstd (dz weight - S1 / M - xhat S2 / M).  S1 and S2 are sums of the very
+// products dz w, act_scale and all, that dx starts from, and rstd is multiplied
+// last: in a group of one element the difference then is zero, not what two
+// roundings leave.
 template <bool BY_OCT>
 struct Gradient {
-    Grouped<BY_OCT> s1, s2;   // minus rstd S1 / M and rstd S2 / M
-    float2 w[4];              // rstd weight
+    Grouped<BY_OCT> s1, s2, rstd;   // -S1 / M and -S2 / M; rstd / act_scale
     // sums: (-S1 / M, -S2 / M) by group of the run
     __device__ __forceinline__ void set(const NormArgs& a, const NormPlace& s, const Chan<BY_OCT>& k,
                                         const float2* sums)
@@ -607,19 +612,16 @@ struct Gradient {
     {
         const float2 f = pair_of(1.f / act_scale(a.act));
 #pragma unroll
-        for (int j = 0; j < (BY_OCT ? 1 : 4); ++j) {
-            s1.v[j] = __fmul2_rn(s1.v[j], k.rstd.v[j]);
-            s2.v[j] = __fmul2_rn(s2.v[j], k.rstd.v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = __fmul2_rn(k.w[j], __fmul2_rn(f, k.rstd.at(j)));
+        for (int j = 0; j < (BY_OCT ? 1 : 4); ++j)
+            rstd.v[j] = __fmul2_rn(f, k.rstd.v[j]);
     }
-    __device__ __forceinline__ void of(const float2 (&dz)[4], const float2 (&xhat)[4], float2 (&dx)[4]) const
+    __device__ __forceinline__ void of(const Chan<BY_OCT>& k, const float2 (&dz)[4], const float2 (&xhat)[4],
+                                       float2 (&dx)[4]) const
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            dx[j] = __ffma2_rn(xhat[j], s2.at(j), __ffma2_rn(dz[j], w[j], s1.at(j)));
+            dx[j] = __fmul2_rn(rstd.at(j),
+                               __ffma2_rn(xhat[j], s2.at(j), add_alone(__fmul2_rn(dz[j], k.w[j]), s1.at(j))));
     }
 };
 
@@ -727,7 +729,7 @@ struct GradRow {
             }
         }
     }
-    // xhat = x rstd + off; of a checkpoint q (scale rstd) + off
+    // xhat = (x - mean) rstd, of a checkpoint with x = q scale
     template <bool BY_OCT>
     __device__ __forceinline__ void hats(const NormArgs& a, const Chan<BY_OCT>& k, float2 (&hat)[4]) const
     {
@@ -736,15 +738,16 @@ struct GradRow {
             oct_floats(x, f);
         else
             held_numbers(q, a.form, f);
-        const float2 one = HELD && VEC && BY_OCT ? __fmul2_rn(k.rstd.at(0), pair_of(scale[0])) : k.rstd.at(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float2 r = BY_OCT ? one : k.rstd.at(j);
-            if constexpr (HELD && VEC && !BY_OCT)
-                r = __fmul2_rn(r, pair_of(scale[0]));
-            else if constexpr (HELD && !VEC)
-                r = __fmul2_rn(r, make_float2(scale[2 * j], scale[2 * j + 1]));
-            hat[j] = __ffma2_rn(f[j], r, k.off.at(j));
+            float2 d;
+            if constexpr (!HELD)
+                d = __fadd2_rn(f[j], k.minus.at(j));
+            else if constexpr (VEC)
+                d = __ffma2_rn(f[j], pair_of(scale[0]), k.minus.at(j));
+            else
+                d = __ffma2_rn(f[j], make_float2(scale[2 * j], scale[2 * j + 1]), k.minus.at(j));
+            hat[j] = __fmul2_rn(d, k.rstd.at(j));
         }
     }
 };

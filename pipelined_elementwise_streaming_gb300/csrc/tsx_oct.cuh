@@ -108,6 +108,13 @@ __device__ __forceinline__ Oct<DT> oct_load(const char* p, const OctAt& at)
 // instruction (fma.rn.f32x2 and its kin), with the rounding of the scalar ones.
 __device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
 
+// A sum that does not become one fma with the paired product before it, as the
+// compiler makes of a paired sum.
+__device__ __forceinline__ float2 add_alone(float2 a, float2 b)
+{
+    return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
 template <int DT>
 __device__ __forceinline__ void oct_floats(const Oct<DT>& o, float2 (&f)[4])
 {
@@ -400,8 +407,7 @@ __device__ __forceinline__ Held held_round(const float2 (&f)[4], float inv, int 
     if (form == TSX_INT8) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            // not as a pair: the paired product and sum would become one fma
-            v[j] = make_float2(__fadd_rn(v[j].x, 12582912.f), __fadd_rn(v[j].y, 12582912.f));
+            v[j] = add_alone(v[j], pair_of(12582912.f));   // the product is rounded by itself
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             h.w[k] = __byte_perm(
