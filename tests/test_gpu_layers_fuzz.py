@@ -7,7 +7,8 @@ Tolerances: an output rounded into its type carries half its spacing, 2^-11,
 value of the output, well under 2^-16 for sums of the lengths drawn (at most
 2^17 terms added in a tree of short runs: errors grow with the depth, below
 2^-18 of the sum of magnitudes, and the sums of magnitudes here are below four
-times the largest output)."""
+times the largest output).  Groups of one element have the gradient zero and
+xhat zero: there the kernels' differences are of equal numbers, and exact."""
 
 import math
 import random
