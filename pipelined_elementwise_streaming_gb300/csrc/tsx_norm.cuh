@@ -758,7 +758,7 @@ struct GradRow {
 // are on their way at any time.
 template <int DT>
 struct RowQueue {
-    static constexpr int kBatch = 4, kBatches = DT == TSX_F32 ? 2 : 3, kRows = kBatch * kBatches;
+    static constexpr int kBatch = 4, kBatches = 2, kRows = kBatch * kBatches;
     static constexpr uint32_t kVecs = elem_size(DT) / 2;   // 16-byte vectors of an oct
     static constexpr uint32_t kStep = kNormThreads * 16;
     static constexpr size_t kBytes = size_t(kRows) * kVecs * kStep;
