@@ -28,6 +28,7 @@ namespace {
 
 using namespace dev;
 
+constexpr int kPartsAtOnce = 16;   // parts that a thread of the gradient's second kernel loads at once
 constexpr int kGradRows = 2;   // rows that a thread loads at once where they go element by element
 
 // CTAs to an SM that the registers are cut for.
@@ -287,14 +288,16 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
         cluster_arrive();
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
-    load_stats(a, s, r.sample, mean, rstd, stats);
-    k.statistics(a, s, stats);
+    auto begin = [&] {
+        load_stats(a, s, r.sample, mean, rstd, stats);
+        k.statistics(a, s, stats);
+    };
     float2 sz[4], szx[4];   // sums of dz and dz xhat, channel by channel
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
     const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, [] {}, [&](const GradRow<DT, VEC, HELD>& g) {
+    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin, [&](const GradRow<DT, VEC, HELD>& g) {
         float2 fd[4], hat[4], dz[4];
         oct_floats(g.dy, fd);
         g.hats(a, k, hat);
@@ -414,9 +417,16 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
         for (int i = threadIdx.x; i < lanes * s.groups; i += threads) {
             const int lane = i / s.groups, group = i - lane * s.groups;
             float2 t = make_float2(0.f, 0.f);
-#pragma unroll 4
-            for (int n = lane; n < count; n += lanes)
-                t = __fadd2_rn(t, first[static_cast<int64_t>(n) * a.groups + group]);
+            for (int n = lane; n < count; n += kPartsAtOnce * lanes) {
+                float2 v[kPartsAtOnce];
+#pragma unroll
+                for (int j = 0; j < kPartsAtOnce; ++j)
+                    v[j] = n + j * lanes < count ? first[static_cast<int64_t>(n + j * lanes) * a.groups + group]
+                                                 : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kPartsAtOnce; ++j)
+                    t = __fadd2_rn(t, v[j]);
+            }
             work[i] = t;
         }
         __syncthreads();
