@@ -29,6 +29,7 @@ struct Place {
     int64_t row0;   // the thread's first row; the others are P apart
     int ch;         // its first channel, counted from the row's start
     int rows;       // how many of its rows exist (0 for spare threads of the last warp)
+    int most;       // the most that a thread of the CTA has
     bool live;      // the thread has channels
 };
 
@@ -36,18 +37,22 @@ template <bool VEC, int ROWS>
 __device__ __forceinline__ Place place(const RowLayout& lay)
 {
     Place s;
-    const int p = static_cast<int>(threadIdx.x) / lay.V, v = static_cast<int>(threadIdx.x) - p * lay.V;
+    const int p = lane_of(threadIdx.x, lay.per_v), v = static_cast<int>(threadIdx.x) - p * lay.V;
     const int chunk0 = static_cast<int>(blockIdx.y) * lay.chunk_cols;
     const int cols = min(lay.chunk_cols, lay.cols - chunk0);
     s.at = oct_at<VEC>(v, lay.team, cols);
     s.ch = chunk0 + s.at.ch;
     s.live = p < lay.P && s.at.ch < cols;
-    s.row0 = static_cast<int64_t>(blockIdx.x) * (lay.P * ROWS) + p;
-    const int64_t left = lay.rows - s.row0;
-    s.rows = 0;
+    const uint32_t first = blockIdx.x * (lay.P * ROWS);   // rows < 2^31
+    s.row0 = first + p;
+    // rows that the CTA has: ROWS * P, or fewer at the end
+    const int left = static_cast<int>(min(static_cast<uint32_t>(lay.rows) - first, static_cast<uint32_t>(lay.P * ROWS)));
+    s.rows = s.most = 0;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-        s.rows += p < lay.P && left > i * lay.P ? 1 : 0;
+    for (int i = 0; i < ROWS; ++i) {
+        s.rows += p < lay.P && left > i * lay.P + p ? 1 : 0;
+        s.most += left > i * lay.P ? 1 : 0;
+    }
     return s;
 }
 
@@ -71,7 +76,7 @@ __device__ __forceinline__ void load_held(const Place& s, const void* q, const f
                                           int64_t blocks, int block, Held (&h)[N], float (&sc)[N])
 {
     const uint8_t* p = static_cast<const uint8_t*>(q) + s.row0 * lay.cols + s.ch;
-    const float* ps = scale + s.row0 * blocks + s.ch / block;
+    const float* ps = scale + s.row0 * blocks + block_of(s.ch, block);
     const int64_t step = static_cast<int64_t>(lay.P) * lay.cols, step_s = lay.P * blocks;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -92,7 +97,7 @@ __global__ void __launch_bounds__(kLayerThreads) pack_kernel(PackArgs a, const v
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
         const Oct<DT> four[4] = {o[i], o[i + 1], o[i + 2], o[i + 3]};
-        if (i < s.rows)
+        if (i < s.most)
             hold_rows<DT, VEC>(four, s.rows - i, s.live, s.at, a.lay.team, a.form, to);
         to.advance(4);
     }

@@ -196,7 +196,9 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
                 rstd[r.sample * a.groups + s.group0 + g] = stats[g].y;
             }
     };
-    each_four<DT, VEC>(walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s), s.at, next_16(stats + a.lay.run_groups), r.mine,
+    // every lane of a warp comes to the checkpoint's shuffles
+    const int loop = HOLD ? (r.rows + P - 1) / P : r.mine;
+    each_four<DT, VEC>(walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s), s.at, next_16(stats + a.lay.run_groups), loop,
                        r.mine, s.live, begin, [&](const Oct<DT>(&o)[4], int n) {
 #pragma unroll
                            for (int i = 0; i < 4; ++i)

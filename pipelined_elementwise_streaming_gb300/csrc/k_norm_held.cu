@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     HeldPtr to;
     if constexpr (HOLD)
         to = HeldPtr(held, h.row0 + h.lane, lay.lanes, a.c, a.blocks, s.ch0 + s.at.ch, a.block);
-    for (int i0 = 0; i0 < h.mine; i0 += 4) {   // the same for all threads of a team
+    const int loop = HOLD ? lay.lane_rows : mine;   // every lane of a warp comes to the checkpoint's shuffles
+    for (int i0 = 0; i0 < loop; i0 += 4) {
         Oct<DT> o[4];
         rows.take4(i0, mine, o);
 #pragma unroll

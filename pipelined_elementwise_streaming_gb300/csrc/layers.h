@@ -11,6 +11,13 @@
 
 namespace tsx {
 
+// t / V for a thread t, as t * per >> 20 with per = (2^20 + e) / V, 0 <= e < V:
+// the product is t / V * 2^20 and less than 2^20 / V more while t e < 2^20,
+// which t, V < 2^10 are.  The kernels' CTAs live for a few rows, so that the
+// tens of instructions of a division count.
+constexpr uint32_t lane_factor(int V) { return ((1u << 20) + uint32_t(V) - 1) / uint32_t(V); }
+TSX_HD constexpr int lane_of(int t, uint32_t per) { return int((uint32_t(t) * per) >> 20); }
+
 // How [rows, cols] is laid over CTAs and threads.  A row is cut into `chunks`
 // runs of chunk_cols channels (grid.y); a CTA holds P rows of one run at a
 // time, V threads to a row, each with eight channels (csrc/tsx_oct.cuh).
@@ -20,6 +27,7 @@ struct RowLayout {
     int chunk_cols;   // channels of a run: a multiple of 8, of the block where there are checkpoints
     int chunks;
     int V;            // threads to a row: ceil(chunk_cols / 8) rounded up to whole teams
+    uint32_t per_v;   // lane_factor(V)
     int P;            // rows side by side
     int team;         // neighbouring threads that share a checkpoint block (1, 2, ..., 16)
     int threads;      // P * V rounded up to whole warps
@@ -79,6 +87,7 @@ struct NormLayout {
     int runs;
     int pieces;          // runs to a group (1 unless a group is wider than a CTA's row)
     int V, P, threads;
+    uint32_t per_v;      // lane_factor(V)
     int64_t splits;      // row ranges of a sample; token kernels: CTAs that share the rows of a run
     int64_t range;       // rows to a range, or to a rank
     // kernels that hold samples on chip: CTAs of a cluster that share a

@@ -40,6 +40,7 @@ RowLayout row_layout(int64_t rows, int64_t cols, int block, bool vec, int want)
     const int64_t chunks = (octs + want - 1) / want;
     const int64_t v = round_up((octs + chunks - 1) / chunks, lay.team);
     lay.V = int(v);
+    lay.per_v = lane_factor(lay.V);
     lay.chunk_cols = lay.V * kOct;
     lay.chunks = int((cols + lay.chunk_cols - 1) / lay.chunk_cols);
     int64_t p = want / v;
@@ -338,6 +339,7 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
     }
     lay.team = team_of(lay.run_cols, block, vec);
     lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
+    lay.per_v = lane_factor(lay.V);
     int64_t p = kNormThreads / lay.V;
     p = p < 1 ? 1 : p > d.l ? d.l : p;
     lay.P = int(p);
@@ -377,6 +379,7 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     lay.team = team_of(lay.run_cols, block, true);
     const int own = int(per / kOct);
     lay.V = round_up(lay.run_cols / kOct, own > lay.team ? own : lay.team);
+    lay.per_v = lane_factor(lay.V);
     int64_t p = kTokenThreads / lay.V;
     p = p < 1 ? 1 : p > d.n ? d.n : p;
     lay.P = int(p);
@@ -420,6 +423,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             lay.runs = int((d.groups + groups - 1) / groups);
             lay.team = team_of(lay.run_cols, block, vec);
             lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
+            lay.per_v = lane_factor(lay.V);
             const int64_t lanes = kNormThreads / lay.V;
             if (lanes == 0)
                 continue;

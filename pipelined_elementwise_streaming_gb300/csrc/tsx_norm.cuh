@@ -48,7 +48,7 @@ __device__ __forceinline__ NormPlace norm_place(const NormArgs& a)
 {
     const NormLayout& lay = a.lay;
     NormPlace s;
-    s.p = static_cast<int>(threadIdx.x) / lay.V;
+    s.p = lane_of(threadIdx.x, lay.per_v);
     const int v = static_cast<int>(threadIdx.x) - s.p * lay.V;
     int cols;
     if (lay.pieces == 1) {
@@ -680,7 +680,7 @@ struct GradWalk {
         if constexpr (HELD) {
             q = static_cast<const uint8_t*>(src.q) + row * a.c + s.ch0 + s.at.ch;
             q_step = static_cast<int64_t>(rows_apart) * a.c;
-            scale = src.scale + row * a.blocks + (VEC ? (s.ch0 + s.at.ch) / a.block : 0);
+            scale = src.scale + row * a.blocks + (VEC ? block_of(s.ch0 + s.at.ch, a.block) : 0);
             scale_step = rows_apart * a.blocks;
         } else {
             x = walk<DT>(src.x, row, rows_apart, a.x_pitch, s);
@@ -725,7 +725,7 @@ struct GradRow {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int ch = s.at.ch + j * s.at.step;
-                scale[j] = ch < s.at.cols ? __ldg(w.scale + i * w.scale_step + (s.ch0 + ch) / a.block) : 0.f;
+                scale[j] = ch < s.at.cols ? __ldg(w.scale + i * w.scale_step + block_of(s.ch0 + ch, a.block)) : 0.f;
             }
         }
     }

@@ -40,7 +40,7 @@ __device__ __forceinline__ OctAt oct_at(int v, int team, int cols)
         o.ch = v * 8;
         o.step = 1;
     } else {
-        o.ch = v / team * 8 * team + v % team;
+        o.ch = (v & ~(team - 1)) * 8 + (v & (team - 1));   // a power of two
         o.step = team;
     }
     return o;
@@ -492,6 +492,9 @@ __device__ __forceinline__ void held_store(uint8_t* p, const OctAt& at, const He
     }
 }
 
+// Block of a channel; blocks are 32, 64 or 128 channels.
+__device__ __forceinline__ int block_of(int ch, int block) { return ch >> (31 - __clz(block)); }
+
 // Where a thread's checkpoint bytes and its team's scale go: first row, and
 // from row to row of its walk.
 struct HeldPtr {
@@ -502,7 +505,7 @@ struct HeldPtr {
     __device__ __forceinline__ HeldPtr(const HeldOut& out, int64_t row, int64_t rows_apart, int cols, int64_t blocks,
                                        int ch, int block)
         : q(static_cast<uint8_t*>(out.q) + row * cols + ch),
-          scale(out.scale + row * blocks + ch / block),
+          scale(out.scale + row * blocks + block_of(ch, block)),
           q_step(rows_apart * cols),
           scale_step(rows_apart * blocks)
     {
@@ -515,9 +518,9 @@ struct HeldPtr {
 };
 
 // N rows of a thread's oct to 8 bits, each with its team's scale, to where
-// `out` points; the first `n` rows exist (0: the thread only lends
-// its lane).  All lanes of a team come together, with the same n; `live`
-// threads hold channels.  The maxima of two rows of 16-bit elements share a
+// `out` points; the first `n` rows exist (none: the thread only lends its
+// lane).  All lanes of a warp come together, those of a team with the same n;
+// `live` threads hold channels.  The maxima of two rows of 16-bit elements share a
 // shuffle, and where a team has as many lanes as there are rows, each lane
 // works out one row's scale for all.
 template <int DT, bool VEC, int N>
@@ -526,7 +529,6 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
 {
     static_assert(N == 2 || N == 4, "rows");
     const int lane = static_cast<int>(threadIdx.x) & 31, base = lane & ~(team - 1);
-    const uint32_t mask = (team == 32 ? 0xffffffffu : (1u << team) - 1u) << base;
     const bool block = at.ch - (lane - base) * (VEC ? kOct : 1) < at.cols;   // the team has a block at all
     uint32_t m[N];
 #pragma unroll
@@ -536,7 +538,7 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
         for (int d = 1; d < team; d <<= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                m[i] = max(m[i], __shfl_xor_sync(mask, m[i], d));
+                m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
     } else {
         uint32_t two[N / 2];
 #pragma unroll
@@ -545,7 +547,7 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
         for (int d = 1; d < team; d <<= 1)
 #pragma unroll
             for (int i = 0; i < N / 2; ++i)
-                two[i] = __vmaxu2(two[i], __shfl_xor_sync(mask, two[i], d));
+                two[i] = __vmaxu2(two[i], __shfl_xor_sync(0xffffffffu, two[i], d));
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             m[2 * i] = two[i] & 0xffffu;
@@ -564,7 +566,7 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
             out.scale[mine * out.scale_step] = s.scale;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            inv[i] = __shfl_sync(mask, s.inv, base + i);
+            inv[i] = __shfl_sync(0xffffffffu, s.inv, base + i);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
