@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kLayerThreads) pack_kernel(PackArgs a, const v
     for (int i = 0; i < N; i += 4) {
         const Oct<DT> four[4] = {o[i], o[i + 1], o[i + 2], o[i + 3]};
         if (i < s.most)
-            hold_rows<DT, VEC>(four, s.rows - i, s.live, s.at, a.lay.team, a.form, to);
+            hold_rows<DT, VEC>(four, s.live, s.at, a.lay.team, a.form, HeldRows{to, s.rows - i});
         to.advance(4);
     }
 }
@@ -145,10 +145,11 @@ __global__ void __launch_bounds__(kLayerThreads)
         oct_store<DT, VEC>(ph + i * step, s.at, oct_round<DT>(fh));
     }
     if constexpr (HOLD) {
-        hold_rows<DT, VEC>(g, s.rows, s.live, s.at, a.lay.team, a.form,
-                           HeldPtr(held_gate, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block));
-        hold_rows<DT, VEC>(u, s.rows, s.live, s.at, a.lay.team, a.form,
-                           HeldPtr(held_up, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block));
+        static_assert(kGatedRows == 2, "four octs");
+        const Oct<DT> four[4] = {g[0], g[1], u[0], u[1]};
+        hold_rows<DT, VEC>(four, s.live, s.at, a.lay.team, a.form,
+                           HeldPairs{HeldPtr(held_gate, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block),
+                                     HeldPtr(held_up, s.row0, a.lay.P, a.lay.cols, a.blocks, s.ch, a.block), s.rows});
     }
 }
 

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
                                }
                            out.p += 4 * out.step;
                            if constexpr (HOLD) {
-                               hold_rows<DT, VEC>(o, n, s.live, s.at, a.lay.team, a.form, to);
+                               hold_rows<DT, VEC>(o, s.live, s.at, a.lay.team, a.form, HeldRows{to, n});
                                to.advance(4);
                            }
                        });

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             }
         out.p += 4 * out.step;
         if constexpr (HOLD) {
-            hold_rows<DT, VEC>(o, h.mine - i0, s.live, s.at, lay.team, a.form, to);
+            hold_rows<DT, VEC>(o, s.live, s.at, lay.team, a.form, HeldRows{to, h.mine - i0});
             to.advance(4);
         }
     }

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
         pm += 4 * step_s;
         pr += 4 * step_s;
         if constexpr (HOLD) {
-            hold_rows<DT, true>(o, n, s.live, s.at, a.lay.team, a.form, hp);
+            hold_rows<DT, true>(o, s.live, s.at, a.lay.team, a.form, HeldRows{hp, n});
             hp.advance(4);
         }
     };

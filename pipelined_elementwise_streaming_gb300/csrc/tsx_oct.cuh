@@ -517,17 +517,36 @@ struct HeldPtr {
     }
 };
 
-// N rows of a thread's oct to 8 bits, each with its team's scale, to where
-// `out` points; the first `n` rows exist (none: the thread only lends its
-// lane).  All lanes of a warp come together, those of a team with the same n;
-// `live` threads hold channels.  The maxima of two rows of 16-bit elements share a
+// Where the octs of hold_rows go: `n` rows of one walk, or two of each of two.
+struct HeldRows {
+    HeldPtr out;
+    int n;
+    __device__ __forceinline__ bool has(int i) const { return i < n; }
+    __device__ __forceinline__ uint8_t* q(int i) const { return out.q + i * out.q_step; }
+    __device__ __forceinline__ float* scale(int i) const { return out.scale + i * out.scale_step; }
+};
+struct HeldPairs {
+    HeldPtr first, second;
+    int n;
+    __device__ __forceinline__ bool has(int i) const { return (i & 1) < n; }
+    __device__ __forceinline__ uint8_t* q(int i) const { return (i < 2 ? first.q : second.q) + (i & 1) * first.q_step; }
+    __device__ __forceinline__ float* scale(int i) const
+    {
+        return (i < 2 ? first.scale : second.scale) + (i & 1) * first.scale_step;
+    }
+};
+
+// Four octs of a thread to 8 bits, each with its team's scale, to where `out`
+// says, which also says which of them exist (none: the thread only lends its
+// lane).  All lanes of a warp come together, those of a team with the same
+// octs; `live` threads hold channels.  The maxima of two rows of 16-bit elements share a
 // shuffle, and where a team has as many lanes as there are rows, each lane
 // works out one row's scale for all.
-template <int DT, bool VEC, int N>
-__device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool live, const OctAt& at, int team,
-                                          int form, const HeldPtr& out)
+template <int DT, bool VEC, class Out>
+__device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[4], bool live, const OctAt& at, int team, int form,
+                                          const Out& out)
 {
-    static_assert(N == 2 || N == 4, "rows");
+    constexpr int N = 4;
     const int lane = static_cast<int>(threadIdx.x) & 31, base = lane & ~(team - 1);
     const bool block = at.ch - (lane - base) * (VEC ? kOct : 1) < at.cols;   // the team has a block at all
     uint32_t m[N];
@@ -562,8 +581,8 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
         for (int i = 1; i < N; ++i)
             own = mine == i ? m[i] : own;
         const HeldScale s = held_scale(magnitude_bits<DT>(own), form);
-        if (block && mine < N && mine < n)
-            out.scale[mine * out.scale_step] = s.scale;
+        if (block && mine < N && out.has(mine))
+            *out.scale(mine) = s.scale;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             inv[i] = __shfl_sync(0xffffffffu, s.inv, base + i);
@@ -572,16 +591,16 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[N], int n, bool liv
         for (int i = 0; i < N; ++i) {
             const HeldScale s = held_scale(magnitude_bits<DT>(m[i]), form);
             inv[i] = s.inv;
-            if (block && lane == base && i < n)
-                out.scale[i * out.scale_step] = s.scale;
+            if (block && lane == base && out.has(i))
+                *out.scale(i) = s.scale;
         }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (live && i < n) {
+        if (live && out.has(i)) {
             float2 f[4];
             oct_floats(o[i], f);
-            held_store<VEC>(out.q + i * out.q_step, at, held_round(f, inv[i], form));
+            held_store<VEC>(out.q(i), at, held_round(f, inv[i], form));
         }
 }
 
