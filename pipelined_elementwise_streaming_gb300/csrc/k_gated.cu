@@ -131,19 +131,20 @@ __global__ void __launch_bounds__(kLayerThreads)
     load_rows<DT, VEC>(s, up, a.in_pitch, a.lay.P, u);
     char* ph = oct_ptr<DT>(h, s.row0, a.out_pitch, s.ch);
     const int64_t step = a.lay.P * a.out_pitch * elem_size(DT);
+    by_act(a.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < kGatedRows; ++i) {
-        if (!(s.live && i < s.rows))
-            continue;
-        float2 fg[4], fu[4], fh[4];
-        oct_floats(g[i], fg);
-        oct_floats(u[i], fu);
-        act_value(a.act, fg, fh);
+        for (int i = 0; i < kGatedRows; ++i) {
+            float2 fg[4], fu[4], fh[4];
+            oct_floats(g[i], fg);
+            oct_floats(u[i], fu);
+            act_value(act, fg, fh);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            fh[j] = __fmul2_rn(fh[j], fu[j]);
-        oct_store<DT, VEC>(ph + i * step, s.at, oct_round<DT>(fh));
-    }
+            for (int j = 0; j < 4; ++j)
+                fh[j] = __fmul2_rn(fh[j], fu[j]);
+            if (s.live && i < s.rows)
+                oct_store<DT, VEC>(ph + i * step, s.at, oct_round<DT>(fh));
+        }
+    });
     if constexpr (HOLD) {
         static_assert(kGatedRows == 2, "four octs");
         const Oct<DT> four[4] = {g[0], g[1], u[0], u[1]};

@@ -200,14 +200,16 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
     const int loop = HOLD ? (r.rows + P - 1) / P : r.mine;
     each_four<DT, VEC>(walk<DT>(x, r.row0 + s.p, P, a.x_pitch, s), s.at, next_16(stats + a.lay.run_groups), loop,
                        r.mine, s.live, begin, [&](const Oct<DT>(&o)[4], int n) {
+                           by_act(a.act, [&](auto act) {
 #pragma unroll
-                           for (int i = 0; i < 4; ++i)
-                               if (s.live && i < n) {
+                               for (int i = 0; i < 4; ++i) {
                                    float2 f[4], v[4];
                                    oct_floats(o[i], f);
-                                   k.apply(a.act, f, v);
-                                   oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
+                                   k.apply(act, f, v);
+                                   if (s.live && i < n)
+                                       oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
                                }
+                           });
                            out.p += 4 * out.step;
                            if constexpr (HOLD) {
                                hold_rows<DT, VEC>(o, s.live, s.at, a.lay.team, a.form, HeldRows{to, n});

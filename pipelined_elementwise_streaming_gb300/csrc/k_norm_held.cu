@@ -209,14 +209,16 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     for (int i0 = 0; i0 < loop; i0 += 4) {
         Oct<DT> o[4];
         rows.take4(i0, mine, o);
+        by_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i0 + i < mine) {
+            for (int i = 0; i < 4; ++i) {
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
-                k.apply(a.act, f, v);
-                oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
+                k.apply(act, f, v);
+                if (i0 + i < mine)
+                    oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
             }
+        });
         out.p += 4 * out.step;
         if constexpr (HOLD) {
             hold_rows<DT, VEC>(o, s.live, s.at, lay.team, a.form, HeldRows{to, h.mine - i0});

@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
             dev[i] = sq.x + sq.y;
         }
         team_sums(dev, lanes);
+        by_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float rs = rstd_of(dev[i], inv_m, a.eps);
-            if (s.live && i < n) {
+            for (int i = 0; i < 4; ++i) {
+                const float rs = rstd_of(dev[i], inv_m, a.eps);
                 float2 f[4], v[4];
                 oct_floats(o[i], f);
 #pragma unroll
@@ -100,14 +100,16 @@ __global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
                     const float2 hat = __fmul2_rn(__fadd2_rn(f[j], pair_of(-mu[i])), pair_of(rs));
                     f[j] = __ffma2_rn(hat, k.scale[j], k.bias[j]);   // weight and bias as they came
                 }
-                act_value(a.act, f, v);
-                oct_store<DT, true>(out + i * to.step, s.at, oct_round<DT>(v));
-                if (first) {
-                    pm[i * step_s] = mu[i];
-                    pr[i * step_s] = rs;
+                act_value(act, f, v);
+                if (s.live && i < n) {
+                    oct_store<DT, true>(out + i * to.step, s.at, oct_round<DT>(v));
+                    if (first) {
+                        pm[i * step_s] = mu[i];
+                        pr[i * step_s] = rs;
+                    }
                 }
             }
-        }
+        });
         out += 4 * to.step;
         pm += 4 * step_s;
         pr += 4 * step_s;

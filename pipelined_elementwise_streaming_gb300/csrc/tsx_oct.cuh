@@ -249,6 +249,34 @@ __device__ __forceinline__ float2 gelu_clamped(float2 z)
     return make_float2(fminf(fmaxf(z.x, -24.f), 24.f), fminf(fmaxf(z.y, -24.f), 24.f));
 }
 
+// f(A) with A the activation (the form of a checkpoint) as a constant.  A
+// choice that every row makes anew cuts the code into blocks of one row, in
+// which little hides the latency of the arithmetic: the kernels choose once for
+// the few rows that they hold, and compute all of them, with zeros in place of
+// those that do not exist.
+template <int V>
+struct Known {
+    __device__ constexpr operator int() const { return V; }
+};
+template <class F>
+__device__ __forceinline__ void by_act(int act, F f)
+{
+    if (act == TSX_ACT_SILU)
+        f(Known<TSX_ACT_SILU>());
+    else if (act == TSX_ACT_GELU)
+        f(Known<TSX_ACT_GELU>());
+    else
+        f(Known<TSX_ACT_NONE>());
+}
+template <class F>
+__device__ __forceinline__ void by_form(int form, F f)
+{
+    if (form == TSX_INT8)
+        f(Known<TSX_INT8>());
+    else
+        f(Known<TSX_E4M3>());
+}
+
 // v = act(z) for an oct.
 __device__ __forceinline__ void act_value(int act, const float2 (&z)[4], float2 (&v)[4])
 {
@@ -595,13 +623,16 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[4], bool live, cons
                 *out.scale(i) = s.scale;
         }
     }
+    by_form(form, [&](auto known) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (live && out.has(i)) {
+        for (int i = 0; i < N; ++i) {
             float2 f[4];
             oct_floats(o[i], f);
-            held_store<VEC>(out.q(i), at, held_round(f, inv[i], form));
+            const Held h = held_round(f, inv[i], known);
+            if (live && out.has(i))
+                held_store<VEC>(out.q(i), at, h);
         }
+    });
 }
 
 }  // namespace dev
