@@ -82,9 +82,8 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>()) norm_stats_k
     const NormPlace s = norm_place<VEC>(a);
     const Range r = range_of(a, s);
     const int P = a.lay.P, width = run_width<BY_OCT>(s), stride = slot_stride(width);
-    float4* spare = shared4;                                                    // [warps]
-    float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);        // [run_groups]
-    float2* ranks = sums + a.lay.run_groups;                                    // clusters: [ranks][run_groups]
+    float2* sums = reinterpret_cast<float2*>(shared4);   // [run_groups]
+    float2* ranks = sums + a.lay.run_groups;             // clusters: [ranks][run_groups]
     float2* slots = ranks + (a.lay.ranks > 1 ? a.lay.ranks * a.lay.run_groups : 0);   // [P][stride]
     let_next_start();
     if (a.lay.ranks > 1)
@@ -100,8 +99,8 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>()) norm_stats_k
         t.leave(s.at, slots + s.p * stride);
     __syncthreads();
     float2* out = part_of(a, s, r, part);
-    join_groups(slots, stride, 1, s.groups, P, group_cols(a, s) / (BY_OCT ? 8 : 1), r.rows, BY_OCT ? 8.f : 1.f,
-                a.lay.ranks > 1 ? sums : out, spare);
+    join_groups(a.lay, slots, stride, 1, s.groups, P, group_cols(a, s) / (BY_OCT ? 8 : 1), r.rows, BY_OCT ? 8.f : 1.f,
+                a.lay.ranks > 1 ? sums : out);
     if (a.lay.ranks > 1) {
         __syncthreads();
         cluster_wait();
@@ -110,16 +109,10 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>()) norm_stats_k
         cluster_arrive();
         cluster_wait();
         if (r.rank == 0)
-            for (int g = threadIdx.x; g < s.groups; g += blockDim.x) {
-                Triples<true> j;
-                j.clear();
-                for (int i = 0; i < a.lay.ranks; ++i) {
-                    const float2 u = ranks[i * s.groups + g];
-                    const float mu[1] = {u.x}, dev[1] = {u.y};
-                    j.join(static_cast<float>(range_rows(a, a.lay.range, r.split + i)) * group_cols(a, s), mu, dev);
-                }
-                out[g] = make_float2(j.mean[0], j.m2[0]);
-            }
+            for (int g = threadIdx.x; g < s.groups; g += blockDim.x)
+                out[g] = join_ranges(ranks + g, s.groups, a.lay.ranks,
+                                     static_cast<int>(max(a.l - r.split * a.lay.range, int64_t(0))),
+                                     static_cast<int>(a.lay.range), static_cast<float>(group_cols(a, s)));
     }
 }
 
@@ -502,8 +495,8 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, const void* x, const void*
     const NormLayout& lay = a.lay;
     const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
     const int width = lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
-    const size_t slots = kNormThreads / 32 * sizeof(float4) +
-                         (rank_sums(lay) + size_t(lay.P) * slot_stride(width)) * sizeof(float2) + row_queue_bytes(dtype, lay);
+    const size_t slots =
+        (rank_sums(lay) + size_t(lay.P) * slot_stride(width)) * sizeof(float2) + row_queue_bytes(dtype, lay);
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
     const size_t stats = items * sizeof(float4) + lay.run_groups * sizeof(float2) + row_queue_bytes(dtype, lay);
     cudaError_t e = cudaSuccess;

@@ -59,16 +59,19 @@ __device__ __forceinline__ HeldPlace held_place(const NormArgs& a, NormPlace& s)
     return h;
 }
 
-// all[ranks][items] = every rank's sums; then says that this CTA has read the
-// others (they may leave once all have).  After a cluster barrier.
-__device__ __forceinline__ void gather_ranks(const float2* sums, int items, int ranks, float2* all)
+// all[ranks][items] of every rank = this rank's sums, for all threads of the
+// cluster on return.  Called after the sums are there for all threads, and
+// after an arrival at the cluster barrier by which every CTA had started.  No
+// rank reads another's memory, so none has to wait for another to leave.
+__device__ __forceinline__ void share_sums(const float2* sums, int items, int rank, int ranks, float2* all)
 {
+    cluster_wait();
     for (int i = threadIdx.x; i < ranks * items; i += blockDim.x) {
-        const int r = i / items;
-        all[i] = cluster_pair(sums + i - r * items, r);
+        const int r = i / items, at = i - r * items;
+        cluster_put(all + rank * items + at, r, sums[at]);
     }
     cluster_arrive();
-    __syncthreads();
+    cluster_wait();
 }
 
 // Rows to a cp.async group: all that a lane may have in at most kAskGroups
@@ -137,10 +140,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     const int mine = s.live ? h.mine : 0;
     const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
     const Slots<DT, VEC> rows(reinterpret_cast<char*>(shared4));
-    float4* spare = shared4 + Slots<DT, VEC>::kVecs * lay.lane_rows * blockDim.x;   // [warps]
-    float2* sums = reinterpret_cast<float2*>(spare + kNormThreads / 32);       // [samples][groups]: (mean, M2) of the part
-    float2* stats = sums + items;                                              // [samples][groups]: (mean, rstd)
-    float2* slots = stats + items;                                             // [P][stride]; then [ranks][items]
+    // [samples][groups]: (mean, M2) of the part; (mean, rstd)
+    float2* sums = reinterpret_cast<float2*>(shared4 + Slots<DT, VEC>::kVecs * lay.lane_rows * blockDim.x);
+    float2* stats = sums + items;
+    float2* all = stats + items;                                    // clusters: [ranks][items]
+    float2* slots = all + (lay.ranks > 1 ? lay.ranks * items : 0);   // [P][stride]
+    if (lay.ranks > 1)
+        cluster_arrive();
     const int each = rows_to_group(lay);
     {
         Walk w = walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
@@ -168,28 +174,17 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     if (s.p < lay.P && s.at.ch < s.at.cols)   // absent samples leave zeros
         t.leave(s.at, slots + s.p * stride);
     __syncthreads();
-    join_groups(slots, stride, lay.samples, s.groups, lay.lanes, a.per_group / (BY_OCT ? 8 : 1), h.rows,
-                BY_OCT ? 8.f : 1.f, sums, spare);
-    if (lay.ranks > 1) {
-        cluster_arrive();
-        cluster_wait();
-        gather_ranks(sums, items, lay.ranks, slots);
-    } else {
-        __syncthreads();
-    }
+    join_groups(lay, slots, stride, lay.samples, s.groups, lay.lanes, a.per_group / (BY_OCT ? 8 : 1), h.rows,
+                BY_OCT ? 8.f : 1.f, sums);
+    __syncthreads();
+    if (lay.ranks > 1)
+        share_sums(sums, items, h.rank, lay.ranks, all);
     const float m = static_cast<float>(a.l) * static_cast<float>(a.per_group);
     for (int i = threadIdx.x; i < items; i += blockDim.x) {
         float2 v = sums[i];
-        if (lay.ranks > 1) {
-            Triples<true> j;
-            j.clear();
-            for (int r = 0; r < lay.ranks; ++r) {
-                const float2 u = slots[r * items + i];
-                const float mu[1] = {u.x}, dev[1] = {u.y};
-                j.join(static_cast<float>(range_rows(a, lay.range, r)) * a.per_group, mu, dev);
-            }
-            v = make_float2(j.mean[0], j.m2[0]);
-        }
+        if (lay.ranks > 1)
+            v = join_ranges(all + i, items, lay.ranks, static_cast<int>(a.l), static_cast<int>(lay.range),
+                            static_cast<float>(a.per_group));
         v.y = rstd_of(v.y, 1.f / m, a.eps);
         stats[i] = v;
         const int q = lay.samples == 1 ? 0 : i / s.groups;
@@ -225,8 +220,6 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             to.advance(4);
         }
     }
-    if (lay.ranks > 1)
-        cluster_wait();   // until every rank has read this one's sums
 }
 
 // The gradient.  dz is formed twice rather than held in fp32: the second time
@@ -254,8 +247,11 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* stats = sums + items;                    // [samples][groups]: (mean, rstd), then -S1 / M, -S2 / M
     float2* work = stats + items;                    // [threads]
     float2* columns = work + kNormThreads;           // [samples][width]
-    float2* slots = columns + lay.samples * width;   // [P][stride]; then [ranks][items]
+    float2* all = columns + lay.samples * width;                     // clusters: [ranks][items]
+    float2* slots = all + (lay.ranks > 1 ? lay.ranks * items : 0);   // [P][stride]
     let_next_start();
+    if (lay.ranks > 1)
+        cluster_arrive();
     const int each = rows_to_group(lay);
     const GradWalk<DT, VEC, HELD> walk_rows(a, s, dy, x, h.row0 + h.lane, lay.lanes);
     {
@@ -335,20 +331,16 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         out[ch] = v.y;
         out[a.c + ch] = v.x;
     }
-    if (lay.ranks > 1) {
-        cluster_arrive();
-        cluster_wait();
-        gather_ranks(sums, items, lay.ranks, slots);
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
+    if (lay.ranks > 1)
+        share_sums(sums, items, h.rank, lay.ranks, all);
     const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
     for (int i = threadIdx.x; i < items; i += threads) {
         float2 v = sums[i];
         if (lay.ranks > 1) {
-            v = slots[i];
+            v = all[i];
             for (int r = 1; r < lay.ranks; ++r)
-                v = __fadd2_rn(v, slots[r * items + i]);
+                v = __fadd2_rn(v, all[r * items + i]);
         }
         stats[i] = make_float2(v.x / m, v.y / m);
     }
@@ -368,8 +360,6 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         oct_store<DT, VEC>(to.p, s.at, oct_round<DT>(res));
         to.p += to.step;
     }
-    if (lay.ranks > 1)
-        cluster_wait();
 }
 
 }  // namespace
@@ -379,14 +369,12 @@ size_t held_bytes(const NormLayout& lay, int es, bool backward, bool held)
     const size_t octs = size_t(lay.lane_rows) * lay.threads;
     const size_t items = size_t(lay.samples) * lay.run_groups;
     const int width = !backward && lay.oct_in_group ? lay.run_cols / 8 : lay.run_cols;
-    size_t slots = size_t(lay.P) * slot_stride(width);
-    if (lay.ranks > 1 && slots < size_t(lay.ranks) * items)
-        slots = size_t(lay.ranks) * items;   // the ranks' sums reuse them
-    size_t pairs = 2 * items + slots;
+    size_t pairs = 2 * items + size_t(lay.P) * slot_stride(width);
+    if (lay.ranks > 1)
+        pairs += size_t(lay.ranks) * items;
     if (backward)
         pairs += kNormThreads + size_t(lay.samples) * width;
-    return octs * es * 8 + (backward ? octs * (held ? 12 : es * 8) : kNormThreads / 32 * sizeof(float4)) +
-           pairs * sizeof(float2);
+    return octs * es * 8 + (backward ? octs * (held ? 12 : es * 8) : 0) + pairs * sizeof(float2);
 }
 
 cudaError_t launch_norm_held(int dtype, const NormArgs& a, const void* x, const void* weight, const void* bias, void* y,

@@ -94,6 +94,7 @@ struct NormLayout {
     // sample, samples side by side in a CTA, row lanes of each (P = samples * lanes)
     int ranks, samples, lanes;
     int lane_rows;       // rows to a lane at most
+    int shares, share_lanes;   // forward: shares of the row lanes that are joined first, and lanes to a share
     int kind;            // NormKind
 };
 // How a call runs: streaming kernels that read their operands twice (any

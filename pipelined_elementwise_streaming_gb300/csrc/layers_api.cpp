@@ -3,6 +3,7 @@
 
 #include "layers.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -481,8 +482,19 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
 // last shapes.
 bool find_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, bool held, NormLayout* out)
 {
-    return token_layout(d, vec, block, backward, out) || held_layout(d, vec, block, backward, held, out) ||
-           stream_layout(d, vec, block, backward, out);
+    if (token_layout(d, vec, block, backward, out))
+        return true;
+    if (!held_layout(d, vec, block, backward, held, out) && !stream_layout(d, vec, block, backward, out))
+        return false;
+    // The forward kernels' sums over row lanes: as many threads to a column as
+    // there are, while an item's columns and shares are a warp's work.
+    const int per = int((out->pieces > 1 ? out->run_cols : d.c / d.groups) / (out->oct_in_group ? kOct : 1));
+    const int columns = out->samples * out->run_groups * per;
+    int shares = std::min({out->threads / columns, 64 / per, out->lanes});
+    shares = std::max(shares, 1);
+    out->share_lanes = (out->lanes + shares - 1) / shares;
+    out->shares = (out->lanes + out->share_lanes - 1) / out->share_lanes;
+    return true;
 }
 
 struct LayoutKey {

@@ -91,18 +91,6 @@ __device__ __forceinline__ int local_group(const NormArgs& a, int ch)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// A pair in the shared memory of the cluster's CTA `rank`, at the place that
-// `p` has in this one.
-__device__ __forceinline__ float2 cluster_pair(const float2* p, int rank)
-{
-    const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    uint32_t there;
-    float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(there) : "memory");
-    return v;
-}
-
 // The place that `p` has in this CTA, in the cluster's CTA `rank`.
 __device__ __forceinline__ void cluster_put(const float2* p, int rank, float2 v)
 {
@@ -265,39 +253,63 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
 }
 
 // (mean, M2) of each of `samples` x `groups` items from the columns that the
-// row lanes left: slots[samples * lanes][slot_stride], `per` neighbouring
-// columns to a group, `scale` elements to a column and row, `rows` rows dealt
-// to the lanes in turn.  Every item has a team of neighbouring threads, up to
-// a warp; where there are fewer items than warps, each warp takes one of an
-// item's `parts` shares of the row lanes, and the shares are joined in their
-// order.  Called by all threads after a barrier; ends without one.
-// spare: [warps].
-__device__ __forceinline__ void join_groups(const float2* slots, int stride, int samples, int groups, int lanes,
-                                            int per, int rows, float scale, float2* out, float4* spare)
+// row lanes left: slots[samples * lanes][slot_stride], which it overwrites;
+// `per` neighbouring columns to a group, `scale` elements to a column and row,
+// `rows` rows dealt to the lanes in turn.  In two steps: threads side by side
+// join side by side columns, each over a share of the lanes, with all its
+// loads on their way at once; then a team of threads to an item, up to a warp,
+// joins its columns' shares.  One step, a team to an item over all lanes, took 3.9 us of the
+// 18.8 of f16 [8, 4096, 320], a chain of 13 dependent rounds.  Called by all
+// threads after a barrier; ends without one.
+__device__ __forceinline__ void join_groups(const NormLayout& lay, float2* slots, int stride, int samples, int groups,
+                                            int lanes, int per, int rows, float scale, float2* out)
 {
-    const int warps = static_cast<int>(blockDim.x) / 32, items = samples * groups;
-    const int parts = items >= warps ? 1 : warps / items;
+    const int threads = static_cast<int>(blockDim.x), items = samples * groups, width = groups * per;
+    const int all = samples * width, len = lay.share_lanes, shares = lay.shares;
+    const int base = rows / lanes, more = rows - base * lanes;   // lane p has base + (p < more) rows
+    const float less = base * scale, much = less + scale;
+    if (len > 1) {
+        for (int i = threadIdx.x; i < shares * all; i += threads) {
+            const int share = shares == 1 ? 0 : i / all, col = i - share * all;
+            const int q = samples == 1 ? 0 : col / width;
+            const int p0 = share * len, p1 = min(p0 + len, lanes);
+            float2* first = slots + q * lanes * stride + col - q * width;
+            float sum = 0.f, dev = 0.f;
+#pragma unroll 4
+            for (int p = p0; p < p1; ++p)
+                sum += (p < more ? much : less) * first[p * stride].x;
+            const float n = ((p1 - p0) * base + max(min(more, p1) - p0, 0)) * scale;
+            const float mean = n > 0.f ? __fdividef(sum, n) : 0.f;
+#pragma unroll 4
+            for (int p = p0; p < p1; ++p) {
+                const float2 v = first[p * stride];
+                const float d = v.x - mean;
+                dev += v.y + (p < more ? much : less) * d * d;
+            }
+            first[p0 * stride] = make_float2(mean, dev);
+        }
+        __syncthreads();
+    }
     int shift = 5;   // log2 of the team
-    while (shift > 0 && (warps << (5 - shift)) < items)
+    while (shift > 0 && (threads >> shift) < items)
         --shift;
-    const int team = 1 << shift, teams = static_cast<int>(blockDim.x) >> shift;
+    const int team = 1 << shift, teams = threads >> shift;
     const int me = static_cast<int>(threadIdx.x) >> shift, t = static_cast<int>(threadIdx.x) & (team - 1);
     int wide = 0;   // log2 of the team's threads side by side along a row
     while (wide < shift && (1 << wide) < per)
         ++wide;
-    const int k0 = t & ((1 << wide) - 1), p0 = t >> wide, step = team >> wide;
-    const int base = rows / lanes, more = rows - base * lanes;   // lane p has base + (p < more) rows
-    for (int u0 = 0; u0 < items * parts; u0 += teams) {
-        const int u = min(u0 + me, items * parts - 1);   // spare teams repeat the last
-        const int part = parts == 1 ? 0 : u / items, item = u - part * items;
+    const int k0 = t & ((1 << wide) - 1), s0 = t >> wide, step = team >> wide;
+    for (int i0 = 0; i0 < items; i0 += teams) {
+        const int item = min(i0 + me, items - 1);   // spare teams repeat the last
         const int q = samples == 1 ? 0 : item / groups, g = item - q * groups;
         const float2* first = slots + q * lanes * stride + g * per;
         float n = 0.f, sum = 0.f, dev = 0.f;
-        for (int p = part * step + p0; p < lanes; p += parts * step) {
-            const float c = (base + (p < more ? 1 : 0)) * scale;
+        for (int share = s0; share < shares; share += step) {
+            const int p0 = share * len, p1 = min(p0 + len, lanes);
+            const float c = ((p1 - p0) * base + max(min(more, p1) - p0, 0)) * scale;
             for (int k = k0; k < per; k += 1 << wide) {
                 n += c;
-                sum += c * first[p * stride + k].x;
+                sum += c * first[p0 * stride + k].x;
             }
         }
         for (int d = 1; d < team; d <<= 1) {
@@ -305,35 +317,44 @@ __device__ __forceinline__ void join_groups(const float2* slots, int stride, int
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
         }
         const float mean = n > 0.f ? __fdividef(sum, n) : 0.f;
-        for (int p = part * step + p0; p < lanes; p += parts * step) {
-            const float c = (base + (p < more ? 1 : 0)) * scale;
+        for (int share = s0; share < shares; share += step) {
+            const int p0 = share * len, p1 = min(p0 + len, lanes);
+            const float c = ((p1 - p0) * base + max(min(more, p1) - p0, 0)) * scale;
             for (int k = k0; k < per; k += 1 << wide) {
-                const float2 v = first[p * stride + k];
+                const float2 v = first[p0 * stride + k];
                 const float d = v.x - mean;
                 dev += v.y + c * d * d;
             }
         }
         dev = lanes_sum(dev, team);
-        if (t == 0 && u0 + me < items * parts) {
-            if (parts == 1)
-                out[item] = make_float2(mean, dev);
-            else
-                spare[u] = make_float4(n, mean, dev, 0.f);
-        }
+        if (t == 0 && i0 + me < items)
+            out[item] = make_float2(mean, dev);
     }
-    if (parts > 1) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < items; i += blockDim.x) {
-            Triples<true> j;
-            j.clear();
-            for (int k = 0; k < parts; ++k) {
-                const float4 v = spare[k * items + i];
-                const float mu[1] = {v.y}, dv[1] = {v.z};
-                j.join(v.x, mu, dv);
-            }
-            out[i] = make_float2(j.mean[0], j.m2[0]);
-        }
+}
+
+// (mean, M2) of the parts v[0], v[step], ... of the ranges of `range` rows that
+// `rows` rows make, `per` elements to a row.
+__device__ __forceinline__ float2 join_ranges(const float2* v, int step, int count, int rows, int range, float per)
+{
+    float n = 0.f, sum = 0.f, dev = 0.f;
+    int left = rows;
+#pragma unroll 4
+    for (int r = 0; r < count; ++r) {
+        const float c = static_cast<float>(min(left, range));
+        n += c;
+        sum += c * v[r * step].x;
+        left = max(left - range, 0);
     }
+    const float mean = n > 0.f ? __fdividef(sum, n) : 0.f;
+    left = rows;
+#pragma unroll 4
+    for (int r = 0; r < count; ++r) {
+        const float2 u = v[r * step];
+        const float d = u.x - mean;
+        dev += u.y + static_cast<float>(min(left, range)) * per * d * d;
+        left = max(left - range, 0);
+    }
+    return make_float2(mean, dev);
 }
 
 // --------------------------------------------------------- sums of pairs
