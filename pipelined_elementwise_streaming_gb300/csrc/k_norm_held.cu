@@ -30,7 +30,10 @@ namespace {
 
 using namespace dev;
 
-constexpr int kAskGroups = 8;   // cp.async groups
+// Rows of a thread to a cp.async group, and groups on their way ahead of the
+// one in use.  Octs that are no vectors are loaded at once: nothing of theirs
+// goes on while a thread computes.
+constexpr int kAhead = 3, kAskRows = 4, kGradAhead = 2, kGradAskRows = 2;
 
 // Which rows a thread holds: lane, lane + lanes, ... of its sample's part.
 struct HeldPlace {
@@ -74,13 +77,6 @@ __device__ __forceinline__ void share_sums(const float2* sums, int items, int ra
     cluster_wait();
 }
 
-// Rows to a cp.async group: all that a lane may have in at most kAskGroups
-// groups of whole fours.
-__device__ __forceinline__ int rows_to_group(const NormLayout& lay)
-{
-    return ((lay.lane_rows + kAskGroups - 1) / kAskGroups + 3) / 4 * 4;
-}
-
 // A thread's octs of one operand in shared memory.  Octs that are no vectors
 // go through registers.
 template <int DT, bool VEC>
@@ -91,19 +87,32 @@ struct Slots {
         : at(smem_addr(shared) + threadIdx.x * 16), step(blockDim.x * 16)
     {
     }
-    __device__ __forceinline__ void ask(int i, const char* from, const OctAt& oct) const
+    // The walk's next N octs, of which n exist, to the places from i on.
+    template <int N>
+    __device__ __forceinline__ void ask(int i, int n, const Walk& w, const OctAt& oct) const
     {
         if constexpr (VEC) {
 #pragma unroll
-            for (uint32_t h = 0; h < kVecs; ++h)
-                cp_async(at + (i * kVecs + h) * step, from + 16 * h, 16, 16);
-        } else {
-            const Oct<DT> o = oct_load<DT, false>(from, oct);
+            for (int k = 0; k < N; ++k)
+                if (k < n)
 #pragma unroll
-            for (uint32_t h = 0; h < kVecs; ++h)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (i * kVecs + h) * step),
-                             "r"(o.w[4 * h]), "r"(o.w[4 * h + 1]), "r"(o.w[4 * h + 2]), "r"(o.w[4 * h + 3])
-                             : "memory");
+                    for (uint32_t h = 0; h < kVecs; ++h)
+                        cp_async(at + ((i + k) * kVecs + h) * step, w.p + k * w.step + 16 * h, 16, 16);
+        } else {
+            Oct<DT> o[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (k < n)
+                    o[k] = oct_load<DT, false>(w.p + k * w.step, oct);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (k < n)
+#pragma unroll
+                    for (uint32_t h = 0; h < kVecs; ++h)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((i + k) * kVecs + h) * step),
+                                     "r"(o[k].w[4 * h]), "r"(o[k].w[4 * h + 1]), "r"(o[k].w[4 * h + 2]),
+                                     "r"(o[k].w[4 * h + 3])
+                                     : "memory");
         }
     }
     __device__ __forceinline__ Oct<DT> take(int i) const
@@ -147,29 +156,27 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     float2* slots = all + (lay.ranks > 1 ? lay.ranks * items : 0);   // [P][stride]
     if (lay.ranks > 1)
         cluster_arrive();
-    const int each = rows_to_group(lay);
-    {
-        Walk w = walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
-        for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
-            for (int i = i0; i < min(i0 + each, mine); ++i) {
-                rows.ask(i, w.p, s.at);
-                w.p += w.step;
-            }
-            cp_async_commit();
-        }
-    }
+    Walk w = walk<DT>(x, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
+    auto ask = [&](int i) {
+        rows.template ask<kAskRows>(i, mine - i, w, s.at);
+        cp_async_commit();
+        w.p += kAskRows * w.step;
+    };
+    const int first = VEC ? kAhead * kAskRows : mine;
+    for (int i = 0; i < first; i += kAskRows)
+        ask(i);
     Affine<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
     Triples<BY_OCT> t;
     t.clear();
-    int pending = (lay.lane_rows + each - 1) / each;
-    for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
-        cp_async_wait(--pending);
-        for (int i = i0; i < min(i0 + each, mine); i += 4) {
-            Oct<DT> o[4];
-            rows.take4(i, mine, o);
-            t.add_octs(o, mine - i);
+    for (int i = 0; i < mine; i += kAskRows) {
+        if constexpr (VEC) {
+            ask(i + kAhead * kAskRows);
+            cp_async_wait(kAhead);
         }
+        Oct<DT> o[4];
+        rows.take4(i, mine, o);
+        t.add_octs(o, mine - i);
     }
     if (s.p < lay.P && s.at.ch < s.at.cols)   // absent samples leave zeros
         t.leave(s.at, slots + s.p * stride);
@@ -252,28 +259,39 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     let_next_start();
     if (lay.ranks > 1)
         cluster_arrive();
-    const int each = rows_to_group(lay);
     const GradWalk<DT, VEC, HELD> walk_rows(a, s, dy, x, h.row0 + h.lane, lay.lanes);
-    {
-        GradWalk<DT, VEC, HELD> w = walk_rows;
-        for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
-            for (int i = i0; i < min(i0 + each, mine); ++i) {
-                rows.ask(i, w.dy.p, s.at);
-                if constexpr (HELD && VEC) {
-                    cp_async(qs + i * threads * 8, w.q, 8, 8);
-                    cp_async(scales + i * threads * 4, w.scale, 4, 4);
-                } else if constexpr (HELD) {
-                    const Held q = held_load<false>(w.q, s.at);
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qs + i * threads * 8), "r"(q.w[0]), "r"(q.w[1])
-                                 : "memory");
-                } else {
-                    xs.ask(i, w.x.p, s.at);
+    GradWalk<DT, VEC, HELD> w = walk_rows;
+    auto ask = [&](int i) {
+        constexpr int N = kGradAskRows;
+        rows.template ask<N>(i, mine - i, w.dy, s.at);
+        if constexpr (!HELD) {
+            xs.template ask<N>(i, mine - i, w.x, s.at);
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (i + k < mine) {
+                    cp_async(qs + (i + k) * threads * 8, w.q + k * w.q_step, 8, 8);
+                    cp_async(scales + (i + k) * threads * 4, w.scale + k * w.scale_step, 4, 4);
                 }
-                w.advance(1);
-            }
-            cp_async_commit();
+        } else {
+            Held q[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (i + k < mine)
+                    q[k] = held_load<false>(w.q + k * w.q_step, s.at);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (i + k < mine)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qs + (i + k) * threads * 8), "r"(q[k].w[0]),
+                                 "r"(q[k].w[1])
+                                 : "memory");
         }
-    }
+        cp_async_commit();
+        w.advance(N);
+    };
+    const int first = VEC ? kGradAhead * kGradAskRows : mine;
+    for (int i = 0; i < first; i += kGradAskRows)
+        ask(i);
     auto take = [&](int i, GradRow<DT, VEC, HELD>& g) {
         g.dy = rows.take(i);
         if constexpr (HELD) {
@@ -300,23 +318,26 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-    int pending = (lay.lane_rows + each - 1) / each;
-    for (int i0 = 0; i0 < lay.lane_rows; i0 += each) {
-        cp_async_wait(--pending);
-#pragma unroll 2
-        for (int i = i0; i < min(i0 + each, mine); ++i) {
-            GradRow<DT, VEC, HELD> g;
-            float2 fd[4], hat[4], dz[4];
-            take(i, g);
-            oct_floats(g.dy, fd);
-            g.hats(a, k, hat);
-            k.slopes(a, fd, hat, dz);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sz[j] = __fadd2_rn(sz[j], dz[j]);
-                szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
-            }
+    for (int i0 = 0; i0 < mine; i0 += kGradAskRows) {
+        if constexpr (VEC) {
+            ask(i0 + kGradAhead * kGradAskRows);
+            cp_async_wait(kGradAhead);
         }
+#pragma unroll
+        for (int i = i0; i < i0 + kGradAskRows; ++i)
+            if (i < mine) {
+                GradRow<DT, VEC, HELD> g;
+                float2 fd[4], hat[4], dz[4];
+                take(i, g);
+                oct_floats(g.dy, fd);
+                g.hats(a, k, hat);
+                k.slopes(a, fd, hat, dz);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sz[j] = __fadd2_rn(sz[j], dz[j]);
+                    szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+                }
+            }
     }
     if (s.p < lay.P && s.at.ch < s.at.cols)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
