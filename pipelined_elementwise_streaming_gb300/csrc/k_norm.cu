@@ -29,7 +29,6 @@ namespace {
 using namespace dev;
 
 constexpr int kPartsAtOnce = 16;   // parts that a thread of the gradient's second kernel loads at once
-constexpr int kGradRows = 2;   // rows that a thread loads at once where they go element by element
 
 // CTAs to an SM that the registers are cut for.
 template <int DT>
@@ -223,42 +222,49 @@ __device__ __forceinline__ void load_stats(const NormArgs& a, const NormPlace& s
     __syncthreads();
 }
 
-// use(row) for each of a thread's `rows` rows, through the queue where they are
-// vectors; begin() runs once the first are on their way.
+// use(g, n) for a thread's `rows` rows, two of them, g, at a time, of which n
+// exist, through the queue where they are vectors; begin() runs once the first
+// are on their way.  The loop over the queue's batches stays a loop: unrolled,
+// with a choice of the activation in each batch, the kernels are so long that
+// fetching them shows (a step of bf16 [4, 16384, 512] over an int8 checkpoint,
+// whose kernels follow one another, 108.4 us against 100.7).
 template <int DT, bool VEC, bool HELD, class Begin, class Use>
-__device__ __forceinline__ void each_row(const NormArgs& a, const NormPlace& s, GradWalk<DT, VEC, HELD> w,
+__device__ __forceinline__ void each_two(const NormArgs& a, const NormPlace& s, GradWalk<DT, VEC, HELD> w,
                                          char* queue, int rows, Begin begin, Use use)
 {
     if constexpr (VEC) {
         GradQueue<DT, HELD> q(w, queue, rows);
         begin();
         for (int left = rows; left > 0; left -= q.kRows)
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < q.kBatches; ++b) {
                 cp_async_wait(q.kBatches - 1);
-                GradRow<DT, true, HELD> g[kQueueBatch];
+                const int n = left - b * kQueueBatch;
+                if (n > 0) {
+                    GradRow<DT, true, HELD> g[kQueueBatch];
 #pragma unroll
-                for (int i = 0; i < kQueueBatch; ++i)
-                    if (b * kQueueBatch + i < left) {
-                        q.take(b, i, g[i]);
-                        use(g[i]);
-                    }
+                    for (int i = 0; i < kQueueBatch; ++i)
+                        if (i < n)
+                            q.take(b, i, g[i]);
+                        else
+                            g[i].clear();
+                    use(g, n);
+                }
                 q.ask(b);
             }
         cp_async_wait(0);
     } else {
         begin();
-        for (int i0 = 0; i0 < rows; i0 += kGradRows) {
-            GradRow<DT, VEC, HELD> g[kGradRows];
+        for (int left = rows; left > 0; left -= kQueueBatch) {
+            GradRow<DT, VEC, HELD> g[kQueueBatch];
 #pragma unroll
-            for (int i = 0; i < kGradRows; ++i)
-                if (i0 + i < rows)
+            for (int i = 0; i < kQueueBatch; ++i)
+                if (i < left)
                     g[i].load(a, s, w, i);
-            w.advance(kGradRows);
-#pragma unroll
-            for (int i = 0; i < kGradRows; ++i)
-                if (i0 + i < rows)
-                    use(g[i]);
+                else
+                    g[i].clear();
+            w.advance(kQueueBatch);
+            use(g, left);
         }
     }
 }
@@ -294,16 +300,22 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
     const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin, [&](const GradRow<DT, VEC, HELD>& g) {
-        float2 fd[4], hat[4], dz[4];
-        oct_floats(g.dy, fd);
-        g.hats(a, k, hat);
-        k.slopes(a, fd, hat, dz);
+    each_two<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin,
+                            [&](const GradRow<DT, VEC, HELD>(&g)[kQueueBatch], int) {
+        by_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            sz[j] = __fadd2_rn(sz[j], dz[j]);
-            szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
-        }
+            for (int i = 0; i < kQueueBatch; ++i) {
+                float2 fd[4], hat[4], dz[4];
+                oct_floats(g[i].dy, fd);
+                g[i].hats(a.form, k, hat);
+                k.slopes(act, fd, hat, dz);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sz[j] = __fadd2_rn(sz[j], dz[j]);
+                    szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+                }
+            }
+        });
     });
     if (s.live)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
@@ -437,14 +449,21 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
         k.statistics(a, s, stats);
         to.set(a, s, k, sums);
     };
-    each_row<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin, [&](const GradRow<DT, VEC, HELD>& g) {
-        float2 fd[4], hat[4], dz[4], v[4];
-        oct_floats(g.dy, fd);
-        g.hats(a, k, hat);
-        k.slopes(a, fd, hat, dz);
-        to.of(k, dz, hat, v);
-        oct_store<DT, VEC>(out.p, s.at, oct_round<DT>(v));
-        out.p += out.step;
+    each_two<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin,
+                            [&](const GradRow<DT, VEC, HELD>(&g)[kQueueBatch], int n) {
+        by_act(a.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < kQueueBatch; ++i) {
+                float2 fd[4], hat[4], dz[4], v[4];
+                oct_floats(g[i].dy, fd);
+                g[i].hats(a.form, k, hat);
+                k.slopes(act, fd, hat, dz);
+                to.of(k, dz, hat, v);
+                if (i < n)
+                    oct_store<DT, VEC>(out.p + i * out.step, s.at, oct_round<DT>(v));
+            }
+        });
+        out.p += kQueueBatch * out.step;
     });
 }
 

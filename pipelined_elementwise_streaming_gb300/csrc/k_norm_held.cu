@@ -292,16 +292,26 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     const int first = VEC ? kGradAhead * kGradAskRows : mine;
     for (int i = 0; i < first; i += kGradAskRows)
         ask(i);
-    auto take = [&](int i, GradRow<DT, VEC, HELD>& g) {
-        g.dy = rows.take(i);
-        if constexpr (HELD) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(g.q.w[0]), "=r"(g.q.w[1]) : "r"(qs + i * threads * 8));
-            if constexpr (VEC)
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g.scale[0]) : "r"(scales + i * threads * 4));
-            else
-                g.load_scales(a, s, walk_rows, i);   // one to a channel: again from L1 or L2
-        } else {
-            g.x = xs.take(i);
+    // rows i, i + 1, ...; those past the thread's last are zeros
+    auto take = [&](int i, GradRow<DT, VEC, HELD>(&g)[kGradAskRows]) {
+#pragma unroll
+        for (int n = 0; n < kGradAskRows; ++n) {
+            if (i + n >= mine) {
+                g[n].clear();
+                continue;
+            }
+            g[n].dy = rows.take(i + n);
+            if constexpr (HELD) {
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(g[n].q.w[0]), "=r"(g[n].q.w[1])
+                             : "r"(qs + (i + n) * threads * 8));
+                if constexpr (VEC)
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g[n].scale[0]) : "r"(scales + (i + n) * threads * 4));
+                else
+                    g[n].load_scales(a, s, walk_rows, i + n);   // one to a channel: again from L1 or L2
+            } else {
+                g[n].x = xs.take(i + n);
+            }
         }
     };
     Chan<BY_OCT> k;
@@ -323,21 +333,22 @@ __global__ void __launch_bounds__(kNormThreads, 2)
             ask(i0 + kGradAhead * kGradAskRows);
             cp_async_wait(kGradAhead);
         }
+        GradRow<DT, VEC, HELD> g[kGradAskRows];
+        take(i0, g);
+        by_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int i = i0; i < i0 + kGradAskRows; ++i)
-            if (i < mine) {
-                GradRow<DT, VEC, HELD> g;
+            for (int i = 0; i < kGradAskRows; ++i) {
                 float2 fd[4], hat[4], dz[4];
-                take(i, g);
-                oct_floats(g.dy, fd);
-                g.hats(a, k, hat);
-                k.slopes(a, fd, hat, dz);
+                oct_floats(g[i].dy, fd);
+                g[i].hats(a.form, k, hat);
+                k.slopes(act, fd, hat, dz);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     sz[j] = __fadd2_rn(sz[j], dz[j]);
                     szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
                 }
             }
+        });
     }
     if (s.p < lay.P && s.at.ch < s.at.cols)
         leave_sums(s.at, sz, szx, slots + s.p * stride);
@@ -369,17 +380,22 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     Gradient<BY_OCT> grad;
     grad.set(a, s, k, stats + (s.live ? h.q : 0) * s.groups);
     WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
-#pragma unroll 2
-    for (int i = 0; i < mine; ++i) {
-        GradRow<DT, VEC, HELD> g;
-        float2 fd[4], hat[4], dz[4], res[4];
-        take(i, g);
-        oct_floats(g.dy, fd);
-        g.hats(a, k, hat);
-        k.slopes(a, fd, hat, dz);
-        grad.of(k, dz, hat, res);
-        oct_store<DT, VEC>(to.p, s.at, oct_round<DT>(res));
-        to.p += to.step;
+    for (int i0 = 0; i0 < mine; i0 += kGradAskRows) {
+        GradRow<DT, VEC, HELD> g[kGradAskRows];
+        take(i0, g);
+        by_act(a.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < kGradAskRows; ++i) {
+                float2 fd[4], hat[4], dz[4], res[4];
+                oct_floats(g[i].dy, fd);
+                g[i].hats(a.form, k, hat);
+                k.slopes(act, fd, hat, dz);
+                grad.of(k, dz, hat, res);
+                if (i0 + i < mine)
+                    oct_store<DT, VEC>(to.p + i * to.step, s.at, oct_round<DT>(res));
+            }
+        });
+        to.p += kGradAskRows * to.step;
     }
 }
 

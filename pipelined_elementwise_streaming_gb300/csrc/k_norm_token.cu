@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
                 float2 fd[4], t1 = make_float2(0.f, 0.f), t2 = t1;
                 oct_floats(g[i].dy, fd);
                 k.statistics(mu[i], rs[i]);
-                g[i].hats(a, k, hat[i]);
-                k.slopes(a, fd, hat[i], dz[i]);
+                g[i].hats(a.form, k, hat[i]);
+                k.slopes(a.act, fd, hat[i], dz[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 dzx = __fmul2_rn(dz[i][j], hat[i][j]);

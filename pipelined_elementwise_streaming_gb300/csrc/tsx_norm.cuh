@@ -595,14 +595,14 @@ struct Chan {
         rstd.v[0] = pair_of(rs);
     }
     // dz
-    __device__ __forceinline__ void slopes(const NormArgs& a, const float2 (&dy)[4], const float2 (&xhat)[4],
+    __device__ __forceinline__ void slopes(int act, const float2 (&dy)[4], const float2 (&xhat)[4],
                                            float2 (&dz)[4]) const
     {
         float2 t[4], slope[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             t[j] = __ffma2_rn(xhat[j], w[j], b[j]);
-        act_slope(a.act, t, slope);
+        act_slope(act, t, slope);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             dz[j] = __fmul2_rn(dy[j], slope[j]);
@@ -737,6 +737,19 @@ struct GradRow {
             x = oct_load<DT, VEC>(w.x.p + i * w.x.step, s.at);
         }
     }
+    // A row that does not exist: its dz is 0.
+    __device__ __forceinline__ void clear()
+    {
+        oct_zero(dy);
+        if constexpr (HELD) {
+            q.w[0] = q.w[1] = 0;
+#pragma unroll
+            for (int j = 0; j < (VEC ? 1 : 8); ++j)
+                scale[j] = 0.f;
+        } else {
+            oct_zero(x);
+        }
+    }
     __device__ __forceinline__ void load_scales(const NormArgs& a, const NormPlace& s,
                                                 const GradWalk<DT, VEC, HELD>& w, int i)
     {
@@ -752,13 +765,13 @@ struct GradRow {
     }
     // xhat = (x - mean) rstd, of a checkpoint with x = q scale
     template <bool BY_OCT>
-    __device__ __forceinline__ void hats(const NormArgs& a, const Chan<BY_OCT>& k, float2 (&hat)[4]) const
+    __device__ __forceinline__ void hats(int form, const Chan<BY_OCT>& k, float2 (&hat)[4]) const
     {
         float2 f[4];
         if constexpr (!HELD)
             oct_floats(x, f);
         else
-            held_numbers(q, a.form, f);
+            held_numbers(q, form, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float2 d;
