@@ -95,9 +95,7 @@ struct Slots {
 #pragma unroll
             for (int k = 0; k < N; ++k)
                 if (k < n)
-#pragma unroll
-                    for (uint32_t h = 0; h < kVecs; ++h)
-                        cp_async(at + ((i + k) * kVecs + h) * step, w.p + k * w.step + 16 * h, 16, 16);
+                    oct_async<DT>(at + (i + k) * kVecs * step, step, w.p + k * w.step);
         } else {
             Oct<DT> o[N];
 #pragma unroll

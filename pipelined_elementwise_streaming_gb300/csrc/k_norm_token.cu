@@ -4,25 +4,14 @@
 // barrier.  HBM bounds it.  A CTA walks rows so that weight and bias (and the
 // sums for their gradients) stay in registers.
 
+#include <algorithm>
+
 #include "tsx_norm.cuh"
 
 namespace tsx {
 namespace {
 
 using namespace dev;
-
-constexpr int kTokenGradRows = 2;   // rows whose loads a thread issues before it uses the first
-
-// How many of a thread's next N rows, P apart, exist with `left` rows to go.
-template <int N>
-__device__ __forceinline__ int rows_at(int64_t left, int P)
-{
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        n += left > i * P ? 1 : 0;
-    return n;
-}
 
 // Sums over each group's lanes, all rows at once: the shuffles of one row hide
 // the latency of another's.
@@ -129,77 +118,103 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
     norm_token_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias,
                            const float* mean, const float* rstd, void* dx, float* chan)
 {
-    extern __shared__ float2 shared[];
+    extern __shared__ float4 shared4[];   // the queue, then the sums for dweight and dbias
+    constexpr int N = kQueueBatch;
     const NormPlace s = norm_place<true>(a);
     const int lanes = a.per_group / 8;
     const float minus_m = -1.f / static_cast<float>(a.per_group);
+    const int group = s.group0 + local_group(a, s.at.ch);
+    const int P = a.lay.P, step_s = P * a.groups;
+    const int64_t share = a.lay.range, first_row = static_cast<int64_t>(blockIdx.x) * share, row0 = first_row + s.p;
+    const int rows = static_cast<int>(min(share, a.n - first_row));
+    const int mine = s.live && s.p < rows ? (rows - s.p + P - 1) / P : 0;
+    let_next_start();
+    GradQueue<DT, HELD> queue(GradWalk<DT, true, HELD>(a, s, dy, x, row0, P), reinterpret_cast<char*>(shared4), mine);
+    // statistics of the next rows: they come a batch ahead, as two loads in
+    // 16 lanes of a group are not worth a queue
+    const float* pm = mean + row0 * a.groups + group;
+    const float* pr = rstd + row0 * a.groups + group;
+    float next_mu[N], next_rs[N];
+    auto ask_stats = [&](int left) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            next_mu[i] = i < left ? __ldg(pm + i * step_s) : 0.f;
+            next_rs[i] = i < left ? __ldg(pr + i * step_s) : 0.f;
+        }
+        pm += N * step_s;
+        pr += N * step_s;
+    };
+    ask_stats(mine);
     Chan<true> k;
     k.params<DT, true>(a, s, weight, bias);
-    const int group = s.group0 + local_group(a, s.at.ch);
-    const int P = a.lay.P;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (P * kTokenGradRows);
-    let_next_start();
-    const int step_s = P * a.groups;
+    WalkOut to = walk_out<DT>(dx, row0, P, a.x_pitch, s);
     float2 sz[4], szx[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         sz[j] = szx[j] = make_float2(0.f, 0.f);
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kTokenGradRows); base < a.n; base += stride) {
-        const int64_t row0 = base + s.p;
-        const int n = s.live ? rows_at<kTokenGradRows>(a.n - row0, P) : 0;
-        const GradWalk<DT, true, HELD> w(a, s, dy, x, row0, P);
-        GradRow<DT, true, HELD> g[kTokenGradRows];
-        const float* pm = mean + row0 * a.groups + group;
-        const float* pr = rstd + row0 * a.groups + group;
-        float mu[kTokenGradRows], rs[kTokenGradRows];
+    const int loop = (rows + P - 1) / P;   // every lane of a warp comes to the shuffles
+    for (int done = 0; done < loop; done += queue.kRows)
+#pragma unroll 1
+        for (int b = 0; b < queue.kBatches && done + b * N < loop; ++b) {
+            const int n = mine - done - b * N;
+            float mu[N], rs[N];
 #pragma unroll
-        for (int i = 0; i < kTokenGradRows; ++i)
-            if (i < n) {
-                g[i].load(a, s, w, i);
-                mu[i] = __ldg(pm + i * step_s);
-                rs[i] = __ldg(pr + i * step_s);
+            for (int i = 0; i < N; ++i) {
+                mu[i] = next_mu[i];
+                rs[i] = next_rs[i];
             }
-        float2 hat[kTokenGradRows][4], dz[kTokenGradRows][4];
-        float s1[kTokenGradRows], s2[kTokenGradRows];
+            ask_stats(n - N);
+            cp_async_wait(queue.kBatches - 1);
+            GradRow<DT, true, HELD> g[N];
 #pragma unroll
-        for (int i = 0; i < kTokenGradRows; ++i) {
-            s1[i] = s2[i] = 0.f;
-            if (i < n) {
-                float2 fd[4], t1 = make_float2(0.f, 0.f), t2 = t1;
-                oct_floats(g[i].dy, fd);
-                k.statistics(mu[i], rs[i]);
-                g[i].hats(a.form, k, hat[i]);
-                k.slopes(a.act, fd, hat[i], dz[i]);
+            for (int i = 0; i < N; ++i)
+                if (i < n)
+                    queue.take(b, i, g[i]);
+                else
+                    g[i].clear();
+            by_act(a.act, [&](auto act) {
+                float2 hat[N][4], dz[N][4];
+                float s1[N], s2[N];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 dzx = __fmul2_rn(dz[i][j], hat[i][j]);
-                    sz[j] = __fadd2_rn(sz[j], dz[i][j]);
-                    szx[j] = __fadd2_rn(szx[j], dzx);
-                    t1 = __ffma2_rn(dz[i][j], k.w[j], t1);
-                    t2 = __ffma2_rn(dzx, k.w[j], t2);
+                for (int i = 0; i < N; ++i) {
+                    float2 fd[4], t1 = make_float2(0.f, 0.f), t2 = t1;
+                    oct_floats(g[i].dy, fd);
+                    k.statistics(mu[i], rs[i]);
+                    g[i].hats(a.form, k, hat[i]);
+                    k.slopes(act, fd, hat[i], dz[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 dzx = __fmul2_rn(dz[i][j], hat[i][j]);
+                        sz[j] = __fadd2_rn(sz[j], dz[i][j]);
+                        szx[j] = __fadd2_rn(szx[j], dzx);
+                        t1 = __ffma2_rn(dz[i][j], k.w[j], t1);
+                        t2 = __ffma2_rn(dzx, k.w[j], t2);
+                    }
+                    s1[i] = t1.x + t1.y;
+                    s2[i] = t2.x + t2.y;
                 }
-                s1[i] = t1.x + t1.y;
-                s2[i] = t2.x + t2.y;
-            }
-        }
-        team_sums(s1, lanes);
-        team_sums(s2, lanes);
-        const WalkOut to = walk_out<DT>(dx, row0, P, a.x_pitch, s);
+                team_sums(s1, lanes);
+                team_sums(s2, lanes);
 #pragma unroll
-        for (int i = 0; i < kTokenGradRows; ++i)
-            if (i < n) {
-                Gradient<true> grad;
-                float2 out[4];
-                k.statistics(mu[i], rs[i]);
-                grad.set(a, k, s1[i] * minus_m, s2[i] * minus_m);
-                grad.of(k, dz[i], hat[i], out);
-                oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(out));
-            }
-    }
+                for (int i = 0; i < N; ++i) {
+                    Gradient<true> grad;
+                    float2 out[4];
+                    k.statistics(mu[i], rs[i]);
+                    grad.set(a, k, s1[i] * minus_m, s2[i] * minus_m);
+                    grad.of(k, dz[i], hat[i], out);
+                    if (i < n)
+                        oct_store<DT, true>(to.p + i * to.step, s.at, oct_round<DT>(out));
+                }
+            });
+            queue.ask(b);
+            to.p += N * to.step;
+        }
+    cp_async_wait(0);
+    __syncthreads();
     const int width = s.at.cols, slot = slot_stride(width);
-    float2* work = shared;                      // [threads]
-    float2* columns = work + kTokenThreads;     // [run_cols]
-    float2* slots = columns + a.lay.run_cols;   // [P][stride]
+    float2* work = reinterpret_cast<float2*>(shared4);   // [threads]
+    float2* columns = work + kTokenThreads;              // [run_cols]
+    float2* slots = columns + a.lay.run_cols;            // [P][stride]
     if (s.live)
         leave_sums(s.at, sz, szx, slots + s.p * slot);
     __syncthreads();
@@ -237,18 +252,20 @@ cudaError_t launch_norm_token_backward(int dtype, const NormArgs& a, const void*
     const dim3 grid(unsigned(a.lay.splits), unsigned(a.lay.runs));
     const size_t slots =
         (kTokenThreads + a.lay.run_cols + size_t(a.lay.P) * slot_stride(a.lay.run_cols)) * sizeof(float2);
-#define CALL(DT)                                                                                              \
-    if (x.q)                                                                                                  \
-        norm_token_grad_kernel<DT, true>                                                                      \
-            <<<grid, a.lay.threads, slots, st>>>(a, dy, x, weight, bias, mean, rstd, dx, scratch.chan);       \
-    else                                                                                                      \
-        norm_token_grad_kernel<DT, false>                                                                     \
-            <<<grid, a.lay.threads, slots, st>>>(a, dy, x, weight, bias, mean, rstd, dx, scratch.chan)
+    cudaError_t e = cudaSuccess;
+#define CALL(DT)                                                                                                 \
+    e = x.q ? launch_grid<norm_token_grad_kernel<DT, true>>(grid, a.lay.threads,                                 \
+                                                            std::max(slots, GradQueue<DT, true>::kBytes), 1,     \
+                                                            false, st, a, dy, x, weight, bias, mean, rstd, dx,   \
+                                                            scratch.chan)                                        \
+            : launch_grid<norm_token_grad_kernel<DT, false>>(grid, a.lay.threads,                                \
+                                                             std::max(slots, GradQueue<DT, false>::kBytes), 1,   \
+                                                             false, st, a, dy, x, weight, bias, mean, rstd, dx,  \
+                                                             scratch.chan)
     if (dtype == TSX_F16) { CALL(TSX_F16); }
     else if (dtype == TSX_BF16) { CALL(TSX_BF16); }
     else { CALL(TSX_F32); }
 #undef CALL
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     return launch_norm_params(a, a.lay.splits, scratch.chan, dweight, dbias, st);

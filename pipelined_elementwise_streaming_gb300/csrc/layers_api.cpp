@@ -390,9 +390,8 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     const int64_t most = (d.n + at_once - 1) / at_once;
     const int64_t want = (backward ? kTokenGradCtas : kTokenCtas) / lay.runs;
     lay.splits = most < want ? most : want < 1 ? 1 : want;
-    lay.range = (d.n + lay.splits - 1) / lay.splits;   // forward: rows to a CTA
-    if (!backward)
-        lay.splits = (d.n + lay.range - 1) / lay.range;
+    lay.range = (d.n + lay.splits - 1) / lay.splits;   // rows to a CTA
+    lay.splits = (d.n + lay.range - 1) / lay.range;
     *out = lay;
     return true;
 }

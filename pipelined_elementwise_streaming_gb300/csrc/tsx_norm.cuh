@@ -786,6 +786,22 @@ struct GradRow {
     }
 };
 
+// An oct's 16-byte vectors on their way to shared memory, `step` apart there.
+template <int DT>
+__device__ __forceinline__ void oct_async(uint32_t dst, uint32_t step, const char* from)
+{
+    if constexpr (DT != TSX_F32) {
+        cp_async(dst, from, 16, 16);
+    } else {
+        // Neighbouring threads' vectors are 32 bytes apart, so each of the two
+        // copies takes half of every sector: through L1 the sectors come once.
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst + h * step), "l"(from + 16 * h)
+                         : "memory");
+    }
+}
+
 // Rows of x on their way: a queue in shared memory that each thread fills by
 // cp.async for itself alone, so that no barrier guards it and the bytes in
 // flight do not depend on registers.  Four rows to a batch; kBatches batches
@@ -811,11 +827,8 @@ struct RowQueue {
     {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            if (i < left) {
-#pragma unroll
-                for (uint32_t h = 0; h < kVecs; ++h)
-                    cp_async(at + ((b * kBatch + i) * kVecs + h) * kStep, w.p + i * w.step + 16 * h, 16, 16);
-            }
+            if (i < left)
+                oct_async<DT>(at + (b * kBatch + i) * kVecs * kStep, kStep, w.p + i * w.step);
         cp_async_commit();
         w.p += kBatch * w.step;
         left -= kBatch;
@@ -897,6 +910,7 @@ struct GradQueue {
     static constexpr int kRows = queue_rows<DT>(), kBatches = kRows / kQueueBatch;
     static constexpr uint32_t kVecs = elem_size(DT) / 2;   // 16-byte vectors of an oct
     static constexpr uint32_t k16 = kNormThreads * 16, k8 = kNormThreads * 8, k4 = kNormThreads * 4;
+    static constexpr size_t kBytes = size_t(kRows) * kNormThreads * queue_row_bytes<DT, HELD>();
     GradWalk<DT, true, HELD> w;
     uint32_t dy, x, scale;   // this thread's place in the queue's arrays
     int left;                // rows that are still to be asked for
@@ -918,18 +932,12 @@ struct GradQueue {
         for (int i = 0; i < kQueueBatch; ++i)
             if (i < left) {
                 const uint32_t slot = b * kQueueBatch + i;
-                const char* pd = w.dy.p + i * w.dy.step;
-#pragma unroll
-                for (uint32_t h = 0; h < kVecs; ++h)
-                    cp_async(dy + (slot * kVecs + h) * k16, pd + 16 * h, 16, 16);
+                oct_async<DT>(dy + slot * kVecs * k16, k16, w.dy.p + i * w.dy.step);
                 if constexpr (HELD) {
                     cp_async(x + slot * k8, w.q + i * w.q_step, 8, 8);
                     cp_async(scale + slot * k4, w.scale + i * w.scale_step, 4, 4);
                 } else {
-                    const char* px = w.x.p + i * w.x.step;
-#pragma unroll
-                    for (uint32_t h = 0; h < kVecs; ++h)
-                        cp_async(x + (slot * kVecs + h) * k16, px + 16 * h, 16, 16);
+                    oct_async<DT>(x + slot * kVecs * k16, k16, w.x.p + i * w.x.step);
                 }
             }
         cp_async_commit();
