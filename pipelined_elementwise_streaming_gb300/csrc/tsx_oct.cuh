@@ -72,6 +72,11 @@ __device__ __forceinline__ char* oct_ptr(void* base, int64_t row, int64_t pitch,
     return static_cast<char*>(base) + (row * pitch + ch) * elem_size(DT);
 }
 
+// An fp32 oct is 32 bytes, which move at once where they are aligned to that:
+// in two halves every sector is asked for twice (tensors are only sure to be
+// aligned to 16).
+__device__ __forceinline__ bool whole_sector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 // The vector loads go past L1.  They are no read-only-cache loads, since an
 // output may be one of the inputs; every thread loads what it overwrites
 // before it stores.
@@ -80,13 +85,21 @@ __device__ __forceinline__ Oct<DT> oct_load(const char* p, const OctAt& at)
 {
     Oct<DT> o;
     if constexpr (VEC) {
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-            : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
-            : "l"(p));
-        if constexpr (DT == TSX_F32)
+        if constexpr (DT == TSX_F32) {
+            if (whole_sector(p)) {
+                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3]), "=r"(o.w[4]), "=r"(o.w[5]),
+                               "=r"(o.w[6]), "=r"(o.w[7])
+                             : "l"(p));
+                return o;
+            }
             asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                : "=r"(o.w[4]), "=r"(o.w[5]), "=r"(o.w[6]), "=r"(o.w[7])
-                : "l"(p + 16));
+                         : "=r"(o.w[4]), "=r"(o.w[5]), "=r"(o.w[6]), "=r"(o.w[7])
+                         : "l"(p + 16));
+        }
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
+                     : "l"(p));
     } else if constexpr (DT == TSX_F32) {
         const float* e = reinterpret_cast<const float*>(p);
 #pragma unroll
@@ -154,9 +167,16 @@ template <int DT, bool VEC>
 __device__ __forceinline__ void oct_store(char* p, const OctAt& at, const Oct<DT>& o)
 {
     if constexpr (VEC) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
-        if constexpr (DT == TSX_F32)
+        if constexpr (DT == TSX_F32) {
+            if (whole_sector(p)) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(o.w[0]), "r"(o.w[1]),
+                             "r"(o.w[2]), "r"(o.w[3]), "r"(o.w[4]), "r"(o.w[5]), "r"(o.w[6]), "r"(o.w[7])
+                             : "memory");
+                return;
+            }
             *reinterpret_cast<uint4*>(p + 16) = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
     } else if constexpr (DT == TSX_F32) {
         uint32_t* e = reinterpret_cast<uint32_t*>(p);
 #pragma unroll
