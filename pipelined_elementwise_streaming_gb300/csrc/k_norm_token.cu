@@ -31,7 +31,7 @@ __device__ __forceinline__ float oct_sum(const float2 (&f)[4])
 }
 
 template <int DT, bool HOLD>
-__global__ void __launch_bounds__(kTokenThreads, DT == TSX_F32 || HOLD ? 2 : 3)
+__global__ void __launch_bounds__(kTokenThreads, HOLD ? 2 : 3)
     norm_token_kernel(NormArgs a, const void* x, const void* weight, const void* bias, void* y, float* mean,
                       float* rstd, HeldOut held)
 {
