@@ -456,10 +456,18 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * ranks;
             if (ranks > 1 && ctas > kHeldWave)
                 continue;
-            // long samples in many CTAs: the backward pass would hold runs of
-            // 128 bytes only (bf16 [256, 256, 512]: 72 us against 58 streaming;
-            // [2000, 64, 256]: 81 against 113)
-            if (backward && d.l >= 128 && ctas > 2 * kHeldCtas)
+            // Backward, two operands and their sums leave room for narrow runs
+            // only, and the CTAs past the first wave pay for their parameters
+            // and sums again.  Short samples gain all the same (bf16 [2000,
+            // 64, 256] 74.6 us against 109.7 streaming, [700, 100, 128] 26.5
+            // against 31.6), longer ones do not ([128, 128, 512] 21.4 against
+            // 18.1, [64, 256, 512] 20.2 against 18.0, [256, 256, 512] 66.5
+            // against 57.9).
+            if (backward && d.l >= 128 && ctas > kHeldCtas)
+                continue;
+            // Nor do clusters whose loads go element by element, and so wait
+            // (fp32 [3, 1009, 198] 13.7 against 11.8, from int8 17.0, 14.8).
+            if (backward && !vec && ranks > 1)
                 continue;
             // the most CTAs, and of those the widest runs and fewest ranks
             if (ctas > best) {
