@@ -216,6 +216,14 @@ def test_norm_parameters_pitches_and_forms(tsx, dtype, param, form, block):
     check_norm(tsx, 3, 11, 130, 13, dtype, "gelu", 6, x_pitch=131, y_pitch=130, param=param, form=form, block=block)
 
 
+@pytest.mark.parametrize("shape", [(3001, 1, 512, 8), (40, 30, 64, 8), (2, 3000, 64, 4), (1, 1000, 320, 32)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_norm_of_rows_that_start_half_a_sector_apart(tsx, shape):
+    """fp32 rows that are aligned to 16 bytes, every other one to 32."""
+    n, l, c, groups = shape
+    check_norm(tsx, n, l, c, groups, "f32", "silu", 7, x_pitch=c + 4, y_pitch=c + 12)
+
+
 def test_norm_of_a_large_mean_keeps_its_digits(tsx):
     """Mean 1000, spread 1: E[x^2] - mean^2 in fp32 would leave an error of
     about 1000^2 2^-24 = 6 % in the variance.  Here it has to be as exact as
@@ -411,6 +419,22 @@ def test_gated_extremes(tsx):
 
 
 # ------------------------------------------------------------- checkpoints
+
+
+def test_gated_rows_that_start_half_a_sector_apart(tsx):
+    check_gated(tsx, 33, 200, "f32", "gelu", "int8", 64, 8, in_pitch=412, out_pitch=204)
+    check_gated(tsx, 7, 4096, "f32", "silu", "e4m3", 32, 9, in_pitch=8196, out_pitch=4100)
+
+
+def test_pack_of_rows_that_start_half_a_sector_apart(tsx):
+    x = dev(values((19, 1032), "f32", 3)[1], "f32")
+    wide = sliced(x, 1036)
+    for form in ("int8", "e4m3"):
+        op = tsx.Packer("f32", 19, 1032, form=form, block=128, pitch=1036)
+        saved = op.pack(wide)
+        check_held(saved, host(x), form, 128, form)
+        dense = tsx.Packer("f32", 19, 1032, form=form, block=128).unpack(saved)
+        assert torch.equal(op.unpack(saved), dense)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
