@@ -1,27 +1,33 @@
 // Group norm of samples that fit on chip: a CTA, or a cluster of CTAs that
 // share a sample's rows, holds a run of channels of a sample in shared memory,
-// so that its operands are read once.  The first step is bound by HBM; where
-// all samples fit on the chip at once, which is where this kernel is taken for
-// samples of more than one CTA, so is the whole but for one chain load - sum -
-// cluster barrier - store.
+// so that its operands are read once.
 //
 // Every thread fills its own slots of shared memory by cp.async and reads them
-// back itself, all rows at once on their way in up to eight groups, so that no
-// barrier guards them and the sums start with the first group.  The
-// statistics go through the CTA's shared memory (tsx_norm.cuh) and, in a
-// cluster, through every CTA's copy of the groups' sums: all ranks join the
-// ranks' sums in the same order, so they agree to the bit.  A CTA takes several
-// small samples side by side.
+// back itself, so that no barrier guards them: it asks for a few rows ahead and
+// sums those that have come.  The statistics go through the CTA's shared memory
+// (tsx_norm.cuh); in a cluster every rank puts its groups' sums into the others'
+// memory, and all join them in the same order, so they agree to the bit.  A CTA
+// takes several small samples side by side.
+//
+// What bounds it is the chain: loads, which overlap with the first sums; the
+// sums over the row lanes; the cluster's barrier; the second pass over the rows,
+// bound by the special-function unit with silu (an exponential and a reciprocal
+// an element, 12 cycles of a quarter SM for 32); the stores.  In cycles of a CTA
+// of f16 [8, 4096, 320]: 9 to 13 thousand, 4, 2, 8.  Two CTAs to an SM do not
+// fill one another's gaps where all of them run side by side.
 //
 // Measured on GB300, GPU time of a call in a CUDA graph, against the streaming
-// kernels: f16 [8, 4096, 320] forward 17.3 us (18.5), bf16 [4, 1024, 1280] 9.9
-// (16.9) and its gradient 16.3 (19.3).  The tensors' own time at HBM's rate is
-// 6.2, 3.1 and 4.6 us; what is left is the chain, of which the arithmetic of
-// two CTAs of 256 threads to an SM is the longest part.  Clusters of 16, or one
-// CTA of 512 threads to an SM, were slower: the SMs hold 14 clusters of 16 at
-// two CTAs to an SM, 36 of eight, and a second wave doubles the time (bf16 [16,
-// 1024, 640] with its checkpoint 46 us in 16 clusters of large CTAs, 21
-// streaming).
+// kernels, and HBM's own time at 6786 GB/s:
+//   forward   f16 [8, 4096, 320], 32 groups  14.6 us, streaming 17.6, HBM 6.2
+//             bf16 [4, 1024, 1280]            9.0             17.0      3.1
+//             bf16 [256, 256, 512]           32.3             42.2     19.8
+//             fp32 [2000, 64, 256]           47.4             83.5     38.6
+//   gradient  bf16 [4, 1024, 1280]           15.6             19.6      4.6
+//             bf16 [2000, 64, 256]           74.6            109.7     29.0
+// Clusters of 16, or one CTA of 512 threads to an SM, were slower: the SMs hold
+// 14 clusters of 16 at two CTAs to an SM, 36 of eight, and a second wave doubles
+// the time (bf16 [16, 1024, 640] with its checkpoint 46 us in 16 clusters of
+// large CTAs, 21 streaming).
 
 #include "tsx_norm.cuh"
 
@@ -31,7 +37,10 @@ namespace {
 using namespace dev;
 
 // Rows of a thread to a cp.async group, and groups on their way ahead of the
-// one in use.  Octs that are no vectors are loaded at once: nothing of theirs
+// one in use.  All rows asked for at once kept the threads from summing (f16 [8,
+// 4096, 320] 17.0 us, 15.5 so; forward 2 groups ahead 34.3 us against 32.2 for
+// bf16 [256, 256, 512], 4 ahead 16.0 against 15.6 for the first; backward 3
+// ahead 77.0 us against 75.4 for [2000, 64, 256]).  Octs that are no vectors are loaded at once: nothing of theirs
 // goes on while a thread computes.
 constexpr int kAhead = 3, kAskRows = 4, kGradAhead = 2, kGradAskRows = 2;
 

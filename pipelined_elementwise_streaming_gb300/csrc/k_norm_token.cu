@@ -1,8 +1,18 @@
 // Group norm of tokens (l = 1) whose groups are a power of two of octs, at
 // most a warp's 32: every group lies in neighbouring lanes of one warp, so its
-// sums are a few shuffles and a row is read once, with no shared memory and no
-// barrier.  HBM bounds it.  A CTA walks rows so that weight and bias (and the
-// sums for their gradients) stay in registers.
+// sums are a few shuffles, a row is read once, and no barrier stands between
+// its load and its store.  A CTA walks a contiguous share of the rows, so that
+// weight and bias (and the sums for their gradients) stay in registers; rows
+// on their way wait in a queue in shared memory that each thread fills for
+// itself.  As many CTAs as the SMs hold at once: three each, two where the
+// gradient or a checkpoint takes the registers.
+//
+// HBM bounds the larger calls, the launch the smallest.  Measured on GB300, GPU
+// time of a call in a CUDA graph, HBM's own time at 6786 GB/s in parentheses:
+// bf16 [8192, 4096] in 32 groups 22.3 us (19.8), 25.4 where nothing of it is
+// left in L2; with an int8 checkpoint 33.2 (24.9); its gradient 42.4 (29.7),
+// from registers in place of the queue 53.9; fp32 [4096, 4096] 21.7 (19.8);
+// bf16 [16, 4096] 3.0.
 
 #include <algorithm>
 

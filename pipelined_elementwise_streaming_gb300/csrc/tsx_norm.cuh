@@ -892,10 +892,11 @@ __device__ __forceinline__ void each_four(Walk w, const OctAt& at, char* queue, 
 }
 
 // The backward pass's rows on their way, dy and x or its checkpoint, the same
-// way.  The streaming kernels hold dz's sums, weights and statistics in over 50
-// registers; with four rows in registers beside them, 57 KB an SM were on their
-// way in bursts (sums of bf16 [4, 16384, 512] from int8: 34 us), with a queue
-// of eight rows twice that without a pause (31 us).
+// way.  The kernels hold dz's sums, weights and statistics in over 50 registers;
+// with four rows in registers beside them, 57 KB an SM were on their way in
+// bursts (sums of bf16 [4, 16384, 512] from int8: 34 us), with a queue of eight
+// rows twice that without a pause (31 us, and 27 with the first rows asked for
+// before the statistics).
 constexpr int kQueueBatch = 2;   // rows to a cp.async group
 template <int DT>
 TSX_HD constexpr int queue_rows() { return DT == TSX_F32 ? 4 : 8; }
