@@ -362,31 +362,46 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     }
 }
 
+// Columns to a CTA of the sums over slices: 32, or 8 where 32 would leave few
+// CTAs (the gradient of bf16 [2000, 64, 256]: 16 CTAs 75.0 us, 64 CTAs 71.8;
+// [1000, 33, 512] 44.4, 42.8; but [4, 1024, 1280] 15.7 in 80 CTAs, 15.9 in 320,
+// tokens [4000, 2048] 14.6 in 128, 16.2 in 512).
+constexpr int kParamCols = 32, kParamFew = 8, kParamCtas = 64;
+
 // dweight and dbias: the sums of the [slices][2][c] partial sums.  A CTA takes
-// 32 of the 2 c columns: every warp adds every warps-th slice, then the warps
-// are added in their order.
-constexpr int kParamCols = 32;
+// COLS of the 2 c columns, a warp 32 / COLS slices at a time; then a warp's
+// lanes and last the warps are added in their order.  work: [warps][COLS].
+template <int COLS>
 __device__ __forceinline__ void add_params(const float* chan, int64_t slices, int c, int64_t block, float* dweight,
                                            float* dbias, float* work)
 {
-    const int lane = static_cast<int>(threadIdx.x) % kParamCols, warp = static_cast<int>(threadIdx.x) / kParamCols;
-    const int warps = static_cast<int>(blockDim.x) / kParamCols;
-    const int64_t col = block * kParamCols + lane;   // of 2 c
+    const int lane = static_cast<int>(threadIdx.x) % 32, warp = static_cast<int>(threadIdx.x) / 32;
+    const int warps = static_cast<int>(blockDim.x) / 32, own = static_cast<int>(threadIdx.x) / COLS;
+    const int64_t col = block * COLS + lane % COLS;   // of 2 c
+    const bool real = col < 2 * static_cast<int64_t>(c);
     float t = 0.f;
-    if (col < 2 * static_cast<int64_t>(c)) {
+    if (real) {
 #pragma unroll 8
-        for (int64_t i = warp; i < slices; i += warps)
+        for (int64_t i = own; i < slices; i += blockDim.x / COLS)
             t += chan[i * 2 * c + col];
     }
-    work[warp * kParamCols + lane] = t;
+    for (int d = COLS; d < 32; d <<= 1)
+        t += __shfl_xor_sync(0xffffffffu, t, d);
+    if (lane < COLS)
+        work[warp * COLS + lane] = t;
     __syncthreads();
-    if (warp == 0 && col < 2 * static_cast<int64_t>(c)) {
-        for (int i = 1; i < warps; ++i)
-            t += work[i * kParamCols + lane];
-        if (col < c)
-            dweight[col] = t;
-        else
-            dbias[col - c] = t;
+    if (warp == 0) {
+        t = 0.f;
+        for (int i = lane / COLS; i < warps; i += 32 / COLS)
+            t += work[i * COLS + lane % COLS];
+        for (int d = COLS; d < 32; d <<= 1)
+            t += __shfl_xor_sync(0xffffffffu, t, d);
+        if (real && lane < COLS) {
+            if (col < c)
+                dweight[col] = t;
+            else
+                dbias[col - c] = t;
+        }
     }
 }
 
@@ -400,7 +415,7 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     const int64_t ranges = a.n * a.lay.splits;
     if (blockIdx.x >= ranges) {
         wait_for_last();
-        add_params(chan, ranges, a.c, (blockIdx.x - ranges) * gridDim.y + blockIdx.y, dweight, dbias,
+        add_params<kParamCols>(chan, ranges, a.c, (blockIdx.x - ranges) * gridDim.y + blockIdx.y, dweight, dbias,
                    reinterpret_cast<float*>(shared));
         return;
     }
@@ -467,12 +482,13 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     });
 }
 
+template <int COLS>
 __global__ void __launch_bounds__(1024)
     norm_params_kernel(const float* chan, int64_t slices, int c, float* dweight, float* dbias)
 {
-    __shared__ float work[1024];
+    __shared__ float work[32 * COLS];
     wait_for_last();
-    add_params(chan, slices, c, blockIdx.x, dweight, dbias, work);
+    add_params<COLS>(chan, slices, c, blockIdx.x, dweight, dbias, work);
 }
 
 __global__ void norm_empty_kernel(float* mean, float* rstd, int64_t count, float eps)
@@ -571,9 +587,12 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
 cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* chan, float* dweight, float* dbias,
                                cudaStream_t st)
 {
-    const int64_t ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
-    return launch_grid<norm_params_kernel>(dim3(unsigned(ctas)), 1024, 0, 1, true, st, chan, slices, a.c, dweight,
-                       dbias);
+    const int64_t cols = 2 * int64_t(a.c);
+    if (cols >= kParamCols * kParamCtas)
+        return launch_grid<norm_params_kernel<kParamCols>>(dim3(unsigned((cols + kParamCols - 1) / kParamCols)), 1024, 0,
+                                                           1, true, st, chan, slices, a.c, dweight, dbias);
+    return launch_grid<norm_params_kernel<kParamFew>>(dim3(unsigned((cols + kParamFew - 1) / kParamFew)), 1024, 0, 1,
+                                                      true, st, chan, slices, a.c, dweight, dbias);
 }
 
 cudaError_t launch_norm_empty(float* mean, float* rstd, int64_t count, float eps, cudaStream_t st)

@@ -459,7 +459,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             // Backward, two operands and their sums leave room for narrow runs
             // only, and the CTAs past the first wave pay for their parameters
             // and sums again.  Short samples gain all the same (bf16 [2000,
-            // 64, 256] 74.6 us against 109.7 streaming, [700, 100, 128] 26.5
+            // 64, 256] 71.6 us against 109.7 streaming, [700, 100, 128] 26.5
             // against 31.6), longer ones do not ([128, 128, 512] 21.4 against
             // 18.1, [64, 256, 512] 20.2 against 18.0, [256, 256, 512] 66.5
             // against 57.9).
