@@ -21,9 +21,9 @@
 //   forward   f16 [8, 4096, 320], 32 groups  14.6 us, streaming 17.6, HBM 6.2
 //             bf16 [4, 1024, 1280]            9.0             17.0      3.1
 //             bf16 [256, 256, 512]           32.3             42.2     19.8
-//             fp32 [2000, 64, 256]           47.4             83.5     38.6
+//             fp32 [2000, 64, 256]           44.5             83.5     38.6
 //   gradient  bf16 [4, 1024, 1280]           15.6             19.6      4.6
-//             bf16 [2000, 64, 256]           71.6            109.7     29.0
+//             bf16 [2000, 64, 256]           68.0            109.7     29.0
 // Clusters of 16, or one CTA of 512 threads to an SM, were slower: the SMs hold
 // 14 clusters of 16 at two CTAs to an SM, 36 of eight, and a second wave doubles
 // the time (bf16 [16, 1024, 640] with its checkpoint 46 us in 16 clusters of

@@ -399,7 +399,7 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     return true;
 }
 
-// Samples on chip.  Two CTAs share an SM.  A sample of several CTAs (a cluster)
+// Samples on chip.  Two CTAs share an SM, or four of half the threads.  A sample of several CTAs (a cluster)
 // is held only if all samples fit on the chip at once: the chain from the loads
 // over the cluster's barrier to the stores is then gone through once, in less
 // time than the streaming kernels' two launches, and beyond that it is not
@@ -414,8 +414,14 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
     const int64_t align = block ? block : vec ? kOct : 1;
     const int64_t unit = align / std::gcd(per, align);
     int64_t best = 0;   // CTAs of the layout found
+    // Samples for several waves of CTAs: four CTAs of half the threads to an SM
+    // rather than two, where a quarter of its memory holds a sample's run (bf16
+    // [2000, 64, 256] 29.3 us, in two 36.8, and its gradient 68.4, 71.4; [1000,
+    // 33, 512] 15.5, 20.3 and 41.2, 43.4).
+    for (int small = d.n >= 2 * kHeldCtas ? 1 : 0; small >= 0; --small)
     for (int64_t groups = d.c <= kNormRun ? d.groups : kNormRun / per / unit * unit; groups > 0;) {
-        for (int ranks = 1; ranks <= kNormRanks; ranks *= 2) {
+        const int64_t threads = small ? kNormThreads / 2 : kNormThreads, wave = small ? 2 * kHeldCtas : kHeldCtas;
+        for (int ranks = 1; ranks <= (small ? 1 : kNormRanks); ranks *= 2) {
             NormLayout lay{};
             lay.kind = kNormHeld;
             lay.vec = vec;
@@ -427,7 +433,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             lay.team = team_of(lay.run_cols, block, vec);
             lay.V = round_up((lay.run_cols + kOct - 1) / kOct, lay.team);
             lay.per_v = lane_factor(lay.V);
-            const int64_t lanes = kNormThreads / lay.V;
+            const int64_t lanes = threads / lay.V;
             if (lanes == 0)
                 continue;
             lay.ranks = ranks;
@@ -438,7 +444,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             // CTAs enough
             int64_t own = lay.range < lanes ? lay.range : lanes, samples = 1;
             if (ranks == 1) {
-                const int64_t few = (lay.range + 7) / 8, most = d.n * lay.runs / kHeldCtas;
+                const int64_t few = (lay.range + 7) / 8, most = d.n * lay.runs / wave;
                 samples = lanes / few < most ? lanes / few : most;
                 samples = samples < 1 ? 1 : samples > kNormSamples ? kNormSamples : samples;
                 own = lanes / samples < own ? lanes / samples : own;
@@ -451,7 +457,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             if (lane_rows > kHeldRows)
                 continue;
             lay.lane_rows = int(lane_rows);
-            if (int64_t(held_bytes(lay, es, backward, held)) > kSmemPerSm / 2 - kSmemPerCtaReserved)
+            if (int64_t(held_bytes(lay, es, backward, held)) > kSmemPerSm / (small ? 4 : 2) - kSmemPerCtaReserved)
                 continue;
             const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * ranks;
             if (ranks > 1 && ctas > kHeldWave)
@@ -459,7 +465,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             // Backward, two operands and their sums leave room for narrow runs
             // only, and the CTAs past the first wave pay for their parameters
             // and sums again.  Short samples gain all the same (bf16 [2000,
-            // 64, 256] 71.6 us against 109.7 streaming, [700, 100, 128] 26.5
+            // 64, 256] 68.0 us against 109.7 streaming, [700, 100, 128] 23.7
             // against 31.6), longer ones do not ([128, 128, 512] 21.4 against
             // 18.1, [64, 256, 512] 20.2 against 18.0, [256, 256, 512] 66.5
             // against 57.9).
@@ -474,7 +480,7 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
                 best = ctas;
                 *out = lay;
             }
-            if (ranks == 1 && ctas >= kHeldCtas)
+            if (ranks == 1 && ctas >= wave)
                 return true;
         }
         const int64_t next = (groups / 2 + unit - 1) / unit * unit;

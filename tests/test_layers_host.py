@@ -2,6 +2,8 @@
 scratch sizes, and the plain definitions against themselves."""
 
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -107,3 +109,11 @@ def test_definition_of_the_checkpoint():
     q, scale = ref.hold(x, "int8", 32)
     assert scale[0, 0] == np.float32(127) * np.float32(1 / 127)
     assert np.array_equal(q[0, :2], [1, -127])
+
+
+def test_header_is_plain_c(tmp_path):
+    source = tmp_path / "client.c"
+    source.write_text('#include "tsx_layers.h"\nint main(void) { return (int)sizeof(tsx_norm_desc) & 1; }\n')
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-pedantic", "-fsyntax-only", "-I", include, str(source)],
+                   check=True)
