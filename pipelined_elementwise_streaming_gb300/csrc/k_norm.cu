@@ -405,7 +405,7 @@ __device__ __forceinline__ void add_params(const float* chan, int64_t slices, in
     }
 }
 
-// Second kernel: dx; the CTAs past the ranges' add up dweight and dbias.
+// Second kernel: dx; the CTAs past the ranges', if any, add up dweight and dbias.
 template <int DT, bool VEC, bool BY_OCT, bool HELD>
 __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     norm_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
@@ -572,8 +572,12 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
         return e;
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
     const size_t stats = (2 * size_t(lay.run_groups) + items) * sizeof(float2) + queue_bytes(dtype, lay, x.q);
+    // An output may be an input: dweight or dbias in the place of weight or bias
+    // is written once no CTA reads those any more, by a kernel of its own, of as
+    // many threads so that it adds in the same order.
+    const bool apart = dweight == weight || dweight == bias || dbias == weight || dbias == bias;
     const int64_t param_ctas = (2 * int64_t(a.c) + kParamCols - 1) / kParamCols;
-    const dim3 all(unsigned(grid.x + (param_ctas + lay.runs - 1) / lay.runs), grid.y);
+    const dim3 all(unsigned(grid.x + (apart ? 0 : (param_ctas + lay.runs - 1) / lay.runs)), grid.y);
 #define CALL(DT, VEC, BY_OCT)                                                                                     \
     e = x.q ? launch_grid<norm_grad_kernel<DT, VEC, BY_OCT, true>>(all, lay.threads, stats, 1, true, st, a, dy, x,  \
                           weight, bias, mean, rstd, dx, dweight, dbias, scratch.part, scratch.chan)               \
@@ -581,7 +585,10 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
                           weight, bias, mean, rstd, dx, dweight, dbias, scratch.part, scratch.chan)
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
-    return e;
+    if (e != cudaSuccess || !apart)
+        return e;
+    return launch_grid<norm_params_kernel<kParamCols>>(dim3(unsigned(param_ctas)), lay.threads, 0, 1, true, st,
+                                                       scratch.chan, a.n * lay.splits, a.c, dweight, dbias);
 }
 
 cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* chan, float* dweight, float* dbias,
