@@ -79,7 +79,8 @@ __device__ __forceinline__ bool whole_sector(const void* p) { return (reinterpre
 
 // The vector loads go past L1.  They are no read-only-cache loads, since an
 // output may be one of the inputs; every thread loads what it overwrites
-// before it stores.
+// before it stores.  The compiler keeps that order: vectors are loaded and
+// stored by volatile assembly, single elements through pointers of one type.
 template <int DT, bool VEC>
 __device__ __forceinline__ Oct<DT> oct_load(const char* p, const OctAt& at)
 {
@@ -101,10 +102,10 @@ __device__ __forceinline__ Oct<DT> oct_load(const char* p, const OctAt& at)
                      : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
                      : "l"(p));
     } else if constexpr (DT == TSX_F32) {
-        const float* e = reinterpret_cast<const float*>(p);
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            o.w[j] = at.ch + j * at.step < at.cols ? __float_as_uint(e[j * at.step]) : 0u;
+            o.w[j] = at.ch + j * at.step < at.cols ? e[j * at.step] : 0u;
     } else {
         const unsigned short* e = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
@@ -163,6 +164,11 @@ __device__ __forceinline__ Oct<DT> oct_round(const float2 (&f)[4])
     return o;
 }
 
+__device__ __forceinline__ void store16(char* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 template <int DT, bool VEC>
 __device__ __forceinline__ void oct_store(char* p, const OctAt& at, const Oct<DT>& o)
 {
@@ -174,9 +180,9 @@ __device__ __forceinline__ void oct_store(char* p, const OctAt& at, const Oct<DT
                              : "memory");
                 return;
             }
-            *reinterpret_cast<uint4*>(p + 16) = make_uint4(o.w[4], o.w[5], o.w[6], o.w[7]);
+            store16(p + 16, o.w[4], o.w[5], o.w[6], o.w[7]);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+        store16(p, o.w[0], o.w[1], o.w[2], o.w[3]);
     } else if constexpr (DT == TSX_F32) {
         uint32_t* e = reinterpret_cast<uint32_t*>(p);
 #pragma unroll
