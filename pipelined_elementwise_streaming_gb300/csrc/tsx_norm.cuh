@@ -563,6 +563,16 @@ struct Affine {
     }
 };
 
+// A bias times act_scale.  One of the type's far end, which shuts a channel or
+// holds it open, stays finite: the slope of silu forms t p, infinity times zero
+// if not.
+__device__ __forceinline__ float scaled_bias(float bias, float factor)
+{
+    constexpr float most = 3.402823466e38f;
+    const float t = bias * factor;
+    return fabsf(t) > most && fabsf(bias) <= most ? copysignf(most, t) : t;
+}
+
 // And backward: xhat = (x - mean) rstd; weight and bias times act_scale, so
 // that act' comes from t = xhat w + b.
 template <bool BY_OCT>
@@ -575,11 +585,11 @@ struct Chan {
     {
         param_floats<DT, VEC>(weight, a.wide_params, a.packed_params, s.ch0, s.at, w);
         param_floats<DT, VEC>(bias, a.wide_params, a.packed_params, s.ch0, s.at, b);
-        const float2 f = pair_of(act_scale(a.act));
+        const float f = act_scale(a.act);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            w[j] = __fmul2_rn(w[j], f);
-            b[j] = __fmul2_rn(b[j], f);
+            w[j] = __fmul2_rn(w[j], pair_of(f));
+            b[j] = make_float2(scaled_bias(b[j].x, f), scaled_bias(b[j].y, f));
         }
     }
     __device__ __forceinline__ void statistics(const NormArgs& a, const NormPlace& s, const float2* stats)
