@@ -239,47 +239,51 @@ dim3 grid_of(const RowLayout& lay, int rows_at_once)
 cudaError_t launch_pack(int dtype, const PackArgs& a, const void* x, HeldOut held, cudaStream_t st)
 {
     const dim3 grid = grid_of(a.lay, dtype == TSX_F32 ? pack_rows<TSX_F32>() : pack_rows<TSX_BF16>());
-#define CALL(DT, VEC) pack_kernel<DT, VEC><<<grid, a.lay.threads, 0, st>>>(a, x, held)
+    cudaError_t e = cudaSuccess;
+#define CALL(DT, VEC) e = launch_grid<pack_kernel<DT, VEC>>(grid, a.lay.threads, 0, 1, false, st, a, x, held)
     TSX_BY_TYPE(dtype, a.lay.vec, CALL);
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_unpack(int dtype, const PackArgs& a, const void* q, const float* scale, void* x, cudaStream_t st)
 {
     const dim3 grid = grid_of(a.lay, kRowsAtOnce);
-#define CALL(DT, VEC) unpack_kernel<DT, VEC><<<grid, a.lay.threads, 0, st>>>(a, q, scale, x)
+    cudaError_t e = cudaSuccess;
+#define CALL(DT, VEC) e = launch_grid<unpack_kernel<DT, VEC>>(grid, a.lay.threads, 0, 1, false, st, a, q, scale, x)
     TSX_BY_TYPE(dtype, a.lay.vec, CALL);
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_gated(int dtype, const GatedArgs& a, const void* gate, const void* up, void* h, HeldOut held_gate,
                          HeldOut held_up, cudaStream_t st)
 {
     const dim3 grid = grid_of(a.lay, kGatedRows);
-#define CALL(DT, VEC)                                                                                            \
-    if (held_gate.q)                                                                                             \
-        gated_kernel<DT, VEC, true><<<grid, a.lay.threads, 0, st>>>(a, gate, up, h, held_gate, held_up);          \
-    else                                                                                                         \
-        gated_kernel<DT, VEC, false><<<grid, a.lay.threads, 0, st>>>(a, gate, up, h, held_gate, held_up)
+    cudaError_t e = cudaSuccess;
+#define CALL(DT, VEC)                                                                                                   \
+    e = held_gate.q ? launch_grid<gated_kernel<DT, VEC, true>>(grid, a.lay.threads, 0, 1, false, st, a, gate, up, h,    \
+                                                               held_gate, held_up)                                     \
+                    : launch_grid<gated_kernel<DT, VEC, false>>(grid, a.lay.threads, 0, 1, false, st, a, gate, up, h,   \
+                                                                held_gate, held_up)
     TSX_BY_TYPE(dtype, a.lay.vec, CALL);
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_gated_backward(int dtype, const GatedArgs& a, const void* dh, Saved gate, Saved up, void* dgate,
                                   void* dup, void* h, cudaStream_t st)
 {
     const dim3 grid = grid_of(a.lay, kGatedRows);
-#define CALL(DT, VEC)                                                                                            \
-    if (gate.q)                                                                                                  \
-        gated_backward_kernel<DT, VEC, true><<<grid, a.lay.threads, 0, st>>>(a, dh, gate, up, dgate, dup, h);     \
-    else                                                                                                         \
-        gated_backward_kernel<DT, VEC, false><<<grid, a.lay.threads, 0, st>>>(a, dh, gate, up, dgate, dup, h)
+    cudaError_t e = cudaSuccess;
+#define CALL(DT, VEC)                                                                                               \
+    e = gate.q ? launch_grid<gated_backward_kernel<DT, VEC, true>>(grid, a.lay.threads, 0, 1, false, st, a, dh,     \
+                                                                   gate, up, dgate, dup, h)                         \
+               : launch_grid<gated_backward_kernel<DT, VEC, false>>(grid, a.lay.threads, 0, 1, false, st, a, dh,    \
+                                                                    gate, up, dgate, dup, h)
     TSX_BY_TYPE(dtype, a.lay.vec, CALL);
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace tsx

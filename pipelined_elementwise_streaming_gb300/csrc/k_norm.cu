@@ -605,8 +605,8 @@ cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* c
 cudaError_t launch_norm_empty(float* mean, float* rstd, int64_t count, float eps, cudaStream_t st)
 {
     const int64_t blocks = (count + 255) / 256;
-    norm_empty_kernel<<<unsigned(blocks < 1024 ? blocks : 1024), 256, 0, st>>>(mean, rstd, count, eps);
-    return cudaGetLastError();
+    return launch_grid<norm_empty_kernel>(dim3(unsigned(blocks < 1024 ? blocks : 1024)), 256, 0, 1, false, st, mean, rstd,
+                                          count, eps);
 }
 
 }  // namespace tsx

@@ -68,8 +68,10 @@ int fail(int rc, const char* call, const char* msg)
 
 int launched(cudaError_t e, const char* call)
 {
-    if (e != cudaSuccess)
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();   // reported here, so no later call's
         return fail(TSX_ERR_CUDA, call, cudaGetErrorString(e));
+    }
     set_last_error("");
     return TSX_OK;
 }

@@ -22,7 +22,6 @@
 // columns over all row lanes.
 #pragma once
 
-#include <atomic>
 #include <type_traits>
 
 #include "tsx_device.cuh"
@@ -980,48 +979,6 @@ struct GradQueue {
 };
 
 }  // namespace dev
-
-// Launch `Kernel` with clusters of `ranks` CTAs along x (1: none); `early`: it
-// may start while the stream's last kernel still runs (it waits by itself).
-// More than 48 KB of shared memory is asked for once on each device.
-template <auto Kernel, class... Args>
-cudaError_t launch_grid(dim3 grid, int threads, size_t smem, int ranks, bool early, cudaStream_t st, Args... args)
-{
-    if (smem > 48 * 1024) {
-        constexpr int kDevices = 64;
-        static std::atomic<bool> allowed[kDevices];
-        int device = 0;
-        cudaError_t e = cudaGetDevice(&device);
-        if (e == cudaSuccess && (device >= kDevices || !allowed[device].load())) {
-            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
-            if (e == cudaSuccess && device < kDevices)
-                allowed[device].store(true);
-        }
-        if (e != cudaSuccess)
-            return e;
-    }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(unsigned(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2]{};
-    if (ranks > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = unsigned(ranks);
-        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
-    }
-    if (early) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-        ++cfg.numAttrs;
-    }
-    cfg.attrs = attr;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, Kernel, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
 
 // f<DT, VEC, BY_OCT>(...) for the runtime type and layout.
 #define TSX_BY_LAYOUT(dtype, lay, CALL)                                                        \

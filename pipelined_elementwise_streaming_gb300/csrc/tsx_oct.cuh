@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "layers.h"
@@ -661,4 +662,46 @@ __device__ __forceinline__ void hold_rows(const Oct<DT> (&o)[4], bool live, cons
 }
 
 }  // namespace dev
+// Launch `Kernel` with clusters of `ranks` CTAs along x (1: none); `early`: it
+// may start while the stream's last kernel still runs (it waits by itself).
+// More than 48 KB of shared memory is asked for once on each device.  The result
+// is this launch's own: the runtime's last error may be another call's.
+template <auto Kernel, class... Args>
+cudaError_t launch_grid(dim3 grid, int threads, size_t smem, int ranks, bool early, cudaStream_t st, Args... args)
+{
+    if (smem > 48 * 1024) {
+        constexpr int kDevices = 64;
+        static std::atomic<bool> allowed[kDevices];
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e == cudaSuccess && (device >= kDevices || !allowed[device].load())) {
+            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
+            if (e == cudaSuccess && device < kDevices)
+                allowed[device].store(true);
+        }
+        if (e != cudaSuccess)
+            return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2]{};
+    if (ranks > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = unsigned(ranks);
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (early) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = attr;
+    return cudaLaunchKernelEx(&cfg, Kernel, args...);
+}
+
 }  // namespace tsx
