@@ -112,7 +112,8 @@ int tsx_group_norm_workspace(const tsx_norm_desc *desc, int backward, int aligne
  * spread costs no digits.  With q and scale (both or neither) x's checkpoint
  * ([n * l, c]) is written too, for tsx_group_norm_backward.  A group that
  * holds an infinity or a NaN becomes NaN throughout.  n, l or c 0: nothing is
- * done, but for l = 0 mean and rstd are set to 0 and 1 / sqrt(eps). */
+ * done, but the statistics of groups without elements (l or c 0) are 0 and
+ * 1 / sqrt(eps); for c = 0 mean and rstd may both be NULL. */
 int tsx_group_norm(const tsx_norm_desc *desc, const void *x, const void *weight, const void *bias, void *y,
                    float *mean, float *rstd, void *q, float *scale, void *workspace, size_t workspace_bytes,
                    tsx_stream_t stream);

@@ -142,7 +142,7 @@ cudaError_t launch_norm_token_backward(int dtype, const NormArgs& a, const void*
 // dweight and dbias from [slices][2][c] partial sums.
 cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* chan, float* dweight, float* dbias,
                                cudaStream_t st);
-// Results of samples without rows: mean 0, rstd 1 / sqrt(eps).
+// Statistics of groups without elements: mean 0, rstd 1 / sqrt(eps).
 cudaError_t launch_norm_empty(float* mean, float* rstd, int64_t count, float eps, cudaStream_t st);
 
 }  // namespace tsx

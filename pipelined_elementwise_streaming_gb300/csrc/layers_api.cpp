@@ -681,13 +681,13 @@ extern "C" int tsx_group_norm(const tsx_norm_desc* desc, const void* x, const vo
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!q != !scale)
         return fail(TSX_ERR_INVALID, call, "q and scale come together");
-    if (d.n == 0 || d.c == 0)
+    if (d.n == 0 || (d.c == 0 && !mean && !rstd))
         return launched(cudaSuccess, call);
     if (!mean || !rstd)
         return fail(TSX_ERR_INVALID, call, "mean and rstd are required");
     if (!aligned(mean, 4) || !aligned(rstd, 4))
         return fail(TSX_ERR_ALIGN, call, "a base pointer is not aligned to its elements");
-    if (d.l == 0)
+    if (d.l == 0 || d.c == 0)
         return launched(launch_norm_empty(mean, rstd, d.n * d.groups, d.eps, st), call);
     if (!x || !weight || !bias || !y)
         return fail(TSX_ERR_INVALID, call, "x, weight, bias and y are required");

@@ -1,4 +1,5 @@
-"""Layer calls on values at the far ends of their types."""
+"""Layer calls on values at the far ends of their types, and on tensors without
+elements."""
 
 import pytest
 
@@ -50,3 +51,20 @@ def test_channels_shut_and_held_open_by_their_bias(tsx, n, l, c, groups, act, pa
         for got, want in zip(grads(far.min, far.max, held), grads(-1e4, 1e4, held)):
             assert torch.isfinite(want).all()
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n,l,c,groups", [(3, 5, 0, 4), (700, 2, 0, 32), (3, 0, 0, 1), (0, 4, 0, 2), (5, 0, 16, 4)])
+def test_statistics_of_groups_without_elements(tsx, n, l, c, groups):
+    """Every output is written, whatever its memory held before."""
+    x = torch.empty(n, l, c, device="cuda")
+    w = torch.empty(c, device="cuda")
+    op = tsx.GroupNorm("f32", n, l, c, groups, eps=1e-4)
+    for _ in range(3):
+        old = [torch.full((n, groups), float("nan"), device="cuda") for _ in range(8)]   # what the allocator hands out next
+        del old
+        y, mean, rstd, saved = op.forward(x, w, w, checkpoint=True)
+        assert y.shape == x.shape and saved.q.shape == (n * l, c)
+        assert mean.shape == rstd.shape == (n, groups)
+        assert torch.all(mean == 0) and torch.allclose(rstd, torch.full_like(rstd, 100.0))
+        dx, dw, db = op.backward(x, x, w, w, mean, rstd)
+        assert dx.shape == x.shape and torch.all(dw == 0) and torch.all(db == 0)
