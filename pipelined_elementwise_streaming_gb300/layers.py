@@ -155,6 +155,8 @@ class _Layer:
         t = self._torch
         if not first.is_cuda:
             _invalid("tensors must be on a CUDA device")
+        if stream is not None and stream.device != first.device:
+            _invalid(f"the stream is one of {stream.device}, the tensors are on {first.device}")
         with t.cuda.device(first.device), t.cuda.stream(stream):
             return call(self, *args)
 
