@@ -102,7 +102,11 @@ typedef struct tsx_norm_desc {
  * 16-byte aligned, that the call overwrites and no later call needs.  aligned
  * 0: enough whatever the alignment of the tensors; 1: enough if the base
  * pointers of x, y (dy, dx) and the checkpoint's q are multiples of 16 bytes.
- * 0 bytes: the workspace may be NULL.  Host only. */
+ * Backward at most 16 MB, or 8 bytes to a channel where that is more, for the
+ * sums of dweight and dbias; beside it, where rows are read twice, 8 bytes to a
+ * group of each range of a sample's rows (of each 2048 channels of wider
+ * groups), a few hundred ranges or one to a sample.  0 bytes: the workspace may
+ * be NULL.  Host only. */
 int tsx_group_norm_workspace(const tsx_norm_desc *desc, int backward, int aligned, size_t *bytes);
 
 /* y = act((x - mean) rstd weight + bias), with mean and rstd = 1 / sqrt(var +

@@ -40,7 +40,7 @@ __device__ __forceinline__ char* next_16(float2* p)
     return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15));
 }
 
-// A CTA's range of rows: blockIdx.x counts ranges sample by sample.  The
+// A range of rows: `at` counts them sample by sample.  The
 // `ranks` CTAs of a cluster take neighbouring ranges and join their sums.
 struct Range {
     int64_t sample, split;
@@ -50,12 +50,12 @@ struct Range {
     int mine;       // rows of the thread's lane: p, p + P, ...
 };
 
-__device__ __forceinline__ Range range_of(const NormArgs& a, const NormPlace& s)
+__device__ __forceinline__ Range range_of(const NormArgs& a, const NormPlace& s, unsigned at)
 {
     Range r;
     const unsigned splits = static_cast<unsigned>(a.lay.splits);
-    r.sample = blockIdx.x / splits;
-    r.split = blockIdx.x % splits;
+    r.sample = at / splits;
+    r.split = at % splits;
     r.rank = static_cast<int>(static_cast<unsigned>(r.split) % static_cast<unsigned>(a.lay.ranks));
     r.row0 = r.sample * a.l + r.split * a.lay.range;
     r.rows = range_rows(a, a.lay.range, r.split);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>()) norm_stats_k
 {
     extern __shared__ float4 shared4[];
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a, s);
+    const Range r = range_of(a, s, blockIdx.x);
     const int P = a.lay.P, width = run_width<BY_OCT>(s), stride = slot_stride(width);
     float2* sums = reinterpret_cast<float2*>(shared4);   // [run_groups]
     float2* ranks = sums + a.lay.run_groups;             // clusters: [ranks][run_groups]
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kNormThreads, forward_ctas<DT>())
 {
     extern __shared__ float4 work[];   // [threads or groups], then [run_groups] statistics
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a, s);
+    const Range r = range_of(a, s, blockIdx.x);
     const int P = a.lay.P;
     Affine<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
@@ -270,15 +270,16 @@ __device__ __forceinline__ void each_two(const NormArgs& a, const NormPlace& s, 
 }
 
 // First kernel: S1 and S2 (times act_scale) of every cluster's range, run and
-// group, and the range's sums for dweight and dbias.
-template <int DT, bool VEC, bool BY_OCT, bool HELD>
+// group, and the CTA's sums for dweight and dbias.  MANY: samples are not cut,
+// and each CTA takes every gridDim.x-th of them, so that dweight and dbias have
+// no more slices than there are CTAs.
+template <int DT, bool VEC, bool BY_OCT, bool HELD, bool MANY>
 __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     norm_sums_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias, const float* mean,
                      const float* rstd, float2* part, float* chan)
 {
     extern __shared__ __align__(16) float2 shared[];
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a, s);
     const int P = a.lay.P, width = s.at.cols, stride = slot_stride(width);
     float2* stats = shared;                         // [run_groups]: (mean, rstd), then (S1, S2)
     float2* ranks = stats + a.lay.run_groups;       // clusters: [ranks][run_groups]
@@ -291,75 +292,76 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
         cluster_arrive();
     Chan<BY_OCT> k;
     k.template params<DT, VEC>(a, s, weight, bias);
-    auto begin = [&] {
-        load_stats(a, s, r.sample, mean, rstd, stats);
-        k.statistics(a, s, stats);
-    };
-    float2 sz[4], szx[4];   // sums of dz and dz xhat, channel by channel
+    unsigned at = blockIdx.x;
+    do {
+        const Range r = range_of(a, s, at);
+        auto begin = [&] {
+            load_stats(a, s, r.sample, mean, rstd, stats);
+            k.statistics(a, s, stats);
+        };
+        float2 sz[4], szx[4];   // sums of dz and dz xhat, channel by channel
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        sz[j] = szx[j] = make_float2(0.f, 0.f);
-    const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
-    each_two<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin,
-                            [&](const GradRow<DT, VEC, HELD>(&g)[kQueueBatch], int) {
-        by_act(a.act, [&](auto act) {
+        for (int j = 0; j < 4; ++j)
+            sz[j] = szx[j] = make_float2(0.f, 0.f);
+        const GradWalk<DT, VEC, HELD> w(a, s, dy, x, r.row0 + s.p, P);
+        each_two<DT, VEC, HELD>(a, s, w, queue, s.live ? r.mine : 0, begin,
+                                [&](const GradRow<DT, VEC, HELD>(&g)[kQueueBatch], int) {
+            by_act(a.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < kQueueBatch; ++i) {
-                float2 fd[4], hat[4], dz[4];
-                oct_floats(g[i].dy, fd);
-                g[i].hats(a.form, k, hat);
-                k.slopes(act, fd, hat, dz);
+                for (int i = 0; i < kQueueBatch; ++i) {
+                    float2 fd[4], hat[4], dz[4];
+                    oct_floats(g[i].dy, fd);
+                    g[i].hats(a.form, k, hat);
+                    k.slopes(act, fd, hat, dz);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sz[j] = __fadd2_rn(sz[j], dz[j]);
-                    szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        sz[j] = __fadd2_rn(sz[j], dz[j]);
+                        szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+                    }
                 }
-            }
+            });
         });
-    });
-    if (s.live)
-        leave_sums(s.at, sz, szx, slots + s.p * stride);
-    float2* sums = part_of(a, s, r, part);
-    float2* mine = a.lay.ranks > 1 ? stats : sums;
-    if constexpr (BY_OCT) {
-        // S1 and S2 from the threads' weighted sums, beside the channels' sums
-        float2 t1 = make_float2(0.f, 0.f), t2 = t1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            t1 = __ffma2_rn(sz[j], k.w[j], t1);
-            t2 = __ffma2_rn(szx[j], k.w[j], t2);
-        }
         if (s.live)
-            work[s.p * (width / 8) + s.at.ch / 8] = make_float2(t1.x + t1.y, t2.x + t2.y);
-        __syncthreads();
-        add_octs(work, width / 8, P, s.groups, group_cols(a, s) / 8, mine);
-        __syncthreads();
-        sum_lanes(slots, stride, 1, P, width, columns, work);
-    } else {
-        __syncthreads();
-        sum_lanes(slots, stride, 1, P, width, columns, work);
-        weigh_columns<DT>(a, s, 1, width, weight, columns, mine);
-    }
-    float* out = chan + (r.sample * a.lay.splits + r.split) * 2 * a.c + s.ch0;
-    for (int ch = threadIdx.x; ch < width; ch += blockDim.x) {
-        out[ch] = columns[ch].y;
-        out[a.c + ch] = columns[ch].x;
-    }
-    if (a.lay.ranks > 1) {
-        __syncthreads();
-        cluster_wait();
-        for (int i = threadIdx.x; i < s.groups; i += blockDim.x)
-            cluster_put(ranks + r.rank * s.groups + i, 0, stats[i]);
-        cluster_arrive();
-        cluster_wait();
-        if (r.rank == 0)
-            for (int i = threadIdx.x; i < s.groups; i += blockDim.x) {
-                float2 t = ranks[i];
-                for (int n = 1; n < a.lay.ranks; ++n)
-                    t = __fadd2_rn(t, ranks[n * s.groups + i]);
-                sums[i] = t;
+            leave_sums(s.at, sz, szx, slots + s.p * stride);
+        float2* sums = part_of(a, s, r, part);
+        float2* mine = a.lay.ranks > 1 ? stats : sums;
+        if constexpr (BY_OCT) {
+            // S1 and S2 from the threads' weighted sums, beside the channels' sums
+            float2 t1 = make_float2(0.f, 0.f), t2 = t1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                t1 = __ffma2_rn(sz[j], k.w[j], t1);
+                t2 = __ffma2_rn(szx[j], k.w[j], t2);
             }
-    }
+            if (s.live)
+                work[s.p * (width / 8) + s.at.ch / 8] = make_float2(t1.x + t1.y, t2.x + t2.y);
+            __syncthreads();
+            add_octs(work, width / 8, P, s.groups, group_cols(a, s) / 8, mine);
+            __syncthreads();
+            sum_lanes(slots, stride, 1, P, width, columns, work);
+        } else {
+            __syncthreads();
+            sum_lanes(slots, stride, 1, P, width, columns, work);
+            weigh_columns<DT>(a, s, 1, width, weight, columns, mine);
+        }
+        add_slice(chan, a.c, s.ch0, width, MANY && at != blockIdx.x, [&](int ch) { return columns[ch]; });
+        if (a.lay.ranks > 1) {
+            __syncthreads();
+            cluster_wait();
+            for (int i = threadIdx.x; i < s.groups; i += blockDim.x)
+                cluster_put(ranks + r.rank * s.groups + i, 0, stats[i]);
+            cluster_arrive();
+            cluster_wait();
+            if (r.rank == 0)
+                for (int i = threadIdx.x; i < s.groups; i += blockDim.x) {
+                    float2 t = ranks[i];
+                    for (int n = 1; n < a.lay.ranks; ++n)
+                        t = __fadd2_rn(t, ranks[n * s.groups + i]);
+                    sums[i] = t;
+                }
+        }
+        at += gridDim.x;
+    } while (MANY && at < static_cast<unsigned>(a.n));
 }
 
 // Columns to a CTA of the sums over slices: 32, or 8 where 32 would leave few
@@ -415,12 +417,12 @@ __global__ void __launch_bounds__(kNormThreads, kBackwardCtas)
     const int64_t ranges = a.n * a.lay.splits;
     if (blockIdx.x >= ranges) {
         wait_for_last();
-        add_params<kParamCols>(chan, ranges, a.c, (blockIdx.x - ranges) * gridDim.y + blockIdx.y, dweight, dbias,
+        add_params<kParamCols>(chan, a.lay.slices, a.c, (blockIdx.x - ranges) * gridDim.y + blockIdx.y, dweight, dbias,
                    reinterpret_cast<float*>(shared));
         return;
     }
     const NormPlace s = norm_place<VEC>(a);
-    const Range r = range_of(a, s);
+    const Range r = range_of(a, s, blockIdx.x);
     const int P = a.lay.P;
     float2* stats = shared;                      // [run_groups]
     float2* sums = stats + a.lay.run_groups;     // [run_groups]: -S1 / M, -S2 / M
@@ -557,17 +559,21 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
                                  float* dbias, NormScratch scratch, cudaStream_t st)
 {
     const NormLayout& lay = a.lay;
-    const dim3 grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
+    const dim3 first(unsigned(lay.slices), unsigned(lay.runs)), grid(unsigned(a.n * lay.splits), unsigned(lay.runs));
     const size_t sums = (rank_sums(lay) + kNormThreads + lay.run_cols +
                          size_t(lay.P) * slot_stride(lay.run_cols)) * sizeof(float2) + queue_bytes(dtype, lay, x.q);
     cudaError_t e = cudaSuccess;
-#define CALL(DT, VEC, BY_OCT)                                                                                       \
-    e = x.q ? launch_grid<norm_sums_kernel<DT, VEC, BY_OCT, true>>(grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
-                          x, weight, bias, mean, rstd, scratch.part, scratch.chan)                                  \
-            : launch_grid<norm_sums_kernel<DT, VEC, BY_OCT, false>>(grid, lay.threads, sums, lay.ranks, false, st, a, dy, \
-                          x, weight, bias, mean, rstd, scratch.part, scratch.chan)
+    const bool many = lay.slices < a.n * lay.splits;
+#define KERNEL(DT, VEC, BY_OCT, HELD, MANY)                                                                       \
+    launch_grid<norm_sums_kernel<DT, VEC, BY_OCT, HELD, MANY>>(first, lay.threads, sums, lay.ranks, false, st, a, \
+                                                               dy, x, weight, bias, mean, rstd, scratch.part,     \
+                                                               scratch.chan)
+#define CALL(DT, VEC, BY_OCT)                                                                                     \
+    e = x.q ? (many ? KERNEL(DT, VEC, BY_OCT, true, true) : KERNEL(DT, VEC, BY_OCT, true, false))                 \
+            : (many ? KERNEL(DT, VEC, BY_OCT, false, true) : KERNEL(DT, VEC, BY_OCT, false, false))
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
+#undef KERNEL
     if (e != cudaSuccess)
         return e;
     const int items = lay.threads > lay.run_groups ? lay.threads : lay.run_groups;
@@ -588,7 +594,7 @@ cudaError_t launch_norm_backward(int dtype, const NormArgs& a, const void* dy, S
     if (e != cudaSuccess || !apart)
         return e;
     return launch_grid<norm_params_kernel<kParamCols>>(dim3(unsigned(param_ctas)), lay.threads, 0, 1, true, st,
-                                                       scratch.chan, a.n * lay.splits, a.c, dweight, dbias);
+                                                       scratch.chan, lay.slices, a.c, dweight, dbias);
 }
 
 cudaError_t launch_norm_params(const NormArgs& a, int64_t slices, const float* chan, float* dweight, float* dbias,

@@ -53,18 +53,19 @@ struct HeldPlace {
     int64_t row0;     // the part's first row, counted through all samples
     int rows;         // rows of the part
     int mine;         // rows of the thread's lane
+    bool live;        // the thread has channels of a sample that exists
 };
 
-__device__ __forceinline__ HeldPlace held_place(const NormArgs& a, NormPlace& s)
+__device__ __forceinline__ HeldPlace held_place(const NormArgs& a, const NormPlace& s, int64_t tile)
 {
     const NormLayout& lay = a.lay;
     HeldPlace h;
-    h.tile = blockIdx.x / lay.ranks;
+    h.tile = tile;
     h.rank = blockIdx.x % lay.ranks;
     h.q = s.p / lay.lanes;
     h.lane = s.p - h.q * lay.lanes;
     h.sample = h.tile * lay.samples + h.q;
-    s.live = s.live && h.sample < a.n;
+    h.live = s.live && h.sample < a.n;
     h.row0 = h.sample * a.l + h.rank * lay.range;
     h.rows = range_rows(a, lay.range, h.rank);
     h.mine = s.p < lay.P && h.sample < a.n && h.lane < h.rows ? (h.rows - h.lane + lay.lanes - 1) / lay.lanes : 0;
@@ -151,9 +152,9 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 {
     extern __shared__ float4 shared4[];
     const NormLayout& lay = a.lay;
-    NormPlace s = norm_place<VEC>(a);
-    const HeldPlace h = held_place(a, s);
-    const int mine = s.live ? h.mine : 0;
+    const NormPlace s = norm_place<VEC>(a);
+    const HeldPlace h = held_place(a, s, blockIdx.x / lay.ranks);
+    const int mine = h.live ? h.mine : 0;
     const int width = run_width<BY_OCT>(s), stride = slot_stride(width), items = lay.samples * s.groups;
     const Slots<DT, VEC> rows(reinterpret_cast<char*>(shared4));
     // [samples][groups]: (mean, M2) of the part; (mean, rstd)
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }
     }
     __syncthreads();
-    k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
+    k.statistics(a, s, stats + (h.live ? h.q : 0) * s.groups);
     WalkOut out = walk_out<DT>(y, h.row0 + h.lane, lay.lanes, a.y_pitch, s);
     HeldPtr to;
     if constexpr (HOLD)
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         });
         out.p += 4 * out.step;
         if constexpr (HOLD) {
-            hold_rows<DT, VEC>(o, s.live, s.at, lay.team, a.form, HeldRows{to, h.mine - i0});
+            hold_rows<DT, VEC>(o, h.live, s.at, lay.team, a.form, HeldRows{to, h.mine - i0});
             to.advance(4);
         }
     }
@@ -238,17 +239,17 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 
 // The gradient.  dz is formed twice rather than held in fp32: the second time
 // costs a few instructions an element, the room would halve the rows that a
-// CTA holds.
-template <int DT, bool VEC, bool BY_OCT, bool HELD>
+// CTA holds.  MANY: each CTA takes every gridDim.x-th tile of samples, so that
+// dweight and dbias have no more slices than there are CTAs.
+template <int DT, bool VEC, bool BY_OCT, bool HELD, bool MANY>
 __global__ void __launch_bounds__(kNormThreads, 2)
     norm_held_grad_kernel(NormArgs a, const void* dy, Saved x, const void* weight, const void* bias,
                           const float* mean, const float* rstd, void* dx, float* chan)
 {
     extern __shared__ float4 shared4[];
     const NormLayout& lay = a.lay;
-    NormPlace s = norm_place<VEC>(a);
-    const HeldPlace h = held_place(a, s);
-    const int mine = s.live ? h.mine : 0, threads = static_cast<int>(blockDim.x);
+    const NormPlace s = norm_place<VEC>(a);
+    const int threads = static_cast<int>(blockDim.x);
     const int width = s.at.cols, stride = slot_stride(width), items = lay.samples * s.groups;
     // dy's octs; x's, or the checkpoint's numbers and scales
     const Slots<DT, VEC> rows(reinterpret_cast<char*>(shared4));
@@ -266,144 +267,152 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     let_next_start();
     if (lay.ranks > 1)
         cluster_arrive();
-    const GradWalk<DT, VEC, HELD> walk_rows(a, s, dy, x, h.row0 + h.lane, lay.lanes);
-    GradWalk<DT, VEC, HELD> w = walk_rows;
-    auto ask = [&](int i) {
-        constexpr int N = kGradAskRows;
-        rows.template ask<N>(i, mine - i, w.dy, s.at);
-        if constexpr (!HELD) {
-            xs.template ask<N>(i, mine - i, w.x, s.at);
-        } else if constexpr (VEC) {
+    const int64_t tiles = (a.n + lay.samples - 1) / lay.samples, tile0 = blockIdx.x / lay.ranks;
+    int64_t tile = tile0;
+    do {
+        const HeldPlace h = held_place(a, s, tile);
+        const int mine = h.live ? h.mine : 0;
+        const GradWalk<DT, VEC, HELD> walk_rows(a, s, dy, x, h.row0 + h.lane, lay.lanes);
+        GradWalk<DT, VEC, HELD> w = walk_rows;
+        auto ask = [&](int i) {
+            constexpr int N = kGradAskRows;
+            rows.template ask<N>(i, mine - i, w.dy, s.at);
+            if constexpr (!HELD) {
+                xs.template ask<N>(i, mine - i, w.x, s.at);
+            } else if constexpr (VEC) {
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (i + k < mine) {
-                    cp_async(qs + (i + k) * threads * 8, w.q + k * w.q_step, 8, 8);
-                    cp_async(scales + (i + k) * threads * 4, w.scale + k * w.scale_step, 4, 4);
-                }
-        } else {
-            Held q[N];
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (i + k < mine)
-                    q[k] = held_load<false>(w.q + k * w.q_step, s.at);
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (i + k < mine)
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qs + (i + k) * threads * 8), "r"(q[k].w[0]),
-                                 "r"(q[k].w[1])
-                                 : "memory");
-        }
-        cp_async_commit();
-        w.advance(N);
-    };
-    const int first = VEC ? kGradAhead * kGradAskRows : mine;
-    for (int i = 0; i < first; i += kGradAskRows)
-        ask(i);
-    // rows i, i + 1, ...; those past the thread's last are zeros
-    auto take = [&](int i, GradRow<DT, VEC, HELD>(&g)[kGradAskRows]) {
-#pragma unroll
-        for (int n = 0; n < kGradAskRows; ++n) {
-            if (i + n >= mine) {
-                g[n].clear();
-                continue;
-            }
-            g[n].dy = rows.take(i + n);
-            if constexpr (HELD) {
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                             : "=r"(g[n].q.w[0]), "=r"(g[n].q.w[1])
-                             : "r"(qs + (i + n) * threads * 8));
-                if constexpr (VEC)
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g[n].scale[0]) : "r"(scales + (i + n) * threads * 4));
-                else
-                    g[n].load_scales(a, s, walk_rows, i + n);   // one to a channel: again from L1 or L2
+                for (int k = 0; k < N; ++k)
+                    if (i + k < mine) {
+                        cp_async(qs + (i + k) * threads * 8, w.q + k * w.q_step, 8, 8);
+                        cp_async(scales + (i + k) * threads * 4, w.scale + k * w.scale_step, 4, 4);
+                    }
             } else {
-                g[n].x = xs.take(i + n);
+                Held q[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (i + k < mine)
+                        q[k] = held_load<false>(w.q + k * w.q_step, s.at);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (i + k < mine)
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qs + (i + k) * threads * 8), "r"(q[k].w[0]),
+                                     "r"(q[k].w[1])
+                                     : "memory");
             }
-        }
-    };
-    Chan<BY_OCT> k;
-    k.template params<DT, VEC>(a, s, weight, bias);
-    for (int i = threadIdx.x; i < items; i += threads) {
-        const int q = lay.samples == 1 ? 0 : i / s.groups;
-        const int64_t sample = h.tile * lay.samples + q;
-        const int64_t at = sample * a.groups + s.group0 + i - q * s.groups;
-        stats[i] = sample < a.n ? make_float2(__ldg(mean + at), __ldg(rstd + at)) : make_float2(0.f, 0.f);
-    }
-    __syncthreads();
-    k.statistics(a, s, stats + (s.live ? h.q : 0) * s.groups);
-    float2 sz[4], szx[4];
+            cp_async_commit();
+            w.advance(N);
+        };
+        const int first = VEC ? kGradAhead * kGradAskRows : mine;
+        for (int i = 0; i < first; i += kGradAskRows)
+            ask(i);
+        // rows i, i + 1, ...; those past the thread's last are zeros
+        auto take = [&](int i, GradRow<DT, VEC, HELD>(&g)[kGradAskRows]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        sz[j] = szx[j] = make_float2(0.f, 0.f);
-    for (int i0 = 0; i0 < mine; i0 += kGradAskRows) {
-        if constexpr (VEC) {
-            ask(i0 + kGradAhead * kGradAskRows);
-            cp_async_wait(kGradAhead);
-        }
-        GradRow<DT, VEC, HELD> g[kGradAskRows];
-        take(i0, g);
-        by_act(a.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < kGradAskRows; ++i) {
-                float2 fd[4], hat[4], dz[4];
-                oct_floats(g[i].dy, fd);
-                g[i].hats(a.form, k, hat);
-                k.slopes(act, fd, hat, dz);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sz[j] = __fadd2_rn(sz[j], dz[j]);
-                    szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+            for (int n = 0; n < kGradAskRows; ++n) {
+                if (i + n >= mine) {
+                    g[n].clear();
+                    continue;
+                }
+                g[n].dy = rows.take(i + n);
+                if constexpr (HELD) {
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(g[n].q.w[0]), "=r"(g[n].q.w[1])
+                                 : "r"(qs + (i + n) * threads * 8));
+                    if constexpr (VEC)
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g[n].scale[0]) : "r"(scales + (i + n) * threads * 4));
+                    else
+                        g[n].load_scales(a, s, walk_rows, i + n);   // one to a channel: again from L1 or L2
+                } else {
+                    g[n].x = xs.take(i + n);
                 }
             }
-        });
-    }
-    if (s.p < lay.P && s.at.ch < s.at.cols)
-        leave_sums(s.at, sz, szx, slots + s.p * stride);
-    __syncthreads();
-    sum_lanes(slots, stride, lay.samples, lay.lanes, width, columns, work);
-    weigh_columns<DT>(a, s, lay.samples, width, weight, columns, sums);
-    float* out = chan + static_cast<int64_t>(blockIdx.x) * 2 * a.c + s.ch0;
-    for (int ch = threadIdx.x; ch < width; ch += threads) {
-        float2 v = columns[ch];
-        for (int q = 1; q < lay.samples; ++q)
-            v = __fadd2_rn(v, columns[q * width + ch]);
-        out[ch] = v.y;
-        out[a.c + ch] = v.x;
-    }
-    __syncthreads();
-    if (lay.ranks > 1)
-        share_sums(sums, items, h.rank, lay.ranks, all);
-    const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
-    for (int i = threadIdx.x; i < items; i += threads) {
-        float2 v = sums[i];
-        if (lay.ranks > 1) {
-            v = all[i];
-            for (int r = 1; r < lay.ranks; ++r)
-                v = __fadd2_rn(v, all[r * items + i]);
+        };
+        Chan<BY_OCT> k;
+        k.template params<DT, VEC>(a, s, weight, bias);
+        for (int i = threadIdx.x; i < items; i += threads) {
+            const int q = lay.samples == 1 ? 0 : i / s.groups;
+            const int64_t sample = h.tile * lay.samples + q;
+            const int64_t at = sample * a.groups + s.group0 + i - q * s.groups;
+            stats[i] = sample < a.n ? make_float2(__ldg(mean + at), __ldg(rstd + at)) : make_float2(0.f, 0.f);
         }
-        stats[i] = make_float2(v.x / m, v.y / m);
-    }
-    __syncthreads();
-    Gradient<BY_OCT> grad;
-    grad.set(a, s, k, stats + (s.live ? h.q : 0) * s.groups);
-    WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
-    for (int i0 = 0; i0 < mine; i0 += kGradAskRows) {
-        GradRow<DT, VEC, HELD> g[kGradAskRows];
-        take(i0, g);
-        by_act(a.act, [&](auto act) {
+        __syncthreads();
+        k.statistics(a, s, stats + (h.live ? h.q : 0) * s.groups);
+        float2 sz[4], szx[4];
 #pragma unroll
-            for (int i = 0; i < kGradAskRows; ++i) {
-                float2 fd[4], hat[4], dz[4], res[4];
-                oct_floats(g[i].dy, fd);
-                g[i].hats(a.form, k, hat);
-                k.slopes(act, fd, hat, dz);
-                grad.of(k, dz, hat, res);
-                if (i0 + i < mine)
-                    oct_store<DT, VEC>(to.p + i * to.step, s.at, oct_round<DT>(res));
+        for (int j = 0; j < 4; ++j)
+            sz[j] = szx[j] = make_float2(0.f, 0.f);
+        for (int i0 = 0; i0 < mine; i0 += kGradAskRows) {
+            if constexpr (VEC) {
+                ask(i0 + kGradAhead * kGradAskRows);
+                cp_async_wait(kGradAhead);
             }
+            GradRow<DT, VEC, HELD> g[kGradAskRows];
+            take(i0, g);
+            by_act(a.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < kGradAskRows; ++i) {
+                    float2 fd[4], hat[4], dz[4];
+                    oct_floats(g[i].dy, fd);
+                    g[i].hats(a.form, k, hat);
+                    k.slopes(act, fd, hat, dz);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sz[j] = __fadd2_rn(sz[j], dz[j]);
+                        szx[j] = __ffma2_rn(dz[j], hat[j], szx[j]);
+                    }
+                }
+            });
+        }
+        if (s.p < lay.P && s.at.ch < s.at.cols)
+            leave_sums(s.at, sz, szx, slots + s.p * stride);
+        __syncthreads();
+        sum_lanes(slots, stride, lay.samples, lay.lanes, width, columns, work);
+        weigh_columns<DT>(a, s, lay.samples, width, weight, columns, sums);
+        add_slice(chan, a.c, s.ch0, width, MANY && tile != tile0, [&](int ch) {
+            float2 v = columns[ch];
+            for (int q = 1; q < lay.samples; ++q)
+                v = __fadd2_rn(v, columns[q * width + ch]);
+            return v;
         });
-        to.p += kGradAskRows * to.step;
-    }
+        __syncthreads();
+        if (lay.ranks > 1)
+            share_sums(sums, items, h.rank, lay.ranks, all);
+        const float m = -static_cast<float>(a.l) * static_cast<float>(a.per_group);
+        for (int i = threadIdx.x; i < items; i += threads) {
+            float2 v = sums[i];
+            if (lay.ranks > 1) {
+                v = all[i];
+                for (int r = 1; r < lay.ranks; ++r)
+                    v = __fadd2_rn(v, all[r * items + i]);
+            }
+            stats[i] = make_float2(v.x / m, v.y / m);
+        }
+        __syncthreads();
+        Gradient<BY_OCT> grad;
+        grad.set(a, s, k, stats + (h.live ? h.q : 0) * s.groups);
+        WalkOut to = walk_out<DT>(dx, h.row0 + h.lane, lay.lanes, a.x_pitch, s);
+        for (int i0 = 0; i0 < mine; i0 += kGradAskRows) {
+            GradRow<DT, VEC, HELD> g[kGradAskRows];
+            take(i0, g);
+            by_act(a.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < kGradAskRows; ++i) {
+                    float2 fd[4], hat[4], dz[4], res[4];
+                    oct_floats(g[i].dy, fd);
+                    g[i].hats(a.form, k, hat);
+                    k.slopes(act, fd, hat, dz);
+                    grad.of(k, dz, hat, res);
+                    if (i0 + i < mine)
+                        oct_store<DT, VEC>(to.p + i * to.step, s.at, oct_round<DT>(res));
+                }
+            });
+            to.p += kGradAskRows * to.step;
+        }
+        if constexpr (MANY) {
+            tile += gridDim.x;   // no cluster
+            __syncthreads();     // stats are read
+        }
+    } while (MANY && tile < tiles);
 }
 
 }  // namespace
@@ -443,20 +452,22 @@ cudaError_t launch_norm_held_backward(int dtype, const NormArgs& a, const void* 
                                       float* dweight, float* dbias, NormScratch scratch, cudaStream_t st)
 {
     const NormLayout& lay = a.lay;
-    const int64_t slices = (a.n + lay.samples - 1) / lay.samples * lay.ranks;
-    const dim3 grid(unsigned(slices), unsigned(lay.runs));
+    const dim3 grid(unsigned(lay.slices), unsigned(lay.runs));
     const size_t smem = held_bytes(lay, elem_size(dtype), true, x.q != nullptr);
     cudaError_t e = cudaSuccess;
-#define CALL(DT, VEC, BY_OCT)                                                                                           \
-    e = x.q ? launch_grid<norm_held_grad_kernel<DT, VEC, BY_OCT, true>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
-                          x, weight, bias, mean, rstd, dx, scratch.chan)                                           \
-            : launch_grid<norm_held_grad_kernel<DT, VEC, BY_OCT, false>>(grid, lay.threads, smem, lay.ranks, false, st, a, dy, \
-                          x, weight, bias, mean, rstd, dx, scratch.chan)
+    const bool many = lay.slices < (a.n + lay.samples - 1) / lay.samples * lay.ranks;
+#define KERNEL(DT, VEC, BY_OCT, HELD, MANY)                                                                            \
+    launch_grid<norm_held_grad_kernel<DT, VEC, BY_OCT, HELD, MANY>>(grid, lay.threads, smem, lay.ranks, false, st, a,  \
+                                                                    dy, x, weight, bias, mean, rstd, dx, scratch.chan)
+#define CALL(DT, VEC, BY_OCT)                                                                                          \
+    e = x.q ? (many ? KERNEL(DT, VEC, BY_OCT, true, true) : KERNEL(DT, VEC, BY_OCT, true, false))                      \
+            : (many ? KERNEL(DT, VEC, BY_OCT, false, true) : KERNEL(DT, VEC, BY_OCT, false, false))
     TSX_BY_LAYOUT(dtype, lay, CALL);
 #undef CALL
+#undef KERNEL
     if (e != cudaSuccess)
         return e;
-    return launch_norm_params(a, slices, scratch.chan, dweight, dbias, st);
+    return launch_norm_params(a, lay.slices, scratch.chan, dweight, dbias, st);
 }
 
 }  // namespace tsx

@@ -229,11 +229,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2)
         leave_sums(s.at, sz, szx, slots + s.p * slot);
     __syncthreads();
     sum_lanes(slots, slot, 1, P, width, columns, work);
-    float* out = chan + static_cast<int64_t>(blockIdx.x) * 2 * a.c + s.ch0;
-    for (int ch = threadIdx.x; ch < width; ch += blockDim.x) {
-        out[ch] = columns[ch].y;
-        out[a.c + ch] = columns[ch].x;
-    }
+    add_slice(chan, a.c, s.ch0, width, false, [&](int ch) { return columns[ch]; });
 }
 
 }  // namespace
@@ -278,7 +274,7 @@ cudaError_t launch_norm_token_backward(int dtype, const NormArgs& a, const void*
 #undef CALL
     if (e != cudaSuccess)
         return e;
-    return launch_norm_params(a, a.lay.splits, scratch.chan, dweight, dbias, st);
+    return launch_norm_params(a, a.lay.slices, scratch.chan, dweight, dbias, st);
 }
 
 }  // namespace tsx

@@ -90,6 +90,7 @@ struct NormLayout {
     uint32_t per_v;      // lane_factor(V)
     int64_t splits;      // row ranges of a sample; token kernels: CTAs that share the rows of a run
     int64_t range;       // rows to a range, or to a rank
+    int64_t slices;      // backward: CTAs that share a run's samples; each adds up its own for dweight and dbias
     // kernels that hold samples on chip: CTAs of a cluster that share a
     // sample, samples side by side in a CTA, row lanes of each (P = samples * lanes)
     int ranks, samples, lanes;
@@ -116,7 +117,8 @@ struct NormArgs {
 // Scratch of one call (see tsx_group_norm_workspace):
 //   part   streaming: [n][splits * pieces][groups] pairs: (mean, sum of squared deviations)
 //          forward, the two sums of the gradient backward
-//   chan   [slices][2][c] backward: sums for dweight and dbias, one slice to each of a run's CTAs
+//   chan   [slices][2][c] backward: sums for dweight and dbias, one slice to each of a run's
+//          CTAs; at most 16 MB, or one slice
 struct NormScratch {
     float2* part;
     float* chan;

@@ -290,6 +290,27 @@ int64_t filled(int64_t cols, int team)
     return v > kNormThreads ? 0 : kNormThreads / v * ((cols + kOct - 1) / kOct);
 }
 
+// Slices for dweight and dbias where `all` CTAs of a run would write one each:
+// as many, unless they would take more than 16 MB.  Then each CTA adds up what it
+// has of eight samples or more (tiles of them), and the CTAs of all runs are as
+// many whole waves, of `wave`, as the 16 MB allow.  8192 tokens of 4096 channels
+// in one group would otherwise have 268 MB of them, four times the bf16 tensor,
+// and take 671 us in place of 534; heads of 80 channels, [8192, 2560], 289 in
+// place of 243.  Under 16 MB the sums to and fro cost as much as the slices
+// ([2000, 64, 256] 63 us in place of 68, but [1200, 16, 512] 24.9 for 24.3, [7088,
+// 3, 363] 94 for 83); above, single elements lose up to 10 % ([70000, 3, 363]
+// 910 us for 882, from a checkpoint 1049 for 948).  In waves that are not whole
+// the last takes as long as the others: [8192, 2560] 265 us in 4.04 of them.
+int64_t shared_slices(const tsx_norm_desc& d, int64_t all, int64_t wave, int64_t runs)
+{
+    constexpr int64_t kSliceBytes = 16 << 20, kEach = 8;
+    const int64_t most = kSliceBytes / (8 * d.c);
+    if (all <= most)
+        return all;
+    const int64_t waves = std::min(most, all / kEach) * runs / wave;
+    return std::min(all, std::max<int64_t>(std::max<int64_t>(waves, 1) * wave / runs, 1));
+}
+
 // The streaming layout for rows of c channels; block: channels to a scale
 // where the call writes checkpoints, else 0.  False if this alignment (vec,
 // block) cannot be had with these groups.
@@ -361,6 +382,8 @@ bool stream_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, N
     splits = splits / lay.ranks * lay.ranks;
     lay.range = (d.l + splits - 1) / splits;   // the last ranges may be short, or empty
     lay.splits = splits;
+    // samples that are cut into ranges make one wave as they are
+    lay.slices = splits > 1 ? d.n * splits : shared_slices(d, d.n, kNormPairs, lay.runs);
     lay.samples = 1;
     lay.lanes = lay.P;
     *out = lay;
@@ -397,6 +420,7 @@ bool token_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, No
     lay.splits = most < want ? most : want < 1 ? 1 : want;
     lay.range = (d.n + lay.splits - 1) / lay.splits;   // rows to a CTA
     lay.splits = (d.n + lay.range - 1) / lay.range;
+    lay.slices = lay.splits;
     *out = lay;
     return true;
 }
@@ -461,7 +485,8 @@ bool held_layout(const tsx_norm_desc& d, bool vec, int block, bool backward, boo
             lay.lane_rows = int(lane_rows);
             if (int64_t(held_bytes(lay, es, backward, held)) > kSmemPerSm / (small ? 4 : 2) - kSmemPerCtaReserved)
                 continue;
-            const int64_t ctas = (d.n + samples - 1) / samples * lay.runs * ranks;
+            const int64_t tiles = (d.n + samples - 1) / samples, ctas = tiles * lay.runs * ranks;
+            lay.slices = ranks > 1 ? tiles * ranks : shared_slices(d, tiles, wave, lay.runs);
             if (ranks > 1 && ctas > kHeldWave)
                 continue;
             // Backward, two operands and their sums leave room for narrow runs
@@ -563,10 +588,7 @@ size_t part_bytes(const tsx_norm_desc& d, const NormLayout& lay)
 }
 size_t chan_bytes(const tsx_norm_desc& d, const NormLayout& lay)
 {
-    const size_t slices = lay.kind == kNormToken  ? size_t(lay.splits)
-                          : lay.kind == kNormHeld ? size_t((d.n + lay.samples - 1) / lay.samples) * lay.ranks
-                                                  : size_t(d.n) * size_t(lay.splits);
-    return slices * 2 * size_t(d.c) * sizeof(float);
+    return size_t(lay.slices) * 2 * size_t(d.c) * sizeof(float);
 }
 
 int check_norm(const char* call, const tsx_norm_desc* d)

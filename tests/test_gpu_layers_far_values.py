@@ -60,7 +60,8 @@ def test_statistics_of_groups_without_elements(tsx, n, l, c, groups):
     w = torch.empty(c, device="cuda")
     op = tsx.GroupNorm("f32", n, l, c, groups, eps=1e-4)
     for _ in range(3):
-        old = [torch.full((n, groups), float("nan"), device="cuda") for _ in range(8)]   # what the allocator hands out next
+        # what the allocator hands out next
+        old = [torch.full((n, groups), float("nan"), device="cuda") for _ in range(8)]
         del old
         y, mean, rstd, saved = op.forward(x, w, w, checkpoint=True)
         assert y.shape == x.shape and saved.q.shape == (n * l, c)
