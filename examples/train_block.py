@@ -5,7 +5,8 @@ One block: heads of the residual stream normalised (group norm over tokens), a
 projection to gate and up side by side, the gated activation, a projection
 back, the residual.  Torch's autograd runs it: two autograd functions wrap the
 operators' forward and backward calls, and keep checkpoints (or, for
-comparison, the tensors themselves)::
+comparison, the tensors themselves).  The gradients have no gradients of their
+own: a second derivative is an error::
 
     python examples/train_block.py [--steps 60] [--saved int8|e4m3|full]
 """
@@ -17,6 +18,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -38,6 +40,7 @@ class Norm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         weight, bias, mean, rstd, *held = ctx.saved_tensors
         src = held[0] if len(held) == 1 else tsx.Checkpoint(*held)
@@ -64,6 +67,7 @@ class Gated(torch.autograd.Function):
         return h @ out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         out, *held = ctx.saved_tensors
         op = ctx.op

@@ -11,6 +11,10 @@ need of it; they own no device memory and may be used from several streams::
     h, gate8, up8 = glu.forward(both[:, :cols], both[:, cols:], checkpoint=True)
     dgate, dup = glu.backward(dh, gate8, up8)
 
+Autograd does not see the calls: what they return has no graph, also for inputs
+that require gradients.  examples/train_block.py wraps forward and backward in
+autograd functions.
+
 Results and scratch come from torch's allocator for the stream that the call
 runs on; tensors that the caller passes with ``stream=`` belong to the caller,
 who keeps them alive until that stream's work is done.
