@@ -53,7 +53,8 @@ typedef enum { TSX_ACT_NONE = 0, TSX_ACT_SILU = 1, TSX_ACT_GELU = 2 } tsx_act;
 typedef enum { TSX_INT8 = 0, TSX_E4M3 = 1 } tsx_form;
 
 /* x [rows, cols] to its 8-bit checkpoint.  x is required with q and scale;
- * rows or cols 0: nothing is done.  rows, cols < 2^31. */
+ * rows or cols 0: nothing is done.  rows and cols are at most 2^31 - 2, here
+ * and below. */
 int tsx_pack(tsx_dtype dtype, int64_t rows, int64_t cols, int64_t pitch, tsx_form form, int block, const void *x,
              void *q, float *scale, tsx_stream_t stream);
 
@@ -90,7 +91,7 @@ int tsx_gated_act_backward(tsx_dtype dtype, int64_t rows, int64_t cols, int64_t 
  *   form, block   of checkpoints (see tsx_form)
  *   x_pitch       row pitch of x and dx; y_pitch of y and dy
  *   eps           added to the variance, >= 0
- * n * l and c < 2^31. */
+ * n * l and c are at most 2^31 - 2. */
 typedef struct tsx_norm_desc {
     int32_t dtype, param_dtype, act, groups, form, block;
     int64_t n, l, c, x_pitch, y_pitch;
