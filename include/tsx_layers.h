@@ -12,8 +12,9 @@
  * the caller gives it.  The device must be the current one.
  *
  * Element types are those of tsx_dtype.  Arithmetic, statistics and sums are
- * in fp32 whatever the element type; results are rounded once, to nearest
- * even.  No result depends on the order in which blocks run: sums are added
+ * in fp32 whatever the element type, rstd and the joins of partial means with
+ * the hardware's approximate reciprocal (square root), within 2 ulps; results
+ * are rounded once, to nearest even.  No result depends on the order in which blocks run: sums are added
  * in an order that the shape fixes.
  *
  * A row pitch counts elements between the starts of consecutive rows (>= the
@@ -34,7 +35,12 @@ extern "C" {
 #endif
 
 /* Activations: z, z sigmoid(z), and the tanh form of gelu,
- * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2, which is z sigmoid(u) with
+ * u = 2 sqrt(2 / pi) (z + 0.044715 z^3).  The sigmoid is taken from the
+ * hardware's approximate exponential and reciprocal, in fp32 calls too: its
+ * relative error is at most 2^-21, and 2^-21 |u| (1 - sigmoid(u)) more by the
+ * rounding of its argument (u = z for silu).  Activations and slopes of under
+ * 2^-118 in magnitude may become 0. */
 typedef enum { TSX_ACT_NONE = 0, TSX_ACT_SILU = 1, TSX_ACT_GELU = 2 } tsx_act;
 
 /* Forms of an 8-bit checkpoint of [rows, cols]: bytes q [rows, cols] and fp32

@@ -245,11 +245,14 @@ __device__ __forceinline__ void param_floats(const void* base, bool wide, bool p
 // ----------------------------------------------------------- activations
 
 // sigmoid(z) = 1 / (1 + 2^t), t = -z log2(e), by the hardware's base-2
-// exponential and reciprocal (ex2.approx, rcp.approx: about 2^-22 each).  The
-// rounding of t adds 2^-24 |z| relative.  For 16-bit elements that is far
-// below the result's own rounding; for fp32 it is 2 to 4 ulps at ordinary z.
-// The division and the exponential with its range reduction would save them,
-// at dozens of instructions an element where a whole kernel has 13 to 25.
+// exponential and reciprocal (ex2.approx, within 2 ulps, and rcp.approx, within
+// 1): under 2^-21 together.  The roundings of t change 2^t, and so the sigmoid by
+// a share 1 - sigmoid(z) of that: 2^-23 |z| for silu, 2^-21 of gelu's argument.
+// For 16-bit elements that is far below the result's own rounding; for fp32 it is
+// 2 to 4 ulps at ordinary z.  The division and the exponential with its range
+// reduction would save them, at dozens of instructions an element where a whole
+// kernel has 13 to 25.  Sigmoids under 2^-126 become 0, and with them silu under
+// 2^-119 (z < -87.3) and its slope, and gelu's slope under 2^-118.
 __device__ __forceinline__ float2 sigmoid_of(float2 t)
 {
     float2 e, r;
