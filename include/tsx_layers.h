@@ -22,8 +22,10 @@
  * vectors are used where rows, pitches and base pointers are multiples of
  * them and the row's length of 8 elements; any other layout works element by
  * element, down to base pointers aligned to one element (else
- * TSX_ERR_ALIGN).  An output may be exactly an input of the same layout; any
- * other overlap is undefined.
+ * TSX_ERR_ALIGN).  An output may be exactly an input of the same layout: a
+ * tensor in the place of one of the same rows, length and pitch, dweight and
+ * dbias in that of an fp32 weight and bias.  Any other overlap is undefined,
+ * also of statistics, checkpoints and scratch with anything else.
  */
 #ifndef TSX_LAYERS_H
 #define TSX_LAYERS_H

@@ -10,13 +10,16 @@
 // From checkpoints gate and up are q * scale in fp32, not rounded to the
 // element type in between.
 //
-// Measured on GB300, GPU time of a call in a CUDA graph, HBM's own time at 6786
-// GB/s in parentheses: bf16 [4096, 12288], silu: forward 46.3 us (44.5), with
-// both checkpoints 66.1 (59.3), backward 75.8 (74.2), from checkpoints and with
-// h 78.5 (74.2); fp32 [4096, 6144] 44.8 (44.5), 53.8 (51.9), 73.5 (74.2), 69.3
-// (66.8).  bf16 [8192, 16384] to 8 bits 67 to 69 (59.3), back 67 (59.3); fp32
-// 103 (98.9), 107 (98.9).  The checkpoints' rounding (about 14 instructions an
-// element) and the writes' share of the traffic are what is left.
+// Measured on GB300, GPU time of a call in a CUDA graph over tensors that take
+// turns, over 600 MB of them, so that nothing is left in L2; in parentheses the
+// time of the bytes, a checkpoint's scales among them, at the 6786 GB/s of a copy
+// (what reads more than it writes can be a little faster).  bf16 [4096, 12288],
+// silu, gate and up side by side: forward 46.2 us (44.5), with both checkpoints
+// 66.1 (59.8), backward 75.5 (74.2), from checkpoints and with h 77.7 (74.6); fp32
+// [4096, 6144] 44.8 (44.5), 53.0 (52.2), 73.5 (74.2), 68.6 (67.0).  bf16 [8192,
+// 16384] to 8 bits 67.8 (59.9), back 67.8 (59.9); fp32 101.8 (99.5), 109.2 (99.5).
+// The checkpoints' rounding (about 14 instructions an element) and the writes'
+// share of the traffic are what is left.
 
 #include "tsx_oct.cuh"
 
@@ -30,7 +33,8 @@ using namespace dev;
 // packed and unpacked: unpacking 2, 4 or 8 rows at once the same, packing 8 rows
 // 266 us, 12 274, 16 296.  Gated: 4 rows took 303.7 us in place of 305.2 for the
 // gradient of bf16 [16384, 12288], but 12.5 in place of 11.3 for fp32 [1777,
-// 2731], whose octs are no vectors, and 3.7 in place of 2.6 for [256, 1024].
+// 2731], whose octs are no vectors, and 3.7 in place of 2.6 for [256, 1024] (three
+// sets of tensors in turn).
 constexpr int kRowsAtOnce = 4;
 constexpr int kGatedRows = 2;
 template <int DT>

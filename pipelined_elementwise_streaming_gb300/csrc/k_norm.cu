@@ -9,17 +9,20 @@
 // for clusters of eight, which join their ranges' sums through rank 0's shared
 // memory, so that the second kernel's CTAs have few parts to join each.
 //
-// Measured on GB300 (GPU time of a call in a CUDA graph, operands from HBM;
-// HBM's own time at 6786 GB/s for what the kernels read and write in
-// parentheses):
-//   bf16 [1, 262144, 128], 32 groups, silu: 40.6 us (29.7)
-//   bf16 [4, 16384, 512], 32 groups, silu, int8 checkpoint: 100.7 us (75.1) for
-//   both passes; its kernels launched alone, cold: statistics 16.4 (9.9), apply
-//   and checkpoint 36.0 (25.0), gradient's sums 28.3 (15.1), dx 32.5 (25.0)
+// Measured on GB300 (GPU time of a call in a CUDA graph over tensors that take
+// turns, so that nothing is left in L2; HBM's own time at 6786 GB/s for what the
+// kernels read and write in parentheses):
+//   bf16 [1, 262144, 128], 32 groups, silu: 40.3 us (29.7)
+//   bf16 [4, 16384, 512], 32 groups, silu, int8 checkpoint: 101.2 us (75.1) for
+//   both passes; its kernels launched alone, cold: statistics 16.1 (9.9), apply
+//   and checkpoint 36.9 (25.0), gradient's sums 28.2 (15.1), dx 33.1 (25.0)
 // About 6 us of each kernel are its start, its first rows' latency and its sums;
 // the rest runs at 85 to 100 % of HBM's rate, but for the checkpoint's and the
 // gradient's arithmetic (13 to 18 instructions an element), which holds those
 // kernels at 75 to 85 %.
+// Samples of few rows, one to a CTA, are far from that: what a CTA does once
+// outweighs its row.  Tokens of 4096 channels in one group, bf16 [8192, 1, 4096]:
+// 642 us forward (29.7; HBM's time for reading once 19.8), 536 backward (49.5).
 
 #include "tsx_norm.cuh"
 

@@ -16,14 +16,19 @@
 // of f16 [8, 4096, 320]: 9 to 13 thousand, 4, 2, 8.  Two CTAs to an SM do not
 // fill one another's gaps where all of them run side by side.
 //
-// Measured on GB300, GPU time of a call in a CUDA graph, against the streaming
-// kernels, and HBM's own time at 6786 GB/s:
-//   forward   f16 [8, 4096, 320], 32 groups  14.6 us, streaming 17.6, HBM 6.2
-//             bf16 [4, 1024, 1280]            9.0             17.0      3.1
-//             bf16 [256, 256, 512]           32.3             42.2     19.8
-//             fp32 [2000, 64, 256]           44.5             83.5     38.6
-//   gradient  bf16 [4, 1024, 1280]           15.6             19.6      4.6
-//             bf16 [2000, 64, 256]           68.0            109.7     29.0
+// Measured on GB300, GPU time of a call in a CUDA graph that repeats it on the same
+// tensors, for both kinds of kernels; with nothing left in L2 (tensors that take
+// turns); HBM's own time at 6786 GB/s:
+//                                         held   streaming   held, cold   HBM
+//   forward   f16 [8, 4096, 320], 32 groups  14.7   17.6        16.4         6.2
+//             bf16 [4, 1024, 1280]            9.2   17.0        10.7         3.1
+//             bf16 [256, 256, 512]           32.1   42.2        32.2        19.8
+//             fp32 [2000, 64, 256]           44.3   83.5        44.3        38.6
+//   gradient  bf16 [4, 1024, 1280]           15.6   19.6        16.8         4.6
+//             bf16 [2000, 64, 256]           68.5  109.7        68.5        29.0
+// Samples of a row or two, one to a CTA, are far from HBM: what a CTA does once
+// outweighs its rows.  Heads of 80 channels, bf16 [8192, 1, 2560] in 32 groups:
+// forward 121 us (12.4), gradient 240 (18.5).
 // Clusters of 16, or one CTA of 512 threads to an SM, were slower: the SMs hold
 // 14 clusters of 16 at two CTAs to an SM, 36 of eight, and a second wave doubles
 // the time (bf16 [16, 1024, 640] with its checkpoint 46 us in 16 clusters of

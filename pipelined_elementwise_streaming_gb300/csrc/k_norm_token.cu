@@ -8,11 +8,11 @@
 // gradient or a checkpoint takes the registers.
 //
 // HBM bounds the larger calls, the launch the smallest.  Measured on GB300, GPU
-// time of a call in a CUDA graph, HBM's own time at 6786 GB/s in parentheses:
-// bf16 [8192, 4096] in 32 groups 22.3 us (19.8), 25.4 where nothing of it is
-// left in L2; with an int8 checkpoint 33.2 (24.9); its gradient 42.4 (29.7),
-// from registers in place of the queue 53.9; fp32 [4096, 4096] 21.7 (19.8);
-// bf16 [16, 4096] 3.0.
+// time of a call in a CUDA graph over tensors that take turns, so that nothing is
+// left in L2, HBM's own time at 6786 GB/s in parentheses: bf16 [8192, 4096] in 32
+// groups 22.8 us (19.8), with an int8 checkpoint 33.6 (24.9), its gradient 41.8
+// (29.7; from registers in place of the queue 12 us more); fp32 [4096, 4096] 22.0
+// (19.8); bf16 [16, 4096] 3.1.
 
 #include <algorithm>
 

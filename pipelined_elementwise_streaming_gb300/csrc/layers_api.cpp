@@ -258,6 +258,8 @@ extern "C" int tsx_gated_act_backward(tsx_dtype dtype, int64_t rows, int64_t col
 }
 
 // ---------------------------------------------------------- group norm
+// The times in the comments below are GPU times of calls in a CUDA graph that
+// repeats them on the same tensors.
 
 namespace {
 
@@ -295,11 +297,11 @@ int64_t filled(int64_t cols, int team)
 // has of eight samples or more (tiles of them), and the CTAs of all runs are as
 // many whole waves, of `wave`, as the 16 MB allow.  8192 tokens of 4096 channels
 // in one group would otherwise have 268 MB of them, four times the bf16 tensor,
-// and take 671 us in place of 534; heads of 80 channels, [8192, 2560], 289 in
-// place of 243.  Under 16 MB the sums to and fro cost as much as the slices
+// and take 671 us in place of 536; heads of 80 channels, [8192, 2560], 289 in
+// place of 239.  Under 16 MB the sums to and fro cost as much as the slices
 // ([2000, 64, 256] 63 us in place of 68, but [1200, 16, 512] 24.9 for 24.3, [7088,
 // 3, 363] 94 for 83); above, single elements lose up to 10 % ([70000, 3, 363]
-// 910 us for 882, from a checkpoint 1049 for 948).  In waves that are not whole
+// 900 us for 877, from a checkpoint 1018 for 948).  In waves that are not whole
 // the last takes as long as the others: [8192, 2560] 265 us in 4.04 of them.
 int64_t shared_slices(const tsx_norm_desc& d, int64_t all, int64_t wave, int64_t runs)
 {
