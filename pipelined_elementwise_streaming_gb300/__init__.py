@@ -368,3 +368,9 @@ class Plan:
 from .layers import (ACTS, FORMS, Checkpoint, GatedAct, GroupNorm, Packer, tsx_gated_act,  # noqa: E402
                      tsx_gated_act_backward, tsx_group_norm, tsx_group_norm_backward, tsx_group_norm_workspace,
                      tsx_norm_desc, tsx_pack, tsx_unpack)
+
+# The operators around attention (include/tsx_attention.h).
+from .attention import (LAYOUTS, SCALINGS, Batch, PagedAttention, Rotary, tsx_batch, tsx_cache,  # noqa: E402
+                        tsx_cache_append, tsx_heads, tsx_paged_attention, tsx_paged_attention_workspace, tsx_rotary,
+                        tsx_rotary_backward, tsx_rotary_desc, tsx_rotary_frequencies, tsx_rotary_turns,
+                        tsx_rotary_workspace)

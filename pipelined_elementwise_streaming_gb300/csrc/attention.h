@@ -1,0 +1,84 @@
+// Internal declarations of the operators around attention
+// (include/tsx_attention.h): their kernels' arguments.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tsx_attention.h"
+#include "tsx_internal.h"
+
+namespace tsx {
+
+constexpr int kRotaryThreads = 256;
+constexpr int kRotaryDim = 256;   // channels of a head at most
+
+// One of the tensors that a rotary call goes over: its CTAs, `first` .. first +
+// ctas - 1, work on the heads of tokens, `parts` teams of threads to a token.
+struct RotaryRole {
+    const char* x;       // forward: what is normed and turned; backward: the gradient
+    const char* saved;   // backward: the forward call's input
+    char* out;
+    int64_t x_pitch, x_head, saved_pitch, saved_head, out_pitch, out_head;
+    const void* weight;   // NULL: ones
+    float* slices;        // backward: [ctas][dim] sums for the weight's gradient, or NULL
+    int heads, parts, first, ctas;
+    int which;            // 0 queries, 1 keys, 2 values
+    int turn;             // 0: neither normed nor turned
+    int paged;            // out is a cache, out_pitch its slots' pitch
+    int packed_weight;    // the weight is aligned to 16 bytes
+};
+
+// Where the tokens of a batch lie (see tsx_batch and tsx_cache).
+struct PagedArgs {
+    const int32_t *starts, *lengths, *pages;
+    int64_t pages_pitch, cache_pages, page_pitch;
+    int seqs, most_pages, page_size;
+};
+
+struct RotaryArgs {
+    RotaryRole role[3];
+    int roles;
+    int64_t tokens;
+    const void* positions;   // NULL: the batch's
+    int wide_positions;      // of 8 bytes
+    int dim, rot, layout, norm, wide_params;
+    int team;                // threads to a head: a power of two
+    float eps, amplitude;
+    PagedArgs paged;
+    uint64_t turns[TSX_ROPE_PAIRS];
+};
+
+// Heads that a thread of the vector kernels loads before it uses the first.
+TSX_HD constexpr int rotary_batch(int dtype) { return dtype == TSX_F32 ? 2 : 4; }
+
+cudaError_t launch_rotary(int dtype, const RotaryArgs& a, bool vec, int ctas, cudaStream_t st);
+cudaError_t launch_rotary_norm_backward(int dtype, const RotaryArgs& a, bool vec, int ctas, cudaStream_t st);
+// dq_weight and dk_weight from the roles' slices.
+cudaError_t launch_rotary_weights(const RotaryArgs& a, float* dq_weight, float* dk_weight, cudaStream_t st);
+
+namespace dev {
+struct Tail;
+}
+
+// Attention over a paged cache (csrc/tsx_attend.cuh).
+struct AttendArgs {
+    PagedArgs paged;
+    const char *k, *v, *q;
+    char* out;
+    float* lse;
+    int64_t slot_pitch, head_pitch, q_pitch, q_head, out_pitch, out_head, tokens;
+    int heads, group, dim;   // heads of the cache, queries to each
+    float scale_log2;        // scale / ln 2
+    int ctas;
+    // scratch: for each CTA two slots of [rows][padded dim] sums and [rows] (maximum, sum of weights), and its Tail
+    float* parts;
+    float2* stats;
+    dev::Tail* tails;
+};
+int attend_few_rows();
+int attend_few_ctas(int dim);
+cudaError_t launch_attend_few(int dtype, const AttendArgs& a, cudaStream_t st);
+
+}  // namespace tsx

@@ -1,0 +1,420 @@
+// Attention over a paged cache for few rows to a head: single new tokens above
+// all.  And the joining of parts.
+//
+// Keys and values are read once, and for a handful of rows that is all there is
+// to do in earnest: HBM bounds it.  A CTA's four warps work for themselves, each
+// on 16 of the 64 keys of a step, with a queue of its own in shared memory that
+// it fills by cp.async (a page may start anywhere, so each row of 16-byte chunks
+// has its own address) and empties with no barrier but its own.  The products are
+// mma.m16n8k16 with the rows as M: 16 rows for up to 16 queries of a key, which
+// leaves most of the tensor cores' work empty, but that is not what bounds it.
+// Scores stay in registers: the accumulators of q k^T are the operand of the
+// product with v.  Running maxima and sums are the warp's own; they and the four
+// sums of values are joined once at the end of a piece.
+
+#include "tsx_attend.cuh"
+#include "tsx_device.cuh"
+
+namespace tsx {
+namespace {
+
+using namespace dev;
+
+constexpr int kRows = 16, kKeys = 64, kWarpKeys = 16, kThreads = 128, kStages = 3;
+constexpr int64_t kLeast = 4;   // steps to a CTA at least
+
+template <int D>
+TSX_HD constexpr int stage_bytes() { return 2 * kWarpKeys * D * 2; }
+// Shared memory: the queues, the warps' statistics, the words of run_of.
+template <int D>
+TSX_HD constexpr int queue_bytes() { return 4 * kStages * stage_bytes<D>(); }
+constexpr int kStatsBytes = 4 * kRows * 8, kSumsBytes = (kThreads / 32 + 3) * 8;
+
+__device__ __forceinline__ void ldmatrix(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+template <int DT>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (DT == TSX_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A stage: keys then values, 16 rows of D / 8 chunks of 16 bytes, chunk c of row
+// r at place c ^ (r & 7) so that ldmatrix meets every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk)
+{
+    return static_cast<uint32_t>(row * (D * 2) + ((chunk ^ (row & 7)) * 16));
+}
+
+// Whether a word of two elements holds an infinity or a NaN.
+template <int DT>
+__device__ __forceinline__ bool not_finite(uint32_t w)
+{
+    const uint32_t e = DT == TSX_BF16 ? 0x7f80u : 0x7c00u;
+    return (w & e) == e || (w >> 16 & e) == e;
+}
+template <int DT>
+__device__ __forceinline__ float value_of(uint16_t w)
+{
+    return DT == TSX_BF16 ? __uint_as_float(static_cast<uint32_t>(w) << 16) : __half2float(__ushort_as_half(w));
+}
+
+// A warp's 16 keys of the next steps of a piece: where each lies, one step ahead
+// of its use (key lane % 16 to a lane).
+struct Keys {
+    int position;   // of the lane's key in the step to come
+    int limit;      // keys before this one are wanted
+    int page;       // read ahead, -1 if there is none
+    const int32_t* pages;
+
+    __device__ __forceinline__ void look(const AttendArgs& a)
+    {
+        page = position < limit ? pages[position / a.paged.page_size] : -1;
+    }
+};
+
+template <int DT, int D>
+__device__ __forceinline__ uint32_t load_step(const AttendArgs& a, const Keys& k, int64_t head_at, uint32_t stage)
+{
+    const int lane = threadIdx.x & 31;
+    const bool there = k.page >= 0 && k.page < a.paged.cache_pages;
+    const int slot = k.position % a.paged.page_size;
+    const int64_t at = there ? (k.page * a.paged.page_pitch + slot * a.slot_pitch + head_at) * 2 : 0;
+    const uint32_t seen = __ballot_sync(0xffffffffu, there) & 0xffffu;
+    constexpr int kChunks = D / 8, kTurns = kWarpKeys * kChunks / 32;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int id = i * 32 + lane, row = id / kChunks, chunk = id % kChunks;
+        const int64_t from = __shfl_sync(0xffffffffu, at, row) + chunk * 16;
+        const uint32_t bytes = (seen >> row & 1) && chunk * 8 < a.dim ? 16 : 0;
+        const uint32_t to = stage + chunk_at<D>(row, chunk);
+        cp_async(to, bytes ? a.k + from : a.k, 16, bytes);
+        cp_async(to + kWarpKeys * D * 2, bytes ? a.v + from : a.v, 16, bytes);
+    }
+    return seen;
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(const __grid_constant__ AttendArgs a)
+{
+    extern __shared__ __align__(128) unsigned char memory[];
+    float2(*stats)[kRows] = reinterpret_cast<float2(*)[kRows]>(memory + queue_bytes<D>());
+    int64_t* sums = reinterpret_cast<int64_t*>(memory + queue_bytes<D>() + kStatsBytes);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, c2 = lane % 4 * 2;
+    const uint32_t queue = smem_addr(memory) + warp * (kStages * stage_bytes<D>());
+    let_next_start();
+    Run run = run_of<kRows, kKeys, kThreads>(a, kLeast, sums);
+    Tail tail{};
+    while (run.from < run.to) {
+        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const int row0 = p.tile * kRows;
+        const int64_t head_at = p.head * a.head_pitch;
+        // queries, as the A operand: rows g and g + 8
+        uint32_t q[D / 16][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = g + half * 8;
+            const char* from = a.q + row_at(a, p.seq.first, p.head, row0 + row, a.q_pitch, a.q_head) * 2;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = k * 16 + e * 8 + c2;
+                    q[k][half + 2 * e] =
+                        row < p.rows && ch < a.dim ? *reinterpret_cast<const uint32_t*>(from + ch * 2) : 0u;
+                }
+        }
+        const int limits[2] = {row_limit(a, p.seq, row0 + g), row_limit(a, p.seq, row0 + g + 8)};
+        const int first_limit = row_limit(a, p.seq, row0);
+        const int last_limit = row_limit(a, p.seq, row0 + p.rows - 1);
+        Keys keys;
+        keys.limit = min(last_limit, p.seq.length);
+        keys.pages = a.paged.pages + p.b * a.paged.pages_pitch;
+        keys.position = p.step * kKeys + warp * kWarpKeys + lane % 16;
+        keys.look(a);
+        uint32_t seen[kStages];
+        const int steps = p.end - p.step;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            seen[i] = 0;
+            if (i < steps) {
+                seen[i] = load_step<DT, D>(a, keys, head_at, queue + i * stage_bytes<D>());
+                keys.position += kKeys;
+                keys.look(a);
+            }
+            cp_async_commit();
+        }
+        float out[D / 8][4], top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                out[i][e] = 0.f;
+        int next_in = kStages - 1, next_out = 0;
+        int base = p.step * kKeys + warp * kWarpKeys;
+        for (int step = 0; step < steps; ++step, base += kKeys) {
+            cp_async_wait(kStages - 2);
+            __syncwarp();
+            const uint32_t mask = seen[0];
+#pragma unroll
+            for (int i = 0; i + 2 < kStages; ++i)
+                seen[i] = seen[i + 1];
+            uint32_t more = 0;
+            if (step + kStages - 1 < steps) {   // into the stage that the last step has left
+                more = load_step<DT, D>(a, keys, head_at, queue + next_in * stage_bytes<D>());
+                keys.position += kKeys;
+                keys.look(a);
+            }
+            seen[kStages - 2] = more;
+            cp_async_commit();
+            const uint32_t stage = queue + next_out * stage_bytes<D>();
+            next_in = next_in + 1 == kStages ? 0 : next_in + 1;
+            next_out = next_out + 1 == kStages ? 0 : next_out + 1;
+            if (mask == 0)
+                continue;
+            float s[2][4] = {};
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                ldmatrix(stage + chunk_at<D>(lane / 16 * 8 + lane % 8, 2 * k + (lane / 8 & 1)), b);
+                mma<DT>(s[0], q[k], b[0], b[1]);
+                mma<DT>(s[1], q[k], b[2], b[3]);
+            }
+            float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = j * 8 + c2 + (e & 1);
+                    const bool sees = (mask >> key & 1) && base + key < limits[e >> 1];
+                    s[j][e] = sees ? s[j][e] * a.scale_log2 : -INFINITY;
+                    most[e >> 1] = fmaxf(most[e >> 1], s[j][e]);
+                }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 1));
+                most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 2));
+                most[r] = fmaxf(most[r], top[r]);
+            }
+            if (__any_sync(0xffffffffu, most[0] != top[0] || most[1] != top[1])) {
+                float f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {   // no score yet: nothing to scale
+                    f[r] = top[r] == -INFINITY ? 1.f : exp2_fast(top[r] - most[r]);
+                    top[r] = most[r];
+                    sum[r] *= f[r];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        out[i][e] *= f[e >> 1];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[j][e] = exp2_fast(s[j][e] - (top[e >> 1] == -INFINITY ? 0.f : top[e >> 1]));
+                    sum[e >> 1] += s[j][e];
+                }
+            const uint32_t w[4] = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]), pack2<DT>(s[1][0], s[1][1]),
+                                   pack2<DT>(s[1][2], s[1][3])};
+            const uint32_t values = stage + kWarpKeys * D * 2;
+            if (base + kWarpKeys > first_limit) {
+                // Some row may not see some key: 0 times an infinity of such a value would be NaN.  What is not
+                // finite is taken out of the product and added to the rows that see it.
+                unsigned char* bytes = memory + (values - smem_addr(memory));
+                bool bad = false;
+                for (int i = lane; i < kWarpKeys * D / 8; i += 32) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(bytes + i * 16);
+                    bad |= not_finite<DT>(v.x) || not_finite<DT>(v.y) || not_finite<DT>(v.z) || not_finite<DT>(v.w);
+                }
+                if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                        for (int key = 0; key < kWarpKeys; ++key) {
+                            const uint32_t pair = *reinterpret_cast<const uint32_t*>(bytes + chunk_at<D>(key, i) + c2 * 2);
+                            if (!not_finite<DT>(pair) || !(mask >> key & 1))
+                                continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint16_t v = static_cast<uint16_t>(e & 1 ? pair >> 16 : pair);
+                                if (not_finite<DT>(v) && base + key < limits[e >> 1])
+                                    out[i][e] += value_of<DT>(v);
+                            }
+                        }
+                    __syncwarp();
+                    for (int i = lane; i < kWarpKeys * D / 2; i += 32) {
+                        uint32_t* at = reinterpret_cast<uint32_t*>(bytes) + i;
+                        const uint32_t v = *at;
+                        if (not_finite<DT>(v))
+                            *at = (not_finite<DT>(v & 0xffffu) ? 0u : v & 0xffffu) |
+                                  (not_finite<DT>(v >> 16) ? 0u : v & 0xffff0000u);
+                    }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; i += 2) {
+                uint32_t b[4];
+                ldmatrix_trans(values + chunk_at<D>((lane / 8 & 1) * 8 + lane % 8, i + lane / 16), b);
+                mma<DT>(out[i], w, b[0], b[1]);
+                mma<DT>(out[i + 1], w, b[2], b[3]);
+            }
+        }
+        // the four warps' sums, each relative to its own maximum
+        cp_async_wait(0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+            if (lane % 4 == 0)
+                stats[warp][g + 8 * r] = make_float2(top[r], sum[r]);
+        }
+        __syncthreads();   // also: the queues are empty, and their memory free
+        float* joined = reinterpret_cast<float*>(memory);   // [4][kRows][D]
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<float2*>(joined + (warp * kRows + g + 8 * r) * D + i * 8 + c2) =
+                    make_float2(out[i][2 * r], out[i][2 * r + 1]);
+        __syncthreads();
+        const bool whole = p.whole();
+        const int slot = part_slot(p);
+        constexpr int kFours = D / 4;
+        for (int i = threadIdx.x; i < p.rows * kFours; i += kThreads) {
+            const int row = i / kFours, ch = i % kFours * 4;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                m = fmaxf(m, stats[w][row].x);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float2 t = stats[w][row];
+                const float f = t.x == -INFINITY ? (t.y != t.y ? t.y : 0.f) : exp2_fast(t.x - m);
+                const float4 o = *reinterpret_cast<const float4*>(joined + (w * kRows + row) * D + ch);
+                if (t.x == -INFINITY && t.y == t.y)
+                    continue;   // nothing seen
+                l += t.y * f;
+                v.x += o.x * f;
+                v.y += o.y * f;
+                v.z += o.z * f;
+                v.w += o.w * f;
+            }
+            if (whole) {
+                const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+                if (ch < a.dim) {
+                    char* to = a.out + (row_at(a, p.seq.first, p.head, row0 + row, a.out_pitch, a.out_head) + ch) * 2;
+                    *reinterpret_cast<uint2*>(to) = make_uint2(pack2<DT>(v.x * f, v.y * f), pack2<DT>(v.z * f, v.w * f));
+                }
+                if (ch == 0)
+                    store_lse(a, p.seq.first, p.head, row0 + row, m, l);
+            } else {
+                *reinterpret_cast<float4*>(a.parts + (static_cast<int64_t>(slot) * kRows + row) * D + ch) = v;
+                if (ch == 0)
+                    a.stats[slot * kRows + row] = make_float2(m, l);
+            }
+        }
+        const Tail t = tail_of<kRows>(run, p);
+        if (t.follow)
+            tail = t;
+        __syncthreads();   // before the queues are used again
+        advance<kRows>(a, run, p);
+    }
+    if (threadIdx.x == 0)
+        a.tails[blockIdx.x] = tail;
+}
+
+// Joins the parts of the tile that CTA blockIdx.x has begun and not ended, four
+// rows to each CTA.
+template <int DT, int D, int M>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a)
+{
+    wait_for_last();
+    const Tail t = a.tails[blockIdx.x];
+    const int row = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (!t.follow || row >= t.rows)
+        return;
+    constexpr int kEach = D / 32;   // channels to a thread
+    const int first = 2 * blockIdx.x + 1;   // then the first slots of the CTAs that follow
+    float m = -INFINITY;
+    for (int i = 0; i <= t.follow; ++i)
+        m = fmaxf(m, a.stats[(i ? first - 1 + 2 * i : first) * M + row].x);
+    float l = 0.f, v[kEach] = {};
+    for (int i = 0; i <= t.follow; ++i) {
+        const int64_t slot = i ? first - 1 + 2 * i : first;
+        const float2 s = a.stats[slot * M + row];
+        if (s.x == -INFINITY && s.y == s.y)
+            continue;
+        const float f = s.x == -INFINITY ? s.y : exp2_fast(s.x - m);
+        l += s.y * f;
+        const float* from = a.parts + (slot * M + row) * D + lane * kEach;
+#pragma unroll
+        for (int e = 0; e < kEach; e += 2) {
+            const float2 o = *reinterpret_cast<const float2*>(from + e);
+            v[e] += o.x * f;
+            v[e + 1] += o.y * f;
+        }
+    }
+    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+    char* to = a.out + (row_at(a, t.token, t.head, t.row0 + row, a.out_pitch, a.out_head) + lane * kEach) * 2;
+#pragma unroll
+    for (int e = 0; e < kEach; e += 2)
+        if (lane * kEach + e < a.dim)
+            *reinterpret_cast<uint32_t*>(to + e * 2) = pack2<DT>(v[e] * f, v[e + 1] * f);
+    if (lane == 0)
+        store_lse(a, t.token, t.head, t.row0 + row, m, l);
+}
+
+template <int DT, int D>
+cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
+{
+    const cudaError_t e = launch_grid<attend_kernel<DT, D>>(dim3(unsigned(a.ctas)), kThreads,
+                                                            queue_bytes<D>() + kStatsBytes + kSumsBytes, 1, false, st, a);
+    if (e != cudaSuccess)
+        return e;
+    return launch_grid<attend_join_kernel<DT, D, kRows>>(dim3(unsigned(a.ctas), kRows / 4), 128, 0, 1, true, st, a);
+}
+
+template <int DT>
+cudaError_t launch_dim(const AttendArgs& a, cudaStream_t st)
+{
+    return a.dim <= 64 ? launch_few<DT, 64>(a, st) : a.dim <= 128 ? launch_few<DT, 128>(a, st) : launch_few<DT, 256>(a, st);
+}
+
+}  // namespace
+
+int attend_few_rows() { return kRows; }
+int attend_few_ctas(int dim) { return dim <= 128 ? 2 * 152 : 152; }
+
+cudaError_t launch_attend_few(int dtype, const AttendArgs& a, cudaStream_t st)
+{
+    return dtype == TSX_BF16 ? launch_dim<TSX_BF16>(a, st) : launch_dim<TSX_F16>(a, st);
+}
+
+}  // namespace tsx

@@ -1,0 +1,743 @@
+// Rotary positions and norms of heads: forward, backward, and forward into a
+// paged cache.
+//
+// A pair (a, b) of a head at position p becomes (a c - b s, b c + a s), c and s
+// the amplitude times the cosine and sine of p f; with a norm the pair is x rstd
+// weight, rstd = 1 / sqrt(mean(x^2) + eps).  Backward, for d the gradient turned
+// back, dx = rstd d w - x rstd^3 sum(d w x) / dim and dw = sum(d x rstd).
+//
+// One pass over the tensors, bound by HBM.  A thread owns 16 channels of a head
+// and keeps them: two octs that hold eight whole pairs, so that a rotation needs
+// no other thread and a norm a few shuffles within the team of threads of a head.
+// It computes its eight sines and cosines once for a token and uses them for the
+// several heads that it goes over.  A table of them would be read instead: 4 bytes
+// to a channel and token, as much as two 16-bit heads.  Angles are whole numbers:
+// the position times the part of a turn that a position adds, modulo 2^64.
+
+#include "attention.h"
+#include "tsx_norm.cuh"
+
+namespace tsx {
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = kRotaryThreads / 32;
+constexpr int kStarts = 1024;   // sequences whose starts a CTA keeps in shared memory
+
+// Sine and cosine of `turn` / 2^32 of a turn.
+template <int DT>
+__device__ __forceinline__ float2 cos_sin(uint32_t turn)
+{
+    float c, s;
+    if constexpr (DT == TSX_F32) {
+        // the nearest quarter turn apart, the rest within an eighth: a rest of 30
+        // bits rounds to fp32 with 2^-26 of a radian at most
+        const uint32_t quarter = (turn + (1u << 29)) >> 30;
+        sincospif(static_cast<float>(static_cast<int32_t>(turn - (quarter << 30))) * 0x1p-31f, &s, &c);
+        const float t = c;
+        if (quarter & 1) {
+            c = -s;
+            s = t;
+        }
+        if (quarter & 2) {
+            c = -c;
+            s = -s;
+        }
+    } else {
+        // the hardware's, within 2^-21 on -pi .. pi, and 2^-22 by the argument's rounding:
+        // a 2^-8 part (fp16) or less of the half step of the result
+        const float x = static_cast<float>(static_cast<int32_t>(turn)) * 1.46291807926715968e-9f;   // pi / 2^31
+        c = __cosf(x);
+        s = __sinf(x);
+    }
+    return make_float2(c, s);
+}
+
+__device__ __forceinline__ uint32_t turn_of(int64_t position, uint64_t turns)
+{
+    return static_cast<uint32_t>((static_cast<uint64_t>(position) * turns) >> 32);
+}
+
+__device__ __forceinline__ int64_t position_of(const RotaryArgs& a, int64_t token)
+{
+    return a.wide_positions ? static_cast<const int64_t*>(a.positions)[token]
+                            : static_cast<const int32_t*>(a.positions)[token];
+}
+
+// Where a token of a batch stands: its position, and the slot that it gets.
+struct TokenPlace {
+    int64_t position;
+    int64_t offset;   // elements from the cache's start
+    bool live;        // it belongs to a sequence
+    bool stored;      // and has a slot
+};
+
+// `starts`: the first min(seqs, kStarts) + 1 of them, in shared memory.
+__device__ __forceinline__ TokenPlace token_place(const PagedArgs& p, const int32_t* starts, int64_t token,
+                                                  int64_t slot_pitch)
+{
+    TokenPlace t{};
+    const int32_t* s = p.seqs <= kStarts ? starts : p.starts;
+    if (token < s[0] || token >= s[p.seqs])
+        return t;
+    int lo = 0, hi = p.seqs;   // s[lo] <= token < s[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s[mid] <= token)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    t.live = true;
+    int64_t length = p.lengths[lo];
+    length = min(length, static_cast<int64_t>(p.most_pages) * p.page_size);
+    t.position = length - s[lo + 1] + token;
+    if (t.position < 0)
+        return t;
+    if (t.position >= length)   // starts that fall
+        return t;
+    const int at = static_cast<int>(t.position), n = at / p.page_size;   // < most_pages
+    const int64_t page = p.pages[lo * p.pages_pitch + n];
+    t.stored = page >= 0 && page < p.cache_pages;
+    t.offset = page * p.page_pitch + (at - n * p.page_size) * slot_pitch;
+    return t;
+}
+
+__device__ __forceinline__ void load_starts(const PagedArgs& p, int32_t* starts)
+{
+    if (p.seqs <= kStarts)
+        for (int i = threadIdx.x; i <= p.seqs; i += blockDim.x)
+            starts[i] = p.starts[i];
+    __syncthreads();
+}
+
+// A thread's 16 channels: two octs of a head, and the first of the eight pairs
+// that they are.
+struct Slot {
+    int ch[2];
+    bool has[2], turned[2];
+    int pair;
+};
+
+template <bool INTER>
+__device__ __forceinline__ Slot slot_of(int j, int dim, int rot)
+{
+    Slot s;
+    s.pair = 8 * j;
+    if (INTER || 16 * j >= rot) {   // neighbours; what does not turn is laid out alike
+        s.ch[0] = 16 * j;
+        s.ch[1] = 16 * j + 8;
+    } else {
+        s.ch[0] = 8 * j;
+        s.ch[1] = rot / 2 + 8 * j;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        s.has[i] = s.ch[i] < dim;
+        s.turned[i] = INTER ? s.ch[i] < rot : 16 * j < rot;
+    }
+    return s;
+}
+
+template <int DT>
+__device__ __forceinline__ void slot_angles(const RotaryArgs& a, const Slot& s, int64_t position, float (&c)[8],
+                                            float (&n)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        c[i] = 1.f;
+        n[i] = 0.f;
+        if (s.pair + i < a.rot / 2) {
+            const float2 v = cos_sin<DT>(turn_of(position, a.turns[s.pair + i]));
+            c[i] = v.x * a.amplitude;
+            n[i] = v.y * a.amplitude;
+        }
+    }
+}
+
+// The pairs of two octs turned by the angles, or (BACK) against them.
+template <bool INTER, bool BACK>
+__device__ __forceinline__ void turn(const Slot& s, const float (&c)[8], const float (&n)[8], float2 (&u)[4],
+                                     float2 (&v)[4])
+{
+    if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (s.turned[0]) {
+                const float2 t = make_float2(BACK ? u[j].y : -u[j].y, BACK ? -u[j].x : u[j].x);
+                u[j] = __ffma2_rn(t, pair_of(n[j]), __fmul2_rn(u[j], pair_of(c[j])));
+            }
+            if (s.turned[1]) {
+                const float2 t = make_float2(BACK ? v[j].y : -v[j].y, BACK ? -v[j].x : v[j].x);
+                v[j] = __ffma2_rn(t, pair_of(n[4 + j]), __fmul2_rn(v[j], pair_of(c[4 + j])));
+            }
+        }
+    } else if (s.turned[0]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 cc = make_float2(c[2 * j], c[2 * j + 1]), nn = make_float2(n[2 * j], n[2 * j + 1]);
+            const float2 mm = make_float2(-nn.x, -nn.y), p = u[j];
+            u[j] = __ffma2_rn(v[j], BACK ? nn : mm, __fmul2_rn(p, cc));
+            v[j] = __ffma2_rn(p, BACK ? mm : nn, __fmul2_rn(v[j], cc));
+        }
+    }
+}
+
+// Sum over the `team` neighbouring threads of a head; every thread of the warp takes part.
+__device__ __forceinline__ float team_sum(float v, int team)
+{
+    for (int m = team / 2; m > 0; m >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+__device__ __forceinline__ float squares(const float2 (&u)[4], const float2 (&v)[4])
+{
+    float2 q = __fmul2_rn(u[0], u[0]);
+#pragma unroll
+    for (int j = 1; j < 4; ++j)
+        q = __ffma2_rn(u[j], u[j], q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        q = __ffma2_rn(v[j], v[j], q);
+    return q.x + q.y;
+}
+
+__device__ __forceinline__ const RotaryRole& role_of(const RotaryArgs& a)
+{
+    const int b = blockIdx.x;
+    return a.role[a.roles > 1 && b >= a.role[1].first ? (a.roles > 2 && b >= a.role[2].first ? 2 : 1) : 0];
+}
+
+template <int DT>
+__device__ __forceinline__ void slot_weights(const RotaryArgs& a, const RotaryRole& r, const Slot& s, float2 (&wu)[4],
+                                             float2 (&wv)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        wu[j] = wv[j] = pair_of(1.f);
+    if (r.weight) {
+        param_floats<DT, true>(r.weight, a.wide_params, r.packed_weight, 0, OctAt{s.ch[0], 1, a.dim}, wu);
+        param_floats<DT, true>(r.weight, a.wide_params, r.packed_weight, 0, OctAt{s.ch[1], 1, a.dim}, wv);
+    }
+}
+
+// Forward.  The gradient of the rotation alone is the same with frequencies of the
+// other sign.
+template <int DT, bool INTER, bool NORM, bool PAGED>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a)
+{
+    constexpr int N = rotary_batch(DT);
+    __shared__ int32_t starts[PAGED ? kStarts + 1 : 1];
+    const RotaryRole& r = role_of(a);
+    if constexpr (PAGED)
+        load_starts(a.paged, starts);
+    const int teams = kRotaryThreads / a.team, lane = threadIdx.x & (a.team - 1);
+    const uint32_t item = (blockIdx.x - r.first) * teams + threadIdx.x / a.team;   // tokens * heads < 2^31
+    const uint32_t which = item / static_cast<uint32_t>(r.parts);
+    const int64_t token = which;
+    const int part = static_cast<int>(item - which * r.parts);
+    const Slot s = slot_of<INTER>(lane, a.dim, a.rot);
+    bool live = token < a.tokens;
+    int64_t position = 0, base = token * r.out_pitch;
+    if constexpr (PAGED) {
+        if (live) {
+            const TokenPlace t = token_place(a.paged, starts, token, r.out_pitch);
+            live = t.live && (t.stored || !r.paged);
+            position = t.position;
+            if (r.paged)
+                base = t.offset;
+        }
+    } else if (live) {
+        position = position_of(a, token);
+    }
+    const char* in = r.x + (token * r.x_pitch) * elem_size(DT);
+    char* out = r.out + base * elem_size(DT);
+    float c[8], n[8];
+    float2 wu[4], wv[4];
+    bool first = true;
+    for (int h0 = part; h0 - part < r.heads; h0 += N * r.parts) {   // alike for all threads of the CTA
+        Oct<DT> u[N], v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int h = h0 + i * r.parts;
+            const char* p = in + h * r.x_head * elem_size(DT);
+            if (live && h < r.heads && s.has[0])
+                u[i] = oct_load<DT, true>(p + s.ch[0] * elem_size(DT), OctAt{});
+            else
+                oct_zero(u[i]);
+            if (live && h < r.heads && s.has[1])
+                v[i] = oct_load<DT, true>(p + s.ch[1] * elem_size(DT), OctAt{});
+            else
+                oct_zero(v[i]);
+        }
+        if (first) {   // while the first heads are on their way
+            first = false;
+            if (r.turn) {
+                slot_angles<DT>(a, s, position, c, n);
+                if constexpr (NORM)
+                    slot_weights<DT>(a, r, s, wu, wv);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int h = h0 + i * r.parts;
+            if (r.turn) {
+                float2 p[4], q[4];
+                oct_floats(u[i], p);
+                oct_floats(v[i], q);
+                if constexpr (NORM) {
+                    const float2 f = pair_of(rsqrtf(team_sum(squares(p, q), a.team) / a.dim + a.eps));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        p[j] = __fmul2_rn(__fmul2_rn(p[j], f), wu[j]);
+                        q[j] = __fmul2_rn(__fmul2_rn(q[j], f), wv[j]);
+                    }
+                }
+                turn<INTER, false>(s, c, n, p, q);
+                if (NORM || s.turned[0])   // the others keep their bits
+                    u[i] = oct_round<DT>(p);
+                if (NORM || s.turned[1])
+                    v[i] = oct_round<DT>(q);
+            }
+            char* p = out + h * r.out_head * elem_size(DT);
+            if (live && h < r.heads && s.has[0])
+                oct_store<DT, true>(p + s.ch[0] * elem_size(DT), OctAt{}, u[i]);
+            if (live && h < r.heads && s.has[1])
+                oct_store<DT, true>(p + s.ch[1] * elem_size(DT), OctAt{}, v[i]);
+        }
+    }
+}
+
+// Sums of a CTA's warps [kWarps][dim] to its slice.
+__device__ __forceinline__ void store_slice(const RotaryRole& r, int dim, const float* sums)
+{
+    __syncthreads();
+    float* to = r.slices + static_cast<int64_t>(blockIdx.x - r.first) * dim;
+    for (int ch = threadIdx.x; ch < dim; ch += blockDim.x) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            v += sums[w * kRotaryDim + ch];
+        to[ch] = v;
+    }
+}
+
+// Backward through norm and rotation.  CTAs stay for all their tokens, so that the
+// weights' gradients come out as one slice to a CTA.
+template <int DT, bool INTER>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_norm_backward_kernel(const __grid_constant__ RotaryArgs a)
+{
+    constexpr int N = rotary_batch(DT) / 2;
+    __shared__ float sums[kWarps * kRotaryDim];
+    const RotaryRole& r = role_of(a);
+    let_next_start();
+    const int teams = kRotaryThreads / a.team, lane = threadIdx.x & (a.team - 1);
+    const Slot s = slot_of<INTER>(lane, a.dim, a.rot);
+    float2 wu[4], wv[4], su[4], sv[4];
+    slot_weights<DT>(a, r, s, wu, wv);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        su[j] = sv[j] = pair_of(0.f);
+    const uint32_t items = static_cast<uint32_t>(a.tokens) * r.parts;   // < 2^31
+    const float by_dim = 1.f / a.dim;
+    for (uint32_t first = (blockIdx.x - r.first) * teams; first < items; first += r.ctas * teams) {
+        const uint32_t item = first + threadIdx.x / a.team, which = item / static_cast<uint32_t>(r.parts);
+        const int64_t token = which;
+        const int part = static_cast<int>(item - which * r.parts);
+        const bool live = item < items;
+        const int64_t position = live ? position_of(a, token) : 0;
+        const char* in = r.x + (token * r.x_pitch) * elem_size(DT);
+        const char* saved = r.saved + (token * r.saved_pitch) * elem_size(DT);
+        char* out = r.out + token * r.out_pitch * elem_size(DT);
+        float c[8], n[8];
+        for (int h0 = part; h0 - part < r.heads; h0 += N * r.parts) {
+            Oct<DT> du[N], dv[N], xu[N], xv[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int h = h0 + i * r.parts;
+                const char* p = in + h * r.x_head * elem_size(DT);
+                const char* q = saved + h * r.saved_head * elem_size(DT);
+                oct_zero(du[i]);
+                oct_zero(xu[i]);
+                oct_zero(dv[i]);
+                oct_zero(xv[i]);
+                if (live && h < r.heads && s.has[0]) {
+                    du[i] = oct_load<DT, true>(p + s.ch[0] * elem_size(DT), OctAt{});
+                    xu[i] = oct_load<DT, true>(q + s.ch[0] * elem_size(DT), OctAt{});
+                }
+                if (live && h < r.heads && s.has[1]) {
+                    dv[i] = oct_load<DT, true>(p + s.ch[1] * elem_size(DT), OctAt{});
+                    xv[i] = oct_load<DT, true>(q + s.ch[1] * elem_size(DT), OctAt{});
+                }
+            }
+            if (h0 == part)
+                slot_angles<DT>(a, s, position, c, n);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int h = h0 + i * r.parts;
+                float2 p[4], q[4], x[4], y[4];
+                oct_floats(du[i], p);
+                oct_floats(dv[i], q);
+                oct_floats(xu[i], x);
+                oct_floats(xv[i], y);
+                turn<INTER, true>(s, c, n, p, q);
+                const float rstd = rsqrtf(team_sum(squares(x, y), a.team) * by_dim + a.eps);
+                float2 along = pair_of(0.f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {   // x becomes xhat, and d weight along it
+                    x[j] = __fmul2_rn(x[j], pair_of(rstd));
+                    y[j] = __fmul2_rn(y[j], pair_of(rstd));
+                    su[j] = __ffma2_rn(p[j], x[j], su[j]);
+                    sv[j] = __ffma2_rn(q[j], y[j], sv[j]);
+                    p[j] = __fmul2_rn(p[j], wu[j]);
+                    q[j] = __fmul2_rn(q[j], wv[j]);
+                    along = __ffma2_rn(p[j], x[j], along);
+                    along = __ffma2_rn(q[j], y[j], along);
+                }
+                const float2 m = pair_of(-team_sum(along.x + along.y, a.team) * by_dim);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    p[j] = __fmul2_rn(__ffma2_rn(x[j], m, p[j]), pair_of(rstd));
+                    q[j] = __fmul2_rn(__ffma2_rn(y[j], m, q[j]), pair_of(rstd));
+                }
+                char* to = out + h * r.out_head * elem_size(DT);
+                if (live && h < r.heads && s.has[0])
+                    oct_store<DT, true>(to + s.ch[0] * elem_size(DT), OctAt{}, oct_round<DT>(p));
+                if (live && h < r.heads && s.has[1])
+                    oct_store<DT, true>(to + s.ch[1] * elem_size(DT), OctAt{}, oct_round<DT>(q));
+            }
+        }
+    }
+    if (!r.slices)
+        return;
+    for (int m = a.team; m < 32; m *= 2)   // over the teams of a warp
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            su[j].x += __shfl_xor_sync(0xffffffffu, su[j].x, m);
+            su[j].y += __shfl_xor_sync(0xffffffffu, su[j].y, m);
+            sv[j].x += __shfl_xor_sync(0xffffffffu, sv[j].x, m);
+            sv[j].y += __shfl_xor_sync(0xffffffffu, sv[j].y, m);
+        }
+    if ((threadIdx.x & 31) < a.team) {
+        float* to = sums + threadIdx.x / 32 * kRotaryDim;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (s.has[0]) {
+                to[s.ch[0] + 2 * j] = su[j].x;
+                to[s.ch[0] + 2 * j + 1] = su[j].y;
+            }
+            if (s.has[1]) {
+                to[s.ch[1] + 2 * j] = sv[j].x;
+                to[s.ch[1] + 2 * j + 1] = sv[j].y;
+            }
+        }
+    }
+    store_slice(r, a.dim, sums);
+}
+
+// ---------------------------------------------------- element by element
+// Any layout: a warp to a head, a lane to every 32nd pair and to every 32nd of
+// the channels that do not turn.
+
+template <int DT>
+struct Elem {
+    using type = unsigned short;
+};
+template <>
+struct Elem<TSX_F32> {
+    using type = float;
+};
+
+template <int DT>
+__device__ __forceinline__ float elem_load(const char* base, int64_t at)
+{
+    const typename Elem<DT>::type v = reinterpret_cast<const typename Elem<DT>::type*>(base)[at];
+    if constexpr (DT == TSX_F32)
+        return v;
+    else if constexpr (DT == TSX_BF16)
+        return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    else
+        return __half2float(__ushort_as_half(v));
+}
+
+template <int DT>
+__device__ __forceinline__ void elem_store(char* base, int64_t at, float f)
+{
+    typename Elem<DT>::type* p = reinterpret_cast<typename Elem<DT>::type*>(base) + at;
+    if constexpr (DT == TSX_F32)
+        *p = f;
+    else if constexpr (DT == TSX_BF16)
+        *p = __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    else
+        *p = __half_as_ushort(__float2half_rn(f));
+}
+
+template <int DT>
+__device__ __forceinline__ void elem_copy(char* to, const char* from, int64_t at)
+{
+    reinterpret_cast<typename Elem<DT>::type*>(to)[at] = reinterpret_cast<const typename Elem<DT>::type*>(from)[at];
+}
+
+template <int DT>
+__device__ __forceinline__ float weight_of(const RotaryArgs& a, const RotaryRole& r, int ch)
+{
+    if (!r.weight)
+        return 1.f;
+    return a.wide_params ? static_cast<const float*>(r.weight)[ch]
+                         : elem_load<DT>(static_cast<const char*>(r.weight), ch);
+}
+
+constexpr int kPairs = kRotaryDim / 64, kOthers = kRotaryDim / 32;   // of a lane at most
+
+// BACK: the gradient through norm and rotation.
+template <int DT, bool BACK>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const __grid_constant__ RotaryArgs a)
+{
+    __shared__ int32_t starts[kStarts + 1];
+    __shared__ float sums[BACK ? kWarps * kRotaryDim : 1];
+    const RotaryRole& r = role_of(a);
+    if constexpr (BACK)
+        let_next_start();
+    if (!a.positions)
+        load_starts(a.paged, starts);
+    const int lane = threadIdx.x & 31, rot = r.turn ? a.rot : 0, half = rot / 2;
+    const bool norm = a.norm && r.turn;
+    const int step = a.layout == TSX_ROPE_INTERLEAVED ? 2 : 1, far = a.layout == TSX_ROPE_INTERLEAVED ? 1 : half;
+    float sa[kPairs], sb[kPairs], so[kOthers];   // sums for the weight's gradient
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k)
+        sa[k] = sb[k] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kOthers; ++k)
+        so[k] = 0.f;
+    const uint32_t items = static_cast<uint32_t>(a.tokens) * r.parts;   // < 2^31
+    for (uint32_t item = (blockIdx.x - r.first) * kWarps + threadIdx.x / 32; item < items;
+         item += r.ctas * kWarps) {   // alike for all threads of a warp
+        const int64_t token = item / static_cast<uint32_t>(r.parts);
+        int64_t position = 0, base = token * r.out_pitch;
+        if (a.positions) {
+            position = position_of(a, token);
+        } else {
+            const TokenPlace t = token_place(a.paged, starts, token, r.out_pitch);
+            if (!t.live || (r.paged && !t.stored))
+                continue;
+            position = t.position;
+            if (r.paged)
+                base = t.offset;
+        }
+        float c[kPairs], n[kPairs];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            c[k] = 1.f;
+            n[k] = 0.f;
+            if (lane + 32 * k < half) {
+                const float2 v = cos_sin<DT>(turn_of(position, a.turns[lane + 32 * k]));
+                c[k] = v.x * a.amplitude;
+                n[k] = v.y * a.amplitude;
+            }
+        }
+        for (int h = static_cast<int>(item - token * r.parts); h < r.heads; h += r.parts) {
+            const char* in = r.x + (token * r.x_pitch + h * r.x_head) * elem_size(DT);
+            const char* saved = r.saved + (token * r.saved_pitch + h * r.saved_head) * elem_size(DT);
+            char* out = r.out + (base + h * r.out_head) * elem_size(DT);
+            float u[kPairs], v[kPairs], o[kOthers], x[kPairs], y[kPairs], z[kOthers];
+            float squares = 0.f, along = 0.f;
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                const int i = lane + 32 * k;
+                u[k] = v[k] = x[k] = y[k] = 0.f;
+                if (i < half) {
+                    u[k] = elem_load<DT>(in, i * step);
+                    v[k] = elem_load<DT>(in, i * step + far);
+                    if constexpr (BACK) {
+                        x[k] = elem_load<DT>(saved, i * step);
+                        y[k] = elem_load<DT>(saved, i * step + far);
+                    }
+                }
+                squares += BACK ? x[k] * x[k] + y[k] * y[k] : u[k] * u[k] + v[k] * v[k];
+            }
+#pragma unroll
+            for (int k = 0; k < kOthers; ++k) {
+                const int ch = rot + lane + 32 * k;
+                o[k] = z[k] = 0.f;
+                if (ch < a.dim) {
+                    o[k] = elem_load<DT>(in, ch);
+                    if constexpr (BACK)
+                        z[k] = elem_load<DT>(saved, ch);
+                }
+                squares += BACK ? z[k] * z[k] : o[k] * o[k];
+            }
+            float rstd = 1.f;
+            if (norm)
+                rstd = rsqrtf(team_sum(squares, 32) / a.dim + a.eps);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                const int i = lane + 32 * k;
+                if (i >= half)
+                    continue;
+                const int c0 = i * step, c1 = i * step + far;
+                if constexpr (BACK) {
+                    const float p = u[k];
+                    u[k] = p * c[k] + v[k] * n[k];
+                    v[k] = v[k] * c[k] - p * n[k];
+                    x[k] *= rstd;
+                    y[k] *= rstd;
+                    sa[k] += u[k] * x[k];
+                    sb[k] += v[k] * y[k];
+                    u[k] *= weight_of<DT>(a, r, c0);
+                    v[k] *= weight_of<DT>(a, r, c1);
+                    along += u[k] * x[k] + v[k] * y[k];
+                } else {
+                    if (norm) {
+                        u[k] = u[k] * rstd * weight_of<DT>(a, r, c0);
+                        v[k] = v[k] * rstd * weight_of<DT>(a, r, c1);
+                    }
+                    const float p = u[k];
+                    u[k] = p * c[k] - v[k] * n[k];
+                    v[k] = v[k] * c[k] + p * n[k];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kOthers; ++k) {
+                const int ch = rot + lane + 32 * k;
+                if (ch >= a.dim)
+                    continue;
+                if constexpr (BACK) {
+                    z[k] *= rstd;
+                    so[k] += o[k] * z[k];
+                    o[k] *= weight_of<DT>(a, r, ch);
+                    along += o[k] * z[k];
+                } else if (norm) {
+                    o[k] = o[k] * rstd * weight_of<DT>(a, r, ch);
+                }
+            }
+            if constexpr (BACK) {
+                const float m = team_sum(along, 32) / a.dim;
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) {
+                    u[k] = (u[k] - x[k] * m) * rstd;
+                    v[k] = (v[k] - y[k] * m) * rstd;
+                }
+#pragma unroll
+                for (int k = 0; k < kOthers; ++k)
+                    o[k] = (o[k] - z[k] * m) * rstd;
+            }
+            __syncwarp();   // all lanes have loaded: the output may lie over an input
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k)
+                if (lane + 32 * k < half) {
+                    elem_store<DT>(out, (lane + 32 * k) * step, u[k]);
+                    elem_store<DT>(out, (lane + 32 * k) * step + far, v[k]);
+                }
+#pragma unroll
+            for (int k = 0; k < kOthers; ++k)
+                if (rot + lane + 32 * k < a.dim) {
+                    if (BACK || norm)
+                        elem_store<DT>(out, rot + lane + 32 * k, o[k]);
+                    else   // as it is, to the bit
+                        elem_copy<DT>(out, in, rot + lane + 32 * k);
+                }
+        }
+    }
+    if constexpr (BACK) {
+        if (!r.slices)
+            return;
+        float* to = sums + threadIdx.x / 32 * kRotaryDim;
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k)
+            if (lane + 32 * k < half) {
+                to[(lane + 32 * k) * step] = sa[k];
+                to[(lane + 32 * k) * step + far] = sb[k];
+            }
+#pragma unroll
+        for (int k = 0; k < kOthers; ++k)
+            if (rot + lane + 32 * k < a.dim)
+                to[rot + lane + 32 * k] = so[k];
+        store_slice(r, a.dim, sums);
+    }
+}
+
+// The weights' gradients from the CTAs' slices: 32 channels to a CTA, 32 threads
+// to a channel, in an order that the number of slices fixes.
+__global__ void __launch_bounds__(1024) rotary_weights_kernel(const __grid_constant__ RotaryArgs a, float* dq_weight,
+                                                              float* dk_weight)
+{
+    __shared__ float part[32][33];
+    const bool of_q = blockIdx.y == 0;
+    float* to = of_q ? dq_weight : dk_weight;
+    const float* slices = nullptr;
+    int count = 0;
+    for (int i = 0; i < a.roles; ++i)   // a role that has no heads is not there, and its gradient 0
+        if ((a.role[i].which == 0) == of_q) {
+            slices = a.role[i].slices;
+            count = a.role[i].ctas;
+        }
+    wait_for_last();
+    if (!to)
+        return;
+    const int ch = blockIdx.x * 32 + threadIdx.x % 32, row = threadIdx.x / 32;
+    float v = 0.f;
+    if (ch < a.dim && slices)
+        for (int i = row; i < count; i += 32)
+            v += slices[static_cast<int64_t>(i) * a.dim + ch];
+    part[row][threadIdx.x % 32] = v;
+    __syncthreads();
+    v = part[threadIdx.x % 32][row];   // a warp to a channel
+    v = team_sum(v, 32);
+    if (threadIdx.x % 32 == 0 && blockIdx.x * 32 + row < a.dim)
+        to[blockIdx.x * 32 + row] = v;
+}
+
+template <int DT, bool NORM, bool PAGED>
+cudaError_t launch_vec(const RotaryArgs& a, int ctas, cudaStream_t st)
+{
+    if (a.layout == TSX_ROPE_INTERLEAVED)
+        return launch_grid<rotary_kernel<DT, true, NORM, PAGED>>(dim3(unsigned(ctas)), kRotaryThreads, 0, 1, false, st, a);
+    return launch_grid<rotary_kernel<DT, false, NORM, PAGED>>(dim3(unsigned(ctas)), kRotaryThreads, 0, 1, false, st, a);
+}
+
+template <int DT>
+cudaError_t launch_forward(const RotaryArgs& a, bool vec, int ctas, cudaStream_t st)
+{
+    if (!vec)
+        return launch_grid<rotary_any_kernel<DT, false>>(dim3(unsigned(ctas)), kRotaryThreads, 0, 1, false, st, a);
+    if (a.positions)
+        return a.norm ? launch_vec<DT, true, false>(a, ctas, st) : launch_vec<DT, false, false>(a, ctas, st);
+    return a.norm ? launch_vec<DT, true, true>(a, ctas, st) : launch_vec<DT, false, true>(a, ctas, st);
+}
+
+template <int DT>
+cudaError_t launch_backward(const RotaryArgs& a, bool vec, int ctas, cudaStream_t st)
+{
+    if (!vec)
+        return launch_grid<rotary_any_kernel<DT, true>>(dim3(unsigned(ctas)), kRotaryThreads, 0, 1, false, st, a);
+    if (a.layout == TSX_ROPE_INTERLEAVED)
+        return launch_grid<rotary_norm_backward_kernel<DT, true>>(dim3(unsigned(ctas)), kRotaryThreads, 0, 1, false, st, a);
+    return launch_grid<rotary_norm_backward_kernel<DT, false>>(dim3(unsigned(ctas)), kRotaryThreads, 0, 1, false, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(int dtype, const RotaryArgs& a, bool vec, int ctas, cudaStream_t st)
+{
+    return dtype == TSX_F32    ? launch_forward<TSX_F32>(a, vec, ctas, st)
+           : dtype == TSX_BF16 ? launch_forward<TSX_BF16>(a, vec, ctas, st)
+                               : launch_forward<TSX_F16>(a, vec, ctas, st);
+}
+
+cudaError_t launch_rotary_norm_backward(int dtype, const RotaryArgs& a, bool vec, int ctas, cudaStream_t st)
+{
+    return dtype == TSX_F32    ? launch_backward<TSX_F32>(a, vec, ctas, st)
+           : dtype == TSX_BF16 ? launch_backward<TSX_BF16>(a, vec, ctas, st)
+                               : launch_backward<TSX_F16>(a, vec, ctas, st);
+}
+
+cudaError_t launch_rotary_weights(const RotaryArgs& a, float* dq_weight, float* dk_weight, cudaStream_t st)
+{
+    return launch_grid<rotary_weights_kernel>(dim3(unsigned((a.dim + 31) / 32), 2), 1024, 0, 1, true, st, a, dq_weight,
+                                              dk_weight);
+}
+
+}  // namespace tsx

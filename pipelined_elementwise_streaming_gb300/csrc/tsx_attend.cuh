@@ -1,0 +1,278 @@
+// How the attention kernels share out their work, and how parts are joined.
+//
+// The queries of a sequence that read one head are rows, `group` to a token, cut
+// into tiles of M rows; a tile goes over the keys that its last row sees, TK at a
+// time.  One such step is a unit.  All units of a call stand in a row (by sequence,
+// head, tile, step), and each of a fixed number of CTAs takes an equal run of them:
+// lengths of sequences need not be known to the host, none of them leaves CTAs
+// without work, and single long ones are split.  A CTA whose run starts or ends
+// within a tile writes a part of that tile's result (the unnormalised sum, the
+// maximum and the sum of weights) to the scratch, and a second kernel joins the
+// parts in order.
+#pragma once
+
+#include "attention.h"
+#include "tsx_norm.cuh"
+
+namespace tsx {
+namespace dev {
+
+// A sequence with new tokens.
+struct Seq {
+    int first;     // its first row of tokens
+    int fresh;     // new tokens
+    int length;    // keys, new ones among them
+    int prior;     // keys before the first new token (negative: a length shorter than that)
+};
+
+__device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b)
+{
+    const int tokens = static_cast<int>(a.tokens);
+    Seq s;
+    s.first = min(max(a.paged.starts[b], 0), tokens);
+    s.fresh = min(max(a.paged.starts[b + 1], s.first), tokens) - s.first;
+    const int64_t most = static_cast<int64_t>(a.paged.most_pages) * a.paged.page_size;
+    s.length = static_cast<int>(min(static_cast<int64_t>(max(a.paged.lengths[b], 0)), most));
+    s.prior = s.length - s.fresh;
+    return s;
+}
+
+// Keys that a row sees: those before this one.
+__device__ __forceinline__ int row_limit(const AttendArgs& a, const Seq& s, int row)
+{
+    return max(s.prior + row / a.group + 1, 0);
+}
+
+// Sum of floor((step i + from) / by) over 0 <= i < n.
+__device__ inline uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
+{
+    uint64_t sum = 0;
+    while (n) {
+        sum += n * (n - 1) / 2 * (step / by) + n * (from / by);
+        step %= by;
+        from %= by;
+        const uint64_t top = step * n + from;
+        n = top / by;   // as many i of the mirrored sum
+        from = top % by;
+        const uint64_t t = by;
+        by = step;
+        step = t;
+    }
+    return sum;
+}
+
+template <int M>
+__device__ __forceinline__ int tiles_of(const AttendArgs& a, const Seq& s)
+{
+    return (s.fresh * a.group + M - 1) / M;   // tokens * heads < 2^31
+}
+
+// Steps of a tile, at least one.
+template <int M, int TK>
+__device__ __forceinline__ int steps_of(const AttendArgs& a, const Seq& s, int tile)
+{
+    if (s.prior < 0)
+        return max((s.length + TK - 1) / TK, 1);
+    const int last = min(s.fresh * a.group - tile * M, M) + tile * M - 1;
+    return (row_limit(a, s, last) + TK - 1) / TK;
+}
+
+// Steps of the first n tiles.
+template <int M, int TK>
+__device__ __forceinline__ int64_t steps_before(const AttendArgs& a, const Seq& s, int n)
+{
+    if (s.prior < 0)
+        return static_cast<int64_t>(n) * max((s.length + TK - 1) / TK, 1);
+    // ceil((prior + 1 + floor(last row / group)) / TK) with the divisions in one
+    return static_cast<int64_t>(floor_sum(static_cast<uint64_t>(n), static_cast<uint64_t>(a.group) * TK, M,
+                                          M - 1 + static_cast<uint64_t>(a.group) * (s.prior + TK)));
+}
+
+template <int M, int TK>
+__device__ __forceinline__ int64_t steps_of_head(const AttendArgs& a, const Seq& s)
+{
+    const int tiles = tiles_of<M>(a, s);
+    if (tiles == 0)
+        return 0;
+    return steps_of<M, TK>(a, s, tiles - 1) + (tiles > 1 ? steps_before<M, TK>(a, s, tiles - 1) : 0);
+}
+
+// A CTA's run of units, and where it starts.
+struct Run {
+    int64_t from, to, per;   // units; per: of a CTA
+    int b, head, tile, step;
+};
+
+// Every thread of the CTA takes part; `sums` holds a word to each warp and three more.
+template <int M, int TK, int THREADS>
+__device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_t* sums)
+{
+    constexpr int kWarps = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    Run r{};
+    int64_t total = 0;
+    for (int pass = 0; pass < 2; ++pass) {   // the sum of all, then who has the first of mine
+        int64_t before = 0;
+        for (int base = 0; base < a.paged.seqs; base += THREADS) {
+            const int b = base + threadIdx.x;
+            int64_t mine = 0, head = 0;
+            if (b < a.paged.seqs) {
+                head = steps_of_head<M, TK>(a, seq_of(a, b));
+                mine = head * a.heads;
+            }
+            int64_t upto = mine;
+#pragma unroll
+            for (int m = 1; m < 32; m *= 2) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, upto, m);
+                upto += lane >= m ? o : 0;
+            }
+            if (lane == 31)
+                sums[warp] = upto;
+            __syncthreads();
+            int64_t all = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                upto += w < warp ? sums[w] : 0;
+                all += sums[w];
+            }
+            upto += before;
+            before += all;
+            if (pass == 0 && base + THREADS >= a.paged.seqs) {
+                total = before;
+                r.per = max((total + gridDim.x - 1) / gridDim.x, least);
+                r.from = min(static_cast<int64_t>(blockIdx.x) * r.per, total);
+                r.to = min(r.from + r.per, total);
+            }
+            // one block of sequences: its sums are at hand
+            if ((pass == 1 || a.paged.seqs <= THREADS) && r.from < r.to && upto - mine <= r.from && r.from < upto) {
+                sums[kWarps] = b;
+                sums[kWarps + 1] = r.from - (upto - mine);
+                sums[kWarps + 2] = head;
+            }
+            __syncthreads();
+        }
+        if (a.paged.seqs <= THREADS || r.from >= r.to)
+            break;
+    }
+    if (r.from >= r.to)
+        return r;
+    r.b = static_cast<int>(sums[kWarps]);
+    int64_t rest = sums[kWarps + 1];
+    const int64_t head = sums[kWarps + 2];
+    r.head = static_cast<int>(rest / head);
+    rest -= r.head * head;
+    const Seq s = seq_of(a, r.b);
+    int lo = 0, hi = tiles_of<M>(a, s);   // the tile: steps_before(lo) <= rest
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (steps_before<M, TK>(a, s, mid) <= rest)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    r.tile = lo;
+    r.step = static_cast<int>(rest - (lo ? steps_before<M, TK>(a, s, lo) : 0));
+    return r;
+}
+
+// A part of a run within one tile: steps `step` .. end - 1 of `steps`.
+struct Piece {
+    Seq seq;
+    int b, head, tile, step, end, steps, rows;
+    __device__ bool whole() const { return step == 0 && end == steps; }
+};
+
+template <int M, int TK>
+__device__ __forceinline__ Piece piece_of(const AttendArgs& a, const Run& r)
+{
+    Piece p;
+    p.seq = seq_of(a, r.b);
+    p.b = r.b;
+    p.head = r.head;
+    p.tile = r.tile;
+    p.step = r.step;
+    p.steps = steps_of<M, TK>(a, p.seq, r.tile);
+    p.end = static_cast<int>(min(static_cast<int64_t>(p.steps), r.step + (r.to - r.from)));
+    p.rows = min(p.seq.fresh * a.group - r.tile * M, M);
+    return p;
+}
+
+template <int M>
+__device__ __forceinline__ void advance(const AttendArgs& a, Run& r, const Piece& p)
+{
+    r.from += p.end - p.step;
+    r.step = 0;
+    if (r.from >= r.to)
+        return;
+    if (++r.tile < tiles_of<M>(a, p.seq))
+        return;
+    r.tile = 0;
+    if (++r.head < a.heads)
+        return;
+    r.head = 0;
+    do
+        ++r.b;
+    while (seq_of(a, r.b).fresh == 0);   // units are left, so some sequence has tokens
+}
+
+// The scratch: parts of a CTA's first and last tile, and what its last one is.
+struct Tail {
+    int follow;   // CTAs that go on with the tile (0: nothing to join)
+    int token, row0, rows, head;
+};
+
+// Where the CTA's part of this piece goes, and what is to be joined.
+__device__ __forceinline__ int part_slot(const Piece& p) { return 2 * blockIdx.x + (p.step == 0 ? 1 : 0); }
+
+template <int M>
+__device__ __forceinline__ Tail tail_of(const Run& r, const Piece& p)
+{
+    Tail t{};
+    if (p.step == 0 && p.end < p.steps) {
+        t.follow = static_cast<int>((r.from + p.steps - 1) / r.per) - static_cast<int>(blockIdx.x);
+        t.token = p.seq.first;
+        t.row0 = p.tile * M;
+        t.rows = p.rows;
+        t.head = p.head;
+    }
+    return t;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Row `row` of a sequence's rows of a head: element of q or out.
+__device__ __forceinline__ int64_t row_at(const AttendArgs& a, int first, int head, int row, int64_t pitch,
+                                          int64_t head_pitch)
+{
+    const int t = row / a.group;
+    return (first + t) * pitch + (head * a.group + row - t * a.group) * head_pitch;
+}
+
+__device__ __forceinline__ void store_lse(const AttendArgs& a, int first, int head, int row, float top, float sum)
+{
+    const int t = row / a.group;
+    if (a.lse)
+        a.lse[static_cast<int64_t>(first + t) * a.heads * a.group + head * a.group + row - t * a.group] =
+            sum > 0.f || sum != sum ? top * 0.69314718055994531f + logf(sum) : -INFINITY;
+}
+
+// Two fp32 values into one word of the element type.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    if constexpr (DT == TSX_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+}  // namespace dev
+}  // namespace tsx
