@@ -71,6 +71,7 @@ struct AttendArgs {
     int64_t slot_pitch, head_pitch, q_pitch, q_head, out_pitch, out_head, tokens;
     int heads, group, dim;   // heads of the cache, queries to each
     float scale_log2;        // scale / ln 2
+    int negated;             // many rows: scores of -q, and scale_log2 above 0
     int ctas;
     // scratch: for each CTA two slots of [rows][padded dim] sums and [rows] (maximum, sum of weights), and its Tail
     float* parts;
@@ -79,6 +80,9 @@ struct AttendArgs {
 };
 int attend_few_rows();
 int attend_few_ctas(int dim);
+// Many rows to a head, dim up to 128: one CTA to an SM.
+int attend_many_rows();
+cudaError_t launch_attend_many(int dtype, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend_few(int dtype, const AttendArgs& a, cudaStream_t st);
 
 }  // namespace tsx

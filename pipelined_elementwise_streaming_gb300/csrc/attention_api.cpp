@@ -596,9 +596,16 @@ struct Parts {
     size_t bytes() const { return sums() + stats() + size_t(ctas) * 32; }
 };
 
-Parts parts_of(int dim)
+// Whether a call takes the kernel for many rows to a head.
+bool many_rows(int dim, int64_t most_new, int group)
 {
-    return Parts{attend_few_rows(), attend_few_ctas(dim), dim <= 64 ? 64 : dim <= 128 ? 128 : 256};
+    return dim <= 128 && most_new * group > attend_few_rows();
+}
+
+Parts parts_of(int dim, bool many)
+{
+    const int padded = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+    return many ? Parts{attend_many_rows(), 152, padded} : Parts{attend_few_rows(), attend_few_ctas(dim), padded};
 }
 
 int check_attention(const char* call, const tsx_cache* cache, int64_t tokens, int q_heads, int64_t most_new)
@@ -608,8 +615,8 @@ int check_attention(const char* call, const tsx_cache* cache, int64_t tokens, in
         return rc;
     if (q_heads < 1 || q_heads % cache->heads)
         return fail(TSX_ERR_INVALID, call, "q_heads must be a multiple of the cache's heads");
-    if (most_new < 0)
-        return fail(TSX_ERR_INVALID, call, "most_new must not be negative");
+    if (most_new < 0 || most_new > kMostItems)
+        return fail(TSX_ERR_INVALID, call, "most_new must be 0 .. 2^31 - 2^20");
     return check_tokens(call, tokens, q_heads);
 }
 
@@ -624,7 +631,7 @@ extern "C" int tsx_paged_attention_workspace(const tsx_cache* cache, int64_t tok
         return rc;
     if (!bytes)
         return fail(TSX_ERR_INVALID, call, "bytes is NULL");
-    *bytes = parts_of(cache->dim).bytes();
+    *bytes = parts_of(cache->dim, many_rows(cache->dim, most_new, q_heads / cache->heads)).bytes();
     set_last_error("");
     return TSX_OK;
 }
@@ -655,7 +662,8 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     if (!cache_vectors(*cache) || !vectors(q, tokens, q_heads, 2) || !vectors(out, tokens, q_heads, 2) ||
         !aligned(lse, 4) || !aligned(workspace, 16))
         return fail(TSX_ERR_ALIGN, call, "pitches must be multiples of 8 elements and pointers of 16 bytes");
-    const Parts parts = parts_of(cache->dim);
+    const bool many = many_rows(cache->dim, most_new, q_heads / cache->heads);
+    const Parts parts = parts_of(cache->dim, many);
     if (!workspace || workspace_bytes < parts.bytes())
         return fail(TSX_ERR_INVALID, call, "the workspace is smaller than tsx_paged_attention_workspace says");
     AttendArgs a{};
@@ -681,5 +689,11 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     a.parts = reinterpret_cast<float*>(scratch);
     a.stats = reinterpret_cast<float2*>(scratch + parts.sums());
     a.tails = reinterpret_cast<dev::Tail*>(scratch + parts.sums() + parts.stats());
-    return launched(launch_attend_few(cache->dtype, a, reinterpret_cast<cudaStream_t>(stream)), call);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!many)
+        return launched(launch_attend_few(cache->dtype, a, st), call);
+    // a positive scale, so that the largest score is the largest product; not 0, which -infinity must not meet
+    a.negated = a.scale_log2 < 0;
+    a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
+    return launched(launch_attend_many(cache->dtype, a, st), call);
 }

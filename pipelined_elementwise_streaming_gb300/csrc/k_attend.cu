@@ -68,13 +68,6 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk)
     return static_cast<uint32_t>(row * (D * 2) + ((chunk ^ (row & 7)) * 16));
 }
 
-// Whether a word of two elements holds an infinity or a NaN.
-template <int DT>
-__device__ __forceinline__ bool not_finite(uint32_t w)
-{
-    const uint32_t e = DT == TSX_BF16 ? 0x7f80u : 0x7c00u;
-    return (w & e) == e || (w >> 16 & e) == e;
-}
 template <int DT>
 __device__ __forceinline__ float value_of(uint16_t w)
 {
@@ -348,47 +341,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
     }
     if (threadIdx.x == 0)
         a.tails[blockIdx.x] = tail;
-}
-
-// Joins the parts of the tile that CTA blockIdx.x has begun and not ended, four
-// rows to each CTA.
-template <int DT, int D, int M>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a)
-{
-    wait_for_last();
-    const Tail t = a.tails[blockIdx.x];
-    const int row = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (!t.follow || row >= t.rows)
-        return;
-    constexpr int kEach = D / 32;   // channels to a thread
-    const int first = 2 * blockIdx.x + 1;   // then the first slots of the CTAs that follow
-    float m = -INFINITY;
-    for (int i = 0; i <= t.follow; ++i)
-        m = fmaxf(m, a.stats[(i ? first - 1 + 2 * i : first) * M + row].x);
-    float l = 0.f, v[kEach] = {};
-    for (int i = 0; i <= t.follow; ++i) {
-        const int64_t slot = i ? first - 1 + 2 * i : first;
-        const float2 s = a.stats[slot * M + row];
-        if (s.x == -INFINITY && s.y == s.y)
-            continue;
-        const float f = s.x == -INFINITY ? s.y : exp2_fast(s.x - m);
-        l += s.y * f;
-        const float* from = a.parts + (slot * M + row) * D + lane * kEach;
-#pragma unroll
-        for (int e = 0; e < kEach; e += 2) {
-            const float2 o = *reinterpret_cast<const float2*>(from + e);
-            v[e] += o.x * f;
-            v[e + 1] += o.y * f;
-        }
-    }
-    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-    char* to = a.out + (row_at(a, t.token, t.head, t.row0 + row, a.out_pitch, a.out_head) + lane * kEach) * 2;
-#pragma unroll
-    for (int e = 0; e < kEach; e += 2)
-        if (lane * kEach + e < a.dim)
-            *reinterpret_cast<uint32_t*>(to + e * 2) = pack2<DT>(v[e] * f, v[e + 1] * f);
-    if (lane == 0)
-        store_lse(a, t.token, t.head, t.row0 + row, m, l);
 }
 
 template <int DT, int D>
