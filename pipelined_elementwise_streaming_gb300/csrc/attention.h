@@ -2,6 +2,7 @@
 // (include/tsx_attention.h): their kernels' arguments.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -35,6 +36,7 @@ struct PagedArgs {
     const int32_t *starts, *lengths, *pages;
     int64_t pages_pitch, cache_pages, page_pitch;
     int seqs, most_pages, page_size;
+    int page_shift;   // log2 of a page size that is a power of two, else -1
 };
 
 struct RotaryArgs {
@@ -82,7 +84,8 @@ int attend_few_rows();
 int attend_few_ctas(int dim);
 // Many rows to a head, dim up to 128: one CTA to an SM.
 int attend_many_rows();
-cudaError_t launch_attend_many(int dtype, const AttendArgs& a, cudaStream_t st);
+// maps: of keys and values in boxes of 64 channels and min(page, 128) slots, or NULL.
+cudaError_t launch_attend_many(int dtype, const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st);
 cudaError_t launch_attend_few(int dtype, const AttendArgs& a, cudaStream_t st);
 
 }  // namespace tsx

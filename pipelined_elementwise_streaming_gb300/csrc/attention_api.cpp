@@ -13,7 +13,7 @@ namespace tsx {
 namespace {
 
 constexpr int64_t kMostItems = 0x7fffffff - (1 << 20);   // tokens * heads
-constexpr int64_t kMostPitch = int64_t(1) << 40;         // elements
+constexpr int64_t kMostPitch = int64_t(1) << 37;         // elements: strides of tensor maps are under 2^40 bytes
 
 int fail(int rc, const char* call, const char* msg)
 {
@@ -524,6 +524,10 @@ PagedArgs paged_args(const tsx_cache& c, const tsx_batch& b)
     p.seqs = b.seqs;
     p.most_pages = b.most_pages;
     p.page_size = c.page_size;
+    p.page_shift = -1;
+    if ((c.page_size & (c.page_size - 1)) == 0)
+        for (p.page_shift = 0; 1 << p.page_shift < c.page_size; ++p.page_shift) {
+        }
     return p;
 }
 
@@ -587,6 +591,25 @@ extern "C" int tsx_cache_append(const tsx_rotary_desc* desc, const tsx_cache* ca
 }
 
 namespace {
+
+// Whether a step's 128 keys are whole pages, or part of one, that start on the
+// eight rows of the swizzle: then boxes of the pages can be copied.
+bool box_pages(const tsx_cache& c)
+{
+    return c.pages > 0 && c.page_size >= 8 && (c.page_size & (c.page_size - 1)) == 0;
+}
+
+int cache_maps(const tsx_cache& c, CUtensorMap (&maps)[2])
+{
+    const uint64_t es = uint64_t(elem_size(c.dtype)), one = 16;   // a stride that is not used
+    const uint64_t dims[4] = {uint64_t(c.dim), uint64_t(c.page_size), uint64_t(c.heads), uint64_t(c.pages)};
+    const uint64_t strides[3] = {c.page_size > 1 ? uint64_t(c.slot_pitch) * es : one,
+                                 c.heads > 1 ? uint64_t(c.head_pitch) * es : one,
+                                 c.pages > 1 ? uint64_t(c.page_pitch) * es : one};
+    const uint32_t box[4] = {64, uint32_t(std::min(c.page_size, 128)), 1, 1};
+    const int rc = encode_pages_map(c.dtype, c.k, dims, strides, box, &maps[0]);
+    return rc != TSX_OK ? rc : encode_pages_map(c.dtype, c.v, dims, strides, box, &maps[1]);
+}
 
 // Bytes of the parts of an attention call: their sums, statistics and tails.
 struct Parts {
@@ -695,5 +718,12 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     // a positive scale, so that the largest score is the largest product; not 0, which -infinity must not meet
     a.negated = a.scale_log2 < 0;
     a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
-    return launched(launch_attend_many(cache->dtype, a, st), call);
+    CUtensorMap maps[2];
+    const bool boxes = box_pages(*cache);
+    if (boxes) {
+        rc = cache_maps(*cache, maps);
+        if (rc != TSX_OK)
+            return rc;
+    }
+    return launched(launch_attend_many(cache->dtype, a, boxes ? maps : nullptr, st), call);
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <algorithm>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -257,6 +258,28 @@ int encode_tensor_map(const Geometry& g, const void* ptr, CUtensorMap* map)
     const CUresult r = fn(map, map_type(g), cuuint32_t(m.rank), const_cast<void*>(ptr), dims, strides, box,
                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, static_cast<CUtensorMapSwizzle>(m.swizzle),
                           static_cast<CUtensorMapL2promotion>(m.l2_promotion), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char buf[96];
+        std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
+        return set_error(TSX_ERR_CUDA, buf);
+    }
+    return TSX_OK;
+}
+
+int encode_pages_map(int dtype, const void* ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                     const uint32_t (&box)[4], CUtensorMap* map)
+{
+    std::string why;
+    EncodeTiledFn fn = encode_fn(&why);
+    if (!fn)
+        return set_error(TSX_ERR_CUDA, why);
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    cuuint64_t d[4], st[3];
+    std::copy(dims, dims + 4, d);
+    std::copy(strides, strides + 3, st);
+    const CUresult r = fn(map, map_dtype(dtype), 4, const_cast<void*>(ptr), d, st, box, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[96];
         std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));

@@ -49,12 +49,12 @@ template <int DT>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     if constexpr (DT == TSX_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -84,7 +84,7 @@ struct Keys {
 
     __device__ __forceinline__ void look(const AttendArgs& a)
     {
-        page = position < limit ? pages[position / a.paged.page_size] : -1;
+        page = position < limit ? pages[page_of(a.paged, position)] : -1;
     }
 };
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t load_step(const AttendArgs& a, const Keys& k
 {
     const int lane = threadIdx.x & 31;
     const bool there = k.page >= 0 && k.page < a.paged.cache_pages;
-    const int slot = k.position % a.paged.page_size;
+    const int slot = k.position - page_of(a.paged, k.position) * a.paged.page_size;
     const int64_t at = there ? (k.page * a.paged.page_pitch + slot * a.slot_pitch + head_at) * 2 : 0;
     const uint32_t seen = __ballot_sync(0xffffffffu, there) & 0xffffu;
     constexpr int kChunks = D / 8, kTurns = kWarpKeys * kChunks / 32;

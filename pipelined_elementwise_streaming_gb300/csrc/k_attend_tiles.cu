@@ -7,11 +7,15 @@
 // tensor cores nor the exponentials wait for the other: 2 x 128^3 multiply-adds a
 // step and tile are 1024 cycles at 4096 a cycle, 128^2 exponentials 512 at 32.
 //
-//   warps 0-3, 4-7   a tile each, a thread to a row: scores, maxima, weights, sums,
-//                    results (no reduction between threads)
-//   warps 8-11       loads: queries, keys and values by cp.async, since a page may
-//                    lie anywhere; which of the step's keys exist
-//   warp 12          one thread issues the products
+//   warps 0-7, 8-15  a tile each, 16 rows to a warp, four threads to a row: scores,
+//                    maxima, weights, sums, results
+//   warp 16          brings keys and values, by TMA: boxes of the pages, one to a
+//                    lane; and tells which of the step's keys exist
+//   warps 17, 18     bring queries, and look through values that not every row sees
+//   warp 19          issues the products
+//
+// Pages that are no power of two of at least 8 slots do not fit the swizzle's eight
+// rows: then warps 16 and 17 bring everything by cp.async.
 //
 // The running maximum is not followed closely: O and the sum are scaled only when
 // a row's maximum has grown by more than 2^8 over the one in use, which is rare
@@ -27,14 +31,15 @@ namespace {
 
 using namespace dev;
 
-constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128, kThreads = 512;
-constexpr int kLoaders = 128;
+constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128;
+constexpr int kWeighers = 512, kLoaders = 64, kThreads = 640;
 constexpr int64_t kLeast = 2;        // steps to a CTA at least
 constexpr int kMasks = 8;            // steps whose keys are remembered
 constexpr int kBlock = kKeys * 128;  // bytes of a block: 128 rows of 64 channels
 constexpr int kLag = 2;              // groups of loads in flight behind the last
 constexpr float kGrowth = 8.f;
 constexpr uint64_t kPatience = 4000000000ull;   // ns
+constexpr int kLoadWarp = kWeighers / 32, kIssueWarp = kLoadWarp + 3;
 
 // Keys or values of a step take a stage.  One CTA to an SM, which is what the
 // tensor memory is for: the stages of D = 64 are as many as keep a second one out.
@@ -48,8 +53,8 @@ struct Shared {
     // barriers
     static constexpr int kFull = kEnd, kEmpty = kFull + 8 * stages<D>(), kQFull = kEmpty + 8 * stages<D>(),
                          kQEmpty = kQFull + 8, kS = kQEmpty + 8, kP = kS + 16, kO = kP + 16,
-                         kReset = kO + 16, kDrain = kReset + 8;
-    static constexpr int kMask = kDrain + 8;                 // [kMasks][4] words
+                         kReset = kO + 16, kDrain = kReset + 8, kRaw = kDrain + 8;
+    static constexpr int kMask = (kRaw + 8 * stages<D>() + 15) / 16 * 16;                 // [kMasks][4] words
     static constexpr int kOdd = kMask + kMasks * 16;      // [3][D] first keys with a NaN, +inf, -inf
     static constexpr int kSums = kOdd + 3 * D * 4;        // words of run_of
     static constexpr int kWords = kSums + (kThreads / 32 + 3) * 8;   // tensor memory, pieces done, odd values met
@@ -65,6 +70,20 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase)
 
 // ------------------------------------------------------------------ loads
 
+// A place in the ring of stages.
+template <int D>
+struct Place {
+    int stage = 0;
+    uint32_t turn = 0;   // how often the ring has been gone round
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == stages<D>()) {
+            stage = 0;
+            ++turn;
+        }
+    }
+};
+
 // What a group of loads announces when it has landed: a barrier, and for values
 // that some rows do not see, where they lie.
 struct Landing {
@@ -77,69 +96,227 @@ struct Landing {
 // Values of keys that not every row sees: 0 times an infinity or a NaN would reach
 // the rows that do not.  Such values are taken out, and the first key of each kind
 // is kept for each channel; the rows from that key on get it added at the end.
+// tile: the values' tile; base: the position of its first key.
 template <int DT, int D>
-__device__ void take_out(unsigned char* memory, const Landing& l)
+__device__ __forceinline__ void take_out(unsigned char* memory, unsigned char* tile, int row, int chunk, int base)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 3;
     int* odd = reinterpret_cast<int*>(memory + Shared<D>::kOdd);
-    int* met = reinterpret_cast<int*>(memory + Shared<D>::kWords) + 2;
-    constexpr int kChunks = D / 8;
-    for (int i = 0; i < kChunks; ++i) {   // the chunks that this thread has copied
-        const int id = i * 32 + lane, row = warp * 32 + id / kChunks, chunk = id % kChunks;
-        uint32_t* at = reinterpret_cast<uint32_t*>(memory + l.stage + chunk / 8 * kBlock + row * 128 +
-                                                   ((chunk & 7) ^ (row & 7)) * 16);
-        for (int w = 0; w < 4; ++w) {
-            uint32_t v = at[w];
-            if (!not_finite<DT>(v))
-                continue;
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t half = v >> (16 * e) & 0xffffu;
-                if (!not_finite<DT>(half))
-                    continue;
-                const bool nan = half & (DT == TSX_BF16 ? 0x7fu : 0x3ffu);
-                atomicMin(odd + (nan ? 0 : half >> 15 ? 2 : 1) * D + chunk * 8 + w * 2 + e, l.base + row);
-                v &= e ? 0x0000ffffu : 0xffff0000u;
-                *met = 1;
-            }
-            at[w] = v;
-        }
+    uint4* place = reinterpret_cast<uint4*>(tile + chunk / 8 * kBlock + row * 128 + ((chunk & 7) ^ (row & 7)) * 16);
+    const uint4 v = *place;
+    if (!(not_finite<DT>(v.x) || not_finite<DT>(v.y) || not_finite<DT>(v.z) || not_finite<DT>(v.w)))
+        return;
+    uint16_t* at = reinterpret_cast<uint16_t*>(place);
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t w = at[e];
+        if (!not_finite<DT>(w))
+            continue;
+        const bool nan = w & (DT == TSX_BF16 ? 0x7fu : 0x3ffu);
+        atomicMin(odd + (nan ? 0 : w >> 15 ? 2 : 1) * D + chunk * 8 + e, base + row);
+        at[e] = 0;
     }
+    reinterpret_cast<int*>(memory + Shared<D>::kWords)[2] = 1;
+}
+
+// Before the first such values of a piece: nothing has been taken out.  False if
+// the last piece's rows have not used what was.
+template <int D>
+__device__ __forceinline__ bool forget(unsigned char* memory, uint32_t piece, uint32_t resets, int mine)
+{
+    using S = Shared<D>;
+    volatile int* done = reinterpret_cast<int*>(memory + S::kWords) + 1;
+    int* odd = reinterpret_cast<int*>(memory + S::kOdd);
+    if (piece) {
+        const uint64_t since = globaltimer_ns();
+        while (!__all_sync(0xffffffffu, *done >= static_cast<int>(kWeighers / 32 * piece)))
+            if (__any_sync(0xffffffffu, globaltimer_ns() - since > kPatience))
+                return false;
+        __threadfence_block();
+    }
+    for (int i = mine; i < 3 * D; i += kLoaders)
+        odd[i] = 0x7fffffff;
+    if (mine == 0)
+        reinterpret_cast<int*>(memory + S::kWords)[2] = 0;
+    mbar_arrive(smem_addr(memory) + S::kReset);
+    return wait_warp(smem_addr(memory) + S::kReset, resets);
 }
 
 template <int DT, int D>
 __device__ __forceinline__ void land(unsigned char* memory, const Landing& l)
 {
-    if (l.check)
-        take_out<DT, D>(memory, l);
+    if (l.check) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 1;
+        for (int i = 0; i < D / 4; ++i)   // the chunks that this thread has copied (load_rows)
+            take_out<DT, D>(memory, memory + l.stage, warp * 64 + i % 16 * 4 + lane / 8, i / 16 * 8 + lane % 8, l.base);
+    }
     fence_proxy_async_smem();
     mbar_arrive(l.bar);
 }
 
-// 32 rows of a warp, whose elements start at `at` (bytes; < 0: zeros), into a tile.
+// 32 rows, whose elements start at `at` (bytes; < 0: zeros) of lane's row, into a
+// tile from its row `row0` on.  Eight lanes copy 128 bytes of a row, so that a row's
+// place is asked for once for both of its halves.
 template <int D>
-__device__ __forceinline__ void load_rows(const char* base, int64_t at, int dim, uint32_t tile)
+__device__ __forceinline__ void load_rows(const char* base, int64_t at, int dim, uint32_t tile, int row0)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 3;
-    constexpr int kChunks = D / 8;
-#pragma unroll 4
-    for (int i = 0; i < kChunks; ++i) {
-        const int id = i * 32 + lane, in_warp = id / kChunks, chunk = id % kChunks, row = warp * 32 + in_warp;
-        const int64_t from = __shfl_sync(0xffffffffu, at, in_warp);
-        const uint32_t bytes = from >= 0 && chunk * 8 < dim ? 16 : 0;
-        cp_async(tile + chunk / 8 * kBlock + row * 128 + ((chunk & 7) ^ (row & 7)) * 16,
-                 bytes ? base + from + chunk * 16 : base, 16, bytes);
+    const int lane = threadIdx.x & 31, chunk = lane & 7, first = lane >> 3;
+    const uint32_t to[2] = {tile + (row0 + first) * 128 + ((chunk ^ first) * 16),
+                            tile + (row0 + first) * 128 + ((chunk ^ (4 + first)) * 16)};
+    base += chunk * 16;
+    if (dim == D && __all_sync(0xffffffffu, at >= 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const char* from = base + __shfl_sync(0xffffffffu, at, 4 * j + first);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+                cp_async_whole(to[j & 1] + half * kBlock + j * 512, from + half * 128);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t from = __shfl_sync(0xffffffffu, at, 4 * j + first);
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+            const uint32_t bytes = from >= 0 && half * 64 + chunk * 8 < dim ? 16 : 0;
+            cp_async(to[j & 1] + half * kBlock + j * 512, base + (bytes ? from + half * 128 : 0), 16, bytes);
+        }
     }
 }
 
+// Half of the queries of both tiles.
+template <int D>
+__device__ __forceinline__ void load_queries(const AttendArgs& a, const Piece& p, uint32_t mem, int which)
+{
+    using S = Shared<D>;
+    for (int t = 0; t < (p.rows > kHalf ? 2 : 1); ++t)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int in_tile = which * 64 + g * 32, row = t * kHalf + in_tile + static_cast<int>(threadIdx.x & 31);
+            const int64_t at =
+                row < p.rows ? row_at(a, p.seq.first, p.head, p.tile * kRows + row, a.q_pitch, a.q_head) * 2 : -1;
+            load_rows<D>(a.q, at, a.dim, mem + S::kQ + t * S::kTile, in_tile);
+        }
+}
+
+// Keys and values in boxes of the pages.  A barrier of its own (kRaw) for values
+// that helper() looks through before it announces them.  Copies in flight where this
+// gives up have been for all of kPatience.
+template <int D>
+__device__ __forceinline__ void boxes(const AttendArgs& a, Run run, unsigned char* memory, const CUtensorMap* keys,
+                                      const CUtensorMap* values)
+{
+    using S = Shared<D>;
+    const uint32_t mem = smem_addr(memory);
+    const int lane = threadIdx.x & 31, rows = min(a.paged.page_size, kKeys), n = kKeys / rows;
+    const int mine = lane % n, half = lane / n;   // the page and the channels of the lane's box
+    const bool active = half < D / 64;
+    const uint32_t to = mem + S::kRing + half * kBlock + mine * rows * 128;
+    Place<D> place;
+    uint32_t count = 0;   // steps of all pieces
+    while (run.from < run.to) {
+        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const int first_limit = row_limit(a, p.seq, p.tile * kRows);
+        const int limit = min(row_limit(a, p.seq, p.tile * kRows + p.rows - 1), p.seq.length);
+        const int32_t* pages = a.paged.pages + p.b * a.paged.pages_pitch;
+        int position = p.step * kKeys + mine * rows;
+        int page = position < limit ? pages[page_of(a.paged, position)] : -1;
+        for (int step = p.step; step < p.end; ++step, ++count) {
+            const int base = step * kKeys, slot = position & (a.paged.page_size - 1);
+            const bool there = page >= 0 && page < a.paged.cache_pages;
+            const uint32_t exist = __ballot_sync(0xffffffffu, there);
+            const int box = there ? page : static_cast<int>(a.paged.cache_pages);   // beyond the tensor: zeros
+            uint4 seen = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (exist != ~0u || base + kKeys > limit) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = i * 32 + lane;
+                    w[i] = __ballot_sync(0xffffffffu, (exist >> (key / rows) & 1) && base + key < limit);
+                }
+                seen = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (lane == 0)   // the step that had this place is long over: its values' stage has been used again
+                *reinterpret_cast<uint4*>(memory + S::kMask + count % kMasks * 16) = seen;
+            position += kKeys;
+            page = position < limit ? pages[page_of(a.paged, position)] : -1;   // a step ahead
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, place.next()) {
+                if (place.turn && !wait_warp(mem + S::kEmpty + 8 * place.stage, place.turn - 1))
+                    return;
+                const bool look = kv == 1 && base + kKeys > first_limit;
+                const uint32_t bar = mem + 8 * place.stage + (look ? S::kRaw : S::kFull);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, S::kTile);
+                    if (!look)   // as the helper's two warps
+                        mbar_arrive(bar);
+                }
+                __syncwarp();
+                if (active)
+                    tma_load_4d(to + place.stage * S::kTile, kv ? values : keys, half * 64, slot, p.head, box, bar);
+            }
+        }
+        advance<kRows>(a, run, p);
+    }
+}
+
+// Queries; and values that not every row sees: those that no row sees become zeros,
+// for the rest see take_out.
+template <int DT, int D>
+__device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned char* memory)
+{
+    using S = Shared<D>;
+    const uint32_t mem = smem_addr(memory);
+    const int mine = threadIdx.x - (kLoadWarp + 1) * 32;
+    uint32_t piece = 0, resets = 0, tile = 0, raw = 0;   // raw: a bit to each stage, the phase to wait for
+    while (run.from < run.to) {
+        const Piece p = piece_of<kRows, kKeys>(a, run);
+        if (piece && !wait_warp(mem + S::kQEmpty, piece - 1))
+            return;
+        load_queries<D>(a, p, mem, mine / 32);
+        cp_async_commit();
+        cp_async_wait(0);
+        fence_proxy_async_smem();
+        mbar_arrive(mem + S::kQFull);
+        const int first_limit = row_limit(a, p.seq, p.tile * kRows);
+        const int limit = min(row_limit(a, p.seq, p.tile * kRows + p.rows - 1), p.seq.length);
+        bool fresh = true;
+        for (int step = max(p.step, first_limit / kKeys); step < p.end; ++step) {   // base + kKeys > first_limit
+            if (fresh && !forget<D>(memory, piece, resets++, mine))
+                return;
+            fresh = false;
+            const int stage = (tile + 2 * (step - p.step) + 1) % stages<D>(), base = step * kKeys;
+            if (!wait_warp(mem + S::kRaw + 8 * stage, raw >> stage))
+                return;
+            raw ^= 1u << stage;
+            unsigned char* values = memory + S::kRing + stage * S::kTile;
+            constexpr int kChunks = D / 8;
+            const int chunk = mine % kChunks;
+            for (int row = mine / kChunks; row < kKeys; row += kLoaders / kChunks)
+                if (base + row < limit)
+                    take_out<DT, D>(memory, values, row, chunk, base);
+                else
+                    *reinterpret_cast<uint4*>(values + chunk / 8 * kBlock + row * 128 + ((chunk & 7) ^ (row & 7)) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (mine % 32 == 0)
+                mbar_arrive(mem + S::kFull + 8 * stage);
+        }
+        tile += 2 * (p.end - p.step);
+        ++piece;
+        advance<kRows>(a, run, p);
+    }
+}
+
+// Everything by cp.async.
 template <int DT, int D>
 __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned char* memory)
 {
     using S = Shared<D>;
     const uint32_t mem = smem_addr(memory);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 3;
-    volatile int* done = reinterpret_cast<int*>(memory + S::kWords) + 1;
-    int* odd = reinterpret_cast<int*>(memory + S::kOdd);
-    uint32_t tile = 0, piece = 0, resets = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 1, mine = threadIdx.x % kLoaders;
+    uint32_t piece = 0, resets = 0, count = 0;   // count: steps of all pieces
+    Place<D> place;
     Landing pending[kLag];
     int waiting = 0;   // of `pending`
     const auto put = [&](const Landing& l) {
@@ -171,56 +348,46 @@ __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned ch
         const Piece p = piece_of<kRows, kKeys>(a, run);
         if (piece && !wait_warp(mem + S::kQEmpty, piece - 1))
             return;
-        for (int t = 0; t < (p.rows > kHalf ? 2 : 1); ++t) {
-            const int row = t * kHalf + warp * 32 + lane;
-            const int64_t at = row < p.rows
-                                   ? row_at(a, p.seq.first, p.head, p.tile * kRows + row, a.q_pitch, a.q_head) * 2
-                                   : -1;
-            load_rows<D>(a.q, at, a.dim, mem + S::kQ + t * S::kTile);
-        }
+        load_queries<D>(a, p, mem, warp);
         put(Landing{mem + S::kQFull, 0, 0, false});
         const int first_limit = row_limit(a, p.seq, p.tile * kRows);
         const int limit = min(row_limit(a, p.seq, p.tile * kRows + p.rows - 1), p.seq.length);
         const int32_t* pages = a.paged.pages + p.b * a.paged.pages_pitch;
-        int position = p.step * kKeys + warp * 32 + lane;
-        int page = position < limit ? pages[position / a.paged.page_size] : -1;
+        int position = p.step * kKeys + warp * 64 + lane;   // and 32 further on
+        int page[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            page[g] = position + 32 * g < limit ? pages[page_of(a.paged, position + 32 * g)] : -1;
         bool fresh = true;   // no value of the piece has been looked at
-        for (int step = p.step; step < p.end; ++step) {
-            const bool there = page >= 0 && page < a.paged.cache_pages;
-            const int slot = position % a.paged.page_size;
-            const int64_t at =
-                there ? (page * a.paged.page_pitch + slot * a.slot_pitch + p.head * a.head_pitch) * 2 : -1;
-            const uint32_t seen = __ballot_sync(0xffffffffu, there);
+        for (int step = p.step; step < p.end; ++step, ++count) {
+            int64_t at[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const bool there = page[g] >= 0 && page[g] < a.paged.cache_pages;
+                const int here = position + 32 * g, slot = here - page_of(a.paged, here) * a.paged.page_size;
+                at[g] = there ? (page[g] * a.paged.page_pitch + slot * a.slot_pitch + p.head * a.head_pitch) * 2 : -1;
+                const uint32_t seen = __ballot_sync(0xffffffffu, there);
+                if (lane == 0)   // the step that had this place is long over: its values' stage has been used again
+                    reinterpret_cast<uint32_t*>(memory + S::kMask)[count % kMasks * 4 + warp * 2 + g] = seen;
+                page[g] = here + kKeys < limit ? pages[page_of(a.paged, here + kKeys)] : -1;   // a step ahead
+            }
             position += kKeys;
-            page = position < limit ? pages[position / a.paged.page_size] : -1;   // a step ahead
             const int base = step * kKeys;
-            for (int kv = 0; kv < 2; ++kv, ++tile) {
-                const int stage = tile % stages<D>();
-                const uint32_t turn = tile / stages<D>();
-                if (turn && !wait_warp(mem + S::kEmpty + 8 * stage, turn - 1))
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, place.next()) {
+                if (place.turn && !wait_warp(mem + S::kEmpty + 8 * place.stage, place.turn - 1))
                     return;
-                if (kv == 0 && lane == 0)
-                    reinterpret_cast<uint32_t*>(memory + S::kMask)[step % kMasks * 4 + warp] = seen;
                 const bool check = kv == 1 && base + kKeys > first_limit;
                 if (check && fresh) {   // the last piece's have been used
                     fresh = false;
-                    if (piece) {
-                        const uint64_t since = globaltimer_ns();
-                        while (!__all_sync(0xffffffffu, *done >= static_cast<int>(8 * piece)))
-                            if (__any_sync(0xffffffffu, globaltimer_ns() - since > kPatience))
-                                return;
-                        __threadfence_block();
-                    }
-                    for (int i = threadIdx.x % kLoaders; i < 3 * D; i += kLoaders)
-                        odd[i] = 0x7fffffff;
-                    if (threadIdx.x % kLoaders == 0)
-                        reinterpret_cast<int*>(memory + S::kWords)[2] = 0;
-                    mbar_arrive(mem + S::kReset);
-                    if (!wait_warp(mem + S::kReset, resets++))
+                    if (!forget<D>(memory, piece, resets++, mine))
                         return;
                 }
-                load_rows<D>(kv ? a.v : a.k, at, a.dim, mem + S::kRing + stage * S::kTile);
-                put(Landing{mem + S::kFull + 8 * stage, S::kRing + stage * S::kTile, base, check});
+                const int stage = S::kRing + place.stage * S::kTile;
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    load_rows<D>(kv ? a.v : a.k, at[g], a.dim, mem + stage, warp * 64 + g * 32);
+                put(Landing{mem + S::kFull + 8 * place.stage, stage, base, check});
             }
         }
         flush();
@@ -238,54 +405,56 @@ __device__ __forceinline__ void issuer(const AttendArgs& a, Run run, unsigned ch
     const uint32_t mem = smem_addr(memory);
     const uint32_t scores = product(DT == TSX_BF16, 128, kKeys, false, a.negated);
     const uint32_t values = product(DT == TSX_BF16, 128, D, true, false);
-    uint32_t tile = 0, piece = 0, weights[2] = {0, 0};
-    const auto full = [&](uint32_t n) { return wait(mem + S::kFull + 8 * (n % stages<D>()), n / stages<D>()); };
-    const auto release = [&](uint32_t n) { mma_commit(mem + S::kEmpty + 8 * (n % stages<D>())); };
-    const auto score = [&](int t, uint32_t n) {
-        const uint32_t q = mem + S::kQ + t * S::kTile, k = mem + S::kRing + n % stages<D>() * S::kTile;
+    uint32_t piece = 0, weights[2] = {0, 0};
+    Place<D> place;
+    const auto full = [&](const Place<D>& at) { return wait_warp(mem + S::kFull + 8 * at.stage, at.turn); };
+    const auto release = [&](const Place<D>& at) { mma_commit(mem + S::kEmpty + 8 * at.stage); };
+    const auto score = [&](int t, const Place<D>& at) {
+        const uint32_t q = mem + S::kQ + t * S::kTile, k = mem + S::kRing + at.stage * S::kTile;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t at = i / 4 * kBlock + i % 4 * 32;
-            mma_smem(tmem + t * kHalf, operand(q + at, 16), operand(k + at, 16), scores, i > 0);
-        }
+        for (int i = 0; i < D / 64; ++i)
+            mma_smem64(tmem + t * kHalf, operand(q + i * kBlock, 16), operand(k + i * kBlock, 16), scores, i > 0);
         mma_commit(mem + S::kS + 8 * t);
     };
     while (run.from < run.to) {
         const Piece p = piece_of<kRows, kKeys>(a, run);
         const int tiles = p.rows > kHalf ? 2 : 1, steps = p.end - p.step;
-        if (!wait(mem + S::kQFull, piece) || !full(tile))
+        if (!wait_warp(mem + S::kQFull, piece) || !full(place))
             return;
         tcgen05_after();
         for (int t = 0; t < tiles; ++t)
-            score(t, tile);
-        release(tile);
+            score(t, place);
+        release(place);
         if (steps == 1)
             mma_commit(mem + S::kQEmpty);
-        for (int i = 0; i < steps; ++i, tile += 2) {
-            if (!full(tile + 1))
+        for (int i = 0; i < steps; ++i) {
+            place.next();
+            const Place<D> values_at = place;
+            if (!full(values_at))
                 return;
             const bool more = i + 1 < steps;
+            place.next();
             for (int t = 0; t < tiles; ++t) {
-                if (!wait(mem + S::kP + 8 * t, weights[t]++))
+                if (!wait_warp(mem + S::kP + 8 * t, weights[t]++))
                     return;
                 tcgen05_after();
-                const uint32_t v = mem + S::kRing + (tile + 1) % stages<D>() * S::kTile;
+                const uint32_t v = mem + S::kRing + values_at.stage * S::kTile;
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_tmem(tmem + kRows + t * kHalf, tmem + t * kHalf + k * 8, operand(v + k * 2048, kBlock), values,
-                             i > 0 || k > 0);
+                for (int k = 0; k < kKeys / 64; ++k)
+                    mma_tmem64(tmem + kRows + t * kHalf, tmem + t * kHalf + k * 32, operand(v + k * 8192, kBlock), values,
+                               i > 0 || k > 0);
                 if (t == tiles - 1)
-                    release(tile + 1);
+                    release(values_at);
                 if (!more) {
                     mma_commit(mem + S::kO + 8 * t);
                 } else {
-                    if (t == 0 && !full(tile + 2))
+                    if (t == 0 && !full(place))
                         return;
-                    score(t, tile + 2);
+                    score(t, place);
                 }
             }
             if (more) {
-                release(tile + 2);
+                release(place);
                 if (i + 2 == steps)
                     mma_commit(mem + S::kQEmpty);
             }
@@ -297,16 +466,42 @@ __device__ __forceinline__ void issuer(const AttendArgs& a, Run run, unsigned ch
 
 // ---------------------------------------------------------------- weights
 
-template <int DT>
-__device__ __forceinline__ void store_row(const AttendArgs& a, const Piece& p, int row, int first, const float* v, int n)
+// NaN is passed over, as by fmaxf.
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
 {
-    char* to = a.out + (row_at(a, p.seq.first, p.head, p.tile * kRows + row, a.out_pitch, a.out_head) + first) * 2;
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return m;
+}
+
+__device__ __forceinline__ float quad_max(float v)
+{
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// Scores of keys that a row does not see become -infinity.  s: 64 columns from key
+// `from` of the step on, laid over the threads as tmem_load32 does.
+__device__ __forceinline__ void hide(uint32_t* s, uint64_t there, int from, const int (&left)[2])
+{
+    const int q2 = threadIdx.x % 4 * 2;
 #pragma unroll
-    for (int c = 0; c < n; c += 8)
-        if (first + c < a.dim)
-            *reinterpret_cast<uint4*>(to + c * 2) = make_uint4(pack2<DT>(v[c], v[c + 1]), pack2<DT>(v[c + 2], v[c + 3]),
-                                                               pack2<DT>(v[c + 4], v[c + 5]),
-                                                               pack2<DT>(v[c + 6], v[c + 7]));
+    for (int r = 0; r < 2; ++r) {
+        const int n = left[r] - from;   // keys of these that the row may see
+        const uint64_t sees = (there & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1)) >> q2;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!(sees >> (8 * j) & 1))
+                s[4 * j + 2 * r] = 0xff800000u;
+            if (!(sees >> (8 * j) & 2))
+                s[4 * j + 2 * r + 1] = 0xff800000u;
+        }
+    }
 }
 
 template <int DT, int D>
@@ -314,146 +509,160 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
 {
     using S = Shared<D>;
     const uint32_t mem = smem_addr(memory);
-    const int t = threadIdx.x / kHalf, mine = threadIdx.x % kHalf, row = t * kHalf + mine;
-    const uint32_t lanes = static_cast<uint32_t>(mine / 32 * 32) << 16;
-    const uint32_t s_at = tmem + t * kHalf + lanes, o_at = tmem + kRows + t * kHalf + lanes;
+    // warps w and w + 4 of a tile reach the same 32 lanes: 16 of them each
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = warp / 8, q2 = lane % 4 * 2;
+    const int row0 = warp % 4 * 32 + warp / 4 % 2 * 16, row = row0 + lane / 4;   // and row + 8, of the tile
+    const uint32_t s_at = tmem + t * kHalf + (static_cast<uint32_t>(row0) << 16);
+    const uint32_t o_at = tmem + kRows + t * kHalf + (static_cast<uint32_t>(row0) << 16);
     const int* odd = reinterpret_cast<const int*>(memory + S::kOdd);
     int* words = reinterpret_cast<int*>(memory + S::kWords);
-    uint32_t scored = 0, ended = 0;
+    uint32_t scored = 0, ended = 0, count = 0;   // count: steps of all pieces
     bool ok = true;
     while (run.from < run.to) {
         const Piece p = piece_of<kRows, kKeys>(a, run);
-        const int all = row_limit(a, p.seq, p.tile * kRows + t * kHalf);   // keys that every row of the tile sees
-        const int limit = row < p.rows ? row_limit(a, p.seq, p.tile * kRows + row) : 0;
+        const int first = p.tile * kRows + t * kHalf;   // of the tile's rows
+        const int all = row_limit(a, p.seq, first);     // keys that every row of the tile sees
+        int limit[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            limit[r] = t * kHalf + row + 8 * r < p.rows ? row_limit(a, p.seq, first + row + 8 * r) : 0;
         const bool busy = p.rows > t * kHalf;
-        float top = -INFINITY, sum = 0.f;
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
         for (int step = p.step; busy && ok && step < p.end; ++step) {
             ok = wait_warp(mem + S::kS + 8 * t, scored);
             if (!ok)
                 break;
             ++scored;
             tcgen05_after();
-            uint32_t s[kKeys];
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 32)
-                tmem_load32(s_at + i, s + i);
-            tmem_wait_loads();
+            uint32_t s[kKeys / 2];
+            tmem_load32(s_at, s);
+            tmem_load32(s_at + 64, s + 32);
             const int base = step * kKeys;
-            const uint4 seen = *reinterpret_cast<const uint4*>(memory + S::kMask + step % kMasks * 16);
-            if (base + kKeys > all || (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu) {
-                const uint32_t words4[4] = {seen.x, seen.y, seen.z, seen.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int left = limit - base - 32 * w;
-                    const uint32_t sees = words4[w] & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!(sees >> i & 1))
-                            s[32 * w + i] = 0xff800000u;
-                }
+            const ulonglong2 there = *reinterpret_cast<const ulonglong2*>(memory + S::kMask + (count + (step - p.step)) % kMasks * 16);
+            tmem_wait32(s);
+            tmem_wait32(s + 32);
+            if (__any_sync(0xffffffffu, base + kKeys > all || (there.x & there.y) != ~0ull)) {
+                asm volatile("" ::: "memory");   // a branch in earnest: as selections they would be made in every step
+                const int left[2] = {limit[0] - base, limit[1] - base};
+                hide(s, there.x, 0, left);
+                hide(s + 32, there.y, 64, left);
             }
-            float most[4];
+            float now[2];
+            bool grows[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                most[i] = __uint_as_float(s[i]);
+            for (int r = 0; r < 2; ++r) {
+                float m[2] = {__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1])};
 #pragma unroll
-            for (int i = 4; i < kKeys; i += 8)
+                for (int j = 1; j < 15; j += 2)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (i + 4 < kKeys)
-                        most[j] = fmaxf(most[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j])));
-                    else
-                        most[j] = fmaxf(most[j], __uint_as_float(s[i + j]));
-            const float now = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * a.scale_log2;
-            const bool grows = now > top + kGrowth || (top == -INFINITY && now > top);
-            if (__any_sync(0xffffffffu, grows)) {
-                const float f = grows && top != -INFINITY ? exp2_fast(top - now) : 1.f;
-                top = grows ? now : top;
-                sum *= f;
-                if (step > p.step && __any_sync(0xffffffffu, f != 1.f)) {
+                    for (int e = 0; e < 2; ++e)
+                        m[e] = max3(m[e], s[4 * j + 2 * r + e], s[4 * j + 4 + 2 * r + e]);
+                now[r] = quad_max(max3(fmaxf(m[0], m[1]), s[60 + 2 * r], s[61 + 2 * r])) * a.scale_log2;
+                grows[r] = now[r] > top[r] + kGrowth || (top[r] == -INFINITY && now[r] > top[r]);
+            }
+            if (__any_sync(0xffffffffu, grows[0] || grows[1])) {
+                float f[2];
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {   // O is at rest: the scores came after its last product
+                for (int r = 0; r < 2; ++r) {
+                    f[r] = grows[r] && top[r] != -INFINITY ? exp2_fast(top[r] - now[r]) : 1.f;
+                    top[r] = grows[r] ? now[r] : top[r];
+                    sum[r] *= f[r];
+                }
+                if (step > p.step && __any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {   // O is at rest: the scores came after its last product
                         uint32_t o[16];
                         tmem_load16(o_at + c, o);
-                        tmem_wait_loads();
+                        tmem_wait16(o);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i / 2 % 2]);
                         tmem_store16(o_at + c, o);
                     }
                 }
             }
-            const float2 less = pair_of(top == -INFINITY ? 0.f : -top), by = pair_of(a.scale_log2);
+            const float2 by = pair_of(a.scale_log2);
+            const float2 less[2] = {pair_of(top[0] == -INFINITY ? 0.f : -top[0]),
+                                    pair_of(top[1] == -INFINITY ? 0.f : -top[1])};
             float2 total[2] = {pair_of(0.f), pair_of(0.f)};
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 64) {
-                uint32_t w[32];
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float2 v = make_float2(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
-                    v = __ffma2_rn(v, by, less);
+                for (int i = 0; i < 16; ++i) {
+                    float2 v = make_float2(__uint_as_float(s[32 * c + 2 * i]), __uint_as_float(s[32 * c + 2 * i + 1]));
+                    v = __ffma2_rn(v, by, less[i & 1]);
                     v.x = exp2_fast(v.x);
                     v.y = exp2_fast(v.y);
                     total[i & 1] = __fadd2_rn(total[i & 1], v);
                     w[i] = pack2<DT>(v.x, v.y);
                 }
-                tmem_store32(s_at + c / 2, w);
+                tmem_store_pairs(s_at + 32 * c, w);
             }
             tmem_wait_stores();
             tcgen05_before();
             mbar_arrive(mem + S::kP + 8 * t);
-            const float2 both = __fadd2_rn(total[0], total[1]);
-            sum += both.x + both.y;
+            sum[0] += total[0].x + total[0].y;
+            sum[1] += total[1].x + total[1].y;
         }
         if (busy) {
             ok = ok && wait_warp(mem + S::kO + 8 * t, ended++);
             tcgen05_after();
-            const bool whole = p.whole(), live = row < p.rows;
-            const int slot = part_slot(p);
+            const bool whole = p.whole();
             const bool strange = ok && p.end * kKeys > row_limit(a, p.seq, p.tile * kRows) && words[2];
-            const float f = !ok ? NAN : !whole ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            const int64_t slot = part_slot(p);
+            float f[2];
+            char* to[2];
+            bool live[2];
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                float v[32];
-                if (ok) {
-                    tmem_load32(o_at + c, o);
-                    tmem_wait_loads();
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = ok ? __uint_as_float(o[i]) : 0.f;
-                if (strange)
-                    for (int k = 0; k < 3; ++k)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (odd[k * D + c + i] < limit)
-                                v[i] += k == 0 ? NAN : k == 1 ? INFINITY : -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] *= f;
-                if (!live)
-                    continue;
-                if (whole) {
-                    store_row<DT>(a, p, row, c, v, 32);
-                } else {
-                    float4* to = reinterpret_cast<float4*>(a.parts + (static_cast<int64_t>(slot) * kRows + row) * D + c);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        to[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int r = 0; r < 2; ++r) {
+                const int mine = row + 8 * r;
+                live[r] = t * kHalf + mine < p.rows;
+                sum[r] = ok ? quad_sum(sum[r]) : NAN;
+                f[r] = !whole && ok ? 1.f : sum[r] > 0.f || sum[r] != sum[r] ? 1.f / sum[r] : 0.f;
+                to[r] = whole ? a.out + row_at(a, p.seq.first, p.head, first + mine, a.out_pitch, a.out_head) * 2
+                              : reinterpret_cast<char*>(a.parts + (slot * kRows + t * kHalf + mine) * D);
+                if (live[r] && q2 == 0) {
+                    if (whole)
+                        store_lse(a, p.seq.first, p.head, first + mine, top[r], sum[r]);
+                    else
+                        a.stats[slot * kRows + t * kHalf + mine] = make_float2(top[r], sum[r]);
                 }
             }
-            if (live && whole)
-                store_lse(a, p.seq.first, p.head, p.tile * kRows + row, top, ok ? sum : NAN);
-            if (live && !whole)
-                a.stats[slot * kRows + row] = make_float2(top, ok ? sum : NAN);
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[16];
+                if (ok) {
+                    tmem_load16(o_at + c, o);
+                    tmem_wait16(o);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {   // two channels of one row
+                    const int r = i & 1, ch = c + i / 2 * 8 + q2;
+                    float2 v = ok ? make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])) : pair_of(0.f);
+                    if (strange)
+                        for (int k = 0; k < 3; ++k) {
+                            const float add = k == 0 ? NAN : k == 1 ? INFINITY : -INFINITY;
+                            v.x += odd[k * D + ch] < limit[r] ? add : 0.f;
+                            v.y += odd[k * D + ch + 1] < limit[r] ? add : 0.f;
+                        }
+                    v = __fmul2_rn(v, pair_of(f[r]));
+                    if (!live[r])
+                        continue;
+                    if (!whole)
+                        *reinterpret_cast<float2*>(to[r] + ch * 4) = v;
+                    else if (ch < a.dim)
+                        *reinterpret_cast<uint32_t*>(to[r] + ch * 2) = pack2<DT>(v.x, v.y);
+                }
+            }
             tcgen05_before();
         }
         __syncwarp();
-        if (threadIdx.x % 32 == 0) {
+        if (lane == 0) {
             __threadfence_block();
             atomicAdd(words + 1, 1);
         }
+        count += p.end - p.step;
         const Tail now = tail_of<kRows>(run, p);
         if (now.follow)
             *tail = now;
@@ -461,8 +670,10 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
     }
 }
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_constant__ AttendArgs a)
+template <int DT, int D, bool BOXES>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tiles_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap keys,
+                        const __grid_constant__ CUtensorMap values)
 {
     extern __shared__ __align__(1024) unsigned char memory[];
     using S = Shared<D>;
@@ -471,14 +682,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     int* words = reinterpret_cast<int*>(memory + S::kWords);
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages<D>(); ++i) {
-            mbar_init(mem + S::kFull + 8 * i, kLoaders);
+            mbar_init(mem + S::kFull + 8 * i, BOXES ? 2 : kLoaders);
             mbar_init(mem + S::kEmpty + 8 * i, 1);
+            mbar_init(mem + S::kRaw + 8 * i, 1);
         }
         mbar_init(mem + S::kQFull, kLoaders);
         mbar_init(mem + S::kQEmpty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(mem + S::kS + 8 * t, 1);
-            mbar_init(mem + S::kP + 8 * t, kHalf);
+            mbar_init(mem + S::kP + 8 * t, kWeighers / 2);
             mbar_init(mem + S::kO + 8 * t, 1);
         }
         mbar_init(mem + S::kReset, kLoaders);
@@ -487,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     let_next_start();
-    if (warp == 12)
+    if (warp == kIssueWarp)
         tmem_alloc(mem + S::kWords, 512);
     tcgen05_before();
     // also the barrier after the initialisation
@@ -495,19 +707,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     __syncthreads();
     tcgen05_after();
     const uint32_t tmem = static_cast<uint32_t>(words[0]);
-    // 128 registers a thread at the launch: 256 x 200 and 256 x 56 are as many
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // 96 registers a thread at the launch: 512 x 104 and 128 x 64 are as many
+    if (warp < kLoadWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         Tail tail{};
         weigher<DT, D>(a, run, memory, tmem, &tail);
         if (threadIdx.x == 0)
             a.tails[blockIdx.x] = tail;
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp < 12) {
-            loader<DT, D>(a, run, memory);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (BOXES && warp == kLoadWarp) {
+            boxes<D>(a, run, memory, &keys, &values);
+        } else if (warp < kLoadWarp + (BOXES ? 3 : 2)) {
+            if constexpr (BOXES)
+                helper<DT, D>(a, run, memory);
+            else
+                loader<DT, D>(a, run, memory);
             cp_async_wait(0);
-        } else if (threadIdx.x == 12 * 32) {
+        } else if (warp == kIssueWarp) {
             issuer<DT, D>(a, run, memory, tmem);
             mma_commit(mem + S::kDrain);   // where it gave up, products may be under way
             (void)wait(mem + S::kDrain, 0);
@@ -517,15 +734,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     tcgen05_before();
     __syncthreads();
     tcgen05_after();
-    if (warp == 12)
+    if (warp == kIssueWarp)
         tmem_free(tmem, 512);
 }
 
 template <int DT, int D>
-cudaError_t launch_many(const AttendArgs& a, cudaStream_t st)
+cudaError_t launch_many(const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st)
 {
+    const dim3 grid(unsigned(a.ctas));
     const cudaError_t e =
-        launch_grid<attend_tiles_kernel<DT, D>>(dim3(unsigned(a.ctas)), kThreads, Shared<D>::kBytes, 1, false, st, a);
+        maps ? launch_grid<attend_tiles_kernel<DT, D, true>>(grid, kThreads, Shared<D>::kBytes, 1, false, st, a, maps[0],
+                                                             maps[1])
+             : launch_grid<attend_tiles_kernel<DT, D, false>>(grid, kThreads, Shared<D>::kBytes, 1, false, st, a,
+                                                              CUtensorMap{}, CUtensorMap{});
     if (e != cudaSuccess)
         return e;
     return launch_grid<attend_join_kernel<DT, D, kRows>>(dim3(unsigned(a.ctas), kRows / 4), 128, 0, 1, true, st, a);
@@ -535,11 +756,11 @@ cudaError_t launch_many(const AttendArgs& a, cudaStream_t st)
 
 int attend_many_rows() { return kRows; }
 
-cudaError_t launch_attend_many(int dtype, const AttendArgs& a, cudaStream_t st)
+cudaError_t launch_attend_many(int dtype, const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st)
 {
     if (dtype == TSX_BF16)
-        return a.dim <= 64 ? launch_many<TSX_BF16, 64>(a, st) : launch_many<TSX_BF16, 128>(a, st);
-    return a.dim <= 64 ? launch_many<TSX_F16, 64>(a, st) : launch_many<TSX_F16, 128>(a, st);
+        return a.dim <= 64 ? launch_many<TSX_BF16, 64>(a, maps, st) : launch_many<TSX_BF16, 128>(a, maps, st);
+    return a.dim <= 64 ? launch_many<TSX_F16, 64>(a, maps, st) : launch_many<TSX_F16, 128>(a, maps, st);
 }
 
 }  // namespace tsx

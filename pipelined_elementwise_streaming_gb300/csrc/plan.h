@@ -118,5 +118,9 @@ void set_last_error(const char* msg);
 
 // Encode the tensor map of base pointer `ptr` for geometry g (capi.cpp).
 int encode_tensor_map(const Geometry& g, const void* ptr, CUtensorMap* map);
+// The same of a tensor of rank 4 with the 128-byte swizzle; strides in bytes,
+// of dimensions 1 to 3.
+int encode_pages_map(int dtype, const void* ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                     const uint32_t (&box)[4], CUtensorMap* map);
 
 }  // namespace tsx

@@ -17,6 +17,12 @@
 namespace tsx {
 namespace dev {
 
+// Which of a sequence's pages holds a position.
+__device__ __forceinline__ int page_of(const PagedArgs& p, int position)
+{
+    return p.page_shift >= 0 ? position >> p.page_shift : position / p.page_size;
+}
+
 // A sequence with new tokens.
 struct Seq {
     int first;     // its first row of tokens
