@@ -7,15 +7,15 @@
 // tensor cores nor the exponentials wait for the other: 2 x 128^3 multiply-adds a
 // step and tile are 1024 cycles at 4096 a cycle, 128^2 exponentials 512 at 32.
 //
-//   warps 0-7, 8-15  a tile each, 16 rows to a warp, four threads to a row: scores,
-//                    maxima, weights, sums, results
-//   warp 16          brings keys and values, by TMA: boxes of the pages, one to a
+//   warps 0-3, 4-7   a tile each, a thread to a row: scores, maxima, weights, sums,
+//                    results (nothing between threads)
+//   warp 8           brings keys and values, by TMA: boxes of the pages, one to a
 //                    lane; and tells which of the step's keys exist
-//   warps 17, 18     bring queries, and look through values that not every row sees
-//   warp 19          issues the products
+//   warps 9, 10      bring queries, and look through values that not every row sees
+//   warp 11          issues the products
 //
 // Pages that are no power of two of at least 8 slots do not fit the swizzle's eight
-// rows: then warps 16 and 17 bring everything by cp.async.
+// rows: then warps 8 and 9 bring everything by cp.async.
 //
 // The running maximum is not followed closely: O and the sum are scaled only when
 // a row's maximum has grown by more than 2^8 over the one in use, which is rare
@@ -32,7 +32,7 @@ namespace {
 using namespace dev;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128;
-constexpr int kWeighers = 512, kLoaders = 64, kThreads = 640;
+constexpr int kWeighers = 256, kLoaders = 64, kThreads = 384;
 constexpr int64_t kLeast = 2;        // steps to a CTA at least
 constexpr int kMasks = 8;            // steps whose keys are remembered
 constexpr int kBlock = kKeys * 128;  // bytes of a block: 128 rows of 64 channels
@@ -474,46 +474,14 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
     return m;
 }
 
-__device__ __forceinline__ float quad_max(float v)
-{
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v)
-{
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
-}
-
-// Scores of keys that a row does not see become -infinity.  s: 64 columns from key
-// `from` of the step on, laid over the threads as tmem_load32 does.
-__device__ __forceinline__ void hide(uint32_t* s, uint64_t there, int from, const int (&left)[2])
-{
-    const int q2 = threadIdx.x % 4 * 2;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int n = left[r] - from;   // keys of these that the row may see
-        const uint64_t sees = (there & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1)) >> q2;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!(sees >> (8 * j) & 1))
-                s[4 * j + 2 * r] = 0xff800000u;
-            if (!(sees >> (8 * j) & 2))
-                s[4 * j + 2 * r + 1] = 0xff800000u;
-        }
-    }
-}
-
 template <int DT, int D>
 __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned char* memory, uint32_t tmem, Tail* tail)
 {
     using S = Shared<D>;
     const uint32_t mem = smem_addr(memory);
-    // warps w and w + 4 of a tile reach the same 32 lanes: 16 of them each
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = warp / 8, q2 = lane % 4 * 2;
-    const int row0 = warp % 4 * 32 + warp / 4 % 2 * 16, row = row0 + lane / 4;   // and row + 8, of the tile
-    const uint32_t s_at = tmem + t * kHalf + (static_cast<uint32_t>(row0) << 16);
-    const uint32_t o_at = tmem + kRows + t * kHalf + (static_cast<uint32_t>(row0) << 16);
+    const int t = threadIdx.x / kHalf, row = threadIdx.x % kHalf;   // of the tile
+    const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
+    const uint32_t s_at = tmem + t * kHalf + lanes, o_at = tmem + kRows + t * kHalf + lanes;
     const int* odd = reinterpret_cast<const int*>(memory + S::kOdd);
     int* words = reinterpret_cast<int*>(memory + S::kWords);
     uint32_t scored = 0, ended = 0, count = 0;   // count: steps of all pieces
@@ -522,88 +490,89 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
         const Piece p = piece_of<kRows, kKeys>(a, run);
         const int first = p.tile * kRows + t * kHalf;   // of the tile's rows
         const int all = row_limit(a, p.seq, first);     // keys that every row of the tile sees
-        int limit[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            limit[r] = t * kHalf + row + 8 * r < p.rows ? row_limit(a, p.seq, first + row + 8 * r) : 0;
-        const bool busy = p.rows > t * kHalf;
-        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        const bool live = t * kHalf + row < p.rows, busy = p.rows > t * kHalf;
+        const int limit = live ? row_limit(a, p.seq, first + row) : 0;
+        float top = -INFINITY, sum = 0.f;
         for (int step = p.step; busy && ok && step < p.end; ++step) {
             ok = wait_warp(mem + S::kS + 8 * t, scored);
             if (!ok)
                 break;
             ++scored;
             tcgen05_after();
-            uint32_t s[kKeys / 2];
-            tmem_load32(s_at, s);
-            tmem_load32(s_at + 64, s + 32);
+            uint32_t s[kKeys];
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32)
+                tmem_load32(s_at + c, s + c);
             const int base = step * kKeys;
-            const ulonglong2 there = *reinterpret_cast<const ulonglong2*>(memory + S::kMask + (count + (step - p.step)) % kMasks * 16);
-            tmem_wait32(s);
-            tmem_wait32(s + 32);
-            if (__any_sync(0xffffffffu, base + kKeys > all || (there.x & there.y) != ~0ull)) {
+            const uint4 there = *reinterpret_cast<const uint4*>(memory + S::kMask + (count + (step - p.step)) % kMasks * 16);
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32)
+                tmem_wait32(s + c);
+            if (__any_sync(0xffffffffu, base + kKeys > all || (there.x & there.y & there.z & there.w) != ~0u)) {
                 asm volatile("" ::: "memory");   // a branch in earnest: as selections they would be made in every step
-                const int left[2] = {limit[0] - base, limit[1] - base};
-                hide(s, there.x, 0, left);
-                hide(s + 32, there.y, 64, left);
-            }
-            float now[2];
-            bool grows[2];
+                const uint32_t w[4] = {there.x, there.y, there.z, there.w};
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float m[2] = {__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1])};
+                for (int c = 0; c < 4; ++c) {
+                    const int left = limit - base - 32 * c;   // keys of these that the row may see
+                    const uint32_t sees = w[c] & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1);
 #pragma unroll
-                for (int j = 1; j < 15; j += 2)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        m[e] = max3(m[e], s[4 * j + 2 * r + e], s[4 * j + 4 + 2 * r + e]);
-                now[r] = quad_max(max3(fmaxf(m[0], m[1]), s[60 + 2 * r], s[61 + 2 * r])) * a.scale_log2;
-                grows[r] = now[r] > top[r] + kGrowth || (top[r] == -INFINITY && now[r] > top[r]);
-            }
-            if (__any_sync(0xffffffffu, grows[0] || grows[1])) {
-                float f[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    f[r] = grows[r] && top[r] != -INFINITY ? exp2_fast(top[r] - now[r]) : 1.f;
-                    top[r] = grows[r] ? now[r] : top[r];
-                    sum[r] *= f[r];
+                    for (int i = 0; i < 32; ++i)
+                        if (!(sees >> i & 1))
+                            s[32 * c + i] = 0xff800000u;
                 }
-                if (step > p.step && __any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+            }
+            float m[4];
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {   // O is at rest: the scores came after its last product
+            for (int j = 0; j < 4; ++j)
+                m[j] = __uint_as_float(s[j]);
+#pragma unroll
+            for (int i = 4; i + 7 < kKeys; i += 8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    m[j] = max3(m[j], s[i + j], s[i + 4 + j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                m[j] = fmaxf(m[j], __uint_as_float(s[kKeys - 4 + j]));
+            const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale_log2;
+            const bool grows = now > top + kGrowth || (top == -INFINITY && now > top);
+            if (__any_sync(0xffffffffu, grows)) {
+                const float f = grows && top != -INFINITY ? exp2_fast(top - now) : 1.f;
+                top = grows ? now : top;
+                sum *= f;
+                if (step > p.step && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {   // O is at rest: the scores came after its last product
                         uint32_t o[16];
                         tmem_load16(o_at + c, o);
                         tmem_wait16(o);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i / 2 % 2]);
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                         tmem_store16(o_at + c, o);
                     }
                 }
             }
-            const float2 by = pair_of(a.scale_log2);
-            const float2 less[2] = {pair_of(top[0] == -INFINITY ? 0.f : -top[0]),
-                                    pair_of(top[1] == -INFINITY ? 0.f : -top[1])};
+            const float2 by = pair_of(a.scale_log2), less = pair_of(top == -INFINITY ? 0.f : -top);
             float2 total[2] = {pair_of(0.f), pair_of(0.f)};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t w[16];
+                uint32_t w[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 v = make_float2(__uint_as_float(s[32 * c + 2 * i]), __uint_as_float(s[32 * c + 2 * i + 1]));
-                    v = __ffma2_rn(v, by, less[i & 1]);
+                for (int i = 0; i < 32; ++i) {
+                    float2 v = make_float2(__uint_as_float(s[64 * c + 2 * i]), __uint_as_float(s[64 * c + 2 * i + 1]));
+                    v = __ffma2_rn(v, by, less);
                     v.x = exp2_fast(v.x);
                     v.y = exp2_fast(v.y);
                     total[i & 1] = __fadd2_rn(total[i & 1], v);
                     w[i] = pack2<DT>(v.x, v.y);
                 }
-                tmem_store_pairs(s_at + 32 * c, w);
+                tmem_store32(s_at + 32 * c, w);
             }
             tmem_wait_stores();
             tcgen05_before();
             mbar_arrive(mem + S::kP + 8 * t);
-            sum[0] += total[0].x + total[0].y;
-            sum[1] += total[1].x + total[1].y;
+            const float2 both = __fadd2_rn(total[0], total[1]);
+            sum += both.x + both.y;
         }
         if (busy) {
             ok = ok && wait_warp(mem + S::kO + 8 * t, ended++);
@@ -611,54 +580,48 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
             const bool whole = p.whole();
             const bool strange = ok && p.end * kKeys > row_limit(a, p.seq, p.tile * kRows) && words[2];
             const int64_t slot = part_slot(p);
-            float f[2];
-            char* to[2];
-            bool live[2];
+            sum = ok ? sum : NAN;
+            const float f = !whole && ok ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            char* to = whole ? a.out + row_at(a, p.seq.first, p.head, first + row, a.out_pitch, a.out_head) * 2
+                             : reinterpret_cast<char*>(a.parts + (slot * kRows + t * kHalf + row) * D);
+            if (live && whole)
+                store_lse(a, p.seq.first, p.head, first + row, top, sum);
+            if (live && !whole)
+                a.stats[slot * kRows + t * kHalf + row] = make_float2(top, sum);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int mine = row + 8 * r;
-                live[r] = t * kHalf + mine < p.rows;
-                sum[r] = ok ? quad_sum(sum[r]) : NAN;
-                f[r] = !whole && ok ? 1.f : sum[r] > 0.f || sum[r] != sum[r] ? 1.f / sum[r] : 0.f;
-                to[r] = whole ? a.out + row_at(a, p.seq.first, p.head, first + mine, a.out_pitch, a.out_head) * 2
-                              : reinterpret_cast<char*>(a.parts + (slot * kRows + t * kHalf + mine) * D);
-                if (live[r] && q2 == 0) {
-                    if (whole)
-                        store_lse(a, p.seq.first, p.head, first + mine, top[r], sum[r]);
-                    else
-                        a.stats[slot * kRows + t * kHalf + mine] = make_float2(top[r], sum[r]);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
+                float v[16];
                 if (ok) {
                     tmem_load16(o_at + c, o);
                     tmem_wait16(o);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {   // two channels of one row
-                    const int r = i & 1, ch = c + i / 2 * 8 + q2;
-                    float2 v = ok ? make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])) : pair_of(0.f);
+                for (int i = 0; i < 16; ++i) {
+                    v[i] = ok ? __uint_as_float(o[i]) : 0.f;
                     if (strange)
-                        for (int k = 0; k < 3; ++k) {
-                            const float add = k == 0 ? NAN : k == 1 ? INFINITY : -INFINITY;
-                            v.x += odd[k * D + ch] < limit[r] ? add : 0.f;
-                            v.y += odd[k * D + ch + 1] < limit[r] ? add : 0.f;
-                        }
-                    v = __fmul2_rn(v, pair_of(f[r]));
-                    if (!live[r])
-                        continue;
-                    if (!whole)
-                        *reinterpret_cast<float2*>(to[r] + ch * 4) = v;
-                    else if (ch < a.dim)
-                        *reinterpret_cast<uint32_t*>(to[r] + ch * 2) = pack2<DT>(v.x, v.y);
+                        for (int k = 0; k < 3; ++k)
+                            v[i] += odd[k * D + c + i] < limit ? (k == 0 ? NAN : k == 1 ? INFINITY : -INFINITY) : 0.f;
+                    v[i] *= f;
                 }
+                if (!live)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 16; i += 8)
+                    if (!whole) {
+                        store16(to + (c + i) * 4, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+                        store16(to + (c + i + 4) * 4, __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
+                                __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
+                    } else if (c + i < a.dim) {
+                        store16(to + (c + i) * 2, pack2<DT>(v[i], v[i + 1]), pack2<DT>(v[i + 2], v[i + 3]),
+                                pack2<DT>(v[i + 4], v[i + 5]), pack2<DT>(v[i + 6], v[i + 7]));
+                    }
             }
             tcgen05_before();
         }
         __syncwarp();
-        if (lane == 0) {
+        if (threadIdx.x % 32 == 0) {
             __threadfence_block();
             atomicAdd(words + 1, 1);
         }
@@ -707,15 +670,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tcgen05_after();
     const uint32_t tmem = static_cast<uint32_t>(words[0]);
-    // 96 registers a thread at the launch: 512 x 104 and 128 x 64 are as many
+    // 168 registers a thread at the launch: 256 x 208 and 128 x 88 are as many
     if (warp < kLoadWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         Tail tail{};
         weigher<DT, D>(a, run, memory, tmem, &tail);
         if (threadIdx.x == 0)
             a.tails[blockIdx.x] = tail;
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (BOXES && warp == kLoadWarp) {
             boxes<D>(a, run, memory, &keys, &values);
         } else if (warp < kLoadWarp + (BOXES ? 3 : 2)) {
