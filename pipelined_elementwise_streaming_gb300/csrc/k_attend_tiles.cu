@@ -68,6 +68,17 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase)
     return __all_sync(0xffffffffu, wait(bar, phase));
 }
 
+// w's two values times 0, and sum.
+template <int DT>
+__device__ __forceinline__ uint32_t times_zero(uint32_t w, uint32_t sum)
+{
+    if constexpr (DT == TSX_BF16)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(w) : "r"(w), "r"(0), "r"(sum));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(w) : "r"(w), "r"(0), "r"(sum));
+    return w;
+}
+
 // ------------------------------------------------------------------ loads
 
 // A place in the ring of stages.
@@ -98,14 +109,11 @@ struct Landing {
 // is kept for each channel; the rows from that key on get it added at the end.
 // tile: the values' tile; base: the position of its first key.
 template <int DT, int D>
-__device__ __forceinline__ void take_out(unsigned char* memory, unsigned char* tile, int row, int chunk, int base)
+__device__ __noinline__ void take_out(unsigned char* memory, unsigned char* tile, int row, int chunk, int base)
 {
     int* odd = reinterpret_cast<int*>(memory + Shared<D>::kOdd);
-    uint4* place = reinterpret_cast<uint4*>(tile + chunk / 8 * kBlock + row * 128 + ((chunk & 7) ^ (row & 7)) * 16);
-    const uint4 v = *place;
-    if (!(not_finite<DT>(v.x) || not_finite<DT>(v.y) || not_finite<DT>(v.z) || not_finite<DT>(v.w)))
-        return;
-    uint16_t* at = reinterpret_cast<uint16_t*>(place);
+    uint16_t* at =
+        reinterpret_cast<uint16_t*>(tile + chunk / 8 * kBlock + row * 128 + ((chunk & 7) ^ (row & 7)) * 16);
     for (int e = 0; e < 8; ++e) {
         const uint32_t w = at[e];
         if (!not_finite<DT>(w))
@@ -113,8 +121,37 @@ __device__ __forceinline__ void take_out(unsigned char* memory, unsigned char* t
         const bool nan = w & (DT == TSX_BF16 ? 0x7fu : 0x3ffu);
         atomicMin(odd + (nan ? 0 : w >> 15 ? 2 : 1) * D + chunk * 8 + e, base + row);
         at[e] = 0;
+        reinterpret_cast<int*>(memory + Shared<D>::kWords)[2] = 1;
     }
-    reinterpret_cast<int*>(memory + Shared<D>::kWords)[2] = 1;
+}
+
+// Chunk i of a thread's chunks of a tile is that of `row(i)` and `chunk(i)`; `keys`
+// of the tile's rows are keys, the others become zeros.  0 times a value is 0 or NaN,
+// which a sum keeps: eight values are looked at in four instructions.
+template <int DT, int D, int N, class Row, class Chunk>
+__device__ __forceinline__ void look_through(unsigned char* memory, unsigned char* tile, int base, int keys, Row row,
+                                             Chunk chunk)
+{
+    const auto place = [&](int i) {
+        return reinterpret_cast<uint4*>(tile + chunk(i) / 8 * kBlock + row(i) * 128 + ((chunk(i) & 7) ^ (row(i) & 7)) * 16);
+    };
+    uint32_t sum = 0;
+    for (int i0 = 0; i0 < N; i0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (row(i0 + i) < keys)
+                v[i] = *place(i0 + i);
+            else
+                *place(i0 + i) = v[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum = times_zero<DT>(v[i].w, times_zero<DT>(v[i].z, times_zero<DT>(v[i].y, times_zero<DT>(v[i].x, sum))));
+    }
+    if (sum & 0x7fff7fffu)   // not 0 or -0
+        for (int i = 0; i < N; ++i)
+            if (row(i) < keys)
+                take_out<DT, D>(memory, tile, row(i), chunk(i), base);
 }
 
 // Before the first such values of a piece: nothing has been taken out.  False if
@@ -144,9 +181,10 @@ template <int DT, int D>
 __device__ __forceinline__ void land(unsigned char* memory, const Landing& l)
 {
     if (l.check) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 1;
-        for (int i = 0; i < D / 4; ++i)   // the chunks that this thread has copied (load_rows)
-            take_out<DT, D>(memory, memory + l.stage, warp * 64 + i % 16 * 4 + lane / 8, i / 16 * 8 + lane % 8, l.base);
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 1;   // the chunks that this thread has copied
+        look_through<DT, D, D / 4>(
+            memory, memory + l.stage, l.base, kKeys, [=](int i) { return warp * 64 + i % 16 * 4 + lane / 8; },
+            [=](int i) { return i / 16 * 8 + lane % 8; });
     }
     fence_proxy_async_smem();
     mbar_arrive(l.bar);
@@ -290,13 +328,9 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
             raw ^= 1u << stage;
             unsigned char* values = memory + S::kRing + stage * S::kTile;
             constexpr int kChunks = D / 8;
-            const int chunk = mine % kChunks;
-            for (int row = mine / kChunks; row < kKeys; row += kLoaders / kChunks)
-                if (base + row < limit)
-                    take_out<DT, D>(memory, values, row, chunk, base);
-                else
-                    *reinterpret_cast<uint4*>(values + chunk / 8 * kBlock + row * 128 + ((chunk & 7) ^ (row & 7)) * 16) =
-                        make_uint4(0, 0, 0, 0);
+            look_through<DT, D, kKeys * kChunks / kLoaders>(
+                memory, values, base, limit - base, [=](int i) { return i * (kLoaders / kChunks) + mine / kChunks; },
+                [=](int) { return mine % kChunks; });
             fence_proxy_async_smem();
             __syncwarp();
             if (mine % 32 == 0)

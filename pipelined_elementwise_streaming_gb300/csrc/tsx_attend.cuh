@@ -49,17 +49,23 @@ __device__ __forceinline__ int row_limit(const AttendArgs& a, const Seq& s, int 
     return max(s.prior + row / a.group + 1, 0);
 }
 
+// a / by; in 32 bits, at a fifth of the instructions, where that is enough.
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t by)
+{
+    return (a | by) >> 32 ? a / by : static_cast<uint32_t>(a) / static_cast<uint32_t>(by);
+}
+
 // Sum of floor((step i + from) / by) over 0 <= i < n.
-__device__ inline uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
+__device__ __forceinline__ uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
 {
     uint64_t sum = 0;
     while (n) {
-        sum += n * (n - 1) / 2 * (step / by) + n * (from / by);
-        step %= by;
-        from %= by;
-        const uint64_t top = step * n + from;
-        n = top / by;   // as many i of the mirrored sum
-        from = top % by;
+        const uint64_t p = quotient(step, by), q = quotient(from, by);
+        sum += n * (n - 1) / 2 * p + n * q;
+        step -= p * by;
+        const uint64_t top = step * n + (from - q * by);
+        n = quotient(top, by);   // as many i of the mirrored sum
+        from = top - n * by;
         const uint64_t t = by;
         by = step;
         step = t;
@@ -145,7 +151,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
             before += all;
             if (pass == 0 && base + THREADS >= a.paged.seqs) {
                 total = before;
-                r.per = max((total + gridDim.x - 1) / gridDim.x, least);
+                r.per = max(static_cast<int64_t>(quotient(total + gridDim.x - 1, gridDim.x)), least);
                 r.from = min(static_cast<int64_t>(blockIdx.x) * r.per, total);
                 r.to = min(r.from + r.per, total);
             }
@@ -165,16 +171,16 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
     r.b = static_cast<int>(sums[kWarps]);
     int64_t rest = sums[kWarps + 1];
     const int64_t head = sums[kWarps + 2];
-    r.head = static_cast<int>(rest / head);
+    r.head = static_cast<int>(quotient(rest, head));
     rest -= r.head * head;
     const Seq s = seq_of(a, r.b);
-    int lo = 0, hi = tiles_of<M>(a, s);   // the tile: steps_before(lo) <= rest
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (steps_before<M, TK>(a, s, mid) <= rest)
-            lo = mid;
-        else
-            hi = mid;
+    int lo = 0, hi = tiles_of<M>(a, s);   // the tile: steps_before(lo) <= rest < steps_before(hi)
+    while (hi - lo > 1) {   // 32 places looked at at once
+        const int apart = (hi - lo + 32) / 33;
+        const int64_t at = lo + static_cast<int64_t>(lane + 1) * apart;
+        const bool under = at < hi && steps_before<M, TK>(a, s, static_cast<int>(at)) <= rest;
+        lo += __popc(__ballot_sync(0xffffffffu, under)) * apart;
+        hi = min(hi, lo + apart);
     }
     r.tile = lo;
     r.step = static_cast<int>(rest - (lo ? steps_before<M, TK>(a, s, lo) : 0));
@@ -235,7 +241,7 @@ __device__ __forceinline__ Tail tail_of(const Run& r, const Piece& p)
 {
     Tail t{};
     if (p.step == 0 && p.end < p.steps) {
-        t.follow = static_cast<int>((r.from + p.steps - 1) / r.per) - static_cast<int>(blockIdx.x);
+        t.follow = static_cast<int>(quotient(r.from + p.steps - 1, r.per)) - static_cast<int>(blockIdx.x);
         t.token = p.seq.first;
         t.row0 = p.tile * M;
         t.rows = p.rows;
@@ -291,45 +297,108 @@ __device__ __forceinline__ bool not_finite(uint32_t w)
 }  // namespace dev
 
 // Joins the parts of the tile that CTA blockIdx.x has begun and not ended, four
-// rows to each CTA.
+// rows to each CTA: a warp to a row where they are few, else the four warps share
+// the parts of one row after the other.  Their statistics are read a lane to a part,
+// so that the sums of values, which do not wait for one another, are all that is
+// read in order.
+constexpr int kFewParts = 8;
+
 template <int DT, int D, int M>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a)
 {
     using namespace dev;
+    constexpr int kEach = D / 32;   // channels to a lane
+    __shared__ float shares[4][D];
+    __shared__ float2 tops[4];
     wait_for_last();
     const Tail t = a.tails[blockIdx.x];
-    const int row = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (!t.follow || row >= t.rows)
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row0 = blockIdx.y * 4;
+    if (!t.follow || row0 >= t.rows)
         return;
-    constexpr int kEach = D / 32;   // channels to a thread
+    const bool few = t.follow < kFewParts;
     const int first = 2 * blockIdx.x + 1;   // then the first slots of the CTAs that follow
-    float m = -INFINITY;
-    for (int i = 0; i <= t.follow; ++i)
-        m = fmaxf(m, a.stats[(i ? first - 1 + 2 * i : first) * M + row].x);
-    float l = 0.f, v[kEach] = {};
-    for (int i = 0; i <= t.follow; ++i) {
-        const int64_t slot = i ? first - 1 + 2 * i : first;
-        const float2 s = a.stats[slot * M + row];
-        if (s.x == -INFINITY && s.y == s.y)
-            continue;
-        const float f = s.x == -INFINITY ? s.y : exp2_fast(s.x - m);
-        l += s.y * f;
-        const float* from = a.parts + (slot * M + row) * D + lane * kEach;
+    for (int row = few ? row0 + warp : row0; row < min(row0 + 4, t.rows); row += few ? 4 : 1) {
+        const int from = few ? 0 : warp, step = few ? 1 : 4, parts = t.follow + 1;
+        // running maximum and sums over 32 of the warp's parts at a time
+        float m = -INFINITY, l = 0.f, v[kEach] = {};
+        for (int i0 = from; i0 < parts; i0 += 32 * step) {
+            const int mine = i0 + lane * step;
+            const int64_t slot = mine ? first - 1 + 2 * static_cast<int64_t>(mine) : first;
+            float2 s = make_float2(-INFINITY, 0.f);
+            if (mine < parts)
+                s = a.stats[slot * M + row];
+            float most = s.x;
 #pragma unroll
-        for (int e = 0; e < kEach; e += 2) {
-            const float2 o = *reinterpret_cast<const float2*>(from + e);
-            v[e] += o.x * f;
-            v[e + 1] += o.y * f;
+            for (int k = 16; k > 0; k /= 2)
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+            const float now = fmaxf(m, most);
+            const float old = m == -INFINITY ? 1.f : exp2_fast(m - now);
+            // nothing seen: no weight; a sum that is NaN stays it
+            float f = s.x == -INFINITY ? (s.y != s.y ? s.y : 0.f) : exp2_fast(s.x - now);
+            float add = s.x == -INFINITY && s.y == s.y ? 0.f : s.y * f;
+#pragma unroll
+            for (int k = 16; k > 0; k /= 2)
+                add += __shfl_xor_sync(0xffffffffu, add, k);
+            l = l * old + add;
+            m = now;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                v[e] *= old;
+            const int n = min(32, (parts - i0 + step - 1) / step);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const int part = i0 + k * step;
+                const int64_t at = part ? first - 1 + 2 * static_cast<int64_t>(part) : first;
+                const float* p = a.parts + (at * M + row) * D + lane * kEach;
+                const float g = __shfl_sync(0xffffffffu, f, k);
+                float2 o[kEach / 2];
+#pragma unroll
+                for (int e = 0; e < kEach / 2; ++e)
+                    o[e] = *reinterpret_cast<const float2*>(p + 2 * e);
+#pragma unroll
+                for (int e = 0; e < kEach / 2; ++e) {   // the sums of a part that has seen nothing are zeros
+                    v[2 * e] += o[e].x * g;
+                    v[2 * e + 1] += o[e].y * g;
+                }
+            }
         }
-    }
-    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-    char* to = a.out + (row_at(a, t.token, t.head, t.row0 + row, a.out_pitch, a.out_head) + lane * kEach) * 2;
+        if (!few) {
 #pragma unroll
-    for (int e = 0; e < kEach; e += 2)
-        if (lane * kEach + e < a.dim)
-            *reinterpret_cast<uint32_t*>(to + e * 2) = pack2<DT>(v[e] * f, v[e + 1] * f);
-    if (lane == 0)
-        store_lse(a, t.token, t.head, t.row0 + row, m, l);
+            for (int e = 0; e < kEach; ++e)
+                shares[warp][lane * kEach + e] = v[e];
+            if (lane == 0)
+                tops[warp] = make_float2(m, l);
+            __syncthreads();
+            float2 s[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                s[w] = tops[w];
+            m = fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x));
+            l = 0.f;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                v[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = s[w].x == -INFINITY ? (s[w].y != s[w].y ? s[w].y : 0.f) : exp2_fast(s[w].x - m);
+                l += s[w].x == -INFINITY && s[w].y == s[w].y ? 0.f : s[w].y * f;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    v[e] += shares[w][lane * kEach + e] * f;
+            }
+            __syncthreads();
+            if (warp)
+                continue;
+        }
+        const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+        char* to = a.out + (row_at(a, t.token, t.head, t.row0 + row, a.out_pitch, a.out_head) + lane * kEach) * 2;
+#pragma unroll
+        for (int e = 0; e < kEach; e += 2)
+            if (lane * kEach + e < a.dim)
+                *reinterpret_cast<uint32_t*>(to + e * 2) = pack2<DT>(v[e] * f, v[e + 1] * f);
+        if (lane == 0)
+            store_lse(a, t.token, t.head, t.row0 + row, m, l);
+    }
 }
 
 }  // namespace tsx
