@@ -21,6 +21,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16, kKeys = 64, kWarpKeys = 16, kThreads = 128, kStages = 3;
+constexpr int kJoinRows = 16;
 constexpr int64_t kLeast = 4;   // steps to a CTA at least
 
 template <int D>
@@ -350,7 +351,8 @@ cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
                                                             queue_bytes<D>() + kStatsBytes + kSumsBytes, 1, false, st, a);
     if (e != cudaSuccess)
         return e;
-    return launch_grid<attend_join_kernel<DT, D, kRows>>(dim3(unsigned(a.ctas), kRows / 4), 128, 0, 1, true, st, a);
+    return launch_grid<attend_join_kernel<DT, D, kRows, kJoinRows>>(dim3(unsigned(a.ctas), kRows / kJoinRows),
+                                                                    kJoinRows * 32, 0, 1, true, st, a);
 }
 
 template <int DT>

@@ -746,7 +746,8 @@ cudaError_t launch_many(const AttendArgs& a, const CUtensorMap* maps, cudaStream
                                                               CUtensorMap{}, CUtensorMap{});
     if (e != cudaSuccess)
         return e;
-    return launch_grid<attend_join_kernel<DT, D, kRows>>(dim3(unsigned(a.ctas), kRows / 4), 128, 0, 1, true, st, a);
+    return launch_grid<attend_join_many_kernel<DT, D, kRows>>(dim3(unsigned(a.ctas), kRows / kJoinMany), 256, 0, 1, true,
+                                                              st, a);
 }
 
 }  // namespace
