@@ -44,12 +44,13 @@ constexpr int kLoadWarp = kWeighers / 32, kIssueWarp = kLoadWarp + 3;
 // Keys or values of a step take a stage.  One CTA to an SM, which is what the
 // tensor memory is for: the stages of D = 64 are as many as keep a second one out.
 template <int D>
-TSX_HD constexpr int stages() { return D == 128 ? 5 : 8; }
+TSX_HD constexpr int stages() { return D == 128 ? 4 : 8; }
 
 template <int D>
 struct Shared {
     static constexpr int kTile = D / 64 * kBlock;   // bytes of 128 rows
-    static constexpr int kQ = 0, kRing = 2 * kTile, kEnd = kRing + stages<D>() * kTile;
+    static constexpr int kQ = 0, kRing = 2 * kTile, kStore = kRing + stages<D>() * kTile,
+                         kEnd = kStore + kWeighers / 32 * 4096;   // kStore: results on their way out
     // barriers
     static constexpr int kFull = kEnd, kEmpty = kFull + 8 * stages<D>(), kQFull = kEmpty + 8 * stages<D>(),
                          kQEmpty = kQFull + 8, kS = kQEmpty + 8, kP = kS + 16, kO = kP + 16,
@@ -508,6 +509,36 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
     return m;
 }
 
+// Results go out through shared memory, 128 bytes of a row at a time: rows lie far
+// apart, and stores of 16 bytes to each of 32 rows took 5 to 20 us for a tile.
+// N words of the thread's row, from its 16-byte chunk `first` of 8 on; chunk c of
+// row r at place c ^ (r & 7).  place: of the warp's 4096 bytes.
+template <int N>
+__device__ __forceinline__ void stage_words(uint4* place, const uint32_t* w, int first)
+{
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        place[lane * 8 + ((first + i) ^ (lane & 7))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// Rows of the warp, at `to` of each lane's row, from their byte `from` on; `width`
+// bytes of a row exist.
+__device__ __forceinline__ void send_rows(const uint4* place, char* to, uint32_t alive, int from, int width)
+{
+    const int lane = threadIdx.x % 32, chunk = lane % 8;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + lane / 8;
+        char* at = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+        const uint4 v = place[row * 8 + (chunk ^ (row & 7))];
+        if ((alive >> row & 1) && from + chunk * 16 < width)
+            *reinterpret_cast<uint4*>(at + from + chunk * 16) = v;
+    }
+    __syncwarp();
+}
+
 template <int DT, int D>
 __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned char* memory, uint32_t tmem, Tail* tail)
 {
@@ -616,41 +647,43 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
             const int64_t slot = part_slot(p);
             sum = ok ? sum : NAN;
             const float f = !whole && ok ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-            char* to = whole ? a.out + row_at(a, p.seq.first, p.head, first + row, a.out_pitch, a.out_head) * 2
-                             : reinterpret_cast<char*>(a.parts + (slot * kRows + t * kHalf + row) * D);
+            char* to = live && whole ? a.out + row_at(a, p.seq.first, p.head, first + row, a.out_pitch, a.out_head) * 2
+                                     : reinterpret_cast<char*>(a.parts + (slot * kRows + t * kHalf + row) * D);
             if (live && whole)
                 store_lse(a, p.seq.first, p.head, first + row, top, sum);
             if (live && !whole)
                 a.stats[slot * kRows + t * kHalf + row] = make_float2(top, sum);
+            uint4* place = reinterpret_cast<uint4*>(memory + S::kStore + threadIdx.x / 32 * 4096);
+            const int width = whole ? a.dim * 2 : D * 4;   // bytes of a row
+            const uint32_t alive = __ballot_sync(0xffffffffu, live);
+#pragma unroll 1   // short code: it runs once in a while, and waits for its instructions
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (ok)
+                    tmem_load32(o_at + c, o);
+                tmem_wait32(o);
+                if (strange)
+#pragma unroll 1
+                    for (int k = 0; k < 3; ++k) {
+                        const float add = k == 0 ? NAN : k == 1 ? INFINITY : -INFINITY;
 #pragma unroll
-            for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                float v[16];
-                if (ok) {
-                    tmem_load16(o_at + c, o);
-                    tmem_wait16(o);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = ok ? __uint_as_float(o[i]) : 0.f;
-                    if (strange)
-                        for (int k = 0; k < 3; ++k)
-                            v[i] += odd[k * D + c + i] < limit ? (k == 0 ? NAN : k == 1 ? INFINITY : -INFINITY) : 0.f;
-                    v[i] *= f;
-                }
-                if (!live)
-                    continue;
-#pragma unroll
-                for (int i = 0; i < 16; i += 8)
-                    if (!whole) {
-                        store16(to + (c + i) * 4, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
-                                __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
-                        store16(to + (c + i + 4) * 4, __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
-                                __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
-                    } else if (c + i < a.dim) {
-                        store16(to + (c + i) * 2, pack2<DT>(v[i], v[i + 1]), pack2<DT>(v[i + 2], v[i + 3]),
-                                pack2<DT>(v[i + 4], v[i + 5]), pack2<DT>(v[i + 6], v[i + 7]));
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) + (odd[k * D + c + i] < limit ? add : 0.f));
                     }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = __float_as_uint(ok ? __uint_as_float(o[i]) * f : NAN);
+                if (whole) {   // 64 channels make 128 bytes
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = pack2<DT>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                    stage_words<16>(place, o, c / 32 % 2 * 4);
+                    if (c / 32 % 2)
+                        send_rows(place, to, alive, (c - 32) * 2, width);
+                } else {
+                    stage_words<32>(place, o, 0);
+                    send_rows(place, to, alive, c * 4, width);
+                }
             }
             tcgen05_before();
         }

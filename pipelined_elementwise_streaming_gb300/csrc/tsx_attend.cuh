@@ -55,8 +55,9 @@ __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t by)
     return (a | by) >> 32 ? a / by : static_cast<uint32_t>(a) / static_cast<uint32_t>(by);
 }
 
-// Sum of floor((step i + from) / by) over 0 <= i < n.
-__device__ __forceinline__ uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
+// Sum of floor((step i + from) / by) over 0 <= i < n.  Once in the code: what runs
+// once in a kernel waits for its instructions, not for its arithmetic.
+static __device__ __noinline__ uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
 {
     uint64_t sum = 0;
     while (n) {
@@ -175,15 +176,19 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
     rest -= r.head * head;
     const Seq s = seq_of(a, r.b);
     int lo = 0, hi = tiles_of<M>(a, s);   // the tile: steps_before(lo) <= rest < steps_before(hi)
+    int64_t before = 0;
     while (hi - lo > 1) {   // 32 places looked at at once
         const int apart = (hi - lo + 32) / 33;
         const int64_t at = lo + static_cast<int64_t>(lane + 1) * apart;
-        const bool under = at < hi && steps_before<M, TK>(a, s, static_cast<int>(at)) <= rest;
-        lo += __popc(__ballot_sync(0xffffffffu, under)) * apart;
+        const int64_t steps = at < hi ? steps_before<M, TK>(a, s, static_cast<int>(at)) : rest + 1;
+        const int under = __popc(__ballot_sync(0xffffffffu, steps <= rest));
+        if (under)
+            before = __shfl_sync(0xffffffffu, steps, under - 1);
+        lo += under * apart;
         hi = min(hi, lo + apart);
     }
     r.tile = lo;
-    r.step = static_cast<int>(rest - (lo ? steps_before<M, TK>(a, s, lo) : 0));
+    r.step = static_cast<int>(rest - before);
     return r;
 }
 
