@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
             }
         }
         const Tail t = tail_of<kRows>(run, p);
-        if (t.follow)
+        if (t.per)
             tail = t;
         __syncthreads();   // before the queues are used again
         advance<kRows>(a, run, p);

@@ -694,7 +694,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
         }
         count += p.end - p.step;
         const Tail now = tail_of<kRows>(run, p);
-        if (now.follow)
+        if (now.per)
             *tail = now;
         advance<kRows>(a, run, p);
     }

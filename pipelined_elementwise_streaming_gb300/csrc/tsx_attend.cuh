@@ -49,27 +49,53 @@ __device__ __forceinline__ int row_limit(const AttendArgs& a, const Seq& s, int 
     return max(s.prior + row / a.group + 1, 0);
 }
 
-// a / by; in 32 bits, at a fifth of the instructions, where that is enough.
+// a / by; in 32 bits, at a fifth of the instructions, where that is enough.  What
+// runs once in a kernel waits for its instructions rather than for its arithmetic, so
+// the long ways are there once (a tile's results took 5 us in place of 2.5 in longer
+// code).
+static __device__ __noinline__ uint64_t long_quotient(uint64_t a, uint64_t by) { return a / by; }
 __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t by)
 {
-    return (a | by) >> 32 ? a / by : static_cast<uint32_t>(a) / static_cast<uint32_t>(by);
+    return (a | by) >> 32 ? long_quotient(a, by) : static_cast<uint32_t>(a) / static_cast<uint32_t>(by);
 }
 
-// Sum of floor((step i + from) / by) over 0 <= i < n.  Once in the code: what runs
-// once in a kernel waits for its instructions, not for its arithmetic.
-static __device__ __noinline__ uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
+// Sum of floor((step i + from) / by) over 0 <= i < n: the whole parts, and the same
+// sum mirrored.
+static __device__ __noinline__ uint64_t long_floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
 {
     uint64_t sum = 0;
     while (n) {
-        const uint64_t p = quotient(step, by), q = quotient(from, by);
+        const uint64_t p = step / by, q = from / by;
         sum += n * (n - 1) / 2 * p + n * q;
         step -= p * by;
         const uint64_t top = step * n + (from - q * by);
-        n = quotient(top, by);   // as many i of the mirrored sum
+        n = top / by;
         from = top - n * by;
         const uint64_t t = by;
         by = step;
         step = t;
+    }
+    return sum;
+}
+__device__ __forceinline__ uint64_t floor_sum(uint64_t n, uint64_t by, uint64_t step, uint64_t from)
+{
+    // n < 2^31: the largest number met in 32 bits is step n + from
+    if ((by | (step * n + from)) >> 32)
+        return long_floor_sum(n, by, step, from);
+    uint32_t n32 = static_cast<uint32_t>(n), by32 = static_cast<uint32_t>(by), step32 = static_cast<uint32_t>(step),
+             from32 = static_cast<uint32_t>(from);
+    uint64_t sum = 0;
+#pragma unroll 1
+    while (n32) {
+        const uint32_t p = step32 / by32, q = from32 / by32;
+        sum += (static_cast<uint64_t>(n32) * (n32 - 1) >> 1) * p + static_cast<uint64_t>(n32) * q;
+        step32 -= p * by32;
+        const uint32_t top = step32 * n32 + (from32 - q * by32);
+        n32 = top / by32;
+        from32 = top - n32 * by32;
+        const uint32_t t = by32;
+        by32 = step32;
+        step32 = t;
     }
     return sum;
 }
@@ -116,67 +142,31 @@ struct Run {
     int b, head, tile, step;
 };
 
-// Every thread of the CTA takes part; `sums` holds a word to each warp and three more.
-template <int M, int TK, int THREADS>
-__device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_t* sums)
+__device__ __forceinline__ void share_out(Run& r, int64_t total, int64_t least)
 {
-    constexpr int kWarps = THREADS / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    Run r{};
-    int64_t total = 0;
-    for (int pass = 0; pass < 2; ++pass) {   // the sum of all, then who has the first of mine
-        int64_t before = 0;
-        for (int base = 0; base < a.paged.seqs; base += THREADS) {
-            const int b = base + threadIdx.x;
-            int64_t mine = 0, head = 0;
-            if (b < a.paged.seqs) {
-                head = steps_of_head<M, TK>(a, seq_of(a, b));
-                mine = head * a.heads;
-            }
-            int64_t upto = mine;
+    r.per = max(static_cast<int64_t>(quotient(total + gridDim.x - 1, gridDim.x)), least);
+    r.from = min(static_cast<int64_t>(blockIdx.x) * r.per, total);
+    r.to = min(r.from + r.per, total);
+}
+
+__device__ __forceinline__ int64_t sum_upto(int64_t v, int lane)
+{
 #pragma unroll
-            for (int m = 1; m < 32; m *= 2) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, upto, m);
-                upto += lane >= m ? o : 0;
-            }
-            if (lane == 31)
-                sums[warp] = upto;
-            __syncthreads();
-            int64_t all = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                upto += w < warp ? sums[w] : 0;
-                all += sums[w];
-            }
-            upto += before;
-            before += all;
-            if (pass == 0 && base + THREADS >= a.paged.seqs) {
-                total = before;
-                r.per = max(static_cast<int64_t>(quotient(total + gridDim.x - 1, gridDim.x)), least);
-                r.from = min(static_cast<int64_t>(blockIdx.x) * r.per, total);
-                r.to = min(r.from + r.per, total);
-            }
-            // one block of sequences: its sums are at hand
-            if ((pass == 1 || a.paged.seqs <= THREADS) && r.from < r.to && upto - mine <= r.from && r.from < upto) {
-                sums[kWarps] = b;
-                sums[kWarps + 1] = r.from - (upto - mine);
-                sums[kWarps + 2] = head;
-            }
-            __syncthreads();
-        }
-        if (a.paged.seqs <= THREADS || r.from >= r.to)
-            break;
+    for (int m = 1; m < 32; m *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, m);
+        v += lane >= m ? o : 0;
     }
-    if (r.from >= r.to)
-        return r;
-    r.b = static_cast<int>(sums[kWarps]);
-    int64_t rest = sums[kWarps + 1];
-    const int64_t head = sums[kWarps + 2];
-    r.head = static_cast<int>(quotient(rest, head));
-    rest -= r.head * head;
-    const Seq s = seq_of(a, r.b);
-    int lo = 0, hi = tiles_of<M>(a, s);   // the tile: steps_before(lo) <= rest < steps_before(hi)
+    return v;
+}
+
+// The tile and step of unit `rest` of a head.
+template <int M, int TK>
+__device__ __forceinline__ void find_tile(const AttendArgs& a, const Seq& s, int64_t rest, Run& r)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = tiles_of<M>(a, s);   // steps_before(lo) <= rest < steps_before(hi)
     int64_t before = 0;
+#pragma unroll 1
     while (hi - lo > 1) {   // 32 places looked at at once
         const int apart = (hi - lo + 32) / 33;
         const int64_t at = lo + static_cast<int64_t>(lane + 1) * apart;
@@ -189,6 +179,76 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
     }
     r.tile = lo;
     r.step = static_cast<int>(rest - before);
+}
+
+// Every thread of the CTA takes part; `sums` holds a word to each warp and three
+// more.  Up to 32 sequences are a lane's each, in every warp alike; more of them are
+// shared out among all threads.
+template <int M, int TK, int THREADS>
+__device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_t* sums)
+{
+    constexpr int kWarps = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    Run r{};
+    int64_t rest, head;   // units before mine in the sequence, and of a head
+    if (a.paged.seqs <= 32) {
+        Seq s{};
+        head = 0;
+        if (lane < a.paged.seqs) {
+            s = seq_of(a, lane);
+            head = steps_of_head<M, TK>(a, s);
+        }
+        const int64_t mine = head * a.heads, upto = sum_upto(mine, lane);
+        share_out(r, __shfl_sync(0xffffffffu, upto, 31), least);
+        if (r.from >= r.to)
+            return r;
+        r.b = __ffs(__ballot_sync(0xffffffffu, upto - mine <= r.from && r.from < upto)) - 1;
+        rest = __shfl_sync(0xffffffffu, r.from - (upto - mine), r.b);
+        head = __shfl_sync(0xffffffffu, head, r.b);
+    } else {
+        int64_t total = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {   // the sum of all, then who has the first of mine
+            int64_t before = 0;
+#pragma unroll 1
+            for (int base = 0; base < a.paged.seqs; base += THREADS) {
+                const int b = base + threadIdx.x;
+                head = b < a.paged.seqs ? steps_of_head<M, TK>(a, seq_of(a, b)) : 0;
+                const int64_t mine = head * a.heads;
+                int64_t upto = sum_upto(mine, lane), all = 0;
+                if (lane == 31)
+                    sums[warp] = upto;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    upto += w < warp ? sums[w] : 0;
+                    all += sums[w];
+                }
+                upto += before;
+                before += all;
+                if (pass == 0 && base + THREADS >= a.paged.seqs) {
+                    total = before;
+                    share_out(r, total, least);
+                }
+                // one block of sequences: its sums are at hand
+                if ((pass == 1 || a.paged.seqs <= THREADS) && r.from < r.to && upto - mine <= r.from && r.from < upto) {
+                    sums[kWarps] = b;
+                    sums[kWarps + 1] = r.from - (upto - mine);
+                    sums[kWarps + 2] = head;
+                }
+                __syncthreads();
+            }
+            if (a.paged.seqs <= THREADS || r.from >= r.to)
+                break;
+        }
+        if (r.from >= r.to)
+            return r;
+        r.b = static_cast<int>(sums[kWarps]);
+        rest = sums[kWarps + 1];
+        head = sums[kWarps + 2];
+    }
+    r.head = static_cast<int>(quotient(rest, head));
+    find_tile<M, TK>(a, seq_of(a, r.b), rest - r.head * head, r);
     return r;
 }
 
@@ -234,8 +294,10 @@ __device__ __forceinline__ void advance(const AttendArgs& a, Run& r, const Piece
 
 // The scratch: parts of a CTA's first and last tile, and what its last one is.
 struct Tail {
-    int follow;   // CTAs that go on with the tile (0: nothing to join)
+    int64_t last, per;   // the tile's last unit, and the units of a CTA; per 0: nothing to join
     int token, row0, rows, head;
+    // CTAs after `cta` that go on with the tile
+    __device__ __forceinline__ int follow(int cta) const { return per ? static_cast<int>(last / per) - cta : 0; }
 };
 
 // Where the CTA's part of this piece goes, and what is to be joined.
@@ -246,7 +308,8 @@ __device__ __forceinline__ Tail tail_of(const Run& r, const Piece& p)
 {
     Tail t{};
     if (p.step == 0 && p.end < p.steps) {
-        t.follow = static_cast<int>(quotient(r.from + p.steps - 1, r.per)) - static_cast<int>(blockIdx.x);
+        t.last = r.from + p.steps - 1;
+        t.per = r.per;
         t.token = p.seq.first;
         t.row0 = p.tile * M;
         t.rows = p.rows;
@@ -329,12 +392,13 @@ __global__ void __launch_bounds__(ROWS * 32) attend_join_kernel(const __grid_con
     const Tail t = a.tails[blockIdx.x];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row0 = blockIdx.y * ROWS;
     const int rows = min(ROWS, t.rows - row0);
-    if (!t.follow || rows <= 0)
+    const int follow = t.follow(blockIdx.x);
+    if (!follow || rows <= 0)
         return;
     int share = 1;   // warps to a row
     while (2 * share * rows <= ROWS)
         share *= 2;
-    const int row = row0 + warp / share, parts = t.follow + 1;
+    const int row = row0 + warp / share, parts = follow + 1;
     const bool live = row < row0 + rows;
     const int first = 2 * blockIdx.x + 1;   // then the first slots of the CTAs that follow
     // running maximum and sums over 32 of the warp's parts at a time
@@ -436,7 +500,8 @@ __global__ void __launch_bounds__(256) attend_join_many_kernel(const __grid_cons
     wait_for_last();
     const Tail t = a.tails[blockIdx.x];
     const int lane = threadIdx.x % 32, row0 = blockIdx.y * kJoinMany + threadIdx.x / 32 * kRowsAtOnce;
-    if (!t.follow || row0 >= t.rows)
+    const int follow = t.follow(blockIdx.x);
+    if (!follow || row0 >= t.rows)
         return;
     float m[kRowsAtOnce], l[kRowsAtOnce], v[kRowsAtOnce][kEach] = {};
 #pragma unroll
@@ -445,7 +510,7 @@ __global__ void __launch_bounds__(256) attend_join_many_kernel(const __grid_cons
         l[r] = 0.f;
     }
 #pragma unroll 2
-    for (int i = 0; i <= t.follow; ++i) {
+    for (int i = 0; i <= follow; ++i) {
         const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (i ? 2 * i : 1)) * M + row0;
         float2 s[kRowsAtOnce], o[kRowsAtOnce][kEach / 2];
 #pragma unroll
