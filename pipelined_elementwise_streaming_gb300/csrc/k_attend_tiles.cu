@@ -605,7 +605,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
                 top = grows ? now : top;
                 sum *= f;
                 if (step > p.step && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 16) {   // O is at rest: the scores came after its last product
                         uint32_t o[16];
                         tmem_load16(o_at + c, o);
