@@ -92,9 +92,8 @@ typedef struct tsx_rotary_desc {
  * tokens' positions [tokens], whole numbers of position_bytes (4 or 8) bytes,
  * negative ones too.  q_weight, k_weight [dim]: NULL for ones; NULL without a
  * norm.  An output may be exactly its input, with the same pitches; any other
- * overlap is undefined.  16-byte vectors are used where dim and rot are
- * multiples of 8 (16 for the rot of TSX_ROPE_HALF), the pitches of 16 bytes,
- * and the pointers aligned to 16; any other layout works element by element.
+ * overlap is undefined.  Vectors are used where dim and rot are
+ * multiples of 8, the pitches of 16 bytes, and the pointers aligned to 16; any other layout works element by element.
  *
  * Angles have an error of 2^-32 of a turn and that of fp32 sines: under 2^-22
  * for fp32 tensors, and for 16-bit ones, which take the hardware's approximate

@@ -109,10 +109,10 @@ bool vectors(const tsx_heads* t, int64_t tokens, int64_t heads, int es)
     return aligned(t->data, 16) && even(t->pitch, tokens, es) && even(t->head_pitch, heads, es);
 }
 
-// Whether heads can be cut into octs of whole pairs.
-bool octs(const tsx_rotary_desc& d)
+// Whether heads can be cut into eights of whole pairs.
+bool eights(const tsx_rotary_desc& d)
 {
-    return d.dim % 8 == 0 && d.rot % (d.layout == TSX_ROPE_HALF ? 16 : 8) == 0;
+    return d.dim % 8 == 0 && d.rot % 8 == 0;
 }
 
 void rotary_args(const tsx_rotary_desc& d, int64_t tokens, RotaryArgs* a)
@@ -126,8 +126,9 @@ void rotary_args(const tsx_rotary_desc& d, int64_t tokens, RotaryArgs* a)
     a->wide_params = d.param_dtype == TSX_F32;
     a->eps = d.eps;
     a->amplitude = d.amplitude;
+    a->by_dim = 1.f / float(d.dim);
     a->team = 1;
-    while (a->team * 16 < d.dim)
+    while (a->team * 8 < d.dim)
         a->team *= 2;
     std::copy(d.turns, d.turns + TSX_ROPE_PAIRS, a->turns);
 }
@@ -151,50 +152,31 @@ RotaryRole role(int which, const tsx_heads* x, const tsx_heads* out, int heads, 
     return r;
 }
 
-// CTAs of a wave: three of 256 threads to each of the 152 SMs.
-constexpr int64_t kRotaryWave = 3 * 152;
-// CTAs of the gradient through a norm, two to each SM: they stay for all their tokens.
-constexpr int64_t kBackwardWave = 2 * 152;
+constexpr int64_t kSms = 152;   // a constant of the chip, not read from it: the order of sums depends on the shape alone
+// Heads that a thread goes over with one set of sines, cosines and weights: forward
+// bf16 [8192, 32 + 8, 128] with a norm 29.8 us in place of 33.3 with eight (27.2 and
+// 27.9 without); the gradient through a norm 56.2 with eight and 70 with sixteen.
+constexpr int kForwardHeads = 16, kBackwardHeads = 8;
 
-// How a forward call's heads are shared out: teams of threads that take one
-// batch of heads each, or single heads where that leaves SMs without work.
-// Element by element a team is a warp.
-int lay_forward(RotaryArgs* a, int dtype, bool vec)
+// How a call's heads are shared out: teams of threads that take several heads of a
+// token each, as many as leave two CTAs of work to each SM (one that stays), down to
+// one.  Element by
+// element a team is a warp.  wave: CTAs at most, each tensor's by its heads, which
+// stay for all their tokens; 0: as many as there is work.
+int lay_out(RotaryArgs* a, bool vec, int each, int64_t wave)
 {
     const int64_t teams = kRotaryThreads / (vec ? a->team : 32);
     int64_t heads = 0;
     for (int i = 0; i < a->roles; ++i)
         heads += a->role[i].heads;
-    const int batch = rotary_batch(dtype);
-    const bool few = a->tokens * heads / batch < teams * kRotaryWave;
+    each = int(std::max<int64_t>(std::min<int64_t>(each, a->tokens * heads / (teams * (wave ? 1 : 2) * kSms)), 1));
     int first = 0;
     for (int i = 0; i < a->roles; ++i) {
         RotaryRole& r = a->role[i];
-        r.parts = few ? r.heads : (r.heads + batch - 1) / batch;
-        r.first = first;
-        r.ctas = int((a->tokens * r.parts + teams - 1) / teams);
-        first += r.ctas;
-    }
-    return first;
-}
-
-// The same of a gradient through the norm, whose CTAs number a wave at most,
-// each tensor's by its heads.
-int lay_backward(RotaryArgs* a, int dtype, bool vec)
-{
-    const int64_t teams = kRotaryThreads / (vec ? a->team : 32);
-    int64_t heads = 0;
-    for (int i = 0; i < a->roles; ++i)
-        heads += a->role[i].heads;
-    const int batch = 2 * rotary_batch(dtype);
-    const bool few = a->tokens * heads / batch < teams * kBackwardWave;
-    int first = 0;
-    for (int i = 0; i < a->roles; ++i) {
-        RotaryRole& r = a->role[i];
-        r.parts = few ? r.heads : (r.heads + batch - 1) / batch;
+        r.parts = (r.heads + each - 1) / each;
         r.first = first;
         const int64_t all = (a->tokens * r.parts + teams - 1) / teams;
-        r.ctas = int(std::min(all, std::max<int64_t>(kBackwardWave * r.heads / heads, 1)));
+        r.ctas = int(wave ? std::min(all, std::max<int64_t>(wave * r.heads / heads, 1)) : all);
         first += r.ctas;
     }
     return first;
@@ -341,7 +323,7 @@ extern "C" int tsx_rotary(const tsx_rotary_desc* desc, int64_t tokens, const voi
     a.positions = positions;
     a.wide_positions = position_bytes == 8;
     const int es = elem_size(d.dtype);
-    bool vec = octs(d);
+    bool vec = eights(d);
     if (d.q_heads) {
         vec = vec && vectors(q, tokens, d.q_heads, es) && vectors(q_out, tokens, d.q_heads, es);
         a.role[a.roles++] = role(0, q, q_out, d.q_heads, q_weight);
@@ -350,7 +332,7 @@ extern "C" int tsx_rotary(const tsx_rotary_desc* desc, int64_t tokens, const voi
         vec = vec && vectors(k, tokens, d.k_heads, es) && vectors(k_out, tokens, d.k_heads, es);
         a.role[a.roles++] = role(1, k, k_out, d.k_heads, k_weight);
     }
-    const int ctas = lay_forward(&a, d.dtype, vec);
+    const int ctas = lay_out(&a, vec, kForwardHeads, 0);
     return launched(launch_rotary(d.dtype, a, vec, ctas, reinterpret_cast<cudaStream_t>(stream)), call);
 }
 
@@ -364,8 +346,8 @@ extern "C" int tsx_rotary_workspace(const tsx_rotary_desc* desc, int64_t tokens,
         return rc;
     if (!bytes)
         return fail(TSX_ERR_INVALID, call, "bytes is NULL");
-    // a slice to each CTA: two waves' at most, whatever the layout
-    *bytes = desc->norm && tokens ? size_t(kBackwardWave + 2) * desc->dim * 4 : 0;
+    // a slice to each CTA: a wave's at most, whatever the layout
+    *bytes = desc->norm && tokens ? size_t(backward_ctas(desc->dtype) * kSms + 2) * desc->dim * 4 : 0;
     set_last_error("");
     return TSX_OK;
 }
@@ -417,7 +399,7 @@ extern "C" int tsx_rotary_backward(const tsx_rotary_desc* desc, int64_t tokens, 
     rotary_args(d, tokens, &a);
     a.positions = positions;
     a.wide_positions = position_bytes == 8;
-    bool vec = octs(d);
+    bool vec = eights(d);
     const tsx_heads* in[2] = {dq, dk};
     const tsx_heads* saved[2] = {q, k};
     const tsx_heads* out[2] = {dq_out, dk_out};
@@ -439,10 +421,10 @@ extern "C" int tsx_rotary_backward(const tsx_rotary_desc* desc, int64_t tokens, 
     if (!d.norm) {   // turned by the opposite angles
         for (uint64_t& t : a.turns)
             t = 0 - t;
-        const int ctas = lay_forward(&a, d.dtype, vec);
+        const int ctas = lay_out(&a, vec, kForwardHeads, 0);
         return launched(launch_rotary(d.dtype, a, vec, ctas, st), call);
     }
-    const int ctas = lay_backward(&a, d.dtype, vec);
+    const int ctas = lay_out(&a, vec, kBackwardHeads, backward_ctas(d.dtype) * kSms);
     const bool sums = dq_weight || dk_weight;
     if (sums) {
         int64_t need = 0;
@@ -575,7 +557,7 @@ extern "C" int tsx_cache_append(const tsx_rotary_desc* desc, const tsx_cache* ca
     RotaryArgs a;
     rotary_args(d, tokens, &a);
     a.paged = paged_args(*cache, *batch);
-    bool vec = octs(d) && cache_vectors(*cache) && vectors(k, tokens, d.k_heads, es) && vectors(v, tokens, d.k_heads, es);
+    bool vec = eights(d) && cache_vectors(*cache) && vectors(k, tokens, d.k_heads, es) && vectors(v, tokens, d.k_heads, es);
     if (d.q_heads) {
         vec = vec && vectors(q, tokens, d.q_heads, es) && vectors(q_out, tokens, d.q_heads, es);
         a.role[a.roles++] = role(0, q, q_out, d.q_heads, q_weight);
@@ -586,7 +568,7 @@ extern "C" int tsx_cache_append(const tsx_rotary_desc* desc, const tsx_cache* ca
     a.role[a.roles++] = role(2, v, &slots[1], d.k_heads, nullptr);
     for (int i = 0; i < a.roles; ++i)
         a.role[i].paged = a.role[i].which > 0;
-    const int ctas = lay_forward(&a, d.dtype, vec);
+    const int ctas = lay_out(&a, vec, kForwardHeads, 0);
     return launched(launch_rotary(d.dtype, a, vec, ctas, reinterpret_cast<cudaStream_t>(stream)), call);
 }
 
