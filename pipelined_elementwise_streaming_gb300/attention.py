@@ -301,6 +301,7 @@ class PagedAttention(_Heads):
         self.scale = self.dim ** -0.5 if scale is None else float(scale)
         if not math.isfinite(self.scale):
             _invalid("scale must be finite")
+        self._scratch = {}
         if rotary is None:
             self._rope = Rotary(dtype, q_heads, kv_heads, dim, rot=0)
         elif (rotary.dtype, rotary.q_heads, rotary.k_heads, rotary.dim) != (dtype, self.q_heads, self.k_heads, self.dim):
@@ -342,6 +343,15 @@ class PagedAttention(_Heads):
             _invalid("starts, lengths and each sequence's pages must be contiguous")
         return tsx_batch(starts.data_ptr(), lengths.data_ptr(), pages.data_ptr(), pages.stride(0), seqs,
                          pages.shape[1])
+
+    def _workspace(self, cache: tsx_cache, most_new: int) -> int:
+        """Bytes of scratch, which do not depend on the tokens; remembered for a
+        few values of most_new."""
+        size = ctypes.c_size_t()
+        _call(tsx_paged_attention_workspace(_ref(cache), 1, self.q_heads, most_new, _ref(size)))
+        if len(self._scratch) < 64:
+            self._scratch[most_new] = size.value
+        return size.value
 
     def append(self, q, k, v, cache, batch: Batch, q_weight=None, k_weight=None, out=None, stream=None):
         """Puts the new tokens' k and v into the cache and returns q turned (a
@@ -386,13 +396,12 @@ class PagedAttention(_Heads):
         out, to = self._result(out, q, tokens, self.q_heads, "out", dev)
         logs = self._new((tokens, self.q_heads), dtype=self._f32, device=q.device) if lse else None
         most_new = int(batch.most_new)
-        size = ctypes.c_size_t()
-        rc = tsx_paged_attention_workspace(_ref(c), tokens, self.q_heads, most_new, _ref(size))
-        if rc:
-            _call(rc)
-        scratch = self._new((size.value,), dtype=self._byte, device=q.device)
+        size = self._scratch.get(most_new)
+        if size is None:
+            size = self._workspace(c, most_new)
+        scratch = self._new((size,), dtype=self._byte, device=q.device)
         rc = tsx_paged_attention(_ref(c), _ref(b), tokens, self.q_heads, most_new, self.scale, _ref(tq), _ref(to),
-                                 None if logs is None else logs.data_ptr(), scratch.data_ptr(), size.value,
+                                 None if logs is None else logs.data_ptr(), scratch.data_ptr(), size,
                                  self._stream(dev))
         if rc:
             _call(rc)

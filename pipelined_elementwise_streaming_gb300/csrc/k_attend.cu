@@ -20,15 +20,20 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRows = 16, kKeys = 64, kWarpKeys = 16, kThreads = 128, kStages = 3;
-constexpr int kJoinRows = 16;
-constexpr int64_t kLeast = 4;   // steps to a CTA at least
+constexpr int kRows = 16, kKeys = 64, kWarpKeys = 16, kThreads = 128;
+// Stages of a warp's queue: as many bytes on their way for either width.
+template <int D>
+TSX_HD constexpr int stages() { return D == 64 ? 6 : 3; }
+constexpr int kJoinRows = 4, kJoinWarps = 8;
+// Steps to a CTA at least: one sequence of 300 keys, 32 heads over 8, 10.5 us with 2,
+// 11.8 with 4, 16.6 with 8.
+constexpr int64_t kLeast = 2;
 
 template <int D>
 TSX_HD constexpr int stage_bytes() { return 2 * kWarpKeys * D * 2; }
 // Shared memory: the queues, the warps' statistics, the words of run_of.
 template <int D>
-TSX_HD constexpr int queue_bytes() { return 4 * kStages * stage_bytes<D>(); }
+TSX_HD constexpr int queue_bytes() { return 4 * stages<D>() * stage_bytes<D>(); }
 constexpr int kStatsBytes = 4 * kRows * 8, kSumsBytes = (kThreads / 32 + 3) * 8;
 
 __device__ __forceinline__ void ldmatrix(uint32_t at, uint32_t (&r)[4])
@@ -117,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
     float2(*stats)[kRows] = reinterpret_cast<float2(*)[kRows]>(memory + queue_bytes<D>());
     int64_t* sums = reinterpret_cast<int64_t*>(memory + queue_bytes<D>() + kStatsBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, c2 = lane % 4 * 2;
+    constexpr int kStages = stages<D>();
     const uint32_t queue = smem_addr(memory) + warp * (kStages * stage_bytes<D>());
     let_next_start();
     Run run = run_of<kRows, kKeys, kThreads>(a, kLeast, sums);
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
-#pragma unroll
+#pragma unroll 1
                         for (int key = 0; key < kWarpKeys; ++key) {
                             const uint32_t pair = *reinterpret_cast<const uint32_t*>(bytes + chunk_at<D>(key, i) + c2 * 2);
                             if (!not_finite<DT>(pair) || !(mask >> key & 1))
@@ -351,8 +357,8 @@ cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
                                                             queue_bytes<D>() + kStatsBytes + kSumsBytes, 1, false, st, a);
     if (e != cudaSuccess)
         return e;
-    return launch_grid<attend_join_kernel<DT, D, kRows, kJoinRows>>(dim3(unsigned(a.ctas), kRows / kJoinRows),
-                                                                    kJoinRows * 32, 0, 1, true, st, a);
+    return launch_grid<attend_join_kernel<DT, D, kRows, kJoinRows, kJoinWarps>>(
+        dim3(unsigned(a.ctas), kRows / kJoinRows), kJoinWarps * 32, 0, 1, true, st, a);
 }
 
 template <int DT>

@@ -376,18 +376,18 @@ __device__ __forceinline__ float part_factor(float2 s, float m, float* add)
 }
 
 // Joins the parts of the tile that CTA blockIdx.x has begun and not ended, of few
-// rows and many parts: a CTA of 16 warps, which share the rows evenly, so that a
+// rows and many parts: WARPS warps to ROWS rows, which they share evenly, so that a
 // row's parts are one warp's or those of several warps that take them in turn.
 // Statistics are read a lane to a part, so that the sums of values do not wait for
 // one another: one sequence of 100003 keys and two heads, 152 parts to a head, 13 us
 // in place of 72 part after part.
-template <int DT, int D, int M, int ROWS>
-__global__ void __launch_bounds__(ROWS * 32) attend_join_kernel(const __grid_constant__ AttendArgs a)
+template <int DT, int D, int M, int ROWS, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) attend_join_kernel(const __grid_constant__ AttendArgs a)
 {
     using namespace dev;
     constexpr int kEach = D / 32, kAtOnce = 32 / kEach;   // channels to a lane, parts in flight
-    __shared__ float sums[ROWS][D];
-    __shared__ float2 tops[ROWS];
+    __shared__ float sums[WARPS][D];
+    __shared__ float2 tops[WARPS];
     wait_for_last();
     const Tail t = a.tails[blockIdx.x];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row0 = blockIdx.y * ROWS;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(ROWS * 32) attend_join_kernel(const __grid_con
     if (!follow || rows <= 0)
         return;
     int share = 1;   // warps to a row
-    while (2 * share * rows <= ROWS)
+    while (2 * share * rows <= WARPS)
         share *= 2;
     const int row = row0 + warp / share, parts = follow + 1;
     const bool live = row < row0 + rows;
