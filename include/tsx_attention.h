@@ -122,7 +122,7 @@ int tsx_rotary_backward(const tsx_rotary_desc *desc, int64_t tokens, const void 
 
 /* --------------------------------------------------------- paged cache */
 
-/* Keys and values in pages of page_size slots: element d of head h in slot s of
+/* Keys and values in pages of page_size (up to 2^20) slots: element d of head h in slot s of
  * page p is k[p * page_pitch + s * slot_pitch + h * head_pitch + d], and the
  * same of v.  Slots before heads ([pages, page_size, heads, dim]) and heads
  * before slots ([pages, heads, page_size, dim]) are both a matter of pitches. */
@@ -141,7 +141,7 @@ typedef struct tsx_cache {
  *             from starts[seqs] on belong to no sequence: nothing is read or
  *             written for them
  *   lengths   [seqs]; at least the sequence's new tokens, at most most_pages *
- *             page_size, and taken for that where it is more
+ *             page_size and 2^31 - 2^20, and taken for that where it is more
  *   pages     [seqs, most_pages]; entries for positions that are not used are
  *             not read.  A page outside of 0 .. pages - 1 holds nothing: no
  *             token is appended to it, and its keys are passed over */

@@ -31,6 +31,9 @@ struct RotaryRole {
     int packed_weight;    // the weight is aligned to 16 bytes
 };
 
+// Keys of a sequence at most, so that positions and what is added to them fit 32 bits.
+constexpr int kMostKeys = 0x7fffffff - (1 << 20);
+
 // Where the tokens of a batch lie (see tsx_batch and tsx_cache).
 struct PagedArgs {
     const int32_t *starts, *lengths, *pages;

@@ -240,8 +240,8 @@ extern "C" int tsx_rotary_turns(int pairs, const double* frequencies, uint64_t* 
     // 64 bits of its fraction are good to a unit or two
     const double hi = 6.283185307179586, lo = 2.4492935982947064e-16;
     for (int i = 0; i < pairs; ++i) {
-        const double f = frequencies[i];
-        if (!std::isfinite(f) || std::fabs(f) > 0x1p30)
+        const double f = std::fabs(frequencies[i]);
+        if (!(f <= 0x1p30))
             return fail(TSX_ERR_INVALID, call, "frequencies must be finite, 2^30 at most");
         const double q = f / hi;
         const double rest = std::fma(-q, lo, std::fma(-q, hi, f));
@@ -249,7 +249,8 @@ extern "C" int tsx_rotary_turns(int pairs, const double* frequencies, uint64_t* 
         // q - whole is exact; both parts in units of 2^-64, where 2^64 itself is 0 again
         const double big = std::ldexp(q - whole, 64), small = std::ldexp(rest / hi, 64);
         const uint64_t b = big >= 0x1p64 ? 0 : uint64_t(big);
-        turns[i] = b + uint64_t(int64_t(std::nearbyint(small + (big >= 0x1p64 ? 0 : big - double(b)))));
+        const uint64_t t = b + uint64_t(int64_t(std::nearbyint(small + (big >= 0x1p64 ? 0 : big - double(b)))));
+        turns[i] = frequencies[i] < 0 ? 0 - t : t;
     }
     set_last_error("");
     return TSX_OK;
@@ -673,8 +674,9 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
         return fail(TSX_ERR_INVALID, call, "the workspace is smaller than tsx_paged_attention_workspace says");
     AttendArgs a{};
     a.paged = paged_args(*cache, *batch);
-    a.k = static_cast<const char*>(cache->k);
-    a.v = static_cast<const char*>(cache->v);
+    // without pages nothing is read, but copies of no bytes name an address
+    a.k = static_cast<const char*>(cache->pages ? cache->k : q->data);
+    a.v = static_cast<const char*>(cache->pages ? cache->v : q->data);
     a.q = static_cast<const char*>(q->data);
     a.out = static_cast<char*>(out->data);
     a.lse = lse;

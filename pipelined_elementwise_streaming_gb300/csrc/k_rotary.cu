@@ -90,8 +90,8 @@ __device__ __forceinline__ TokenPlace token_place(const PagedArgs& p, const int3
             hi = mid;
     }
     t.live = true;
-    int64_t length = p.lengths[lo];
-    length = min(length, static_cast<int64_t>(p.most_pages) * p.page_size);
+    const int64_t most = min(static_cast<int64_t>(p.most_pages) * p.page_size, static_cast<int64_t>(kMostKeys));
+    const int64_t length = min(static_cast<int64_t>(p.lengths[lo]), most);
     t.position = length - s[lo + 1] + token;
     if (t.position < 0)
         return t;

@@ -37,7 +37,7 @@ __device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b)
     Seq s;
     s.first = min(max(a.paged.starts[b], 0), tokens);
     s.fresh = min(max(a.paged.starts[b + 1], s.first), tokens) - s.first;
-    const int64_t most = static_cast<int64_t>(a.paged.most_pages) * a.paged.page_size;
+    const int64_t most = min(static_cast<int64_t>(a.paged.most_pages) * a.paged.page_size, static_cast<int64_t>(kMostKeys));
     s.length = static_cast<int>(min(static_cast<int64_t>(max(a.paged.lengths[b], 0)), most));
     s.prior = s.length - s.fresh;
     return s;

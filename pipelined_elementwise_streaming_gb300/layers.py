@@ -80,7 +80,7 @@ def _invalid(message: str):
 
 def _named(table: dict, key, what: str) -> int:
     if key not in table:
-        _invalid(f"unknown {what} {key!r}: one of {', '.join(table)}")
+        _invalid(f"unknown {what} {key!r}: one of {', '.join(map(str, table))}")
     return table[key]
 
 
