@@ -11,6 +11,15 @@
 // Scores stay in registers: the accumulators of q k^T are the operand of the
 // product with v.  Running maxima and sums are the warp's own; they and the four
 // sums of values are joined once at the end of a piece.
+//
+// Measured on GB300, GPU time of a call in a CUDA graph over inputs that take turns;
+// in parentheses the time of the bytes at the 6791 GB/s of a copy.  One new token to
+// each of 64 sequences of 1000 to 16384, bf16, 32 heads over 8 of 128, pages of 16: 220
+// us (213).  One sequence of 100003 keys, f16, 16 heads over 2 of 64: 23 (7.5), of which
+// the join of 152 parts a head takes 7 and a CTA's start, first pages and end 5.  16
+// sequences up to 4096: 25.8 (12.6); one of 300: 10.1.  Queues of three stages of 8 KB
+// a warp keep 128 KB of an SM on their way; of 64 channels the stages are half as large
+// and there are six.
 
 #include "tsx_attend.cuh"
 #include "tsx_device.cuh"

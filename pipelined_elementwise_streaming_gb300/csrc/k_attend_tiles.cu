@@ -22,6 +22,20 @@
 // after the first steps; weights are then up to 2^8, with the same relative error.
 //
 // Every wait gives up after kPatience; then the CTA's remaining rows become NaN.
+//
+// Measured on GB300 as in the kernel for few rows; in parentheses the time of the
+// products at the 1897 TFLOP/s of cuBLAS.  bf16, chunks of 1024 tokens of two prompts of
+// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 257 us (192), 1.42 PFLOP/s; the
+// products alone would take 150 of them at the tensor cores' 4096 multiply-adds a
+// cycle.  A ragged batch of 12 (1 to 300 new tokens, up to 3000 keys, f16, 10 heads over
+// 2 of 64): 33, most of it the start and end of pieces of five steps and their joins.
+// Steps that led here, for the first of them: mma.m16n8k16 2316 us; tcgen05 from one
+// thread, cp.async loads 489; an elected lane 464; loads with few shuffles 371; four
+// threads to a row and boxes of pages 337; one thread to a row 287; short code for what
+// runs once 257.  What bounds a step now (2700 cycles for two tiles): a tile's chain of
+// scores, weights and products, 1260 + 1024 cycles and the hand-overs between them.
+// The weights of half a step handed over early, waits that poll without a pause, and
+// weights taken before their maximum is known were no faster, or slower.
 
 #include "tsx_attend.cuh"
 #include "tsx_tcgen05.cuh"
