@@ -55,7 +55,7 @@ def check(att, q, cache, batch, out, lse=None, exclude=None):
     with np.errstate(invalid="ignore"):
         size, _ = ref.attend(q64, k, np.abs(v), starts, lengths, pages, att.scale)
     longest = np.abs(np.nan_to_num(k)).max(axis=(0, 1))   # [heads, dim]
-    most = np.einsum("thd,hd->th", np.abs(q64), np.repeat(longest, q.shape[1] // k.shape[2], 0)) * att.scale
+    most = np.einsum("thd,hd->th", np.abs(q64), np.repeat(longest, q.shape[1] // k.shape[2], 0)) * abs(att.scale)
     score = most * (q.shape[2] / 16 + 4) * 2.0**-21
     steps = HALF_STEP[att.dtype]
     weight = steps + 2 * score + (lengths.max() / 16 + 8) * 2.0**-21
