@@ -317,17 +317,19 @@ class PagedAttention(_Heads):
 
     def _cache(self, cache, dev: int) -> tsx_cache:
         k, v = cache
-        dt = self._torch_dtype
+        dt, shape, strides = self._torch_dtype, k.shape, k.stride()
+        if (len(shape) == 4 and shape == v.shape and strides == v.stride() and k.dtype is dt and v.dtype is dt
+                and k.get_device() == dev and v.get_device() == dev):   # as a rule; else what is wrong
+            pages, slots, heads, dim = shape
+            if slots == self.page_size and heads == self.k_heads and dim == self.dim and (strides[3] == 1 or dim == 1):
+                return tsx_cache(self._dtype_code, heads, dim, slots, pages, strides[0], strides[1], strides[2],
+                                 k.data_ptr(), v.data_ptr())
         if k.dtype is not dt or v.dtype is not dt or k.get_device() != dev or v.get_device() != dev:
             _invalid(f"the cache must be two {self.dtype} tensors on cuda:{dev}")
-        shape, strides = k.shape, k.stride()
         if len(shape) != 4 or shape[1:] != (self.page_size, self.k_heads, self.dim) or v.shape != shape:
             _invalid(f"keys and values must have shape [pages, {self.page_size}, {self.k_heads}, {self.dim}], got "
                      f"{list(shape)} and {list(v.shape)}")
-        if v.stride() != strides or (strides[3] != 1 and self.dim > 1):
-            _invalid("keys and values must have the same strides, and channels side by side")
-        return tsx_cache(self._dtype_code, self.k_heads, self.dim, self.page_size, shape[0], *strides[:3], k.data_ptr(),
-                         v.data_ptr())
+        _invalid("keys and values must have the same strides, and channels side by side")
 
     def _batch(self, batch: Batch, dev: int) -> tsx_batch:
         starts, lengths, pages, _ = batch
@@ -335,14 +337,12 @@ class PagedAttention(_Heads):
         if (starts.dtype is not i32 or lengths.dtype is not i32 or pages.dtype is not i32
                 or starts.get_device() != dev or lengths.get_device() != dev or pages.get_device() != dev):
             _invalid(f"starts, lengths and pages must be int32 tensors on cuda:{dev}")
-        seqs = lengths.shape[0] if lengths.dim() == 1 else -1
-        if seqs < 0 or starts.shape != (seqs + 1,) or pages.dim() != 2 or pages.shape[0] != seqs:
+        shape, strides, seqs = pages.shape, pages.stride(), lengths.numel()
+        if len(shape) != 2 or shape[0] != seqs or lengths.dim() != 1 or starts.shape != (seqs + 1,):
             _invalid("starts must be [seqs + 1], lengths [seqs] and pages [seqs, most pages of a sequence]")
-        if not starts.is_contiguous() or not lengths.is_contiguous() or (
-                pages.stride(1) != 1 and pages.shape[1] > 1):
+        if not starts.is_contiguous() or not lengths.is_contiguous() or (strides[1] != 1 and shape[1] > 1):
             _invalid("starts, lengths and each sequence's pages must be contiguous")
-        return tsx_batch(starts.data_ptr(), lengths.data_ptr(), pages.data_ptr(), pages.stride(0), seqs,
-                         pages.shape[1])
+        return tsx_batch(starts.data_ptr(), lengths.data_ptr(), pages.data_ptr(), strides[0], seqs, shape[1])
 
     def _workspace(self, cache: tsx_cache, most_new: int) -> int:
         """Bytes of scratch, which do not depend on the tokens; remembered for a

@@ -354,3 +354,32 @@ def test_attention_definition_is_a_softmax():
         w = np.exp(x) / np.exp(x).sum(-1, keepdims=True)
         np.testing.assert_allclose(out[t], w @ values[:n])
         np.testing.assert_allclose(lse[t], np.log(np.exp(x).sum(-1)))
+
+
+def test_caches_and_batches_of_other_shapes_are_refused(tsx):
+    """By the class, before any call: host tensors stand for a device's."""
+    import torch
+
+    att = tsx.PagedAttention("bf16", 4, 2, 64, 16)
+    good = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16)
+    dev = good.get_device()
+    assert att._cache((good, good), dev).pages == 3
+    assert att._cache((good.transpose(1, 2).contiguous().transpose(1, 2),) * 2, dev).head_pitch == 16 * 64
+    for k, v, word in ((good.half(), good.half(), "bf16"), (good, good.half(), "bf16"), (good[0], good[0], "shape"),
+                       (good[:, :8], good[:, :8], "shape"), (good[:, :, :1], good[:, :, :1], "shape"),
+                       (good[..., :32], good[..., :32], "shape"), (good, good[:2], "shape"),
+                       (good, torch.zeros(3, 16, 2, 128, dtype=good.dtype)[..., :64], "strides"),
+                       (torch.zeros(3, 16, 2, 128, dtype=good.dtype)[..., ::2],) * 2 + ("strides",)):
+        with pytest.raises(tsx.TsxError, match=word):
+            att._cache((k, v), dev)
+    i32 = torch.zeros(9, dtype=torch.int32)
+    pages = torch.zeros(3, 5, dtype=torch.int32)
+    assert att._batch(tsx.Batch(i32[:4], i32[:3], pages, 1), dev).most_pages == 5
+    assert att._batch(tsx.Batch(i32[:4], i32[:3], torch.zeros(3, 9, dtype=torch.int32)[:, :5], 1), dev).pages_pitch == 9
+    for b, word in ((tsx.Batch(i32[:4].long(), i32[:3], pages, 1), "int32"), (tsx.Batch(i32[:3], i32[:3], pages, 1), "seqs"),
+                    (tsx.Batch(i32[:4], i32[:4], pages, 1), "seqs"), (tsx.Batch(i32[:4], i32[:3], pages[0], 1), "seqs"),
+                    (tsx.Batch(i32[:4], pages[:, :1], pages, 1), "seqs"), (tsx.Batch(i32[:8:2], i32[:3], pages, 1), "contig"),
+                    (tsx.Batch(i32[:4], i32[:6:2], pages, 1), "contig"),
+                    (tsx.Batch(i32[:4], i32[:3], torch.zeros(3, 10, dtype=torch.int32)[:, ::2], 1), "contig")):
+        with pytest.raises(tsx.TsxError, match=word):
+            att._batch(b, dev)
