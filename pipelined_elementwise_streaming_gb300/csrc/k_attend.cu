@@ -1,5 +1,4 @@
-// Attention over a paged cache for few rows to a head: single new tokens above
-// all.  And the joining of parts.
+// Attention over a paged cache for few rows to a head: single new tokens above all.
 //
 // Keys and values are read once, and for a handful of rows that is all there is
 // to do in earnest: HBM bounds it.  A CTA's four warps work for themselves, each
