@@ -266,13 +266,9 @@ class Rotary(_Heads):
         if tdk is not None:
             k_out, rk = self._result(k_out, first, tokens, self.k_heads, "k_out", dev)
         new, device = self._new, first.device
-        gq = gk = scratch = None
-        if wq is not None and wk is not None:   # two rows of one tensor, which costs less than two
-            gq, gk = new((2, self.dim), dtype=self._f32, device=device).unbind(0)
-        elif wq is not None:
-            gq = new((self.dim,), dtype=self._f32, device=device)
-        elif wk is not None:
-            gk = new((self.dim,), dtype=self._f32, device=device)
+        gq = None if wq is None else new((self.dim,), dtype=self._f32, device=device)
+        gk = None if wk is None else new((self.dim,), dtype=self._f32, device=device)
+        scratch = None
         if gq is not None or gk is not None:
             scratch = new((self._scratch,), dtype=self._byte, device=device)
         rc = tsx_rotary_backward(self._ref, tokens, at, wide, _addr(tdq), _addr(tdk), _addr(tq), _addr(tk), wq, wk,

@@ -14,9 +14,9 @@
 // Measured on GB300, GPU time of a call in a CUDA graph over inputs that take turns;
 // in parentheses the time of the bytes at the 6791 GB/s of a copy.  One new token to
 // each of 64 sequences of 1000 to 16384, bf16, 32 heads over 8 of 128, pages of 16: 220
-// us (213).  One sequence of 100003 keys, f16, 16 heads over 2 of 64: 23 (7.5), of which
+// us (213).  One sequence of 100003 keys, f16, 16 heads over 2 of 64: 22.5 (7.5), of which
 // the join of 152 parts a head takes 7 and a CTA's start, first pages and end 5.  16
-// sequences up to 4096: 25.8 (12.6); one of 300: 10.1.  Queues of three stages of 8 KB
+// sequences up to 4096: 23.7 (12.6); one of 300: 10.3.  Queues of three stages of 8 KB
 // a warp keep 128 KB of an SM on their way; of 64 channels the stages are half as large
 // and there are six.
 
@@ -33,9 +33,11 @@ constexpr int kRows = 16, kKeys = 64, kWarpKeys = 16, kThreads = 128;
 template <int D>
 TSX_HD constexpr int stages() { return D == 64 ? 6 : 3; }
 constexpr int kJoinRows = 4, kJoinWarps = 8;
-// Steps to a CTA at least: one sequence of 300 keys, 32 heads over 8, 10.5 us with 2,
-// 11.8 with 4, 16.6 with 8.
-constexpr int64_t kLeast = 2;
+// What a tile costs beside its steps, in steps, and units to a CTA at least: 16
+// sequences of up to 4096 keys, 32 heads over 8, 26.2 us with 0, 23.7 with 3, 24.6 with
+// 6; four of up to 1000 10.3 us in runs of at least 4, 11.1 of 5, 12.3 of 7.
+constexpr int kCost = 3;
+constexpr int64_t kLeast = 4;
 
 template <int D>
 TSX_HD constexpr int stage_bytes() { return 2 * kWarpKeys * D * 2; }
@@ -133,10 +135,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
     constexpr int kStages = stages<D>();
     const uint32_t queue = smem_addr(memory) + warp * (kStages * stage_bytes<D>());
     let_next_start();
-    Run run = run_of<kRows, kKeys, kThreads>(a, kLeast, sums);
+    Run run = run_of<kRows, kKeys, kCost, kThreads>(a, kLeast, sums);
     Tail tail{};
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        if (p.empty())
+            break;   // the run's last units, before a tile's first step
         const int row0 = p.tile * kRows;
         const int64_t head_at = p.head * a.head_pitch;
         // queries, as the A operand: rows g and g + 8
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                     a.stats[slot * kRows + row] = make_float2(m, l);
             }
         }
-        const Tail t = tail_of<kRows>(run, p);
+        const Tail t = tail_of<kRows, kCost>(run, p);
         if (t.per)
             tail = t;
         __syncthreads();   // before the queues are used again

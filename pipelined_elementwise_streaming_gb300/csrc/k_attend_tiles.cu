@@ -25,14 +25,14 @@
 //
 // Measured on GB300 as in the kernel for few rows; in parentheses the time of the
 // products at the 1897 TFLOP/s of cuBLAS.  bf16, chunks of 1024 tokens of two prompts of
-// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 257 us (192), 1.42 PFLOP/s; the
+// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 247 us (192), 1.47 PFLOP/s; the
 // products alone would take 150 of them at the tensor cores' 4096 multiply-adds a
 // cycle.  A ragged batch of 12 (1 to 300 new tokens, up to 3000 keys, f16, 10 heads over
-// 2 of 64): 33, most of it the start and end of pieces of five steps and their joins.
+// 2 of 64): 26, most of it the start and end of pieces of five steps and their joins.
 // Steps that led here, for the first of them: mma.m16n8k16 2316 us; tcgen05 from one
 // thread, cp.async loads 489; an elected lane 464; loads with few shuffles 371; four
 // threads to a row and boxes of pages 337; one thread to a row 287; short code for what
-// runs once 257.  What bounds a step now (2700 cycles for two tiles): a tile's chain of
+// runs once 257; a tile's start and end counted as work 247.  What bounds a step now (2700 cycles for two tiles): a tile's chain of
 // scores, weights and products, 1260 + 1024 cycles and the hand-overs between them.
 // The weights of half a step handed over early, waits that poll without a pause, and
 // weights taken before their maximum is known were no faster, or slower.
@@ -47,7 +47,11 @@ using namespace dev;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128;
 constexpr int kWeighers = 256, kLoaders = 64, kThreads = 384;
-constexpr int64_t kLeast = 2;        // steps to a CTA at least
+// What a tile costs beside its steps, in steps, and units to a CTA at least.  The
+// ragged batch above takes 34.0 us with a cost of 0, 28.4 with 2, 26.1 with 3, 27.2 with 4; the
+// large one 254, 250, 247, 247.
+constexpr int kCost = 3;
+constexpr int64_t kLeast = 4;
 constexpr int kMasks = 8;            // steps whose keys are remembered
 constexpr int kBlock = kKeys * 128;  // bytes of a block: 128 rows of 64 channels
 constexpr int kLag = 2;              // groups of loads in flight behind the last
@@ -267,7 +271,9 @@ __device__ __forceinline__ void boxes(const AttendArgs& a, Run run, unsigned cha
     Place<D> place;
     uint32_t count = 0;   // steps of all pieces
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        if (p.empty())
+            break;   // the run's last units, before a tile's first step
         const int first_limit = row_limit(a, p.seq, p.tile * kRows);
         const int limit = min(row_limit(a, p.seq, p.tile * kRows + p.rows - 1), p.seq.length);
         const int32_t* pages = a.paged.pages + p.b * a.paged.pages_pitch;
@@ -322,7 +328,9 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
     const int mine = threadIdx.x - (kLoadWarp + 1) * 32;
     uint32_t piece = 0, resets = 0, tile = 0, raw = 0;   // raw: a bit to each stage, the phase to wait for
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        if (p.empty())
+            break;   // the run's last units, before a tile's first step
         if (piece && !wait_warp(mem + S::kQEmpty, piece - 1))
             return;
         load_queries<D>(a, p, mem, mine / 32);
@@ -394,7 +402,9 @@ __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned ch
         waiting = 0;
     };
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        if (p.empty())
+            break;   // the run's last units, before a tile's first step
         if (piece && !wait_warp(mem + S::kQEmpty, piece - 1))
             return;
         load_queries<D>(a, p, mem, warp);
@@ -466,7 +476,9 @@ __device__ __forceinline__ void issuer(const AttendArgs& a, Run run, unsigned ch
         mma_commit(mem + S::kS + 8 * t);
     };
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        if (p.empty())
+            break;   // the run's last units, before a tile's first step
         const int tiles = p.rows > kHalf ? 2 : 1, steps = p.end - p.step;
         if (!wait_warp(mem + S::kQFull, piece) || !full(place))
             return;
@@ -566,7 +578,9 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
     uint32_t scored = 0, ended = 0, count = 0;   // count: steps of all pieces
     bool ok = true;
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys>(a, run);
+        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        if (p.empty())
+            break;   // the run's last units, before a tile's first step
         const int first = p.tile * kRows + t * kHalf;   // of the tile's rows
         const int all = row_limit(a, p.seq, first);     // keys that every row of the tile sees
         const bool live = t * kHalf + row < p.rows, busy = p.rows > t * kHalf;
@@ -707,7 +721,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
             atomicAdd(words + 1, 1);
         }
         count += p.end - p.step;
-        const Tail now = tail_of<kRows>(run, p);
+        const Tail now = tail_of<kRows, kCost>(run, p);
         if (now.per)
             *tail = now;
         advance<kRows>(a, run, p);
@@ -747,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(mem + S::kWords, 512);
     tcgen05_before();
     // also the barrier after the initialisation
-    const Run run = run_of<kRows, kKeys, kThreads>(a, kLeast, reinterpret_cast<int64_t*>(memory + S::kSums));
+    const Run run = run_of<kRows, kKeys, kCost, kThreads>(a, kLeast, reinterpret_cast<int64_t*>(memory + S::kSums));
     __syncthreads();
     tcgen05_after();
     const uint32_t tmem = static_cast<uint32_t>(words[0]);

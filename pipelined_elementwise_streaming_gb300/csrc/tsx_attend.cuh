@@ -2,10 +2,11 @@
 //
 // The queries of a sequence that read one head are rows, `group` to a token, cut
 // into tiles of M rows; a tile goes over the keys that its last row sees, TK at a
-// time.  One such step is a unit.  All units of a call stand in a row (by sequence,
-// head, tile, step), and each of a fixed number of CTAs takes an equal run of them:
-// lengths of sequences need not be known to the host, none of them leaves CTAs
-// without work, and single long ones are split.  A CTA whose run starts or ends
+// time.  One such step is a unit, and as many more before a tile's first step, COST,
+// stand for its start and end.  All units of a call stand in a row (by sequence, head,
+// tile, step), and each of a fixed number of CTAs takes an equal run of them: lengths
+// of sequences need not be known to the host, none of them leaves CTAs without work,
+// and single long ones are split.  A CTA whose run starts or ends
 // within a tile writes a part of that tile's result (the unnormalised sum, the
 // maximum and the sum of weights) to the scratch, and a second kernel joins the
 // parts in order.
@@ -127,19 +128,27 @@ __device__ __forceinline__ int64_t steps_before(const AttendArgs& a, const Seq& 
                                           M - 1 + static_cast<uint64_t>(a.group) * (s.prior + TK)));
 }
 
-template <int M, int TK>
-__device__ __forceinline__ int64_t steps_of_head(const AttendArgs& a, const Seq& s)
+// Units of the first n tiles, and of a head.
+template <int M, int TK, int COST>
+__device__ __forceinline__ int64_t units_before(const AttendArgs& a, const Seq& s, int n)
+{
+    return steps_before<M, TK>(a, s, n) + static_cast<int64_t>(n) * COST;
+}
+
+template <int M, int TK, int COST>
+__device__ __forceinline__ int64_t units_of_head(const AttendArgs& a, const Seq& s)
 {
     const int tiles = tiles_of<M>(a, s);
     if (tiles == 0)
         return 0;
-    return steps_of<M, TK>(a, s, tiles - 1) + (tiles > 1 ? steps_before<M, TK>(a, s, tiles - 1) : 0);
+    return COST + steps_of<M, TK>(a, s, tiles - 1) + (tiles > 1 ? units_before<M, TK, COST>(a, s, tiles - 1) : 0);
 }
 
 // A CTA's run of units, and where it starts.
 struct Run {
     int64_t from, to, per;   // units; per: of a CTA
-    int b, head, tile, step;
+    int b, head, tile;
+    int64_t off;             // units of the tile before `from`
 };
 
 __device__ __forceinline__ void share_out(Run& r, int64_t total, int64_t least)
@@ -159,32 +168,32 @@ __device__ __forceinline__ int64_t sum_upto(int64_t v, int lane)
     return v;
 }
 
-// The tile and step of unit `rest` of a head.
-template <int M, int TK>
+// The tile of unit `rest` of a head.
+template <int M, int TK, int COST>
 __device__ __forceinline__ void find_tile(const AttendArgs& a, const Seq& s, int64_t rest, Run& r)
 {
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = tiles_of<M>(a, s);   // steps_before(lo) <= rest < steps_before(hi)
+    int lo = 0, hi = tiles_of<M>(a, s);   // units_before(lo) <= rest < units_before(hi)
     int64_t before = 0;
 #pragma unroll 1
     while (hi - lo > 1) {   // 32 places looked at at once
         const int apart = (hi - lo + 32) / 33;
         const int64_t at = lo + static_cast<int64_t>(lane + 1) * apart;
-        const int64_t steps = at < hi ? steps_before<M, TK>(a, s, static_cast<int>(at)) : rest + 1;
-        const int under = __popc(__ballot_sync(0xffffffffu, steps <= rest));
+        const int64_t units = at < hi ? units_before<M, TK, COST>(a, s, static_cast<int>(at)) : rest + 1;
+        const int under = __popc(__ballot_sync(0xffffffffu, units <= rest));
         if (under)
-            before = __shfl_sync(0xffffffffu, steps, under - 1);
+            before = __shfl_sync(0xffffffffu, units, under - 1);
         lo += under * apart;
         hi = min(hi, lo + apart);
     }
     r.tile = lo;
-    r.step = static_cast<int>(rest - before);
+    r.off = rest - before;
 }
 
 // Every thread of the CTA takes part; `sums` holds a word to each warp and three
 // more.  Up to 32 sequences are a lane's each, in every warp alike; more of them are
 // shared out among all threads.
-template <int M, int TK, int THREADS>
+template <int M, int TK, int COST, int THREADS>
 __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_t* sums)
 {
     constexpr int kWarps = THREADS / 32;
@@ -196,7 +205,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
         head = 0;
         if (lane < a.paged.seqs) {
             s = seq_of(a, lane);
-            head = steps_of_head<M, TK>(a, s);
+            head = units_of_head<M, TK, COST>(a, s);
         }
         const int64_t mine = head * a.heads, upto = sum_upto(mine, lane);
         share_out(r, __shfl_sync(0xffffffffu, upto, 31), least);
@@ -213,7 +222,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
 #pragma unroll 1
             for (int base = 0; base < a.paged.seqs; base += THREADS) {
                 const int b = base + threadIdx.x;
-                head = b < a.paged.seqs ? steps_of_head<M, TK>(a, seq_of(a, b)) : 0;
+                head = b < a.paged.seqs ? units_of_head<M, TK, COST>(a, seq_of(a, b)) : 0;
                 const int64_t mine = head * a.heads;
                 int64_t upto = sum_upto(mine, lane), all = 0;
                 if (lane == 31)
@@ -248,18 +257,21 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, int64_t least, int64_
         head = sums[kWarps + 2];
     }
     r.head = static_cast<int>(quotient(rest, head));
-    find_tile<M, TK>(a, seq_of(a, r.b), rest - r.head * head, r);
+    find_tile<M, TK, COST>(a, seq_of(a, r.b), rest - r.head * head, r);
     return r;
 }
 
-// A part of a run within one tile: steps `step` .. end - 1 of `steps`.
+// A part of a run within one tile: steps `step` .. end - 1 of `steps`; none where the
+// run ends before the tile's first.
 struct Piece {
     Seq seq;
     int b, head, tile, step, end, steps, rows;
-    __device__ bool whole() const { return step == 0 && end == steps; }
+    int64_t units;
+    __device__ __forceinline__ bool whole() const { return step == 0 && end == steps; }
+    __device__ __forceinline__ bool empty() const { return end <= step; }
 };
 
-template <int M, int TK>
+template <int M, int TK, int COST>
 __device__ __forceinline__ Piece piece_of(const AttendArgs& a, const Run& r)
 {
     Piece p;
@@ -267,9 +279,10 @@ __device__ __forceinline__ Piece piece_of(const AttendArgs& a, const Run& r)
     p.b = r.b;
     p.head = r.head;
     p.tile = r.tile;
-    p.step = r.step;
     p.steps = steps_of<M, TK>(a, p.seq, r.tile);
-    p.end = static_cast<int>(min(static_cast<int64_t>(p.steps), r.step + (r.to - r.from)));
+    p.units = min(p.steps + COST - r.off, r.to - r.from);
+    p.step = static_cast<int>(max(r.off - COST, static_cast<int64_t>(0)));
+    p.end = static_cast<int>(max(r.off + p.units - COST, static_cast<int64_t>(0)));
     p.rows = min(p.seq.fresh * a.group - r.tile * M, M);
     return p;
 }
@@ -277,8 +290,8 @@ __device__ __forceinline__ Piece piece_of(const AttendArgs& a, const Run& r)
 template <int M>
 __device__ __forceinline__ void advance(const AttendArgs& a, Run& r, const Piece& p)
 {
-    r.from += p.end - p.step;
-    r.step = 0;
+    r.from += p.units;
+    r.off = 0;
     if (r.from >= r.to)
         return;
     if (++r.tile < tiles_of<M>(a, p.seq))
@@ -303,12 +316,12 @@ struct Tail {
 // Where the CTA's part of this piece goes, and what is to be joined.
 __device__ __forceinline__ int part_slot(const Piece& p) { return 2 * blockIdx.x + (p.step == 0 ? 1 : 0); }
 
-template <int M>
+template <int M, int COST>
 __device__ __forceinline__ Tail tail_of(const Run& r, const Piece& p)
 {
     Tail t{};
     if (p.step == 0 && p.end < p.steps) {
-        t.last = r.from + p.steps - 1;
+        t.last = r.from - r.off + COST + p.steps - 1;
         t.per = r.per;
         t.token = p.seq.first;
         t.row0 = p.tile * M;
