@@ -25,17 +25,19 @@
 //
 // Measured on GB300 as in the kernel for few rows; in parentheses the time of the
 // products at the 1897 TFLOP/s of cuBLAS.  bf16, chunks of 1024 tokens of two prompts of
-// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 247 us (192), 1.47 PFLOP/s; the
+// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 240 us (192), 1.51 PFLOP/s; the
 // products alone would take 150 of them at the tensor cores' 4096 multiply-adds a
 // cycle.  A ragged batch of 12 (1 to 300 new tokens, up to 3000 keys, f16, 10 heads over
 // 2 of 64): 26, most of it the start and end of pieces of five steps and their joins.
 // Steps that led here, for the first of them: mma.m16n8k16 2316 us; tcgen05 from one
 // thread, cp.async loads 489; an elected lane 464; loads with few shuffles 371; four
 // threads to a row and boxes of pages 337; one thread to a row 287; short code for what
-// runs once 257; a tile's start and end counted as work 247.  What bounds a step now (2700 cycles for two tiles): a tile's chain of
-// scores, weights and products, 1260 + 1024 cycles and the hand-overs between them.
-// The weights of half a step handed over early, waits that poll without a pause, and
-// weights taken before their maximum is known were no faster, or slower.
+// runs once 257; a tile's start and end counted as work 247; the weights of half a step
+// handed over while the others are computed 240.  What bounds a step now (2600 cycles
+// for two tiles): a tile's chain of scores, weights and products, 1260 + 1024 cycles
+// and the hand-overs between them.
+// Waits that poll without a pause, and weights taken before their maximum is known,
+// were slower.
 
 #include "tsx_attend.cuh"
 #include "tsx_tcgen05.cuh"
@@ -71,7 +73,7 @@ struct Shared {
                          kEnd = kStore + kWeighers / 32 * 4096;   // kStore: results on their way out
     // barriers
     static constexpr int kFull = kEnd, kEmpty = kFull + 8 * stages<D>(), kQFull = kEmpty + 8 * stages<D>(),
-                         kQEmpty = kQFull + 8, kS = kQEmpty + 8, kP = kS + 16, kO = kP + 16,
+                         kQEmpty = kQFull + 8, kS = kQEmpty + 8, kP = kS + 16, kO = kP + 32,
                          kReset = kO + 16, kDrain = kReset + 8, kRaw = kDrain + 8;
     static constexpr int kMask = (kRaw + 8 * stages<D>() + 15) / 16 * 16;                 // [kMasks][4] words
     static constexpr int kOdd = kMask + kMasks * 16;      // [3][D] first keys with a NaN, +inf, -inf
@@ -496,14 +498,16 @@ __device__ __forceinline__ void issuer(const AttendArgs& a, Run run, unsigned ch
             const bool more = i + 1 < steps;
             place.next();
             for (int t = 0; t < tiles; ++t) {
-                if (!wait_warp(mem + S::kP + 8 * t, weights[t]++))
-                    return;
-                tcgen05_after();
                 const uint32_t v = mem + S::kRing + values_at.stage * S::kTile;
 #pragma unroll
-                for (int k = 0; k < kKeys / 64; ++k)
+                for (int k = 0; k < kKeys / 64; ++k) {   // as the weights come, 64 keys at a time
+                    if (!wait_warp(mem + S::kP + 16 * t + 8 * k, weights[t]))
+                        return;
+                    tcgen05_after();
                     mma_tmem64(tmem + kRows + t * kHalf, tmem + t * kHalf + k * 32, operand(v + k * 8192, kBlock), values,
                                i > 0 || k > 0);
+                }
+                ++weights[t];
                 if (t == tiles - 1)
                     release(values_at);
                 if (!more) {
@@ -660,10 +664,10 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
                     w[i] = pack2<DT>(v.x, v.y);
                 }
                 tmem_store32(s_at + 32 * c, w);
+                tmem_wait_stores();
+                tcgen05_before();
+                mbar_arrive(mem + S::kP + 16 * t + 8 * c);
             }
-            tmem_wait_stores();
-            tcgen05_before();
-            mbar_arrive(mem + S::kP + 8 * t);
             const float2 both = __fadd2_rn(total[0], total[1]);
             sum += both.x + both.y;
         }
@@ -748,7 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(mem + S::kQEmpty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(mem + S::kS + 8 * t, 1);
-            mbar_init(mem + S::kP + 8 * t, kWeighers / 2);
+            mbar_init(mem + S::kP + 16 * t, kWeighers / 2);
+            mbar_init(mem + S::kP + 16 * t + 8, kWeighers / 2);
             mbar_init(mem + S::kO + 8 * t, 1);
         }
         mbar_init(mem + S::kReset, kLoaders);
