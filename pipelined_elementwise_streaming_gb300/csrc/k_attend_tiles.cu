@@ -78,7 +78,7 @@ struct Shared {
     static constexpr int kMask = (kRaw + 8 * stages<D>() + 15) / 16 * 16;                 // [kMasks][4] words
     static constexpr int kOdd = kMask + kMasks * 16;      // [3][D] first keys with a NaN, +inf, -inf
     static constexpr int kSums = kOdd + 3 * D * 4;        // words of run_of
-    static constexpr int kWords = kSums + (kThreads / 32 + 3) * 8;   // tensor memory, pieces done, odd values met
+    static constexpr int kWords = kSums + (kThreads / 32 + 3) * 8;   // tensor memory, first tiles done, odd values met, second tiles done
     static constexpr int kBytes = kWords + 16;
 };
 
@@ -176,16 +176,22 @@ __device__ __forceinline__ void look_through(unsigned char* memory, unsigned cha
 }
 
 // Before the first such values of a piece: nothing has been taken out.  False if
-// the last piece's rows have not used what was.
+// the last piece's rows have not used what was: every piece before has a first
+// tile, `seconds` of them a second one, and the warps of a tile count for themselves
+// (those of a second tile that is not there run ahead, and must not stand in for
+// the first's).
 template <int D>
-__device__ __forceinline__ bool forget(unsigned char* memory, uint32_t piece, uint32_t resets, int mine)
+__device__ __forceinline__ bool forget(unsigned char* memory, uint32_t piece, uint32_t seconds, uint32_t resets,
+                                       int mine)
 {
     using S = Shared<D>;
-    volatile int* done = reinterpret_cast<int*>(memory + S::kWords) + 1;
+    constexpr int kTileWarps = kHalf / 32;
+    const volatile int* words = reinterpret_cast<const int*>(memory + S::kWords);
     int* odd = reinterpret_cast<int*>(memory + S::kOdd);
     if (piece) {
         const uint64_t since = globaltimer_ns();
-        while (!__all_sync(0xffffffffu, *done >= static_cast<int>(kWeighers / 32 * piece)))
+        while (!__all_sync(0xffffffffu, words[1] >= static_cast<int>(kTileWarps * piece) &&
+                                            words[3] >= static_cast<int>(kTileWarps * seconds)))
             if (__any_sync(0xffffffffu, globaltimer_ns() - since > kPatience))
                 return false;
         __threadfence_block();
@@ -328,7 +334,7 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
     using S = Shared<D>;
     const uint32_t mem = smem_addr(memory);
     const int mine = threadIdx.x - (kLoadWarp + 1) * 32;
-    uint32_t piece = 0, resets = 0, tile = 0, raw = 0;   // raw: a bit to each stage, the phase to wait for
+    uint32_t piece = 0, seconds = 0, resets = 0, tile = 0, raw = 0;   // raw: a bit to each stage, the phase to wait for
     while (run.from < run.to) {
         const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
         if (p.empty())
@@ -344,7 +350,7 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
         const int limit = min(row_limit(a, p.seq, p.tile * kRows + p.rows - 1), p.seq.length);
         bool fresh = true;
         for (int step = max(p.step, first_limit / kKeys); step < p.end; ++step) {   // base + kKeys > first_limit
-            if (fresh && !forget<D>(memory, piece, resets++, mine))
+            if (fresh && !forget<D>(memory, piece, seconds, resets++, mine))
                 return;
             fresh = false;
             const int stage = (tile + 2 * (step - p.step) + 1) % stages<D>(), base = step * kKeys;
@@ -363,6 +369,7 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
         }
         tile += 2 * (p.end - p.step);
         ++piece;
+        seconds += p.rows > kHalf;
         advance<kRows>(a, run, p);
     }
 }
@@ -374,7 +381,7 @@ __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned ch
     using S = Shared<D>;
     const uint32_t mem = smem_addr(memory);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 1, mine = threadIdx.x % kLoaders;
-    uint32_t piece = 0, resets = 0, count = 0;   // count: steps of all pieces
+    uint32_t piece = 0, seconds = 0, resets = 0, count = 0;   // count: steps of all pieces
     Place<D> place;
     Landing pending[kLag];
     int waiting = 0;   // of `pending`
@@ -441,7 +448,7 @@ __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned ch
                 const bool check = kv == 1 && base + kKeys > first_limit;
                 if (check && fresh) {   // the last piece's have been used
                     fresh = false;
-                    if (!forget<D>(memory, piece, resets++, mine))
+                    if (!forget<D>(memory, piece, seconds, resets++, mine))
                         return;
                 }
                 const int stage = S::kRing + place.stage * S::kTile;
@@ -453,6 +460,7 @@ __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned ch
         }
         flush();
         ++piece;
+        seconds += p.rows > kHalf;
         advance<kRows>(a, run, p);
     }
 }
@@ -720,9 +728,9 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
             tcgen05_before();
         }
         __syncwarp();
-        if (threadIdx.x % 32 == 0) {
+        if (busy && threadIdx.x % 32 == 0) {   // what has been taken out is used
             __threadfence_block();
-            atomicAdd(words + 1, 1);
+            atomicAdd(words + 1 + 2 * t, 1);
         }
         count += p.end - p.step;
         const Tail now = tail_of<kRows, kCost>(run, p);
@@ -758,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(mem + S::kReset, kLoaders);
         mbar_init(mem + S::kDrain, 1);
-        words[1] = words[2] = 0;
+        words[1] = words[2] = words[3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     let_next_start();
