@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kRotaryThreads, backward_ctas(DT))
             team_sums(sums2, a.team);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float rstd = rsqrtf(sums2[2 * i] * a.by_dim + a.eps);
+                // 0 where there is no head: with an eps of 0 the root of its zeros is infinite, and its sums NaN
+                const float rstd = i < left ? rsqrtf(sums2[2 * i] * a.by_dim + a.eps) : 0.f;
                 const float2 f = pair_of(rstd), m = pair_of(-(sums2[2 * i + 1] * rstd) * a.by_dim);
                 float2 xu[2], xv[2];
                 x.u[i].floats(xu);
