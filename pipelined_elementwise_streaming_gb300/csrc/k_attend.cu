@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
     int64_t* sums = reinterpret_cast<int64_t*>(memory + queue_bytes<D>() + kStatsBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, c2 = lane % 4 * 2;
     constexpr int kStages = stages<D>();
+    constexpr float kLift = lift<DT, 0>();
     const uint32_t queue = smem_addr(memory) + warp * (kStages * stage_bytes<D>());
     let_next_start();
     Run run = run_of<kRows, kKeys, kCost, kThreads>(a, kLeast, sums);
@@ -234,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 float f[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {   // no score yet: nothing to scale
-                    f[r] = top[r] == -INFINITY ? 1.f : exp2_fast(top[r] - most[r]);
+                    f[r] = top[r] == -INFINITY ? 1.f
+                                               : exp2_fast(reference(top[r], kLift) - reference(most[r], kLift));
                     top[r] = most[r];
                     sum[r] *= f[r];
                 }
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[j][e] = exp2_fast(s[j][e] - (top[e >> 1] == -INFINITY ? 0.f : top[e >> 1]));
+                    s[j][e] = exp2_fast(s[j][e] - (top[e >> 1] == -INFINITY ? 0.f : reference(top[e >> 1], kLift)));
                     sum[e >> 1] += s[j][e];
                 }
             const uint32_t w[4] = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]), pack2<DT>(s[1][0], s[1][1]),
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
             if (lane % 4 == 0)
-                stats[warp][g + 8 * r] = make_float2(top[r], sum[r]);
+                stats[warp][g + 8 * r] = make_float2(reference(top[r], kLift), sum[r]);
         }
         __syncthreads();   // also: the queues are empty, and their memory free
         float* joined = reinterpret_cast<float*>(memory);   // [4][kRows][D]

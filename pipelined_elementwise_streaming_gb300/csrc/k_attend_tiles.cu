@@ -19,7 +19,8 @@
 //
 // The running maximum is not followed closely: O and the sum are scaled only when
 // a row's maximum has grown by more than 2^8 over the one in use, which is rare
-// after the first steps; weights are then up to 2^8, with the same relative error.
+// after the first steps; weights are then up to 2^8 (2^15 in fp16, where they are
+// taken 2^7 larger), with the same relative error.
 //
 // Every wait gives up after kPatience; then the CTA's remaining rows become NaN.
 //
@@ -585,6 +586,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
     const int t = threadIdx.x / kHalf, row = threadIdx.x % kHalf;   // of the tile
     const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
     const uint32_t s_at = tmem + t * kHalf + lanes, o_at = tmem + kRows + t * kHalf + lanes;
+    constexpr float kLift = lift<DT, int(kGrowth)>();
     const int* odd = reinterpret_cast<const int*>(memory + S::kOdd);
     int* words = reinterpret_cast<int*>(memory + S::kWords);
     uint32_t scored = 0, ended = 0, count = 0;   // count: steps of all pieces
@@ -597,7 +599,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
         const int all = row_limit(a, p.seq, first);     // keys that every row of the tile sees
         const bool live = t * kHalf + row < p.rows, busy = p.rows > t * kHalf;
         const int limit = live ? row_limit(a, p.seq, first + row) : 0;
-        float top = -INFINITY, sum = 0.f;
+        float top = -INFINITY, sum = 0.f;   // the weights' reference, and their sum
         for (int step = p.step; busy && ok && step < p.end; ++step) {
             ok = wait_warp(mem + S::kS + 8 * t, scored);
             if (!ok)
@@ -639,10 +641,10 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
             for (int j = 0; j < 4; ++j)
                 m[j] = fmaxf(m[j], __uint_as_float(s[kKeys - 4 + j]));
             const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale_log2;
-            const bool grows = now > top + kGrowth || (top == -INFINITY && now > top);
+            const bool grows = now - top > kGrowth + kLift;   // not where both are infinite
             if (__any_sync(0xffffffffu, grows)) {
-                const float f = grows && top != -INFINITY ? exp2_fast(top - now) : 1.f;
-                top = grows ? now : top;
+                const float next = reference(now, kLift), f = grows && top != -INFINITY ? exp2_fast(top - next) : 1.f;
+                top = grows ? next : top;
                 sum *= f;
                 if (step > p.step && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1

@@ -338,6 +338,16 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Weights are exp2(score - reference), the reference 2^kLift under the maximum that is
+// in use: fp16 has no normal numbers under 2^-14, and of a row whose first key leads
+// all others by 2^25 nothing but that key would be left in the product with v (a lead of
+// 2^24.5 over 16384 keys took a fifth of the result).  MOST: weights are 2^MOST at most
+// relative to the maximum, and 2^15 in all.  bf16 has the exponents of fp32.
+template <int DT, int MOST>
+TSX_HD constexpr float lift() { return DT == TSX_F16 ? 15 - MOST : 0; }
+// Rounded up, so that no weight is larger.
+__device__ __forceinline__ float reference(float top, float under) { return __fsub_ru(top, under); }
+
 // Row `row` of a sequence's rows of a head: element of q or out.
 __device__ __forceinline__ int64_t row_at(const AttendArgs& a, int first, int head, int row, int64_t pitch,
                                           int64_t head_pitch)
