@@ -174,7 +174,7 @@ int tsx_paged_attention_workspace(const tsx_cache *cache, int64_t tokens, int q_
  *   most_new   the most new tokens that a sequence has, as far as the caller
  *              knows (tokens, if not).  It chooses between kernels, and any
  *              value gives right results
- *   scale      finite; 1 / sqrt(dim) as a rule
+ *   scale      1 / sqrt(dim) as a rule; up to 2^127, of either sign, or 0
  *   lse        [tokens, q_heads] fp32, or NULL: log of the sum of exp(scale q
  *              k^T), by which parts over different keys can be joined
  * fp16 and bf16 (TSX_ERR_UNSUPPORTED for fp32), dim a multiple of 8, pitches

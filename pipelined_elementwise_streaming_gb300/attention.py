@@ -28,7 +28,6 @@ belong to the caller, who keeps them alive until that stream's work is done.
 from __future__ import annotations
 
 import ctypes
-import math
 from typing import NamedTuple
 
 from . import DTYPES, lib
@@ -299,8 +298,8 @@ class PagedAttention(_Heads):
         if self.k_heads < 1 or self.q_heads < 1 or self.q_heads % self.k_heads:
             _invalid("q_heads must be a multiple of kv_heads, and both above 0")
         self.scale = self.dim ** -0.5 if scale is None else float(scale)
-        if not math.isfinite(self.scale):
-            _invalid("scale must be finite")
+        if not abs(self.scale) <= 2.0**127:
+            _invalid("scale must be finite, 2^127 at most")
         self._scratch = {}
         if rotary is None:
             self._rope = Rotary(dtype, q_heads, kv_heads, dim, rot=0)

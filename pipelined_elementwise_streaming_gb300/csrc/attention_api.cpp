@@ -652,8 +652,8 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
         rc = check_batch(call, batch);
     if (rc != TSX_OK)
         return rc;
-    if (!std::isfinite(scale))
-        return fail(TSX_ERR_INVALID, call, "scale must be finite");
+    if (!(std::fabs(scale) <= 0x1p127f))   // scale / ln 2 is an fp32 number too
+        return fail(TSX_ERR_INVALID, call, "scale must be finite, 2^127 at most");
     if (cache->dtype == TSX_F32)
         return fail(TSX_ERR_UNSUPPORTED, call, "fp32 is not supported: fp16 and bf16 are");
     if (cache->dim % 8)
@@ -699,9 +699,10 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!many)
         return launched(launch_attend_few(cache->dtype, a, st), call);
-    // a positive scale, so that the largest score is the largest product; not 0, which -infinity must not meet
+    // a positive scale, so that the largest score is the largest product; not 0, which -infinity must not meet: with
+    // the least number above it the largest product's score is 2^-21
     a.negated = a.scale_log2 < 0;
-    a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
+    a.scale_log2 = std::max(std::fabs(a.scale_log2), 0x1p-149f);
     CUtensorMap maps[2];
     const bool boxes = box_pages(*cache);
     if (boxes) {
