@@ -59,6 +59,9 @@ constexpr int kMasks = 8;            // steps whose keys are remembered
 constexpr int kBlock = kKeys * 128;  // bytes of a block: 128 rows of 64 channels
 constexpr int kLag = 2;              // groups of loads in flight behind the last
 constexpr float kGrowth = 8.f;
+// Scores (times 1 / ln 2) from which on half a step of fp32, 2^-4, is too much between a
+// rounded score, which the reference is, and the exact one of an fma.
+constexpr float kFar = 0x1p20f;
 constexpr uint64_t kPatience = 4000000000ull;   // ns
 constexpr int kLoadWarp = kWeighers / 32, kIssueWarp = kLoadWarp + 3;
 
@@ -600,6 +603,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
         const bool live = t * kHalf + row < p.rows, busy = p.rows > t * kHalf;
         const int limit = live ? row_limit(a, p.seq, first + row) : 0;
         float top = -INFINITY, sum = 0.f;   // the weights' reference, and their sum
+        bool far = false;                   // the reference is beyond kFar
         for (int step = p.step; busy && ok && step < p.end; ++step) {
             ok = wait_warp(mem + S::kS + 8 * t, scored);
             if (!ok)
@@ -642,9 +646,11 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
                 m[j] = fmaxf(m[j], __uint_as_float(s[kKeys - 4 + j]));
             const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale_log2;
             const bool grows = now - top > kGrowth + kLift;   // not where both are infinite
-            if (__any_sync(0xffffffffu, grows)) {
+            float scale = a.scale_log2;
+            if (__any_sync(0xffffffffu, grows || far)) {
                 const float next = reference(now, kLift), f = grows && top != -INFINITY ? exp2_fast(top - next) : 1.f;
                 top = grows ? next : top;
+                far = fabsf(top) > kFar && top != -INFINITY;
                 sum *= f;
                 if (step > p.step && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -658,8 +664,15 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
                         tmem_store16(o_at + c, o);
                     }
                 }
+                if (__any_sync(0xffffffffu, far)) {   // rounded as the maximum is, that their differences are exact
+                    asm volatile("" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        s[i] = __float_as_uint(__uint_as_float(s[i]) * scale);
+                    scale = 1.f;
+                }
             }
-            const float2 by = pair_of(a.scale_log2), less = pair_of(top == -INFINITY ? 0.f : -top);
+            const float2 by = pair_of(scale), less = pair_of(top == -INFINITY ? 0.f : -top);
             float2 total[2] = {pair_of(0.f), pair_of(0.f)};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
