@@ -186,7 +186,9 @@ int tsx_paged_attention_workspace(const tsx_cache *cache, int64_t tokens, int q_
  * tokens, the rest of the last page, pages that hold nothing) has no effect on
  * it, also where it is NaN or infinite.  A token that sees no key, or whose
  * scores are all -infinity, gets zeros and the lse -infinity.  out may be
- * exactly q. */
+ * exactly q.  Blocks that wait give up after four seconds in which nothing of
+ * their work has moved (no input brings that about, a GPU taken away for so long
+ * may): the rows that they have left, and their lse, become NaN. */
 int tsx_paged_attention(const tsx_cache *cache, const tsx_batch *batch, int64_t tokens, int q_heads, int64_t most_new,
                         float scale, const tsx_heads *q, const tsx_heads *out, float *lse, void *workspace,
                         size_t workspace_bytes, tsx_stream_t stream);

@@ -22,7 +22,9 @@
 // after the first steps; weights are then up to 2^8 (2^15 in fp16, where they are
 // taken 2^7 larger), with the same relative error.
 //
-// Every wait gives up after kPatience; then the CTA's remaining rows become NaN.
+// Every wait gives up after kPatience; then the CTA's remaining rows become NaN.  Waits
+// that may be for a whole piece (of the queries' warps) or several (of a second tile's,
+// for a piece that has one) go on for as long as steps are brought.
 //
 // Measured on GB300 as in the kernel for few rows; in parentheses the time of the
 // products at the 1897 TFLOP/s of cuBLAS.  bf16, chunks of 1024 tokens of two prompts of
@@ -83,14 +85,58 @@ struct Shared {
     static constexpr int kOdd = kMask + kMasks * 16;      // [3][D] first keys with a NaN, +inf, -inf
     static constexpr int kSums = kOdd + 3 * D * 4;        // words of run_of
     static constexpr int kWords = kSums + (kThreads / 32 + 3) * 8;   // tensor memory, first tiles done, odd values met, second tiles done
-    static constexpr int kBytes = kWords + 16;
+    static constexpr int kBrought = kWords + 16;          // steps of which loads have been issued
+    static constexpr int kBytes = kBrought + 16;
 };
+
+// False once nothing has been brought since the last time that this was asked.
+template <int D>
+__device__ __forceinline__ bool goes_on(uint32_t mem, uint32_t& seen)
+{
+    const uint32_t before = seen;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(seen) : "r"(mem + Shared<D>::kBrought) : "memory");
+    return seen != before;
+}
+template <int D>
+__device__ __forceinline__ void brought(uint32_t mem, uint32_t steps)
+{
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(mem + Shared<D>::kBrought), "r"(steps) : "memory");
+}
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase) { return mbar_wait(bar, phase & 1, kPatience); }
 // The same answer for all threads of the warp.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase)
 {
     return __all_sync(0xffffffffu, wait(bar, phase));
+}
+// Where the wait may be for more than the ring's steps: for as long as steps are brought.
+// Two forms of it, the first where a step's time shows (the large chunk above takes 240.7
+// us, 239.5 with no such wait, 242.6 with the first form in both places, 247 and 259 with
+// either in every wait).
+template <int D>
+__device__ __forceinline__ bool wait_on(uint32_t mem, int bar, uint32_t phase)
+{
+    bool done = true;
+    if (!mbar_try_wait(mem + bar, phase & 1)) {
+        uint64_t since = globaltimer_ns();
+        uint32_t seen = ~0u;
+#pragma unroll 1
+        while (done && !mbar_try_wait(mem + bar, phase & 1))
+            if (globaltimer_ns() - since > kPatience) {
+                done = goes_on<D>(mem, seen);
+                since = globaltimer_ns();
+            }
+    }
+    return __all_sync(0xffffffffu, done);
+}
+template <int D>
+__device__ __forceinline__ bool wait_long(uint32_t mem, int bar, uint32_t phase)
+{
+    uint32_t seen = ~0u;
+    while (!wait_warp(mem + bar, phase))
+        if (!__all_sync(0xffffffffu, goes_on<D>(mem, seen)))
+            return false;
+    return true;
 }
 
 // w's two values times 0, and sum.
@@ -306,8 +352,10 @@ __device__ __forceinline__ void boxes(const AttendArgs& a, Run run, unsigned cha
                 }
                 seen = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (lane == 0)   // the step that had this place is long over: its values' stage has been used again
+            if (lane == 0) {   // the step that had this place is long over: its values' stage has been used again
                 *reinterpret_cast<uint4*>(memory + S::kMask + count % kMasks * 16) = seen;
+                brought<D>(mem, count);
+            }
             position += kKeys;
             page = position < limit ? pages[page_of(a.paged, position)] : -1;   // a step ahead
 #pragma unroll
@@ -343,7 +391,7 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
         const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
         if (p.empty())
             break;   // the run's last units, before a tile's first step
-        if (piece && !wait_warp(mem + S::kQEmpty, piece - 1))
+        if (piece && !wait_long<D>(mem, S::kQEmpty, piece - 1))
             return;
         load_queries<D>(a, p, mem, mine / 32);
         cp_async_commit();
@@ -358,7 +406,7 @@ __device__ __forceinline__ void helper(const AttendArgs& a, Run run, unsigned ch
                 return;
             fresh = false;
             const int stage = (tile + 2 * (step - p.step) + 1) % stages<D>(), base = step * kKeys;
-            if (!wait_warp(mem + S::kRaw + 8 * stage, raw >> stage))
+            if (!wait_long<D>(mem, S::kRaw + 8 * stage, raw >> stage))
                 return;
             raw ^= 1u << stage;
             unsigned char* values = memory + S::kRing + stage * S::kTile;
@@ -444,6 +492,8 @@ __device__ __forceinline__ void loader(const AttendArgs& a, Run run, unsigned ch
                 page[g] = here + kKeys < limit ? pages[page_of(a.paged, here + kKeys)] : -1;   // a step ahead
             }
             position += kKeys;
+            if (mine == 0)
+                brought<D>(mem, count);
             const int base = step * kKeys;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, place.next()) {
@@ -605,7 +655,7 @@ __device__ __forceinline__ void weigher(const AttendArgs& a, Run run, unsigned c
         float top = -INFINITY, sum = 0.f;   // the weights' reference, and their sum
         bool far = false;                   // the reference is beyond kFar
         for (int step = p.step; busy && ok && step < p.end; ++step) {
-            ok = wait_warp(mem + S::kS + 8 * t, scored);
+            ok = wait_on<D>(mem, S::kS + 8 * t, scored);
             if (!ok)
                 break;
             ++scored;
@@ -782,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(mem + S::kReset, kLoaders);
         mbar_init(mem + S::kDrain, 1);
         words[1] = words[2] = words[3] = 0;
+        brought<D>(mem, 0);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     let_next_start();
