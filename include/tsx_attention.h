@@ -60,10 +60,11 @@ typedef enum { TSX_ROPE_PLAIN = 0, TSX_ROPE_LINEAR = 1, TSX_ROPE_NTK = 2, TSX_RO
 int tsx_rotary_frequencies(int rot, double base, tsx_rope_scaling scaling, double factor, double length, double fast,
                            double slow, double *frequencies, float *amplitude);
 
-/* Any finite frequencies [pairs] (radians to a position) as tsx_rotary_desc
- * takes them: the part of a turn that a position adds, in units of 2^-64.  The
- * angle of position p is p times that, modulo 2^64: exact whatever p.  Host
- * only. */
+/* Frequencies [pairs] (radians to a position, of either sign, 2^30 at most) as
+ * tsx_rotary_desc takes them: the part of a turn that a position adds, to two
+ * units of 2^-64.  The angle of position p is p times that, modulo 2^64, and so
+ * within |p| 2^-63 of a turn: 2^-32 for positions of 32 bits, more beyond them
+ * (2^-13 at 2^50).  Host only. */
 int tsx_rotary_turns(int pairs, const double *frequencies, uint64_t *turns);
 
 #define TSX_ROPE_PAIRS 128
@@ -95,9 +96,10 @@ typedef struct tsx_rotary_desc {
  * overlap is undefined.  Vectors are used where dim and rot are
  * multiples of 8, the pitches of 16 bytes, and the pointers aligned to 16; any other layout works element by element.
  *
- * Angles have an error of 2^-32 of a turn and that of fp32 sines: under 2^-22
- * for fp32 tensors, and for 16-bit ones, which take the hardware's approximate
- * sine and cosine, under 2^-19 (both absolute).  tokens 0: nothing is done. */
+ * Angles have the error that tsx_rotary_turns names and 2^-32 of a turn.  With
+ * positions of 32 bits that and the error of fp32 sines is under 2^-22 for fp32
+ * tensors, and for 16-bit ones, which take the hardware's approximate sine and
+ * cosine, under 2^-19 (both absolute).  tokens 0: nothing is done. */
 int tsx_rotary(const tsx_rotary_desc *desc, int64_t tokens, const void *positions, int position_bytes,
                const tsx_heads *q, const tsx_heads *k, const void *q_weight, const void *k_weight,
                const tsx_heads *q_out, const tsx_heads *k_out, tsx_stream_t stream);
