@@ -10,12 +10,12 @@
 // and keeps them: two quads that hold four whole pairs, so that a rotation needs no
 // other thread and a norm a few shuffles within the team of threads of a head.  It
 // computes its four sines and cosines once for a token and uses them for the several
-// heads that it goes over, the next of them on their way while it works on some.
-// Sixteen channels to a thread, one batch of heads at a time, took 35 us where this
-// takes 27 (see below), for want of warps: 112 registers a thread in place of 58 to 73.  A table of them would be read instead: 4 bytes
-// to a channel and token, as much as two 16-bit heads.  Angles are whole numbers:
-// the position times the part of a turn that a position adds, modulo 2^64.
-
+// heads that it goes over, the next of them on their way while it works on some.  A
+// table of sines and cosines would be read instead: 4 bytes to a channel and token, as
+// much as two 16-bit heads.  Angles are whole numbers: the position times the part of
+// a turn that a position adds, modulo 2^64.  Sixteen channels to a thread, one batch of
+// heads at a time, took 35 us where this takes 27 (see below), for want of warps: 112
+// registers a thread in place of 58 to 73.
 //
 // Measured on GB300, GPU time of a call in a CUDA graph over tensors that take turns;
 // in parentheses the time of the bytes at the 6791 GB/s of a copy.  bf16 [8192, 32 + 8
