@@ -1,4 +1,5 @@
-"""Gradients of head norms on a GPU where rows of threads have no head to work on."""
+"""Gradients of head norms on a GPU where threads have no head to work on, and of
+very many tokens."""
 
 import numpy as np
 import pytest
@@ -44,3 +45,41 @@ def test_gradients_without_eps(tsx, dtype, tokens, hq, hk, dim, rot):
         near(grads[i], dx, HALF_STEP[dtype] * np.abs(dx) * (1 + 2**-8) + 4 * k * terms + LEAST[dtype], f"backward {i}")
         total = (size * np.abs(hat)).sum((0, 1))
         near(grads[2 + i], dw, (2 * k + (tokens * h + 40) * 2.0**-24) * total + 1e-30, f"dweight {i}")
+
+
+def weight_gradient64(f, dy, x, pos):
+    """(the weight's gradient, the sum of magnitudes that its roundings are relative
+    to) in 64 bits on the device, of heads in halves with an rms norm."""
+    freq = torch.tensor(f.frequencies, dtype=torch.float64, device="cuda")
+    dw, total = (torch.zeros(x.shape[-1], dtype=torch.float64, device="cuda") for _ in range(2))
+    for at in range(0, len(x), 1 << 14):
+        part = slice(at, at + (1 << 14))
+        angle = pos[part].double()[:, None, None] * freq
+        d, h = dy[part].double(), x[part].double()
+        hat = h * (h.square().mean(-1, keepdim=True) + f.eps).rsqrt()
+        a, b = d.chunk(2, -1)
+        c, s = angle.cos(), angle.sin()
+        back = torch.cat([a * c + b * s, b * c - a * s], -1)
+        reach = (a.abs() + b.abs()).repeat(1, 1, 2)
+        dw += (back * hat).sum((0, 1))
+        total += (reach * hat.abs()).sum((0, 1))
+    return dw, total
+
+
+@pytest.mark.parametrize("dtype,dim,heads", [("bf16", 8, 1), ("f16", 128, 3), ("f32", 20, 2), ("f32", 64, 5)])
+def test_weights_gradients_of_very_many_tokens(tsx, dtype, dim, heads):
+    """300001 tokens, each block staying for many rounds of them; all terms of the
+    sum have one sign, so that a round left out or taken twice shows."""
+    n = 300001
+    f = tsx.Rotary(dtype, heads, 0, dim, norm="rms")
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    x = torch.randn(n, heads, dim, generator=gen, device="cuda").to(_gpu.TORCH_DTYPE[dtype])
+    w = 0.5 + torch.rand(dim, generator=gen, device="cuda")
+    pos = torch.randint(1 << 20, (n,), generator=gen, device="cuda")
+    y, _ = f.forward(x, None, pos, w)
+    _, _, dw, _ = f.backward(y, None, pos, x, None, w)
+    want, total = weight_gradient64(f, y, x, pos)
+    assert (want > 0.4 * n * heads).all()
+    # A thread adds 200 heads at most (900003 over 304 blocks of 16 teams, 600002 over 456 of 8 warps), then lanes,
+    # warps and blocks 64 sums more; each term as in the tests of few tokens
+    assert ((dw.double() - want).abs() <= (2 * TURNED[dtype] + 264 * 2.0**-24) * total).all()
