@@ -184,7 +184,8 @@ int tsx_paged_attention_workspace(const tsx_cache *cache, int64_t tokens, int q_
  *
  * Scores, maxima and sums are fp32; the weights exp(score - maximum) are
  * rounded into the element type for the product with v (their sum is that of
- * the unrounded ones).  What lies in slots that a token does not see (later
+ * the unrounded ones), or where most_new * q_heads / heads is 8 at most, into
+ * two numbers of that type, which lose 2^-16 (bf16) or 2^-22 of a weight.  What lies in slots that a token does not see (later
  * tokens, the rest of the last page, pages that hold nothing) has no effect on
  * it, also where it is NaN or infinite.  A token that sees no key, or whose
  * scores are all -infinity, gets zeros and the lse -infinity.  out may be

@@ -88,12 +88,12 @@ struct AttendArgs {
     float2* stats;
     dev::Tail* tails;
 };
-int attend_few_rows();
+// Few rows to a head, any dim: tiles of 8 or of 16 `rows`.
 int attend_few_ctas(int dim);
 // Many rows to a head, dim up to 128: one CTA to an SM.
 int attend_many_rows();
 // maps: of keys and values in boxes of 64 channels and min(page, 128) slots, or NULL.
 cudaError_t launch_attend_many(int dtype, const AttendArgs& a, const CUtensorMap* maps, cudaStream_t st);
-cudaError_t launch_attend_few(int dtype, const AttendArgs& a, cudaStream_t st);
+cudaError_t launch_attend_few(int dtype, const AttendArgs& a, int rows, cudaStream_t st);
 
 }  // namespace tsx

@@ -602,16 +602,14 @@ struct Parts {
     size_t bytes() const { return sums() + stats() + size_t(ctas) * 32; }
 };
 
-// Whether a call takes the kernel for many rows to a head.
-bool many_rows(int dim, int64_t most_new, int group)
-{
-    return dim <= 128 && most_new * group > attend_few_rows();
-}
-
-Parts parts_of(int dim, bool many)
+// By rows to a head: tiles of 8 or 16 for as many, and of many for more in heads of up to
+// 128 channels.
+Parts parts_of(int dim, int64_t most_new, int group)
 {
     const int padded = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-    return many ? Parts{attend_many_rows(), 152, padded} : Parts{attend_few_rows(), attend_few_ctas(dim), padded};
+    if (dim <= 128 && most_new * group > 16)
+        return Parts{attend_many_rows(), 152, padded};
+    return Parts{most_new * group > 8 ? 16 : 8, attend_few_ctas(dim), padded};
 }
 
 int check_attention(const char* call, const tsx_cache* cache, int64_t tokens, int q_heads, int64_t most_new)
@@ -637,7 +635,7 @@ extern "C" int tsx_paged_attention_workspace(const tsx_cache* cache, int64_t tok
         return rc;
     if (!bytes)
         return fail(TSX_ERR_INVALID, call, "bytes is NULL");
-    *bytes = parts_of(cache->dim, many_rows(cache->dim, most_new, q_heads / cache->heads)).bytes();
+    *bytes = parts_of(cache->dim, most_new, q_heads / cache->heads).bytes();
     set_last_error("");
     return TSX_OK;
 }
@@ -668,8 +666,7 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     if (!cache_vectors(*cache) || !vectors(q, tokens, q_heads, 2) || !vectors(out, tokens, q_heads, 2) ||
         !aligned(lse, 4) || !aligned(workspace, 16))
         return fail(TSX_ERR_ALIGN, call, "pitches must be multiples of 8 elements and pointers of 16 bytes");
-    const bool many = many_rows(cache->dim, most_new, q_heads / cache->heads);
-    const Parts parts = parts_of(cache->dim, many);
+    const Parts parts = parts_of(cache->dim, most_new, q_heads / cache->heads);
     if (!workspace || workspace_bytes < parts.bytes())
         return fail(TSX_ERR_INVALID, call, "the workspace is smaller than tsx_paged_attention_workspace says");
     AttendArgs a{};
@@ -697,8 +694,8 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     a.stats = reinterpret_cast<float2*>(scratch + parts.sums());
     a.tails = reinterpret_cast<dev::Tail*>(scratch + parts.sums() + parts.stats());
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!many)
-        return launched(launch_attend_few(cache->dtype, a, st), call);
+    if (parts.rows != attend_many_rows())
+        return launched(launch_attend_few(cache->dtype, a, parts.rows, st), call);
     // a positive scale, so that the largest score is the largest product; not 0, which -infinity must not meet: with
     // the least number above it the largest product's score is 2^-21
     a.negated = a.scale_log2 < 0;

@@ -11,6 +11,15 @@
 // product with v.  Running maxima and sums are the warp's own; they and the four
 // sums of values are joined once at the end of a piece.
 //
+// In the product with v a weight rounded into the element type loses up to 2^-8 (bf16)
+// or 2^-11 of itself, which shows beside the result's own rounding (relative to the
+// result's norm 2.0e-3 in place of 1.66e-3 for bf16).  So tiles are of 8 rows where no
+// head has more: the other 8 rows of the instruction then take what rounding has left
+// of the weights, and 2^-16 or 2^-22 is lost, with the same instructions.  The two sums
+// are added at the end of a piece.  9 to 16 rows fill the instruction, and rests in a
+// second product took 2 to 8 % longer and made infinite values NaN: weights are rounded
+// there, as in the kernel for many rows.
+//
 // Measured on GB300, GPU time of a call in a CUDA graph over inputs that take turns;
 // in parentheses the time of the bytes at the 6791 GB/s of a copy.  One new token to
 // each of 64 sequences of 1000 to 16384, bf16, 32 heads over 8 of 128, pages of 16: 220
@@ -28,7 +37,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRows = 16, kKeys = 64, kWarpKeys = 16, kThreads = 128;
+constexpr int kKeys = 64, kWarpKeys = 16, kThreads = 128;
 // Stages of a warp's queue: as many bytes on their way for either width.
 template <int D>
 TSX_HD constexpr int stages() { return D == 64 ? 6 : 3; }
@@ -44,7 +53,7 @@ TSX_HD constexpr int stage_bytes() { return 2 * kWarpKeys * D * 2; }
 // Shared memory: the queues, the warps' statistics, the words of run_of.
 template <int D>
 TSX_HD constexpr int queue_bytes() { return 4 * stages<D>() * stage_bytes<D>(); }
-constexpr int kStatsBytes = 4 * kRows * 8, kSumsBytes = (kThreads / 32 + 3) * 8;
+constexpr int kStatsBytes = 4 * 16 * 8, kSumsBytes = (kThreads / 32 + 3) * 8;
 
 __device__ __forceinline__ void ldmatrix(uint32_t at, uint32_t (&r)[4])
 {
@@ -125,29 +134,31 @@ __device__ __forceinline__ uint32_t load_step(const AttendArgs& a, const Keys& k
     return seen;
 }
 
-template <int DT, int D>
+// M: rows of a tile, 8 or 16.  A thread has row g of them and, of 16, row g + 8.
+template <int DT, int D, int M>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(const __grid_constant__ AttendArgs a)
 {
+    constexpr int kMine = M / 8;
     extern __shared__ __align__(128) unsigned char memory[];
-    float2(*stats)[kRows] = reinterpret_cast<float2(*)[kRows]>(memory + queue_bytes<D>());
+    float2(*stats)[M] = reinterpret_cast<float2(*)[M]>(memory + queue_bytes<D>());
     int64_t* sums = reinterpret_cast<int64_t*>(memory + queue_bytes<D>() + kStatsBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, c2 = lane % 4 * 2;
     constexpr int kStages = stages<D>();
     constexpr float kLift = lift<DT, 0>();
     const uint32_t queue = smem_addr(memory) + warp * (kStages * stage_bytes<D>());
     let_next_start();
-    Run run = run_of<kRows, kKeys, kCost, kThreads>(a, kLeast, sums);
+    Run run = run_of<M, kKeys, kCost, kThreads>(a, kLeast, sums);
     Tail tail{};
     while (run.from < run.to) {
-        const Piece p = piece_of<kRows, kKeys, kCost>(a, run);
+        const Piece p = piece_of<M, kKeys, kCost>(a, run);
         if (p.empty())
             break;   // the run's last units, before a tile's first step
-        const int row0 = p.tile * kRows;
+        const int row0 = p.tile * M;
         const int64_t head_at = p.head * a.head_pitch;
         // queries, as the A operand: rows g and g + 8
-        uint32_t q[D / 16][4];
+        uint32_t q[D / 16][4] = {};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < kMine; ++half) {
             const int row = g + half * 8;
             const char* from = a.q + row_at(a, p.seq.first, p.head, row0 + row, a.q_pitch, a.q_head) * 2;
 #pragma unroll
@@ -159,7 +170,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                         row < p.rows && ch < a.dim ? *reinterpret_cast<const uint32_t*>(from + ch * 2) : 0u;
                 }
         }
-        const int limits[2] = {row_limit(a, p.seq, row0 + g), row_limit(a, p.seq, row0 + g + 8)};
+        int limits[kMine];
+#pragma unroll
+        for (int r = 0; r < kMine; ++r)
+            limits[r] = row_limit(a, p.seq, row0 + g + 8 * r);
         const int first_limit = row_limit(a, p.seq, row0);
         const int last_limit = row_limit(a, p.seq, row0 + p.rows - 1);
         Keys keys;
@@ -179,7 +193,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
             }
             cp_async_commit();
         }
-        float out[D / 8][4], top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        float out[D / 8][4], top[kMine], sum[kMine];
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) {
+            top[r] = -INFINITY;
+            sum[r] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -215,26 +234,31 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 mma<DT>(s[0], q[k], b[0], b[1]);
                 mma<DT>(s[1], q[k], b[2], b[3]);
             }
-            float most[2] = {-INFINITY, -INFINITY};
+            float most[kMine];
+#pragma unroll
+            for (int r = 0; r < kMine; ++r)
+                most[r] = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2 * kMine; ++e) {
                     const int key = j * 8 + c2 + (e & 1);
                     const bool sees = (mask >> key & 1) && base + key < limits[e >> 1];
                     s[j][e] = sees ? s[j][e] * a.scale_log2 : -INFINITY;
                     most[e >> 1] = fmaxf(most[e >> 1], s[j][e]);
                 }
+            bool grows = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < kMine; ++r) {
                 most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 1));
                 most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 2));
                 most[r] = fmaxf(most[r], top[r]);
+                grows |= most[r] != top[r];
             }
-            if (__any_sync(0xffffffffu, most[0] != top[0] || most[1] != top[1])) {
-                float f[2];
+            if (__any_sync(0xffffffffu, grows)) {
+                float f[kMine];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {   // no score yet: nothing to scale
+                for (int r = 0; r < kMine; ++r) {   // no score yet: nothing to scale
                     f[r] = top[r] == -INFINITY ? 1.f
                                                : exp2_fast(reference(top[r], kLift) - reference(most[r], kLift));
                     top[r] = most[r];
@@ -244,17 +268,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 for (int i = 0; i < D / 8; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        out[i][e] *= f[e >> 1];
+                        out[i][e] *= f[M == 8 ? 0 : e >> 1];
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2 * kMine; ++e) {
                     s[j][e] = exp2_fast(s[j][e] - (top[e >> 1] == -INFINITY ? 0.f : reference(top[e >> 1], kLift)));
                     sum[e >> 1] += s[j][e];
                 }
-            const uint32_t w[4] = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]), pack2<DT>(s[1][0], s[1][1]),
-                                   pack2<DT>(s[1][2], s[1][3])};
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                w[2 * j] = pack2<DT>(s[j][0], s[j][1]);
+                w[2 * j + 1] = M == 16 ? pack2<DT>(s[j][2], s[j][3])
+                                       : pack2<DT>(s[j][0] - value_of<DT>(static_cast<uint16_t>(w[2 * j])),
+                                                   s[j][1] - value_of<DT>(static_cast<uint16_t>(w[2 * j] >> 16)));
+            }
             const uint32_t values = stage + kWarpKeys * D * 2;
             if (base + kWarpKeys > first_limit) {
                 // Some row may not see some key: 0 times an infinity of such a value would be NaN.  What is not
@@ -274,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                             if (!not_finite<DT>(pair) || !(mask >> key & 1))
                                 continue;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
+                            for (int e = 0; e < 2 * kMine; ++e) {
                                 const uint16_t v = static_cast<uint16_t>(e & 1 ? pair >> 16 : pair);
                                 if (not_finite<DT>(v) && base + key < limits[e >> 1])
                                     out[i][e] += value_of<DT>(v);
@@ -301,20 +331,26 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
         }
         // the four warps' sums, each relative to its own maximum
         cp_async_wait(0);
+        if constexpr (M == 8)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)   // of an infinite value the rests are not wanted: theirs have any sign
+                    out[i][e] += fabsf(out[i][e]) < INFINITY ? out[i][e + 2] : 0.f;
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) {
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
             if (lane % 4 == 0)
                 stats[warp][g + 8 * r] = make_float2(reference(top[r], kLift), sum[r]);
         }
         __syncthreads();   // also: the queues are empty, and their memory free
-        float* joined = reinterpret_cast<float*>(memory);   // [4][kRows][D]
+        float* joined = reinterpret_cast<float*>(memory);   // [4][M][D]
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                *reinterpret_cast<float2*>(joined + (warp * kRows + g + 8 * r) * D + i * 8 + c2) =
+            for (int r = 0; r < kMine; ++r)
+                *reinterpret_cast<float2*>(joined + (warp * M + g + 8 * r) * D + i * 8 + c2) =
                     make_float2(out[i][2 * r], out[i][2 * r + 1]);
         __syncthreads();
         const bool whole = p.whole();
@@ -331,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
             for (int w = 0; w < 4; ++w) {
                 const float2 t = stats[w][row];
                 const float f = t.x == -INFINITY ? (t.y != t.y ? t.y : 0.f) : exp2_fast(t.x - m);
-                const float4 o = *reinterpret_cast<const float4*>(joined + (w * kRows + row) * D + ch);
+                const float4 o = *reinterpret_cast<const float4*>(joined + (w * M + row) * D + ch);
                 if (t.x == -INFINITY && t.y == t.y)
                     continue;   // nothing seen
                 l += t.y * f;
@@ -349,46 +385,53 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 if (ch == 0)
                     store_lse(a, p.seq.first, p.head, row0 + row, m, l);
             } else {
-                *reinterpret_cast<float4*>(a.parts + (static_cast<int64_t>(slot) * kRows + row) * D + ch) = v;
+                *reinterpret_cast<float4*>(a.parts + (static_cast<int64_t>(slot) * M + row) * D + ch) = v;
                 if (ch == 0)
-                    a.stats[slot * kRows + row] = make_float2(m, l);
+                    a.stats[slot * M + row] = make_float2(m, l);
             }
         }
-        const Tail t = tail_of<kRows, kCost>(run, p);
+        const Tail t = tail_of<M, kCost>(run, p);
         if (t.per)
             tail = t;
         __syncthreads();   // before the queues are used again
-        advance<kRows>(a, run, p);
+        advance<M>(a, run, p);
     }
     if (threadIdx.x == 0)
         a.tails[blockIdx.x] = tail;
 }
 
-template <int DT, int D>
-cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
+template <int DT, int D, int M>
+cudaError_t launch_rows(const AttendArgs& a, cudaStream_t st)
 {
-    const cudaError_t e = launch_grid<attend_kernel<DT, D>>(dim3(unsigned(a.ctas)), kThreads,
-                                                            queue_bytes<D>() + kStatsBytes + kSumsBytes, 1, false, st, a);
+    const cudaError_t e = launch_grid<attend_kernel<DT, D, M>>(dim3(unsigned(a.ctas)), kThreads,
+                                                               queue_bytes<D>() + kStatsBytes + kSumsBytes, 1, false, st, a);
     if (e != cudaSuccess)
         return e;
-    return launch_grid<attend_join_kernel<DT, D, kRows, kJoinRows, kJoinWarps>>(
-        dim3(unsigned(a.ctas), kRows / kJoinRows), kJoinWarps * 32, 0, 1, true, st, a);
+    return launch_grid<attend_join_kernel<DT, D, M, kJoinRows, kJoinWarps>>(
+        dim3(unsigned(a.ctas), M / kJoinRows), kJoinWarps * 32, 0, 1, true, st, a);
+}
+
+template <int DT, int M>
+cudaError_t launch_dim(const AttendArgs& a, cudaStream_t st)
+{
+    return a.dim <= 64    ? launch_rows<DT, 64, M>(a, st)
+           : a.dim <= 128 ? launch_rows<DT, 128, M>(a, st)
+                          : launch_rows<DT, 256, M>(a, st);
 }
 
 template <int DT>
-cudaError_t launch_dim(const AttendArgs& a, cudaStream_t st)
+cudaError_t launch_few(const AttendArgs& a, int rows, cudaStream_t st)
 {
-    return a.dim <= 64 ? launch_few<DT, 64>(a, st) : a.dim <= 128 ? launch_few<DT, 128>(a, st) : launch_few<DT, 256>(a, st);
+    return rows == 8 ? launch_dim<DT, 8>(a, st) : launch_dim<DT, 16>(a, st);
 }
 
 }  // namespace
 
-int attend_few_rows() { return kRows; }
 int attend_few_ctas(int dim) { return dim <= 128 ? 2 * 152 : 152; }
 
-cudaError_t launch_attend_few(int dtype, const AttendArgs& a, cudaStream_t st)
+cudaError_t launch_attend_few(int dtype, const AttendArgs& a, int rows, cudaStream_t st)
 {
-    return dtype == TSX_BF16 ? launch_dim<TSX_BF16>(a, st) : launch_dim<TSX_F16>(a, st);
+    return dtype == TSX_BF16 ? launch_few<TSX_BF16>(a, rows, st) : launch_few<TSX_F16>(a, rows, st);
 }
 
 }  // namespace tsx
