@@ -79,7 +79,8 @@ int tsx_rotary_turns(int pairs, const double *frequencies, uint64_t *turns);
  *                 normed and not turned
  *   layout        tsx_rope_layout
  *   norm          0: none; 1: x rstd weight before the rotation, rstd = 1 /
- *                 sqrt(mean of x^2 over the head's dim channels + eps)
+ *                 sqrt(mean of x^2 over the head's dim channels + eps); the sum
+ *                 of squares has the range of fp32
  *   eps           >= 0
  *   amplitude     the turned channels grow by it
  *   turns         the pairs' frequencies (tsx_rotary_turns) */

@@ -5,8 +5,8 @@
 // on 16 of the 64 keys of a step, with a queue of its own in shared memory that
 // it fills by cp.async (a page may start anywhere, so each row of 16-byte chunks
 // has its own address) and empties with no barrier but its own.  The products are
-// mma.m16n8k16 with the rows as M: 16 rows for up to 16 queries of a key, which
-// leaves most of the tensor cores' work empty, but that is not what bounds it.
+// mma.m16n8k16 with the rows as M: up to 16 queries of a key, most of whose places
+// stay empty, but that is not what bounds it.
 // Scores stay in registers: the accumulators of q k^T are the operand of the
 // product with v.  Running maxima and sums are the warp's own; they and the four
 // sums of values are joined once at the end of a piece.
@@ -22,12 +22,13 @@
 //
 // Measured on GB300, GPU time of a call in a CUDA graph over inputs that take turns;
 // in parentheses the time of the bytes at the 6791 GB/s of a copy.  One new token to
-// each of 64 sequences of 1000 to 16384, bf16, 32 heads over 8 of 128, pages of 16: 220
-// us (213).  One sequence of 100003 keys, f16, 16 heads over 2 of 64: 22.5 (7.5), of which
-// the join of 152 parts a head takes 7 and a CTA's start, first pages and end 5.  16
-// sequences up to 4096: 23.7 (12.6); one of 300: 10.3.  Queues of three stages of 8 KB
-// a warp keep 128 KB of an SM on their way; of 64 channels the stages are half as large
-// and there are six.
+// each of 64 sequences of 1000 to 16384, bf16, 32 heads over 8 of 128, pages of 16: 217
+// to 224 us (213) from one machine to the next; 256 channels 487 (427), 136 490 (227): such
+// heads are handled as 256.  One sequence of 100003 keys, f16, 16 heads over 2 of 64: 22.3
+// (7.5), of which the join of 152 parts a head takes 7 and a CTA's start, first pages and
+// end 5.  16 sequences up to 4096: 22.7 (12.6); one of 300: 9.8.  Queues of three stages
+// of 8 KB a warp keep 128 KB of an SM on their way; of 64 channels the stages are half as
+// large and there are six.
 
 #include "tsx_attend.cuh"
 #include "tsx_device.cuh"
@@ -43,8 +44,8 @@ template <int D>
 TSX_HD constexpr int stages() { return D == 64 ? 6 : 3; }
 constexpr int kJoinRows = 4, kJoinWarps = 8;
 // What a tile costs beside its steps, in steps, and units to a CTA at least: 16
-// sequences of up to 4096 keys, 32 heads over 8, 26.2 us with 0, 23.7 with 3, 24.6 with
-// 6; four of up to 1000 10.3 us in runs of at least 4, 11.1 of 5, 12.3 of 7.
+// sequences of up to 4096 keys, 32 heads over 8, 24.8 us with 0, 22.5 with 3, 23.5 with
+// 6; four of up to 1000 10.0 us in runs of at least 4, 10.7 of 5, 11.8 of 7.
 constexpr int kCost = 3;
 constexpr int64_t kLeast = 4;
 

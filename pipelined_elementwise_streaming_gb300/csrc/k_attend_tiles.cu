@@ -33,10 +33,12 @@
 //
 // Measured on GB300 as in the kernel for few rows; in parentheses the time of the
 // products at the 1897 TFLOP/s of cuBLAS.  bf16, chunks of 1024 tokens of two prompts of
-// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 240 us (192), 1.51 PFLOP/s; the
+// 16384 and 13000, 32 heads over 8 of 128, pages of 32: 241 us (192), 1.51 PFLOP/s; the
 // products alone would take 150 of them at the tensor cores' 4096 multiply-adds a
-// cycle.  A ragged batch of 12 (1 to 300 new tokens, up to 3000 keys, f16, 10 heads over
-// 2 of 64): 26, most of it the start and end of pieces of five steps and their joins.
+// cycle.  With heads of 64 channels 198 (96): the exponentials are as many; of 72, 80 and
+// 96 233, 234 and 237 (108, 120, 144): products are those of 128.  A ragged batch of 12 (1
+// to 300 new tokens, up to 3000 keys, f16, 10 heads over 2 of 64): 27, most of it the start
+// and end of pieces of five steps and their joins.
 // Steps that led here, for the first of them: mma.m16n8k16 2316 us; tcgen05 from one
 // thread, cp.async loads 489; an elected lane 464; loads with few shuffles 371; four
 // threads to a row and boxes of pages 337; one thread to a row 287; short code for what
@@ -58,8 +60,8 @@ using namespace dev;
 constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128;
 constexpr int kWeighers = 256, kLoaders = 64, kThreads = 384;
 // What a tile costs beside its steps, in steps, and units to a CTA at least.  The
-// ragged batch above takes 34.0 us with a cost of 0, 28.4 with 2, 26.1 with 3, 27.2 with 4; the
-// large one 254, 250, 247, 247.
+// ragged batch above takes 33.6 us with a cost of 0, 29.2 with 2, 26.8 with 3, 27.7 with 4;
+// the large one 250, 247, 243, 245.
 constexpr int kCost = 3;
 constexpr int64_t kLeast = 4;
 constexpr int kMasks = 8;            // steps whose keys are remembered
@@ -849,7 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tcgen05_after();
     const uint32_t tmem = static_cast<uint32_t>(words[0]);
-    // 168 registers a thread at the launch: 256 x 208 and 128 x 88 are as many
+    // 168 registers a thread at the launch: 256 x 208 and 128 x 88 are as many.  The weighers' 128
+    // scores and what stands beside them spill some 430 bytes: 0.4 % of the instructions that run
     if (warp < kLoadWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         Tail tail{};
