@@ -87,7 +87,11 @@ struct AttendArgs {
     float* parts;
     float2* stats;
     dev::Tail* tails;
+    float4* folded;   // and for each of its threads with sums a row of those and one more
 };
+// Threads of a CTA that hold sums, and how many fours of them each.
+TSX_HD constexpr int fold_threads(bool many) { return many ? 256 : 128; }
+TSX_HD constexpr int fold_fours(bool many, int padded) { return many ? padded / 4 : padded / 8; }
 // Few rows to a head, any dim: tiles of 8 or of 16 `rows`.
 int attend_few_ctas(int dim);
 // Many rows to a head, dim up to 128: one CTA to an SM.

@@ -594,12 +594,16 @@ int cache_maps(const tsx_cache& c, CUtensorMap (&maps)[2])
     return rc != TSX_OK ? rc : encode_pages_map(c.dtype, c.v, dims, strides, box, &maps[1]);
 }
 
-// Bytes of the parts of an attention call: their sums, statistics and tails.
+// Bytes of the parts of an attention call: their sums, statistics and tails, and the
+// sums that threads fold.
 struct Parts {
     int rows, ctas, padded;
+    bool many() const { return rows == attend_many_rows(); }
     size_t sums() const { return size_t(2) * ctas * rows * padded * 4; }
     size_t stats() const { return size_t(2) * ctas * rows * 8; }
-    size_t bytes() const { return sums() + stats() + size_t(ctas) * 32; }
+    size_t tails() const { return size_t(ctas) * 32; }
+    size_t folded() const { return size_t(ctas) * fold_threads(many()) * (fold_fours(many(), padded) + 1) * 16; }
+    size_t bytes() const { return sums() + stats() + tails() + folded(); }
 };
 
 // By rows to a head: tiles of 8 or 16 for as many, and of many for more in heads of up to
@@ -693,8 +697,9 @@ extern "C" int tsx_paged_attention(const tsx_cache* cache, const tsx_batch* batc
     a.parts = reinterpret_cast<float*>(scratch);
     a.stats = reinterpret_cast<float2*>(scratch + parts.sums());
     a.tails = reinterpret_cast<dev::Tail*>(scratch + parts.sums() + parts.stats());
+    a.folded = reinterpret_cast<float4*>(scratch + parts.sums() + parts.stats() + parts.tails());
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (parts.rows != attend_many_rows())
+    if (!parts.many())
         return launched(launch_attend_few(cache->dtype, a, parts.rows, st), call);
     // a positive scale, so that the largest score is the largest product; not 0, which -infinity must not meet: with
     // the least number above it the largest product's score is 2^-21

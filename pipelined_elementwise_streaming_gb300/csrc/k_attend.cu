@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
     float2(*stats)[M] = reinterpret_cast<float2(*)[M]>(memory + queue_bytes<D>());
     int64_t* sums = reinterpret_cast<int64_t*>(memory + queue_bytes<D>() + kStatsBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, c2 = lane % 4 * 2;
-    constexpr int kStages = stages<D>();
+    constexpr int kStages = stages<D>(), kFours = fold_fours(false, D);
+    static_assert(kThreads == fold_threads(false), "a row of folded sums to each thread");
     constexpr float kLift = lift<DT, 0>();
     const uint32_t queue = smem_addr(memory) + warp * (kStages * stage_bytes<D>());
     let_next_start();
@@ -207,7 +208,40 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 out[i][e] = 0.f;
         int next_in = kStages - 1, next_out = 0;
         int base = p.step * kKeys + warp * kWarpKeys;
+        float4* const folded = folded_at<kThreads, kFours>(a);
+        const auto fold = [&](bool first, auto&& each) {
+            float4 held = make_float4(0.f, -INFINITY, 0.f, -INFINITY);
+            if (!first)
+                held = folded[kFours * kThreads];
+            const float now[2] = {reference(top[0], kLift), reference(top[kMine - 1], kLift)};
+            const float f[2] = {refer(held.y, now[0]), M == 8 ? refer(held.y, now[0]) : refer(held.w, now[1])};
+            sum[0] += held.x * f[0];
+            if constexpr (M == 16)
+                sum[1] += held.z * f[1];
+#pragma unroll
+            for (int i = 0; i < kFours; ++i) {
+                if (!first) {
+                    const float4 g = folded[i * kThreads];
+                    out[i][0] += g.x * f[0];
+                    out[i][1] += g.y * f[0];
+                    out[i][2] += g.z * f[1];
+                    out[i][3] += g.w * f[1];
+                }
+                each(i);
+            }
+        };
         for (int step = 0; step < steps; ++step, base += kKeys) {
+            if (step > 0 && step % kFold == 0) {
+                fold(step == kFold, [&](int i) {
+                    folded[i * kThreads] = make_float4(out[i][0], out[i][1], out[i][2], out[i][3]);
+                    out[i][0] = out[i][1] = out[i][2] = out[i][3] = 0.f;
+                });
+                folded[kFours * kThreads] = make_float4(sum[0], reference(top[0], kLift), sum[kMine - 1],
+                                                        reference(top[kMine - 1], kLift));
+#pragma unroll
+                for (int r = 0; r < kMine; ++r)
+                    sum[r] = 0.f;
+            }
             cp_async_wait(kStages - 2);
             __syncwarp();
             const uint32_t mask = seen[0];
@@ -332,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
         }
         // the four warps' sums, each relative to its own maximum
         cp_async_wait(0);
+        if (steps > kFold)
+            fold(false, [](int) {});
         if constexpr (M == 8)
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -356,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
         __syncthreads();
         const bool whole = p.whole();
         const int slot = part_slot(p);
-        constexpr int kFours = D / 4;
-        for (int i = threadIdx.x; i < p.rows * kFours; i += kThreads) {
-            const int row = i / kFours, ch = i % kFours * 4;
+        constexpr int kRowFours = D / 4;
+        for (int i = threadIdx.x; i < p.rows * kRowFours; i += kThreads) {
+            const int row = i / kRowFours, ch = i % kRowFours * 4;
             float m = -INFINITY, l = 0.f;
 #pragma unroll
             for (int w = 0; w < 4; ++w)

@@ -348,6 +348,23 @@ TSX_HD constexpr float lift() { return DT == TSX_F16 ? 15 - MOST : 0; }
 // Rounded up, so that no weight is larger.
 __device__ __forceinline__ float reference(float top, float under) { return __fsub_ru(top, under); }
 
+// The tensor cores add with truncation: N products one after the other lose some N
+// 2^-23.5 of their sum (0.6 % of 1M keys alike in weight, 2.3 % of 4M).  So after every
+// kFold products of a piece a thread adds its sums to others that it keeps in the scratch,
+// where fp32 rounds to nearest: its row there has `fours` fours of sums, then a sum of
+// weights and its reference, for each of the thread's rows.  What is lost is 2^-13.5 of a
+// result whatever the length.
+constexpr int kFold = 1024;
+
+template <int THREADS, int FOURS>
+__device__ __forceinline__ float4* folded_at(const AttendArgs& a)
+{
+    return a.folded + static_cast<int64_t>(blockIdx.x) * THREADS * (FOURS + 1) + threadIdx.x;
+}
+
+// By which sums of the reference `top` are scaled to the reference `now`.
+__device__ __forceinline__ float refer(float top, float now) { return top == -INFINITY ? 0.f : exp2_fast(top - now); }
+
 // Row `row` of a sequence's rows of a head: element of q or out.
 __device__ __forceinline__ int64_t row_at(const AttendArgs& a, int first, int head, int row, int64_t pitch,
                                           int64_t head_pitch)
