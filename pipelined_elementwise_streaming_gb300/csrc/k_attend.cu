@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) attend_kernel(cons
                 out[i][e] = 0.f;
         int next_in = kStages - 1, next_out = 0;
         int base = p.step * kKeys + warp * kWarpKeys;
+        // what has been folded (see kFold) added to the sums; then `each` of them may be put away
         float4* const folded = folded_at<kThreads, kFours>(a);
         const auto fold = [&](bool first, auto&& each) {
             float4 held = make_float4(0.f, -INFINITY, 0.f, -INFINITY);
